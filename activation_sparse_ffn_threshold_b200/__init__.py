@@ -10,6 +10,13 @@ fails loudly; there is no fallback implementation.
     idx, count = layer.predict(x)      # the predicted set only
     Y = layer.forward_batch(X)         # b tokens through the union of their sets
     XL = forward_stack([l0, l1], X0)   # residual stack
+    Y = layer.forward_prompt(X)        # many tokens through all neurons (dense)
+
+The dense operators (no handle, fp16 or bf16, differentiable) are in ``dense``:
+
+    y = gated_ffn(x, w_gate, w_up, w_down, b, checkpoint="act8")   # torch.autograd
+    y, saved = gated_ffn_forward(...); grads = gated_ffn_backward(dy, saved, ...)
+    q = quantize_act8(x); x = dequantize_act8(q)                   # 8-bit activation blocks
 """
 from __future__ import annotations
 
@@ -22,10 +29,11 @@ import torch
 __all__ = ["SparseFFN", "SfnnError", "forward_stack", "predict_noalloc", "hotness_order", "library_path",
            "load_library",
            "RELU", "REGLU", "F32", "F16", "I8", "I4", "BATCH_AUTO", "BATCH_CUDA_CORE", "BATCH_TENSOR_CORE",
-           "BATCH_FUSED"]
+           "BATCH_FUSED", "BF16", "gated_ffn", "gated_ffn_forward", "gated_ffn_backward", "GatedSaved",
+           "quantize_act8", "dequantize_act8", "Act8", "dense_error"]
 
 RELU, REGLU = 0, 1
-F32, F16, I8, I4 = 0, 1, 2, 3
+F32, F16, I8, I4, BF16 = 0, 1, 2, 3, 4
 BATCH_AUTO, BATCH_CUDA_CORE, BATCH_TENSOR_CORE, BATCH_FUSED = 0, 1, 2, 3
 STATUS = {0: "SFNN_OK", 1: "SFNN_ERR_INVALID_ARG", 2: "SFNN_ERR_CUDA", 3: "SFNN_ERR_OOM",
           4: "SFNN_ERR_UNSUPPORTED", 5: "SFNN_ERR_TIMEOUT"}
@@ -73,7 +81,7 @@ def load_library():
         raise ImportError(f"{_LIB_PATH} is missing: build it with "
                           f"`python -m activation_sparse_ffn_threshold_b200.build` (nvcc, sm_100a)")
     lib = ctypes.CDLL(_LIB_PATH)
-    P, I, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int
+    P, I, L, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int
     sig = {
         "sfnn_create": ([ctypes.POINTER(LayerDesc), P, ctypes.POINTER(P)], S),
         "sfnn_destroy": ([P], S),
@@ -98,6 +106,12 @@ def load_library():
         "sfnn_status_str": ([S], ctypes.c_char_p),
         "sfnn_hotness_order": ([ctypes.POINTER(ctypes.c_float), I, ctypes.POINTER(ctypes.c_int32)], S),
         "sfnn_predict_noalloc": ([P, P, P, P, I, I, I, I, P, P, P], S),
+        "sfnn_gated_workspace": ([I, I, I, I], L),
+        "sfnn_gated_forward": ([P, P, L, I, P, P, L, P, P], S),
+        "sfnn_gated_backward": ([P, P, L, P, P, P, P, P, P, P, L, P, P], S),
+        "sfnn_forward_prompt": ([P, P, I, P, P, L, P], S),
+        "sfnn_act8_quantize": ([P, L, I, I, I, I, P, L, P, L, P], S),
+        "sfnn_act8_restore": ([P, L, P, L, I, I, I, I, P, L, P], S),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -258,6 +272,22 @@ class SparseFFN:
                                             _stream(stream)), "sfnn_forward_batch")
         return (Y, idx, counts) if return_sets else Y
 
+    def forward_prompt(self, X, Y=None, stream=None):
+        """Y [T, d] fp32 for T tokens (any number) through all neurons, without the predictor."""
+        T = X.shape[0]
+        self._check_x(X, rows=T)
+        Y = Y if Y is not None else torch.empty((T, self.d), dtype=torch.float32, device=X.device)
+        if Y.dtype != torch.float32 or Y.device != X.device or not Y.is_contiguous() or Y.numel() != T * self.d:
+            raise ValueError(f"Y must be a contiguous fp32 tensor of {T}x{self.d} elements on X's device")
+        stream = stream if stream is not None else torch.cuda.current_stream(X.device)
+        nbytes = self._lib.sfnn_gated_workspace(T, self.d, self.n, 0)
+        with torch.cuda.stream(stream):  # the workspace belongs to the stream that uses it
+            ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=X.device)
+        with torch.cuda.device(X.device):
+            _check(self._lib.sfnn_forward_prompt(self._h, _ptr(X), T, _ptr(Y), _ptr(ws), ws.numel(),
+                                                 _stream(stream)), "sfnn_forward_prompt")
+        return Y
+
     def set_batch_path(self, path: int):
         _check(self._lib.sfnn_set_batch_path(self._h, int(path)), "sfnn_set_batch_path")
 
@@ -393,3 +423,7 @@ def forward_stack(layers, X0, XL=None, idx=None, counts=None, return_sets: bool 
     _check(getattr(lib, name)(arr, len(layers), _ptr(X0), b, _ptr(XL), _ptr(idx), _ptr(counts), _stream(stream)),
            name)
     return (XL, idx, counts) if return_sets else XL
+
+
+from .dense import (Act8, GatedSaved, dense_error, dequantize_act8, gated_ffn, gated_ffn_backward,  # noqa: E402
+                    gated_ffn_forward, quantize_act8)

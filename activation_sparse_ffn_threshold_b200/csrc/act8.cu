@@ -1,0 +1,179 @@
+// act8.cu -- 16-bit rows to 8-bit blocks and back (the format is in dense.cuh).
+//
+// Bound by bytes: 2 read + 1.0625 written per value (and back).  A warp takes 2048 columns
+// of one row: every lane requests up to eight 16-byte vectors before it uses the first, so
+// a row's bytes are in flight together; eight neighbouring lanes hold one 64-value block
+// and find its largest magnitude with three shuffles, so a value is read once.
+#include "dense.cuh"
+#include "launch.cuh"
+
+namespace sfnn {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kVecs = 8;               // 8-value vectors per lane
+constexpr int kChunk = 32 * kVecs * 8;  // columns per warp
+
+__device__ __forceinline__ uint4 load8(const uint16_t *p, int have, bool vec) {
+  uint4 w = make_uint4(0, 0, 0, 0);
+  if (have >= 8 && vec) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "l"(p));
+  } else if (have > 0) {
+    uint32_t a[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < have) a[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+    w = make_uint4(a[0], a[1], a[2], a[3]);
+  }
+  return w;
+}
+
+template <bool RELU>
+__global__ void __launch_bounds__(kWarps * 32)
+    k_act8_quantize(const uint16_t *__restrict__ x, int64_t ldx, int T, int cols, int bf16, int vec,
+                    uint8_t *__restrict__ codes, int64_t ldq, float *__restrict__ scales, int64_t lds) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (row >= T) return;
+  const int c0 = blockIdx.y * kChunk + lane * 8;
+  uint4 w[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = c0 + i * 256;
+    w[i] = load8(x + row * ldx + c, cols - c, vec);
+  }
+  const int end = (cols + kAct8Block - 1) / kAct8Block * kAct8Block;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = c0 + i * 256;
+    const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    float v[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack16(a[j], bf16);
+      v[2 * j] = f.x;
+      v[2 * j + 1] = f.y;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (RELU) v[j] = v[j] < 0.f ? 0.f : v[j];
+      top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (c >= end) continue;
+    const Act8Scale s = act8_scale(top, RELU ? 255.f : 127.f);
+    uint32_t q[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      q[j >> 2] |= (RELU ? act8_code_relu(v[j], s.inv) : act8_code_signed(v[j], s.inv)) << (8 * (j & 3));
+    *reinterpret_cast<uint2 *>(codes + row * ldq + c) = make_uint2(q[0], q[1]);
+    if ((lane & 7) == 0) scales[row * lds + (c >> 6)] = s.scale;
+  }
+}
+
+template <bool RELU>
+__global__ void __launch_bounds__(kWarps * 32)
+    k_act8_restore(const uint8_t *__restrict__ codes, int64_t ldq, const float *__restrict__ scales, int64_t lds, int T,
+                   int cols, int bf16, int vec, uint16_t *__restrict__ out, int64_t ldo) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (row >= T) return;
+  const int c0 = blockIdx.y * kChunk + lane * 8;
+  uint2 w[kVecs];
+  float s[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = c0 + i * 256;
+    if (c < cols) {
+      w[i] = __ldg(reinterpret_cast<const uint2 *>(codes + row * ldq + c));
+      s[i] = __ldg(scales + row * lds + (c >> 6));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = c0 + i * 256;
+    if (c >= cols) continue;
+    const uint32_t a[2] = {w[i].x, w[i].y};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = (a[j >> 1] >> (16 * (j & 1))) & 0xffu, hi = (a[j >> 1] >> (16 * (j & 1) + 8)) & 0xffu;
+      o[j] = RELU ? pack16((float)lo * s[i], (float)hi * s[i], bf16)
+                  : pack16((float)(int8_t)lo * s[i], (float)(int8_t)hi * s[i], bf16);
+    }
+    uint16_t *p = out + row * ldo + c;
+    if (vec && cols - c >= 8) {
+      *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < cols) p[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+    }
+  }
+}
+
+bool aligned16(const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
+dim3 grid_of(int T, int cols) { return dim3((T + kWarps - 1) / kWarps, (cols + kChunk - 1) / kChunk); }
+
+}  // namespace
+
+cudaError_t launch_act8_quantize(const void *x, int64_t ldx, int T, int cols, int bf16, bool relu, uint8_t *codes,
+                                 int64_t ldq, float *scales, int64_t lds, cudaStream_t s) {
+  return launch_pdl(relu ? k_act8_quantize<true> : k_act8_quantize<false>, grid_of(T, cols), dim3(kWarps * 32), 0, s,
+                    static_cast<const uint16_t *>(x), ldx, T, cols, bf16, (int)aligned16(x, ldx), codes, ldq, scales,
+                    lds);
+}
+
+cudaError_t launch_act8_restore(const uint8_t *codes, int64_t ldq, const float *scales, int64_t lds, int T, int cols,
+                                bool relu, int bf16, void *out, int64_t ldo, cudaStream_t s) {
+  return launch_pdl(relu ? k_act8_restore<true> : k_act8_restore<false>, grid_of(T, cols), dim3(kWarps * 32), 0, s,
+                    codes, ldq, scales, lds, T, cols, bf16, (int)aligned16(out, ldo), static_cast<uint16_t *>(out), ldo);
+}
+
+}  // namespace sfnn
+
+extern "C" {
+
+static sfnn_status act8_check(const void *x, int64_t ldx, int32_t T, int32_t cols, int32_t dtype, const void *codes,
+                              int64_t ldq, const void *scales, int64_t lds) {
+  if (T < 0 || cols < 1 || (dtype != SFNN_F16 && dtype != SFNN_BF16)) return SFNN_ERR_INVALID_ARG;
+  const int64_t blocks = ((int64_t)cols + SFNN_ACT8_BLOCK - 1) / SFNN_ACT8_BLOCK;
+  if (ldx < cols || ldq < blocks * SFNN_ACT8_BLOCK || ldq % 16 || lds < blocks) return SFNN_ERR_INVALID_ARG;
+  if (T == 0) return SFNN_OK;
+  if (!x || !codes || !scales) return SFNN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(codes) & 15u) || (reinterpret_cast<uintptr_t>(scales) & 3u) ||
+      (reinterpret_cast<uintptr_t>(x) & 1u))
+    return SFNN_ERR_INVALID_ARG;
+  if ((cols + sfnn::kChunk - 1) / sfnn::kChunk > 65535) return SFNN_ERR_UNSUPPORTED;
+  return SFNN_OK;
+}
+
+sfnn_status sfnn_act8_quantize(const void *x, int64_t ldx, int32_t T, int32_t cols, int32_t dtype, int32_t relu,
+                               void *codes, int64_t ldq, float *scales, int64_t lds, sfnn_stream_t stream) {
+  const sfnn_status st = act8_check(x, ldx, T, cols, dtype, codes, ldq, scales, lds);
+  if (st != SFNN_OK || T == 0) return st;
+  return sfnn::launch_act8_quantize(x, ldx, T, cols, dtype == SFNN_BF16, relu != 0, static_cast<uint8_t *>(codes), ldq,
+                                    scales, lds, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SFNN_OK
+             : SFNN_ERR_CUDA;
+}
+
+sfnn_status sfnn_act8_restore(const void *codes, int64_t ldq, const float *scales, int64_t lds, int32_t T, int32_t cols,
+                              int32_t relu, int32_t dtype, void *out, int64_t ldo, sfnn_stream_t stream) {
+  const sfnn_status st = act8_check(out, ldo, T, cols, dtype, codes, ldq, scales, lds);
+  if (st != SFNN_OK || T == 0) return st;
+  return sfnn::launch_act8_restore(static_cast<const uint8_t *>(codes), ldq, scales, lds, T, cols, relu != 0,
+                                   dtype == SFNN_BF16, out, ldo, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SFNN_OK
+             : SFNN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,111 @@
+// dense.cuh -- the dense tensor-core product shared by the gated FFN's forward and
+// backward: its parameters and host launcher, and the 8-bit block format its epilogues
+// write and read.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "sfnn.h"
+#include "umma.cuh"
+
+namespace sfnn {
+
+// ---------------------------------------------------------------- 16-bit elements
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float2 unpack16(uint32_t w, bool bf16) {
+  if (bf16) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+__device__ __forceinline__ float load16(const void *p, int64_t i, bool bf16) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : __half2float(static_cast<const __half *>(p)[i]);
+}
+
+// ---------------------------------------------------------------- act8
+// 64 values of a row share an fp32 scale: max|v| / 127 with codes -127..127, or for
+// relu(v) max / 255 with codes 0..255.  A code is rint(v * (qmax / max)): one multiply per
+// value, off from the nearest code only where two are equally near to an fp32 rounding.  A
+// positive relu'd value keeps a code of at least 1: code > 0 is exactly the ReLU's mask,
+// which the backward pass needs.  A block with a NaN or an infinity gets a NaN scale (and so
+// restores as NaN); a block whose largest magnitude is below 2^-119 gets scale 0.
+constexpr int kAct8Block = 64;
+
+struct Act8Scale {
+  float scale, inv;
+};
+// `top`: the largest fp32 bit pattern of the block's magnitudes (NaN > inf > finite).
+__device__ __forceinline__ Act8Scale act8_scale(uint32_t top, float qmax) {
+  const float m = __uint_as_float(top);
+  Act8Scale s;
+  s.scale = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : (top < 0x04000000u ? 0.f : __fdiv_rn(m, qmax));
+  s.inv = (top >= 0x7f800000u || top < 0x04000000u) ? 0.f : __fdiv_rn(qmax, m);
+  return s;
+}
+__device__ __forceinline__ uint32_t act8_code_signed(float v, float inv) {
+  return (uint32_t)max(-127, min(127, __float2int_rn(v * inv))) & 0xffu;
+}
+__device__ __forceinline__ uint32_t act8_code_relu(float r, float inv) {  // r = relu(v)
+  const int c = min(255, __float2int_rn(r * inv));
+  return (uint32_t)(r > 0.f ? max(c, 1) : 0);
+}
+
+// ---------------------------------------------------------------- the product
+// C = sum over up to two (A, B) pairs of A . B^T, tiles of 256 x 256 by CTA pairs.
+enum DenseEpi : int {
+  kEpiStore = 0,  // C as 16-bit or fp32 values
+  kEpiGated = 1,  // B0 = gate rows, B1 = up rows (128 each per tile): H = relu(G + b) * U
+  kEpiDGated = 2  // C = dH: dU = dH * R, dG = dH * U * [R > 0], H = R * U
+};
+
+struct alignas(64) DenseParams {
+  CUtensorMap a0, b0, a1, b1;
+  int M, N;       // rows and columns of C (gated: neurons)
+  int nk0, nk;    // K chunks of 64 of the first pair, of both
+  int tiles_m, tiles_n;
+  int bf16;
+  int out32;      // kEpiStore: fp32 C
+  int relu;       // kEpiStore: C = relu(C + bias)
+  void *out;      // C, or H
+  int64_t ldo;
+  const void *bias;   // kEpiGated, relu: [N] or null
+  int save;           // sfnn_save of r and u
+  void *r, *u;        // kEpiGated: written; kEpiDGated: read
+  float *rs, *us;
+  int64_t ldr, lds;   // their row strides (elements), their scales' row strides
+  void *dg, *du;      // kEpiDGated: written, row stride ldo as out (H)
+  int32_t *err;
+};
+
+// The kernel's dynamic shared memory limit on the current device (once per device).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &ready) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+cudaError_t launch_dense(const DenseParams &P, int epi, bool a_mn, bool b_mn, int num_sms, cudaStream_t s);
+
+// Rows of 16-bit values to act8 blocks and back (act8.cu).  Code rows are ldq bytes apart
+// (a multiple of 16, at least T's columns rounded up to 64), scale rows lds floats.
+cudaError_t launch_act8_quantize(const void *x, int64_t ldx, int T, int cols, int bf16, bool relu, uint8_t *codes,
+                                 int64_t ldq, float *scales, int64_t lds, cudaStream_t s);
+cudaError_t launch_act8_restore(const uint8_t *codes, int64_t ldq, const float *scales, int64_t lds, int T, int cols,
+                                bool relu, int bf16, void *out, int64_t ldo, cudaStream_t s);
+
+}  // namespace sfnn

@@ -1,0 +1,340 @@
+// gated.cu -- the gated FFN over all neurons: forward, backward, and the entry points.
+#include <atomic>
+
+#include "common.cuh"
+#include "context.cuh"
+#include "dense.cuh"
+#include "launch.cuh"
+
+namespace sfnn {
+namespace {
+
+int num_sms_of_current() {
+  static std::atomic<int> known[64];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < 64) {
+    const int k = known[dev].load(std::memory_order_relaxed);
+    if (k) return k;
+  }
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// ---------------------------------------------------------------- column sums (db)
+// db[i] = sum over tokens of dG[t][i].  A block sums 64 columns of its share of the rows:
+// 8 lanes across (16 bytes each), 32 rows at a time, then the 32 row sums in a fixed order.
+// Bound by the bytes of dG (2 T n).
+__global__ void __launch_bounds__(256) k_colsum(const uint16_t *__restrict__ v, int64_t ld, int T, int n, int bf16,
+                                                int rows_per, float *__restrict__ part, void *__restrict__ out) {
+  __shared__ float sum[32][65];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int cl = threadIdx.x & 7, rl = threadIdx.x >> 3;
+  const int col = blockIdx.x * 64 + cl * 8;
+  const int64_t t0 = (int64_t)blockIdx.y * rows_per, t1 = min((int64_t)T, t0 + rows_per);
+  float a[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (col < n) {
+#pragma unroll 4
+    for (int64_t t = t0 + rl; t < t1; t += 32) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(v + t * ld + col));
+      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack16(q[j], bf16);
+        a[2 * j] += f.x;
+        a[2 * j + 1] += f.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[rl][cl * 8 + j] = a[j];
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int c = blockIdx.x * 64 + threadIdx.x;
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) s += sum[r][threadIdx.x];
+    if (c < n) {
+      if (part)
+        part[(int64_t)blockIdx.y * n + c] = s;
+      else
+        static_cast<uint16_t *>(out)[c] = (uint16_t)(pack16(s, 0.f, bf16) & 0xffffu);
+    }
+  }
+}
+__global__ void __launch_bounds__(256) k_colsum_join(const float *__restrict__ part, int splits, int n, int bf16,
+                                                     uint16_t *__restrict__ out) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= n) return;
+  float s = 0.f;
+  for (int k = 0; k < splits; ++k) s += part[(int64_t)k * n + c];
+  out[c] = (uint16_t)(pack16(s, 0.f, bf16) & 0xffffu);
+}
+
+constexpr int kSumRows = 512;  // rows of a column-sum block
+int sum_splits(int T) { return (T + kSumRows - 1) / kSumRows; }
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+int64_t hidden_bytes(int64_t T, int64_t n) { return up(T * up(n, 8) * 2, 256); }
+
+bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool mat_ok(const void *p, int64_t ld, int64_t cols) { return p && a16(p) && ld >= cols && ld % 8 == 0 && ld <= (1ll << 36); }
+
+sfnn_status check(const sfnn_gated_desc *q) {
+  if (!q || q->T < 0 || q->d < 1 || q->n < 1) return SFNN_ERR_INVALID_ARG;
+  if (q->dtype != SFNN_F16 && q->dtype != SFNN_BF16)
+    return q->dtype == SFNN_F32 ? SFNN_ERR_UNSUPPORTED : SFNN_ERR_INVALID_ARG;
+  if (q->d % 8) return SFNN_ERR_UNSUPPORTED;
+  if (q->down_layout != SFNN_DOWN_WIDTH_MAJOR && q->down_layout != SFNN_DOWN_NEURON_MAJOR) return SFNN_ERR_INVALID_ARG;
+  if (q->down_layout == SFNN_DOWN_WIDTH_MAJOR && q->n % 8) return SFNN_ERR_UNSUPPORTED;
+  if (q->d > (1 << 20) || q->n > (1 << 20) || q->T > (1 << 24)) return SFNN_ERR_UNSUPPORTED;
+  if (!mat_ok(q->w_gate, q->ld_gate, q->d) || !mat_ok(q->w_up, q->ld_up, q->d) ||
+      !mat_ok(q->w_down, q->ld_down, q->down_layout == SFNN_DOWN_WIDTH_MAJOR ? q->n : q->d))
+    return SFNN_ERR_INVALID_ARG;
+  if (q->T > 0 && !mat_ok(q->x, q->ldx, q->d)) return SFNN_ERR_INVALID_ARG;
+  return SFNN_OK;
+}
+
+sfnn_status check_saved(const sfnn_gated_desc *q, const sfnn_gated_saved *sv) {
+  if (sv->kind == SFNN_SAVE_FULL) {
+    if (q->n % 8) return SFNN_ERR_UNSUPPORTED;
+    if (q->T > 0 && (!mat_ok(sv->r, sv->ld, q->n) || !mat_ok(sv->u, sv->ld, q->n))) return SFNN_ERR_INVALID_ARG;
+    return SFNN_OK;
+  }
+  if (sv->kind != SFNN_SAVE_ACT8) return SFNN_ERR_INVALID_ARG;
+  if (q->n % 8) return SFNN_ERR_UNSUPPORTED;
+  const int64_t nb = up(q->n, kAct8Block) / kAct8Block, db = up(q->d, kAct8Block) / kAct8Block;
+  if (sv->ld < nb * kAct8Block || sv->ld % 16 || sv->lds < nb || sv->ld_x < db * kAct8Block || sv->ld_x % 16 ||
+      sv->lds_x < db)
+    return SFNN_ERR_INVALID_ARG;
+  if (q->T > 0 && (!sv->r || !sv->u || !sv->r_scales || !sv->u_scales || !sv->x || !sv->x_scales || !a16(sv->r) ||
+                   !a16(sv->u) || !a16(sv->x)))
+    return SFNN_ERR_INVALID_ARG;
+  return SFNN_OK;
+}
+
+// C [M x N] = A . B^T: tensor maps and tile counts.  a_mn: A is stored [K x M]; b_mn: B is [K x N].
+struct Operand {
+  const void *p;
+  int64_t ld;
+  bool mn;
+};
+bool set_pair(DenseParams &P, int which, const Operand &a, const Operand &b, int M, int N, int64_t K) {
+  CUtensorMap *ma = which ? &P.a1 : &P.a0, *mb = which ? &P.b1 : &P.b0;
+  return (a.mn ? make_tensor_map(ma, a.p, 2, K, M, a.ld, 64, 64, true)
+               : make_tensor_map(ma, a.p, 2, M, K, a.ld, 128, 64, true)) &&
+         (b.mn ? make_tensor_map(mb, b.p, 2, K, N, b.ld, 64, 64, true)
+               : make_tensor_map(mb, b.p, 2, N, K, b.ld, 128, 64, true));
+}
+int chunks(int64_t K) { return (int)((K + 63) / 64); }
+
+sfnn_status product(const Operand &a, const Operand &b, int M, int N, int64_t K, const Operand *a1, const Operand *b1,
+                    int64_t K1, void *out, int64_t ldo, int out32, int bf16, int32_t *err, cudaStream_t s,
+                    const void *relu_bias = nullptr) {
+  DenseParams P{};
+  P.relu = relu_bias != nullptr;
+  P.bias = relu_bias;
+  P.M = M;
+  P.N = N;
+  P.nk0 = P.nk = chunks(K);
+  if (!set_pair(P, 0, a, b, M, N, K)) return SFNN_ERR_CUDA;
+  if (a1) {
+    if (!set_pair(P, 1, *a1, *b1, M, N, K1)) return SFNN_ERR_CUDA;
+    P.nk += chunks(K1);
+  }
+  P.tiles_m = (M + 255) / 256;
+  P.tiles_n = (N + 255) / 256;
+  P.bf16 = bf16;
+  P.out = out;
+  P.ldo = ldo;
+  P.out32 = out32;
+  P.err = err;
+  return launch_dense(P, kEpiStore, a.mn, b.mn, num_sms_of_current(), s) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace sfnn
+
+using namespace sfnn;
+
+extern "C" {
+
+int64_t sfnn_gated_workspace(int32_t T, int32_t d, int32_t n, int32_t backward) {
+  if (T < 0 || d < 1 || n < 1) return -1;
+  if (!backward) return hidden_bytes(T, n);
+  return 3 * hidden_bytes(T, n) + hidden_bytes(T, d) + up((int64_t)sum_splits(T) * n * 4, 256);
+}
+
+sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, int32_t y_dtype, sfnn_gated_saved *sv,
+                               void *ws, int64_t ws_bytes, int32_t *err, sfnn_stream_t stream) {
+  sfnn_status st = check(q);
+  if (st != SFNN_OK) return st;
+  const int kind = sv ? sv->kind : SFNN_SAVE_NONE;
+  if (kind != SFNN_SAVE_NONE && (st = check_saved(q, sv)) != SFNN_OK) return st;
+  if (y_dtype != q->dtype && y_dtype != SFNN_F32) return SFNN_ERR_INVALID_ARG;
+  if (q->T == 0) return SFNN_OK;
+  if (!mat_ok(y, y_dtype == SFNN_F32 ? ldy * 2 : ldy, q->d) || ldy < q->d || !err || !ws || !a16(ws) || ws_bytes < sfnn_gated_workspace(q->T, q->d, q->n, 0))
+    return SFNN_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int bf16 = q->dtype == SFNN_BF16;
+  const int64_t ldh = up(q->n, 8);
+  if (kind == SFNN_SAVE_ACT8 &&
+      launch_act8_quantize(q->x, q->ldx, q->T, q->d, bf16, false, static_cast<uint8_t *>(sv->x), sv->ld_x,
+                           sv->x_scales, sv->lds_x, s) != cudaSuccess)
+    return SFNN_ERR_CUDA;
+  DenseParams P{};
+  P.M = q->T;
+  P.N = q->n;
+  P.nk0 = P.nk = chunks(q->d);
+  if (!make_tensor_map(&P.a0, q->x, 2, q->T, q->d, q->ldx, 128, 64, true) ||
+      !make_tensor_map(&P.b0, q->w_gate, 2, q->n, q->d, q->ld_gate, 128, 64, true) ||
+      !make_tensor_map(&P.b1, q->w_up, 2, q->n, q->d, q->ld_up, 128, 64, true))
+    return SFNN_ERR_CUDA;
+  P.tiles_m = (q->T + 255) / 256;
+  P.tiles_n = (q->n + 127) / 128;
+  P.bf16 = bf16;
+  P.out = ws;
+  P.ldo = ldh;
+  P.bias = q->b;
+  P.save = kind;
+  if (kind != SFNN_SAVE_NONE) {
+    P.r = sv->r;
+    P.u = sv->u;
+    P.ldr = sv->ld;
+    P.rs = sv->r_scales;
+    P.us = sv->u_scales;
+    P.lds = sv->lds;
+  }
+  P.err = err;
+  if (launch_dense(P, kEpiGated, false, false, num_sms_of_current(), s) != cudaSuccess) return SFNN_ERR_CUDA;
+  const Operand h{ws, ldh, false}, wd{q->w_down, q->ld_down, q->down_layout == SFNN_DOWN_NEURON_MAJOR};
+  return product(h, wd, q->T, q->d, q->n, nullptr, nullptr, 0, y, ldy, y_dtype == SFNN_F32, bf16, err, s);
+}
+
+sfnn_status sfnn_gated_backward(const sfnn_gated_desc *q, const void *dy, int64_t lddy, const sfnn_gated_saved *sv,
+                                void *dx, void *dw_gate, void *dw_up, void *dw_down, void *db, void *ws,
+                                int64_t ws_bytes, int32_t *err, sfnn_stream_t stream) {
+  if (!q || !sv) return SFNN_ERR_INVALID_ARG;
+  sfnn_gated_desc qq = *q;  // act8: x is not read, its blocks are
+  if (sv->kind == SFNN_SAVE_ACT8) {
+    qq.x = q->w_gate;
+    qq.ldx = q->ld_gate;
+  }
+  sfnn_status st = check(&qq);
+  if (st != SFNN_OK) return st;
+  if (q->down_layout != SFNN_DOWN_WIDTH_MAJOR) return SFNN_ERR_UNSUPPORTED;
+  if ((st = check_saved(q, sv)) != SFNN_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int T = q->T, d = q->d, n = q->n, bf16 = q->dtype == SFNN_BF16;
+  if ((dx && !a16(dx)) || (dw_gate && !a16(dw_gate)) || (dw_up && !a16(dw_up)) || (dw_down && !a16(dw_down)))
+    return SFNN_ERR_INVALID_ARG;
+  if (T == 0) {  // sums over no tokens
+    if ((dw_gate && cudaMemsetAsync(dw_gate, 0, (size_t)n * d * 2, s) != cudaSuccess) ||
+        (dw_up && cudaMemsetAsync(dw_up, 0, (size_t)n * d * 2, s) != cudaSuccess) ||
+        (dw_down && cudaMemsetAsync(dw_down, 0, (size_t)n * d * 2, s) != cudaSuccess) ||
+        (db && cudaMemsetAsync(db, 0, (size_t)n * 2, s) != cudaSuccess))
+      return SFNN_ERR_CUDA;
+    return SFNN_OK;
+  }
+  if (!mat_ok(dy, lddy, d) || !err || !ws || !a16(ws) || ws_bytes < sfnn_gated_workspace(T, d, n, 1))
+    return SFNN_ERR_INVALID_ARG;
+  const int64_t hb = hidden_bytes(T, n), ldh = up(n, 8);
+  unsigned char *w = static_cast<unsigned char *>(ws);
+  void *h = w, *dg = w + hb, *du = w + 2 * hb, *xr = w + 3 * hb;
+  float *part = reinterpret_cast<float *>(w + 3 * hb + hidden_bytes(T, d));
+
+  DenseParams P{};
+  P.M = T;
+  P.N = n;
+  P.nk0 = P.nk = chunks(d);
+  if (!set_pair(P, 0, Operand{dy, lddy, false}, Operand{q->w_down, q->ld_down, true}, T, n, d)) return SFNN_ERR_CUDA;
+  P.tiles_m = (T + 255) / 256;
+  P.tiles_n = (n + 255) / 256;
+  P.bf16 = bf16;
+  P.out = h;
+  P.dg = dg;
+  P.du = du;
+  P.ldo = ldh;
+  P.save = sv->kind;
+  P.r = sv->r;
+  P.u = sv->u;
+  P.ldr = sv->ld;
+  P.rs = sv->r_scales;
+  P.us = sv->u_scales;
+  P.lds = sv->lds;
+  P.err = err;
+  const int sms = num_sms_of_current();
+  if (launch_dense(P, kEpiDGated, false, true, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
+
+  Operand x{q->x, q->ldx, true};
+  if (sv->kind == SFNN_SAVE_ACT8 && (dw_gate || dw_up)) {
+    if (launch_act8_restore(static_cast<const uint8_t *>(sv->x), sv->ld_x, sv->x_scales, sv->lds_x, T, d, false, bf16, xr,
+                            up(d, 8), s) != cudaSuccess)
+      return SFNN_ERR_CUDA;
+    x = Operand{xr, up(d, 8), true};
+  }
+  if (db) {
+    const int splits = sum_splits(T);
+    if (launch_pdl(k_colsum, dim3((n + 63) / 64, splits), dim3(256), 0, s, static_cast<const uint16_t *>(dg), ldh, T, n,
+                   bf16, kSumRows, splits > 1 ? part : nullptr, db) != cudaSuccess)
+      return SFNN_ERR_CUDA;
+    if (splits > 1 && launch_pdl(k_colsum_join, dim3((n + 255) / 256), dim3(256), 0, s, part, splits, n, bf16,
+                                 static_cast<uint16_t *>(db)) != cudaSuccess)
+      return SFNN_ERR_CUDA;
+  }
+  if (dx) {
+    const Operand ag{dg, ldh, false}, au{du, ldh, false}, bg{q->w_gate, q->ld_gate, true}, bu{q->w_up, q->ld_up, true};
+    if ((st = product(ag, bg, T, d, n, &au, &bu, n, dx, d, 0, bf16, err, s)) != SFNN_OK) return st;
+  }
+  const Operand tg{dg, ldh, true}, tu{du, ldh, true}, th{h, ldh, true}, ty{dy, lddy, true};
+  if (dw_gate && (st = product(tg, x, n, d, T, nullptr, nullptr, 0, dw_gate, d, 0, bf16, err, s)) != SFNN_OK) return st;
+  if (dw_up && (st = product(tu, x, n, d, T, nullptr, nullptr, 0, dw_up, d, 0, bf16, err, s)) != SFNN_OK) return st;
+  if (dw_down && (st = product(ty, th, d, n, T, nullptr, nullptr, 0, dw_down, n, 0, bf16, err, s)) != SFNN_OK) return st;
+  return SFNN_OK;
+}
+
+sfnn_status sfnn_forward_prompt(sfnn_handle h, const void *X, int32_t T, float *Y, void *ws, int64_t ws_bytes,
+                                sfnn_stream_t stream) {
+  if (!h || T < 0) return SFNN_ERR_INVALID_ARG;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != h->device) return SFNN_ERR_INVALID_ARG;
+  const Layout &L = h->L;
+  if (L.dt != SFNN_F16 || L.rows_q) return SFNN_ERR_UNSUPPORTED;
+  if (T == 0) return SFNN_OK;
+  const uint16_t *rows = static_cast<const uint16_t *>(h->rows);
+  const int64_t ld = (int64_t)L.nproj * L.d;
+  if (L.act == SFNN_REGLU) {
+    sfnn_gated_desc q{};
+    q.T = T;
+    q.d = L.d;
+    q.n = L.n;
+    q.dtype = SFNN_F16;
+    q.down_layout = SFNN_DOWN_NEURON_MAJOR;
+    q.x = X;
+    q.ldx = L.d;
+    q.w_gate = rows;
+    q.w_up = rows + L.d;
+    q.w_down = rows + 2 * (int64_t)L.d;
+    q.ld_gate = q.ld_up = q.ld_down = ld;
+    q.b = h->bias;
+    const sfnn_status st = sfnn_gated_forward(&q, Y, L.d, SFNN_F32, nullptr, ws, ws_bytes, h->err, stream);
+    if (st == SFNN_OK) h->launches += 2;
+    return st;
+  }
+  if (!mat_ok(X, L.d, L.d) || !Y || !a16(Y) || !ws || !a16(ws) || ws_bytes < sfnn_gated_workspace(T, L.d, L.n, 0))
+    return SFNN_ERR_INVALID_ARG;
+  if (T > (1 << 24)) return SFNN_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const Operand x{X, L.d, false}, wu{rows, ld, false}, hh{ws, up(L.n, 8), false}, wd{rows + L.d, ld, true};
+  sfnn_status st = product(x, wu, T, L.n, L.d, nullptr, nullptr, 0, ws, up(L.n, 8), 0, 0, h->err, s, h->bias);
+  if (st == SFNN_OK) st = product(hh, wd, T, L.d, L.n, nullptr, nullptr, 0, Y, L.d, 1, 0, h->err, s);
+  if (st == SFNN_OK) h->launches += 2;
+  return st;
+}
+
+}  // extern "C"

@@ -86,7 +86,8 @@ typedef enum {
 } sfnn_status;
 
 typedef enum { SFNN_RELU = 0, SFNN_REGLU = 1 } sfnn_act;
-typedef enum { SFNN_F32 = 0, SFNN_F16 = 1, SFNN_I8 = 2, SFNN_I4 = 3 } sfnn_dtype;
+/* SFNN_BF16: the dense operators only (sfnn_gated_*, sfnn_act8_*, sfnn_mxfp4_*). */
+typedef enum { SFNN_F32 = 0, SFNN_F16 = 1, SFNN_I8 = 2, SFNN_I4 = 3, SFNN_BF16 = 4 } sfnn_dtype;
 
 /*
  * Which kernels the batched path (b > 1, and explicit sets) uses.  The tensor-core
@@ -422,6 +423,109 @@ SFNN_API sfnn_status sfnn_query(sfnn_handle h, sfnn_info *info);
 
 /* Return and clear the latched device-side error of h (synchronises h's device). */
 SFNN_API sfnn_status sfnn_get_error(sfnn_handle h);
+
+/*
+ * The gated FFN over all its neurons, for prompts, fine-tuning and dense layers:
+ *
+ *     G = X . W_gate^T + b,  U = X . W_up^T,  H = relu(G) * U,  Y = H . W_down^T
+ *
+ * and its backward pass
+ *
+ *     dH = dY . W_down,  dU = dH * relu(G),  dG = dH * U * [G > 0],
+ *     dX = dG . W_gate + dU . W_up,  dW_gate = dG^T . X,  dW_up = dU^T . X,
+ *     dW_down = dY^T . H,  db = sum over tokens of dG.
+ *
+ * fp16 or bf16 values (fp32: SFNN_ERR_UNSUPPORTED), fp32 sums on the tensor cores; H, dG
+ * and dU are rounded to the values' type between the products that make and read them.
+ * These calls need no handle: weights are read where the caller keeps them, and the caller
+ * gives the workspace (sfnn_gated_workspace bytes, 16-byte aligned), which is free again
+ * when the call's kernels have run and must not be shared by calls that run at the same
+ * time.  A bounded device-side wait that runs out stores SFNN_ERR_TIMEOUT in *err if it
+ * holds 0 (a device word that the caller zeroes; calls may share it).
+ *
+ * Matrices are row-major with a row stride in elements (a multiple of 8, at least the row's
+ * length) and a 16-byte aligned base; d must be a multiple of 8, and n too except for a
+ * forward pass with SFNN_DOWN_NEURON_MAJOR that saves nothing (else SFNN_ERR_UNSUPPORTED).
+ * T = 0 is valid: no token, zero weight gradients.
+ */
+#define SFNN_ACT8_BLOCK 64
+typedef enum {
+    SFNN_DOWN_WIDTH_MAJOR = 0, /* w_down [d x n], PyTorch's down.weight */
+    SFNN_DOWN_NEURON_MAJOR = 1 /* w_down [n x d], a row per neuron (forward only) */
+} sfnn_down_layout;
+/* What the forward pass keeps for the backward pass: nothing; relu(G) and U in the values'
+ * type (the caller keeps X); or X, relu(G) and U as 8-bit blocks (sfnn_act8_quantize). */
+typedef enum { SFNN_SAVE_NONE = 0, SFNN_SAVE_FULL = 1, SFNN_SAVE_ACT8 = 2 } sfnn_save;
+typedef struct {
+    int32_t T, d, n;         /* tokens, width, neurons */
+    int32_t dtype;           /* SFNN_F16 or SFNN_BF16: x, weights, b, gradients */
+    int32_t down_layout;     /* sfnn_down_layout */
+    int32_t reserved;
+    const void *x;           /* [T x d]; not read by a backward pass from 8-bit blocks */
+    int64_t ldx;
+    const void *w_gate;      /* [n x d] */
+    int64_t ld_gate;
+    const void *w_up;        /* [n x d] */
+    int64_t ld_up;
+    const void *w_down;
+    int64_t ld_down;
+    const void *b;           /* [n] or NULL (zeros) */
+} sfnn_gated_desc;
+typedef struct {
+    int32_t kind;            /* sfnn_save */
+    int32_t reserved;
+    void *r, *u;             /* [T x n] relu(G), U: values (FULL) or codes (ACT8), ld elements apart */
+    int64_t ld;              /* ACT8: a multiple of 16, at least n rounded up to 64 */
+    float *r_scales, *u_scales; /* ACT8: [T x n/64 rounded up], lds apart */
+    int64_t lds;
+    void *x;                 /* ACT8: X's codes, ld_x apart, and scales, lds_x apart */
+    int64_t ld_x;
+    float *x_scales;
+    int64_t lds_x;
+} sfnn_gated_saved;
+
+/* Workspace bytes of one call (negative: bad sizes). */
+SFNN_API int64_t sfnn_gated_workspace(int32_t T, int32_t d, int32_t n, int32_t backward);
+
+/* Y [T x d], ldy elements apart, in q->dtype or SFNN_F32; saved (may be NULL) is filled as
+ * its kind says. */
+SFNN_API sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, int32_t y_dtype,
+                                        sfnn_gated_saved *saved, void *ws, int64_t ws_bytes, int32_t *err,
+                                        sfnn_stream_t stream);
+
+/* The gradients, contiguous, in q->dtype: dx [T x d], dw_gate and dw_up [n x d], dw_down
+ * [d x n], db [n]; a NULL one is not computed.  w_down must be SFNN_DOWN_WIDTH_MAJOR. */
+SFNN_API sfnn_status sfnn_gated_backward(const sfnn_gated_desc *q, const void *dy, int64_t lddy,
+                                         const sfnn_gated_saved *saved, void *dx, void *dw_gate, void *dw_up,
+                                         void *dw_down, void *db, void *ws, int64_t ws_bytes, int32_t *err,
+                                         sfnn_stream_t stream);
+
+/*
+ * Y [T x d] for T tokens through ALL neurons of a handle's layer (a prompt): the dense FFN,
+ * the predictor is not used.  The handle's own rows are the products' operands, so the layer
+ * is held once for prompts and decode.  fp16 layers (fp32 and quantized rows:
+ * SFNN_ERR_UNSUPPORTED), X contiguous, T up to 2^24 and independent of max_batch; ws as
+ * sfnn_gated_forward's, sfnn_gated_workspace(T, d, n, 0) bytes.  Device-side errors are
+ * latched in the handle.
+ */
+SFNN_API sfnn_status sfnn_forward_prompt(sfnn_handle h, const void *X, int32_t T, float *Y, void *ws, int64_t ws_bytes,
+                                         sfnn_stream_t stream);
+
+/*
+ * 8-bit activation blocks.  Each 64 values of a row (the last block may be short) share an
+ * fp32 scale: with relu = 0, max|v| / 127 and signed codes; with relu = 1, relu(v) is held,
+ * scale max / 255 and codes 0..255, and a positive value keeps a code of at least 1, so
+ * that code > 0 is the ReLU's mask.  code = rint(v / scale).  A block with a NaN or an
+ * infinity restores as NaN; one whose largest magnitude is below 2^-119 is held as zeros.
+ * x [T x cols] fp16 or bf16 values, any row stride; code rows ldq bytes apart (a multiple
+ * of 16, at least cols rounded up to 64; columns past cols get code 0), 16-byte aligned;
+ * scale rows lds floats apart.
+ */
+SFNN_API sfnn_status sfnn_act8_quantize(const void *x, int64_t ldx, int32_t T, int32_t cols, int32_t dtype, int32_t relu,
+                                        void *codes, int64_t ldq, float *scales, int64_t lds, sfnn_stream_t stream);
+SFNN_API sfnn_status sfnn_act8_restore(const void *codes, int64_t ldq, const float *scales, int64_t lds, int32_t T,
+                                       int32_t cols, int32_t relu, int32_t dtype, void *out, int64_t ldo,
+                                       sfnn_stream_t stream);
 
 /* Static description of a status code; never NULL. */
 SFNN_API const char *sfnn_status_str(sfnn_status s);
