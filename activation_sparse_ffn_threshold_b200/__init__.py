@@ -17,6 +17,7 @@ The dense operators (no handle, fp16 or bf16, differentiable) are in ``dense``:
     y = gated_ffn(x, w_gate, w_up, w_down, b, checkpoint="act8")   # torch.autograd
     y, saved = gated_ffn_forward(...); grads = gated_ffn_backward(dy, saved, ...)
     q = quantize_act8(x); x = dequantize_act8(q)                   # 8-bit activation blocks
+    w = quantize_mxfp4(weight); y = mxfp4_linear(x, w)             # 4-bit weights and activations
 """
 from __future__ import annotations
 
@@ -30,7 +31,8 @@ __all__ = ["SparseFFN", "SfnnError", "forward_stack", "predict_noalloc", "hotnes
            "load_library",
            "RELU", "REGLU", "F32", "F16", "I8", "I4", "BATCH_AUTO", "BATCH_CUDA_CORE", "BATCH_TENSOR_CORE",
            "BATCH_FUSED", "BF16", "gated_ffn", "gated_ffn_forward", "gated_ffn_backward", "GatedSaved",
-           "quantize_act8", "dequantize_act8", "Act8", "dense_error"]
+           "quantize_act8", "dequantize_act8", "Act8", "dense_error", "quantize_mxfp4", "dequantize_mxfp4", "mxfp4_matmul",
+           "mxfp4_linear", "Mxfp4"]
 
 RELU, REGLU = 0, 1
 F32, F16, I8, I4, BF16 = 0, 1, 2, 3, 4
@@ -111,6 +113,12 @@ def load_library():
         "sfnn_gated_backward": ([P, P, L, P, P, P, P, P, P, P, L, P, P], S),
         "sfnn_forward_prompt": ([P, P, I, P, P, L, P], S),
         "sfnn_act8_quantize": ([P, L, I, I, I, I, P, L, P, L, P], S),
+        "sfnn_mxfp4_scale_bytes": ([L, I], L),
+        "sfnn_mxfp4_quantize": ([P, L, I, I, I, P, P, P], S),
+        "sfnn_mxfp4_restore": ([P, P, I, I, I, P, L, P], S),
+        "sfnn_mxfp4_product": ([P, P, I, P, P, I, I, P, L, I, P, P], S),
+        "sfnn_mxfp4_linear_workspace": ([I, I], L),
+        "sfnn_mxfp4_linear": ([P, L, I, I, P, P, I, I, P, L, I, P, L, P, P], S),
         "sfnn_act8_restore": ([P, L, P, L, I, I, I, I, P, L, P], S),
     }
     for name, (args, res) in sig.items():
@@ -425,5 +433,5 @@ def forward_stack(layers, X0, XL=None, idx=None, counts=None, return_sets: bool 
     return (XL, idx, counts) if return_sets else XL
 
 
-from .dense import (Act8, GatedSaved, dense_error, dequantize_act8, gated_ffn, gated_ffn_backward,  # noqa: E402
-                    gated_ffn_forward, quantize_act8)
+from .dense import (Act8, GatedSaved, Mxfp4, dense_error, dequantize_act8, dequantize_mxfp4, gated_ffn,  # noqa: E402
+                    gated_ffn_backward, gated_ffn_forward, mxfp4_linear, mxfp4_matmul, quantize_act8, quantize_mxfp4)

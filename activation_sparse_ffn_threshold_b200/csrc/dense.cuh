@@ -99,6 +99,8 @@ cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &ready) {
   return e;
 }
 
+int device_sms();  // SMs of the current device (0: no device)
+
 cudaError_t launch_dense(const DenseParams &P, int epi, bool a_mn, bool b_mn, int num_sms, cudaStream_t s);
 
 // Rows of 16-bit values to act8 blocks and back (act8.cu).  Code rows are ldq bytes apart

@@ -7,9 +7,8 @@
 #include "launch.cuh"
 
 namespace sfnn {
-namespace {
 
-int num_sms_of_current() {
+int device_sms() {
   static std::atomic<int> known[64];
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
@@ -22,6 +21,8 @@ int num_sms_of_current() {
   if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
+
+namespace {
 
 // ---------------------------------------------------------------- column sums (db)
 // db[i] = sum over tokens of dG[t][i].  A block sums 64 columns of its share of the rows:
@@ -154,7 +155,7 @@ sfnn_status product(const Operand &a, const Operand &b, int M, int N, int64_t K,
   P.ldo = ldo;
   P.out32 = out32;
   P.err = err;
-  return launch_dense(P, kEpiStore, a.mn, b.mn, num_sms_of_current(), s) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
+  return launch_dense(P, kEpiStore, a.mn, b.mn, device_sms(), s) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
 }
 
 }  // namespace
@@ -211,7 +212,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
     P.lds = sv->lds;
   }
   P.err = err;
-  if (launch_dense(P, kEpiGated, false, false, num_sms_of_current(), s) != cudaSuccess) return SFNN_ERR_CUDA;
+  if (launch_dense(P, kEpiGated, false, false, device_sms(), s) != cudaSuccess) return SFNN_ERR_CUDA;
   const Operand h{ws, ldh, false}, wd{q->w_down, q->ld_down, q->down_layout == SFNN_DOWN_NEURON_MAJOR};
   return product(h, wd, q->T, q->d, q->n, nullptr, nullptr, 0, y, ldy, y_dtype == SFNN_F32, bf16, err, s);
 }
@@ -268,7 +269,7 @@ sfnn_status sfnn_gated_backward(const sfnn_gated_desc *q, const void *dy, int64_
   P.us = sv->u_scales;
   P.lds = sv->lds;
   P.err = err;
-  const int sms = num_sms_of_current();
+  const int sms = device_sms();
   if (launch_dense(P, kEpiDGated, false, true, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
 
   Operand x{q->x, q->ldx, true};

@@ -1,4 +1,4 @@
-"""The dense operators: the gated FFN with its backward pass, 8-bit activation blocks.
+"""The dense operators: the gated FFN with its backward pass, 8-bit activation blocks, MXFP4.
 
 As the rest of the binding, this module only checks and marshals arguments into
 ``libsfnn.so`` (include/sfnn.h); PyTorch provides memory, streams and the autograd graph.
@@ -16,7 +16,7 @@ from torch.autograd.function import once_differentiable
 from . import BF16, F16, F32, SfnnError, _check, load_library
 
 __all__ = ["gated_ffn", "gated_ffn_forward", "gated_ffn_backward", "GatedSaved", "quantize_act8", "dequantize_act8",
-           "Act8", "dense_error"]
+           "Act8", "dense_error", "quantize_mxfp4", "dequantize_mxfp4", "mxfp4_matmul", "mxfp4_linear", "Mxfp4"]
 
 SAVE = {None: 0, "full": 1, "act8": 2}
 ACT8_BLOCK = 64
@@ -201,6 +201,92 @@ def dequantize_act8(q: Act8, dtype=None, out=None, stream=None):
                                                 q.scales.shape[1], T, cols, int(q.relu), code, p, ld, at.raw),
                "sfnn_act8_restore")
     return out
+
+
+# ------------------------------------------------------------------ mxfp4
+class Mxfp4:
+    """Rows held as 4-bit codes with a power of two per 32 values (sfnn_mxfp4_quantize)."""
+
+    __slots__ = ("codes", "scales", "shape", "dtype")
+
+    def __init__(self, codes, scales, shape, dtype):
+        self.codes, self.scales, self.shape, self.dtype = codes, scales, shape, dtype
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def quantize_mxfp4(x, stream=None) -> Mxfp4:
+    """x [..., K] (K a multiple of 32) as MXFP4 rows."""
+    code = _code(x.dtype) if isinstance(x, torch.Tensor) else 0
+    p, R, K, ld = _rows(x, "x")
+    if K % 32 or not K:
+        raise ValueError(f"the last dimension must be a positive multiple of 32, got {K}")
+    if ld < K:
+        raise ValueError("x: rows must not overlap")
+    lib = load_library()
+    with _Place(x.device, stream) as at:
+        q = torch.empty((R, K // 2), dtype=torch.uint8, device=x.device)
+        s = torch.empty(lib.sfnn_mxfp4_scale_bytes(R, K), dtype=torch.uint8, device=x.device)
+        _check(lib.sfnn_mxfp4_quantize(p, ld, R, K, code, q.data_ptr(), s.data_ptr(), at.raw), "sfnn_mxfp4_quantize")
+    return Mxfp4(q, s, tuple(x.shape), x.dtype)
+
+
+def dequantize_mxfp4(q: Mxfp4, dtype=None, stream=None):
+    """The values that q stands for, in ``dtype`` (default: the quantised tensor's)."""
+    dtype = dtype or q.dtype
+    K = q.shape[-1]
+    with _Place(q.codes.device, stream) as at:
+        out = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
+        _check(load_library().sfnn_mxfp4_restore(q.codes.data_ptr(), q.scales.data_ptr(), q.codes.shape[0], K,
+                                                 _code(dtype), out.data_ptr(), K, at.raw), "sfnn_mxfp4_restore")
+    return out
+
+
+def _mx_out(shape, w, out_dtype, device):
+    if not isinstance(w, Mxfp4) or len(w.shape) != 2 or not w.shape[0]:
+        raise TypeError("w must be an Mxfp4 of a matrix [N, K]")
+    if shape[-1] != w.shape[1]:
+        raise ValueError(f"x has {shape[-1]} columns, w {w.shape[1]}")
+    if w.codes.device != device:
+        raise ValueError("all tensors must be on one device")
+    return F32 if out_dtype == torch.float32 else _code(out_dtype)
+
+
+def mxfp4_matmul(x: Mxfp4, w: Mxfp4, out_dtype=None, stream=None):
+    """x w^T for x [..., K] and w [N, K], both MXFP4; ``out_dtype`` (fp16, bf16 or fp32)
+    defaults to the tensor's that x was quantised from."""
+    dt = out_dtype or x.dtype
+    dev = x.codes.device
+    code = _mx_out(x.shape, w, dt, dev)
+    N, K = w.shape
+    T = x.codes.shape[0]
+    with _Place(dev, stream) as at:
+        y = torch.empty(x.shape[:-1] + (N,), dtype=dt, device=dev)
+        _check(load_library().sfnn_mxfp4_product(x.codes.data_ptr(), x.scales.data_ptr(), T, w.codes.data_ptr(),
+                                                 w.scales.data_ptr(), N, K, y.data_ptr(), N, code,
+                                                 _err_word(dev).data_ptr(), at.raw), "sfnn_mxfp4_product")
+    return y
+
+
+def mxfp4_linear(x, w: Mxfp4, out_dtype=None, stream=None):
+    """A linear layer with MXFP4 weights: x [..., K] in fp16 or bf16 is quantised by the call."""
+    dt = out_dtype or (x.dtype if isinstance(x, torch.Tensor) else None)
+    p, T, K, ld = _rows(x, "x")
+    xcode = _code(x.dtype)
+    dev = x.device
+    code = _mx_out(x.shape, w, dt, dev)
+    if ld < K:
+        raise ValueError("x: rows must not overlap")
+    N = w.shape[0]
+    lib = load_library()
+    with _Place(dev, stream) as at:
+        y = torch.empty(x.shape[:-1] + (N,), dtype=dt, device=dev)
+        ws = torch.empty(max(16, lib.sfnn_mxfp4_linear_workspace(T, K)), dtype=torch.uint8, device=dev)
+        _check(lib.sfnn_mxfp4_linear(p, ld, T, xcode, w.codes.data_ptr(), w.scales.data_ptr(), N, K, y.data_ptr(), N, code,
+                                     ws.data_ptr(), ws.numel(), _err_word(dev).data_ptr(), at.raw), "sfnn_mxfp4_linear")
+    return y
 
 
 # ------------------------------------------------------------------ gated FFN

@@ -527,6 +527,33 @@ SFNN_API sfnn_status sfnn_act8_restore(const void *codes, int64_t ldq, const flo
                                        int32_t cols, int32_t relu, int32_t dtype, void *out, int64_t ldo,
                                        sfnn_stream_t stream);
 
+/*
+ * Microscaled 4-bit values (MXFP4).  32 values along a row share a power of two 2^e,
+ * e = floor(log2 max|v|) - 2 clamped to [-127, 127]; each is held as one of 0, .5, 1, 1.5,
+ * 2, 3, 4, 6 times 2^e with a sign, rounded to nearest even, saturating at 6.  A block with a
+ * NaN or an infinity stands for NaNs.  Codes: two a byte, element 2k in the low nibble, rows
+ * of K / 2 bytes without gaps.  Scales: sfnn_mxfp4_scale_bytes bytes, a byte e + 127 (255:
+ * NaN) for row r, block c at ((r / 128) KT + c / 4) 512 + (r % 32) 16 + (r / 32 % 4) 4 + c % 4
+ * with KT = 2 ceil(K / 256), rows padded to 256; padding holds zero bytes.
+ * K must be a multiple of 32 (else SFNN_ERR_UNSUPPORTED); codes and scales start on 16-byte
+ * boundaries; x and out have any row stride of at least K.
+ */
+SFNN_API int64_t sfnn_mxfp4_scale_bytes(int64_t rows, int32_t K);
+SFNN_API sfnn_status sfnn_mxfp4_quantize(const void *x, int64_t ldx, int32_t rows, int32_t K, int32_t dtype, void *codes,
+                                         void *scales, sfnn_stream_t stream);
+SFNN_API sfnn_status sfnn_mxfp4_restore(const void *codes, const void *scales, int32_t rows, int32_t K, int32_t dtype,
+                                        void *out, int64_t ldo, sfnn_stream_t stream);
+/* Y [T x N] = Xq . Wq^T in fp32 sums; y_dtype SFNN_F16, SFNN_BF16 or SFNN_F32; err as for
+ * sfnn_gated_forward. */
+SFNN_API sfnn_status sfnn_mxfp4_product(const void *x_codes, const void *x_scales, int32_t T, const void *w_codes,
+                                        const void *w_scales, int32_t N, int32_t K, void *y, int64_t ldy, int32_t y_dtype,
+                                        int32_t *err, sfnn_stream_t stream);
+/* The same for x [T x K] in fp16 or bf16, quantised by the call (workspace as sfnn_gated_forward's). */
+SFNN_API int64_t sfnn_mxfp4_linear_workspace(int32_t T, int32_t K);
+SFNN_API sfnn_status sfnn_mxfp4_linear(const void *x, int64_t ldx, int32_t T, int32_t dtype, const void *w_codes,
+                                       const void *w_scales, int32_t N, int32_t K, void *y, int64_t ldy, int32_t y_dtype,
+                                       void *ws, int64_t ws_bytes, int32_t *err, sfnn_stream_t stream);
+
 /* Static description of a status code; never NULL. */
 SFNN_API const char *sfnn_status_str(sfnn_status s);
 

@@ -105,3 +105,35 @@ def test_binding_refuses_host_tensors():
         sf.quantize_act8(x)
     with pytest.raises(TypeError):
         sf.quantize_act8(x.float())
+
+
+def test_mxfp4_refuses():
+    lib = sf.load_library()
+    assert lib.sfnn_mxfp4_scale_bytes(1, 32) == 2 * 2 * 512 and lib.sfnn_mxfp4_scale_bytes(257, 288) == 4 * 4 * 512
+    assert lib.sfnn_mxfp4_scale_bytes(-1, 32) < 0 and lib.sfnn_mxfp4_linear_workspace(1, 0) < 0
+
+    def quant(x=4096, ldx=64, rows=2, K=64, dtype=sf.F16, codes=4096, scales=4096):
+        return lib.sfnn_mxfp4_quantize(x, ldx, rows, K, dtype, codes, scales, None)
+    for kw, want in ((dict(x=None), INVALID), (dict(ldx=63), INVALID), (dict(rows=-1), INVALID), (dict(K=0), INVALID),
+                     (dict(K=48, ldx=48), UNSUPPORTED), (dict(dtype=sf.F32), INVALID), (dict(codes=4104), INVALID),
+                     (dict(scales=None), INVALID), (dict(K=(1 << 20) + 32, ldx=1 << 21), UNSUPPORTED),
+                     (dict(rows=(1 << 24) + 1), UNSUPPORTED)):
+        assert quant(**kw) == want, kw
+    assert quant(rows=0) == 0
+    assert lib.sfnn_mxfp4_restore(4096, 4096, 2, 64, sf.I4, 4096, 64, None) == INVALID
+
+    def prod(xc=4096, T=4, wc=4096, N=8, K=64, y=4096, ldy=8, dt=sf.F32, err=4096):
+        return lib.sfnn_mxfp4_product(xc, 4096, T, wc, 4096, N, K, y, ldy, dt, err, None)
+    for kw in (dict(xc=None), dict(T=-1), dict(wc=8), dict(N=0), dict(y=None), dict(ldy=7), dict(dt=sf.I8),
+               dict(err=None), dict(y=4097)):
+        assert prod(**kw) == INVALID, kw
+    assert prod(K=40) == UNSUPPORTED and prod(T=0) == 0
+
+    def linear(ws=4096, nbytes=1 << 30, x=4096, ldx=64):
+        return lib.sfnn_mxfp4_linear(x, ldx, 4, sf.F16, 4096, 4096, 8, 64, 4096, 8, sf.F16, ws, nbytes, 4096, None)
+    assert linear(ws=None) == INVALID and linear(nbytes=8) == INVALID and linear(x=None) == INVALID
+    assert linear(ldx=32) == INVALID
+    with pytest.raises(TypeError):
+        sf.quantize_mxfp4(torch.zeros(2, 64, dtype=torch.float16))
+    with pytest.raises(TypeError):
+        sf.mxfp4_linear(torch.zeros(2, 64, dtype=torch.float16), None)
