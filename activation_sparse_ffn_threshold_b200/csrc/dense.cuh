@@ -103,6 +103,22 @@ int device_sms();  // SMs of the current device (0: no device)
 
 cudaError_t launch_dense(const DenseParams &P, int epi, bool a_mn, bool b_mn, int num_sms, cudaStream_t s);
 
+// The products of few tokens (slim.cu): out = x . w0^T, or with w1 the gated hidden layer
+// relu(x . w0^T + bias) * (x . w1^T).  K-major weights; `early`: w0 may be read while the
+// kernel launched before still runs (it waited for everything before it).
+struct SlimArgs {
+  const void *x, *w0, *w1, *bias;
+  int64_t ldx, ldw0, ldw1;
+  int T, N;
+  int64_t K;
+  void *out;
+  int64_t ldo;
+  int bf16, out32, relu, early;
+  int32_t *err;
+};
+bool slim_serves(int T);
+sfnn_status launch_slim(const SlimArgs &q, int num_sms, cudaStream_t s);
+
 // Rows of 16-bit values to act8 blocks and back (act8.cu).  Code rows are ldq bytes apart
 // (a multiple of 16, at least T's columns rounded up to 64), scale rows lds floats.
 cudaError_t launch_act8_quantize(const void *x, int64_t ldx, int T, int cols, int bf16, bool relu, uint8_t *codes,

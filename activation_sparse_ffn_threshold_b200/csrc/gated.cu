@@ -188,6 +188,46 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
       launch_act8_quantize(q->x, q->ldx, q->T, q->d, bf16, false, static_cast<uint8_t *>(sv->x), sv->ld_x,
                            sv->x_scales, sv->lds_x, s) != cudaSuccess)
     return SFNN_ERR_CUDA;
+  const bool slim = slim_serves(q->T);
+  const Operand h{ws, ldh, false}, wd{q->w_down, q->ld_down, q->down_layout == SFNN_DOWN_NEURON_MAJOR};
+  auto down = [&](int early) -> sfnn_status {
+    if (!slim || wd.mn)
+      return product(h, wd, q->T, q->d, q->n, nullptr, nullptr, 0, y, ldy, y_dtype == SFNN_F32, bf16, err, s);
+    SlimArgs a{};
+    a.x = ws;
+    a.ldx = ldh;
+    a.w0 = q->w_down;
+    a.ldw0 = q->ld_down;
+    a.T = q->T;
+    a.N = q->d;
+    a.K = q->n;
+    a.out = y;
+    a.ldo = ldy;
+    a.bf16 = bf16;
+    a.out32 = y_dtype == SFNN_F32;
+    a.early = early;
+    a.err = err;
+    return launch_slim(a, device_sms(), s);
+  };
+  if (slim && kind == SFNN_SAVE_NONE) {
+    SlimArgs a{};
+    a.x = q->x;
+    a.ldx = q->ldx;
+    a.w0 = q->w_gate;
+    a.ldw0 = q->ld_gate;
+    a.w1 = q->w_up;
+    a.ldw1 = q->ld_up;
+    a.bias = q->b;
+    a.T = q->T;
+    a.N = q->n;
+    a.K = q->d;
+    a.out = ws;
+    a.ldo = ldh;
+    a.bf16 = bf16;
+    a.err = err;
+    if ((st = launch_slim(a, device_sms(), s)) != SFNN_OK) return st;
+    return down(1);
+  }
   DenseParams P{};
   P.M = q->T;
   P.N = q->n;
@@ -213,8 +253,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
   }
   P.err = err;
   if (launch_dense(P, kEpiGated, false, false, device_sms(), s) != cudaSuccess) return SFNN_ERR_CUDA;
-  const Operand h{ws, ldh, false}, wd{q->w_down, q->ld_down, q->down_layout == SFNN_DOWN_NEURON_MAJOR};
-  return product(h, wd, q->T, q->d, q->n, nullptr, nullptr, 0, y, ldy, y_dtype == SFNN_F32, bf16, err, s);
+  return down(0);
 }
 
 sfnn_status sfnn_gated_backward(const sfnn_gated_desc *q, const void *dy, int64_t lddy, const sfnn_gated_saved *sv,

@@ -73,7 +73,8 @@ SHAPES = [(1, 8, 8), (1, 512, 2048), (2, 64, 64), (5, 72, 40), (31, 136, 1000), 
 
 
 @pytest.mark.parametrize("dt", KINDS)
-@pytest.mark.parametrize("T,d,n", SHAPES)
+@pytest.mark.parametrize("T,d,n", SHAPES + [(33, 1000, 4096), (40, 520, 1024), (64, 264, 8200), (100, 2048, 4104),
+                                            (128, 4096, 2504), (1, 4096, 11008), (3, 1024, 28672), (2, 24, 40000)])
 def test_forward(T, d, n, dt):
     x, wg, wu, wd, b, _ = layer(T, d, n, dt, seed=T + d, pad=8 * (T % 3), bias=T % 2 == 1)
     y, saved = sf.gated_ffn_forward(x, wg, wu, wd, b)
