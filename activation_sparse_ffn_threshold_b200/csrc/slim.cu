@@ -1,17 +1,16 @@
 // slim.cu -- the dense products for few tokens (T <= 128): bound by the weights' bytes.
 //
-// The tokens lie on the MMA's M side (128 lanes, T of them real; the rest of the A tile is
-// whatever shared memory holds, and only reaches accumulator lanes nobody reads), the
-// weights on its N side, so a CTA can own ANY number of weight rows: the rows are dealt out
-// evenly over the SMs (75 or 76 neurons each of 11008 over 148), every CTA streams its own
-// rows over all of K once, and nothing is split or joined.  A stage holds one or more
-// 64-deep chunks of every row (TMA, 128-byte swizzle), as many stages as about 100 KB hold,
-// so that two CTAs of consecutive kernels fit one SM: the down projection's CTA starts
-// while the gate/up kernel drains, and requests its first weights before it waits for H.
+// The weights lie on the MMA's M side (128 lanes), the tokens on its N side.  A tile need not
+// fill the 128 lanes: the rest of the A tile is whatever shared memory holds, and only
+// reaches accumulator lanes nobody reads.  So a tile is any number of weight rows, the rows
+// are dealt out evenly over the SMs (75 neurons each of 11008 over 148), and every byte of
+// them is read once.  Where an even share would be a thin tile (28 of 4096 rows of the down
+// projection: an MMA reads all 128 lanes of A from shared memory, so a thin tile's weights
+// pass slower than they come from DRAM), a cluster of 2 or 4 CTAs takes a wider tile, splits
+// its K, and adds the parts through distributed shared memory in rank order.
 //
-// Down projection with more than 32 tokens: a CTA's share of the weight rows (28 of 4096)
-// no longer outweighs the H rows it reads with them, so a cluster of CTAs splits K over wider
-// tiles and adds its parts through distributed shared memory in rank order.
+// A stage holds at least two 64-deep chunks of every row: 256 contiguous bytes of it (TMA,
+// 128-byte swizzle).
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,19 +20,19 @@
 namespace sfnn {
 namespace {
 
-constexpr int kThreads = 192;  // warp 0 loads, warp 1 issues the MMAs, warps 2-5 take 32 tokens each
+constexpr int kThreads = 192;  // warp 0 loads, warp 1 issues the MMAs, warps 2-5 take 32 weight rows each
 constexpr int kMaxStages = 8;
 
 struct alignas(64) SlimParams {
-  CUtensorMap a, b0, b1;
+  CUtensorMap x, w0, w1;
   int T, N, nk;         // nk: 64-deep chunks of K
-  int nb, nb8, n16;     // weight rows of a tile; rounded up to 8 (bytes), to 16 (MMA N)
+  int nb, nb8;          // weight rows of a tile; rounded up to 8 (its place in a stage)
   int tiles;
-  int tb8;              // T rounded up to 8
+  int t8, t16;          // T rounded up to 8 (rows loaded), to 16 (MMA N)
   int kps, stages;      // chunks per stage
   int split;            // CTAs of a cluster that share a tile's K
   int early;            // weights may be read before the kernel before has finished
-  int tmem_cols;
+  int tmem_cols, up_col;
   int bf16, out32, relu;
   const void *bias;
   void *out;
@@ -41,23 +40,18 @@ struct alignas(64) SlimParams {
   int32_t *err;
 };
 
-// `cols` values of one token to p (4-byte aligned when 16-bit: tiles start on even columns).
-__device__ __forceinline__ void store_cols(const SlimParams &P, int64_t row, int col, const float v[32], int cols) {
+// This thread's weight row: its accumulators of tokens [t0, t0 + 32) -> out[t][col].
+__device__ __forceinline__ void store_tokens(const SlimParams &P, int col, int t0, const float v[32]) {
   if (P.out32) {
-    float *o = static_cast<float *>(P.out) + row * P.ldo + col;
+    float *o = static_cast<float *>(P.out) + t0 * P.ldo + col;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      if (i < cols) o[i] = v[i];
+      if (t0 + i < P.T) o[i * P.ldo] = v[i];
   } else {
-    uint16_t *o = static_cast<uint16_t *>(P.out) + row * P.ldo + col;
+    uint16_t *o = static_cast<uint16_t *>(P.out) + t0 * P.ldo + col;
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const uint32_t w = pack16(v[i], v[i + 1], P.bf16);
-      if (i + 1 < cols)
-        *reinterpret_cast<uint32_t *>(o + i) = w;
-      else if (i < cols)
-        o[i] = (uint16_t)w;
-    }
+    for (int i = 0; i < 32; ++i)
+      if (t0 + i < P.T) o[i * P.ldo] = (uint16_t)pack16(v[i], 0.f, P.bf16);
   }
 }
 
@@ -66,19 +60,21 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty;
   __shared__ uint32_t tmem_slot;
+  constexpr int NP = GATED ? 2 : 1;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t stage0 = (raw + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = GATED ? 1 : P.split;
+  const int split = P.split;
   const int part = split > 1 ? (int)cluster_rank() : 0;
   const int unit = blockIdx.x / split, units = gridDim.x / split;
-  const uint32_t a_bytes = (uint32_t)P.tb8 * 128u, b_bytes = (uint32_t)P.nb8 * 128u;
-  const uint32_t chunk_bytes = a_bytes + (GATED ? 2u : 1u) * b_bytes;
+  // a chunk: the tokens' rows, then the weight tiles (an MMA reads past a tile's rows into
+  // what follows, at the end into the overhang behind the last stage)
+  const uint32_t x_bytes = (uint32_t)P.t8 * 128u, w_bytes = (uint32_t)P.nb8 * 128u;
+  const uint32_t chunk_bytes = x_bytes + NP * w_bytes;
   const uint32_t stage_bytes = chunk_bytes * (uint32_t)P.kps;
   const int stages = P.stages;
   const int k_lo = (int)((int64_t)part * P.nk / split), k_hi = (int)((int64_t)(part + 1) * P.nk / split);
   const int steps = (k_hi - k_lo + P.kps - 1) / P.kps;
-  const uint32_t up_col = (uint32_t)P.n16;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -97,27 +93,25 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
 
   if (warp == 0) {
     if (lane == 0) {
-      // the box rows are tb8 and nb: a tile's rows past N and T read as zeros and still count
-      auto load_b = [&](int s, int t, int k0, int kn) {
-        const uint32_t st = stage0 + (uint32_t)s * stage_bytes;
-        for (int c = 0; c < kn; ++c) {
-          const uint32_t at = st + (uint32_t)c * chunk_bytes + a_bytes;
-          tma_load_2d(at, &P.b0, (k0 + c) * 64, t * P.nb, &full[s]);
-          if (GATED) tma_load_2d(at + b_bytes, &P.b1, (k0 + c) * 64, t * P.nb, &full[s]);
-        }
+      auto load_w = [&](int s, int t, int k0, int kn) {
+        const uint32_t at = stage0 + (uint32_t)s * stage_bytes + x_bytes;
+        for (int c = 0; c < kn; ++c) tma_load_2d(at + (uint32_t)c * chunk_bytes, &P.w0, (k0 + c) * 64, t * P.nb, &full[s]);
+        if (GATED)
+          for (int c = 0; c < kn; ++c)
+            tma_load_2d(at + w_bytes + (uint32_t)c * chunk_bytes, &P.w1, (k0 + c) * 64, t * P.nb, &full[s]);
       };
-      auto load_a = [&](int s, int k0, int kn) {
+      auto load_x = [&](int s, int k0, int kn) {
         const uint32_t st = stage0 + (uint32_t)s * stage_bytes;
-        for (int c = 0; c < kn; ++c) tma_load_2d(st + (uint32_t)c * chunk_bytes, &P.a, (k0 + c) * 64, 0, &full[s]);
+        for (int c = 0; c < kn; ++c) tma_load_2d(st + (uint32_t)c * chunk_bytes, &P.x, (k0 + c) * 64, 0, &full[s]);
       };
-      const uint32_t chunk_tx = a_bytes + (GATED ? 2u : 1u) * (uint32_t)P.nb * 128u;
-      const int pre = P.early ? min(stages, steps) : 0;
-      if (unit < P.tiles)
-        for (int i = 0; i < pre; ++i) {
-          const int k0 = k_lo + i * P.kps, kn = min(P.kps, k_hi - k0);
-          bar_expect_tx(&full[i], chunk_tx * (uint32_t)kn);
-          load_b(i, unit, k0, kn);
-        }
+      // rows of a box past T or N read as zeros and count like the others
+      const uint32_t chunk_tx = x_bytes + NP * (uint32_t)P.nb * 128u;
+      const int pre = P.early && unit < P.tiles ? min(stages, steps) : 0;
+      for (int i = 0; i < pre; ++i) {
+        const int k0 = k_lo + i * P.kps, kn = min(P.kps, k_hi - k0);
+        bar_expect_tx(&full[i], chunk_tx * (uint32_t)kn);
+        load_w(i, unit, k0, kn);
+      }
       pdl_wait();
       pdl_launch_dependents();
       int it = 0;
@@ -131,9 +125,9 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
               break;
             }
             bar_expect_tx(&full[s], chunk_tx * (uint32_t)kn);
-            load_b(s, t, k0, kn);
+            load_w(s, t, k0, kn);
           }
-          load_a(s, k0, kn);
+          load_x(s, k0, kn);
         }
       }
       for (int s = 0; s < stages && ok; ++s) {  // every load has been consumed before the CTA ends
@@ -144,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = mma_desc_16(128, P.n16, P.bf16, 0, 0);
+      const uint32_t idesc = mma_desc_16(128, P.t16, P.bf16, 0, 0);
       int it = 0, n = 0;
       bool ok = true;
       for (int t = unit; t < P.tiles && ok; t += units, ++n) {
@@ -161,13 +155,13 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
           }
           tm_fence_after();
           for (int c = 0; c < kn; ++c) {
-            const uint32_t a = stage0 + (uint32_t)s * stage_bytes + (uint32_t)c * chunk_bytes, b = a + a_bytes;
+            const uint32_t x = stage0 + (uint32_t)s * stage_bytes + (uint32_t)c * chunk_bytes, w = x + x_bytes;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t acc = (i > 0 || c > 0 || k > 0) ? 1u : 0u;
-              const uint64_t da = mat_desc(a + k * 32, 16, 1024);
-              mma_16<1>(tmem, da, mat_desc(b + k * 32, 16, 1024), idesc, acc);
-              if (GATED) mma_16<1>(tmem + up_col, da, mat_desc(b + b_bytes + k * 32, 16, 1024), idesc, acc);
+              const uint64_t dx = mat_desc(x + k * 32, 16, 1024);
+              mma_16<1>(tmem, mat_desc(w + k * 32, 16, 1024), dx, idesc, acc);
+              if (GATED) mma_16<1>(tmem + (uint32_t)P.up_col, mat_desc(w + w_bytes + k * 32, 16, 1024), dx, idesc, acc);
             }
           }
           mma_commit(&empty[s]);
@@ -176,11 +170,46 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
       }
       if (!ok) latch_error(P.err, kErrTimeout);
     }
-  } else {
-    const int quad = warp & 3;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const int row = quad * 32 + lane;
-    const bool busy = quad * 32 < P.T;
+  }
+  const int quad = warp & 3, row = quad * 32 + lane;
+  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+  const bool worker = warp >= 2;
+  // the epilogue of this thread's weight row, with the other parts of a split tile at `sums`
+  auto epilogue = [&](int t, const float *sums) {
+    const int col = t * P.nb + row;
+    const bool live = row < P.nb && col < P.N;
+    const float bias = (GATED || P.relu) && P.bias && live ? load16(P.bias, col, P.bf16) : 0.f;
+    for (int c = 0; c < P.T; c += 32) {
+      uint32_t g[32], u[32];
+      float v[32];
+      __syncwarp();
+      tm_ld32(lanes + c, g);
+      if (GATED) tm_ld32(lanes + (uint32_t)P.up_col + c, u);
+      tm_wait_ld();
+      if (!live) continue;
+      if (sums)
+        for (int p = 0; p < split - 1; ++p) {
+          const float *a = sums + ((size_t)(p * NP) * P.t16 + c) * 128 + row;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < P.T) {
+              g[i] = __float_as_uint(__uint_as_float(g[i]) + a[i * 128]);
+              if (GATED) u[i] = __float_as_uint(__uint_as_float(u[i]) + a[(P.t16 + i) * 128]);
+            }
+        }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        v[i] = __uint_as_float(g[i]);
+        if (GATED || P.relu) {
+          v[i] += bias;
+          v[i] = v[i] < 0.f ? 0.f : v[i];
+        }
+        if (GATED) v[i] *= __uint_as_float(u[i]);
+      }
+      store_tokens(P, col, c, v);
+    }
+  };
+  if (worker) {
     pdl_wait();  // nothing is written before the kernel before has finished
     int n = 0;
     for (int t = unit; t < P.tiles; t += units, ++n) {
@@ -190,37 +219,8 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
       }
       __syncwarp();
       tm_fence_after();
-      const int n0 = t * P.nb, rows = min(P.nb, P.N - n0);
       if (split > 1) break;  // one tile per cluster, joined below
-      if (busy)
-        for (int c = 0; c < rows; c += 32) {
-          uint32_t g[32];
-          float v[32];
-          __syncwarp();
-          tm_ld32(lanes + c, g);
-          if (GATED) {
-            uint32_t u[32];
-            tm_ld32(lanes + up_col + c, u);
-            tm_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float x = __uint_as_float(g[i]);
-              if (P.bias && c + i < rows) x += load16(P.bias, n0 + c + i, P.bf16);
-              v[i] = (x < 0.f ? 0.f : x) * __uint_as_float(u[i]);
-            }
-          } else {
-            tm_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              v[i] = __uint_as_float(g[i]);
-              if (P.relu) {
-                if (P.bias && c + i < rows) v[i] += load16(P.bias, n0 + c + i, P.bf16);
-                v[i] = v[i] < 0.f ? 0.f : v[i];
-              }
-            }
-          }
-          if (row < P.T) store_cols(P, row, n0 + c, v, rows - c);
-        }
+      if (quad * 32 < P.nb) epilogue(t, nullptr);
       tm_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty, 0));
@@ -230,46 +230,29 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
   if (split > 1) {
     // Every CTA of the cluster has its accumulators: the others put theirs into rank 0's
     // stage memory (no load or MMA touches it any more), rank 0 adds them in rank order.
-    const int quad = warp & 3, row = quad * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const bool busy = warp >= 2 && quad * 32 < P.T;
-    const int n0 = unit * P.nb, rows = min(P.nb, P.N - n0);
     const uint32_t sums = stage0 - raw;  // the same offset in every CTA
+    const bool busy = worker && quad * 32 < P.nb;
     cluster_sync_all();
     tm_fence_after();
     if (busy && part > 0) {
-      const uint32_t dst0 = cluster_addr(smem_raw, 0) + sums;
-      for (int c = 0; c < rows; c += 32) {
-        uint32_t g[32];
-        __syncwarp();
-        tm_ld32(lanes + c, g);
-        tm_wait_ld();
-        const uint32_t dst = dst0 + (uint32_t)(((part - 1) * P.n16 + c) * 128 + row) * 4u;
+      const uint32_t dst0 = cluster_addr(smem_raw, 0) + sums + (uint32_t)((part - 1) * NP * P.t16 * 128 + row) * 4u;
+#pragma unroll 1
+      for (int p = 0; p < NP; ++p)
+        for (int c = 0; c < P.T; c += 32) {
+          uint32_t g[32];
+          __syncwarp();
+          tm_ld32(lanes + (uint32_t)(p * P.up_col + c), g);
+          tm_wait_ld();
+          const uint32_t dst = dst0 + (uint32_t)(p * P.t16 + c) * 512u;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < rows)
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + (uint32_t)i * 512u), "r"(g[i]) : "memory");
-      }
+          for (int i = 0; i < 32; ++i)
+            if (c + i < P.T)
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + (uint32_t)i * 512u), "r"(g[i]) : "memory");
+        }
     }
     __syncwarp();
     cluster_sync_all();
-    if (busy && part == 0)
-      for (int c = 0; c < rows; c += 32) {
-        uint32_t g[32];
-        float v[32];
-        __syncwarp();
-        tm_ld32(lanes + c, g);
-        tm_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(g[i]);
-        for (int p = 1; p < split; ++p) {
-          const float *src = reinterpret_cast<const float *>(smem_raw + sums) + ((p - 1) * P.n16 + c) * 128 + row;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < rows) v[i] += src[i * 128];
-        }
-        if (row < P.T) store_cols(P, row, n0 + c, v, rows - c);
-      }
+    if (busy && part == 0) epilogue(unit, reinterpret_cast<const float *>(smem_raw + sums));
     __syncwarp();
   }
   tm_fence_before();
@@ -294,7 +277,7 @@ cudaError_t launch(SlimParams &P, int grid, size_t smem, cudaStream_t s) {
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[0].val.programmaticStreamSerializationAllowed = 1;
   attrs[1].id = cudaLaunchAttributeClusterDimension;
-  attrs[1].val.clusterDim.x = (unsigned)(GATED ? 1 : P.split);
+  attrs[1].val.clusterDim.x = (unsigned)P.split;
   attrs[1].val.clusterDim.y = 1;
   attrs[1].val.clusterDim.z = 1;
   cfg.attrs = attrs;
@@ -308,38 +291,36 @@ bool slim_serves(int T) { return T <= 128; }
 
 sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
   const bool gated = q.w1 != nullptr;
+  const int np = gated ? 2 : 1;
   SlimParams P{};
   P.T = q.T;
   P.N = q.N;
   P.nk = (int)((q.K + 63) / 64);
-  P.tb8 = up_to(q.T, 8);
-  P.split = 1;
-  // weight rows of a CTA: an even share (an even number, so that 16-bit results go out in
-  // 4-byte words), at most 128, at least 16
+  P.t8 = up_to(q.T, 8);
+  P.t16 = up_to(q.T, 16);
+  // Weight rows of a tile: an even share, at most 128.  A share under 64 rows is widened by
+  // splitting K over a cluster (while a part keeps 8 chunks and the parts fit rank 0's memory).
   const int rounds = (q.N + sms * 128 - 1) / (sms * 128);
-  P.nb = std::max(16, up_to((q.N + sms * rounds - 1) / (sms * rounds), 2));
-  if (!gated && q.T > 32 && P.nb < q.T) {
-    // a cluster splits K: tiles of about 128 rows, so that H's rows are read by fewer CTAs
-    int split = 2;
-    while (split < 4 && split * 2 * P.nb <= 128 && P.nk >= split * 16) split *= 2;
-    if (rounds == 1 && P.nk >= split * 8) {
-      P.split = split;
-      P.nb = std::min(128, std::max(16, up_to((int)(((int64_t)q.N * split + sms - 1) / sms), 2)));
-    }
+  P.split = 1;
+  P.nb = (q.N + sms * rounds - 1) / (sms * rounds);
+  while (rounds == 1 && P.split < 4 && P.nb < 64 && P.nk >= 16 * P.split && (2 * P.split - 1) * np * P.t16 <= 384) {
+    P.split *= 2;
+    P.nb = std::min(128, (int)(((int64_t)q.N * P.split + sms - 1) / sms));
   }
+  P.nb = std::max(P.nb, 8);
   P.nb8 = up_to(P.nb, 8);
-  P.n16 = up_to(P.nb, 16);
   P.tiles = (q.N + P.nb - 1) / P.nb;
+  P.up_col = gated ? up_to(P.t16, 32) : 0;  // tensor memory is read 32 columns at a time
   P.tmem_cols = 32;
-  while (P.tmem_cols < (gated ? 2 : 1) * P.n16 || P.tmem_cols < up_to(P.n16, 32) + (gated ? P.n16 : 0)) P.tmem_cols *= 2;
-  const int chunk = P.tb8 * 128 + (gated ? 2 : 1) * P.nb8 * 128;
-  // two CTAs on an SM (besides the A tile's overhang), where that leaves enough in flight
-  const int budget = (q.T > 64 || chunk > 24 * 1024 ? 200 : 92) * 1024;
-  P.kps = std::max(1, std::min({4, 20 * 1024 / chunk, (P.nk + P.split - 1) / P.split}));
+  while (P.tmem_cols < P.up_col + up_to(P.t16, 32)) P.tmem_cols *= 2;
+  const int chunk = (P.t8 + np * P.nb8) * 128;
+  const int over = std::max(0, 16384 - P.nb8 * 128);  // the last tile's MMA reads 128 rows
+  const int64_t share = (int64_t)q.N * q.K * 2 * np / sms;
+  const int budget = share > (2048 << 10) ? 190 * 1024 : 227 * 512 - 1024 - 1024 - 512 - over;
+  P.kps = std::max(2, std::min(8, 24 * 1024 / chunk));
   P.stages = std::max(2, std::min(kMaxStages, budget / (P.kps * chunk)));
-  // (a cluster's parts are joined in rank 0's stage memory: T lanes x nb columns of 3 parts)
-  size_t smem = (size_t)P.stages * P.kps * chunk + 16384 + 1024;
-  if (P.split > 1) smem = std::max(smem, (size_t)(P.split - 1) * P.n16 * 512 + 1024);
+  size_t smem = (size_t)P.stages * P.kps * chunk + over + 1024;
+  if (P.split > 1) smem = std::max(smem, (size_t)(P.split - 1) * np * P.t16 * 512 + 1024);
   P.early = q.early;
   P.bf16 = q.bf16;
   P.out32 = q.out32;
@@ -348,9 +329,9 @@ sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
   P.out = q.out;
   P.ldo = q.ldo;
   P.err = q.err;
-  if (!make_tensor_map(&P.a, q.x, 2, q.T, q.K, q.ldx, P.tb8, 64, true) ||
-      !make_tensor_map(&P.b0, q.w0, 2, q.N, q.K, q.ldw0, P.nb, 64, true) ||
-      (gated && !make_tensor_map(&P.b1, q.w1, 2, q.N, q.K, q.ldw1, P.nb, 64, true)))
+  if (!make_tensor_map(&P.x, q.x, 2, q.T, q.K, q.ldx, P.t8, 64, true) ||
+      !make_tensor_map(&P.w0, q.w0, 2, q.N, q.K, q.ldw0, P.nb, 64, true) ||
+      (gated && !make_tensor_map(&P.w1, q.w1, 2, q.N, q.K, q.ldw1, P.nb, 64, true)))
     return SFNN_ERR_CUDA;
   const int grid = P.split > 1 ? P.tiles * P.split : std::min(P.tiles, sms);
   const cudaError_t e = gated ? launch<true>(P, grid, smem, s) : launch<false>(P, grid, smem, s);
