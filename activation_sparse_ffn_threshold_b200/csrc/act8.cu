@@ -30,9 +30,20 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p, int have, bool vec) {
   return w;
 }
 
-template <bool RELU>
+// relu of two 16-bit values (NaNs stay)
+template <bool bf16>
+__device__ __forceinline__ uint32_t relu16(uint32_t w) {
+  if (bf16) {
+    const __nv_bfloat162 v = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&w), __floats2bfloat162_rn(0.f, 0.f));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  const __half2 v = __hmax2_nan(*reinterpret_cast<const __half2 *>(&w), __floats2half2_rn(0.f, 0.f));
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <bool RELU, bool bf16>
 __global__ void __launch_bounds__(kWarps * 32)
-    k_act8_quantize(const uint16_t *__restrict__ x, int64_t ldx, int T, int cols, int bf16, int vec,
+    k_act8_quantize(const uint16_t *__restrict__ x, int64_t ldx, int T, int cols, int vec,
                     uint8_t *__restrict__ codes, int64_t ldq, float *__restrict__ scales, int64_t lds) {
   pdl_wait();
   pdl_launch_dependents();
@@ -50,37 +61,43 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int c = c0 + i * 256;
-    const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    // relu and the block's largest magnitude on pairs of 16-bit values (their bit patterns order
+    // like their magnitudes, NaNs above infinities)
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (RELU) a[j] = relu16<bf16>(a[j]);
+      m = __vmaxu2(m, a[j] & 0x7fff7fffu);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (c >= end) continue;
+    const uint32_t top = max(m & 0xffffu, m >> 16);
+    const Act8Scale s = act8_scale(__float_as_uint(unpack16(top, bf16).x), RELU ? 255.f : 127.f);
     float v[8];
-    uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = unpack16(a[j], bf16);
       v[2 * j] = f.x;
       v[2 * j + 1] = f.y;
     }
+    uint32_t q[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (RELU) v[j] = v[j] < 0.f ? 0.f : v[j];
-      top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+    for (int j = 0; j < 2; ++j) {
+      q[j] = act8_codes(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], s.inv);
+      if (RELU)  // a relu'd value is positive where its bits are not zero
+        q[j] = act8_lift(q[j], __byte_perm(__vminu2(a[2 * j], 0x00010001u), __vminu2(a[2 * j + 1], 0x00010001u), 0x6420));
     }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (c >= end) continue;
-    const Act8Scale s = act8_scale(top, RELU ? 255.f : 127.f);
-    uint32_t q[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      q[j >> 2] |= (RELU ? act8_code_relu(v[j], s.inv) : act8_code_signed(v[j], s.inv)) << (8 * (j & 3));
     *reinterpret_cast<uint2 *>(codes + row * ldq + c) = make_uint2(q[0], q[1]);
     if ((lane & 7) == 0) scales[row * lds + (c >> 6)] = s.scale;
   }
 }
 
-template <bool RELU>
+template <bool RELU, bool bf16>
 __global__ void __launch_bounds__(kWarps * 32)
     k_act8_restore(const uint8_t *__restrict__ codes, int64_t ldq, const float *__restrict__ scales, int64_t lds, int T,
-                   int cols, int bf16, int vec, uint16_t *__restrict__ out, int64_t ldo) {
+                   int cols, int vec, uint16_t *__restrict__ out, int64_t ldo) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -127,15 +144,18 @@ dim3 grid_of(int T, int cols) { return dim3((T + kWarps - 1) / kWarps, (cols + k
 
 cudaError_t launch_act8_quantize(const void *x, int64_t ldx, int T, int cols, int bf16, bool relu, uint8_t *codes,
                                  int64_t ldq, float *scales, int64_t lds, cudaStream_t s) {
-  return launch_pdl(relu ? k_act8_quantize<true> : k_act8_quantize<false>, grid_of(T, cols), dim3(kWarps * 32), 0, s,
-                    static_cast<const uint16_t *>(x), ldx, T, cols, bf16, (int)aligned16(x, ldx), codes, ldq, scales,
-                    lds);
+  auto *k = relu ? (bf16 ? k_act8_quantize<true, true> : k_act8_quantize<true, false>)
+                 : (bf16 ? k_act8_quantize<false, true> : k_act8_quantize<false, false>);
+  return launch_pdl(k, grid_of(T, cols), dim3(kWarps * 32), 0, s, static_cast<const uint16_t *>(x), ldx, T, cols,
+                    (int)aligned16(x, ldx), codes, ldq, scales, lds);
 }
 
 cudaError_t launch_act8_restore(const uint8_t *codes, int64_t ldq, const float *scales, int64_t lds, int T, int cols,
                                 bool relu, int bf16, void *out, int64_t ldo, cudaStream_t s) {
-  return launch_pdl(relu ? k_act8_restore<true> : k_act8_restore<false>, grid_of(T, cols), dim3(kWarps * 32), 0, s,
-                    codes, ldq, scales, lds, T, cols, bf16, (int)aligned16(out, ldo), static_cast<uint16_t *>(out), ldo);
+  auto *k = relu ? (bf16 ? k_act8_restore<true, true> : k_act8_restore<true, false>)
+                 : (bf16 ? k_act8_restore<false, true> : k_act8_restore<false, false>);
+  return launch_pdl(k, grid_of(T, cols), dim3(kWarps * 32), 0, s, codes, ldq, scales, lds, T, cols,
+                    (int)aligned16(out, ldo), static_cast<uint16_t *>(out), ldo);
 }
 
 }  // namespace sfnn

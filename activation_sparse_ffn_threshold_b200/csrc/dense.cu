@@ -179,12 +179,12 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, uint32_t tgate, 
       uint32_t wr[4], wu[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        wr[j] = wu[j] = 0;
+        const float *a = r + 16 * i + 4 * j, *c = u + 16 * i + 4 * j;
+        uint32_t pos = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          wr[j] |= act8_code_relu(r[16 * i + 4 * j + k], sr.inv) << (8 * k);
-          wu[j] |= act8_code_signed(u[16 * i + 4 * j + k], su.inv) << (8 * k);
-        }
+        for (int k = 0; k < 4; ++k) pos |= a[k] > 0.f ? 1u << (8 * k) : 0u;
+        wr[j] = act8_lift(act8_codes(a[0], a[1], a[2], a[3], sr.inv), pos);
+        wu[j] = act8_codes(c[0], c[1], c[2], c[3], su.inv);
       }
       rp[i] = make_uint4(wr[0], wr[1], wr[2], wr[3]);
       up[i] = make_uint4(wu[0], wu[1], wu[2], wu[3]);

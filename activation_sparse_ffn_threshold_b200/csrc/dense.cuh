@@ -33,11 +33,12 @@ __device__ __forceinline__ float load16(const void *p, int64_t i, bool bf16) {
 
 // ---------------------------------------------------------------- act8
 // 64 values of a row share an fp32 scale: max|v| / 127 with codes -127..127, or for
-// relu(v) max / 255 with codes 0..255.  A code is rint(v * (qmax / max)): one multiply per
-// value, off from the nearest code only where two are equally near to an fp32 rounding.  A
+// relu(v) max / 255 with codes 0..255.  A code is rint(v / scale), as one multiply-add per value
+// by the scale's reciprocal: off from the nearest code only where two are equally near to
+// within fp32 roundings.  A
 // positive relu'd value keeps a code of at least 1: code > 0 is exactly the ReLU's mask,
 // which the backward pass needs.  A block with a NaN or an infinity gets a NaN scale (and so
-// restores as NaN); a block whose largest magnitude is below 2^-119 gets scale 0.
+// restores as NaN); a block whose largest magnitude is below 2^-112 gets scale 0.
 constexpr int kAct8Block = 64;
 
 struct Act8Scale {
@@ -45,18 +46,27 @@ struct Act8Scale {
 };
 // `top`: the largest fp32 bit pattern of the block's magnitudes (NaN > inf > finite).
 __device__ __forceinline__ Act8Scale act8_scale(uint32_t top, float qmax) {
-  const float m = __uint_as_float(top);
   Act8Scale s;
-  s.scale = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : (top < 0x04000000u ? 0.f : __fdiv_rn(m, qmax));
-  s.inv = (top >= 0x7f800000u || top < 0x04000000u) ? 0.f : __fdiv_rn(qmax, m);
+  s.scale = __uint_as_float(top) * (1.f / qmax);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inv) : "f"(s.scale));  // within an ulp: a code is off only next to a tie
+  if (top < 0x07800000u) s.scale = s.inv = 0.f;
+  if (top >= 0x7f800000u) s.scale = __uint_as_float(0x7fffffffu);
   return s;
 }
-__device__ __forceinline__ uint32_t act8_code_signed(float v, float inv) {
-  return (uint32_t)max(-127, min(127, __float2int_rn(v * inv))) & 0xffu;
+// Codes of four values as bytes: v * inv + 1.5 * 2^23 in one fused multiply-add leaves the
+// nearest integer (ties to even) in the low byte.  |v * inv| <= qmax (1 + 2^-21), so no code
+// leaves its range; in a NaN block the codes mean nothing.
+__device__ __forceinline__ uint32_t act8_codes(float a, float b, float c, float d, float inv) {
+  constexpr float kMagic = 12582912.f;
+  const uint32_t x = __float_as_uint(fmaf(a, inv, kMagic)), y = __float_as_uint(fmaf(b, inv, kMagic));
+  const uint32_t z = __float_as_uint(fmaf(c, inv, kMagic)), w = __float_as_uint(fmaf(d, inv, kMagic));
+  return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
 }
-__device__ __forceinline__ uint32_t act8_code_relu(float r, float inv) {  // r = relu(v)
-  const int c = min(255, __float2int_rn(r * inv));
-  return (uint32_t)(r > 0.f ? max(c, 1) : 0);
+// ... and of four relu'd values: a positive one whose code is 0 gets code 1 (`positive`: bit 0
+// of each byte whose value is positive).
+__device__ __forceinline__ uint32_t act8_lift(uint32_t codes, uint32_t positive) {
+  const uint32_t some = ((codes & 0x7f7f7f7fu) + 0x7f7f7f7fu) | codes;  // bit 7 of each byte that is not zero
+  return codes | (positive & ~(some >> 7));
 }
 
 // ---------------------------------------------------------------- the product

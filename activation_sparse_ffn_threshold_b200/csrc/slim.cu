@@ -4,10 +4,10 @@
 // fill the 128 lanes: the rest of the A tile is whatever shared memory holds, and only
 // reaches accumulator lanes nobody reads.  So a tile is any number of weight rows, the rows
 // are dealt out evenly over the SMs (75 neurons each of 11008 over 148), and every byte of
-// them is read once.  Where an even share would be a thin tile (28 of 4096 rows of the down
-// projection: an MMA reads all 128 lanes of A from shared memory, so a thin tile's weights
-// pass slower than they come from DRAM), a cluster of 2 or 4 CTAs takes a wider tile, splits
-// its K, and adds the parts through distributed shared memory in rank order.
+// them is read once.  An even share under 64 rows would be a thin tile (28 of 4096 rows of
+// the down projection), slow in small copies: a cluster of 2 or 4 CTAs takes a wider tile,
+// splits its K, and adds the parts through distributed shared memory in rank order (1 token,
+// 4096 x 11008, both kernels: 61 us against 76 with thin tiles).
 //
 // A stage holds at least two 64-deep chunks of every row: 256 contiguous bytes of it (TMA,
 // 128-byte swizzle).
@@ -31,6 +31,8 @@ struct alignas(64) SlimParams {
   int t8, t16;          // T rounded up to 8 (rows loaded), to 16 (MMA N)
   int kps, stages;      // chunks per stage
   int split;            // CTAs of a cluster that share a tile's K
+  int apart;            // the parts are joined in memory of their own behind the stages (else in the stages)
+  int m64;              // 64-lane MMAs (a row's accumulators: lane r % 16 of quarter r / 16)
   int early;            // weights may be read before the kernel before has finished
   int tmem_cols, up_col;
   int bf16, out32, relu;
@@ -58,7 +60,7 @@ __device__ __forceinline__ void store_tokens(const SlimParams &P, int col, int t
 template <bool GATED>
 __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimParams P) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty;
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty, parts_in;
   __shared__ uint32_t tmem_slot;
   constexpr int NP = GATED ? 2 : 1;
   const uint32_t raw = smem_u32(smem_raw);
@@ -83,8 +85,10 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
     }
     bar_init(&acc_full, 1);
     bar_init(&acc_empty, 4);
+    bar_init(&parts_in, 4u * (uint32_t)(split > 1 ? split - 1 : 1));
     bar_init_fence();
   }
+  if (split > 1) cluster_sync_all();  // rank 0's barrier is there before a part arrives
   if (warp == 1) tm_alloc<1>(&tmem_slot, (uint32_t)P.tmem_cols);
   tm_fence_before();
   __syncthreads();
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = mma_desc_16(128, P.t16, P.bf16, 0, 0);
+      const uint32_t idesc = mma_desc_16(P.m64 ? 64 : 128, P.t16, P.bf16, 0, 0);
       int it = 0, n = 0;
       bool ok = true;
       for (int t = unit; t < P.tiles && ok; t += units, ++n) {
@@ -171,14 +175,19 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
       if (!ok) latch_error(P.err, kErrTimeout);
     }
   }
-  const int quad = warp & 3, row = quad * 32 + lane;
+  const int quad = warp & 3;
+  const int row = P.m64 ? (lane < 16 ? quad * 16 + lane : 128) : quad * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   const bool worker = warp >= 2;
+  const bool busy = worker && quad * (P.m64 ? 16 : 32) < P.nb;
+  auto load_bias = [&](int t) {
+    const int col = t * P.nb + row;
+    return (GATED || P.relu) && P.bias && row < P.nb && col < P.N ? load16(P.bias, col, P.bf16) : 0.f;
+  };
   // the epilogue of this thread's weight row, with the other parts of a split tile at `sums`
-  auto epilogue = [&](int t, const float *sums) {
+  auto epilogue = [&](int t, float bias, const float *sums) {
     const int col = t * P.nb + row;
     const bool live = row < P.nb && col < P.N;
-    const float bias = (GATED || P.relu) && P.bias && live ? load16(P.bias, col, P.bf16) : 0.f;
     for (int c = 0; c < P.T; c += 32) {
       uint32_t g[32], u[32];
       float v[32];
@@ -189,12 +198,12 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
       if (!live) continue;
       if (sums)
         for (int p = 0; p < split - 1; ++p) {
-          const float *a = sums + ((size_t)(p * NP) * P.t16 + c) * 128 + row;
+          const float *a = sums + ((size_t)(p * NP) * P.T + c) * 128 + row;
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (c + i < P.T) {
               g[i] = __float_as_uint(__uint_as_float(g[i]) + a[i * 128]);
-              if (GATED) u[i] = __float_as_uint(__uint_as_float(u[i]) + a[(P.t16 + i) * 128]);
+              if (GATED) u[i] = __float_as_uint(__uint_as_float(u[i]) + a[(P.T + i) * 128]);
             }
         }
 #pragma unroll
@@ -213,6 +222,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
     pdl_wait();  // nothing is written before the kernel before has finished
     int n = 0;
     for (int t = unit; t < P.tiles; t += units, ++n) {
+      const float bias = load_bias(t);
       if (!__all_sync(0xffffffffu, bar_wait(&acc_full, (uint32_t)(n & 1)))) {
         if (lane == 0) latch_error(P.err, kErrTimeout);
         break;
@@ -220,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
       __syncwarp();
       tm_fence_after();
       if (split > 1) break;  // one tile per cluster, joined below
-      if (quad * 32 < P.nb) epilogue(t, nullptr);
+      if (busy) epilogue(t, bias, nullptr);
       tm_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty, 0));
@@ -228,32 +238,43 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
   }
   __syncwarp();
   if (split > 1) {
-    // Every CTA of the cluster has its accumulators: the others put theirs into rank 0's
-    // stage memory (no load or MMA touches it any more), rank 0 adds them in rank order.
-    const uint32_t sums = stage0 - raw;  // the same offset in every CTA
-    const bool busy = worker && quad * 32 < P.nb;
-    cluster_sync_all();
+    // The other ranks put their accumulators into rank 0's shared memory, which adds them in
+    // rank order: behind the stages where they fit, else into the stages, once every CTA of
+    // the cluster has its accumulators (no load or MMA touches the stages any more).
+    const uint32_t sums = stage0 - raw + (P.apart ? (uint32_t)stages * stage_bytes : 0u);  // the same offset in every CTA
+    if (!P.apart) cluster_sync_all();
     tm_fence_after();
-    if (busy && part > 0) {
-      const uint32_t dst0 = cluster_addr(smem_raw, 0) + sums + (uint32_t)((part - 1) * NP * P.t16 * 128 + row) * 4u;
+    if (worker && part > 0) {
+      const uint32_t dst0 = cluster_addr(smem_raw, 0) + sums + (uint32_t)((part - 1) * NP * P.T * 128 + row) * 4u;
+      if (busy)
 #pragma unroll 1
-      for (int p = 0; p < NP; ++p)
-        for (int c = 0; c < P.T; c += 32) {
-          uint32_t g[32];
-          __syncwarp();
-          tm_ld32(lanes + (uint32_t)(p * P.up_col + c), g);
-          tm_wait_ld();
-          const uint32_t dst = dst0 + (uint32_t)(p * P.t16 + c) * 512u;
+        for (int p = 0; p < NP; ++p)
+          for (int c = 0; c < P.T; c += 32) {
+            uint32_t g[32];
+            __syncwarp();
+            tm_ld32(lanes + (uint32_t)(p * P.up_col + c), g);
+            tm_wait_ld();
+            const uint32_t dst = dst0 + (uint32_t)(p * P.T + c) * 512u;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < P.T)
-              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + (uint32_t)i * 512u), "r"(g[i]) : "memory");
-        }
+            for (int i = 0; i < 32; ++i)
+              if (c + i < P.T)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + (uint32_t)i * 512u), "r"(g[i]) : "memory");
+          }
+      asm volatile("fence.acq_rel.cluster;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive_cluster(cluster_addr(&parts_in, 0));
+    }
+    if (worker && part == 0) {
+      const float bias = load_bias(unit);
+      if (!__all_sync(0xffffffffu, bar_wait(&parts_in, 0))) {
+        if (lane == 0) latch_error(P.err, kErrTimeout);
+      } else {
+        __syncwarp();
+        if (busy) epilogue(unit, bias, reinterpret_cast<const float *>(smem_raw + sums));
+      }
     }
     __syncwarp();
-    cluster_sync_all();
-    if (busy && part == 0) epilogue(unit, reinterpret_cast<const float *>(smem_raw + sums));
-    __syncwarp();
+    if (!P.apart) cluster_sync_all();
   }
   tm_fence_before();
   __syncthreads();
@@ -285,6 +306,32 @@ cudaError_t launch(SlimParams &P, int grid, size_t smem, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_slim<GATED>, P);
 }
 
+// Clusters of `split` CTAs, one CTA to an SM, that the device runs at a time (a cluster lies
+// within one GPC, so fours leave some SMs over).  0: the query failed.
+int active_clusters(int split) {
+  static std::atomic<int> known[64][2];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::atomic<int> &slot = known[dev][split == 4];
+  int n = slot.load(std::memory_order_relaxed);
+  if (n) return n;
+  static std::atomic<uint64_t> ready{0};
+  if (allow_smem(k_slim<false>, 224 * 1024, ready) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(split * 64);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 190 * 1024;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, k_slim<false>, &cfg) != cudaSuccess) return 0;
+  slot.store(n, std::memory_order_relaxed);
+  return n;
+}
+
 }  // namespace
 
 bool slim_serves(int T) { return T <= 128; }
@@ -303,24 +350,31 @@ sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
   const int rounds = (q.N + sms * 128 - 1) / (sms * 128);
   P.split = 1;
   P.nb = (q.N + sms * rounds - 1) / (sms * rounds);
-  while (rounds == 1 && P.split < 4 && P.nb < 64 && P.nk >= 16 * P.split && (2 * P.split - 1) * np * P.t16 <= 384) {
+  while (rounds == 1 && P.split < 4 && P.nb < 64 && P.nk >= 16 * P.split && (2 * P.split - 1) * np * P.T <= 384) {
+    // no more tiles than clusters run at a time: another wave would double the time
+    const int clusters = active_clusters(2 * P.split);
+    if (clusters < 1 || (q.N + clusters - 1) / clusters > 128) break;
     P.split *= 2;
-    P.nb = std::min(128, (int)(((int64_t)q.N * P.split + sms - 1) / sms));
+    P.nb = (q.N + clusters - 1) / clusters;
   }
   P.nb = std::max(P.nb, 8);
   P.nb8 = up_to(P.nb, 8);
+  P.m64 = P.split == 1 && P.nb <= 64;
   P.tiles = (q.N + P.nb - 1) / P.nb;
   P.up_col = gated ? up_to(P.t16, 32) : 0;  // tensor memory is read 32 columns at a time
   P.tmem_cols = 32;
   while (P.tmem_cols < P.up_col + up_to(P.t16, 32)) P.tmem_cols *= 2;
   const int chunk = (P.t8 + np * P.nb8) * 128;
-  const int over = std::max(0, 16384 - P.nb8 * 128);  // the last tile's MMA reads 128 rows
-  const int64_t share = (int64_t)q.N * q.K * 2 * np / sms;
-  const int budget = share > (2048 << 10) ? 190 * 1024 : 227 * 512 - 1024 - 1024 - 512 - over;
+  const int over = std::max(0, (P.m64 ? 8192 : 16384) - P.nb8 * 128);  // an MMA reads all its lanes' rows
+  // All of shared memory in flight (1 token, 4096 x 11008: 59 us; with half of it each, so that
+  // the gate/up and the down kernel share an SM, 63 to 64; 37 tokens, 8192 x 28672: 225 and 256).
+  const int budget = 190 * 1024;
+  const int parts = (P.split - 1) * np * P.T * 512;  // bytes of the other ranks' accumulators
+  P.apart = parts <= 16 * 1024;
   P.kps = std::max(2, std::min(8, 24 * 1024 / chunk));
-  P.stages = std::max(2, std::min(kMaxStages, budget / (P.kps * chunk)));
-  size_t smem = (size_t)P.stages * P.kps * chunk + over + 1024;
-  if (P.split > 1) smem = std::max(smem, (size_t)(P.split - 1) * np * P.t16 * 512 + 1024);
+  P.stages = std::max(2, std::min(kMaxStages, (budget - (P.apart ? parts : 0)) / (P.kps * chunk)));
+  const int stage_mem = P.stages * P.kps * chunk;
+  const size_t smem = 1024 + std::max(stage_mem + over, P.apart ? stage_mem + parts : parts);
   P.early = q.early;
   P.bf16 = q.bf16;
   P.out32 = q.out32;
