@@ -153,14 +153,13 @@ constexpr int kThreads = 320;
 constexpr int kMaxStages = 6;
 constexpr int kTmem = 512;
 constexpr int kAcc = 0, kSf = 256;      // tensor-memory columns: accumulators, scale slots
-constexpr int kSfSlot = 32;             // A: 2 x 4 columns; B: 2 x 12 from column 8 on
+constexpr int kSfSlot = 32;             // of a stage: A 2 x 4 columns, B 2 x 8 from column 8 on
+constexpr uint32_t kPairStage = 16384 + 16384 + 1024 + 2048 + 1024;  // A, B, their scales (a multiple of 1024)
 
 struct alignas(64) MxParams {
   CUtensorMap a, b, sa, sb;
   int M, N, nk;          // nk: 256-deep steps
   int tiles_m, tiles_n;
-  int nt;                // columns of C per tile (CG = 2: 256)
-  int stages;
   int out_dtype, vec;    // vec: rows of C are 16-byte aligned
   void *out;
   int64_t ldo;
@@ -212,27 +211,23 @@ __device__ __forceinline__ TilePos tile_pos(int t, int tiles_m, int tiles_n) {  
   return {band * kBand + r % rows, r / rows};
 }
 
-// CG = 2: 256 x 256 tiles by CTA pairs, 128 rows of X and of W in each CTA.  CG = 1: 128
-// tokens x nt columns (nt a multiple of 32) by single CTAs, for few tokens: nt is chosen so
-// that the tiles fill the SMs.
+// 256 x 256 tiles by CTA pairs, 128 rows of X and of W in each CTA (more than 128 tokens).
 //
 // The accumulators are single (256 columns; the scales need the rest of tensor memory): the
 // epilogue warps copy a finished tile to registers, hand the columns back, and store while
 // the next tile's MMAs run.  Scale slots go by stage: a slot is written again only after the
 // stage's MMAs have completed.
-template <int CG>
-__global__ void __launch_bounds__(kThreads, 1) k_mx(const __grid_constant__ MxParams P) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_mx(const __grid_constant__ MxParams P) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty;
   __shared__ uint32_t tmem_slot;
   const uint32_t stage0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-  const int unit = CG == 2 ? blockIdx.x >> 1 : blockIdx.x, units = CG == 2 ? gridDim.x >> 1 : gridDim.x;
+  const uint32_t rank = cluster_rank();
+  const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
   const int ntiles = P.tiles_m * P.tiles_n;
-  const uint32_t b_bytes = CG == 2 ? 16384u : (uint32_t)P.nt * 128u;
-  const uint32_t stage_bytes = 16384u + b_bytes + 4096u;
-  const int stages = P.stages;
+  constexpr uint32_t b_bytes = 16384u, stage_bytes = kPairStage;
+  constexpr int stages = kMaxStages, nsf = 2;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -240,13 +235,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx(const __grid_constant__ MxPa
       bar_init(&empty[s], 1);
     }
     bar_init(&acc_full, 1);
-    bar_init(&acc_empty, 8 * CG);
+    bar_init(&acc_empty, 16);
     bar_init_fence();
   }
-  if (warp == 1) tm_alloc<CG>(&tmem_slot, kTmem);
+  if (warp == 1) tm_alloc<2>(&tmem_slot, kTmem);
   tm_fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync_all();
+  cluster_sync_all();
   tm_fence_after();
   const uint32_t tmem = tmem_slot;
   pdl_wait();
@@ -258,32 +253,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx(const __grid_constant__ MxPa
       bool ok = true;
       for (int t = unit; t < ntiles && ok; t += units) {
         const TilePos pos = tile_pos(t, P.tiles_m, P.tiles_n);
-        const int m0 = (CG == 2 ? pos.m * 256 : pos.m * 128) + (int)rank * 128;
-        const int n0 = pos.n * P.nt;                                   // the tile's columns
-        const int nb0 = CG == 2 ? n0 + (int)rank * 128 : n0;           // this CTA's rows of W
-        const int rb = n0 >> 7;                                        // first scale tile row of W
-        const int nsf = CG == 2 ? 2 : ((n0 & 127) + P.nt + 127) >> 7;  // and how many
+        const int m0 = pos.m * 256 + (int)rank * 128;
+        const int n0 = pos.n * 256, nb0 = n0 + (int)rank * 128;  // the tile's columns, this CTA's rows of W
+        const int rb = n0 >> 7;                                  // first scale tile row of W
         for (int kc = 0; kc < P.nk; ++kc, ++it) {
           const int s = it % stages;
           if (!bar_wait(&empty[s], (uint32_t)((it / stages) & 1) ^ 1u)) {
             ok = false;
             break;
           }
-          const uint32_t bytes = 16384u + b_bytes + 1024u + (uint32_t)nsf * 1024u;
-          if (rank == 0) bar_expect_tx(&full[s], CG * bytes);
+          constexpr uint32_t bytes = 16384u + b_bytes + 1024u + nsf * 1024u;
+          if (rank == 0) bar_expect_tx(&full[s], 2 * bytes);
           const uint32_t a = stage0 + (uint32_t)s * stage_bytes, b = a + 16384u, sa = b + b_bytes, sb = sa + 1024u;
-          if (CG == 2) {
-            const uint32_t bar = cluster_addr(&full[s], 0);
-            tma_load_2d_pair(a, &P.a, kc * 128, m0, bar);
-            tma_load_2d_pair(b, &P.b, kc * 128, nb0, bar);
-            tma_load_2d_pair(sa, &P.sa, 0, (m0 >> 7) * P.nk + kc, bar);
-            for (int r = 0; r < nsf; ++r) tma_load_2d_pair(sb + r * 1024u, &P.sb, 0, (rb + r) * P.nk + kc, bar);
-          } else {
-            tma_load_2d(a, &P.a, kc * 128, m0, &full[s]);
-            tma_load_2d(b, &P.b, kc * 128, nb0, &full[s]);
-            tma_load_2d(sa, &P.sa, 0, (m0 >> 7) * P.nk + kc, &full[s]);
-            for (int r = 0; r < nsf; ++r) tma_load_2d(sb + r * 1024u, &P.sb, 0, (rb + r) * P.nk + kc, &full[s]);
-          }
+          const uint32_t bar = cluster_addr(&full[s], 0);
+          tma_load_2d_pair(a, &P.a, kc * 128, m0, bar);
+          tma_load_2d_pair(b, &P.b, kc * 128, nb0, bar);
+          tma_load_2d_pair(sa, &P.sa, 0, (m0 >> 7) * P.nk + kc, bar);
+          for (int r = 0; r < nsf; ++r) tma_load_2d_pair(sb + r * 1024u, &P.sb, 0, (rb + r) * P.nk + kc, bar);
         }
       }
       if (!ok) latch_error(P.err, kErrTimeout);
@@ -296,69 +282,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx(const __grid_constant__ MxPa
       }
     }
   } else if (warp == 1) {
-    if (rank == 0) {
+    if (rank == 0 && lane == 0) {
       int it = 0, i = 0;
       bool ok = true;
-      const uint32_t id0 = mx_idesc(128 * CG, P.nt, 0), id2 = mx_idesc(128 * CG, P.nt, 2);
+      const uint32_t id0 = mx_idesc(256, 256, 0), id2 = mx_idesc(256, 256, 2);
       for (int t = unit; t < ntiles && ok; t += units, ++i) {
-        const TilePos pos = tile_pos(t, P.tiles_m, P.tiles_n);
-        const int n0 = pos.n * P.nt;
-        const int nsf = CG == 2 ? 2 : ((n0 & 127) + P.nt + 127) >> 7;
-        const int shift = CG == 2 ? 0 : (n0 & 127) >> 5;  // 32-row groups of the first scale tile before the tile
-        if (!__all_sync(0xffffffffu, bar_wait(&acc_empty, (uint32_t)(i & 1) ^ 1u))) {
+        if (!bar_wait(&acc_empty, (uint32_t)(i & 1) ^ 1u)) {
           ok = false;
           break;
         }
         tm_fence_after();
         for (int kc = 0; kc < P.nk; ++kc, ++it) {
           const int s = it % stages;
-          if (!__all_sync(0xffffffffu, bar_wait(&full[s], (uint32_t)((it / stages) & 1)))) {
+          if (!bar_wait(&full[s], (uint32_t)((it / stages) & 1))) {
             ok = false;
             break;
           }
+          tm_fence_after();
           const uint32_t a = stage0 + (uint32_t)s * stage_bytes, b = a + 16384u, sa = b + b_bytes, sb = sa + 1024u;
-          if (CG == 1 && shift) {
-            // the MMA wants the tile's first column's scales in an aligned tensor-memory column:
-            // move the 32-row groups (a 4-byte word of each lane's 16) down to the tile's start
-            for (int h = 0; h < 2; ++h)
-              for (int c = 0; c < P.nt >> 5; ++c) {
-                const int f = c + shift;
-                const uint32_t at = sb + (uint32_t)(h * 512 + lane * 16);
-                uint32_t w;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at + (uint32_t)((f >> 2) * 1024 + (f & 3) * 4)));
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + (uint32_t)((c >> 2) * 1024 + (c & 3) * 4)), "r"(w)
-                             : "memory");
-              }
-            fence_async_shared();
-            __syncwarp();
-          }
-          if (lane == 0) {
-            tm_fence_after();
-            const uint32_t ta = tmem + kSf + (uint32_t)(s * kSfSlot), tb = ta + 8u;
+          const uint32_t ta = tmem + kSf + (uint32_t)(s * kSfSlot), tb = ta + 8u;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // the step's two 128-deep scale tiles
-              copy_scales<CG>(ta + h * 4, sa + h * 512);
-              for (int r = 0; r < nsf; ++r) copy_scales<CG>(tb + h * 12 + r * 4, sb + r * 1024 + h * 512);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_mx<CG>(tmem + kAcc, mat_desc(a + k * 32, 16, 1024), mat_desc(b + k * 32, 16, 1024), (k & 1) ? id2 : id0,
-                         ta + (k >> 1) * 4, tb + (k >> 1) * 12, (kc > 0 || k > 0) ? 1u : 0u);
-            if (CG == 2)
-              mma_commit_pair(&empty[s]);
-            else
-              mma_commit(&empty[s]);
+          for (int h = 0; h < 2; ++h) {  // the step's two 128-deep scale tiles
+            copy_scales<2>(ta + h * 4, sa + h * 512);
+            for (int r = 0; r < nsf; ++r) copy_scales<2>(tb + h * 8 + r * 4, sb + r * 1024 + h * 512);
           }
-          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_mx<2>(tmem + kAcc, mat_desc(a + k * 32, 16, 1024), mat_desc(b + k * 32, 16, 1024), (k & 1) ? id2 : id0,
+                      ta + (k >> 1) * 4, tb + (k >> 1) * 8, (kc > 0 || k > 0) ? 1u : 0u);
+          mma_commit_pair(&empty[s]);
         }
-        if (ok && lane == 0) {
-          if (CG == 2)
-            mma_commit_pair(&acc_full);
-          else
-            mma_commit(&acc_full);
-        }
+        if (ok) mma_commit_pair(&acc_full);
       }
-      if (!ok && lane == 0) latch_error(P.err, kErrTimeout);
+      if (!ok) latch_error(P.err, kErrTimeout);
     }
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
@@ -371,13 +327,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx(const __grid_constant__ MxPa
       __syncwarp();
       tm_fence_after();
       const TilePos pos = tile_pos(t, P.tiles_m, P.tiles_n);
-      const int64_t row = (int64_t)pos.m * (128 * CG) + rank * 128 + quad * 32 + lane;
-      const int n0 = pos.n * P.nt;
+      const int64_t row = (int64_t)pos.m * 256 + rank * 128 + quad * 32 + lane;
+      const int n0 = pos.n * 256;
       // 32-column units half, half + 2, ...: at most four
       uint32_t v[4][32];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if ((half + 2 * u) * 32 < P.nt) tm_ld32(tmem + ((uint32_t)(quad * 32) << 16) + kAcc + (half + 2 * u) * 32, v[u]);
+        tm_ld32(tmem + ((uint32_t)(quad * 32) << 16) + kAcc + (half + 2 * u) * 32, v[u]);
       tm_wait_ld();
       tm_fence_before();
       __syncwarp();
@@ -386,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx(const __grid_constant__ MxPa
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int col = n0 + (half + 2 * u) * 32;
-        const int cols = min(32, min(P.N, n0 + P.nt) - col);
-        if ((half + 2 * u) * 32 >= P.nt || cols <= 0) continue;
+        const int cols = min(32, P.N - col);
+        if (cols <= 0) continue;
         if (P.out_dtype == SFNN_F32) {
           float *o = static_cast<float *>(P.out) + row * P.ldo + col;
           if (P.vec && cols == 32) {
@@ -422,37 +378,432 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx(const __grid_constant__ MxPa
   __syncwarp();
   tm_fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync_all();
+  cluster_sync_all();
   tm_fence_after();
-  if (warp == 1) tm_dealloc<CG>(tmem, kTmem);
+  if (warp == 1) tm_dealloc<2>(tmem, kTmem);
 }
 
-size_t mx_smem(int stages, uint32_t b_bytes) { return (size_t)stages * (16384 + b_bytes + 4096) + 1024; }
+// ---------------------------------------------------------------- one to four tokens
+// Y = Xq . Wq^T on CUDA cores with the tokens quantised by every CTA itself: one launch, no
+// workspace.  Bound by the weights' bytes (half a byte a value); the products run on bytes,
+// exactly: a code is turned into twice its value (0, 1, 2, 3, 4, 6, 8, 12) by byte permutes,
+// four products an instruction (dp4a), 32 of them an int32 that the two block scales then
+// multiply.  A negative weight's byte is its one's complement; the sum of x over the negative
+// weights, which that takes too much, is added back by a second dp4a on the sign bytes.
+//
+// A CTA owns a contiguous share of the rows, a warp takes one row at a time: a lane holds 32
+// values (16 bytes) of every 1024, a row's loads go out while the row before is multiplied.
+constexpr int kRowThreads = 512;
+constexpr int kRowLoads = 4;  // 16-byte loads of a lane in flight for a row: 4096 values
 
-cudaError_t launch_mx(const MxParams &P, bool pair, int num_sms, cudaStream_t s) {
-  static std::atomic<uint64_t> ready1{0}, ready2{0};
-  const size_t limit = 220 * 1024;
-  const cudaError_t attr = pair ? allow_smem(k_mx<2>, limit, ready2) : allow_smem(k_mx<1>, limit, ready1);
+__device__ __forceinline__ uint32_t mx_magnitudes(uint32_t sel) { return __byte_perm(0x03020100u, 0x0c080604u, sel); }
+__device__ __forceinline__ uint32_t mx_signs(uint32_t sel) { return __byte_perm(0x0000ff00u, 0u, sel); }
+
+template <int TT>
+__global__ void __launch_bounds__(kRowThreads)
+    k_mx_rows(const uint16_t *__restrict__ x, int64_t ldx, int T, int vec, int bf16, const uint4 *__restrict__ codes,
+              const uint8_t *__restrict__ scales, int N, int K, void *__restrict__ out, int64_t ldo, int out_dtype) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int nb = K / kBlock;
+  // bytes of token t: two planes of 16 bytes a block (a warp's 16-byte reads then have no bank
+  // conflicts), then its scales
+  uint4 *xq = reinterpret_cast<uint4 *>(smem);
+  float *xs = reinterpret_cast<float *>(smem + (size_t)TT * K);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = (int)((int64_t)blockIdx.x * N / gridDim.x), r1 = (int)((int64_t)(blockIdx.x + 1) * N / gridDim.x);
+  const int64_t kt = mx_ktiles(K);
+  pdl_wait();
+  pdl_launch_dependents();
+
+  uint4 w[kRowLoads];
+  uint32_t sb[kRowLoads];
+  auto request = [&](int row, int b0) {
+#pragma unroll
+    for (int i = 0; i < kRowLoads; ++i) {
+      const int b = b0 + i * 32 + lane;
+      w[i] = make_uint4(0, 0, 0, 0);
+      sb[i] = 0;
+      if (row < r1 && b < nb) {
+        w[i] = ld_stream(codes + (int64_t)row * nb + b);
+        sb[i] = __ldg(scales + mx_scale_at(row, b, kt));
+      }
+    }
+  };
+  request(r0 + warp, 0);
+
+  for (int g0 = 0; g0 < TT * nb * 4; g0 += kRowThreads) {  // 8 values a thread; 4 neighbouring lanes a block
+    const int g = g0 + threadIdx.x, t = g / (nb * 4), c = (g - t * nb * 4) * 8;
+    uint32_t a[4] = {0, 0, 0, 0};
+    if (t < T) {
+      const uint16_t *p = x + t * ldx + c;
+      if (vec) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p));
+        a[0] = q.x, a[1] = q.y, a[2] = q.z, a[3] = q.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j >> 1] |= (uint32_t)__ldg(p + j) << (16 * (j & 1));
+      }
+    }
+    uint32_t top = 0;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack16(a[j], bf16);
+      v[2 * j] = f.x;
+      v[2 * j + 1] = f.y;
+      top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if (t >= TT) continue;
+    const uint32_t e = mx_scale_byte(top);
+    uint32_t q = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q |= mx_pair(mx_unscale(v[2 * j], e), mx_unscale(v[2 * j + 1], e)) << (8 * j);
+    const uint32_t sel = q & 0x77777777u, neg = (q >> 3) & 0x11111111u;
+    const uint32_t s0 = mx_signs(neg), s1 = mx_signs(neg >> 16);
+    const uint32_t lo = __vsub4(mx_magnitudes(sel) ^ s0, s0), hi = __vsub4(mx_magnitudes(sel >> 16) ^ s1, s1);
+    const int b = c >> 5, part = (c >> 3) & 3;  // 8 values: half a plane's 16 bytes
+    reinterpret_cast<uint2 *>(xq + ((size_t)t * 2 + (part >> 1)) * nb + b)[part & 1] = make_uint2(lo, hi);
+    if (part == 0) xs[t * nb + b] = mx_scale_value(e);
+  }
+  __syncthreads();
+
+  for (int row = r0 + warp; row < r1; row += kRowThreads / 32) {
+    float acc[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = 0.f;
+    for (int b0 = 0; b0 < nb; b0 += 32 * kRowLoads) {
+      uint4 cw[kRowLoads];
+      uint32_t cs[kRowLoads];
+#pragma unroll
+      for (int i = 0; i < kRowLoads; ++i) {
+        cw[i] = w[i];
+        cs[i] = sb[i];
+      }
+      const bool more = b0 + 32 * kRowLoads < nb;
+      request(more ? row : row + kRowThreads / 32, more ? b0 + 32 * kRowLoads : 0);
+#pragma unroll
+      for (int i = 0; i < kRowLoads; ++i) {
+        const int b = b0 + i * 32 + lane;
+        if (b >= nb) continue;
+        const uint32_t word[4] = {cw[i].x, cw[i].y, cw[i].z, cw[i].w};
+        uint32_t val[8], sgn[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t sel = word[j] & 0x77777777u, neg = (word[j] >> 3) & 0x11111111u;
+          sgn[2 * j] = mx_signs(neg);
+          sgn[2 * j + 1] = mx_signs(neg >> 16);
+          val[2 * j] = mx_magnitudes(sel) ^ sgn[2 * j];
+          val[2 * j + 1] = mx_magnitudes(sel >> 16) ^ sgn[2 * j + 1];
+        }
+        const float ws = mx_scale_value(cs[i]);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const uint4 p0 = xq[(size_t)(t * 2) * nb + b], p1 = xq[(size_t)(t * 2 + 1) * nb + b];
+          const uint32_t xv[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+          int dot = 0, over = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            dot = __dp4a((int)xv[j], (int)val[j], dot);
+            over = __dp4a((int)xv[j], (int)sgn[j], over);
+          }
+          acc[t] = fmaf((float)(dot - over) * (0.25f * xs[t * nb + b]), ws, acc[t]);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const float s = warp_sum(acc[t]);
+      if (lane == 0 && t < T) {
+        if (out_dtype == SFNN_F32)
+          static_cast<float *>(out)[t * ldo + row] = s;
+        else
+          static_cast<uint16_t *>(out)[t * ldo + row] = (uint16_t)pack16(s, 0.f, out_dtype == SFNN_BF16);
+      }
+    }
+  }
+}
+
+bool rows_serve(int T, int K) { return T <= 4 && (int64_t)T * K <= 65536; }
+
+template <int TT>
+cudaError_t launch_rows(const void *x, int64_t ldx, int T, int vec, int bf16, const void *wc, const void *wsc, int N, int K,
+                        void *y, int64_t ldy, int y_dtype, int sms, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t attr = allow_smem(k_mx_rows<TT>, (size_t)(TT == 4 ? 65536 / 3 * 4 : 65536) * 9 / 8 + 256, ready);
   if (attr != cudaSuccess) return attr;
+  return launch_pdl(k_mx_rows<TT>, dim3(std::min(sms, (N + 15) / 16)), dim3(kRowThreads), (size_t)TT * K * 9 / 8, s,
+                    static_cast<const uint16_t *>(x), ldx, T, vec, bf16, static_cast<const uint4 *>(wc),
+                    static_cast<const uint8_t *>(wsc), N, K, y, ldy, y_dtype);
+}
+
+// ---------------------------------------------------------------- up to 128 tokens
+// The weights on the MMA's M side (128-row tiles, as their scales lie), the tokens on its N
+// side.  Bound by the weights' bytes and, in small layers, by latency: a cluster of 2 or 4
+// CTAs splits a tile's K so that the SMs are filled, each CTA then adds up a share of the
+// tokens: its own accumulators and, in rank order, those the other CTAs put into its shared
+// memory.
+constexpr int kFewThreads = 192;  // warp 0 loads, warp 1 issues the MMAs, warps 2-5 take 32 weight rows each
+constexpr int kFewStages = 8;
+constexpr int kFewSf = 16;  // scale columns of a stage: A 2 x 4, B 2 x 4 (128 tokens)
+
+struct alignas(64) FewParams {
+  CUtensorMap w, x, sw, sx;
+  int T, N, nk;   // nk: 256-deep steps
+  int tiles;
+  int t8, t16;    // T rounded up to 8 (rows loaded), to 16 (MMA N)
+  int stages, split, share;  // share: tokens that a CTA of a cluster adds up
+  int apart;                 // the parts land behind the stages (else in them)
+  int acc_cols, tmem_cols;   // columns of the accumulators (then the scales), of all
+  int out_dtype;
+  void *out;
+  int64_t ldo;
+  int32_t *err;
+};
+
+__global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ FewParams P) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[kFewStages], empty[kFewStages], acc_full, acc_empty, parts_in;
+  __shared__ uint32_t tmem_slot;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t stage0 = (raw + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = P.split, part = split > 1 ? (int)cluster_rank() : 0;
+  const int unit = blockIdx.x / split, units = gridDim.x / split;
+  const uint32_t x_bytes = (uint32_t)P.t8 * 128u;
+  // w (16 KB), its scales, x, its scales; an MMA may read 1 KB past x's rows, into the scales
+  const uint32_t stage_bytes = 16384u + 1024u + x_bytes + 1024u;
+  const int stages = P.stages;
+  const int k_lo = (int)((int64_t)part * P.nk / split), steps = (int)((int64_t)(part + 1) * P.nk / split) - k_lo;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      bar_init(&full[s], 1);
+      bar_init(&empty[s], 1);
+    }
+    bar_init(&acc_full, 1);
+    bar_init(&acc_empty, 4);
+    bar_init(&parts_in, 4u * (uint32_t)(split > 1 ? split - 1 : 1));
+    bar_init_fence();
+  }
+  if (split > 1) cluster_sync_all();  // every CTA's barrier is there before a part arrives
+  if (warp == 1) tm_alloc<1>(&tmem_slot, (uint32_t)P.tmem_cols);
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      pdl_wait();
+      pdl_launch_dependents();
+      const uint32_t bytes = 16384u + 1024u + x_bytes + 1024u;
+      int it = 0;
+      bool ok = true;
+      for (int t = unit; t < P.tiles && ok; t += units) {
+        for (int i = 0; i < steps; ++i, ++it) {
+          const int s = it % stages, k = k_lo + i;
+          if (!bar_wait(&empty[s], (uint32_t)((it / stages) & 1) ^ 1u)) {
+            ok = false;
+            break;
+          }
+          bar_expect_tx(&full[s], bytes);
+          const uint32_t w = stage0 + (uint32_t)s * stage_bytes, x = w + 16384u, sw = x + x_bytes, sx = sw + 1024u;
+          tma_load_2d(w, &P.w, k * 128, t * 128, &full[s]);
+          tma_load_2d(sw, &P.sw, 0, t * P.nk + k, &full[s]);
+          tma_load_2d(x, &P.x, k * 128, 0, &full[s]);
+          tma_load_2d(sx, &P.sx, 0, k, &full[s]);
+        }
+      }
+      for (int s = 0; s < stages && ok; ++s) {  // every load has been consumed before the CTA ends
+        const int j = it - stages + s;
+        if (j >= 0 && !bar_wait(&empty[j % stages], (uint32_t)((j / stages) & 1))) ok = false;
+      }
+      if (!ok) latch_error(P.err, kErrTimeout);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id0 = mx_idesc(128, P.t16, 0), id2 = mx_idesc(128, P.t16, 2);
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int t = unit; t < P.tiles && ok; t += units, ++n) {
+        if (!bar_wait(&acc_empty, (uint32_t)(n & 1) ^ 1u)) {
+          ok = false;
+          break;
+        }
+        tm_fence_after();
+        for (int i = 0; i < steps; ++i, ++it) {
+          const int s = it % stages;
+          if (!bar_wait(&full[s], (uint32_t)((it / stages) & 1))) {
+            ok = false;
+            break;
+          }
+          tm_fence_after();
+          const uint32_t w = stage0 + (uint32_t)s * stage_bytes, x = w + 16384u, sw = x + x_bytes, sx = sw + 1024u;
+          const uint32_t ta = tmem + (uint32_t)(P.acc_cols + s * kFewSf), tb = ta + 8u;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            copy_scales<1>(ta + h * 4, sw + h * 512);
+            copy_scales<1>(tb + h * 4, sx + h * 512);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_mx<1>(tmem, mat_desc(w + k * 32, 16, 1024), mat_desc(x + k * 32, 16, 1024), (k & 1) ? id2 : id0,
+                      ta + (k >> 1) * 4, tb + (k >> 1) * 4, (i > 0 || k > 0) ? 1u : 0u);
+          mma_commit(&empty[s]);
+        }
+        if (ok) mma_commit(&acc_full);
+      }
+      if (!ok) latch_error(P.err, kErrTimeout);
+    }
+  }
+  const int quad = warp & 3, row = quad * 32 + lane;
+  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+  const bool worker = warp >= 2;
+  // this thread's weight row for tokens [t0, t1): out[t][col], with the other CTAs' parts
+  auto finish = [&](int tile, int t0, int t1, const float *sums) {
+    const int col = tile * 128 + row;
+    for (int c = t0; c < t1; c += 32) {
+      uint32_t g[32];
+      float v[32];
+      __syncwarp();
+      tm_ld32(lanes + c, g);
+      tm_wait_ld();
+      if (col >= P.N) continue;
+      if (sums) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        for (int p = 0; p < split; ++p) {  // rank order, this CTA's own in its place
+          const float *a = sums + ((size_t)(p < part ? p : p - 1) * P.share + (c - t0)) * 128 + row;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < t1) v[i] += p == part ? __uint_as_float(g[i]) : a[i * 128];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(g[i]);
+      }
+      if (P.out_dtype == SFNN_F32) {
+        float *o = static_cast<float *>(P.out) + c * P.ldo + col;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < t1) o[i * P.ldo] = v[i];
+      } else {
+        const bool bf16 = P.out_dtype == SFNN_BF16;
+        uint16_t *o = static_cast<uint16_t *>(P.out) + c * P.ldo + col;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < t1) o[i * P.ldo] = (uint16_t)pack16(v[i], 0.f, bf16);
+      }
+    }
+  };
+  bool good = true;
+  if (worker) {
+    pdl_wait();
+    int n = 0;
+    for (int t = unit; t < P.tiles; t += units, ++n) {
+      if (!__all_sync(0xffffffffu, bar_wait(&acc_full, (uint32_t)(n & 1)))) {
+        if (lane == 0) latch_error(P.err, kErrTimeout);
+        good = false;
+        break;
+      }
+      __syncwarp();
+      tm_fence_after();
+      if (split > 1) break;  // one tile per cluster
+      finish(t, 0, P.T, nullptr);
+      tm_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty, 0));
+    }
+  }
+  __syncwarp();
+  if (split > 1) {
+    const uint32_t sums = stage0 - raw + (P.apart ? (uint32_t)stages * stage_bytes : 0u);  // the same offset in every CTA
+    if (!P.apart) cluster_sync_all();  // no load or MMA touches a stage any more
+    tm_fence_after();
+    if (worker) {
+      for (int q = 0; q < split; ++q) {
+        if (q == part) continue;
+        const int t0 = min(P.T, q * P.share), t1 = min(P.T, t0 + P.share);
+        const uint32_t dst0 = cluster_addr(smem_raw, (uint32_t)q) + sums +
+                              (uint32_t)((part < q ? part : part - 1) * P.share * 128 + row) * 4u;
+        for (int c = t0; c < t1; c += 32) {
+          uint32_t g[32];
+          __syncwarp();
+          tm_ld32(lanes + c, g);
+          tm_wait_ld();
+          const uint32_t dst = dst0 + (uint32_t)(c - t0) * 512u;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < t1)
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + (uint32_t)i * 512u), "r"(g[i]) : "memory");
+        }
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(cluster_addr(&parts_in, (uint32_t)q));
+      }
+      if (!__all_sync(0xffffffffu, bar_wait(&parts_in, 0))) {
+        if (lane == 0) latch_error(P.err, kErrTimeout);
+      } else if (good && unit < P.tiles) {
+        __syncwarp();
+        const int t0 = min(P.T, part * P.share);
+        finish(unit, t0, min(P.T, t0 + P.share), reinterpret_cast<const float *>(smem_raw + sums));
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA leaves while another may still write to it
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  if (warp == 1) tm_dealloc<1>(tmem, (uint32_t)P.tmem_cols);
+}
+
+cudaError_t launch_pair(const MxParams &P, int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  const size_t smem = (size_t)kMaxStages * kPairStage + 1024;
+  const cudaError_t attr = allow_smem(k_mx, smem, ready);
+  if (attr != cudaSuccess) return attr;
+  return launch_pdl(k_mx, dim3(2 * std::min(num_sms / 2, P.tiles_m * P.tiles_n)), dim3(kThreads), smem, s, P);
+}
+
+cudaError_t launch_few(FewParams &P, int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t attr = allow_smem(k_mx_few, 224 * 1024, ready);
+  if (attr != cudaSuccess) return attr;
+  P.t8 = (P.T + 7) / 8 * 8;
+  P.t16 = (P.T + 15) / 16 * 16;
+  P.tiles = (P.N + 127) / 128;
+  P.split = 1;
+  // more CTAs to a tile while they fit two to an SM and each keeps two steps
+  while (P.split < 4 && P.tiles * P.split * 2 <= 2 * num_sms && P.nk >= 4 * P.split) P.split *= 2;
+  P.share = (P.T + P.split - 1) / P.split;
+  const int stage = 16384 + 1024 + P.t8 * 128 + 1024;
+  const int parts = P.split > 1 ? (P.split - 1) * P.share * 512 : 0;
+  P.apart = parts <= 16 * 1024;
+  const int steps = (P.nk + P.split - 1) / P.split;
+  P.stages = std::min({kFewStages, steps, (108 * 1024 - (P.apart ? parts : 0)) / stage});
+  const int stage_mem = P.stages * stage;
+  const size_t smem = 1024 + (P.apart ? stage_mem + parts : std::max(stage_mem, parts));
+  P.acc_cols = (P.t16 + 31) / 32 * 32 + 32;  // read 32 columns at a time, from any token on
+  P.tmem_cols = 32;
+  while (P.tmem_cols < P.acc_cols + P.stages * kFewSf) P.tmem_cols *= 2;
   cudaLaunchConfig_t cfg = {};
-  const int tiles = P.tiles_m * P.tiles_n;
-  cfg.gridDim = dim3(pair ? 2 * std::min(num_sms / 2, tiles) : std::min(num_sms, tiles));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = mx_smem(P.stages, pair ? 16384u : (uint32_t)P.nt * 128u);
+  cfg.gridDim = dim3(P.split > 1 ? P.tiles * P.split : std::min(P.tiles, 2 * num_sms));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attrs[2];
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = (unsigned)P.split;
+  attrs[1].val.clusterDim.y = 1;
+  attrs[1].val.clusterDim.z = 1;
   cfg.attrs = attrs;
-  cfg.numAttrs = 1;
-  if (pair) {
-    attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim.x = 2;
-    attrs[1].val.clusterDim.y = 1;
-    attrs[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-  }
-  return pair ? cudaLaunchKernelEx(&cfg, k_mx<2>, P) : cudaLaunchKernelEx(&cfg, k_mx<1>, P);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_mx_few, P);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -483,36 +834,41 @@ sfnn_status product(const void *xc, const void *xs, int T, const void *wc, const
                     int64_t ldo, int32_t out_dtype, int32_t *err, cudaStream_t s) {
   const int sms = device_sms();
   if (sms < 2) return SFNN_ERR_CUDA;
+  const int nk = (K + 255) / 256;
+  const int64_t rows_x = mx_rtiles(T) * nk, rows_w = mx_rtiles(N) * nk;
+  if (T <= 128) {
+    FewParams P{};
+    P.T = T;
+    P.N = N;
+    P.nk = nk;
+    P.out = out;
+    P.ldo = ldo;
+    P.out_dtype = out_dtype;
+    P.err = err;
+    if (!make_tensor_map(&P.x, xc, 1, T, K / 2, K / 2, (T + 7) / 8 * 8, 128, true) ||
+        !make_tensor_map(&P.w, wc, 1, N, K / 2, K / 2, 128, 128, true) ||
+        !make_tensor_map(&P.sx, xs, 4, rows_x, 256, 256, 1, 256, false) ||
+        !make_tensor_map(&P.sw, wsc, 4, rows_w, 256, 256, 1, 256, false))
+      return SFNN_ERR_CUDA;
+    return launch_few(P, sms, s) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
+  }
   MxParams P{};
   P.M = T;
   P.N = N;
-  P.nk = (K + 255) / 256;
+  P.nk = nk;
   P.out = out;
   P.ldo = ldo;
   P.out_dtype = out_dtype;
   P.vec = rows16(out, ldo, out_dtype == SFNN_F32 ? 4 : 2);
   P.err = err;
-  const bool pair = T > 128;
-  if (pair) {
-    P.nt = 256;
-    P.tiles_m = (T + 255) / 256;
-    P.stages = kMaxStages;
-  } else {
-    // the narrowest tile (a multiple of 32) that still needs the fewest rounds over the SMs
-    P.tiles_m = 1;
-    const int units = (N + 31) / 32;
-    const int rounds = (units + 8 * sms - 1) / (8 * sms);
-    P.nt = 32 * std::min(8, (units + rounds * sms - 1) / (rounds * sms));
-    P.stages = std::min<int>(kMaxStages, (int)((219 * 1024) / (16384 + P.nt * 128 + 4096)));
-  }
-  P.tiles_n = (N + P.nt - 1) / P.nt;
-  const int64_t rows_a = mx_rtiles(T) * P.nk, rows_b = mx_rtiles(N) * P.nk;
+  P.tiles_m = (T + 255) / 256;
+  P.tiles_n = (N + 255) / 256;
   if (!make_tensor_map(&P.a, xc, 1, T, K / 2, K / 2, 128, 128, true) ||
-      !make_tensor_map(&P.b, wc, 1, N, K / 2, K / 2, pair ? 128 : P.nt, 128, true) ||
-      !make_tensor_map(&P.sa, xs, 4, rows_a, 256, 256, 1, 256, false) ||
-      !make_tensor_map(&P.sb, wsc, 4, rows_b, 256, 256, 1, 256, false))
+      !make_tensor_map(&P.b, wc, 1, N, K / 2, K / 2, 128, 128, true) ||
+      !make_tensor_map(&P.sa, xs, 4, rows_x, 256, 256, 1, 256, false) ||
+      !make_tensor_map(&P.sb, wsc, 4, rows_w, 256, 256, 1, 256, false))
     return SFNN_ERR_CUDA;
-  return launch_mx(P, pair, sms, s) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
+  return launch_pair(P, sms, s) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
 }
 
 }  // namespace
@@ -565,6 +921,7 @@ sfnn_status sfnn_mxfp4_product(const void *x_codes, const void *x_scales, int32_
 
 int64_t sfnn_mxfp4_linear_workspace(int32_t T, int32_t K) {
   if (T < 0 || K < 1) return -1;
+  if (rows_serve(T, K)) return 0;
   return ((int64_t)T * K / 2 + 255) / 256 * 256 + sfnn_mxfp4_scale_bytes(T, K);
 }
 
@@ -576,8 +933,18 @@ sfnn_status sfnn_mxfp4_linear(const void *x, int64_t ldx, int32_t T, int32_t dty
   if (st == SFNN_OK) st = value_check(x, ldx, T, K, dtype, false);
   if (st == SFNN_OK) st = value_check(y, ldy, T, N, y_dtype, true);
   if (st != SFNN_OK || T == 0) return st;
-  if (!err || !ws || !aligned(ws, 16) || ws_bytes < sfnn_mxfp4_linear_workspace(T, K)) return SFNN_ERR_INVALID_ARG;
+  if (!err) return SFNN_ERR_INVALID_ARG;
+  const int64_t need = sfnn_mxfp4_linear_workspace(T, K);
+  if (need > 0 && (!ws || !aligned(ws, 16) || ws_bytes < need)) return SFNN_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (rows_serve(T, K)) {
+    const int vec = rows16(x, ldx, 2), bf16 = dtype == SFNN_BF16, sms = device_sms();
+    if (sms < 1) return SFNN_ERR_CUDA;
+    const cudaError_t e = T == 1   ? launch_rows<1>(x, ldx, T, vec, bf16, w_codes, w_scales, N, K, y, ldy, y_dtype, sms, s)
+                          : T == 2 ? launch_rows<2>(x, ldx, T, vec, bf16, w_codes, w_scales, N, K, y, ldy, y_dtype, sms, s)
+                                   : launch_rows<4>(x, ldx, T, vec, bf16, w_codes, w_scales, N, K, y, ldy, y_dtype, sms, s);
+    return e == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
+  }
   void *scales = static_cast<unsigned char *>(ws) + ((int64_t)T * K / 2 + 255) / 256 * 256;
   if (quantize(x, ldx, T, K, dtype, ws, scales, s) != cudaSuccess) return SFNN_ERR_CUDA;
   return product(ws, scales, T, w_codes, w_scales, N, K, y, ldy, y_dtype, err, s);

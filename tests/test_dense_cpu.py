@@ -130,7 +130,7 @@ def test_mxfp4_refuses():
     assert prod(K=40) == UNSUPPORTED and prod(T=0) == 0
 
     def linear(ws=4096, nbytes=1 << 30, x=4096, ldx=64):
-        return lib.sfnn_mxfp4_linear(x, ldx, 4, sf.F16, 4096, 4096, 8, 64, 4096, 8, sf.F16, ws, nbytes, 4096, None)
+        return lib.sfnn_mxfp4_linear(x, ldx, 16, sf.F16, 4096, 4096, 8, 64, 4096, 8, sf.F16, ws, nbytes, 4096, None)
     assert linear(ws=None) == INVALID and linear(nbytes=8) == INVALID and linear(x=None) == INVALID
     assert linear(ldx=32) == INVALID
     with pytest.raises(TypeError):
