@@ -13,7 +13,7 @@ import ctypes
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import BF16, F16, F32, SfnnError, _check, load_library
+from . import BF16, F16, F32, _check, load_library
 
 __all__ = ["gated_ffn", "gated_ffn_forward", "gated_ffn_backward", "GatedSaved", "quantize_act8", "dequantize_act8",
            "Act8", "dense_error", "quantize_mxfp4", "dequantize_mxfp4", "mxfp4_matmul", "mxfp4_linear", "Mxfp4"]
@@ -40,17 +40,20 @@ class _GatedSaved(ctypes.Structure):
 
 # ------------------------------------------------------------------ helpers
 _err_words: dict[int, torch.Tensor] = {}
+_err_ptrs: dict[int, int] = {}
 
 
-def _err_word(device) -> torch.Tensor:
-    w = _err_words.get(device.index)
-    if w is None:
+def _err_ptr(index: int) -> int:
+    """The device's error word (its address)."""
+    p = _err_ptrs.get(index)
+    if p is None:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the first dense call on a device allocates its error word: make one before capturing")
-        w = torch.zeros(1, dtype=torch.int32, device=device)
-        torch.cuda.synchronize(device)  # zeroed before a call on another stream uses it
-        _err_words[device.index] = w
-    return w
+        w = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", index))
+        torch.cuda.synchronize(index)  # zeroed before a call on another stream uses it
+        _err_words[index] = w
+        p = _err_ptrs[index] = w.data_ptr()
+    return p
 
 
 def dense_error(device=None) -> int:
@@ -70,51 +73,83 @@ def dense_error(device=None) -> int:
     return code
 
 
-class _Place:
-    """The device of the call's tensors made current, and the stream that it runs on."""
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
-    __slots__ = ("dev", "stream", "raw", "_d", "_s")
 
-    def __init__(self, device, stream):
-        self.dev = device
-        self._d = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        self._s = None if stream is None else torch.cuda.stream(stream)
-        self.stream = stream
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same handle without building a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+class _Here:
+    """A call on the current device and stream: nothing to switch."""
 
     def __enter__(self):
-        if self._d is not None:
-            self._d.__enter__()
-        if self._s is not None:
-            self._s.__enter__()
-        self.raw = (self.stream or torch.cuda.current_stream(self.dev)).cuda_stream
         return self
 
     def __exit__(self, *a):
-        if self._s is not None:
-            self._s.__exit__(*a)
-        if self._d is not None:
-            self._d.__exit__(*a)
+        pass
+
+
+class _Place:
+    """The device of the call's tensors made current, and the stream that it runs on."""
+
+    __slots__ = ("_d", "_s")
+
+    def __init__(self, index, stream):
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+        self._d = torch.cuda.device(index)
+        self._s = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._d.__enter__()
+        self._s.__enter__()
+        return self
+
+    def __exit__(self, *a):
+        self._s.__exit__(*a)
+        self._d.__exit__(*a)
+
+
+_HERE = _Here()
+
+
+def _on(index: int, stream):
+    if stream is None and _current_device() == index:
+        return _HERE
+    return _Place(index, stream)
+
+
+_CODES = {torch.float16: F16, torch.bfloat16: BF16}
 
 
 def _code(dtype) -> int:
-    if dtype == torch.float16:
-        return F16
-    if dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"the dense operators take fp16 or bf16 tensors, got {dtype}")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"the dense operators take fp16 or bf16 tensors, got {dtype}")
+    return code
 
 
 def _rows(t, name, cols=None):
     """(pointer, rows, cols, row stride) of a tensor [..., cols] whose rows lie evenly apart."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
-        if t.dim() == 0:
+    shape = t.shape
+    if t.is_contiguous() and shape:
+        c = shape[-1]
+        r = shape[0] if len(shape) == 2 else (t.numel() // c if c else 0)
+        if cols is not None and c != cols:
+            raise ValueError(f"{name} must have {cols} columns, got {c}")
+        return t.data_ptr(), r, c, c
+    if len(shape) != 2:
+        if not shape:
             raise ValueError(f"{name} must have at least one dimension")
         try:
-            t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(0, t.shape[-1])
+            t = t.view(-1, shape[-1]) if t.numel() else t.reshape(0, shape[-1])
         except RuntimeError:
             raise ValueError(f"{name}: its leading dimensions must be viewable as rows") from None
     r, c = t.shape
@@ -138,9 +173,9 @@ def _mat(t, name, dtype, rows=None, cols=None):
     return p, r, c, ld
 
 
-def _same_device(ts, device):
+def _same_device(index, *ts):
     for t in ts:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError("all tensors must be on one device")
 
 
@@ -162,43 +197,47 @@ class Act8:
         return self.codes.numel() + 4 * self.scales.numel()
 
 
-def _act8_empty(T, cols, device):
+def _act8_empty(like, T, cols):
     nb = (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
-    return (torch.empty((T, nb * ACT8_BLOCK), dtype=torch.uint8, device=device),
-            torch.empty((T, nb), dtype=torch.float32, device=device))
+    return like.new_empty((T, nb * ACT8_BLOCK), dtype=torch.uint8), like.new_empty((T, nb), dtype=torch.float32)
 
 
 def quantize_act8(x, relu: bool = False, stream=None) -> Act8:
     """x [..., cols] as 8-bit blocks; with ``relu``, relu(x) (a positive value keeps a positive code)."""
-    code = _code(x.dtype) if isinstance(x, torch.Tensor) else 0
     p, T, cols, ld = _rows(x, "x")
+    code = _code(x.dtype)
     if cols < 1:
         raise ValueError("x must have at least one column")
     if ld < cols:
         raise ValueError("x: rows must not overlap")
-    with _Place(x.device, stream) as at:
-        q, s = _act8_empty(T, cols, x.device)
-        _check(load_library().sfnn_act8_quantize(p, ld, T, cols, code, int(bool(relu)), q.data_ptr(), q.shape[1],
-                                                 s.data_ptr(), s.shape[1], at.raw), "sfnn_act8_quantize")
-    return Act8(q, s, tuple(x.shape), x.dtype, bool(relu))
+    index = x.get_device()
+    with _on(index, stream):
+        q, s = _act8_empty(x, T, cols)
+        _check(load_library().sfnn_act8_quantize(p, ld, T, cols, code, 1 if relu else 0, q.data_ptr(), q.shape[1],
+                                                 s.data_ptr(), s.shape[1], _raw_stream(index)), "sfnn_act8_quantize")
+    return Act8(q, s, x.shape, x.dtype, bool(relu))
 
 
 def dequantize_act8(q: Act8, dtype=None, out=None, stream=None):
     """The values that q stands for, [..., cols] in ``dtype`` (default: the quantised tensor's)."""
     dtype = dtype or (out.dtype if out is not None else q.dtype)
     code = _code(dtype)
+    codes, scales = q.codes, q.scales
+    T, ldq = codes.shape
     cols = q.shape[-1]
-    T = q.codes.shape[0]
-    with _Place(q.codes.device, stream) as at:
+    index = codes.get_device()
+    with _on(index, stream):
         if out is None:
-            out = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
-        elif out.dtype != dtype or tuple(out.shape) != tuple(q.shape) or out.device != q.codes.device:
-            raise ValueError(f"out must be a {dtype} tensor of shape {tuple(q.shape)} on {q.codes.device}")
-        p, _, _, ld = _rows(out, "out", cols)
-        if ld < cols:
-            raise ValueError("out: rows must not overlap")
-        _check(load_library().sfnn_act8_restore(q.codes.data_ptr(), q.codes.shape[1], q.scales.data_ptr(),
-                                                q.scales.shape[1], T, cols, int(q.relu), code, p, ld, at.raw),
+            out = codes.new_empty(q.shape, dtype=dtype)
+            ld = cols
+        else:
+            if out.dtype != dtype or out.shape != q.shape or out.get_device() != index:
+                raise ValueError(f"out must be a {dtype} tensor of shape {tuple(q.shape)} on {codes.device}")
+            _, _, _, ld = _rows(out, "out", cols)
+            if ld < cols:
+                raise ValueError("out: rows must not overlap")
+        _check(load_library().sfnn_act8_restore(codes.data_ptr(), ldq, scales.data_ptr(), scales.shape[1], T, cols,
+                                                1 if q.relu else 0, code, out.data_ptr(), ld, _raw_stream(index)),
                "sfnn_act8_restore")
     return out
 
@@ -219,73 +258,80 @@ class Mxfp4:
 
 def quantize_mxfp4(x, stream=None) -> Mxfp4:
     """x [..., K] (K a multiple of 32) as MXFP4 rows."""
-    code = _code(x.dtype) if isinstance(x, torch.Tensor) else 0
     p, R, K, ld = _rows(x, "x")
+    code = _code(x.dtype)
     if K % 32 or not K:
         raise ValueError(f"the last dimension must be a positive multiple of 32, got {K}")
     if ld < K:
         raise ValueError("x: rows must not overlap")
     lib = load_library()
-    with _Place(x.device, stream) as at:
-        q = torch.empty((R, K // 2), dtype=torch.uint8, device=x.device)
-        s = torch.empty(lib.sfnn_mxfp4_scale_bytes(R, K), dtype=torch.uint8, device=x.device)
-        _check(lib.sfnn_mxfp4_quantize(p, ld, R, K, code, q.data_ptr(), s.data_ptr(), at.raw), "sfnn_mxfp4_quantize")
-    return Mxfp4(q, s, tuple(x.shape), x.dtype)
+    index = x.get_device()
+    with _on(index, stream):
+        q = x.new_empty((R, K // 2), dtype=torch.uint8)
+        s = x.new_empty(lib.sfnn_mxfp4_scale_bytes(R, K), dtype=torch.uint8)
+        _check(lib.sfnn_mxfp4_quantize(p, ld, R, K, code, q.data_ptr(), s.data_ptr(), _raw_stream(index)),
+               "sfnn_mxfp4_quantize")
+    return Mxfp4(q, s, x.shape, x.dtype)
 
 
 def dequantize_mxfp4(q: Mxfp4, dtype=None, stream=None):
     """The values that q stands for, in ``dtype`` (default: the quantised tensor's)."""
     dtype = dtype or q.dtype
+    code = _code(dtype)
     K = q.shape[-1]
-    with _Place(q.codes.device, stream) as at:
-        out = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
-        _check(load_library().sfnn_mxfp4_restore(q.codes.data_ptr(), q.scales.data_ptr(), q.codes.shape[0], K,
-                                                 _code(dtype), out.data_ptr(), K, at.raw), "sfnn_mxfp4_restore")
+    index = q.codes.get_device()
+    with _on(index, stream):
+        out = q.codes.new_empty(q.shape, dtype=dtype)
+        _check(load_library().sfnn_mxfp4_restore(q.codes.data_ptr(), q.scales.data_ptr(), q.codes.shape[0], K, code,
+                                                 out.data_ptr(), K, _raw_stream(index)), "sfnn_mxfp4_restore")
     return out
 
 
-def _mx_out(shape, w, out_dtype, device):
+def _mx_out(K, w, out_dtype, index):
+    """(N, the output's type code) of a product with w."""
     if not isinstance(w, Mxfp4) or len(w.shape) != 2 or not w.shape[0]:
         raise TypeError("w must be an Mxfp4 of a matrix [N, K]")
-    if shape[-1] != w.shape[1]:
-        raise ValueError(f"x has {shape[-1]} columns, w {w.shape[1]}")
-    if w.codes.device != device:
+    N, wk = w.shape
+    if K != wk:
+        raise ValueError(f"x has {K} columns, w {wk}")
+    if w.codes.get_device() != index:
         raise ValueError("all tensors must be on one device")
-    return F32 if out_dtype == torch.float32 else _code(out_dtype)
+    return N, F32 if out_dtype == torch.float32 else _code(out_dtype)
 
 
 def mxfp4_matmul(x: Mxfp4, w: Mxfp4, out_dtype=None, stream=None):
     """x w^T for x [..., K] and w [N, K], both MXFP4; ``out_dtype`` (fp16, bf16 or fp32)
     defaults to the tensor's that x was quantised from."""
     dt = out_dtype or x.dtype
-    dev = x.codes.device
-    code = _mx_out(x.shape, w, dt, dev)
-    N, K = w.shape
-    T = x.codes.shape[0]
-    with _Place(dev, stream) as at:
-        y = torch.empty(x.shape[:-1] + (N,), dtype=dt, device=dev)
-        _check(load_library().sfnn_mxfp4_product(x.codes.data_ptr(), x.scales.data_ptr(), T, w.codes.data_ptr(),
-                                                 w.scales.data_ptr(), N, K, y.data_ptr(), N, code,
-                                                 _err_word(dev).data_ptr(), at.raw), "sfnn_mxfp4_product")
+    index = x.codes.get_device()
+    K = x.shape[-1]
+    N, code = _mx_out(K, w, dt, index)
+    with _on(index, stream):
+        y = x.codes.new_empty(x.shape[:-1] + (N,), dtype=dt)
+        _check(load_library().sfnn_mxfp4_product(x.codes.data_ptr(), x.scales.data_ptr(), x.codes.shape[0],
+                                                 w.codes.data_ptr(), w.scales.data_ptr(), N, K, y.data_ptr(), N, code,
+                                                 _err_ptr(index), _raw_stream(index)), "sfnn_mxfp4_product")
     return y
 
 
 def mxfp4_linear(x, w: Mxfp4, out_dtype=None, stream=None):
     """A linear layer with MXFP4 weights: x [..., K] in fp16 or bf16 is quantised by the call."""
-    dt = out_dtype or (x.dtype if isinstance(x, torch.Tensor) else None)
     p, T, K, ld = _rows(x, "x")
-    xcode = _code(x.dtype)
-    dev = x.device
-    code = _mx_out(x.shape, w, dt, dev)
+    dt = x.dtype
+    xcode = _code(dt)
+    if out_dtype is not None:
+        dt = out_dtype
+    index = x.get_device()
+    N, code = _mx_out(K, w, dt, index)
     if ld < K:
         raise ValueError("x: rows must not overlap")
-    N = w.shape[0]
     lib = load_library()
-    with _Place(dev, stream) as at:
-        y = torch.empty(x.shape[:-1] + (N,), dtype=dt, device=dev)
-        ws = torch.empty(max(16, lib.sfnn_mxfp4_linear_workspace(T, K)), dtype=torch.uint8, device=dev)
+    with _on(index, stream):
+        y = x.new_empty(x.shape[:-1] + (N,), dtype=dt)
+        nbytes = lib.sfnn_mxfp4_linear_workspace(T, K)
+        ws = x.new_empty(nbytes, dtype=torch.uint8).data_ptr() if nbytes else None
         _check(lib.sfnn_mxfp4_linear(p, ld, T, xcode, w.codes.data_ptr(), w.scales.data_ptr(), N, K, y.data_ptr(), N, code,
-                                     ws.data_ptr(), ws.numel(), _err_word(dev).data_ptr(), at.raw), "sfnn_mxfp4_linear")
+                                     ws, nbytes, _err_ptr(index), _raw_stream(index)), "sfnn_mxfp4_linear")
     return y
 
 
@@ -306,24 +352,21 @@ class GatedSaved:
         return sum(t.numel() * t.element_size() for t in self.tensors())
 
     def _fill(self):
-        c = _GatedSaved()
-        c.kind = SAVE[self.kind]
-        c.r, c.u, c.ld = _vp(self.r), _vp(self.u), self.r.shape[1]
-        if self.kind == "act8":
-            c.r_scales, c.u_scales, c.lds = _vp(self.r_scales), _vp(self.u_scales), self.r_scales.shape[1]
-            c.x, c.ld_x = _vp(self.x_codes), self.x_codes.shape[1]
-            c.x_scales, c.lds_x = _vp(self.x_scales), self.x_scales.shape[1]
-        return c
+        if self.kind == "full":
+            return _GatedSaved(1, 0, self.r.data_ptr(), self.u.data_ptr(), self.r.shape[1])
+        return _GatedSaved(2, 0, self.r.data_ptr(), self.u.data_ptr(), self.r.shape[1], self.r_scales.data_ptr(),
+                           self.u_scales.data_ptr(), self.r_scales.shape[1], self.x_codes.data_ptr(),
+                           self.x_codes.shape[1], self.x_scales.data_ptr(), self.x_scales.shape[1])
 
 
-def _weights(desc, dtype, w_gate, w_up, w_down, d=None):
-    desc.w_gate, n, d, desc.ld_gate = _mat(w_gate, "w_gate", dtype, None, d)
-    desc.w_up, _, _, desc.ld_up = _mat(w_up, "w_up", dtype, n, d)
-    desc.w_down, _, _, desc.ld_down = _mat(w_down, "w_down", dtype, d, n)
+def _weights(dtype, w_gate, w_up, w_down, d):
+    """(n, and the descriptor's six fields of the weights)."""
+    pg, n, d, lg = _mat(w_gate, "w_gate", dtype, None, d)
+    pu, _, _, lu = _mat(w_up, "w_up", dtype, n, d)
+    pd, _, _, ld = _mat(w_down, "w_down", dtype, d, n)
     if d % 8 or n % 8 or not d or not n:
         raise ValueError(f"d and n must be positive multiples of 8, got d = {d}, n = {n}")
-    desc.d, desc.n, desc.dtype = d, n, _code(dtype)
-    return n, d
+    return n, (pg, lg, pu, lu, pd, ld)
 
 
 def gated_ffn_forward(x, w_gate, w_up, w_down, b=None, save=None, stream=None):
@@ -334,41 +377,41 @@ def gated_ffn_forward(x, w_gate, w_up, w_down, b=None, save=None, stream=None):
     None), "full" (relu(G), U and a reference to x) or "act8" (all three as 8-bit blocks)."""
     if save not in SAVE:
         raise ValueError("save must be None, 'full' or 'act8'")
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError("x must be a CUDA tensor")
     dt = x.dtype
     code = _code(dt)
-    q = _GatedDesc()
-    q.x, T, d, q.ldx = _mat(x, "x", dt)
-    n, d = _weights(q, dt, w_gate, w_up, w_down, d)
-    q.T = T
+    px, T, d, ldx = _mat(x, "x", dt)
+    n, wf = _weights(dt, w_gate, w_up, w_down, d)
+    pb = None
     if b is not None:
-        if b.dtype != dt or tuple(b.shape) != (n,) or not b.is_contiguous():
+        if b.dtype != dt or b.shape != (n,) or not b.is_contiguous():
             raise ValueError(f"b must be a contiguous {dt} tensor of {n} elements")
-        q.b = b.data_ptr()
-    dev = x.device
-    _same_device((w_gate, w_up, w_down, b), dev)
+        pb = b.data_ptr()
+    index = x.get_device()
+    _same_device(index, w_gate, w_up, w_down, b)
     lib = load_library()
-    with _Place(dev, stream) as at:
-        y = torch.empty(x.shape, dtype=dt, device=dev)
+    with _on(index, stream):
+        y = x.new_empty(x.shape)
         saved = csaved = None
         if save is not None:
             saved = GatedSaved()
-            saved.kind, saved.shape, saved.dtype, saved.has_b = save, tuple(x.shape), dt, b is not None
+            saved.kind, saved.shape, saved.dtype, saved.has_b = save, x.shape, dt, b is not None
             saved.x = saved.r_scales = saved.u_scales = saved.x_codes = saved.x_scales = None
             if save == "full":
                 saved.x = x
-                ru = torch.empty((2, T, n), dtype=dt, device=dev)
-                saved.r, saved.u = ru[0], ru[1]
+                saved.r, saved.u = x.new_empty((T, n)), x.new_empty((T, n))
             else:
-                saved.r, saved.r_scales = _act8_empty(T, n, dev)
-                saved.u, saved.u_scales = _act8_empty(T, n, dev)
-                saved.x_codes, saved.x_scales = _act8_empty(T, d, dev)
+                saved.r, saved.r_scales = _act8_empty(x, T, n)
+                saved.u, saved.u_scales = _act8_empty(x, T, n)
+                saved.x_codes, saved.x_scales = _act8_empty(x, T, d)
             csaved = ctypes.byref(saved._fill())
         if T:
-            ws = torch.empty(lib.sfnn_gated_workspace(T, d, n, 0), dtype=torch.uint8, device=dev)
-            _check(lib.sfnn_gated_forward(ctypes.byref(q), y.data_ptr(), d, code, csaved, ws.data_ptr(), ws.numel(),
-                                          _err_word(dev).data_ptr(), at.raw), "sfnn_gated_forward")
+            nbytes = lib.sfnn_gated_workspace(T, d, n, 0)
+            ws = x.new_empty(nbytes, dtype=torch.uint8)
+            q = _GatedDesc(T, d, n, code, 0, 0, px, ldx, *wf, pb)
+            _check(lib.sfnn_gated_forward(ctypes.byref(q), y.data_ptr(), d, code, csaved, ws.data_ptr(), nbytes,
+                                          _err_ptr(index), _raw_stream(index)), "sfnn_gated_forward")
     return y, saved
 
 
@@ -376,28 +419,30 @@ def gated_ffn_backward(dy, saved: GatedSaved, w_gate, w_up, w_down, need=(True, 
     """(dx, dw_gate, dw_up, dw_down, db) from dy [..., d] and a forward pass's ``saved``; those
     that ``need`` leaves out, and db without a bias, are None."""
     dt = saved.dtype
-    q = _GatedDesc()
     d = saved.shape[-1]
     pdy, T, _, lddy = _mat(dy, "dy", dt, None, d)
-    n, d = _weights(q, dt, w_gate, w_up, w_down, d)
-    if tuple(dy.shape) != saved.shape or saved.r.shape[1] != (n if saved.kind == "full" else -(-n // 64) * 64):
+    n, wf = _weights(dt, w_gate, w_up, w_down, d)
+    full = saved.kind == "full"
+    if dy.shape != saved.shape or saved.r.shape[1] != (n if full else -(-n // ACT8_BLOCK) * ACT8_BLOCK):
         raise ValueError("dy and the weights must have the forward pass's shapes")
-    q.T = T
-    if saved.kind == "full":
-        q.x, _, _, q.ldx = _mat(saved.x, "x", dt, T, d)
-    dev = dy.device
-    _same_device((w_gate, w_up, w_down, saved.r), dev)
+    px, ldx = None, 0
+    if full:
+        px, _, _, ldx = _mat(saved.x, "x", dt, T, d)
+    index = dy.get_device()
+    _same_device(index, w_gate, w_up, w_down, saved.r)
     lib = load_library()
-    with _Place(dev, stream) as at:
-        def out(on, *shape):
-            return torch.empty(shape, dtype=dt, device=dev) if on else None
-        dx = torch.empty(dy.shape, dtype=dt, device=dev) if need[0] else None
-        dwg, dwu, dwd = out(need[1], n, d), out(need[2], n, d), out(need[3], d, n)
-        db = out(need[4] and saved.has_b, n)
-        ws = torch.empty(max(16, lib.sfnn_gated_workspace(T, d, n, 1)), dtype=torch.uint8, device=dev)
+    with _on(index, stream):
+        dx = dy.new_empty(dy.shape) if need[0] else None
+        dwg = dy.new_empty((n, d)) if need[1] else None
+        dwu = dy.new_empty((n, d)) if need[2] else None
+        dwd = dy.new_empty((d, n)) if need[3] else None
+        db = dy.new_empty((n,)) if need[4] and saved.has_b else None
+        nbytes = lib.sfnn_gated_workspace(T, d, n, 1)
+        ws = dy.new_empty(max(16, nbytes), dtype=torch.uint8)
+        q = _GatedDesc(T, d, n, _code(dt), 0, 0, px, ldx, *wf, None)
         _check(lib.sfnn_gated_backward(ctypes.byref(q), pdy, lddy, ctypes.byref(saved._fill()), _vp(dx), _vp(dwg),
-                                       _vp(dwu), _vp(dwd), _vp(db), ws.data_ptr(), ws.numel(),
-                                       _err_word(dev).data_ptr(), at.raw), "sfnn_gated_backward")
+                                       _vp(dwu), _vp(dwd), _vp(db), ws.data_ptr(), max(16, nbytes), _err_ptr(index),
+                                       _raw_stream(index)), "sfnn_gated_backward")
     return dx, dwg, dwu, dwd, db
 
 
