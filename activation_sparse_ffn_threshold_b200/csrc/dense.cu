@@ -45,6 +45,75 @@ __device__ __forceinline__ TilePos tile_pos(int t, int tiles_m, int tiles_n) {
   return {band * kBand + r % rows, r / rows};
 }
 
+// The unit of work that pair `i` takes in its `n`-th turn (-1: none left).
+struct Walk {
+  int pair, pairs, first, rest, extra, mine, light;
+  __device__ __forceinline__ Walk(const DenseParams &P, int pair_, int pairs_)
+      : pair(pair_), pairs(pairs_), first(P.first), rest(P.rest) {
+    const int over = first % pairs;  // pairs below `over` take one long unit more
+    mine = first / pairs + (pair < over);
+    light = over && pair >= over ? pair - over : -1;
+    extra = over ? P.extra : 0;
+    gap = over ? pairs - over : 0;
+  }
+  int gap;  // pairs with one long unit less
+  __device__ __forceinline__ int unit(int n) const {
+    if (n < mine) return pair + n * pairs;
+    int k = n - mine;
+    if (light >= 0) {
+      if (k < extra) {
+        const int u = light + gap * k;
+        return u < rest ? first + u : -1;
+      }
+      k -= extra;
+    }
+    const int u = gap * extra + pair + pairs * k;
+    return u < rest ? first + u : -1;
+  }
+};
+struct Unit {
+  const DenseProblem *p;  // for its tensor maps; what loops read is copied (it lies in the
+  TilePos pos;            // kernel's parameters, and an indexed read of those is slow)
+  int part, k_lo, k_hi;
+  int M, N, nk0, a_mn, b_mn, out32, relu, split;
+  void *out;
+  int64_t ldo;
+  float *parts;
+};
+__device__ __forceinline__ Unit unit_at(const DenseParams &P, int u) {
+  int i = 0, units = P.p[0].tiles_m * P.p[0].tiles_n * P.p[0].split;
+  while (u >= units) {
+    u -= units;
+    ++i;
+    units = P.p[i].tiles_m * P.p[i].tiles_n * P.p[i].split;
+  }
+  Unit r;
+  r.p = &P.p[i];
+  r.part = 0;
+  r.k_lo = 0;
+  r.k_hi = r.p->nk;
+  int tile = u;
+  if (r.p->split > 1) {  // (at most 16 parts of K: 32 bits hold the products)
+    tile = u / r.p->split;
+    r.part = u - tile * r.p->split;
+    r.k_lo = (int)((uint32_t)r.part * (uint32_t)r.p->nk / (uint32_t)r.p->split);
+    r.k_hi = (int)((uint32_t)(r.part + 1) * (uint32_t)r.p->nk / (uint32_t)r.p->split);
+  }
+  r.pos = tile_pos(tile, r.p->tiles_m, r.p->tiles_n);
+  r.M = r.p->M;
+  r.N = r.p->N;
+  r.nk0 = r.p->nk0;
+  r.a_mn = r.p->a_mn;
+  r.b_mn = r.p->b_mn;
+  r.out32 = r.p->out32;
+  r.relu = r.p->relu;
+  r.split = r.p->split;
+  r.out = r.p->out;
+  r.ldo = r.p->ldo;
+  r.parts = r.p->part;
+  return r;
+}
+
 // 32 values as 16-bit elements to p (16-byte aligned); `cols` of them exist (multiple of 8).
 __device__ __forceinline__ void store32(void *p, const float v[32], int cols, bool bf16) {
   uint4 *q = reinterpret_cast<uint4 *>(p);
@@ -100,8 +169,11 @@ __device__ __forceinline__ void load32(const void *p, float v[32], int cols, boo
 // Each thread owns one row of the tile (its tensor-memory lane) and a half of the tile's
 // columns.  `row` < M on entry.
 
-__device__ __forceinline__ void epi_store(const DenseParams &P, uint32_t taddr, int64_t row, bool live, int n0) {
-  const bool bf16 = P.bf16;
+__device__ __forceinline__ void epi_store(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row, bool live,
+                                          int n0) {
+  const bool bf16 = P.bf16, parts = Q.split > 1;
+  const int64_t ld = parts ? Q.N : Q.ldo;
+  float *f32 = parts ? Q.parts + ((int64_t)Q.part * Q.M + row) * ld : static_cast<float *>(Q.out) + row * ld;
 #pragma unroll 1
   for (int c = 0; c < 128; c += 32) {
     uint32_t raw[32];
@@ -109,33 +181,34 @@ __device__ __forceinline__ void epi_store(const DenseParams &P, uint32_t taddr, 
     tm_ld32(taddr + c, raw);
     tm_wait_ld();
     // relu: the hidden layer, whose rows are padded to 8 columns
-    const int cols = (P.relu ? (P.N + 7) / 8 * 8 : P.N) - (n0 + c);
+    const int cols = (Q.relu ? (Q.N + 7) / 8 * 8 : Q.N) - (n0 + c);
     if (!live || cols <= 0) continue;
     float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       v[i] = __uint_as_float(raw[i]);
-      if (P.relu) {
-        if (P.bias && n0 + c + i < P.N) v[i] += load16(P.bias, n0 + c + i, bf16);
+      if (Q.relu) {
+        if (P.bias && n0 + c + i < Q.N) v[i] += load16(P.bias, n0 + c + i, bf16);
         v[i] = v[i] < 0.f ? 0.f : v[i];
       }
     }
-    if (P.out32) {
-      float *o = static_cast<float *>(P.out) + row * P.ldo + n0 + c;
+    if (Q.out32 || parts) {
+      float *o = f32 + n0 + c;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i * 4 < cols) reinterpret_cast<float4 *>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     } else {
-      store32(static_cast<uint16_t *>(P.out) + row * P.ldo + n0 + c, v, cols, bf16);
+      store32(static_cast<uint16_t *>(Q.out) + row * ld + n0 + c, v, cols, bf16);
     }
   }
 }
 
 // The pair's tile holds 128 neurons: gate columns 0..127, up columns 128..255.  This
 // thread takes 64 of them from n0 on (one act8 block).
-__device__ __forceinline__ void epi_gated(const DenseParams &P, uint32_t tgate, int64_t row, bool live, int n0) {
+__device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, uint32_t tgate, int64_t row,
+                                          bool live, int n0) {
   const bool bf16 = P.bf16;
-  const int cols64 = (int)min((int64_t)64, P.ldo - n0);  // writable columns of H (a multiple of 8)
+  const int cols64 = (int)min((int64_t)64, Q.ldo - n0);  // writable columns of H (a multiple of 8)
   float r[64], u[64];
 #pragma unroll
   for (int c = 0; c < 64; c += 32) {
@@ -148,7 +221,7 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, uint32_t tgate, 
       float g = __uint_as_float(a[i]);
       if (P.bias) {
         const int col = n0 + c + i;
-        g += col < P.N ? load16(P.bias, col, bf16) : 0.f;
+        g += col < Q.N ? load16(P.bias, col, bf16) : 0.f;
       }
       r[c + i] = g < 0.f ? 0.f : g;  // NaN stays NaN
       u[c + i] = __uint_as_float(b[i]);
@@ -190,7 +263,7 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, uint32_t tgate, 
       up[i] = make_uint4(wu[0], wu[1], wu[2], wu[3]);
     }
   }
-  uint16_t *hp = static_cast<uint16_t *>(P.out) + row * P.ldo + n0;
+  uint16_t *hp = static_cast<uint16_t *>(Q.out) + row * Q.ldo + n0;
 #pragma unroll
   for (int c = 0; c < 64; c += 32) {
 #pragma unroll
@@ -199,13 +272,29 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, uint32_t tgate, 
   }
 }
 
+// Sums of 32 columns over a warp's 32 rows: lane i gets column i's.
+__device__ __forceinline__ float column_sums(float v[32], int lane) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const bool hi = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float give = hi ? v[i] : v[i + o], keep = hi ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  return v[0];
+}
+
 // 128 columns of dH from n0 on; reads the saved relu(G) and U of this row, writes dG, dU, H.
-__device__ __forceinline__ void epi_dgated(const DenseParams &P, uint32_t taddr, int64_t row, bool live, int n0) {
+__device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row,
+                                           bool live, int n0) {
   const bool bf16 = P.bf16;
+  const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int c = 0; c < 128; c += 32) {
     uint32_t raw[32];
-    const int cols = P.N - (n0 + c);
+    const int cols = Q.N - (n0 + c);
     const bool on = live && cols > 0;
     float r[32], u[32];
     if (on) {
@@ -236,24 +325,34 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, uint32_t taddr,
     __syncwarp();
     tm_ld32(taddr + c, raw);
     tm_wait_ld();
-    if (!on) continue;
     float dg[32], du[32];
+    if (on) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float dh = __uint_as_float(raw[i]);
-      du[i] = dh * r[i];
-      dg[i] = r[i] > 0.f ? dh * u[i] : 0.f;
-      r[i] *= u[i];
+      for (int i = 0; i < 32; ++i) {
+        const float dh = __uint_as_float(raw[i]);
+        du[i] = dh * r[i];
+        dg[i] = r[i] > 0.f ? dh * u[i] : 0.f;
+        r[i] *= u[i];
+      }
+      const int64_t at = row * Q.ldo + n0 + c;
+      store32(static_cast<uint16_t *>(P.dg) + at, dg, cols, bf16);
+      store32(static_cast<uint16_t *>(P.du) + at, du, cols, bf16);
+      store32(static_cast<uint16_t *>(Q.out) + at, r, cols, bf16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) dg[i] = 0.f;
     }
-    const int64_t at = row * P.ldo + n0 + c;
-    store32(static_cast<uint16_t *>(P.dg) + at, dg, cols, bf16);
-    store32(static_cast<uint16_t *>(P.du) + at, du, cols, bf16);
-    store32(static_cast<uint16_t *>(P.out) + at, r, cols, bf16);
+    if (P.colpart) {
+      __syncwarp();
+      const float sum = column_sums(dg, lane);
+      const int64_t block = (row - lane) >> 5;
+      if (block * 32 < Q.M && lane < cols) P.colpart[block * Q.N + n0 + c + lane] = sum;
+    }
   }
 }
 
 // ---------------------------------------------------------------- the kernel
-template <bool A_MN, bool B_MN, int EPI>
+template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_dense(const __grid_constant__ DenseParams P) {
   extern __shared__ unsigned char smem_raw[];
@@ -263,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int ntiles = P.tiles_m * P.tiles_n;
+  const Walk walk(P, pair, pairs);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -287,16 +386,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      tma_prefetch_desc(&P.a0);
-      tma_prefetch_desc(&P.b0);
       int it = 0;
       bool ok = true;
-      for (int t = pair; t < ntiles && ok; t += pairs) {
-        const TilePos pos = tile_pos(t, P.tiles_m, P.tiles_n);
-        const int m0 = pos.m * kTile + (int)rank * 128;
+      int id = walk.unit(0);
+      Unit w{}, next = unit_at(P, max(id, 0));
+      for (int n = 0; ok && id >= 0; ++n) {
+        w = next;
+        const CUtensorMap *a0 = &w.p->a0, *b0 = &w.p->b0, *a1 = &w.p->a1, *b1 = &w.p->b1;
+        const int m0 = w.pos.m * kTile + (int)rank * 128;
         // gated: the first CTA loads 128 gate rows, the second the same 128 up rows
-        const int n0 = EPI == kEpiGated ? pos.n * 128 : pos.n * kTile + (int)rank * 128;
-        for (int kc = 0; kc < P.nk; ++kc, ++it) {
+        const int n0 = EPI == kEpiGated ? w.pos.n * 128 : w.pos.n * kTile + (int)rank * 128;
+        for (int kc = w.k_lo; kc < w.k_hi; ++kc, ++it) {
+          if (kc == w.k_lo + 1 || w.k_hi == w.k_lo + 1) {  // the next unit, while this one's loads are under way
+            id = walk.unit(n + 1);
+            next = unit_at(P, max(id, 0));
+          }
           const int s = it % kStages;
           if (!bar_wait(&empty[s], (uint32_t)((it / kStages) & 1) ^ 1u)) {
             ok = false;
@@ -305,17 +409,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (rank == 0) bar_expect_tx(&full[s], 2 * kStageBytes);
           const uint32_t bar = cluster_addr(&full[s], 0);
           const uint32_t sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + 16384u;
-          const bool second = kc >= P.nk0;
-          const int k0 = (second ? kc - P.nk0 : kc) * 64;
-          const CUtensorMap *ma = second ? &P.a1 : &P.a0;
-          const CUtensorMap *mb = EPI == kEpiGated ? (rank ? &P.b1 : &P.b0) : (second ? &P.b1 : &P.b0);
-          if (A_MN) {
+          const bool second = kc >= w.nk0;
+          const int k0 = (second ? kc - w.nk0 : kc) * 64;
+          const CUtensorMap *ma = second ? a1 : a0;
+          const CUtensorMap *mb = (EPI == kEpiGated ? rank != 0 : second) ? b1 : b0;
+          if (EPI == kEpiStore && w.a_mn) {
             tma_load_2d_pair(sa, ma, m0, k0, bar);
             tma_load_2d_pair(sa + 8192u, ma, m0 + 64, k0, bar);
           } else {
             tma_load_2d_pair(sa, ma, k0, m0, bar);
           }
-          if (B_MN) {
+          if (EPI == kEpiDGated || (EPI == kEpiStore && w.b_mn)) {
             tma_load_2d_pair(sb, mb, n0, k0, bar);
             tma_load_2d_pair(sb + 8192u, mb, n0 + 64, k0, bar);
           } else {
@@ -335,18 +439,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      const uint32_t idesc = mma_desc_16(256, 256, P.bf16, A_MN, B_MN);
-      int it = 0, i = 0;
+      int it = 0;
       bool ok = true;
-      for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
-        const int buf = i & 1;
-        if (!bar_wait(&acc_empty[buf], (uint32_t)((i >> 1) & 1) ^ 1u)) {
+      int id = walk.unit(0);
+      Unit w{}, next = unit_at(P, max(id, 0));
+      for (int n = 0; ok && id >= 0; ++n) {
+        w = next;
+        const int a_mn = EPI == kEpiStore ? w.a_mn : 0, b_mn = EPI == kEpiStore ? w.b_mn : EPI == kEpiDGated;
+        const uint32_t idesc = mma_desc_16(256, 256, P.bf16, a_mn, b_mn);
+        // a 16-deep step of an operand: 2 KB of an MN-major tile, 32 bytes of a K-major one
+        const uint32_t step_a = a_mn ? 2048u : 32u, step_b = b_mn ? 2048u : 32u;
+        const uint32_t lbo_a = a_mn ? 8192u : 16u, lbo_b = b_mn ? 8192u : 16u;
+        const int buf = n & 1;
+        if (!bar_wait(&acc_empty[buf], (uint32_t)((n >> 1) & 1) ^ 1u)) {
           ok = false;
           break;
         }
         tm_fence_after();
         const uint32_t d = tmem + (uint32_t)buf * 256u;
-        for (int kc = 0; kc < P.nk; ++kc, ++it) {
+        for (int kc = w.k_lo; kc < w.k_hi; ++kc, ++it) {
+          if (kc == w.k_lo + 1 || w.k_hi == w.k_lo + 1) {  // the next unit, while this one's MMAs run
+            id = walk.unit(n + 1);
+            next = unit_at(P, max(id, 0));
+          }
           const int s = it % kStages;
           if (!bar_wait(&full[s], (uint32_t)((it / kStages) & 1))) {
             ok = false;
@@ -355,11 +470,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tm_fence_after();
           const uint32_t sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + 16384u;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t da = A_MN ? mat_desc(sa + k * 2048, 8192, 1024) : mat_desc(sa + k * 32, 16, 1024);
-            const uint64_t db = B_MN ? mat_desc(sb + k * 2048, 8192, 1024) : mat_desc(sb + k * 32, 16, 1024);
-            mma_16<2>(d, da, db, idesc, (kc > 0 || k > 0) ? 1u : 0u);
-          }
+          for (uint32_t k = 0; k < 4; ++k)
+            mma_16<2>(d, mat_desc(sa + k * step_a, lbo_a, 1024), mat_desc(sb + k * step_b, lbo_b, 1024), idesc,
+                      (kc > w.k_lo || k > 0) ? 1u : 0u);
           mma_commit_pair(&empty[s]);
         }
         if (ok) mma_commit_pair(&acc_full[buf]);
@@ -369,25 +482,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    int i = 0;
-    for (int t = pair; t < ntiles; t += pairs, ++i) {
-      const int buf = i & 1;
-      if (!__all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((i >> 1) & 1)))) {
+    if (EPI == kEpiStore && P.colsum) {  // while the first tile is multiplied: db from its 32-row sums
+      for (int c = blockIdx.x * 256 + threadIdx.x - 64; c < P.cols; c += gridDim.x * 256) {
+        float sum = 0.f;
+#pragma unroll 8
+        for (int b = 0; b < P.col_blocks; ++b) sum += __ldg(P.colpart + (int64_t)b * P.cols + c);
+        P.colsum[c] = (uint16_t)pack16(sum, 0.f, P.bf16);
+      }
+    }
+    __syncwarp();
+    for (int n = 0, id; (id = walk.unit(n)) >= 0; ++n) {
+      const Unit w = unit_at(P, id);
+      const int buf = n & 1;
+      if (!__all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((n >> 1) & 1)))) {
         if (lane == 0) latch_error(P.err, kErrTimeout);
         break;
       }
       __syncwarp();
       tm_fence_after();
-      const TilePos pos = tile_pos(t, P.tiles_m, P.tiles_n);
-      const int64_t row = (int64_t)pos.m * kTile + rank * 128 + quad * 32 + lane;
-      const bool live = row < P.M;
+      const int64_t row = (int64_t)w.pos.m * kTile + rank * 128 + quad * 32 + lane;
+      const bool live = row < w.M;
       const uint32_t acc = tmem + lanes + (uint32_t)buf * 256u;
       if (EPI == kEpiGated)
-        epi_gated(P, acc + half * 64, row, live, pos.n * 128 + half * 64);
+        epi_gated(P, w, acc + half * 64, row, live, w.pos.n * 128 + half * 64);
       else if (EPI == kEpiDGated)
-        epi_dgated(P, acc + half * 128, row, live, pos.n * kTile + half * 128);
+        epi_dgated(P, w, acc + half * 128, row, live, w.pos.n * kTile + half * 128);
       else
-        epi_store(P, acc + half * 128, row, live, pos.n * kTile + half * 128);
+        epi_store(P, w, acc + half * 128, row, live, w.pos.n * kTile + half * 128);
       tm_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
@@ -403,23 +524,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;
 
-template <bool A_MN, bool B_MN, int EPI>
+template <int EPI>
 cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose kernel attribute is set
-  const cudaError_t attr = allow_smem(k_dense<A_MN, B_MN, EPI>, kSmem, ready);
+  const cudaError_t attr = allow_smem(k_dense<EPI>, kSmem, ready);
   if (attr != cudaSuccess) return attr;
-  const int grid = 2 * std::min(num_sms / 2, P.tiles_m * P.tiles_n);
-  return launch_pdl(k_dense<A_MN, B_MN, EPI>, dim3(grid), dim3(kThreads), kSmem, s, P);
+  const int grid = 2 * std::min(num_sms / 2, P.first + P.rest);
+  return launch_pdl(k_dense<EPI>, dim3(grid), dim3(kThreads), kSmem, s, P);
 }
 
 }  // namespace
 
-cudaError_t launch_dense(const DenseParams &P, int epi, bool a_mn, bool b_mn, int num_sms, cudaStream_t s) {
-  if (epi == kEpiGated) return run<false, false, kEpiGated>(P, num_sms, s);
-  if (epi == kEpiDGated) return run<false, true, kEpiDGated>(P, num_sms, s);
-  if (a_mn && b_mn) return run<true, true, kEpiStore>(P, num_sms, s);
-  if (b_mn) return run<false, true, kEpiStore>(P, num_sms, s);
-  return run<false, false, kEpiStore>(P, num_sms, s);
+cudaError_t launch_dense(DenseParams &P, int epi, int num_sms, cudaStream_t s) {
+  auto units = [&](int i) { return P.p[i].tiles_m * P.p[i].tiles_n * P.p[i].split; };
+  P.first = units(0);
+  P.rest = 0;
+  int len = 1;
+  for (int i = 1; i < P.count; ++i) {
+    P.rest += units(i);
+    len = std::max(len, P.p[i].nk / P.p[i].split);
+  }
+  P.extra = P.count > 1 ? (P.p[0].nk / P.p[0].split + len / 2) / len : 0;
+  if (epi == kEpiGated) return run<kEpiGated>(P, num_sms, s);
+  if (epi == kEpiDGated) return run<kEpiDGated>(P, num_sms, s);
+  return run<kEpiStore>(P, num_sms, s);
 }
 
 }  // namespace sfnn

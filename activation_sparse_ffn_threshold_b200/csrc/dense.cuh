@@ -77,22 +77,39 @@ enum DenseEpi : int {
   kEpiDGated = 2  // C = dH: dU = dH * R, dG = dH * U * [R > 0], H = R * U
 };
 
-struct alignas(64) DenseParams {
+struct alignas(64) DenseProblem {
   CUtensorMap a0, b0, a1, b1;
   int M, N;       // rows and columns of C (gated: neurons)
   int nk0, nk;    // K chunks of 64 of the first pair, of both
   int tiles_m, tiles_n;
-  int bf16;
-  int out32;      // kEpiStore: fp32 C
-  int relu;       // kEpiStore: C = relu(C + bias)
+  int split;      // parts of K, each a unit of work of its own (kEpiStore)
+  int a_mn, b_mn; // the operands' majors
+  int out32;      // fp32 C
+  int relu;       // C = relu(C + bias)
   void *out;      // C, or H
   int64_t ldo;
+  float *part;    // split > 1: [split][M][N] fp32 sums instead of C
+};
+constexpr int kMaxProblems = 4;
+
+struct DenseParams {
+  DenseProblem p[kMaxProblems];
+  int count;
+  // Work of pair `i` of `pairs`: units i, i + pairs, ... of the first problem (its units take
+  // longest), then of the others' units, where a pair with one long unit less first takes
+  // `extra` more (the host sets it to the two lengths' ratio).
+  int first, rest, extra;
+  int bf16;
   const void *bias;   // kEpiGated, relu: [N] or null
   int save;           // sfnn_save of r and u
   void *r, *u;        // kEpiGated: written; kEpiDGated: read
   float *rs, *us;
   int64_t ldr, lds;   // their row strides (elements), their scales' row strides
   void *dg, *du;      // kEpiDGated: written, row stride ldo as out (H)
+  float *colpart;     // kEpiDGated: [rows / 32][N] sums of dG over 32 rows, or null;
+                      // kEpiStore: such sums to add up over `col_blocks` blocks into
+  uint16_t *colsum;   // this, of `cols` columns (null: none)
+  int col_blocks, cols;
   int32_t *err;
 };
 
@@ -111,7 +128,8 @@ cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &ready) {
 
 int device_sms();  // SMs of the current device (0: no device)
 
-cudaError_t launch_dense(const DenseParams &P, int epi, bool a_mn, bool b_mn, int num_sms, cudaStream_t s);
+// Fills first, rest and extra from the problems.
+cudaError_t launch_dense(DenseParams &P, int epi, int num_sms, cudaStream_t s);
 
 // The products of few tokens (slim.cu): out = x . w0^T, or with w1 the gated hidden layer
 // relu(x . w0^T + bias) * (x . w1^T).  K-major weights; `early`: w0 may be read while the

@@ -1,4 +1,5 @@
 // gated.cu -- the gated FFN over all neurons: forward, backward, and the entry points.
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -24,61 +25,41 @@ int device_sms() {
 
 namespace {
 
-// ---------------------------------------------------------------- column sums (db)
-// db[i] = sum over tokens of dG[t][i].  A block sums 64 columns of its share of the rows:
-// 8 lanes across (16 bytes each), 32 rows at a time, then the 32 row sums in a fixed order.
-// Bound by the bytes of dG (2 T n).
-__global__ void __launch_bounds__(256) k_colsum(const uint16_t *__restrict__ v, int64_t ld, int T, int n, int bf16,
-                                                int rows_per, float *__restrict__ part, void *__restrict__ out) {
-  __shared__ float sum[32][65];
+// out[i] = sum over the parts of a split product, in their order.  Bound by the parts' bytes.
+__global__ void __launch_bounds__(256) k_join(const float *__restrict__ part, int parts, int M, int N, int bf16, int out32,
+                                              void *__restrict__ out, int64_t ldo) {
   pdl_wait();
   pdl_launch_dependents();
-  const int cl = threadIdx.x & 7, rl = threadIdx.x >> 3;
-  const int col = blockIdx.x * 64 + cl * 8;
-  const int64_t t0 = (int64_t)blockIdx.y * rows_per, t1 = min((int64_t)T, t0 + rows_per);
-  float a[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (col < n) {
+  const int64_t total = (int64_t)M * N / 4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int64_t t = t0 + rl; t < t1; t += 32) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(v + t * ld + col));
-      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack16(q[j], bf16);
-        a[2 * j] += f.x;
-        a[2 * j + 1] += f.y;
-      }
+    for (int p = 0; p < parts; ++p) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(part) + p * total + i);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) sum[rl][cl * 8 + j] = a[j];
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    const int c = blockIdx.x * 64 + threadIdx.x;
-    float s = 0.f;
-#pragma unroll
-    for (int r = 0; r < 32; ++r) s += sum[r][threadIdx.x];
-    if (c < n) {
-      if (part)
-        part[(int64_t)blockIdx.y * n + c] = s;
-      else
-        static_cast<uint16_t *>(out)[c] = (uint16_t)(pack16(s, 0.f, bf16) & 0xffffu);
-    }
+    const int64_t row = i * 4 / N, col = i * 4 - row * N;
+    if (out32)
+      *reinterpret_cast<float4 *>(static_cast<float *>(out) + row * ldo + col) = s;
+    else
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + row * ldo + col) =
+          make_uint2(pack16(s.x, s.y, bf16), pack16(s.z, s.w, bf16));
   }
 }
-__global__ void __launch_bounds__(256) k_colsum_join(const float *__restrict__ part, int splits, int n, int bf16,
-                                                     uint16_t *__restrict__ out) {
+// db[i] = the sum of its 32-row sums (where no product follows that adds them up on the way).
+__global__ void __launch_bounds__(256) k_colsum(const float *__restrict__ part, int blocks, int n, int bf16,
+                                                uint16_t *__restrict__ out) {
   pdl_wait();
   pdl_launch_dependents();
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= n) return;
   float s = 0.f;
-  for (int k = 0; k < splits; ++k) s += part[(int64_t)k * n + c];
+#pragma unroll 8
+  for (int k = 0; k < blocks; ++k) s += part[(int64_t)k * n + c];
   out[c] = (uint16_t)(pack16(s, 0.f, bf16) & 0xffffu);
 }
 
-constexpr int kSumRows = 512;  // rows of a column-sum block
-int sum_splits(int T) { return (T + kSumRows - 1) / kSumRows; }
+int64_t row_blocks(int64_t T) { return (T + 31) / 32; }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 int64_t hidden_bytes(int64_t T, int64_t n) { return up(T * up(n, 8) * 2, 256); }
@@ -125,7 +106,7 @@ struct Operand {
   int64_t ld;
   bool mn;
 };
-bool set_pair(DenseParams &P, int which, const Operand &a, const Operand &b, int M, int N, int64_t K) {
+bool set_pair(DenseProblem &P, int which, const Operand &a, const Operand &b, int M, int N, int64_t K) {
   CUtensorMap *ma = which ? &P.a1 : &P.a0, *mb = which ? &P.b1 : &P.b0;
   return (a.mn ? make_tensor_map(ma, a.p, 2, K, M, a.ld, 64, 64, true)
                : make_tensor_map(ma, a.p, 2, M, K, a.ld, 128, 64, true)) &&
@@ -134,28 +115,55 @@ bool set_pair(DenseParams &P, int which, const Operand &a, const Operand &b, int
 }
 int chunks(int64_t K) { return (int)((K + 63) / 64); }
 
-sfnn_status product(const Operand &a, const Operand &b, int M, int N, int64_t K, const Operand *a1, const Operand *b1,
-                    int64_t K1, void *out, int64_t ldo, int out32, int bf16, int32_t *err, cudaStream_t s,
-                    const void *relu_bias = nullptr) {
-  DenseParams P{};
-  P.relu = relu_bias != nullptr;
-  P.bias = relu_bias;
+// Parts of K of an M x N product of nk chunks: where its 256 x 256 tiles leave most SMs idle
+// and K is long, as many as fill the SMs, of at least 8 chunks each.
+int parts_of(int64_t M, int64_t N, int nk, int sms) {
+  const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256), pairs = sms / 2;
+  if (tiles < 1 || tiles * 2 > pairs) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({pairs / tiles, nk / 8, 16}));
+}
+int64_t parts_bytes(int64_t M, int64_t N, int nk, int sms) {
+  const int p = parts_of(M, N, nk, sms);
+  return p > 1 ? up(p * M * N * 4, 256) : 0;
+}
+
+bool set_problem(DenseProblem &P, const Operand &a, const Operand &b, int M, int N, int64_t K, void *out, int64_t ldo) {
   P.M = M;
   P.N = N;
   P.nk0 = P.nk = chunks(K);
-  if (!set_pair(P, 0, a, b, M, N, K)) return SFNN_ERR_CUDA;
-  if (a1) {
-    if (!set_pair(P, 1, *a1, *b1, M, N, K1)) return SFNN_ERR_CUDA;
-    P.nk += chunks(K1);
-  }
   P.tiles_m = (M + 255) / 256;
   P.tiles_n = (N + 255) / 256;
-  P.bf16 = bf16;
+  P.split = 1;
+  P.a_mn = a.mn;
+  P.b_mn = b.mn;
   P.out = out;
   P.ldo = ldo;
-  P.out32 = out32;
+  return set_pair(P, 0, a, b, M, N, K);
+}
+cudaError_t join(const DenseProblem &P, int bf16, int sms, cudaStream_t s) {
+  if (P.split == 1) return cudaSuccess;
+  const int64_t blocks = ((int64_t)P.M * P.N / 4 + 255) / 256;
+  return launch_pdl(k_join, dim3((unsigned)std::min<int64_t>(blocks, 8 * sms)), dim3(256), 0, s, P.part, P.split, P.M, P.N,
+                    bf16, P.out32, P.out, P.ldo);
+}
+
+sfnn_status product(const Operand &a, const Operand &b, int M, int N, int64_t K, void *out, int64_t ldo, int out32, int bf16,
+                    float *parts, int32_t *err, cudaStream_t s, const void *relu_bias = nullptr) {
+  const int sms = device_sms();
+  DenseParams P{};
+  P.count = 1;
+  if (!set_problem(P.p[0], a, b, M, N, K, out, ldo)) return SFNN_ERR_CUDA;
+  P.p[0].out32 = out32;
+  P.p[0].relu = relu_bias != nullptr;
+  if (parts) {
+    P.p[0].split = parts_of(M, N, P.p[0].nk, sms);
+    P.p[0].part = parts;
+  }
+  P.bias = relu_bias;
+  P.bf16 = bf16;
   P.err = err;
-  return launch_dense(P, kEpiStore, a.mn, b.mn, device_sms(), s) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
+  if (launch_dense(P, kEpiStore, sms, s) != cudaSuccess || join(P.p[0], bf16, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
+  return SFNN_OK;
 }
 
 }  // namespace
@@ -167,8 +175,10 @@ extern "C" {
 
 int64_t sfnn_gated_workspace(int32_t T, int32_t d, int32_t n, int32_t backward) {
   if (T < 0 || d < 1 || n < 1) return -1;
-  if (!backward) return hidden_bytes(T, n);
-  return 3 * hidden_bytes(T, n) + hidden_bytes(T, d) + up((int64_t)sum_splits(T) * n * 4, 256);
+  const int sms = device_sms();
+  if (!backward) return hidden_bytes(T, n) + parts_bytes(T, d, chunks(n), sms);
+  return 3 * hidden_bytes(T, n) + hidden_bytes(T, d) + up(row_blocks(T) * n * 4, 256) +
+         parts_bytes(T, d, 2 * chunks(n), sms);
 }
 
 sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, int32_t y_dtype, sfnn_gated_saved *sv,
@@ -189,10 +199,10 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
                            sv->x_scales, sv->lds_x, s) != cudaSuccess)
     return SFNN_ERR_CUDA;
   const bool slim = slim_serves(q->T);
+  float *parts = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + hidden_bytes(q->T, q->n));
   const Operand h{ws, ldh, false}, wd{q->w_down, q->ld_down, q->down_layout == SFNN_DOWN_NEURON_MAJOR};
   auto down = [&](int early) -> sfnn_status {
-    if (!slim || wd.mn)
-      return product(h, wd, q->T, q->d, q->n, nullptr, nullptr, 0, y, ldy, y_dtype == SFNN_F32, bf16, err, s);
+    if (!slim || wd.mn) return product(h, wd, q->T, q->d, q->n, y, ldy, y_dtype == SFNN_F32, bf16, parts, err, s);
     SlimArgs a{};
     a.x = ws;
     a.ldx = ldh;
@@ -229,18 +239,21 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
     return down(1);
   }
   DenseParams P{};
-  P.M = q->T;
-  P.N = q->n;
-  P.nk0 = P.nk = chunks(q->d);
-  if (!make_tensor_map(&P.a0, q->x, 2, q->T, q->d, q->ldx, 128, 64, true) ||
-      !make_tensor_map(&P.b0, q->w_gate, 2, q->n, q->d, q->ld_gate, 128, 64, true) ||
-      !make_tensor_map(&P.b1, q->w_up, 2, q->n, q->d, q->ld_up, 128, 64, true))
+  DenseProblem &Q = P.p[0];
+  P.count = 1;
+  Q.M = q->T;
+  Q.N = q->n;
+  Q.nk0 = Q.nk = chunks(q->d);
+  Q.split = 1;
+  Q.tiles_m = (q->T + 255) / 256;
+  Q.tiles_n = (q->n + 127) / 128;
+  Q.out = ws;
+  Q.ldo = ldh;
+  if (!make_tensor_map(&Q.a0, q->x, 2, q->T, q->d, q->ldx, 128, 64, true) ||
+      !make_tensor_map(&Q.b0, q->w_gate, 2, q->n, q->d, q->ld_gate, 128, 64, true) ||
+      !make_tensor_map(&Q.b1, q->w_up, 2, q->n, q->d, q->ld_up, 128, 64, true))
     return SFNN_ERR_CUDA;
-  P.tiles_m = (q->T + 255) / 256;
-  P.tiles_n = (q->n + 127) / 128;
   P.bf16 = bf16;
-  P.out = ws;
-  P.ldo = ldh;
   P.bias = q->b;
   P.save = kind;
   if (kind != SFNN_SAVE_NONE) {
@@ -252,7 +265,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
     P.lds = sv->lds;
   }
   P.err = err;
-  if (launch_dense(P, kEpiGated, false, false, device_sms(), s) != cudaSuccess) return SFNN_ERR_CUDA;
+  if (launch_dense(P, kEpiGated, device_sms(), s) != cudaSuccess) return SFNN_ERR_CUDA;
   return down(0);
 }
 
@@ -286,30 +299,9 @@ sfnn_status sfnn_gated_backward(const sfnn_gated_desc *q, const void *dy, int64_
   const int64_t hb = hidden_bytes(T, n), ldh = up(n, 8);
   unsigned char *w = static_cast<unsigned char *>(ws);
   void *h = w, *dg = w + hb, *du = w + 2 * hb, *xr = w + 3 * hb;
-  float *part = reinterpret_cast<float *>(w + 3 * hb + hidden_bytes(T, d));
-
-  DenseParams P{};
-  P.M = T;
-  P.N = n;
-  P.nk0 = P.nk = chunks(d);
-  if (!set_pair(P, 0, Operand{dy, lddy, false}, Operand{q->w_down, q->ld_down, true}, T, n, d)) return SFNN_ERR_CUDA;
-  P.tiles_m = (T + 255) / 256;
-  P.tiles_n = (n + 255) / 256;
-  P.bf16 = bf16;
-  P.out = h;
-  P.dg = dg;
-  P.du = du;
-  P.ldo = ldh;
-  P.save = sv->kind;
-  P.r = sv->r;
-  P.u = sv->u;
-  P.ldr = sv->ld;
-  P.rs = sv->r_scales;
-  P.us = sv->u_scales;
-  P.lds = sv->lds;
-  P.err = err;
+  float *colpart = reinterpret_cast<float *>(w + 3 * hb + hidden_bytes(T, d));
+  float *parts = colpart + up(row_blocks(T) * n * 4, 256) / 4;
   const int sms = device_sms();
-  if (launch_dense(P, kEpiDGated, false, true, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
 
   Operand x{q->x, q->ldx, true};
   if (sv->kind == SFNN_SAVE_ACT8 && (dw_gate || dw_up)) {
@@ -318,23 +310,56 @@ sfnn_status sfnn_gated_backward(const sfnn_gated_desc *q, const void *dy, int64_
       return SFNN_ERR_CUDA;
     x = Operand{xr, up(d, 8), true};
   }
-  if (db) {
-    const int splits = sum_splits(T);
-    if (launch_pdl(k_colsum, dim3((n + 63) / 64, splits), dim3(256), 0, s, static_cast<const uint16_t *>(dg), ldh, T, n,
-                   bf16, kSumRows, splits > 1 ? part : nullptr, db) != cudaSuccess)
+  {
+    DenseParams P{};
+    P.count = 1;
+    if (!set_problem(P.p[0], Operand{dy, lddy, false}, Operand{q->w_down, q->ld_down, true}, T, n, d, h, ldh))
       return SFNN_ERR_CUDA;
-    if (splits > 1 && launch_pdl(k_colsum_join, dim3((n + 255) / 256), dim3(256), 0, s, part, splits, n, bf16,
-                                 static_cast<uint16_t *>(db)) != cudaSuccess)
-      return SFNN_ERR_CUDA;
+    P.bf16 = bf16;
+    P.dg = dg;
+    P.du = du;
+    P.colpart = db ? colpart : nullptr;
+    P.save = sv->kind;
+    P.r = sv->r;
+    P.u = sv->u;
+    P.ldr = sv->ld;
+    P.rs = sv->r_scales;
+    P.us = sv->u_scales;
+    P.lds = sv->lds;
+    P.err = err;
+    if (launch_dense(P, kEpiDGated, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
   }
+  // dX, dWg, dWu and dWd in one launch (they all wait for dG, dU and H only), dX's long tiles
+  // first; db is added up by its epilogue warps while they wait for the first tile
+  DenseParams P{};
+  const DenseProblem *split = nullptr;
   if (dx) {
+    DenseProblem &Q = P.p[P.count++];
     const Operand ag{dg, ldh, false}, au{du, ldh, false}, bg{q->w_gate, q->ld_gate, true}, bu{q->w_up, q->ld_up, true};
-    if ((st = product(ag, bg, T, d, n, &au, &bu, n, dx, d, 0, bf16, err, s)) != SFNN_OK) return st;
+    if (!set_problem(Q, ag, bg, T, d, n, dx, d) || !set_pair(Q, 1, au, bu, T, d, n)) return SFNN_ERR_CUDA;
+    Q.nk += chunks(n);
+    Q.split = parts_of(T, d, Q.nk, sms);
+    Q.part = parts;
+    split = &Q;
   }
   const Operand tg{dg, ldh, true}, tu{du, ldh, true}, th{h, ldh, true}, ty{dy, lddy, true};
-  if (dw_gate && (st = product(tg, x, n, d, T, nullptr, nullptr, 0, dw_gate, d, 0, bf16, err, s)) != SFNN_OK) return st;
-  if (dw_up && (st = product(tu, x, n, d, T, nullptr, nullptr, 0, dw_up, d, 0, bf16, err, s)) != SFNN_OK) return st;
-  if (dw_down && (st = product(ty, th, d, n, T, nullptr, nullptr, 0, dw_down, n, 0, bf16, err, s)) != SFNN_OK) return st;
+  if (dw_gate && !set_problem(P.p[P.count++], tg, x, n, d, T, dw_gate, d)) return SFNN_ERR_CUDA;
+  if (dw_up && !set_problem(P.p[P.count++], tu, x, n, d, T, dw_up, d)) return SFNN_ERR_CUDA;
+  if (dw_down && !set_problem(P.p[P.count++], ty, th, d, n, T, dw_down, n)) return SFNN_ERR_CUDA;
+  const int blocks = (int)row_blocks(T);
+  if (P.count) {
+    P.bf16 = bf16;
+    P.err = err;
+    P.colpart = colpart;
+    P.colsum = static_cast<uint16_t *>(db);
+    P.col_blocks = blocks;
+    P.cols = n;
+    if (launch_dense(P, kEpiStore, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
+    if (split && join(*split, bf16, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
+  } else if (db && launch_pdl(k_colsum, dim3((n + 255) / 256), dim3(256), 0, s, colpart, blocks, n, bf16,
+                              static_cast<uint16_t *>(db)) != cudaSuccess) {
+    return SFNN_ERR_CUDA;
+  }
   return SFNN_OK;
 }
 
@@ -370,9 +395,10 @@ sfnn_status sfnn_forward_prompt(sfnn_handle h, const void *X, int32_t T, float *
     return SFNN_ERR_INVALID_ARG;
   if (T > (1 << 24)) return SFNN_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  float *parts = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + hidden_bytes(T, L.n));
   const Operand x{X, L.d, false}, wu{rows, ld, false}, hh{ws, up(L.n, 8), false}, wd{rows + L.d, ld, true};
-  sfnn_status st = product(x, wu, T, L.n, L.d, nullptr, nullptr, 0, ws, up(L.n, 8), 0, 0, h->err, s, h->bias);
-  if (st == SFNN_OK) st = product(hh, wd, T, L.d, L.n, nullptr, nullptr, 0, Y, L.d, 1, 0, h->err, s);
+  sfnn_status st = product(x, wu, T, L.n, L.d, ws, up(L.n, 8), 0, 0, nullptr, h->err, s, h->bias);
+  if (st == SFNN_OK) st = product(hh, wd, T, L.d, L.n, Y, L.d, 1, 0, parts, h->err, s);
   if (st == SFNN_OK) h->launches += 2;
   return st;
 }

@@ -137,3 +137,8 @@ def test_mxfp4_refuses():
         sf.quantize_mxfp4(torch.zeros(2, 64, dtype=torch.float16))
     with pytest.raises(TypeError):
         sf.mxfp4_linear(torch.zeros(2, 64, dtype=torch.float16), None)
+
+
+def test_workspace_of_no_tokens():
+    lib = sf.load_library()
+    assert lib.sfnn_gated_workspace(0, 64, 128, 0) >= 0 and lib.sfnn_gated_workspace(0, 64, 128, 1) >= 0

@@ -98,7 +98,7 @@ def backward64(x, wg, wu, wd, dy, R, U, on):
 
 
 @pytest.mark.parametrize("dt", KINDS)
-@pytest.mark.parametrize("T,d,n", SHAPES)
+@pytest.mark.parametrize("T,d,n", SHAPES + [(5000, 1024, 4104), (2100, 1104, 520), (40, 2048, 8)])
 def test_backward_full(T, d, n, dt):
     x, wg, wu, wd, b, dy = layer(T, d, n, dt, seed=7 * T + d, bias=T % 2 == 1)
     y, saved = sf.gated_ffn_forward(x, wg, wu, wd, b, save="full")
