@@ -114,19 +114,83 @@ __device__ __forceinline__ Unit unit_at(const DenseParams &P, int u) {
   return r;
 }
 
-// 32 values as 16-bit elements to p (16-byte aligned); `cols` of them exist (multiple of 8).
-__device__ __forceinline__ void store32(void *p, const float v[32], int cols, bool bf16) {
-  uint4 *q = reinterpret_cast<uint4 *>(p);
+// ---------------------------------------------------------------- staging
+// An accumulator lane is a row, so a thread's values lie along a row, and 32 threads writing
+// 16 bytes each would touch 32 lines an instruction (measured: 9 to 17 us for one tile's
+// epilogue).  A warp's values pass through shared memory instead, 64 bytes of each of its 32
+// rows at a time: written by row, read (and stored) with 4 lanes to a row.  The 16-byte
+// pieces of row r are rotated by (r / 2) % 4, so neither side has bank conflicts.
+constexpr uint32_t kPanel = 2048;      // 32 rows x 64 bytes
+constexpr uint32_t kWarpStage = 2 * kPanel;
+__device__ __forceinline__ uint32_t panel_at(uint32_t panel, int row, int piece) {
+  return panel + (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ void sts16(uint32_t a, const uint4 &v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// 64 bytes of this lane's row, to `base` (the warp's first row) + row * ld bytes for the rows
+// and 16-byte pieces that exist.  The whole warp; the panel is free again afterwards.
+__device__ __forceinline__ void panel_out(uint32_t panel, const uint4 w[4], unsigned char *base, int64_t ld, int rows,
+                                          int pieces) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i * 8 < cols) {
-      uint4 w;
-      w.x = pack16(v[8 * i], v[8 * i + 1], bf16);
-      w.y = pack16(v[8 * i + 2], v[8 * i + 3], bf16);
-      w.z = pack16(v[8 * i + 4], v[8 * i + 5], bf16);
-      w.w = pack16(v[8 * i + 6], v[8 * i + 7], bf16);
-      q[i] = w;
+  for (int j = 0; j < 4; ++j) sts16(panel_at(panel, lane, j), w[j]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (lane >> 2), piece = lane & 3;
+    const uint4 v = lds16(panel_at(panel, row, piece));
+    if (row < rows && piece < pieces) *reinterpret_cast<uint4 *>(base + row * ld + piece * 16) = v;
+  }
+}
+// The way in: request 64 bytes of each of the warp's rows (zeros where none exist) ...
+__device__ __forceinline__ void panel_request(uint4 v[4], const unsigned char *base, int64_t ld, int rows, int pieces) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (lane >> 2), piece = lane & 3;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows && piece < pieces) v[i] = __ldg(reinterpret_cast<const uint4 *>(base + row * ld + piece * 16));
+  }
+}
+// ... and hand each lane its row's.
+__device__ __forceinline__ void panel_in(uint32_t panel, const uint4 v[4], uint4 w[4]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sts16(panel_at(panel, i * 8 + (lane >> 2), lane & 3), v[i]);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = lds16(panel_at(panel, lane, j));
+}
+
+// 32 values as 16-bit elements.
+__device__ __forceinline__ void pack32(uint4 w[4], const float v[32], bool bf16) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i].x = pack16(v[8 * i], v[8 * i + 1], bf16);
+    w[i].y = pack16(v[8 * i + 2], v[8 * i + 3], bf16);
+    w[i].z = pack16(v[8 * i + 4], v[8 * i + 5], bf16);
+    w[i].w = pack16(v[8 * i + 6], v[8 * i + 7], bf16);
+  }
+}
+__device__ __forceinline__ void unpack32(const uint4 w[4], float v[32], bool bf16) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack16(a[j], bf16);
+      v[8 * i + 2 * j] = f.x;
+      v[8 * i + 2 * j + 1] = f.y;
     }
+  }
 }
 // relu(G) as 16-bit elements: a positive value that rounds to zero keeps the type's
 // smallest positive value, so that the stored value's sign is the ReLU's mask.
@@ -136,104 +200,102 @@ __device__ __forceinline__ uint32_t pack16_relu(float a, float b, bool bf16) {
   if (b > 0.f && (w >> 16) == 0) w |= 0x10000u;
   return w;
 }
-__device__ __forceinline__ void store32_relu(void *p, const float v[32], int cols, bool bf16) {
-  uint4 *q = reinterpret_cast<uint4 *>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i * 8 < cols) {
-      uint4 w;
-      w.x = pack16_relu(v[8 * i], v[8 * i + 1], bf16);
-      w.y = pack16_relu(v[8 * i + 2], v[8 * i + 3], bf16);
-      w.z = pack16_relu(v[8 * i + 4], v[8 * i + 5], bf16);
-      w.w = pack16_relu(v[8 * i + 6], v[8 * i + 7], bf16);
-      q[i] = w;
-    }
-}
-__device__ __forceinline__ void load32(const void *p, float v[32], int cols, bool bf16) {
-  const uint4 *q = reinterpret_cast<const uint4 *>(p);
+__device__ __forceinline__ void pack32_relu(uint4 w[4], const float v[32], bool bf16) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (i * 8 < cols) w = __ldg(q + i);
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack16(a[j], bf16);
-      v[8 * i + 2 * j] = f.x;
-      v[8 * i + 2 * j + 1] = f.y;
-    }
+    w[i].x = pack16_relu(v[8 * i], v[8 * i + 1], bf16);
+    w[i].y = pack16_relu(v[8 * i + 2], v[8 * i + 3], bf16);
+    w[i].z = pack16_relu(v[8 * i + 4], v[8 * i + 5], bf16);
+    w[i].w = pack16_relu(v[8 * i + 6], v[8 * i + 7], bf16);
   }
 }
 
 // ---------------------------------------------------------------- epilogues
 // Each thread owns one row of the tile (its tensor-memory lane) and a half of the tile's
-// columns.  `row` < M on entry.
+// columns; a warp owns 32 rows from `row0` on and stores them through its `panel`s.
 
-__device__ __forceinline__ void epi_store(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row, bool live,
-                                          int n0) {
+__device__ __forceinline__ void epi_store(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
+                                          uint32_t panel) {
   const bool bf16 = P.bf16, parts = Q.split > 1;
-  const int64_t ld = parts ? Q.N : Q.ldo;
-  float *f32 = parts ? Q.parts + ((int64_t)Q.part * Q.M + row) * ld : static_cast<float *>(Q.out) + row * ld;
+  const int rows = (int)min((int64_t)32, Q.M - row0);
+  // relu: the hidden layer, whose rows are padded to 8 columns
+  const int end = Q.relu ? (Q.N + 7) / 8 * 8 : Q.N;
+  const bool wide = Q.out32 || parts;
+  const int64_t ld = (parts ? (int64_t)Q.N : Q.ldo) * (wide ? 4 : 2);
+  unsigned char *base = parts ? reinterpret_cast<unsigned char *>(Q.parts) + ((int64_t)Q.part * Q.M + row0) * ld
+                              : static_cast<unsigned char *>(Q.out) + row0 * ld;
 #pragma unroll 1
   for (int c = 0; c < 128; c += 32) {
+    const int cols = end - (n0 + c);
+    if (rows <= 0 || cols <= 0) break;  // (the whole warp)
     uint32_t raw[32];
+    float v[32];
     __syncwarp();
     tm_ld32(taddr + c, raw);
     tm_wait_ld();
-    // relu: the hidden layer, whose rows are padded to 8 columns
-    const int cols = (Q.relu ? (Q.N + 7) / 8 * 8 : Q.N) - (n0 + c);
-    if (!live || cols <= 0) continue;
-    float v[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      v[i] = __uint_as_float(raw[i]);
-      if (Q.relu) {
-        if (P.bias && n0 + c + i < Q.N) v[i] += load16(P.bias, n0 + c + i, bf16);
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+    if (Q.relu) {
+      const float own = P.bias && n0 + c + (int)(threadIdx.x & 31) < Q.N ? load16(P.bias, n0 + c + (threadIdx.x & 31), bf16) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        v[i] += __shfl_sync(0xffffffffu, own, i);
         v[i] = v[i] < 0.f ? 0.f : v[i];
       }
     }
-    if (Q.out32 || parts) {
-      float *o = f32 + n0 + c;
+    if (wide) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i * 4 < cols) reinterpret_cast<float4 *>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      for (int h = 0; h < 2; ++h) {
+        uint4 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = make_uint4(__float_as_uint(v[16 * h + 4 * j]), __float_as_uint(v[16 * h + 4 * j + 1]),
+                            __float_as_uint(v[16 * h + 4 * j + 2]), __float_as_uint(v[16 * h + 4 * j + 3]));
+        panel_out(panel + h * kPanel, w, base + (n0 + c + 16 * h) * 4, ld, rows, (cols - 16 * h + 3) / 4);
+      }
     } else {
-      store32(static_cast<uint16_t *>(Q.out) + row * ld + n0 + c, v, cols, bf16);
+      uint4 w[4];
+      pack32(w, v, bf16);
+      panel_out(panel + ((c >> 5) & 1) * kPanel, w, base + (n0 + c) * 2, ld, rows, (cols + 7) / 8);
     }
   }
 }
 
 // The pair's tile holds 128 neurons: gate columns 0..127, up columns 128..255.  This
-// thread takes 64 of them from n0 on (one act8 block).
-__device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, uint32_t tgate, int64_t row,
-                                          bool live, int n0) {
+// warp takes 64 of them from n0 on (one act8 block); `bias` holds n0 + lane's and
+// n0 + 32 + lane's.
+__device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, uint32_t tgate, int64_t row0, int n0,
+                                          const float bias[2], uint32_t panel) {
   const bool bf16 = P.bf16;
-  const int cols64 = (int)min((int64_t)64, Q.ldo - n0);  // writable columns of H (a multiple of 8)
+  const int lane = threadIdx.x & 31;
+  const int rows = (int)min((int64_t)32, Q.M - row0);
+  const int cols = (int)min((int64_t)64, Q.ldo - n0);  // writable columns of H (a multiple of 8)
   float r[64], u[64];
 #pragma unroll
   for (int c = 0; c < 64; c += 32) {
     uint32_t a[32], b[32];
+    __syncwarp();
     tm_ld32(tgate + c, a);
     tm_ld32(tgate + 128 + c, b);
     tm_wait_ld();
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      float g = __uint_as_float(a[i]);
-      if (P.bias) {
-        const int col = n0 + c + i;
-        g += col < Q.N ? load16(P.bias, col, bf16) : 0.f;
-      }
+      const float g = __uint_as_float(a[i]) + __shfl_sync(0xffffffffu, bias[c >> 5], i);
       r[c + i] = g < 0.f ? 0.f : g;  // NaN stays NaN
       u[c + i] = __uint_as_float(b[i]);
     }
   }
-  if (!live || cols64 <= 0) return;
+  if (rows <= 0 || cols <= 0) return;  // (the whole warp)
+  uint4 w[4];
   if (P.save == SFNN_SAVE_FULL) {
-    uint16_t *rp = static_cast<uint16_t *>(P.r) + row * P.ldr + n0, *up = static_cast<uint16_t *>(P.u) + row * P.ldr + n0;
+    unsigned char *rp = static_cast<unsigned char *>(P.r) + (row0 * P.ldr + n0) * 2;
+    unsigned char *up = static_cast<unsigned char *>(P.u) + (row0 * P.ldr + n0) * 2;
 #pragma unroll
     for (int c = 0; c < 64; c += 32) {
-      store32_relu(rp + c, r + c, cols64 - c, bf16);
-      store32(up + c, u + c, cols64 - c, bf16);
+      pack32_relu(w, r + c, bf16);
+      panel_out(panel, w, rp + c * 2, P.ldr * 2, rows, (cols - c) / 8);
+      pack32(w, u + c, bf16);
+      panel_out(panel + kPanel, w, up + c * 2, P.ldr * 2, rows, (cols - c) / 8);
     }
   } else if (P.save == SFNN_SAVE_ACT8) {
     uint32_t rt = 0, ut = 0;
@@ -243,32 +305,40 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, u
       ut = max(ut, __float_as_uint(u[i]) & 0x7fffffffu);
     }
     const Act8Scale sr = act8_scale(rt, 255.f), su = act8_scale(ut, 127.f);
-    P.rs[row * P.lds + (n0 >> 6)] = sr.scale;
-    P.us[row * P.lds + (n0 >> 6)] = su.scale;
-    uint4 *rp = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(P.r) + row * P.ldr + n0);
-    uint4 *up = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(P.u) + row * P.ldr + n0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // whole blocks: code rows are padded to 64 columns
-      uint32_t wr[4], wu[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float *a = r + 16 * i + 4 * j, *c = u + 16 * i + 4 * j;
-        uint32_t pos = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) pos |= a[k] > 0.f ? 1u << (8 * k) : 0u;
-        wr[j] = act8_lift(act8_codes(a[0], a[1], a[2], a[3], sr.inv), pos);
-        wu[j] = act8_codes(c[0], c[1], c[2], c[3], su.inv);
-      }
-      rp[i] = make_uint4(wr[0], wr[1], wr[2], wr[3]);
-      up[i] = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+    if (lane < rows) {
+      P.rs[(row0 + lane) * P.lds + (n0 >> 6)] = sr.scale;
+      P.us[(row0 + lane) * P.lds + (n0 >> 6)] = su.scale;
     }
+    auto codes = [&](const float *v, float inv, bool relu) {  // whole blocks: code rows are padded to 64 columns
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float *a = v + 16 * i + 4 * j;
+          q[j] = act8_codes(a[0], a[1], a[2], a[3], inv);
+          if (relu) {
+            uint32_t pos = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pos |= a[k] > 0.f ? 1u << (8 * k) : 0u;
+            q[j] = act8_lift(q[j], pos);
+          }
+        }
+        w[i] = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+    };
+    codes(r, sr.inv, true);
+    panel_out(panel, w, static_cast<unsigned char *>(P.r) + row0 * P.ldr + n0, P.ldr, rows, 4);
+    codes(u, su.inv, false);
+    panel_out(panel + kPanel, w, static_cast<unsigned char *>(P.u) + row0 * P.ldr + n0, P.ldr, rows, 4);
   }
-  uint16_t *hp = static_cast<uint16_t *>(Q.out) + row * Q.ldo + n0;
+  unsigned char *hp = static_cast<unsigned char *>(Q.out) + (row0 * Q.ldo + n0) * 2;
 #pragma unroll
   for (int c = 0; c < 64; c += 32) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) r[c + i] *= u[c + i];
-    store32(hp + c, r + c, cols64 - c, bf16);
+    pack32(w, r + c, bf16);
+    panel_out(panel + (c >> 5) * kPanel, w, hp + c * 2, Q.ldo * 2, rows, (cols - c) / 8);
   }
 }
 
@@ -286,29 +356,83 @@ __device__ __forceinline__ float column_sums(float v[32], int lane) {
   return v[0];
 }
 
-// 128 columns of dH from n0 on; reads the saved relu(G) and U of this row, writes dG, dU, H.
-__device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row,
-                                           bool live, int n0) {
+// The saved relu(G) and U of a warp's rows: 64 bytes a row of each, requested before the
+// accumulators are waited for.  Values: 32 columns; codes: 64, with the two scales.
+struct SavedPiece {
+  uint4 r[4], u[4];
+  float sr, su;
+};
+template <bool CODES>
+__device__ __forceinline__ void saved_request(const DenseParams &P, const Unit &Q, int64_t row0, int n0, SavedPiece &s) {
+  const int rows = (int)min((int64_t)32, Q.M - row0), lane = threadIdx.x & 31;
+  if (CODES) {
+    const int pieces = n0 < Q.N ? 4 : 0;  // code rows are padded to 64 columns
+    panel_request(s.r, static_cast<const unsigned char *>(P.r) + row0 * P.ldr + n0, P.ldr, rows, pieces);
+    panel_request(s.u, static_cast<const unsigned char *>(P.u) + row0 * P.ldr + n0, P.ldr, rows, pieces);
+    s.sr = s.su = 0.f;
+    if (pieces && lane < rows) {
+      s.sr = __ldg(P.rs + (row0 + lane) * P.lds + (n0 >> 6));
+      s.su = __ldg(P.us + (row0 + lane) * P.lds + (n0 >> 6));
+    }
+  } else {
+    const int pieces = (Q.N - n0) / 8;
+    panel_request(s.r, static_cast<const unsigned char *>(P.r) + (row0 * P.ldr + n0) * 2, P.ldr * 2, rows, pieces);
+    panel_request(s.u, static_cast<const unsigned char *>(P.u) + (row0 * P.ldr + n0) * 2, P.ldr * 2, rows, pieces);
+  }
+}
+
+// 32 columns of dH: dG, dU and H from the row's relu(G) and U (r, u).
+__device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0, float r[32],
+                                         float u[32], uint32_t panel) {
   const bool bf16 = P.bf16;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, rows = (int)min((int64_t)32, Q.M - row0), pieces = (Q.N - n0) / 8;
+  uint32_t raw[32];
+  uint4 w[4];
+  __syncwarp();
+  tm_ld32(taddr, raw);
+  tm_wait_ld();
+  if (rows <= 0 || pieces <= 0) return;  // (the whole warp)
+  const int64_t at = (row0 * Q.ldo + n0) * 2, ld = Q.ldo * 2;
+  float t[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) t[i] = __uint_as_float(raw[i]) * r[i];
+  pack32(w, t, bf16);
+  panel_out(panel, w, static_cast<unsigned char *>(P.du) + at, ld, rows, pieces);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) t[i] = r[i] * u[i];
+  pack32(w, t, bf16);
+  panel_out(panel + kPanel, w, static_cast<unsigned char *>(Q.out) + at, ld, rows, pieces);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) t[i] = r[i] > 0.f ? __uint_as_float(raw[i]) * u[i] : 0.f;  // rows past M: r = 0
+  pack32(w, t, bf16);
+  panel_out(panel, w, static_cast<unsigned char *>(P.dg) + at, ld, rows, pieces);
+  if (P.colpart) {
+    __syncwarp();
+    const float sum = column_sums(t, lane);
+    if (n0 + lane < Q.N) P.colpart[(row0 >> 5) * Q.N + n0 + lane] = sum;
+  }
+}
+
+// 128 columns of dH from n0 on; `s` holds the first saved piece.
+template <bool CODES>
+__device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
+                                           SavedPiece &s, uint32_t panel) {
+  constexpr int STEP = CODES ? 64 : 32;
 #pragma unroll 1
-  for (int c = 0; c < 128; c += 32) {
-    uint32_t raw[32];
-    const int cols = Q.N - (n0 + c);
-    const bool on = live && cols > 0;
+  for (int c = 0; c < 128; c += STEP) {
+    uint4 wr[4], wu[4];
+    panel_in(panel, s.r, wr);
+    panel_in(panel + kPanel, s.u, wu);
+    const float sr = s.sr, su = s.su;
+    if (c + STEP < 128) saved_request<CODES>(P, Q, row0, n0 + c + STEP, s);
     float r[32], u[32];
-    if (on) {
-      if (P.save == SFNN_SAVE_FULL) {
-        load32(static_cast<const uint16_t *>(P.r) + row * P.ldr + n0 + c, r, cols, bf16);
-        load32(static_cast<const uint16_t *>(P.u) + row * P.ldr + n0 + c, u, cols, bf16);
-      } else {
-        const float sr = __ldg(P.rs + row * P.lds + ((n0 + c) >> 6)), su = __ldg(P.us + row * P.lds + ((n0 + c) >> 6));
-        const uint4 *rp = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(P.r) + row * P.ldr + n0 + c);
-        const uint4 *up = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(P.u) + row * P.ldr + n0 + c);
+    if (CODES) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint4 wr = __ldg(rp + i), wu = __ldg(up + i);
-          const uint32_t ar[4] = {wr.x, wr.y, wr.z, wr.w}, au[4] = {wu.x, wu.y, wu.z, wu.w};
+          const uint4 a4 = wr[2 * h + i], b4 = wu[2 * h + i];
+          const uint32_t ar[4] = {a4.x, a4.y, a4.z, a4.w}, au[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -320,33 +444,12 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, 
               u[16 * i + 4 * j + k] = (float)(int8_t)((au[j] >> (8 * k)) & 0xffu) * su;
             }
         }
+        dgated32(P, Q, taddr + c + 32 * h, row0, n0 + c + 32 * h, r, u, panel);
       }
-    }
-    __syncwarp();
-    tm_ld32(taddr + c, raw);
-    tm_wait_ld();
-    float dg[32], du[32];
-    if (on) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float dh = __uint_as_float(raw[i]);
-        du[i] = dh * r[i];
-        dg[i] = r[i] > 0.f ? dh * u[i] : 0.f;
-        r[i] *= u[i];
-      }
-      const int64_t at = row * Q.ldo + n0 + c;
-      store32(static_cast<uint16_t *>(P.dg) + at, dg, cols, bf16);
-      store32(static_cast<uint16_t *>(P.du) + at, du, cols, bf16);
-      store32(static_cast<uint16_t *>(Q.out) + at, r, cols, bf16);
     } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) dg[i] = 0.f;
-    }
-    if (P.colpart) {
-      __syncwarp();
-      const float sum = column_sums(dg, lane);
-      const int64_t block = (row - lane) >> 5;
-      if (block * 32 < Q.M && lane < cols) P.colpart[block * Q.N + n0 + c + lane] = sum;
+      unpack32(wr, r, P.bf16);
+      unpack32(wu, u, P.bf16);
+      dgated32(P, Q, taddr + c, row0, n0 + c, r, u, panel);
     }
   }
 }
@@ -355,6 +458,7 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, 
 template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_dense(const __grid_constant__ DenseParams P) {
+  constexpr bool kDGated = EPI == kEpiDGated || EPI == kEpiDGated8;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
@@ -419,7 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           } else {
             tma_load_2d_pair(sa, ma, k0, m0, bar);
           }
-          if (EPI == kEpiDGated || (EPI == kEpiStore && w.b_mn)) {
+          if (kDGated || (EPI == kEpiStore && w.b_mn)) {
             tma_load_2d_pair(sb, mb, n0, k0, bar);
             tma_load_2d_pair(sb + 8192u, mb, n0 + 64, k0, bar);
           } else {
@@ -445,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Unit w{}, next = unit_at(P, max(id, 0));
       for (int n = 0; ok && id >= 0; ++n) {
         w = next;
-        const int a_mn = EPI == kEpiStore ? w.a_mn : 0, b_mn = EPI == kEpiStore ? w.b_mn : EPI == kEpiDGated;
+        const int a_mn = EPI == kEpiStore ? w.a_mn : 0, b_mn = EPI == kEpiStore ? w.b_mn : kDGated;
         const uint32_t idesc = mma_desc_16(256, 256, P.bf16, a_mn, b_mn);
         // a 16-deep step of an operand: 2 KB of an MN-major tile, 32 bytes of a K-major one
         const uint32_t step_a = a_mn ? 2048u : 32u, step_b = b_mn ? 2048u : 32u;
@@ -482,6 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t panel = stage0 + kStages * kStageBytes + (uint32_t)(warp - 2) * kWarpStage;
     if (EPI == kEpiStore && P.colsum) {  // while the first tile is multiplied: db from its 32-row sums
       for (int c = blockIdx.x * 256 + threadIdx.x - 64; c < P.cols; c += gridDim.x * 256) {
         float sum = 0.f;
@@ -494,21 +599,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int n = 0, id; (id = walk.unit(n)) >= 0; ++n) {
       const Unit w = unit_at(P, id);
       const int buf = n & 1;
+      const int64_t row0 = (int64_t)w.pos.m * kTile + rank * 128 + quad * 32;
+      const int n0 = EPI == kEpiGated ? w.pos.n * 128 + half * 64 : w.pos.n * kTile + half * 128;
+      // what the epilogue reads besides the accumulators, requested before they are there
+      float bias[2] = {0.f, 0.f};
+      SavedPiece saved;
+      if (EPI == kEpiGated && P.bias) {
+        if (n0 + lane < w.N) bias[0] = load16(P.bias, n0 + lane, P.bf16);
+        if (n0 + 32 + lane < w.N) bias[1] = load16(P.bias, n0 + 32 + lane, P.bf16);
+      }
+      if (kDGated) saved_request<EPI == kEpiDGated8>(P, w, row0, n0, saved);
       if (!__all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((n >> 1) & 1)))) {
         if (lane == 0) latch_error(P.err, kErrTimeout);
         break;
       }
       __syncwarp();
       tm_fence_after();
-      const int64_t row = (int64_t)w.pos.m * kTile + rank * 128 + quad * 32 + lane;
-      const bool live = row < w.M;
       const uint32_t acc = tmem + lanes + (uint32_t)buf * 256u;
       if (EPI == kEpiGated)
-        epi_gated(P, w, acc + half * 64, row, live, w.pos.n * 128 + half * 64);
-      else if (EPI == kEpiDGated)
-        epi_dgated(P, w, acc + half * 128, row, live, w.pos.n * kTile + half * 128);
+        epi_gated(P, w, acc + half * 64, row0, n0, bias, panel);
+      else if (kDGated)
+        epi_dgated<EPI == kEpiDGated8>(P, w, acc + half * 128, row0, n0, saved, panel);
       else
-        epi_store(P, w, acc + half * 128, row, live, w.pos.n * kTile + half * 128);
+        epi_store(P, w, acc + half * 128, row0, n0, panel);
       tm_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
@@ -522,7 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) tm_dealloc<2>(tmem, kTmem);
 }
 
-constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;
+constexpr size_t kSmem = (size_t)kStages * kStageBytes + 8 * kWarpStage + 1024;
 
 template <int EPI>
 cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
@@ -546,7 +659,7 @@ cudaError_t launch_dense(DenseParams &P, int epi, int num_sms, cudaStream_t s) {
   }
   P.extra = P.count > 1 ? (P.p[0].nk / P.p[0].split + len / 2) / len : 0;
   if (epi == kEpiGated) return run<kEpiGated>(P, num_sms, s);
-  if (epi == kEpiDGated) return run<kEpiDGated>(P, num_sms, s);
+  if (epi == kEpiDGated) return P.save == SFNN_SAVE_ACT8 ? run<kEpiDGated8>(P, num_sms, s) : run<kEpiDGated>(P, num_sms, s);
   return run<kEpiStore>(P, num_sms, s);
 }
 

@@ -74,7 +74,8 @@ __device__ __forceinline__ uint32_t act8_lift(uint32_t codes, uint32_t positive)
 enum DenseEpi : int {
   kEpiStore = 0,  // C as 16-bit or fp32 values
   kEpiGated = 1,  // B0 = gate rows, B1 = up rows (128 each per tile): H = relu(G + b) * U
-  kEpiDGated = 2  // C = dH: dU = dH * R, dG = dH * U * [R > 0], H = R * U
+  kEpiDGated = 2,  // C = dH: dU = dH * R, dG = dH * U * [R > 0], H = R * U
+  kEpiDGated8 = 3  // the same with R and U held as 8-bit blocks
 };
 
 struct alignas(64) DenseProblem {
