@@ -214,9 +214,10 @@ __device__ __forceinline__ void pack32_relu(uint4 w[4], const float v[32], bool 
 // Each thread owns one row of the tile (its tensor-memory lane) and a half of the tile's
 // columns; a warp owns 32 rows from `row0` on and stores them through its `panel`s.
 
+template <bool bf16>
 __device__ __forceinline__ void epi_store(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
                                           uint32_t panel) {
-  const bool bf16 = P.bf16, parts = Q.split > 1;
+  const bool parts = Q.split > 1;
   const int rows = (int)min((int64_t)32, Q.M - row0);
   // relu: the hidden layer, whose rows are padded to 8 columns
   const int end = Q.relu ? (Q.N + 7) / 8 * 8 : Q.N;
@@ -264,9 +265,9 @@ __device__ __forceinline__ void epi_store(const DenseParams &P, const Unit &Q, u
 // The pair's tile holds 128 neurons: gate columns 0..127, up columns 128..255.  This
 // warp takes 64 of them from n0 on (one act8 block); `bias` holds n0 + lane's and
 // n0 + 32 + lane's.
+template <bool bf16>
 __device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, uint32_t tgate, int64_t row0, int n0,
                                           const float bias[2], uint32_t panel) {
-  const bool bf16 = P.bf16;
   const int lane = threadIdx.x & 31;
   const int rows = (int)min((int64_t)32, Q.M - row0);
   const int cols = (int)min((int64_t)64, Q.ldo - n0);  // writable columns of H (a multiple of 8)
@@ -342,18 +343,24 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, u
   }
 }
 
-// Sums of 32 columns over a warp's 32 rows: lane i gets column i's.
-__device__ __forceinline__ float column_sums(float v[32], int lane) {
+// Sums of a panel's 32 columns of 16-bit values over its 32 rows: a lane adds two columns of
+// every other row; lanes 0..15 get columns 2 lane and 2 lane + 1.
+template <bool bf16>
+__device__ __forceinline__ float2 column_sums(uint32_t panel) {
+  const int lane = threadIdx.x & 31, pair = lane & 15;
+  float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const bool hi = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float give = hi ? v[i] : v[i + o], keep = hi ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-    }
+  for (int i = 0; i < 16; ++i) {
+    const int row = 2 * i + (lane >> 4);
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(panel_at(panel, row, pair >> 2) + (uint32_t)((pair & 3) * 4)));
+    const float2 f = unpack16(w, bf16);
+    s.x += f.x;
+    s.y += f.y;
   }
-  return v[0];
+  s.x += __shfl_down_sync(0xffffffffu, s.x, 16);
+  s.y += __shfl_down_sync(0xffffffffu, s.y, 16);
+  return s;
 }
 
 // The saved relu(G) and U of a warp's rows: 64 bytes a row of each, requested before the
@@ -382,9 +389,9 @@ __device__ __forceinline__ void saved_request(const DenseParams &P, const Unit &
 }
 
 // 32 columns of dH: dG, dU and H from the row's relu(G) and U (r, u).
+template <bool bf16>
 __device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0, float r[32],
                                          float u[32], uint32_t panel) {
-  const bool bf16 = P.bf16;
   const int lane = threadIdx.x & 31, rows = (int)min((int64_t)32, Q.M - row0), pieces = (Q.N - n0) / 8;
   uint32_t raw[32];
   uint4 w[4];
@@ -406,15 +413,15 @@ __device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, ui
   for (int i = 0; i < 32; ++i) t[i] = r[i] > 0.f ? __uint_as_float(raw[i]) * u[i] : 0.f;  // rows past M: r = 0
   pack32(w, t, bf16);
   panel_out(panel, w, static_cast<unsigned char *>(P.dg) + at, ld, rows, pieces);
-  if (P.colpart) {
-    __syncwarp();
-    const float sum = column_sums(t, lane);
-    if (n0 + lane < Q.N) P.colpart[(row0 >> 5) * Q.N + n0 + lane] = sum;
+  if (P.colpart) {  // of dG as it was rounded, which the panel still holds
+    const float2 sum = column_sums<bf16>(panel);
+    if (lane < 16 && n0 + 2 * lane < Q.N)
+      *reinterpret_cast<float2 *>(P.colpart + (row0 >> 5) * Q.N + n0 + 2 * lane) = sum;
   }
 }
 
 // 128 columns of dH from n0 on; `s` holds the first saved piece.
-template <bool CODES>
+template <bool CODES, bool bf16>
 __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
                                            SavedPiece &s, uint32_t panel) {
   constexpr int STEP = CODES ? 64 : 32;
@@ -424,9 +431,12 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, 
     panel_in(panel, s.r, wr);
     panel_in(panel + kPanel, s.u, wu);
     const float sr = s.sr, su = s.su;
-    if (c + STEP < 128) saved_request<CODES>(P, Q, row0, n0 + c + STEP, s);
+    if (!CODES && c + STEP < 128) saved_request<CODES>(P, Q, row0, n0 + c + STEP, s);
     float r[32], u[32];
     if (CODES) {
+// a code as a float: its byte under the exponent of 2^23, less 2^23 (and 128 for a signed one).
+      // A lifted code of a block whose scale is zero keeps its neuron on.
+      const float rs = sr == 0.f ? __uint_as_float(1u) : sr, r0 = -8388608.f * rs;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -434,28 +444,28 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, 
           const uint4 a4 = wr[2 * h + i], b4 = wu[2 * h + i];
           const uint32_t ar[4] = {a4.x, a4.y, a4.z, a4.w}, au[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t biased = au[j] ^ 0x80808080u;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t code = (ar[j] >> (8 * k)) & 0xffu;
-              // a code above zero keeps its neuron on even where its scale is zero
-              const float v = (float)code * sr;
-              r[16 * i + 4 * j + k] = code && v == 0.f ? __uint_as_float(1u) : v;
-              u[16 * i + 4 * j + k] = (float)(int8_t)((au[j] >> (8 * k)) & 0xffu) * su;
+              r[16 * i + 4 * j + k] = fmaf(__uint_as_float(__byte_perm(ar[j], 0x4b000000u, 0x7440 + k)), rs, r0);
+              u[16 * i + 4 * j + k] = (__uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7440 + k)) - 8388736.f) * su;
             }
+          }
         }
-        dgated32(P, Q, taddr + c + 32 * h, row0, n0 + c + 32 * h, r, u, panel);
+        if (h == 1 && c + STEP < 128) saved_request<CODES>(P, Q, row0, n0 + c + STEP, s);
+        dgated32<bf16>(P, Q, taddr + c + 32 * h, row0, n0 + c + 32 * h, r, u, panel);
       }
     } else {
-      unpack32(wr, r, P.bf16);
-      unpack32(wu, u, P.bf16);
-      dgated32(P, Q, taddr + c, row0, n0 + c, r, u, panel);
+      unpack32(wr, r, bf16);
+      unpack32(wu, u, bf16);
+      dgated32<bf16>(P, Q, taddr + c, row0, n0 + c, r, u, panel);
     }
   }
 }
 
 // ---------------------------------------------------------------- the kernel
-template <int EPI>
+template <int EPI, bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_dense(const __grid_constant__ DenseParams P) {
   constexpr bool kDGated = EPI == kEpiDGated || EPI == kEpiDGated8;
@@ -550,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int n = 0; ok && id >= 0; ++n) {
         w = next;
         const int a_mn = EPI == kEpiStore ? w.a_mn : 0, b_mn = EPI == kEpiStore ? w.b_mn : kDGated;
-        const uint32_t idesc = mma_desc_16(256, 256, P.bf16, a_mn, b_mn);
+        const uint32_t idesc = mma_desc_16(256, 256, BF16, a_mn, b_mn);
         // a 16-deep step of an operand: 2 KB of an MN-major tile, 32 bytes of a K-major one
         const uint32_t step_a = a_mn ? 2048u : 32u, step_b = b_mn ? 2048u : 32u;
         const uint32_t lbo_a = a_mn ? 8192u : 16u, lbo_b = b_mn ? 8192u : 16u;
@@ -592,7 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float sum = 0.f;
 #pragma unroll 8
         for (int b = 0; b < P.col_blocks; ++b) sum += __ldg(P.colpart + (int64_t)b * P.cols + c);
-        P.colsum[c] = (uint16_t)pack16(sum, 0.f, P.bf16);
+        P.colsum[c] = (uint16_t)pack16(sum, 0.f, BF16);
       }
     }
     __syncwarp();
@@ -605,8 +615,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float bias[2] = {0.f, 0.f};
       SavedPiece saved;
       if (EPI == kEpiGated && P.bias) {
-        if (n0 + lane < w.N) bias[0] = load16(P.bias, n0 + lane, P.bf16);
-        if (n0 + 32 + lane < w.N) bias[1] = load16(P.bias, n0 + 32 + lane, P.bf16);
+        if (n0 + lane < w.N) bias[0] = load16(P.bias, n0 + lane, BF16);
+        if (n0 + 32 + lane < w.N) bias[1] = load16(P.bias, n0 + 32 + lane, BF16);
       }
       if (kDGated) saved_request<EPI == kEpiDGated8>(P, w, row0, n0, saved);
       if (!__all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((n >> 1) & 1)))) {
@@ -617,11 +627,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tm_fence_after();
       const uint32_t acc = tmem + lanes + (uint32_t)buf * 256u;
       if (EPI == kEpiGated)
-        epi_gated(P, w, acc + half * 64, row0, n0, bias, panel);
+        epi_gated<BF16>(P, w, acc + half * 64, row0, n0, bias, panel);
       else if (kDGated)
-        epi_dgated<EPI == kEpiDGated8>(P, w, acc + half * 128, row0, n0, saved, panel);
+        epi_dgated<EPI == kEpiDGated8, BF16>(P, w, acc + half * 128, row0, n0, saved, panel);
       else
-        epi_store(P, w, acc + half * 128, row0, n0, panel);
+        epi_store<BF16>(P, w, acc + half * 128, row0, n0, panel);
       tm_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
@@ -637,13 +647,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 constexpr size_t kSmem = (size_t)kStages * kStageBytes + 8 * kWarpStage + 1024;
 
-template <int EPI>
-cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
+template <int EPI, bool BF16>
+cudaError_t run_as(const DenseParams &P, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose kernel attribute is set
-  const cudaError_t attr = allow_smem(k_dense<EPI>, kSmem, ready);
+  const cudaError_t attr = allow_smem(k_dense<EPI, BF16>, kSmem, ready);
   if (attr != cudaSuccess) return attr;
   const int grid = 2 * std::min(num_sms / 2, P.first + P.rest);
-  return launch_pdl(k_dense<EPI>, dim3(grid), dim3(kThreads), kSmem, s, P);
+  return launch_pdl(k_dense<EPI, BF16>, dim3(grid), dim3(kThreads), kSmem, s, P);
+}
+template <int EPI>
+cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
+  return P.bf16 ? run_as<EPI, true>(P, num_sms, s) : run_as<EPI, false>(P, num_sms, s);
 }
 
 }  // namespace
