@@ -27,7 +27,10 @@ namespace sfnn {
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kStages = 6;
+// K chunks in flight; the backward epilogue's saved values take one's place (below)
+template <int EPI>
+constexpr int kStagesOf = EPI == kEpiDGated || EPI == kEpiDGated8 ? 5 : 6;
+constexpr int kMaxStages = 6;
 constexpr uint32_t kStageBytes = 32768;  // per CTA: 128 x 64 of A, 128 x 64 of B
 constexpr int kTile = 256;
 constexpr int kTmem = 512;
@@ -121,7 +124,8 @@ __device__ __forceinline__ Unit unit_at(const DenseParams &P, int u) {
 // rows at a time: written by row, read (and stored) with 4 lanes to a row.  The 16-byte
 // pieces of row r are rotated by (r / 2) % 4, so neither side has bank conflicts.
 constexpr uint32_t kPanel = 2048;      // 32 rows x 64 bytes
-constexpr uint32_t kWarpStage = 2 * kPanel;
+template <int EPI>  // a warp's panels: two, and two more for the saved values that come in
+constexpr uint32_t kWarpPanels = EPI == kEpiDGated || EPI == kEpiDGated8 ? 4 * kPanel : 2 * kPanel;
 __device__ __forceinline__ uint32_t panel_at(uint32_t panel, int row, int piece) {
   return panel + (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
 }
@@ -149,25 +153,27 @@ __device__ __forceinline__ void panel_out(uint32_t panel, const uint4 w[4], unsi
     if (row < rows && piece < pieces) *reinterpret_cast<uint4 *>(base + row * ld + piece * 16) = v;
   }
 }
-// The way in: request 64 bytes of each of the warp's rows (zeros where none exist) ...
-__device__ __forceinline__ void panel_request(uint4 v[4], const unsigned char *base, int64_t ld, int rows, int pieces) {
+// The way in: request 64 bytes of each of the warp's rows (zeros where none exist) into a
+// panel, without waiting (cp.async) ...
+__device__ __forceinline__ void panel_request(uint32_t panel, const unsigned char *base, int64_t ld, int rows, int pieces) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = i * 8 + (lane >> 2), piece = lane & 3;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows && piece < pieces) v[i] = __ldg(reinterpret_cast<const uint4 *>(base + row * ld + piece * 16));
+    const bool there = row < rows && piece < pieces;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(panel_at(panel, row, piece)),
+                 "l"(there ? base + row * ld + piece * 16 : base), "r"(there ? 16 : 0)
+                 : "memory");
   }
 }
-// ... and hand each lane its row's.
-__device__ __forceinline__ void panel_in(uint32_t panel, const uint4 v[4], uint4 w[4]) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
+// ... and, once it is there, N 16-byte pieces of this lane's row from piece j on.
+template <int N>
+__device__ __forceinline__ void panel_row(uint32_t panel, int j, uint32_t w[4 * N]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sts16(panel_at(panel, i * 8 + (lane >> 2), lane & 3), v[i]);
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = lds16(panel_at(panel, lane, j));
+  for (int i = 0; i < N; ++i) {
+    const uint4 v = lds16(panel_at(panel, threadIdx.x & 31, j + i));
+    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+  }
 }
 
 // 32 values as 16-bit elements.
@@ -178,18 +184,6 @@ __device__ __forceinline__ void pack32(uint4 w[4], const float v[32], bool bf16)
     w[i].y = pack16(v[8 * i + 2], v[8 * i + 3], bf16);
     w[i].z = pack16(v[8 * i + 4], v[8 * i + 5], bf16);
     w[i].w = pack16(v[8 * i + 6], v[8 * i + 7], bf16);
-  }
-}
-__device__ __forceinline__ void unpack32(const uint4 w[4], float v[32], bool bf16) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack16(a[j], bf16);
-      v[8 * i + 2 * j] = f.x;
-      v[8 * i + 2 * j + 1] = f.y;
-    }
   }
 }
 // relu(G) as 16-bit elements: a positive value that rounds to zero keeps the type's
@@ -363,55 +357,104 @@ __device__ __forceinline__ float2 column_sums(uint32_t panel) {
   return s;
 }
 
-// The saved relu(G) and U of a warp's rows: 64 bytes a row of each, requested before the
-// accumulators are waited for.  Values: 32 columns; codes: 64, with the two scales.
-struct SavedPiece {
-  uint4 r[4], u[4];
-  float sr, su;
-};
+// Request the saved relu(G) and U of a warp's rows into the panels `in` and `in` + 1: 64 bytes
+// a row of each, 32 values or 64 codes (whose two scales a lane keeps).
 template <bool CODES>
-__device__ __forceinline__ void saved_request(const DenseParams &P, const Unit &Q, int64_t row0, int n0, SavedPiece &s) {
+__device__ __forceinline__ void saved_request(const DenseParams &P, const Unit &Q, int64_t row0, int n0, uint32_t in,
+                                              float2 &scales) {
   const int rows = (int)min((int64_t)32, Q.M - row0), lane = threadIdx.x & 31;
+  constexpr int E = CODES ? 1 : 2;
+  const int pieces = CODES ? (n0 < Q.N ? 4 : 0) : (Q.N - n0) / 8;  // code rows are padded to 64 columns
+  const int64_t at = pieces > 0 && rows > 0 ? (row0 * P.ldr + n0) * E : 0;
+  panel_request(in, static_cast<const unsigned char *>(P.r) + at, P.ldr * E, rows, pieces);
+  panel_request(in + kPanel, static_cast<const unsigned char *>(P.u) + at, P.ldr * E, rows, pieces);
+  cp_async_commit();
   if (CODES) {
-    const int pieces = n0 < Q.N ? 4 : 0;  // code rows are padded to 64 columns
-    panel_request(s.r, static_cast<const unsigned char *>(P.r) + row0 * P.ldr + n0, P.ldr, rows, pieces);
-    panel_request(s.u, static_cast<const unsigned char *>(P.u) + row0 * P.ldr + n0, P.ldr, rows, pieces);
-    s.sr = s.su = 0.f;
-    if (pieces && lane < rows) {
-      s.sr = __ldg(P.rs + (row0 + lane) * P.lds + (n0 >> 6));
-      s.su = __ldg(P.us + (row0 + lane) * P.lds + (n0 >> 6));
-    }
-  } else {
-    const int pieces = (Q.N - n0) / 8;
-    panel_request(s.r, static_cast<const unsigned char *>(P.r) + (row0 * P.ldr + n0) * 2, P.ldr * 2, rows, pieces);
-    panel_request(s.u, static_cast<const unsigned char *>(P.u) + (row0 * P.ldr + n0) * 2, P.ldr * 2, rows, pieces);
+    scales = make_float2(0.f, 0.f);
+    if (pieces && lane < rows)
+      scales = make_float2(__ldg(P.rs + (row0 + lane) * P.lds + (n0 >> 6)), __ldg(P.us + (row0 + lane) * P.lds + (n0 >> 6)));
   }
 }
 
-// 32 columns of dH: dG, dU and H from the row's relu(G) and U (r, u).
-template <bool bf16>
-__device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0, float r[32],
-                                         float u[32], uint32_t panel) {
+// relu(G) and U of 32 columns of a row, as they were saved: 16 words of two values, or 8 words
+// of four codes and the scales.  They are widened where they are used and not before: held
+// as floats they cost the kernel its registers, and a spill here misses L1 (shared memory
+// leaves it next to nothing; measured: 13 to 20 us a tile instead of 3 to 5).
+template <bool CODES, bool bf16>
+struct SavedWords {
+  uint32_t r[CODES ? 8 : 16], u[CODES ? 8 : 16];
+  float rs, r0, us;  // a code as a float: its byte under the exponent of 2^23, less 2^23 (and 128 if signed)
+  __device__ __forceinline__ void set_scales(float sr, float su) {
+    rs = sr == 0.f ? __uint_as_float(1u) : sr;  // a lifted code of a block whose scale is zero keeps its neuron on
+    r0 = -8388608.f * rs;
+    us = su;
+  }
+  // columns 2 i and 2 i + 1
+  __device__ __forceinline__ void get(int i, float2 &rv, float2 &uv) const {
+    if (CODES) {
+      const uint32_t a = r[i >> 1], b = u[i >> 1] ^ 0x80808080u, k = 0x7440u + 2u * (i & 1);
+      rv.x = fmaf(__uint_as_float(__byte_perm(a, 0x4b000000u, k)), rs, r0);
+      rv.y = fmaf(__uint_as_float(__byte_perm(a, 0x4b000000u, k + 1)), rs, r0);
+      uv.x = (__uint_as_float(__byte_perm(b, 0x4b000000u, k)) - 8388736.f) * us;
+      uv.y = (__uint_as_float(__byte_perm(b, 0x4b000000u, k + 1)) - 8388736.f) * us;
+    } else {
+      rv = unpack16(r[i], bf16);
+      uv = unpack16(u[i], bf16);
+    }
+  }
+  __device__ __forceinline__ void forget() {  // (the widened values of an earlier use)
+#pragma unroll
+    for (int i = 0; i < (CODES ? 8 : 16); ++i) asm volatile("" : "+r"(r[i]), "+r"(u[i]));
+  }
+};
+__device__ __forceinline__ void words_to(uint4 w[4], const uint32_t a[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+}
+
+// 32 columns of dH: H, dU and dG.
+template <bool CODES, bool bf16>
+__device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
+                                         SavedWords<CODES, bf16> &v, uint32_t panel) {
   const int lane = threadIdx.x & 31, rows = (int)min((int64_t)32, Q.M - row0), pieces = (Q.N - n0) / 8;
-  uint32_t raw[32];
-  uint4 w[4];
-  __syncwarp();
-  tm_ld32(taddr, raw);
-  tm_wait_ld();
   if (rows <= 0 || pieces <= 0) return;  // (the whole warp)
   const int64_t at = (row0 * Q.ldo + n0) * 2, ld = Q.ldo * 2;
-  float t[32];
+  uint4 w[4];
+  {
+    uint32_t h[16];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) t[i] = __uint_as_float(raw[i]) * r[i];
-  pack32(w, t, bf16);
-  panel_out(panel, w, static_cast<unsigned char *>(P.du) + at, ld, rows, pieces);
+    for (int i = 0; i < 16; ++i) {
+      float2 r, u;
+      v.get(i, r, u);
+      h[i] = pack16(r.x * u.x, r.y * u.y, bf16);
+    }
+    words_to(w, h);
+  }
+  panel_out(panel, w, static_cast<unsigned char *>(Q.out) + at, ld, rows, pieces);
+  v.forget();
+  uint32_t dg[16];
+  {
+    uint32_t du[16];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) t[i] = r[i] * u[i];
-  pack32(w, t, bf16);
-  panel_out(panel + kPanel, w, static_cast<unsigned char *>(Q.out) + at, ld, rows, pieces);
+    for (int c = 0; c < 2; ++c) {
+      uint32_t raw[16];
+      __syncwarp();
+      tm_ld16(taddr + 16 * c, raw);
+      tm_wait_ld();
 #pragma unroll
-  for (int i = 0; i < 32; ++i) t[i] = r[i] > 0.f ? __uint_as_float(raw[i]) * u[i] : 0.f;  // rows past M: r = 0
-  pack32(w, t, bf16);
+      for (int j = 0; j < 8; ++j) {
+        const int i = 8 * c + j;
+        float2 r, u;
+        v.get(i, r, u);
+        const float x = __uint_as_float(raw[2 * j]), y = __uint_as_float(raw[2 * j + 1]);
+        du[i] = pack16(x * r.x, y * r.y, bf16);
+        dg[i] = pack16(r.x > 0.f ? x * u.x : 0.f, r.y > 0.f ? y * u.y : 0.f, bf16);  // rows past M: r = 0
+      }
+    }
+    words_to(w, du);
+  }
+  panel_out(panel + kPanel, w, static_cast<unsigned char *>(P.du) + at, ld, rows, pieces);
+  words_to(w, dg);
   panel_out(panel, w, static_cast<unsigned char *>(P.dg) + at, ld, rows, pieces);
   if (P.colpart) {  // of dG as it was rounded, which the panel still holds
     const float2 sum = column_sums<bf16>(panel);
@@ -420,48 +463,30 @@ __device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, ui
   }
 }
 
-// 128 columns of dH from n0 on; `s` holds the first saved piece.
+// 128 columns of dH from n0 on; the first saved piece has been requested.
 template <bool CODES, bool bf16>
 __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
-                                           SavedPiece &s, uint32_t panel) {
-  constexpr int STEP = CODES ? 64 : 32;
+                                           float2 scales, uint32_t panel) {
+  const uint32_t in = panel + 2 * kPanel;
 #pragma unroll 1
-  for (int c = 0; c < 128; c += STEP) {
-    uint4 wr[4], wu[4];
-    panel_in(panel, s.r, wr);
-    panel_in(panel + kPanel, s.u, wu);
-    const float sr = s.sr, su = s.su;
-    if (!CODES && c + STEP < 128) saved_request<CODES>(P, Q, row0, n0 + c + STEP, s);
-    float r[32], u[32];
-    if (CODES) {
-// a code as a float: its byte under the exponent of 2^23, less 2^23 (and 128 for a signed one).
-      // A lifted code of a block whose scale is zero keeps its neuron on.
-      const float rs = sr == 0.f ? __uint_as_float(1u) : sr, r0 = -8388608.f * rs;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 a4 = wr[2 * h + i], b4 = wu[2 * h + i];
-          const uint32_t ar[4] = {a4.x, a4.y, a4.z, a4.w}, au[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t biased = au[j] ^ 0x80808080u;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              r[16 * i + 4 * j + k] = fmaf(__uint_as_float(__byte_perm(ar[j], 0x4b000000u, 0x7440 + k)), rs, r0);
-              u[16 * i + 4 * j + k] = (__uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7440 + k)) - 8388736.f) * su;
-            }
-          }
-        }
-        if (h == 1 && c + STEP < 128) saved_request<CODES>(P, Q, row0, n0 + c + STEP, s);
-        dgated32<bf16>(P, Q, taddr + c + 32 * h, row0, n0 + c + 32 * h, r, u, panel);
-      }
-    } else {
-      unpack32(wr, r, bf16);
-      unpack32(wu, u, bf16);
-      dgated32<bf16>(P, Q, taddr + c, row0, n0 + c, r, u, panel);
+  for (int c = 0; c < 128; c += 32) {
+    const bool first = !CODES || (c & 32) == 0, last = !CODES || (c & 32);  // of a saved piece
+    SavedWords<CODES, bf16> v;
+    v.set_scales(scales.x, scales.y);
+    if (first) {
+      cp_async_wait<0>();
+      __syncwarp();
     }
+    const int piece = CODES && (c & 32) ? 2 : 0;
+    panel_row<CODES ? 2 : 4>(in, piece, v.r);
+    panel_row<CODES ? 2 : 4>(in + kPanel, piece, v.u);
+    if (last && c + 32 < 128) {
+      __syncwarp();  // every lane has its row
+      saved_request<CODES>(P, Q, row0, n0 + c + 32, in, scales);
+    }
+    dgated32(P, Q, taddr + c, row0, n0 + c, v, panel);
   }
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -469,8 +494,9 @@ template <int EPI, bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_dense(const __grid_constant__ DenseParams P) {
   constexpr bool kDGated = EPI == kEpiDGated || EPI == kEpiDGated8;
+  constexpr int kStages = kStagesOf<EPI>;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
   const uint32_t stage0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -596,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t panel = stage0 + kStages * kStageBytes + (uint32_t)(warp - 2) * kWarpStage;
+    const uint32_t panel = stage0 + kStages * kStageBytes + (uint32_t)(warp - 2) * kWarpPanels<EPI>;
     if (EPI == kEpiStore && P.colsum) {  // while the first tile is multiplied: db from its 32-row sums
       for (int c = blockIdx.x * 256 + threadIdx.x - 64; c < P.cols; c += gridDim.x * 256) {
         float sum = 0.f;
@@ -613,12 +639,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n0 = EPI == kEpiGated ? w.pos.n * 128 + half * 64 : w.pos.n * kTile + half * 128;
       // what the epilogue reads besides the accumulators, requested before they are there
       float bias[2] = {0.f, 0.f};
-      SavedPiece saved;
+      float2 scales;
       if (EPI == kEpiGated && P.bias) {
         if (n0 + lane < w.N) bias[0] = load16(P.bias, n0 + lane, BF16);
         if (n0 + 32 + lane < w.N) bias[1] = load16(P.bias, n0 + 32 + lane, BF16);
       }
-      if (kDGated) saved_request<EPI == kEpiDGated8>(P, w, row0, n0, saved);
+      if (kDGated) saved_request<EPI == kEpiDGated8>(P, w, row0, n0, panel + 2 * kPanel, scales);
       if (!__all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((n >> 1) & 1)))) {
         if (lane == 0) latch_error(P.err, kErrTimeout);
         break;
@@ -629,13 +655,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (EPI == kEpiGated)
         epi_gated<BF16>(P, w, acc + half * 64, row0, n0, bias, panel);
       else if (kDGated)
-        epi_dgated<EPI == kEpiDGated8, BF16>(P, w, acc + half * 128, row0, n0, saved, panel);
+        epi_dgated<EPI == kEpiDGated8, BF16>(P, w, acc + half * 128, row0, n0, scales, panel);
       else
         epi_store<BF16>(P, w, acc + half * 128, row0, n0, panel);
       tm_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
     }
+    if (kDGated) cp_async_wait<0>();
   }
   __syncwarp();
   tm_fence_before();
@@ -645,15 +672,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) tm_dealloc<2>(tmem, kTmem);
 }
 
-constexpr size_t kSmem = (size_t)kStages * kStageBytes + 8 * kWarpStage + 1024;
+template <int EPI>
+constexpr size_t kSmem = (size_t)kStagesOf<EPI> * kStageBytes + 8 * kWarpPanels<EPI> + 1024;
 
 template <int EPI, bool BF16>
 cudaError_t run_as(const DenseParams &P, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose kernel attribute is set
-  const cudaError_t attr = allow_smem(k_dense<EPI, BF16>, kSmem, ready);
+  const cudaError_t attr = allow_smem(k_dense<EPI, BF16>, kSmem<EPI>, ready);
   if (attr != cudaSuccess) return attr;
   const int grid = 2 * std::min(num_sms / 2, P.first + P.rest);
-  return launch_pdl(k_dense<EPI, BF16>, dim3(grid), dim3(kThreads), kSmem, s, P);
+  return launch_pdl(k_dense<EPI, BF16>, dim3(grid), dim3(kThreads), kSmem<EPI>, s, P);
 }
 template <int EPI>
 cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
