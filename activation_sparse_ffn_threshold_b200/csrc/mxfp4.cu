@@ -415,17 +415,24 @@ __global__ void __launch_bounds__(kRowThreads)
   pdl_wait();
   pdl_launch_dependents();
 
+  // a lane's block of iteration `it` is it * 32 + lane: its codes lie 512 bytes and its scale
+  // byte 8 tiles (4096 bytes) from those of the iteration before
+  const int iters = (nb + 31) / 32;
+  const uint4 *codes_at = codes + lane;
+  const uint8_t *scales_at = scales + (lane >> 2) * 512 + (lane & 3);
   uint4 w[kRowLoads];
   uint32_t sb[kRowLoads];
-  auto request = [&](int row, int b0) {
+  auto request = [&](int row, int it) {
+    const uint4 *c = codes_at + (int64_t)row * nb + it * 32;
+    const uint8_t *e = scales_at + ((int64_t)(row >> 7) * kt + it * 8) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+    const int left = row < r1 ? nb - it * 32 - lane : 0;
 #pragma unroll
     for (int i = 0; i < kRowLoads; ++i) {
-      const int b = b0 + i * 32 + lane;
       w[i] = make_uint4(0, 0, 0, 0);
       sb[i] = 0;
-      if (row < r1 && b < nb) {
-        w[i] = ld_stream(codes + (int64_t)row * nb + b);
-        sb[i] = __ldg(scales + mx_scale_at(row, b, kt));
+      if (i * 32 < left) {
+        w[i] = ld_stream(c + i * 32);
+        sb[i] = __ldg(e + i * 4096);
       }
     }
   };
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(kRowThreads)
     const uint32_t lo = __vsub4(mx_magnitudes(sel) ^ s0, s0), hi = __vsub4(mx_magnitudes(sel >> 16) ^ s1, s1);
     const int b = c >> 5, part = (c >> 3) & 3;  // 8 values: half a plane's 16 bytes
     reinterpret_cast<uint2 *>(xq + ((size_t)t * 2 + (part >> 1)) * nb + b)[part & 1] = make_uint2(lo, hi);
-    if (part == 0) xs[t * nb + b] = mx_scale_value(e);
+    if (part == 0) xs[t * nb + b] = 0.25f * mx_scale_value(e);  // the products are of doubled values
   }
   __syncthreads();
 
@@ -473,7 +480,7 @@ __global__ void __launch_bounds__(kRowThreads)
     float acc[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[t] = 0.f;
-    for (int b0 = 0; b0 < nb; b0 += 32 * kRowLoads) {
+    for (int it = 0; it < iters; it += kRowLoads) {
       uint4 cw[kRowLoads];
       uint32_t cs[kRowLoads];
 #pragma unroll
@@ -481,11 +488,12 @@ __global__ void __launch_bounds__(kRowThreads)
         cw[i] = w[i];
         cs[i] = sb[i];
       }
-      const bool more = b0 + 32 * kRowLoads < nb;
-      request(more ? row : row + kRowThreads / 32, more ? b0 + 32 * kRowLoads : 0);
+      const bool more = it + kRowLoads < iters;
+      request(more ? row : row + kRowThreads / 32, more ? it + kRowLoads : 0);
 #pragma unroll
       for (int i = 0; i < kRowLoads; ++i) {
-        const int b = b0 + i * 32 + lane;
+        if (it + i >= iters) break;  // (the whole warp)
+        const int b = (it + i) * 32 + lane;
         if (b >= nb) continue;
         const uint32_t word[4] = {cw[i].x, cw[i].y, cw[i].z, cw[i].w};
         uint32_t val[8], sgn[8];
@@ -500,7 +508,7 @@ __global__ void __launch_bounds__(kRowThreads)
         const float ws = mx_scale_value(cs[i]);
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const uint4 p0 = xq[(size_t)(t * 2) * nb + b], p1 = xq[(size_t)(t * 2 + 1) * nb + b];
+          const uint4 p0 = xq[t * 2 * nb + b], p1 = xq[t * 2 * nb + nb + b];
           const uint32_t xv[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
           int dot = 0, over = 0;
 #pragma unroll
@@ -508,7 +516,7 @@ __global__ void __launch_bounds__(kRowThreads)
             dot = __dp4a((int)xv[j], (int)val[j], dot);
             over = __dp4a((int)xv[j], (int)sgn[j], over);
           }
-          acc[t] = fmaf((float)(dot - over) * (0.25f * xs[t * nb + b]), ws, acc[t]);
+          acc[t] = fmaf((float)(dot - over) * xs[t * nb + b], ws, acc[t]);
         }
       }
     }
@@ -662,39 +670,49 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   const bool worker = warp >= 2;
   // this thread's weight row for tokens [t0, t1): out[t][col], with the other CTAs' parts
-  auto finish = [&](int tile, int t0, int t1, const float *sums) {
+  // (four tokens of a row side by side, then the next row: 16-byte accesses without conflicts)
+  auto finish = [&](int tile, int t0, int t1, const unsigned char *sums) {
     const int col = tile * 128 + row;
-    for (int c = t0; c < t1; c += 32) {
-      uint32_t g[32];
-      float v[32];
+    for (int c = t0; c < t1; c += 16) {
+      uint32_t g[16];
+      float v[16];
       __syncwarp();
-      tm_ld32(lanes + c, g);
+      tm_ld16(lanes + c, g);
       tm_wait_ld();
       if (col >= P.N) continue;
-      if (sums) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        for (int p = 0; p < split; ++p) {  // rank order, this CTA's own in its place
-          const float *a = sums + ((size_t)(p < part ? p : p - 1) * P.share + (c - t0)) * 128 + row;
+      for (int i = 0; i < 16; ++i) v[i] = sums && part > 0 ? 0.f : __uint_as_float(g[i]);
+      if (sums)
+        for (int p = part > 0 ? 0 : 1; p < split; ++p) {  // rank order, this CTA's own in its place
+          if (p == part) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < t1) v[i] += p == part ? __uint_as_float(g[i]) : a[i * 128];
+            for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(g[i]);
+          } else {
+            const unsigned char *a = sums + ((size_t)(p < part ? p : p - 1) * P.share + (c - t0)) * 512 + row * 16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (c + 4 * i < t1) {
+                const float4 q = *reinterpret_cast<const float4 *>(a + i * 2048);
+                v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
+              }
+          }
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(g[i]);
-      }
       if (P.out_dtype == SFNN_F32) {
         float *o = static_cast<float *>(P.out) + c * P.ldo + col;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < t1) o[i * P.ldo] = v[i];
+        for (int i = 0; i < 16; ++i, o += P.ldo)
+          if (c + i < t1) *o = v[i];
       } else {
         const bool bf16 = P.out_dtype == SFNN_BF16;
         uint16_t *o = static_cast<uint16_t *>(P.out) + c * P.ldo + col;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < t1) o[i * P.ldo] = (uint16_t)pack16(v[i], 0.f, bf16);
+        for (int i = 0; i < 16; i += 2) {
+          const uint32_t w = pack16(v[i], v[i + 1], bf16);
+          if (c + i < t1) *o = (uint16_t)w;
+          o += P.ldo;
+          if (c + i + 1 < t1) *o = (uint16_t)(w >> 16);
+          o += P.ldo;
+        }
       }
     }
   };
@@ -723,36 +741,37 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
     if (!P.apart) cluster_sync_all();  // no load or MMA touches a stage any more
     tm_fence_after();
     if (worker) {
-      for (int q = 0; q < split; ++q) {
-        if (q == part) continue;
+      for (int k = 1; k < split; ++k) {
+        const int q = (part + k) % split;  // each CTA begins with another
         const int t0 = min(P.T, q * P.share), t1 = min(P.T, t0 + P.share);
         const uint32_t dst0 = cluster_addr(smem_raw, (uint32_t)q) + sums +
-                              (uint32_t)((part < q ? part : part - 1) * P.share * 128 + row) * 4u;
-        for (int c = t0; c < t1; c += 32) {
-          uint32_t g[32];
+                              (uint32_t)((part < q ? part : part - 1) * P.share * 512 + row * 16);
+        for (int c = t0; c < t1; c += 16) {
+          uint32_t g[16];
           __syncwarp();
-          tm_ld32(lanes + c, g);
+          tm_ld16(lanes + c, g);
           tm_wait_ld();
           const uint32_t dst = dst0 + (uint32_t)(c - t0) * 512u;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < t1)
-              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + (uint32_t)i * 512u), "r"(g[i]) : "memory");
+          for (int i = 0; i < 4; ++i)
+            if (c + 4 * i < t1)
+              asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (uint32_t)i * 2048u), "r"(g[4 * i]),
+                           "r"(g[4 * i + 1]), "r"(g[4 * i + 2]), "r"(g[4 * i + 3])
+                           : "memory");
         }
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");
-        __syncwarp();
+        __syncwarp();  // the arrival releases the whole warp's stores
         if (lane == 0) bar_arrive_cluster(cluster_addr(&parts_in, (uint32_t)q));
       }
+      // (every CTA waits for all that is written to it, so none leaves too early)
       if (!__all_sync(0xffffffffu, bar_wait(&parts_in, 0))) {
         if (lane == 0) latch_error(P.err, kErrTimeout);
       } else if (good && unit < P.tiles) {
         __syncwarp();
         const int t0 = min(P.T, part * P.share);
-        finish(unit, t0, min(P.T, t0 + P.share), reinterpret_cast<const float *>(smem_raw + sums));
+        finish(unit, t0, min(P.T, t0 + P.share), smem_raw + sums);
       }
     }
     __syncwarp();
-    cluster_sync_all();  // no CTA leaves while another may still write to it
   }
   tm_fence_before();
   __syncthreads();
@@ -778,7 +797,7 @@ cudaError_t launch_few(FewParams &P, int num_sms, cudaStream_t s) {
   P.split = 1;
   // more CTAs to a tile while they fit two to an SM and each keeps two steps
   while (P.split < 4 && P.tiles * P.split * 2 <= 2 * num_sms && P.nk >= 4 * P.split) P.split *= 2;
-  P.share = (P.T + P.split - 1) / P.split;
+  P.share = ((P.T + P.split - 1) / P.split + 3) / 4 * 4;
   const int stage = 16384 + 1024 + P.t8 * 128 + 1024;
   const int parts = P.split > 1 ? (P.split - 1) * P.share * 512 : 0;
   P.apart = parts <= 16 * 1024;
