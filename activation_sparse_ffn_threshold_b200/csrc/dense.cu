@@ -176,6 +176,10 @@ __device__ __forceinline__ void panel_row(uint32_t panel, int j, uint32_t w[4 * 
   }
 }
 
+__device__ __forceinline__ void words_to(uint4 w[4], const uint32_t a[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+}
 // 32 values as 16-bit elements.
 __device__ __forceinline__ void pack32(uint4 w[4], const float v[32], bool bf16) {
 #pragma unroll
@@ -186,24 +190,6 @@ __device__ __forceinline__ void pack32(uint4 w[4], const float v[32], bool bf16)
     w[i].w = pack16(v[8 * i + 6], v[8 * i + 7], bf16);
   }
 }
-// relu(G) as 16-bit elements: a positive value that rounds to zero keeps the type's
-// smallest positive value, so that the stored value's sign is the ReLU's mask.
-__device__ __forceinline__ uint32_t pack16_relu(float a, float b, bool bf16) {
-  uint32_t w = pack16(a, b, bf16);
-  if (a > 0.f && (w & 0xffffu) == 0) w |= 1u;
-  if (b > 0.f && (w >> 16) == 0) w |= 0x10000u;
-  return w;
-}
-__device__ __forceinline__ void pack32_relu(uint4 w[4], const float v[32], bool bf16) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i].x = pack16_relu(v[8 * i], v[8 * i + 1], bf16);
-    w[i].y = pack16_relu(v[8 * i + 2], v[8 * i + 3], bf16);
-    w[i].z = pack16_relu(v[8 * i + 4], v[8 * i + 5], bf16);
-    w[i].w = pack16_relu(v[8 * i + 6], v[8 * i + 7], bf16);
-  }
-}
-
 // ---------------------------------------------------------------- epilogues
 // Each thread owns one row of the tile (its tensor-memory lane) and a half of the tile's
 // columns; a warp owns 32 rows from `row0` on and stores them through its `panel`s.
@@ -282,50 +268,59 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, u
   }
   if (rows <= 0 || cols <= 0) return;  // (the whole warp)
   uint4 w[4];
-  if (P.save == SFNN_SAVE_FULL) {
-    unsigned char *rp = static_cast<unsigned char *>(P.r) + (row0 * P.ldr + n0) * 2;
-    unsigned char *up = static_cast<unsigned char *>(P.u) + (row0 * P.ldr + n0) * 2;
-#pragma unroll
-    for (int c = 0; c < 64; c += 32) {
-      pack32_relu(w, r + c, bf16);
-      panel_out(panel, w, rp + c * 2, P.ldr * 2, rows, (cols - c) / 8);
-      pack32(w, u + c, bf16);
-      panel_out(panel + kPanel, w, up + c * 2, P.ldr * 2, rows, (cols - c) / 8);
-    }
-  } else if (P.save == SFNN_SAVE_ACT8) {
+  if (P.save != SFNN_SAVE_NONE) {  // whole blocks: code rows are padded to 64 columns
+    const bool full = P.save == SFNN_SAVE_FULL;
     uint32_t rt = 0, ut = 0;
 #pragma unroll
     for (int i = 0; i < 64; ++i) {
       rt = max(rt, __float_as_uint(r[i]) & 0x7fffffffu);
       ut = max(ut, __float_as_uint(u[i]) & 0x7fffffffu);
     }
-    const Act8Scale sr = act8_scale(rt, 255.f), su = act8_scale(ut, 127.f);
+    const Act8Scale sr = full ? block_scale(rt, 65535.f, 0x0b800000u) : act8_scale(rt, 255.f);
+    const Act8Scale su = full ? block_scale(ut, 32767.f, 0x0b800000u) : act8_scale(ut, 127.f);
     if (lane < rows) {
       P.rs[(row0 + lane) * P.lds + (n0 >> 6)] = sr.scale;
       P.us[(row0 + lane) * P.lds + (n0 >> 6)] = su.scale;
     }
-    auto codes = [&](const float *v, float inv, bool relu) {  // whole blocks: code rows are padded to 64 columns
+    if (full) {
+      unsigned char *rp = static_cast<unsigned char *>(P.r) + (row0 * P.ldr + n0) * 2;
+      unsigned char *up = static_cast<unsigned char *>(P.u) + (row0 * P.ldr + n0) * 2;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t q[4];
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t q[16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float *a = v + 16 * i + 4 * j;
-          q[j] = act8_codes(a[0], a[1], a[2], a[3], inv);
-          if (relu) {
-            uint32_t pos = 0;
+        for (int i = 0; i < 16; ++i) q[i] = code16_pair_relu(r[c + 2 * i], r[c + 2 * i + 1], sr.inv);
+        words_to(w, q);
+        panel_out(panel, w, rp + c * 2, P.ldr * 2, rows, 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) pos |= a[k] > 0.f ? 1u << (8 * k) : 0u;
-            q[j] = act8_lift(q[j], pos);
-          }
-        }
-        w[i] = make_uint4(q[0], q[1], q[2], q[3]);
+        for (int i = 0; i < 16; ++i) q[i] = code16_pair(u[c + 2 * i], u[c + 2 * i + 1], su.inv);
+        words_to(w, q);
+        panel_out(panel + kPanel, w, up + c * 2, P.ldr * 2, rows, 4);
       }
-    };
-    codes(r, sr.inv, true);
-    panel_out(panel, w, static_cast<unsigned char *>(P.r) + row0 * P.ldr + n0, P.ldr, rows, 4);
-    codes(u, su.inv, false);
-    panel_out(panel + kPanel, w, static_cast<unsigned char *>(P.u) + row0 * P.ldr + n0, P.ldr, rows, 4);
+    } else {
+      auto codes = [&](const float *v, float inv, bool relu) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t q[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float *a = v + 16 * i + 4 * j;
+            q[j] = act8_codes(a[0], a[1], a[2], a[3], inv);
+            if (relu) {
+              uint32_t pos = 0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) pos |= a[k] > 0.f ? 1u << (8 * k) : 0u;
+              q[j] = act8_lift(q[j], pos);
+            }
+          }
+          w[i] = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+      };
+      codes(r, sr.inv, true);
+      panel_out(panel, w, static_cast<unsigned char *>(P.r) + row0 * P.ldr + n0, P.ldr, rows, 4);
+      codes(u, su.inv, false);
+      panel_out(panel + kPanel, w, static_cast<unsigned char *>(P.u) + row0 * P.ldr + n0, P.ldr, rows, 4);
+    }
   }
   unsigned char *hp = static_cast<unsigned char *>(Q.out) + (row0 * Q.ldo + n0) * 2;
 #pragma unroll
@@ -358,32 +353,30 @@ __device__ __forceinline__ float2 column_sums(uint32_t panel) {
 }
 
 // Request the saved relu(G) and U of a warp's rows into the panels `in` and `in` + 1: 64 bytes
-// a row of each, 32 values or 64 codes (whose two scales a lane keeps).
-template <bool CODES>
+// a row of each, 32 codes of 16 bits or 64 of 8; a lane keeps its row's two scales.
+template <bool CODES8>
 __device__ __forceinline__ void saved_request(const DenseParams &P, const Unit &Q, int64_t row0, int n0, uint32_t in,
                                               float2 &scales) {
   const int rows = (int)min((int64_t)32, Q.M - row0), lane = threadIdx.x & 31;
-  constexpr int E = CODES ? 1 : 2;
-  const int pieces = CODES ? (n0 < Q.N ? 4 : 0) : (Q.N - n0) / 8;  // code rows are padded to 64 columns
+  constexpr int E = CODES8 ? 1 : 2;
+  const int pieces = n0 < Q.N ? 4 : 0;  // code rows are padded to 64 columns
   const int64_t at = pieces > 0 && rows > 0 ? (row0 * P.ldr + n0) * E : 0;
   panel_request(in, static_cast<const unsigned char *>(P.r) + at, P.ldr * E, rows, pieces);
   panel_request(in + kPanel, static_cast<const unsigned char *>(P.u) + at, P.ldr * E, rows, pieces);
   cp_async_commit();
-  if (CODES) {
-    scales = make_float2(0.f, 0.f);
-    if (pieces && lane < rows)
-      scales = make_float2(__ldg(P.rs + (row0 + lane) * P.lds + (n0 >> 6)), __ldg(P.us + (row0 + lane) * P.lds + (n0 >> 6)));
-  }
+  scales = make_float2(0.f, 0.f);
+  if (pieces && lane < rows)
+    scales = make_float2(__ldg(P.rs + (row0 + lane) * P.lds + (n0 >> 6)), __ldg(P.us + (row0 + lane) * P.lds + (n0 >> 6)));
 }
 
-// relu(G) and U of 32 columns of a row, as they were saved: 16 words of two values, or 8 words
-// of four codes and the scales.  They are widened where they are used and not before: held
-// as floats they cost the kernel its registers, and a spill here misses L1 (shared memory
-// leaves it next to nothing; measured: 13 to 20 us a tile instead of 3 to 5).
-template <bool CODES, bool bf16>
+// relu(G) and U of 32 columns of a row, as they were saved: 8 words of four codes or 16 of
+// two, and the scales.  They are widened where they are used and not before: held as floats
+// they cost the kernel its registers, and a spill here misses L1 (shared memory leaves it
+// next to nothing; measured: 13 to 20 us a tile instead of 3 to 5).
+template <bool CODES8>
 struct SavedWords {
-  uint32_t r[CODES ? 8 : 16], u[CODES ? 8 : 16];
-  float rs, r0, us;  // a code as a float: its byte under the exponent of 2^23, less 2^23 (and 128 if signed)
+  uint32_t r[CODES8 ? 8 : 16], u[CODES8 ? 8 : 16];
+  float rs, r0, us;  // a code as a float: its bits under the exponent of 2^23, less 2^23 (and half the range if signed)
   __device__ __forceinline__ void set_scales(float sr, float su) {
     rs = sr == 0.f ? __uint_as_float(1u) : sr;  // a lifted code of a block whose scale is zero keeps its neuron on
     r0 = -8388608.f * rs;
@@ -391,31 +384,24 @@ struct SavedWords {
   }
   // columns 2 i and 2 i + 1
   __device__ __forceinline__ void get(int i, float2 &rv, float2 &uv) const {
-    if (CODES) {
-      const uint32_t a = r[i >> 1], b = u[i >> 1] ^ 0x80808080u, k = 0x7440u + 2u * (i & 1);
-      rv.x = fmaf(__uint_as_float(__byte_perm(a, 0x4b000000u, k)), rs, r0);
-      rv.y = fmaf(__uint_as_float(__byte_perm(a, 0x4b000000u, k + 1)), rs, r0);
-      uv.x = (__uint_as_float(__byte_perm(b, 0x4b000000u, k)) - 8388736.f) * us;
-      uv.y = (__uint_as_float(__byte_perm(b, 0x4b000000u, k + 1)) - 8388736.f) * us;
-    } else {
-      rv = unpack16(r[i], bf16);
-      uv = unpack16(u[i], bf16);
-    }
+    const uint32_t a = r[CODES8 ? i >> 1 : i], b = u[CODES8 ? i >> 1 : i] ^ (CODES8 ? 0x80808080u : 0x80008000u);
+    const uint32_t lo = CODES8 ? 0x7440u + 2u * (i & 1) : 0x7410u, hi = CODES8 ? lo + 1 : 0x7432u;
+    constexpr float kZero = CODES8 ? 8388608.f + 128.f : 8388608.f + 32768.f;
+    rv.x = fmaf(__uint_as_float(__byte_perm(a, 0x4b000000u, lo)), rs, r0);
+    rv.y = fmaf(__uint_as_float(__byte_perm(a, 0x4b000000u, hi)), rs, r0);
+    uv.x = (__uint_as_float(__byte_perm(b, 0x4b000000u, lo)) - kZero) * us;
+    uv.y = (__uint_as_float(__byte_perm(b, 0x4b000000u, hi)) - kZero) * us;
   }
   __device__ __forceinline__ void forget() {  // (the widened values of an earlier use)
 #pragma unroll
-    for (int i = 0; i < (CODES ? 8 : 16); ++i) asm volatile("" : "+r"(r[i]), "+r"(u[i]));
+    for (int i = 0; i < (CODES8 ? 8 : 16); ++i) asm volatile("" : "+r"(r[i]), "+r"(u[i]));
   }
 };
-__device__ __forceinline__ void words_to(uint4 w[4], const uint32_t a[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
-}
 
 // 32 columns of dH: H, dU and dG.
-template <bool CODES, bool bf16>
+template <bool CODES8, bool bf16>
 __device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
-                                         SavedWords<CODES, bf16> &v, uint32_t panel) {
+                                         SavedWords<CODES8> &v, uint32_t panel) {
   const int lane = threadIdx.x & 31, rows = (int)min((int64_t)32, Q.M - row0), pieces = (Q.N - n0) / 8;
   if (rows <= 0 || pieces <= 0) return;  // (the whole warp)
   const int64_t at = (row0 * Q.ldo + n0) * 2, ld = Q.ldo * 2;
@@ -464,27 +450,27 @@ __device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, ui
 }
 
 // 128 columns of dH from n0 on; the first saved piece has been requested.
-template <bool CODES, bool bf16>
+template <bool CODES8, bool bf16>
 __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
                                            float2 scales, uint32_t panel) {
   const uint32_t in = panel + 2 * kPanel;
 #pragma unroll 1
   for (int c = 0; c < 128; c += 32) {
-    const bool first = !CODES || (c & 32) == 0, last = !CODES || (c & 32);  // of a saved piece
-    SavedWords<CODES, bf16> v;
+    const bool first = !CODES8 || (c & 32) == 0, last = !CODES8 || (c & 32);  // of a saved piece
+    SavedWords<CODES8> v;
     v.set_scales(scales.x, scales.y);
     if (first) {
       cp_async_wait<0>();
       __syncwarp();
     }
-    const int piece = CODES && (c & 32) ? 2 : 0;
-    panel_row<CODES ? 2 : 4>(in, piece, v.r);
-    panel_row<CODES ? 2 : 4>(in + kPanel, piece, v.u);
+    const int piece = CODES8 && (c & 32) ? 2 : 0;
+    panel_row<CODES8 ? 2 : 4>(in, piece, v.r);
+    panel_row<CODES8 ? 2 : 4>(in + kPanel, piece, v.u);
     if (last && c + 32 < 128) {
       __syncwarp();  // every lane has its row
-      saved_request<CODES>(P, Q, row0, n0 + c + 32, in, scales);
+      saved_request<CODES8>(P, Q, row0, n0 + c + 32, in, scales);
     }
-    dgated32(P, Q, taddr + c, row0, n0 + c, v, panel);
+    dgated32<CODES8, bf16>(P, Q, taddr + c, row0, n0 + c, v, panel);
   }
   __syncwarp();
 }

@@ -44,15 +44,18 @@ constexpr int kAct8Block = 64;
 struct Act8Scale {
   float scale, inv;
 };
-// `top`: the largest fp32 bit pattern of the block's magnitudes (NaN > inf > finite).
-__device__ __forceinline__ Act8Scale act8_scale(uint32_t top, float qmax) {
+// `top`: the largest fp32 bit pattern of the block's magnitudes (NaN > inf > finite); below
+// `least` (2^-112 for 8-bit codes, 2^-104 for 16-bit ones) the reciprocal could overflow.
+__device__ __forceinline__ Act8Scale block_scale(uint32_t top, float qmax, uint32_t least) {
   Act8Scale s;
   s.scale = __uint_as_float(top) * (1.f / qmax);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inv) : "f"(s.scale));  // within an ulp: a code is off only next to a tie
-  if (top < 0x07800000u) s.scale = s.inv = 0.f;
+  if (top < least) s.scale = s.inv = 0.f;
   if (top >= 0x7f800000u) s.scale = __uint_as_float(0x7fffffffu);
   return s;
 }
+__device__ __forceinline__ Act8Scale act8_scale(uint32_t top, float qmax) { return block_scale(top, qmax, 0x07800000u); }
+
 // Codes of four values as bytes: v * inv + 1.5 * 2^23 in one fused multiply-add leaves the
 // nearest integer (ties to even) in the low byte.  |v * inv| <= qmax (1 + 2^-21), so no code
 // leaves its range; in a NaN block the codes mean nothing.
@@ -67,6 +70,21 @@ __device__ __forceinline__ uint32_t act8_codes(float a, float b, float c, float 
 __device__ __forceinline__ uint32_t act8_lift(uint32_t codes, uint32_t positive) {
   const uint32_t some = ((codes & 0x7f7f7f7fu) + 0x7f7f7f7fu) | codes;  // bit 7 of each byte that is not zero
   return codes | (positive & ~(some >> 7));
+}
+
+// ---------------------------------------------------------------- the saved hidden layer in 16 bits
+// What the forward pass keeps at full precision: the same blocks of 64 with 16-bit codes,
+// relu(G) max / 65535 with codes 0..65535 (again at least 1 where positive), U max|v| / 32767
+// signed.  They hold a value to 2^-17 of its block's largest, where the values' own types
+// would round each to 2^-9 (bf16) or 2^-12 of itself: of all a gradient's error, what is left
+// is the one rounding of dG, dU or H to the tensor cores' type, and its own.
+__device__ __forceinline__ uint32_t code16_pair(float a, float b, float inv) {
+  constexpr float kMagic = 12582912.f;
+  return __byte_perm(__float_as_uint(fmaf(a, inv, kMagic)), __float_as_uint(fmaf(b, inv, kMagic)), 0x5410);
+}
+__device__ __forceinline__ uint32_t code16_pair_relu(float a, float b, float inv) {
+  const uint32_t positive = (a > 0.f ? 1u : 0u) | (b > 0.f ? 0x10000u : 0u);
+  return __vmaxu2(code16_pair(a, b, inv), positive);
 }
 
 // ---------------------------------------------------------------- the product

@@ -83,20 +83,15 @@ sfnn_status check(const sfnn_gated_desc *q) {
 }
 
 sfnn_status check_saved(const sfnn_gated_desc *q, const sfnn_gated_saved *sv) {
-  if (sv->kind == SFNN_SAVE_FULL) {
-    if (q->n % 8) return SFNN_ERR_UNSUPPORTED;
-    if (q->T > 0 && (!mat_ok(sv->r, sv->ld, q->n) || !mat_ok(sv->u, sv->ld, q->n))) return SFNN_ERR_INVALID_ARG;
-    return SFNN_OK;
-  }
-  if (sv->kind != SFNN_SAVE_ACT8) return SFNN_ERR_INVALID_ARG;
+  if (sv->kind != SFNN_SAVE_FULL && sv->kind != SFNN_SAVE_ACT8) return SFNN_ERR_INVALID_ARG;
   if (q->n % 8) return SFNN_ERR_UNSUPPORTED;
+  const bool eight = sv->kind == SFNN_SAVE_ACT8;
   const int64_t nb = up(q->n, kAct8Block) / kAct8Block, db = up(q->d, kAct8Block) / kAct8Block;
-  if (sv->ld < nb * kAct8Block || sv->ld % 16 || sv->lds < nb || sv->ld_x < db * kAct8Block || sv->ld_x % 16 ||
-      sv->lds_x < db)
-    return SFNN_ERR_INVALID_ARG;
-  if (q->T > 0 && (!sv->r || !sv->u || !sv->r_scales || !sv->u_scales || !sv->x || !sv->x_scales || !a16(sv->r) ||
-                   !a16(sv->u) || !a16(sv->x)))
-    return SFNN_ERR_INVALID_ARG;
+  if (sv->ld < nb * kAct8Block || sv->ld % 16 || sv->lds < nb) return SFNN_ERR_INVALID_ARG;
+  if (eight && (sv->ld_x < db * kAct8Block || sv->ld_x % 16 || sv->lds_x < db)) return SFNN_ERR_INVALID_ARG;
+  if (q->T == 0) return SFNN_OK;
+  if (!sv->r || !sv->u || !sv->r_scales || !sv->u_scales || !a16(sv->r) || !a16(sv->u)) return SFNN_ERR_INVALID_ARG;
+  if (eight && (!sv->x || !sv->x_scales || !a16(sv->x))) return SFNN_ERR_INVALID_ARG;
   return SFNN_OK;
 }
 

@@ -197,9 +197,9 @@ class Act8:
         return self.codes.numel() + 4 * self.scales.numel()
 
 
-def _act8_empty(like, T, cols):
+def _act8_empty(like, T, cols, dtype=torch.uint8):
     nb = (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
-    return like.new_empty((T, nb * ACT8_BLOCK), dtype=torch.uint8), like.new_empty((T, nb), dtype=torch.float32)
+    return like.new_empty((T, nb * ACT8_BLOCK), dtype=dtype), like.new_empty((T, nb), dtype=torch.float32)
 
 
 def quantize_act8(x, relu: bool = False, stream=None) -> Act8:
@@ -337,8 +337,8 @@ def mxfp4_linear(x, w: Mxfp4, out_dtype=None, stream=None):
 
 # ------------------------------------------------------------------ gated FFN
 class GatedSaved:
-    """What gated_ffn_forward keeps for gated_ffn_backward: relu(G) and U, and X itself
-    ("full") or everything as 8-bit blocks ("act8")."""
+    """What gated_ffn_forward keeps for gated_ffn_backward: relu(G) and U as 16-bit blocks and
+    X itself ("full"), or everything as 8-bit blocks ("act8"); see sfnn_gated_saved."""
 
     __slots__ = ("kind", "x", "r", "u", "r_scales", "u_scales", "x_codes", "x_scales", "shape", "dtype", "has_b")
 
@@ -353,7 +353,8 @@ class GatedSaved:
 
     def _fill(self):
         if self.kind == "full":
-            return _GatedSaved(1, 0, self.r.data_ptr(), self.u.data_ptr(), self.r.shape[1])
+            return _GatedSaved(1, 0, self.r.data_ptr(), self.u.data_ptr(), self.r.shape[1], self.r_scales.data_ptr(),
+                               self.u_scales.data_ptr(), self.r_scales.shape[1])
         return _GatedSaved(2, 0, self.r.data_ptr(), self.u.data_ptr(), self.r.shape[1], self.r_scales.data_ptr(),
                            self.u_scales.data_ptr(), self.r_scales.shape[1], self.x_codes.data_ptr(),
                            self.x_codes.shape[1], self.x_scales.data_ptr(), self.x_scales.shape[1])
@@ -374,7 +375,8 @@ def gated_ffn_forward(x, w_gate, w_up, w_down, b=None, save=None, stream=None):
 
     x [..., d]; w_gate, w_up [n, d]; w_down [d, n]; b [n] or None; fp16 or bf16, d and n
     multiples of 8, rows 16-byte aligned (any even row stride).  ``save``: None (saved is
-    None), "full" (relu(G), U and a reference to x) or "act8" (all three as 8-bit blocks)."""
+    None), "full" (relu(G) and U as 16-bit blocks, a reference to x) or "act8" (all three as
+    8-bit blocks)."""
     if save not in SAVE:
         raise ValueError("save must be None, 'full' or 'act8'")
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
@@ -397,13 +399,13 @@ def gated_ffn_forward(x, w_gate, w_up, w_down, b=None, save=None, stream=None):
         if save is not None:
             saved = GatedSaved()
             saved.kind, saved.shape, saved.dtype, saved.has_b = save, x.shape, dt, b is not None
-            saved.x = saved.r_scales = saved.u_scales = saved.x_codes = saved.x_scales = None
+            saved.x = saved.x_codes = saved.x_scales = None
             if save == "full":
                 saved.x = x
-                saved.r, saved.u = x.new_empty((T, n)), x.new_empty((T, n))
-            else:
-                saved.r, saved.r_scales = _act8_empty(x, T, n)
-                saved.u, saved.u_scales = _act8_empty(x, T, n)
+            codes = torch.int16 if save == "full" else torch.uint8
+            saved.r, saved.r_scales = _act8_empty(x, T, n, codes)
+            saved.u, saved.u_scales = _act8_empty(x, T, n, codes)
+            if save == "act8":
                 saved.x_codes, saved.x_scales = _act8_empty(x, T, d)
             csaved = ctypes.byref(saved._fill())
         if T:
@@ -423,7 +425,7 @@ def gated_ffn_backward(dy, saved: GatedSaved, w_gate, w_up, w_down, need=(True, 
     pdy, T, _, lddy = _mat(dy, "dy", dt, None, d)
     n, wf = _weights(dt, w_gate, w_up, w_down, d)
     full = saved.kind == "full"
-    if dy.shape != saved.shape or saved.r.shape[1] != (n if full else -(-n // ACT8_BLOCK) * ACT8_BLOCK):
+    if dy.shape != saved.shape or saved.r.shape[1] != -(-n // ACT8_BLOCK) * ACT8_BLOCK:
         raise ValueError("dy and the weights must have the forward pass's shapes")
     px, ldx = None, 0
     if full:

@@ -453,8 +453,10 @@ typedef enum {
     SFNN_DOWN_WIDTH_MAJOR = 0, /* w_down [d x n], PyTorch's down.weight */
     SFNN_DOWN_NEURON_MAJOR = 1 /* w_down [n x d], a row per neuron (forward only) */
 } sfnn_down_layout;
-/* What the forward pass keeps for the backward pass: nothing; relu(G) and U in the values'
- * type (the caller keeps X); or X, relu(G) and U as 8-bit blocks (sfnn_act8_quantize). */
+/* What the forward pass keeps for the backward pass: nothing; relu(G) and U as blocks of 64
+ * 16-bit codes with an fp32 scale each, max / 65535 for relu(G) (a positive value keeps a code
+ * of at least 1) and max|U| / 32767, signed (the caller keeps X); or X, relu(G) and U as 8-bit
+ * blocks (sfnn_act8_quantize).  A block with a NaN or an infinity gives NaN gradients. */
 typedef enum { SFNN_SAVE_NONE = 0, SFNN_SAVE_FULL = 1, SFNN_SAVE_ACT8 = 2 } sfnn_save;
 typedef struct {
     int32_t T, d, n;         /* tokens, width, neurons */
@@ -474,9 +476,9 @@ typedef struct {
 typedef struct {
     int32_t kind;            /* sfnn_save */
     int32_t reserved;
-    void *r, *u;             /* [T x n] relu(G), U: values (FULL) or codes (ACT8), ld elements apart */
-    int64_t ld;              /* ACT8: a multiple of 16, at least n rounded up to 64 */
-    float *r_scales, *u_scales; /* ACT8: [T x n/64 rounded up], lds apart */
+    void *r, *u;             /* [T x n] relu(G), U: 16-bit (FULL) or 8-bit (ACT8) codes, ld codes apart */
+    int64_t ld;              /* a multiple of 16, at least n rounded up to 64 */
+    float *r_scales, *u_scales; /* [T x n/64 rounded up], lds apart */
     int64_t lds;
     void *x;                 /* ACT8: X's codes, ld_x apart, and scales, lds_x apart */
     int64_t ld_x;

@@ -25,7 +25,7 @@ def forward(q, y=4096, ldy=None, y_dtype=None, saved=None, ws=4096, ws_bytes=1 <
 
 
 def saved_of(T=4, d=64, n=128, kind=1):
-    s = dense._GatedSaved(kind, 0, 4096, 4096, n if kind == 1 else -(-n // 64) * 64, 4096, 4096, -(-n // 64), 4096,
+    s = dense._GatedSaved(kind, 0, 4096, 4096, -(-n // 64) * 64, 4096, 4096, -(-n // 64), 4096,
                           -(-d // 64) * 64, 4096, -(-d // 64))
     return s
 
