@@ -13,8 +13,10 @@
 //
 // Product: Y = (Xq 2^ex) . (Wq 2^ew)^T with tcgen05's block-scaled MMA (kind::mxf4, K = 64 an
 // instruction, four times the 16-bit rate), fp32 accumulators.  At that rate a 256 x 256 x 256
-// step of a CTA pair takes about 512 cycles and moves 35 KB per SM from L2: what bounds it is
-// the L2 -> shared memory path as much as the tensor pipe.
+// step of a CTA pair takes 512 cycles; the six copies of its scales into tensor memory take
+// their turn in the same pipe and add about 300 (4096 x 28672 x 8192: 474 us, 4.1 PFLOP/s;
+// 337 with the copies left out).  Issuing them a step ahead (499 us) or writing the scales
+// from registers by four warps of their own (760 us) measured slower.
 #include <algorithm>
 
 #include "common.cuh"
