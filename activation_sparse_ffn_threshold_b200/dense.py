@@ -184,22 +184,61 @@ def _vp(t):
 
 
 # ------------------------------------------------------------------ act8
+def _blocks(cols) -> int:
+    return (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
+
+
+class _Planes:
+    """Blocks of 64: codes [T, cols rounded up to 64] of ``esize`` bytes and, behind them in
+    the same allocation, their fp32 scales [T, blocks]."""
+
+    __slots__ = ("buf", "at", "T", "nb", "esize")
+
+    def __init__(self, buf, at, T, cols, esize):
+        self.buf, self.at, self.T, self.nb, self.esize = buf, at, T, _blocks(cols), esize
+
+    @staticmethod
+    def size(T, cols, esize) -> int:
+        return T * _blocks(cols) * (ACT8_BLOCK * esize + 4)  # a multiple of 4: the next planes start aligned
+
+    def pointers(self):
+        """(codes, codes' row stride, scales, scales' row stride)."""
+        p = self.buf.data_ptr() + self.at
+        ld = self.nb * ACT8_BLOCK
+        return p, ld, p + self.T * ld * self.esize, self.nb
+
+    @property
+    def codes(self):
+        n = self.T * self.nb * ACT8_BLOCK * self.esize
+        c = self.buf[self.at:self.at + n].view(self.T, self.nb * ACT8_BLOCK * self.esize)
+        return c if self.esize == 1 else c.view(torch.int16)
+
+    @property
+    def scales(self):
+        a = self.at + self.T * self.nb * ACT8_BLOCK * self.esize
+        return self.buf[a:a + 4 * self.T * self.nb].view(torch.float32).view(self.T, self.nb)
+
+
 class Act8:
     """Rows held as 8-bit codes with an fp32 scale per 64 values (sfnn_act8_quantize)."""
 
-    __slots__ = ("codes", "scales", "shape", "dtype", "relu")
+    __slots__ = ("_p", "shape", "dtype", "relu")
 
-    def __init__(self, codes, scales, shape, dtype, relu):
-        self.codes, self.scales, self.shape, self.dtype, self.relu = codes, scales, shape, dtype, relu
+    def __init__(self, planes, shape, dtype, relu):
+        self._p, self.shape, self.dtype, self.relu = planes, shape, dtype, relu
+
+    @property
+    def codes(self):
+        """uint8 [T, cols rounded up to 64]; without ``relu`` the bytes are int8."""
+        return self._p.codes
+
+    @property
+    def scales(self):
+        return self._p.scales
 
     @property
     def nbytes(self) -> int:
-        return self.codes.numel() + 4 * self.scales.numel()
-
-
-def _act8_empty(like, T, cols, dtype=torch.uint8):
-    nb = (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
-    return like.new_empty((T, nb * ACT8_BLOCK), dtype=dtype), like.new_empty((T, nb), dtype=torch.float32)
+        return self._p.buf.numel()
 
 
 def quantize_act8(x, relu: bool = False, stream=None) -> Act8:
@@ -212,33 +251,33 @@ def quantize_act8(x, relu: bool = False, stream=None) -> Act8:
         raise ValueError("x: rows must not overlap")
     index = x.get_device()
     with _on(index, stream):
-        q, s = _act8_empty(x, T, cols)
-        _check(load_library().sfnn_act8_quantize(p, ld, T, cols, code, 1 if relu else 0, q.data_ptr(), q.shape[1],
-                                                 s.data_ptr(), s.shape[1], _raw_stream(index)), "sfnn_act8_quantize")
-    return Act8(q, s, x.shape, x.dtype, bool(relu))
+        q = _Planes(x.new_empty(_Planes.size(T, cols, 1), dtype=torch.uint8), 0, T, cols, 1)
+        pc, ldq, ps, lds = q.pointers()
+        _check(load_library().sfnn_act8_quantize(p, ld, T, cols, code, 1 if relu else 0, pc, ldq, ps, lds,
+                                                 _raw_stream(index)), "sfnn_act8_quantize")
+    return Act8(q, x.shape, x.dtype, bool(relu))
 
 
 def dequantize_act8(q: Act8, dtype=None, out=None, stream=None):
     """The values that q stands for, [..., cols] in ``dtype`` (default: the quantised tensor's)."""
     dtype = dtype or (out.dtype if out is not None else q.dtype)
     code = _code(dtype)
-    codes, scales = q.codes, q.scales
-    T, ldq = codes.shape
+    buf, T = q._p.buf, q._p.T
+    pc, ldq, ps, lds = q._p.pointers()
     cols = q.shape[-1]
-    index = codes.get_device()
+    index = buf.get_device()
     with _on(index, stream):
         if out is None:
-            out = codes.new_empty(q.shape, dtype=dtype)
+            out = buf.new_empty(q.shape, dtype=dtype)
             ld = cols
         else:
             if out.dtype != dtype or out.shape != q.shape or out.get_device() != index:
-                raise ValueError(f"out must be a {dtype} tensor of shape {tuple(q.shape)} on {codes.device}")
+                raise ValueError(f"out must be a {dtype} tensor of shape {tuple(q.shape)} on {buf.device}")
             _, _, _, ld = _rows(out, "out", cols)
             if ld < cols:
                 raise ValueError("out: rows must not overlap")
-        _check(load_library().sfnn_act8_restore(codes.data_ptr(), ldq, scales.data_ptr(), scales.shape[1], T, cols,
-                                                1 if q.relu else 0, code, out.data_ptr(), ld, _raw_stream(index)),
-               "sfnn_act8_restore")
+        _check(load_library().sfnn_act8_restore(pc, ldq, ps, lds, T, cols, 1 if q.relu else 0, code, out.data_ptr(), ld,
+                                                _raw_stream(index)), "sfnn_act8_restore")
     return out
 
 
@@ -340,24 +379,35 @@ class GatedSaved:
     """What gated_ffn_forward keeps for gated_ffn_backward: relu(G) and U as 16-bit blocks and
     X itself ("full"), or everything as 8-bit blocks ("act8"); see sfnn_gated_saved."""
 
-    __slots__ = ("kind", "x", "r", "u", "r_scales", "u_scales", "x_codes", "x_scales", "shape", "dtype", "has_b")
+    __slots__ = ("kind", "x", "_r", "_u", "_x", "shape", "dtype", "has_b")
 
-    def tensors(self):
-        return [t for t in (self.x, self.r, self.u, self.r_scales, self.u_scales, self.x_codes, self.x_scales)
-                if t is not None]
+    def __init__(self, kind, x, T, d, n, has_b):
+        self.kind, self.shape, self.dtype, self.has_b = kind, x.shape, x.dtype, has_b
+        e = 2 if kind == "full" else 1
+        size = (_Planes.size(T, n, e) + 15) // 16 * 16  # each plane on 16 bytes
+        buf = x.new_empty(2 * size + (0 if e == 2 else _Planes.size(T, d, 1)), dtype=torch.uint8)
+        self._r, self._u = _Planes(buf, 0, T, n, e), _Planes(buf, size, T, n, e)
+        self.x, self._x = (x, None) if e == 2 else (None, _Planes(buf, 2 * size, T, d, 1))
+
+    r = property(lambda self: self._r.codes, doc="codes of relu(G): int16 (the bits of a uint16) or uint8")
+    u = property(lambda self: self._u.codes, doc="codes of U: int16, or uint8 (the bits of an int8)")
+    r_scales = property(lambda self: self._r.scales)
+    u_scales = property(lambda self: self._u.scales)
+    x_codes = property(lambda self: None if self._x is None else self._x.codes)
+    x_scales = property(lambda self: None if self._x is None else self._x.scales)
 
     @property
     def nbytes(self) -> int:
         """Bytes held, X of "full" included."""
-        return sum(t.numel() * t.element_size() for t in self.tensors())
+        return self._r.buf.numel() + (0 if self.x is None else self.x.numel() * self.x.element_size())
 
     def _fill(self):
-        if self.kind == "full":
-            return _GatedSaved(1, 0, self.r.data_ptr(), self.u.data_ptr(), self.r.shape[1], self.r_scales.data_ptr(),
-                               self.u_scales.data_ptr(), self.r_scales.shape[1])
-        return _GatedSaved(2, 0, self.r.data_ptr(), self.u.data_ptr(), self.r.shape[1], self.r_scales.data_ptr(),
-                           self.u_scales.data_ptr(), self.r_scales.shape[1], self.x_codes.data_ptr(),
-                           self.x_codes.shape[1], self.x_scales.data_ptr(), self.x_scales.shape[1])
+        pr, ld, prs, lds = self._r.pointers()
+        pu, _, pus, _ = self._u.pointers()
+        if self._x is None:
+            return _GatedSaved(1, 0, pr, pu, ld, prs, pus, lds)
+        px, ldx, pxs, ldxs = self._x.pointers()
+        return _GatedSaved(2, 0, pr, pu, ld, prs, pus, lds, px, ldx, pxs, ldxs)
 
 
 def _weights(dtype, w_gate, w_up, w_down, d):
@@ -397,16 +447,7 @@ def gated_ffn_forward(x, w_gate, w_up, w_down, b=None, save=None, stream=None):
         y = x.new_empty(x.shape)
         saved = csaved = None
         if save is not None:
-            saved = GatedSaved()
-            saved.kind, saved.shape, saved.dtype, saved.has_b = save, x.shape, dt, b is not None
-            saved.x = saved.x_codes = saved.x_scales = None
-            if save == "full":
-                saved.x = x
-            codes = torch.int16 if save == "full" else torch.uint8
-            saved.r, saved.r_scales = _act8_empty(x, T, n, codes)
-            saved.u, saved.u_scales = _act8_empty(x, T, n, codes)
-            if save == "act8":
-                saved.x_codes, saved.x_scales = _act8_empty(x, T, d)
+            saved = GatedSaved(save, x, T, d, n, b is not None)
             csaved = ctypes.byref(saved._fill())
         if T:
             nbytes = lib.sfnn_gated_workspace(T, d, n, 0)
@@ -425,13 +466,13 @@ def gated_ffn_backward(dy, saved: GatedSaved, w_gate, w_up, w_down, need=(True, 
     pdy, T, _, lddy = _mat(dy, "dy", dt, None, d)
     n, wf = _weights(dt, w_gate, w_up, w_down, d)
     full = saved.kind == "full"
-    if dy.shape != saved.shape or saved.r.shape[1] != -(-n // ACT8_BLOCK) * ACT8_BLOCK:
+    if dy.shape != saved.shape or saved._r.nb != _blocks(n):
         raise ValueError("dy and the weights must have the forward pass's shapes")
     px, ldx = None, 0
     if full:
         px, _, _, ldx = _mat(saved.x, "x", dt, T, d)
     index = dy.get_device()
-    _same_device(index, w_gate, w_up, w_down, saved.r)
+    _same_device(index, w_gate, w_up, w_down, saved._r.buf)
     lib = load_library()
     with _on(index, stream):
         dx = dy.new_empty(dy.shape) if need[0] else None
@@ -468,7 +509,7 @@ class _GatedFFN(torch.autograd.Function):
         if dy.stride() != torch.empty(dy.shape, device="meta").stride() or dy.data_ptr() % 16:
             dy = dy.contiguous() if not dy.is_contiguous() else dy.clone()
         if x:
-            full = GatedSaved()
+            full = GatedSaved.__new__(GatedSaved)
             for k in GatedSaved.__slots__:
                 setattr(full, k, getattr(saved, k))
             full.x = x[0]
