@@ -678,14 +678,18 @@ cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
 
 cudaError_t launch_dense(DenseParams &P, int epi, int num_sms, cudaStream_t s) {
   auto units = [&](int i) { return P.p[i].tiles_m * P.p[i].tiles_n * P.p[i].split; };
+  // a unit's length in K chunks: a tile's epilogue (about 2.5 us) takes as long as nine
+  constexpr int kEpilogue = 9;
   P.first = units(0);
   P.rest = 0;
-  int len = 1;
+  int len = kEpilogue;
   for (int i = 1; i < P.count; ++i) {
     P.rest += units(i);
     len = std::max(len, P.p[i].nk / P.p[i].split);
   }
-  P.extra = P.count > 1 ? (P.p[0].nk / P.p[0].split + len / 2) / len : 0;
+  // (a part of a split K goes out in fp32, about half an epilogue more)
+  const int lead = std::max(kEpilogue, P.p[0].nk / P.p[0].split) + (P.p[0].split > 1 ? kEpilogue / 2 : 0);
+  P.extra = P.count > 1 ? (lead + len / 2 + 1) / len : 0;
   if (epi == kEpiGated) return run<kEpiGated>(P, num_sms, s);
   if (epi == kEpiDGated) return P.save == SFNN_SAVE_ACT8 ? run<kEpiDGated8>(P, num_sms, s) : run<kEpiDGated>(P, num_sms, s);
   return run<kEpiStore>(P, num_sms, s);

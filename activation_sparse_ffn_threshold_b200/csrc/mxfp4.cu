@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 // ---------------------------------------------------------------- the product
 constexpr int kThreads = 320;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 5;
 constexpr int kTmem = 512;
 constexpr int kAcc = 0, kSf = 256;      // tensor-memory columns: accumulators, scale slots
 constexpr int kSfSlot = 32;             // of a stage: A 2 x 4 columns, B 2 x 8 from column 8 on
@@ -211,6 +211,73 @@ __device__ __forceinline__ TilePos tile_pos(int t, int tiles_m, int tiles_n) {  
   const int band = t / per, r = t - band * per;
   const int rows = min(kBand, tiles_m - band * kBand);
   return {band * kBand + r % rows, r / rows};
+}
+
+// 128 bytes (of E-byte values) of each of a warp's rows: a lane holds its row's (w), the warp
+// stores them through a 4 KB panel of shared memory with 8 lanes of 16 bytes to a row, or,
+// where rows do not start on 16 bytes, value by value along the row (a lane storing its own
+// row touches 32 lines an instruction: 2508 x 9175 x 480 took 241 us).  `left`: columns that
+// exist from the first on.
+constexpr uint32_t kPanel = 4096;
+template <int E>
+__device__ __forceinline__ void panel_store(uint32_t panel, const uint32_t w[32], unsigned char *base, int64_t ld, int rows,
+                                            int left, int vec) {
+  const int lane = threadIdx.x & 31;
+  constexpr int COLS = 128 / E;
+  if (left <= 0) return;  // (the whole warp)
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(panel + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4))),
+                 "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                 : "memory");
+  __syncwarp();
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = i * 4 + (lane >> 3), piece = lane & 7;
+      uint4 q;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                   : "r"(panel + (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)))
+                   : "memory");
+      if (row >= rows) continue;
+      unsigned char *o = base + row * ld + piece * 16;
+      const int have = left - piece * (16 / E);
+      if (have >= 16 / E) {
+        *reinterpret_cast<uint4 *>(o) = q;
+      } else {
+        const uint32_t a[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 16 / E; ++j)
+          if (j < have) {
+            if (E == 4)
+              reinterpret_cast<uint32_t *>(o)[j] = a[j];
+            else
+              reinterpret_cast<uint16_t *>(o)[j] = (uint16_t)(a[(j >> 1) & 3] >> (16 * (j & 1)));
+          }
+      }
+    }
+  } else {
+    const int cols = min(COLS, left);
+#pragma unroll 4
+    for (int row = 0; row < rows; ++row) {
+      unsigned char *o = base + row * ld;
+#pragma unroll
+      for (int c = lane; c < COLS; c += 32) {
+        const uint32_t at = panel + (uint32_t)(row * 128 + (((c * E >> 4) ^ (row & 7)) << 4) + (c * E & 15));
+        if (E == 4) {
+          uint32_t v;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+          if (c < cols) reinterpret_cast<uint32_t *>(o)[c] = v;
+        } else {
+          uint16_t v;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+          if (c < cols) reinterpret_cast<uint16_t *>(o)[c] = v;
+        }
+      }
+    }
+  }
 }
 
 // 256 x 256 tiles by CTA pairs, 128 rows of X and of W in each CTA (more than 128 tokens).
@@ -320,6 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_mx(co
     }
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t panel = stage0 + stages * stage_bytes + (uint32_t)(warp - 2) * kPanel;
     int i = 0;
     for (int t = unit; t < ntiles; t += units, ++i) {
       if (!__all_sync(0xffffffffu, bar_wait(&acc_full, (uint32_t)(i & 1)))) {
@@ -330,49 +398,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_mx(co
       tm_fence_after();
       const TilePos pos = tile_pos(t, P.tiles_m, P.tiles_n);
       const int64_t row = (int64_t)pos.m * 256 + rank * 128 + quad * 32 + lane;
-      const int n0 = pos.n * 256;
-      // 32-column units half, half + 2, ...: at most four
-      uint32_t v[4][32];
+      const int64_t row0 = row - lane;
+      const int n0 = pos.n * 256 + half * 128;
+      uint32_t v[4][32];  // this warp's 128 columns
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        tm_ld32(tmem + ((uint32_t)(quad * 32) << 16) + kAcc + (half + 2 * u) * 32, v[u]);
+        tm_ld32(tmem + ((uint32_t)(quad * 32) << 16) + kAcc + half * 128 + u * 32, v[u]);
       tm_wait_ld();
       tm_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty, 0));
-      if (row >= P.M) continue;
+      const int rows = (int)min((int64_t)32, P.M - row0);
+      if (rows <= 0 || n0 >= P.N) continue;  // (the whole warp)
+      if (P.out_dtype == SFNN_F32) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int col = n0 + (half + 2 * u) * 32;
-        const int cols = min(32, P.N - col);
-        if (cols <= 0) continue;
-        if (P.out_dtype == SFNN_F32) {
-          float *o = static_cast<float *>(P.out) + row * P.ldo + col;
-          if (P.vec && cols == 32) {
+        for (int u = 0; u < 4; ++u)
+          panel_store<4>(panel, v[u], static_cast<unsigned char *>(P.out) + (row0 * P.ldo + n0 + u * 32) * 4, P.ldo * 4, rows,
+                         P.N - (n0 + u * 32), P.vec);
+      } else {
+        const bool bf16 = P.out_dtype == SFNN_BF16;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              reinterpret_cast<uint4 *>(o)[j] = make_uint4(v[u][4 * j], v[u][4 * j + 1], v[u][4 * j + 2], v[u][4 * j + 3]);
-          } else {
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < cols) o[j] = __uint_as_float(v[u][j]);
-          }
-        } else {
-          const bool bf16 = P.out_dtype == SFNN_BF16;
-          uint16_t *o = static_cast<uint16_t *>(P.out) + row * P.ldo + col;
-          uint32_t p[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            p[j] = pack16(__uint_as_float(v[u][2 * j]), __uint_as_float(v[u][2 * j + 1]), bf16);
-          if (P.vec && cols == 32) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              reinterpret_cast<uint4 *>(o)[j] = make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < cols) o[j] = (uint16_t)(p[j >> 1] >> (16 * (j & 1)));
-          }
+          for (int j = 0; j < 32; ++j)
+            p[j] = pack16(__uint_as_float(v[2 * h + (j >> 4)][2 * (j & 15)]),
+                          __uint_as_float(v[2 * h + (j >> 4)][2 * (j & 15) + 1]), bf16);
+          panel_store<2>(panel, p, static_cast<unsigned char *>(P.out) + (row0 * P.ldo + n0 + h * 64) * 2, P.ldo * 2, rows,
+                         P.N - (n0 + h * 64), P.vec);
         }
       }
     }
@@ -783,7 +836,7 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
 
 cudaError_t launch_pair(const MxParams &P, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  const size_t smem = (size_t)kMaxStages * kPairStage + 1024;
+  const size_t smem = (size_t)kMaxStages * kPairStage + 8 * kPanel + 1024;
   const cudaError_t attr = allow_smem(k_mx, smem, ready);
   if (attr != cudaSuccess) return attr;
   return launch_pdl(k_mx, dim3(2 * std::min(num_sms / 2, P.tiles_m * P.tiles_n)), dim3(kThreads), smem, s, P);
