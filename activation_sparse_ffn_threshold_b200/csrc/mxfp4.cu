@@ -14,7 +14,7 @@
 // Product: Y = (Xq 2^ex) . (Wq 2^ew)^T with tcgen05's block-scaled MMA (kind::mxf4, K = 64 an
 // instruction, four times the 16-bit rate), fp32 accumulators.  At that rate a 256 x 256 x 256
 // step of a CTA pair takes 512 cycles; the six copies of its scales into tensor memory take
-// their turn in the same pipe and add about 300 (4096 x 28672 x 8192: 474 us, 4.1 PFLOP/s;
+// their turn in the same pipe and add about 300 (4096 x 28672 x 8192: about 470 us, 4.1 PFLOP/s;
 // 337 with the copies left out).  Issuing them a step ahead (499 us) or writing the scales
 // from registers by four warps of their own (760 us) measured slower.
 #include <algorithm>
@@ -152,11 +152,11 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 // ---------------------------------------------------------------- the product
 constexpr int kThreads = 320;
-constexpr int kMaxStages = 5;
+constexpr int kMaxStages = 6;
 constexpr int kTmem = 512;
 constexpr int kAcc = 0, kSf = 256;      // tensor-memory columns: accumulators, scale slots
 constexpr int kSfSlot = 32;             // of a stage: A 2 x 4 columns, B 2 x 8 from column 8 on
-constexpr uint32_t kPairStage = 16384 + 16384 + 1024 + 2048 + 1024;  // A, B, their scales (a multiple of 1024)
+constexpr uint32_t kPairStage = 16384 + 16384 + 1024 + 2048;  // A, B, their scales (a multiple of 1024)
 
 struct alignas(64) MxParams {
   CUtensorMap a, b, sa, sb;
@@ -213,33 +213,34 @@ __device__ __forceinline__ TilePos tile_pos(int t, int tiles_m, int tiles_n) {  
   return {band * kBand + r % rows, r / rows};
 }
 
-// 128 bytes (of E-byte values) of each of a warp's rows: a lane holds its row's (w), the warp
-// stores them through a 4 KB panel of shared memory with 8 lanes of 16 bytes to a row, or,
+// 64 bytes (of E-byte values) of each of a warp's rows: a lane holds its row's (w), the warp
+// stores them through a 2 KB panel of shared memory with 4 lanes of 16 bytes to a row, or,
 // where rows do not start on 16 bytes, value by value along the row (a lane storing its own
-// row touches 32 lines an instruction: 2508 x 9175 x 480 took 241 us).  `left`: columns that
-// exist from the first on.
-constexpr uint32_t kPanel = 4096;
+// row touches 32 lines an instruction: 2508 x 9175 x 480 took 241 us, now 32).  `left`:
+// columns that exist from the first on.
+constexpr uint32_t kPanel = 2048;
 template <int E>
-__device__ __forceinline__ void panel_store(uint32_t panel, const uint32_t w[32], unsigned char *base, int64_t ld, int rows,
+__device__ __forceinline__ void panel_store(uint32_t panel, const uint32_t w[16], unsigned char *base, int64_t ld, int rows,
                                             int left, int vec) {
   const int lane = threadIdx.x & 31;
-  constexpr int COLS = 128 / E;
+  constexpr int COLS = 64 / E;
   if (left <= 0) return;  // (the whole warp)
+  auto at = [&](int row, int piece) { return panel + (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4)); };
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(panel + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4))),
-                 "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+  for (int j = 0; j < 4; ++j)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at(lane, j)), "r"(w[4 * j]), "r"(w[4 * j + 1]),
+                 "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
                  : "memory");
   __syncwarp();
   if (vec) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = i * 4 + (lane >> 3), piece = lane & 7;
+    for (int i = 0; i < 4; ++i) {
+      const int row = i * 8 + (lane >> 2), piece = lane & 3;
       uint4 q;
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                   : "r"(panel + (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)))
+                   : "r"(at(row, piece))
                    : "memory");
       if (row >= rows) continue;
       unsigned char *o = base + row * ld + piece * 16;
@@ -252,29 +253,28 @@ __device__ __forceinline__ void panel_store(uint32_t panel, const uint32_t w[32]
         for (int j = 0; j < 16 / E; ++j)
           if (j < have) {
             if (E == 4)
-              reinterpret_cast<uint32_t *>(o)[j] = a[j];
+              reinterpret_cast<uint32_t *>(o)[j] = a[j & 3];
             else
               reinterpret_cast<uint16_t *>(o)[j] = (uint16_t)(a[(j >> 1) & 3] >> (16 * (j & 1)));
           }
       }
     }
   } else {
-    const int cols = min(COLS, left);
-#pragma unroll 4
-    for (int row = 0; row < rows; ++row) {
+    // 32 lanes: one row's 32 values, or two rows' 16
+    const int c = lane % COLS, cols = min(COLS, left);
+#pragma unroll 8
+    for (int r = 0; r < 32; r += 32 / COLS) {
+      const int row = r + lane / COLS;
+      const uint32_t p = at(row, c * E >> 4) + (uint32_t)(c * E & 15);
       unsigned char *o = base + row * ld;
-#pragma unroll
-      for (int c = lane; c < COLS; c += 32) {
-        const uint32_t at = panel + (uint32_t)(row * 128 + (((c * E >> 4) ^ (row & 7)) << 4) + (c * E & 15));
-        if (E == 4) {
-          uint32_t v;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-          if (c < cols) reinterpret_cast<uint32_t *>(o)[c] = v;
-        } else {
-          uint16_t v;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
-          if (c < cols) reinterpret_cast<uint16_t *>(o)[c] = v;
-        }
+      if (E == 4) {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
+        if (row < rows && c < cols) reinterpret_cast<uint32_t *>(o)[c] = v;
+      } else {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p) : "memory");
+        if (row < rows && c < cols) reinterpret_cast<uint16_t *>(o)[c] = v;
       }
     }
   }
@@ -288,9 +288,17 @@ __device__ __forceinline__ void panel_store(uint32_t panel, const uint32_t w[32]
 // stage's MMAs have completed.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_mx(const __grid_constant__ MxParams P) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty;
-  __shared__ uint32_t tmem_slot;
-  const uint32_t stage0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  // stages, panels, barriers: all of the SM's shared memory, so none is spent on alignment --
+  // dynamic shared memory alone starts on 1024 bytes (checked: the swizzle needs it)
+  const uint32_t stage0 = smem_u32(smem_raw);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem_raw + kMaxStages * kPairStage + 8 * kPanel);
+  uint64_t *full = bars, *empty = bars + kMaxStages;
+  uint64_t &acc_full = bars[2 * kMaxStages], &acc_empty = bars[2 * kMaxStages + 1];
+  uint32_t &tmem_slot = *reinterpret_cast<uint32_t *>(&bars[2 * kMaxStages + 2]);
+  if (stage0 & 1023u) {
+    if (threadIdx.x == 0) latch_error(P.err, SFNN_ERR_UNSUPPORTED);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
@@ -410,22 +418,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_mx(co
       if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty, 0));
       const int rows = (int)min((int64_t)32, P.M - row0);
       if (rows <= 0 || n0 >= P.N) continue;  // (the whole warp)
-      if (P.out_dtype == SFNN_F32) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          panel_store<4>(panel, v[u], static_cast<unsigned char *>(P.out) + (row0 * P.ldo + n0 + u * 32) * 4, P.ldo * 4, rows,
-                         P.N - (n0 + u * 32), P.vec);
-      } else {
-        const bool bf16 = P.out_dtype == SFNN_BF16;
+      for (int u = 0; u < 4; ++u) {
+        const int c = n0 + u * 32;
+        if (P.out_dtype == SFNN_F32) {
+          unsigned char *o = static_cast<unsigned char *>(P.out) + (row0 * P.ldo + c) * 4;
+          panel_store<4>(panel, v[u], o, P.ldo * 4, rows, P.N - c, P.vec);
+          panel_store<4>(panel, v[u] + 16, o + 64, P.ldo * 4, rows, P.N - c - 16, P.vec);
+        } else {
+          const bool bf16 = P.out_dtype == SFNN_BF16;
+          uint32_t p[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            p[j] = pack16(__uint_as_float(v[2 * h + (j >> 4)][2 * (j & 15)]),
-                          __uint_as_float(v[2 * h + (j >> 4)][2 * (j & 15) + 1]), bf16);
-          panel_store<2>(panel, p, static_cast<unsigned char *>(P.out) + (row0 * P.ldo + n0 + h * 64) * 2, P.ldo * 2, rows,
-                         P.N - (n0 + h * 64), P.vec);
+          for (int j = 0; j < 16; ++j) p[j] = pack16(__uint_as_float(v[u][2 * j]), __uint_as_float(v[u][2 * j + 1]), bf16);
+          panel_store<2>(panel, p, static_cast<unsigned char *>(P.out) + (row0 * P.ldo + c) * 2, P.ldo * 2, rows, P.N - c,
+                         P.vec);
         }
       }
     }
@@ -836,7 +842,7 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
 
 cudaError_t launch_pair(const MxParams &P, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  const size_t smem = (size_t)kMaxStages * kPairStage + 8 * kPanel + 1024;
+  const size_t smem = (size_t)kMaxStages * kPairStage + 8 * kPanel + (2 * kMaxStages + 3) * 8;
   const cudaError_t attr = allow_smem(k_mx, smem, ready);
   if (attr != cudaSuccess) return attr;
   return launch_pdl(k_mx, dim3(2 * std::min(num_sms / 2, P.tiles_m * P.tiles_n)), dim3(kThreads), smem, s, P);
