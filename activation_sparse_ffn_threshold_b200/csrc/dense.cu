@@ -243,11 +243,10 @@ __device__ __forceinline__ void epi_store(const DenseParams &P, const Unit &Q, u
 }
 
 // The pair's tile holds 128 neurons: gate columns 0..127, up columns 128..255.  This
-// warp takes 64 of them from n0 on (one act8 block); `bias` holds n0 + lane's and
-// n0 + 32 + lane's.
-template <bool bf16>
+// warp takes 64 of them from n0 on (one act8 block); its first panel holds their biases.
+template <bool bf16, class Done>
 __device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, uint32_t tgate, int64_t row0, int n0,
-                                          const float bias[2], uint32_t panel) {
+                                          uint32_t panel, Done done) {
   const int lane = threadIdx.x & 31;
   const int rows = (int)min((int64_t)32, Q.M - row0);
   const int cols = (int)min((int64_t)64, Q.ldo - n0);  // writable columns of H (a multiple of 8)
@@ -260,12 +259,18 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, u
     tm_ld32(tgate + 128 + c, b);
     tm_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float g = __uint_as_float(a[i]) + __shfl_sync(0xffffffffu, bias[c >> 5], i);
-      r[c + i] = g < 0.f ? 0.f : g;  // NaN stays NaN
-      u[c + i] = __uint_as_float(b[i]);
+    for (int i = 0; i < 32; i += 4) {
+      const uint4 q = lds16(panel + (uint32_t)(c + i) * 4u);  // biases (zeros without one)
+      const uint32_t bias[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float g = __uint_as_float(a[i + j]) + __uint_as_float(bias[j]);
+        r[c + i + j] = g < 0.f ? 0.f : g;  // NaN stays NaN
+        u[c + i + j] = __uint_as_float(b[i + j]);
+      }
     }
   }
+  done();  // the accumulators are free
   if (rows <= 0 || cols <= 0) return;  // (the whole warp)
   uint4 w[4];
   if (P.save != SFNN_SAVE_NONE) {  // whole blocks: code rows are padded to 64 columns
@@ -624,11 +629,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int64_t row0 = (int64_t)w.pos.m * kTile + rank * 128 + quad * 32;
       const int n0 = EPI == kEpiGated ? w.pos.n * 128 + half * 64 : w.pos.n * kTile + half * 128;
       // what the epilogue reads besides the accumulators, requested before they are there
-      float bias[2] = {0.f, 0.f};
       float2 scales;
-      if (EPI == kEpiGated && P.bias) {
-        if (n0 + lane < w.N) bias[0] = load16(P.bias, n0 + lane, BF16);
-        if (n0 + 32 + lane < w.N) bias[1] = load16(P.bias, n0 + 32 + lane, BF16);
+      if (EPI == kEpiGated) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          const float b = P.bias && n0 + c + lane < w.N ? load16(P.bias, n0 + c + lane, BF16) : 0.f;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(panel + (uint32_t)(c + lane) * 4u), "f"(b) : "memory");
+        }
       }
       if (kDGated) saved_request<EPI == kEpiDGated8>(P, w, row0, n0, panel + 2 * kPanel, scales);
       if (!__all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((n >> 1) & 1)))) {
@@ -638,15 +646,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       tm_fence_after();
       const uint32_t acc = tmem + lanes + (uint32_t)buf * 256u;
-      if (EPI == kEpiGated)
-        epi_gated<BF16>(P, w, acc + half * 64, row0, n0, bias, panel);
-      else if (kDGated)
-        epi_dgated<EPI == kEpiDGated8, BF16>(P, w, acc + half * 128, row0, n0, scales, panel);
-      else
-        epi_store<BF16>(P, w, acc + half * 128, row0, n0, panel);
-      tm_fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+      auto done = [&] {
+        tm_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster_relaxed(cluster_addr(&acc_empty[buf], 0));
+      };
+      if (EPI == kEpiGated) {
+        epi_gated<BF16>(P, w, acc + half * 64, row0, n0, panel, done);
+      } else {
+        if (kDGated)
+          epi_dgated<EPI == kEpiDGated8, BF16>(P, w, acc + half * 128, row0, n0, scales, panel);
+        else
+          epi_store<BF16>(P, w, acc + half * 128, row0, n0, panel);
+        done();
+      }
     }
     if (kDGated) cp_async_wait<0>();
   }

@@ -415,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_mx(co
       tm_wait_ld();
       tm_fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty, 0));
+      if (lane == 0) bar_arrive_cluster_relaxed(cluster_addr(&acc_empty, 0));
       const int rows = (int)min((int64_t)32, P.M - row0);
       if (rows <= 0 || n0 >= P.N) continue;  // (the whole warp)
 #pragma unroll
@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
       finish(t, 0, P.T, nullptr);
       tm_fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty, 0));
+      if (lane == 0) bar_arrive_cluster_relaxed(cluster_addr(&acc_empty, 0));
     }
   }
   __syncwarp();

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
       if (busy) epilogue(t, bias, nullptr);
       tm_fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty, 0));
+      if (lane == 0) bar_arrive_cluster_relaxed(cluster_addr(&acc_empty, 0));
     }
   }
   __syncwarp();
