@@ -362,3 +362,106 @@ def test_prompt_through_a_handle(act, d, n):
             hq.forward_prompt(X)
         assert e.value.status == sf.STATUS_CODES["SFNN_ERR_UNSUPPORTED"]
         hq.close()
+
+
+def test_autograd_captured_in_a_graph():
+    """Forward and torch.autograd.grad captured together, as a training loop would."""
+    x, wg, wu, wd, b, dy = layer(48, 64, 128, torch.bfloat16, seed=9)
+    leaves = [t.clone().requires_grad_() for t in (x, wg, wu, wd, b)]
+    want = [t.clone() for t in torch.autograd.grad(sf.gated_ffn(*leaves, checkpoint="act8"), leaves, dy)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            torch.autograd.grad(sf.gated_ffn(*leaves, checkpoint="act8"), leaves, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        grads = torch.autograd.grad(sf.gated_ffn(*leaves, checkpoint="act8"), leaves, dy)
+    for _ in range(2):
+        for t in grads:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, c in zip(grads, want):
+            assert torch.equal(a, c)
+    assert sf.dense_error() == 0
+
+
+def test_offsets_beyond_32_bits():
+    """Hidden layers of more than 2^31 elements; checked at tokens and neurons at both ends."""
+    T, d, n, dt = 70001, 64, 32768, torch.bfloat16
+    assert T * n > 2 ** 31
+    x, wg, wu, wd, b, dy = layer(T, d, n, dt, seed=10)
+    y, saved = sf.gated_ffn_forward(x, wg, wu, wd, b, save="full")
+    rows = torch.tensor([0, 1, 35000, T - 257, T - 2, T - 1], device="cuda")
+    G, U, H = forward64(x[rows], wg, wu, wd, b)
+    near(y[rows], H @ wd.double().t(), H.abs() @ wd.double().abs().t(), dt, 1, n)
+    dx, dwg, dwu, dwd, db = sf.gated_ffn_backward(dy, saved, wg, wu, wd)
+    del saved
+    on = (G > 0).double()
+    (wdx, *_), (tdx, *_) = backward64(x[rows], wg, wu, wd, dy[rows], G * on, U, on)
+    near(dx[rows], wdx, 1.02 * tdx, dt, 1, 2 * n + d)
+    cols = torch.tensor([0, 77, n // 2, n - 65, n - 1], device="cuda")
+    Gc, Uc, Hc = forward64(x, wg[cols], wu[cols], wd[:, cols], b[cols])
+    onc = (Gc > 0).double()
+    want, terms = backward64(x, wg[cols], wu[cols], wd[:, cols], dy, Gc * onc, Uc, onc)
+    near(dwg[cols], want[1], 1.02 * terms[1], dt, 1, T + d)
+    near(dwu[cols], want[2], 1.02 * terms[2], dt, 1, T + d)
+    near(dwd[:, cols], want[3], 1.02 * terms[3], dt, 1, T + d)
+    near(db[cols], want[4], 1.02 * terms[4], dt, 1, T + d)
+    del dx, dwg, dwu, dwd, db, y
+    C = 32768
+    big = torch.zeros(T, C, dtype=dt, device="cuda")
+    big[rows] = torch.randn(6, C, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(dt)
+    q = sf.quantize_act8(big)
+    few = sf.dequantize_act8(sf.quantize_act8(big[rows].contiguous()))
+    out = sf.dequantize_act8(q)
+    assert torch.equal(out[rows], few) and int((out != 0).any(1).sum()) == 6
+    assert sf.dense_error() == 0
+
+
+def test_refusals():
+    x, wg, wu, wd, b, dy = layer(16, 64, 128, torch.float16, seed=11)
+    ok = lambda **k: sf.gated_ffn_forward(*[k.get(n, t) for n, t in
+                                            (("x", x), ("wg", wg), ("wu", wu), ("wd", wd), ("b", b))])
+    ok()
+    for err, k in ((TypeError, dict(x=x.float())), (TypeError, dict(wg=wg.bfloat16())), (TypeError, dict(wd=wd.cpu())),
+                   (ValueError, dict(x=x[:, :56])), (ValueError, dict(wu=wu[:64])), (ValueError, dict(wd=wd.t())),
+                   (ValueError, dict(b=b[:64])), (ValueError, dict(b=b.float())), (ValueError, dict(x=x.t())),
+                   (ValueError, dict(x=x[:1].expand(16, 64))),
+                   (ValueError, dict(x=torch.zeros(16 * 64 + 4, dtype=x.dtype, device="cuda")[4:].view(16, 64))),
+                   (ValueError, dict(wg=torch.zeros(128, 68, dtype=x.dtype, device="cuda")[:, 4:]))):
+        with pytest.raises(err):
+            ok(**k)
+    with pytest.raises(ValueError):  # widths in steps of 8
+        sf.gated_ffn_forward(x[:, :60].contiguous(), wg[:, :60].contiguous(), wu[:, :60].contiguous(), wd[:60].contiguous())
+    _, saved = sf.gated_ffn_forward(x, wg, wu, wd, b, save="full")
+    with pytest.raises(ValueError):
+        sf.gated_ffn_backward(dy[:8], saved, wg, wu, wd)
+    with pytest.raises(TypeError):
+        sf.gated_ffn_backward(dy.float(), saved, wg, wu, wd)
+    w = x.clone().requires_grad_()
+    y = sf.gated_ffn(w * 1, wg, wu, wd, b)
+    with torch.no_grad():
+        q = sf.quantize_mxfp4(wg)
+    with pytest.raises(ValueError):
+        sf.mxfp4_linear(x[:, :32], q)
+    with pytest.raises(ValueError):
+        sf.quantize_mxfp4(x[:, :48].contiguous())
+    with pytest.raises(TypeError):
+        sf.mxfp4_linear(x, q, out_dtype=torch.float64)
+    with pytest.raises(ValueError):
+        sf.dequantize_act8(sf.quantize_act8(x), out=torch.empty(16, 63, dtype=x.dtype, device="cuda"))
+    y.sum().backward()
+    assert w.grad is not None and sf.dense_error() == 0
+
+
+def test_a_weight_changed_between_the_passes_is_noticed():
+    x, wg, wu, wd, b, dy = layer(16, 64, 128, torch.float16, seed=12)
+    wg = wg.requires_grad_()
+    y = sf.gated_ffn(x, wg, wu, wd, b)
+    with torch.no_grad():
+        wg.mul_(2.0)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y, wg, dy)

@@ -150,3 +150,16 @@ def test_graph_and_streams():
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[k]) for k, y in outs)
     assert sf.dense_error() == 0
+
+
+def test_outputs_beyond_32_bits():
+    T, N, K = 70001, 32768, 64
+    x, w = data(T, K, torch.bfloat16, 11), data(N, K, torch.bfloat16, 12)
+    wq = sf.quantize_mxfp4(w)
+    y = sf.mxfp4_linear(x, wq)
+    rows = torch.tensor([0, 255, 40000, T - 130, T - 1], device="cuda")
+    want = values64(x[rows]) @ values64(w).t()
+    # half a step of bf16 is 2^-8 of the value (165.5 may go to 166: its neighbours are 1 apart)
+    tol = torch.finfo(torch.bfloat16).eps / 2 * want.abs() + K * 2.0 ** -23 * (values64(x[rows]).abs() @ values64(w).abs().t()) + 1e-30
+    assert ((y[rows].double() - want).abs() <= tol).all()
+    assert sf.dense_error() == 0
