@@ -882,7 +882,7 @@ cudaError_t launch_few(FewParams &P, int num_sms, cudaStream_t s) {
   attrs[1].val.clusterDim.y = 1;
   attrs[1].val.clusterDim.z = 1;
   cfg.attrs = attrs;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = P.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k_mx_few, P);
 }
 

@@ -302,7 +302,7 @@ cudaError_t launch(SlimParams &P, int grid, size_t smem, cudaStream_t s) {
   attrs[1].val.clusterDim.y = 1;
   attrs[1].val.clusterDim.z = 1;
   cfg.attrs = attrs;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = P.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k_slim<GATED>, P);
 }
 
