@@ -42,17 +42,19 @@ struct alignas(64) SlimParams {
   int32_t *err;
 };
 
-// This thread's weight row: its accumulators of tokens [t0, t0 + 32) -> out[t][col].
-__device__ __forceinline__ void store_tokens(const SlimParams &P, int col, int t0, const float v[32]) {
+// This thread's weight row: its accumulators of tokens [t0, t0 + 8) -> out[t][col].  (The
+// epilogues go by eight tokens in a loop: unrolled further, a single token's few instructions
+// lie far apart, and each first fetch of them is a microsecond at the kernel's end.)
+__device__ __forceinline__ void store_tokens(const SlimParams &P, int col, int t0, const float v[8]) {
   if (P.out32) {
     float *o = static_cast<float *>(P.out) + t0 * P.ldo + col;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < 8; ++i)
       if (t0 + i < P.T) o[i * P.ldo] = v[i];
   } else {
     uint16_t *o = static_cast<uint16_t *>(P.out) + t0 * P.ldo + col;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < 8; ++i)
       if (t0 + i < P.T) o[i * P.ldo] = (uint16_t)pack16(v[i], 0.f, P.bf16);
   }
 }
@@ -78,6 +80,16 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
   const int k_lo = (int)((int64_t)part * P.nk / split), k_hi = (int)((int64_t)(part + 1) * P.nk / split);
   const int steps = (k_hi - k_lo + P.kps - 1) / P.kps;
 
+  const int pre = P.early && unit < P.tiles ? min(stages, steps) : 0;  // stages of weights requested ahead
+  auto load_w = [&](int s, int t, int k0, int kn) {
+    const uint32_t at = stage0 + (uint32_t)s * stage_bytes + x_bytes;
+    for (int c = 0; c < kn; ++c) tma_load_2d(at + (uint32_t)c * chunk_bytes, &P.w0, (k0 + c) * 64, t * P.nb, &full[s]);
+    if (GATED)
+      for (int c = 0; c < kn; ++c)
+        tma_load_2d(at + w_bytes + (uint32_t)c * chunk_bytes, &P.w1, (k0 + c) * 64, t * P.nb, &full[s]);
+  };
+  // rows of a box past T or N read as zeros and count like the others
+  const uint32_t chunk_tx = x_bytes + NP * (uint32_t)P.nb * 128u;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       bar_init(&full[s], 1);
@@ -87,7 +99,15 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
     bar_init(&acc_empty, 4);
     bar_init(&parts_in, 4u * (uint32_t)(split > 1 ? split - 1 : 1));
     bar_init_fence();
+    fence_async_shared();
+    // the first weights, before the rest of the CTA is set up
+    for (int i = 0; i < pre; ++i) {
+      const int k0 = k_lo + i * P.kps, kn = min(P.kps, k_hi - k0);
+      bar_expect_tx(&full[i], chunk_tx * (uint32_t)kn);
+      load_w(i, unit, k0, kn);
+    }
   }
+  __syncwarp();
   if (split > 1) cluster_sync_all();  // rank 0's barrier is there before a part arrives
   if (warp == 1) tm_alloc<1>(&tmem_slot, (uint32_t)P.tmem_cols);
   tm_fence_before();
@@ -97,25 +117,10 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
 
   if (warp == 0) {
     if (lane == 0) {
-      auto load_w = [&](int s, int t, int k0, int kn) {
-        const uint32_t at = stage0 + (uint32_t)s * stage_bytes + x_bytes;
-        for (int c = 0; c < kn; ++c) tma_load_2d(at + (uint32_t)c * chunk_bytes, &P.w0, (k0 + c) * 64, t * P.nb, &full[s]);
-        if (GATED)
-          for (int c = 0; c < kn; ++c)
-            tma_load_2d(at + w_bytes + (uint32_t)c * chunk_bytes, &P.w1, (k0 + c) * 64, t * P.nb, &full[s]);
-      };
       auto load_x = [&](int s, int k0, int kn) {
         const uint32_t st = stage0 + (uint32_t)s * stage_bytes;
         for (int c = 0; c < kn; ++c) tma_load_2d(st + (uint32_t)c * chunk_bytes, &P.x, (k0 + c) * 64, 0, &full[s]);
       };
-      // rows of a box past T or N read as zeros and count like the others
-      const uint32_t chunk_tx = x_bytes + NP * (uint32_t)P.nb * 128u;
-      const int pre = P.early && unit < P.tiles ? min(stages, steps) : 0;
-      for (int i = 0; i < pre; ++i) {
-        const int k0 = k_lo + i * P.kps, kn = min(P.kps, k_hi - k0);
-        bar_expect_tx(&full[i], chunk_tx * (uint32_t)kn);
-        load_w(i, unit, k0, kn);
-      }
       pdl_wait();
       pdl_launch_dependents();
       int it = 0;
@@ -188,26 +193,28 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
   auto epilogue = [&](int t, float bias, const float *sums) {
     const int col = t * P.nb + row;
     const bool live = row < P.nb && col < P.N;
-    for (int c = 0; c < P.T; c += 32) {
-      uint32_t g[32], u[32];
-      float v[32];
+#pragma unroll 1
+    for (int c = 0; c < P.T; c += 8) {
+      uint32_t g[8], u[8];
+      float v[8];
       __syncwarp();
-      tm_ld32(lanes + c, g);
-      if (GATED) tm_ld32(lanes + (uint32_t)P.up_col + c, u);
+      tm_ld8(lanes + c, g);
+      if (GATED) tm_ld8(lanes + (uint32_t)P.up_col + c, u);
       tm_wait_ld();
       if (!live) continue;
       if (sums)
+#pragma unroll 1
         for (int p = 0; p < split - 1; ++p) {
           const float *a = sums + ((size_t)(p * NP) * P.T + c) * 128 + row;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
+          for (int i = 0; i < 8; ++i)
             if (c + i < P.T) {
               g[i] = __float_as_uint(__uint_as_float(g[i]) + a[i * 128]);
               if (GATED) u[i] = __float_as_uint(__uint_as_float(u[i]) + a[(P.T + i) * 128]);
             }
         }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < 8; ++i) {
         v[i] = __uint_as_float(g[i]);
         if (GATED || P.relu) {
           v[i] += bias;
@@ -249,19 +256,19 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
       if (busy)
 #pragma unroll 1
         for (int p = 0; p < NP; ++p)
-          for (int c = 0; c < P.T; c += 32) {
-            uint32_t g[32];
+#pragma unroll 1
+          for (int c = 0; c < P.T; c += 8) {
+            uint32_t g[8];
             __syncwarp();
-            tm_ld32(lanes + (uint32_t)(p * P.up_col + c), g);
+            tm_ld8(lanes + (uint32_t)(p * P.up_col + c), g);
             tm_wait_ld();
             const uint32_t dst = dst0 + (uint32_t)(p * P.T + c) * 512u;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 8; ++i)
               if (c + i < P.T)
                 asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + (uint32_t)i * 512u), "r"(g[i]) : "memory");
           }
-      asm volatile("fence.acq_rel.cluster;" ::: "memory");
-      __syncwarp();
+      __syncwarp();  // the arrival releases the whole warp's stores
       if (lane == 0) bar_arrive_cluster(cluster_addr(&parts_in, 0));
     }
     if (worker && part == 0) {
