@@ -146,11 +146,40 @@ __device__ __forceinline__ void panel_out(uint32_t panel, const uint4 w[4], unsi
 #pragma unroll
   for (int j = 0; j < 4; ++j) sts16(panel_at(panel, lane, j), w[j]);
   __syncwarp();
+  uint4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = lds16(panel_at(panel, i * 8 + (lane >> 2), lane & 3));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = i * 8 + (lane >> 2), piece = lane & 3;
-    const uint4 v = lds16(panel_at(panel, row, piece));
-    if (row < rows && piece < pieces) *reinterpret_cast<uint4 *>(base + row * ld + piece * 16) = v;
+    if (row < rows && piece < pieces) *reinterpret_cast<uint4 *>(base + row * ld + piece * 16) = v[i];
+  }
+}
+// Two of them at a time, through two panels: half the waits.
+__device__ __forceinline__ void panels_out(uint32_t panel, const uint32_t a[16], unsigned char *pa, const uint32_t b[16],
+                                           unsigned char *pb, int64_t ld, int rows, int pieces) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    sts16(panel_at(panel, lane, j), make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]));
+    sts16(panel_at(panel + kPanel, lane, j), make_uint4(b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]));
+  }
+  __syncwarp();
+  uint4 v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t at = panel_at(panel, i * 8 + (lane >> 2), lane & 3);
+    v[i] = lds16(at);
+    v[4 + i] = lds16(at + kPanel);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (lane >> 2), piece = lane & 3;
+    if (row < rows && piece < pieces) {
+      *reinterpret_cast<uint4 *>(pa + row * ld + piece * 16) = v[i];
+      *reinterpret_cast<uint4 *>(pb + row * ld + piece * 16) = v[4 + i];
+    }
   }
 }
 // The way in: request 64 bytes of each of the warp's rows (zeros where none exist) into a
@@ -397,10 +426,6 @@ struct SavedWords {
     uv.x = (__uint_as_float(__byte_perm(b, 0x4b000000u, lo)) - kZero) * us;
     uv.y = (__uint_as_float(__byte_perm(b, 0x4b000000u, hi)) - kZero) * us;
   }
-  __device__ __forceinline__ void forget() {  // (the widened values of an earlier use)
-#pragma unroll
-    for (int i = 0; i < (CODES8 ? 8 : 16); ++i) asm volatile("" : "+r"(r[i]), "+r"(u[i]));
-  }
 };
 
 // 32 columns of dH: H, dU and dG.
@@ -410,41 +435,24 @@ __device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, ui
   const int lane = threadIdx.x & 31, rows = (int)min((int64_t)32, Q.M - row0), pieces = (Q.N - n0) / 8;
   if (rows <= 0 || pieces <= 0) return;  // (the whole warp)
   const int64_t at = (row0 * Q.ldo + n0) * 2, ld = Q.ldo * 2;
-  uint4 w[4];
+  uint32_t h[16], du[16], dg[16];
   {
-    uint32_t h[16];
+    uint32_t raw[32];
+    __syncwarp();
+    tm_ld32(taddr, raw);
+    tm_wait_ld();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float2 r, u;
       v.get(i, r, u);
+      const float x = __uint_as_float(raw[2 * i]), y = __uint_as_float(raw[2 * i + 1]);
       h[i] = pack16(r.x * u.x, r.y * u.y, bf16);
+      du[i] = pack16(x * r.x, y * r.y, bf16);
+      dg[i] = pack16(r.x > 0.f ? x * u.x : 0.f, r.y > 0.f ? y * u.y : 0.f, bf16);  // rows past M: r = 0
     }
-    words_to(w, h);
   }
-  panel_out(panel, w, static_cast<unsigned char *>(Q.out) + at, ld, rows, pieces);
-  v.forget();
-  uint32_t dg[16];
-  {
-    uint32_t du[16];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t raw[16];
-      __syncwarp();
-      tm_ld16(taddr + 16 * c, raw);
-      tm_wait_ld();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = 8 * c + j;
-        float2 r, u;
-        v.get(i, r, u);
-        const float x = __uint_as_float(raw[2 * j]), y = __uint_as_float(raw[2 * j + 1]);
-        du[i] = pack16(x * r.x, y * r.y, bf16);
-        dg[i] = pack16(r.x > 0.f ? x * u.x : 0.f, r.y > 0.f ? y * u.y : 0.f, bf16);  // rows past M: r = 0
-      }
-    }
-    words_to(w, du);
-  }
-  panel_out(panel + kPanel, w, static_cast<unsigned char *>(P.du) + at, ld, rows, pieces);
+  panels_out(panel, h, static_cast<unsigned char *>(Q.out) + at, du, static_cast<unsigned char *>(P.du) + at, ld, rows, pieces);
+  uint4 w[4];
   words_to(w, dg);
   panel_out(panel, w, static_cast<unsigned char *>(P.dg) + at, ld, rows, pieces);
   if (P.colpart) {  // of dG as it was rounded, which the panel still holds
