@@ -183,6 +183,11 @@ def _vp(t):
     return None if t is None else t.data_ptr()
 
 
+def _like(t):
+    """An uninitialised contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 # ------------------------------------------------------------------ act8
 def _blocks(cols) -> int:
     return (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
@@ -444,7 +449,7 @@ def gated_ffn_forward(x, w_gate, w_up, w_down, b=None, save=None, stream=None):
     _same_device(index, w_gate, w_up, w_down, b)
     lib = load_library()
     with _on(index, stream):
-        y = x.new_empty(x.shape)
+        y = _like(x)
         saved = csaved = None
         if save is not None:
             saved = GatedSaved(save, x, T, d, n, b is not None)
@@ -475,11 +480,11 @@ def gated_ffn_backward(dy, saved: GatedSaved, w_gate, w_up, w_down, need=(True, 
     _same_device(index, w_gate, w_up, w_down, saved._r.buf)
     lib = load_library()
     with _on(index, stream):
-        dx = dy.new_empty(dy.shape) if need[0] else None
-        dwg = dy.new_empty((n, d)) if need[1] else None
-        dwu = dy.new_empty((n, d)) if need[2] else None
-        dwd = dy.new_empty((d, n)) if need[3] else None
-        db = dy.new_empty((n,)) if need[4] and saved.has_b else None
+        dx = _like(dy) if need[0] else None
+        dwg = _like(w_gate) if need[1] else None
+        dwu = _like(w_up) if need[2] else None
+        dwd = _like(w_down) if need[3] else None
+        db = dy.new_empty(n) if need[4] and saved.has_b else None
         nbytes = lib.sfnn_gated_workspace(T, d, n, 1)
         ws = dy.new_empty(max(16, nbytes), dtype=torch.uint8)
         q = _GatedDesc(T, d, n, _code(dt), 0, 0, px, ldx, *wf, None)
