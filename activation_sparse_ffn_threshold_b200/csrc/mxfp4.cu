@@ -823,7 +823,10 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
         __syncwarp();  // the arrival releases the whole warp's stores
         if (lane == 0) bar_arrive_cluster(cluster_addr(&parts_in, (uint32_t)q));
       }
-      // (every CTA waits for all that is written to it, so none leaves too early)
+    }
+    __syncwarp();
+    cluster_arrive();  // this CTA writes to no other any more
+    if (worker) {
       if (!__all_sync(0xffffffffu, bar_wait(&parts_in, 0))) {
         if (lane == 0) latch_error(P.err, kErrTimeout);
       } else if (good && unit < P.tiles) {
@@ -833,6 +836,7 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
       }
     }
     __syncwarp();
+    cluster_wait();  // nor does another write to this one
   }
   tm_fence_before();
   __syncthreads();

@@ -271,6 +271,8 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
       __syncwarp();  // the arrival releases the whole warp's stores
       if (lane == 0) bar_arrive_cluster(cluster_addr(&parts_in, 0));
     }
+    __syncwarp();
+    cluster_arrive();  // this CTA writes to no other any more
     if (worker && part == 0) {
       const float bias = load_bias(unit);
       if (!__all_sync(0xffffffffu, bar_wait(&parts_in, 0))) {
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
       }
     }
     __syncwarp();
-    if (!P.apart) cluster_sync_all();
+    cluster_wait();  // nor does another write to this one
   }
   tm_fence_before();
   __syncthreads();

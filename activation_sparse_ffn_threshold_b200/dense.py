@@ -4,7 +4,8 @@ As the rest of the binding, this module only checks and marshals arguments into
 ``libsfnn.so`` (include/sfnn.h); PyTorch provides memory, streams and the autograd graph.
 Tensors are fp16 or bf16 on one CUDA device; results belong to the current stream (or to
 ``stream``, which the call then runs on).  A bounded device-side wait that runs out is
-latched per device and returned by ``dense_error``.
+latched per device and returned by ``dense_error``; the word it is latched in is allocated
+by a device's first call, which must not be inside a graph capture.
 """
 from __future__ import annotations
 

@@ -486,7 +486,7 @@ typedef struct {
     int64_t lds_x;
 } sfnn_gated_saved;
 
-/* Workspace bytes of one call (negative: bad sizes). */
+/* Workspace bytes of one call on the current device (negative: bad sizes). */
 SFNN_API int64_t sfnn_gated_workspace(int32_t T, int32_t d, int32_t n, int32_t backward);
 
 /* Y [T x d], ldy elements apart, in q->dtype or SFNN_F32; saved (may be NULL) is filled as
