@@ -65,7 +65,9 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 int64_t hidden_bytes(int64_t T, int64_t n) { return up(T * up(n, 8) * 2, 256); }
 
 bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool mat_ok(const void *p, int64_t ld, int64_t cols) { return p && a16(p) && ld >= cols && ld % 8 == 0 && ld <= (1ll << 36); }
+bool mat_ok(const void *p, int64_t ld, int64_t cols) {
+  return p && a16(p) && ld >= cols && ld % 8 == 0 && ld <= (1ll << 36);
+}
 
 sfnn_status check(const sfnn_gated_desc *q) {
   if (!q || q->T < 0 || q->d < 1 || q->n < 1) return SFNN_ERR_INVALID_ARG;
@@ -184,7 +186,8 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
   if (kind != SFNN_SAVE_NONE && (st = check_saved(q, sv)) != SFNN_OK) return st;
   if (y_dtype != q->dtype && y_dtype != SFNN_F32) return SFNN_ERR_INVALID_ARG;
   if (q->T == 0) return SFNN_OK;
-  if (!mat_ok(y, y_dtype == SFNN_F32 ? ldy * 2 : ldy, q->d) || ldy < q->d || !err || !ws || !a16(ws) || ws_bytes < sfnn_gated_workspace(q->T, q->d, q->n, 0))
+  if (!mat_ok(y, y_dtype == SFNN_F32 ? ldy * 2 : ldy, q->d) || ldy < q->d || !err || !ws || !a16(ws) ||
+      ws_bytes < sfnn_gated_workspace(q->T, q->d, q->n, 0))
     return SFNN_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int bf16 = q->dtype == SFNN_BF16;
