@@ -261,7 +261,7 @@ def quantize_act8(x, relu: bool = False, stream=None) -> Act8:
         pc, ldq, ps, lds = q.pointers()
         _check(load_library().sfnn_act8_quantize(p, ld, T, cols, code, 1 if relu else 0, pc, ldq, ps, lds,
                                                  _raw_stream(index)), "sfnn_act8_quantize")
-    return Act8(q, x.shape, x.dtype, bool(relu))
+    return Act8(q, tuple(x.shape), x.dtype, bool(relu))
 
 
 def dequantize_act8(q: Act8, dtype=None, out=None, stream=None):
@@ -277,7 +277,7 @@ def dequantize_act8(q: Act8, dtype=None, out=None, stream=None):
             out = buf.new_empty(q.shape, dtype=dtype)
             ld = cols
         else:
-            if out.dtype != dtype or out.shape != q.shape or out.get_device() != index:
+            if out.dtype != dtype or tuple(out.shape) != q.shape or out.get_device() != index:
                 raise ValueError(f"out must be a {dtype} tensor of shape {tuple(q.shape)} on {buf.device}")
             _, _, _, ld = _rows(out, "out", cols)
             if ld < cols:
@@ -385,35 +385,42 @@ class GatedSaved:
     """What gated_ffn_forward keeps for gated_ffn_backward: relu(G) and U as 16-bit blocks and
     X itself ("full"), or everything as 8-bit blocks ("act8"); see sfnn_gated_saved."""
 
-    __slots__ = ("kind", "x", "_r", "_u", "_x", "shape", "dtype", "has_b")
+    __slots__ = ("kind", "x", "_buf", "_c", "_dims", "shape", "dtype", "has_b")
 
     def __init__(self, kind, x, T, d, n, has_b):
         self.kind, self.shape, self.dtype, self.has_b = kind, x.shape, x.dtype, has_b
-        e = 2 if kind == "full" else 1
-        size = (_Planes.size(T, n, e) + 15) // 16 * 16  # each plane on 16 bytes
-        buf = x.new_empty(2 * size + (0 if e == 2 else _Planes.size(T, d, 1)), dtype=torch.uint8)
-        self._r, self._u = _Planes(buf, 0, T, n, e), _Planes(buf, size, T, n, e)
-        self.x, self._x = (x, None) if e == 2 else (None, _Planes(buf, 2 * size, T, d, 1))
+        full = kind == "full"
+        e = 2 if full else 1
+        nb, db = (n + 63) >> 6, (d + 63) >> 6
+        codes, scales = T * nb * 64 * e, T * nb * 4
+        size = (codes + scales + 15) & ~15  # each plane (codes, then scales) on 16 bytes
+        self._buf = buf = x.new_empty(2 * size + (0 if full else T * db * 68), dtype=torch.uint8)
+        p = buf.data_ptr()
+        if full:
+            self.x = x
+            self._c = _GatedSaved(1, 0, p, p + size, nb * 64, p + codes, p + size + codes, nb)
+        else:
+            self.x = None
+            q = p + 2 * size
+            self._c = _GatedSaved(2, 0, p, p + size, nb * 64, p + codes, p + size + codes, nb, q, db * 64,
+                                  q + T * db * 64, db)
+        self._dims = (T, d, n, e, size)
 
-    r = property(lambda self: self._r.codes, doc="codes of relu(G): int16 (the bits of a uint16) or uint8")
-    u = property(lambda self: self._u.codes, doc="codes of U: int16, or uint8 (the bits of an int8)")
-    r_scales = property(lambda self: self._r.scales)
-    u_scales = property(lambda self: self._u.scales)
-    x_codes = property(lambda self: None if self._x is None else self._x.codes)
-    x_scales = property(lambda self: None if self._x is None else self._x.scales)
+    def _planes(self, i):
+        T, d, n, e, size = self._dims
+        return _Planes(self._buf, i * size, T, d if i == 2 else n, 1 if i == 2 else e)
+
+    r = property(lambda self: self._planes(0).codes, doc="codes of relu(G): int16 (the bits of a uint16) or uint8")
+    u = property(lambda self: self._planes(1).codes, doc="codes of U: int16, or uint8 (the bits of an int8)")
+    r_scales = property(lambda self: self._planes(0).scales)
+    u_scales = property(lambda self: self._planes(1).scales)
+    x_codes = property(lambda self: None if self.kind == "full" else self._planes(2).codes)
+    x_scales = property(lambda self: None if self.kind == "full" else self._planes(2).scales)
 
     @property
     def nbytes(self) -> int:
         """Bytes held, X of "full" included."""
-        return self._r.buf.numel() + (0 if self.x is None else self.x.numel() * self.x.element_size())
-
-    def _fill(self):
-        pr, ld, prs, lds = self._r.pointers()
-        pu, _, pus, _ = self._u.pointers()
-        if self._x is None:
-            return _GatedSaved(1, 0, pr, pu, ld, prs, pus, lds)
-        px, ldx, pxs, ldxs = self._x.pointers()
-        return _GatedSaved(2, 0, pr, pu, ld, prs, pus, lds, px, ldx, pxs, ldxs)
+        return self._buf.numel() + (0 if self.x is None else self.x.numel() * self.x.element_size())
 
 
 def _weights(dtype, w_gate, w_up, w_down, d):
@@ -454,7 +461,7 @@ def gated_ffn_forward(x, w_gate, w_up, w_down, b=None, save=None, stream=None):
         saved = csaved = None
         if save is not None:
             saved = GatedSaved(save, x, T, d, n, b is not None)
-            csaved = ctypes.byref(saved._fill())
+            csaved = ctypes.byref(saved._c)
         if T:
             nbytes = lib.sfnn_gated_workspace(T, d, n, 0)
             ws = x.new_empty(nbytes, dtype=torch.uint8)
@@ -472,13 +479,13 @@ def gated_ffn_backward(dy, saved: GatedSaved, w_gate, w_up, w_down, need=(True, 
     pdy, T, _, lddy = _mat(dy, "dy", dt, None, d)
     n, wf = _weights(dt, w_gate, w_up, w_down, d)
     full = saved.kind == "full"
-    if dy.shape != saved.shape or saved._r.nb != _blocks(n):
+    if dy.shape != saved.shape or saved._dims[2] != n:
         raise ValueError("dy and the weights must have the forward pass's shapes")
     px, ldx = None, 0
     if full:
         px, _, _, ldx = _mat(saved.x, "x", dt, T, d)
     index = dy.get_device()
-    _same_device(index, w_gate, w_up, w_down, saved._r.buf)
+    _same_device(index, w_gate, w_up, w_down, saved._buf)
     lib = load_library()
     with _on(index, stream):
         dx = _like(dy) if need[0] else None
@@ -489,7 +496,7 @@ def gated_ffn_backward(dy, saved: GatedSaved, w_gate, w_up, w_down, need=(True, 
         nbytes = lib.sfnn_gated_workspace(T, d, n, 1)
         ws = dy.new_empty(max(16, nbytes), dtype=torch.uint8)
         q = _GatedDesc(T, d, n, _code(dt), 0, 0, px, ldx, *wf, None)
-        _check(lib.sfnn_gated_backward(ctypes.byref(q), pdy, lddy, ctypes.byref(saved._fill()), _vp(dx), _vp(dwg),
+        _check(lib.sfnn_gated_backward(ctypes.byref(q), pdy, lddy, ctypes.byref(saved._c), _vp(dx), _vp(dwg),
                                        _vp(dwu), _vp(dwd), _vp(db), ws.data_ptr(), max(16, nbytes), _err_ptr(index),
                                        _raw_stream(index)), "sfnn_gated_backward")
     return dx, dwg, dwu, dwd, db
