@@ -227,7 +227,7 @@ __device__ __forceinline__ void pack32(uint4 w[4], const float v[32], bool bf16)
 // Each thread owns one row of the tile (its tensor-memory lane) and a half of the tile's
 // columns; a warp owns 32 rows from `row0` on and stores them through its `panel`s.
 
-template <bool bf16>
+template <bool bf16, int width>
 __device__ __forceinline__ void epi_store(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
                                           uint32_t panel) {
   const bool parts = Q.split > 1;
@@ -239,7 +239,7 @@ __device__ __forceinline__ void epi_store(const DenseParams &P, const Unit &Q, u
   unsigned char *base = parts ? reinterpret_cast<unsigned char *>(Q.parts) + ((int64_t)Q.part * Q.M + row0) * ld
                               : static_cast<unsigned char *>(Q.out) + row0 * ld;
 #pragma unroll 1
-  for (int c = 0; c < 128; c += 32) {
+  for (int c = 0; c < width; c += 32) {
     const int cols = end - (n0 + c);
     if (rows <= 0 || cols <= 0) break;  // (the whole warp)
     uint32_t raw[32];
@@ -468,13 +468,13 @@ __device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, ui
   }
 }
 
-// 128 columns of dH from n0 on; the first saved piece has been requested.
-template <bool CODES8, bool bf16>
+// `width` columns of dH from n0 on; the first saved piece has been requested.
+template <bool CODES8, bool bf16, int width>
 __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
                                            float2 scales, uint32_t panel) {
   const uint32_t in = panel + 2 * kPanel;
 #pragma unroll 1
-  for (int c = 0; c < 128; c += 32) {
+  for (int c = 0; c < width; c += 32) {
     const bool first = !CODES8 || (c & 32) == 0, last = !CODES8 || (c & 32);  // of a saved piece
     SavedWords<CODES8> v;
     v.set_scales(scales.x, scales.y);
@@ -485,7 +485,7 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, 
     const int piece = CODES8 && (c & 32) ? 2 : 0;
     panel_row<CODES8 ? 2 : 4>(in, piece, v.r);
     panel_row<CODES8 ? 2 : 4>(in + kPanel, piece, v.u);
-    if (last && c + 32 < 128) {
+    if (last && c + 32 < width) {
       __syncwarp();  // every lane has its row
       saved_request<CODES8>(P, Q, row0, n0 + c + 32, in, scales);
     }
@@ -495,7 +495,7 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, 
 }
 
 // ---------------------------------------------------------------- the kernel
-template <int EPI, bool BF16>
+template <int EPI, bool BF16, int TN>  // TN: columns of a tile
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_dense(const __grid_constant__ DenseParams P) {
   constexpr bool kDGated = EPI == kEpiDGated || EPI == kEpiDGated8;
@@ -540,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const CUtensorMap *a0 = &w.p->a0, *b0 = &w.p->b0, *a1 = &w.p->a1, *b1 = &w.p->b1;
         const int m0 = w.pos.m * kTile + (int)rank * 128;
         // gated: the first CTA loads 128 gate rows, the second the same 128 up rows
-        const int n0 = EPI == kEpiGated ? w.pos.n * 128 : w.pos.n * kTile + (int)rank * 128;
+        const int n0 = EPI == kEpiGated ? w.pos.n * 128 : w.pos.n * TN + (int)rank * (TN / 2);
         for (int kc = w.k_lo; kc < w.k_hi; ++kc, ++it) {
           if (kc == w.k_lo + 1 || w.k_hi == w.k_lo + 1) {  // the next unit, while this one's loads are under way
             id = walk.unit(n + 1);
@@ -551,7 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (rank == 0) bar_expect_tx(&full[s], 2 * kStageBytes);
+          if (rank == 0) bar_expect_tx(&full[s], 2 * 16384u + (uint32_t)TN * 128u);
           const uint32_t bar = cluster_addr(&full[s], 0);
           const uint32_t sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + 16384u;
           const bool second = kc >= w.nk0;
@@ -566,7 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (kDGated || (EPI == kEpiStore && w.b_mn)) {
             tma_load_2d_pair(sb, mb, n0, k0, bar);
-            tma_load_2d_pair(sb + 8192u, mb, n0 + 64, k0, bar);
+            if (TN == 256) tma_load_2d_pair(sb + 8192u, mb, n0 + 64, k0, bar);
           } else {
             tma_load_2d_pair(sb, mb, k0, n0, bar);
           }
@@ -591,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int n = 0; ok && id >= 0; ++n) {
         w = next;
         const int a_mn = EPI == kEpiStore ? w.a_mn : 0, b_mn = EPI == kEpiStore ? w.b_mn : kDGated;
-        const uint32_t idesc = mma_desc_16(256, 256, BF16, a_mn, b_mn);
+        const uint32_t idesc = mma_desc_16(256, TN, BF16, a_mn, b_mn);
         // a 16-deep step of an operand: 2 KB of an MN-major tile, 32 bytes of a K-major one
         const uint32_t step_a = a_mn ? 2048u : 32u, step_b = b_mn ? 2048u : 32u;
         const uint32_t lbo_a = a_mn ? 8192u : 16u, lbo_b = b_mn ? 8192u : 16u;
@@ -641,7 +641,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Unit w = unit_at(P, id);
       const int buf = n & 1;
       const int64_t row0 = (int64_t)w.pos.m * kTile + rank * 128 + quad * 32;
-      const int n0 = EPI == kEpiGated ? w.pos.n * 128 + half * 64 : w.pos.n * kTile + half * 128;
+      constexpr int kWide = TN / 2;  // columns of this warp
+      const int n0 = EPI == kEpiGated ? w.pos.n * 128 + half * 64 : w.pos.n * TN + half * kWide;
       // what the epilogue reads besides the accumulators, requested before they are there
       float2 scales;
       if (EPI == kEpiGated) {
@@ -669,9 +670,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         epi_gated<BF16>(P, w, acc + half * 64, row0, n0, panel, done);
       } else {
         if (kDGated)
-          epi_dgated<EPI == kEpiDGated8, BF16>(P, w, acc + half * 128, row0, n0, scales, panel);
+          epi_dgated<EPI == kEpiDGated8, BF16, kWide>(P, w, acc + half * kWide, row0, n0, scales, panel);
         else
-          epi_store<BF16>(P, w, acc + half * 128, row0, n0, panel);
+          epi_store<BF16, kWide>(P, w, acc + half * kWide, row0, n0, panel);
         done();
       }
     }
@@ -688,17 +689,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int EPI>
 constexpr size_t kSmem = (size_t)kStagesOf<EPI> * kStageBytes + 8 * kWarpPanels<EPI> + 1024;
 
-template <int EPI, bool BF16>
+template <int EPI, bool BF16, int TN>
 cudaError_t run_as(const DenseParams &P, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose kernel attribute is set
-  const cudaError_t attr = allow_smem(k_dense<EPI, BF16>, kSmem<EPI>, ready);
+  const cudaError_t attr = allow_smem(k_dense<EPI, BF16, TN>, kSmem<EPI>, ready);
   if (attr != cudaSuccess) return attr;
   const int grid = 2 * std::min(num_sms / 2, P.first + P.rest);
-  return launch_pdl(k_dense<EPI, BF16>, dim3(grid), dim3(kThreads), kSmem<EPI>, s, P);
+  return launch_pdl(k_dense<EPI, BF16, TN>, dim3(grid), dim3(kThreads), kSmem<EPI>, s, P);
 }
 template <int EPI>
 cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
-  return P.bf16 ? run_as<EPI, true>(P, num_sms, s) : run_as<EPI, false>(P, num_sms, s);
+  if (EPI != kEpiGated && P.p[0].tn == 128) {
+    constexpr int kNarrow = EPI != kEpiGated ? 128 : 256;
+    return P.bf16 ? run_as<EPI, true, kNarrow>(P, num_sms, s) : run_as<EPI, false, kNarrow>(P, num_sms, s);
+  }
+  return P.bf16 ? run_as<EPI, true, 256>(P, num_sms, s) : run_as<EPI, false, 256>(P, num_sms, s);
 }
 
 }  // namespace

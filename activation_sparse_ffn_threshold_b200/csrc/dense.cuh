@@ -100,6 +100,7 @@ struct alignas(64) DenseProblem {
   CUtensorMap a0, b0, a1, b1;
   int M, N;       // rows and columns of C (gated: neurons)
   int nk0, nk;    // K chunks of 64 of the first pair, of both
+  int tn;         // columns of a tile: 256, or 128 (never gated); one launch's problems have the same
   int tiles_m, tiles_n;
   int split;      // parts of K, each a unit of work of its own (kEpiStore)
   int a_mn, b_mn; // the operands' majors

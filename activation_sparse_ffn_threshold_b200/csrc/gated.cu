@@ -108,7 +108,7 @@ bool set_pair(DenseProblem &P, int which, const Operand &a, const Operand &b, in
   return (a.mn ? make_tensor_map(ma, a.p, 2, K, M, a.ld, 64, 64, true)
                : make_tensor_map(ma, a.p, 2, M, K, a.ld, 128, 64, true)) &&
          (b.mn ? make_tensor_map(mb, b.p, 2, K, N, b.ld, 64, 64, true)
-               : make_tensor_map(mb, b.p, 2, N, K, b.ld, 128, 64, true));
+               : make_tensor_map(mb, b.p, 2, N, K, b.ld, P.tn / 2, 64, true));
 }
 int chunks(int64_t K) { return (int)((K + 63) / 64); }
 
@@ -124,13 +124,23 @@ int64_t parts_bytes(int64_t M, int64_t N, int nk, int sms) {
   return p > 1 ? up(p * M * N * 4, 256) : 0;
 }
 
-bool set_problem(DenseProblem &P, const Operand &a, const Operand &b, int M, int N, int64_t K, void *out, int64_t ldo) {
+// Columns of a tile: 128 where that many tiles still fit one round of CTA pairs (a tile's
+// latency counts: step of 257 tokens, 512 x 2048, 46.7 us against 51.8 with 256).  Beyond, 256,
+// even where halves would fill the last round better: they read each operand byte for half
+// the products (4096 tokens, 4096 x 11008, with halves in the down product: 2585 us against 2365).
+int tile_columns(int M, int N, int split, int sms) {
+  return (int64_t)((M + 255) / 256) * ((N + 127) / 128) * split <= sms / 2 ? 128 : 256;
+}
+
+bool set_problem(DenseProblem &P, const Operand &a, const Operand &b, int M, int N, int64_t K, void *out, int64_t ldo,
+                 int split = 1, int tn = 256) {
   P.M = M;
   P.N = N;
   P.nk0 = P.nk = chunks(K);
+  P.tn = tn;
   P.tiles_m = (M + 255) / 256;
-  P.tiles_n = (N + 255) / 256;
-  P.split = 1;
+  P.tiles_n = (N + tn - 1) / tn;
+  P.split = split;
   P.a_mn = a.mn;
   P.b_mn = b.mn;
   P.out = out;
@@ -149,13 +159,11 @@ sfnn_status product(const Operand &a, const Operand &b, int M, int N, int64_t K,
   const int sms = device_sms();
   DenseParams P{};
   P.count = 1;
-  if (!set_problem(P.p[0], a, b, M, N, K, out, ldo)) return SFNN_ERR_CUDA;
+  const int split = parts ? parts_of(M, N, chunks(K), sms) : 1;
+  if (!set_problem(P.p[0], a, b, M, N, K, out, ldo, split, tile_columns(M, N, split, sms))) return SFNN_ERR_CUDA;
   P.p[0].out32 = out32;
   P.p[0].relu = relu_bias != nullptr;
-  if (parts) {
-    P.p[0].split = parts_of(M, N, P.p[0].nk, sms);
-    P.p[0].part = parts;
-  }
+  P.p[0].part = parts;
   P.bias = relu_bias;
   P.bf16 = bf16;
   P.err = err;
@@ -243,6 +251,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
   Q.N = q->n;
   Q.nk0 = Q.nk = chunks(q->d);
   Q.split = 1;
+  Q.tn = 256;  // 128 neurons, gate and up
   Q.tiles_m = (q->T + 255) / 256;
   Q.tiles_n = (q->n + 127) / 128;
   Q.out = ws;
@@ -311,7 +320,8 @@ sfnn_status sfnn_gated_backward(const sfnn_gated_desc *q, const void *dy, int64_
   {
     DenseParams P{};
     P.count = 1;
-    if (!set_problem(P.p[0], Operand{dy, lddy, false}, Operand{q->w_down, q->ld_down, true}, T, n, d, h, ldh))
+    if (!set_problem(P.p[0], Operand{dy, lddy, false}, Operand{q->w_down, q->ld_down, true}, T, n, d, h, ldh, 1,
+                     tile_columns(T, n, 1, sms)))
       return SFNN_ERR_CUDA;
     P.bf16 = bf16;
     P.dg = dg;
