@@ -164,7 +164,7 @@ struct SlimArgs {
   int bf16, out32, relu, early;
   int32_t *err;
 };
-bool slim_serves(int T);
+int64_t slim_cost(int T, int N, int64_t K, bool gated, int num_sms);
 sfnn_status launch_slim(const SlimArgs &q, int num_sms, cudaStream_t s);
 
 // Rows of 16-bit values to act8 blocks and back (act8.cu).  Code rows are ldq bytes apart

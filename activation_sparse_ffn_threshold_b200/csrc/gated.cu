@@ -132,6 +132,24 @@ int tile_columns(int M, int N, int split, int sms) {
   return (int64_t)((M + 255) / 256) * ((N + 127) / 128) * split <= sms / 2 ? 128 : 256;
 }
 
+// Up to 128 tokens, two kernels can form weights [N x K] . x: the slim one, whose tiles have
+// all tokens and an even share of the weight rows, and the square tiles of the dense one.  The
+// dense one's time in the units of slim_cost: rounds of tiles, each SM of a pair reading half of
+// the tile's weight rows and tokens, and 1000 (3 us) for its longer way in and out.  Measured
+// at 33 pairs of sizes from 280 x 2048 to 8192 x 14000 and 4 to 128 tokens, forward passes are
+// 1.5 % on average above the best of the four pairings (both products slim: 17 %, both dense:
+// 15 %).  Both slim / both dense, us, at 64 tokens: 512 x 2048 22.2 / 16.9, 280 x 25376 56.5 /
+// 32.8, 2048 x 8192 43.1 / 36.0, 8192 x 14000 129 / 153; at 4: 12.7 / 16.2, 34.2 / 34.4, 31.7 /
+// 35.5, 115 / 174.
+bool slim_serves(int T, int N, int64_t K, bool gated, int sms) {
+  if (T > 128 || sms < 2) return false;
+  const int split = gated ? 1 : parts_of(T, N, chunks(K), sms);
+  const int rows = gated ? 256 : tile_columns(T, N, split, sms), outs = gated ? 128 : rows;
+  const int64_t units = (int64_t)((N + outs - 1) / outs) * split, pairs = sms / 2;
+  const int64_t dense = (units + pairs - 1) / pairs * (rows + T) / 2 * chunks(K) / split + 1000;
+  return slim_cost(T, N, K, gated, sms) < dense;
+}
+
 bool set_problem(DenseProblem &P, const Operand &a, const Operand &b, int M, int N, int64_t K, void *out, int64_t ldo,
                  int split = 1, int tn = 256) {
   P.M = M;
@@ -204,11 +222,14 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
       launch_act8_quantize(q->x, q->ldx, q->T, q->d, bf16, false, static_cast<uint8_t *>(sv->x), sv->ld_x,
                            sv->x_scales, sv->lds_x, s) != cudaSuccess)
     return SFNN_ERR_CUDA;
-  const bool slim = slim_serves(q->T);
+  const int sms = device_sms();
+  const bool slim_up = kind == SFNN_SAVE_NONE && slim_serves(q->T, q->n, q->d, true, sms);
+  const bool slim_down =
+      q->down_layout == SFNN_DOWN_WIDTH_MAJOR && slim_serves(q->T, q->d, q->n, false, sms);
   float *parts = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + hidden_bytes(q->T, q->n));
   const Operand h{ws, ldh, false}, wd{q->w_down, q->ld_down, q->down_layout == SFNN_DOWN_NEURON_MAJOR};
   auto down = [&](int early) -> sfnn_status {
-    if (!slim || wd.mn) return product(h, wd, q->T, q->d, q->n, y, ldy, y_dtype == SFNN_F32, bf16, parts, err, s);
+    if (!slim_down) return product(h, wd, q->T, q->d, q->n, y, ldy, y_dtype == SFNN_F32, bf16, parts, err, s);
     SlimArgs a{};
     a.x = ws;
     a.ldx = ldh;
@@ -223,9 +244,9 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
     a.out32 = y_dtype == SFNN_F32;
     a.early = early;
     a.err = err;
-    return launch_slim(a, device_sms(), s);
+    return launch_slim(a, sms, s);
   };
-  if (slim && kind == SFNN_SAVE_NONE) {
+  if (slim_up) {
     SlimArgs a{};
     a.x = q->x;
     a.ldx = q->ldx;
@@ -241,7 +262,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
     a.ldo = ldh;
     a.bf16 = bf16;
     a.err = err;
-    if ((st = launch_slim(a, device_sms(), s)) != SFNN_OK) return st;
+    if ((st = launch_slim(a, sms, s)) != SFNN_OK) return st;
     return down(1);
   }
   DenseParams P{};
@@ -272,7 +293,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
     P.lds = sv->lds;
   }
   P.err = err;
-  if (launch_dense(P, kEpiGated, device_sms(), s) != cudaSuccess) return SFNN_ERR_CUDA;
+  if (launch_dense(P, kEpiGated, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
   return down(0);
 }
 

@@ -1,4 +1,5 @@
-// slim.cu -- the dense products for few tokens (T <= 128): bound by the weights' bytes.
+// slim.cu -- the dense products for few tokens (T <= 128) whose time is the weights' bytes (the
+// rule is slim_serves in gated.cu).
 //
 // The weights lie on the MMA's M side (128 lanes), the tokens on its N side.  A tile need not
 // fill the 128 lanes: the rest of the A tile is whatever shared memory holds, and only
@@ -344,9 +345,38 @@ int active_clusters(int split) {
   return n;
 }
 
+struct SlimPlan {
+  int nb, split, rounds;
+};
+// Weight rows of a tile: an even share, at most 128.  A share under 64 rows is widened by
+// splitting K over a cluster (while a part keeps 8 chunks and the parts fit rank 0's memory).
+SlimPlan plan(int T, int N, int64_t K, int np, int sms) {
+  const int nk = (int)((K + 63) / 64);
+  SlimPlan p;
+  p.rounds = (N + sms * 128 - 1) / (sms * 128);
+  p.split = 1;
+  p.nb = (N + sms * p.rounds - 1) / (sms * p.rounds);
+  while (p.rounds == 1 && p.split < 4 && p.nb < 64 && nk >= 16 * p.split && (2 * p.split - 1) * np * T <= 384) {
+    // no more tiles than clusters run at a time: another wave would double the time
+    const int clusters = active_clusters(2 * p.split);
+    if (clusters < 1 || (N + clusters - 1) / clusters > 128) break;
+    p.split *= 2;
+    p.nb = (N + clusters - 1) / clusters;
+  }
+  p.nb = std::max(p.nb, 8);
+  return p;
+}
+
 }  // namespace
 
-bool slim_serves(int T) { return T <= 128; }
+// Time of the kernel in units of 128 bytes read by one SM (2.9 ns at its share of the copy
+// rate): the weight rows and tokens of its tiles times their chunks, and the epilogue, about
+// 15 units a token for each product and part of K (fitted to 330 products of 4 to 128 tokens).
+int64_t slim_cost(int T, int N, int64_t K, bool gated, int sms) {
+  const int np = gated ? 2 : 1;
+  const SlimPlan p = plan(T, N, K, np, sms);
+  return p.rounds * (int64_t)(np * p.nb + T) * ((K + 63) / 64) / p.split + 15 * np * p.split * T;
+}
 
 sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
   const bool gated = q.w1 != nullptr;
@@ -357,19 +387,9 @@ sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
   P.nk = (int)((q.K + 63) / 64);
   P.t8 = up_to(q.T, 8);
   P.t16 = up_to(q.T, 16);
-  // Weight rows of a tile: an even share, at most 128.  A share under 64 rows is widened by
-  // splitting K over a cluster (while a part keeps 8 chunks and the parts fit rank 0's memory).
-  const int rounds = (q.N + sms * 128 - 1) / (sms * 128);
-  P.split = 1;
-  P.nb = (q.N + sms * rounds - 1) / (sms * rounds);
-  while (rounds == 1 && P.split < 4 && P.nb < 64 && P.nk >= 16 * P.split && (2 * P.split - 1) * np * P.T <= 384) {
-    // no more tiles than clusters run at a time: another wave would double the time
-    const int clusters = active_clusters(2 * P.split);
-    if (clusters < 1 || (q.N + clusters - 1) / clusters > 128) break;
-    P.split *= 2;
-    P.nb = (q.N + clusters - 1) / clusters;
-  }
-  P.nb = std::max(P.nb, 8);
+  const SlimPlan shape = plan(q.T, q.N, q.K, np, sms);
+  P.nb = shape.nb;
+  P.split = shape.split;
   P.nb8 = up_to(P.nb, 8);
   P.m64 = P.split == 1 && P.nb <= 64;
   P.tiles = (q.N + P.nb - 1) / P.nb;

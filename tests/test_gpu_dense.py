@@ -85,6 +85,13 @@ def test_forward(T, d, n, dt):
     assert sf.dense_error() == 0
 
 
+@pytest.mark.parametrize("T,d,n", [(60, 9504, 2048), (100, 9504, 2048), (128, 9504, 2048), (100, 304, 25376),
+                                   (48, 8192, 4104), (17, 280, 20312)])
+def test_forward_each_product_in_either_kernel(T, d, n):
+    """Sizes at which up to 128 tokens take the slim kernel for both products, one or neither."""
+    test_forward(T, d, n, torch.float16)
+
+
 def backward64(x, wg, wu, wd, dy, R, U, on):
     x, wg, wu, wd, dy = (t.double() for t in (x, wg, wu, wd, dy))
     dH = dy @ wd
