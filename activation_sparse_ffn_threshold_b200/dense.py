@@ -374,9 +374,10 @@ def mxfp4_linear(x, w: Mxfp4, out_dtype=None, stream=None):
     with _on(index, stream):
         y = x.new_empty(x.shape[:-1] + (N,), dtype=dt)
         nbytes = lib.sfnn_mxfp4_linear_workspace(T, K)
-        ws = x.new_empty(nbytes, dtype=torch.uint8).data_ptr() if nbytes else None
+        ws = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None  # held until the call is queued
         _check(lib.sfnn_mxfp4_linear(p, ld, T, xcode, w.codes.data_ptr(), w.scales.data_ptr(), N, K, y.data_ptr(), N, code,
-                                     ws, nbytes, _err_ptr(index), _raw_stream(index)), "sfnn_mxfp4_linear")
+                                     None if ws is None else ws.data_ptr(), nbytes, _err_ptr(index),
+                                     _raw_stream(index)), "sfnn_mxfp4_linear")
     return y
 
 

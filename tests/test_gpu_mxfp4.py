@@ -6,12 +6,18 @@ fp32 accumulation: at most K 2^-23 of the terms' magnitudes (each of fewer than 
 in blocks, loses at most 2^-23 of the running magnitude when an addend is cut rather than
 rounded).
 """
+import pathlib
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import activation_sparse_ffn_threshold_b200 as sf
 
 pytestmark = pytest.mark.gpu
+
+ROOT = pathlib.Path(__file__).resolve().parent.parent
 
 KINDS = [torch.float16, torch.bfloat16]
 
@@ -163,3 +169,19 @@ def test_outputs_beyond_32_bits():
     tol = torch.finfo(torch.bfloat16).eps / 2 * want.abs() + K * 2.0 ** -23 * (values64(x[rows]).abs() @ values64(w).abs().t()) + 1e-30
     assert ((y[rows].double() - want).abs() <= tol).all()
     assert sf.dense_error() == 0
+
+
+def test_workspace_and_error_word_are_apart_in_a_new_process():
+    """The process's first dense call allocates the error word while the call's workspace lives."""
+    code = """
+import torch
+import activation_sparse_ffn_threshold_b200 as sf
+g = torch.Generator(device="cuda").manual_seed(1)
+w = sf.quantize_mxfp4(torch.randn(64, 256, device="cuda", generator=g).half())
+x = torch.randn(8, 256, device="cuda", generator=g).half()
+for _ in range(3):
+    sf.mxfp4_linear(x, w)
+assert sf.dense_error() == 0, "the error word was written to"
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
