@@ -871,10 +871,14 @@ cudaError_t launch_few(FewParams &P, int num_sms, cudaStream_t s) {
   const int steps = (P.nk + P.split - 1) / P.split;
   P.stages = std::min({kFewStages, steps, (108 * 1024 - (P.apart ? parts : 0)) / stage});
   const int stage_mem = P.stages * stage;
-  const size_t smem = 1024 + (P.apart ? stage_mem + parts : std::max(stage_mem, parts));
   P.acc_cols = (P.t16 + 31) / 32 * 32 + 32;  // read 32 columns at a time, from any token on
   P.tmem_cols = 32;
   while (P.tmem_cols < P.acc_cols + P.stages * kFewSf) P.tmem_cols *= 2;
+  // The SM's share of shared memory that goes with the share of tensor memory (456 bytes a
+  // column, less what the launch adds): CTAs that could not all allocate never share an SM,
+  // or one would wait for columns held by a cluster that waits for it.
+  const size_t smem = std::max<size_t>(1024 + (P.apart ? stage_mem + parts : std::max(stage_mem, parts)),
+                                       P.tmem_cols * 456 - 2048);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(P.split > 1 ? P.tiles * P.split : std::min(P.tiles, 2 * num_sms));
   cfg.blockDim = dim3(kFewThreads);

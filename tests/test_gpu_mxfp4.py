@@ -102,6 +102,20 @@ def test_product(T, N, K, dt):
     assert sf.dense_error() == 0
 
 
+@pytest.mark.parametrize("T,N,K", [(128, 8192, 2048), (128, 4096, 1024), (100, 9400, 2048), (70, 16300, 1056)])
+def test_short_products_that_fill_every_sm(T, N, K):
+    """Few steps leave little shared memory to a CTA: no more of them may share an SM than
+    its tensor memory holds.  Calls in a row, so that each begins while the last one ends."""
+    x, w = data(T, K, torch.float16, 3), data(N, K, torch.float16, 4)
+    qx, qw = sf.quantize_mxfp4(x), sf.quantize_mxfp4(w)
+    want = values64(x) @ values64(w).t()
+    terms = values64(x).abs() @ values64(w).abs().t()
+    got = [sf.mxfp4_matmul(qx, qw, out_dtype=torch.float32) for _ in range(12)]
+    assert ((got[0].double() - want).abs() <= (2.0 ** -24 + K * 2.0 ** -23) * terms).all()
+    assert all(torch.equal(g, got[0]) for g in got)
+    assert sf.dense_error() == 0
+
+
 def test_product_of_views_nan_rows_and_empty():
     x, w = data(40, 128, torch.bfloat16, 1), data(96, 128, torch.bfloat16, 2)
     wq = sf.quantize_mxfp4(w)
