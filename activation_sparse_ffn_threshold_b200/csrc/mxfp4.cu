@@ -280,7 +280,7 @@ __device__ __forceinline__ void panel_store(uint32_t panel, const uint32_t w[16]
   }
 }
 
-// 256 x 256 tiles by CTA pairs, 128 rows of X and of W in each CTA (more than 128 tokens).
+// 256 x 256 tiles by CTA pairs, 128 rows of X and of W in each CTA (more tokens: few_serves).
 //
 // The accumulators are single (256 columns; the scales need the rest of tensor memory): the
 // epilogue warps copy a finished tile to registers, hand the columns back, and store while
@@ -609,13 +609,14 @@ cudaError_t launch_rows(const void *x, int64_t ldx, int T, int vec, int bf16, co
                     static_cast<const uint8_t *>(wsc), N, K, y, ldy, y_dtype);
 }
 
-// ---------------------------------------------------------------- up to 128 tokens
-// The weights on the MMA's M side (128-row tiles, as their scales lie), the tokens on its N
-// side.  Bound by the weights' bytes and, in small layers, by latency: a cluster of 2 or 4
+// ---------------------------------------------------------------- few tokens
+// The weights on the MMA's M side (128-row tiles, as their scales lie), up to 128 tokens on its
+// N side (blockIdx.y: which 128).  Bound by the weights' bytes and, in small layers, by latency: a cluster of 2 or 4
 // CTAs splits a tile's K so that the SMs are filled, each CTA then adds up a share of the
 // tokens: its own accumulators and, in rank order, those the other CTAs put into its shared
 // memory.
 constexpr int kFewThreads = 192;  // warp 0 loads, warp 1 issues the MMAs, warps 2-5 take 32 weight rows each
+constexpr int kFewTokens = 128;  // of a CTA: the rows that a tile of their scales holds
 constexpr int kFewStages = 8;
 constexpr int kFewSf = 16;  // scale columns of a stage: A 2 x 4, B 2 x 4 (128 tokens)
 
@@ -642,6 +643,7 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = P.split, part = split > 1 ? (int)cluster_rank() : 0;
   const int unit = blockIdx.x / split, units = gridDim.x / split;
+  const int group = blockIdx.y, T = min(P.T - group * kFewTokens, kFewTokens);  // this CTA's tokens
   const uint32_t x_bytes = (uint32_t)P.t8 * 128u;
   // w (16 KB), its scales, x, its scales; an MMA may read 1 KB past x's rows, into the scales
   const uint32_t stage_bytes = 16384u + 1024u + x_bytes + 1024u;
@@ -683,8 +685,8 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
           const uint32_t w = stage0 + (uint32_t)s * stage_bytes, x = w + 16384u, sw = x + x_bytes, sx = sw + 1024u;
           tma_load_2d(w, &P.w, k * 128, t * 128, &full[s]);
           tma_load_2d(sw, &P.sw, 0, t * P.nk + k, &full[s]);
-          tma_load_2d(x, &P.x, k * 128, 0, &full[s]);
-          tma_load_2d(sx, &P.sx, 0, k, &full[s]);
+          tma_load_2d(x, &P.x, k * 128, group * kFewTokens, &full[s]);
+          tma_load_2d(sx, &P.sx, 0, group * P.nk + k, &full[s]);
         }
       }
       for (int s = 0; s < stages && ok; ++s) {  // every load has been consumed before the CTA ends
@@ -761,13 +763,13 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
           }
         }
       if (P.out_dtype == SFNN_F32) {
-        float *o = static_cast<float *>(P.out) + c * P.ldo + col;
+        float *o = static_cast<float *>(P.out) + (group * kFewTokens + c) * P.ldo + col;
 #pragma unroll
         for (int i = 0; i < 16; ++i, o += P.ldo)
           if (c + i < t1) *o = v[i];
       } else {
         const bool bf16 = P.out_dtype == SFNN_BF16;
-        uint16_t *o = static_cast<uint16_t *>(P.out) + c * P.ldo + col;
+        uint16_t *o = static_cast<uint16_t *>(P.out) + (group * kFewTokens + c) * P.ldo + col;
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
           const uint32_t w = pack16(v[i], v[i + 1], bf16);
@@ -792,7 +794,7 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
       __syncwarp();
       tm_fence_after();
       if (split > 1) break;  // one tile per cluster
-      finish(t, 0, P.T, nullptr);
+      finish(t, 0, T, nullptr);
       tm_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_cluster_relaxed(cluster_addr(&acc_empty, 0));
@@ -806,7 +808,7 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
     if (worker) {
       for (int k = 1; k < split; ++k) {
         const int q = (part + k) % split;  // each CTA begins with another
-        const int t0 = min(P.T, q * P.share), t1 = min(P.T, t0 + P.share);
+        const int t0 = min(T, q * P.share), t1 = min(T, t0 + P.share);
         const uint32_t dst0 = cluster_addr(smem_raw, (uint32_t)q) + sums +
                               (uint32_t)((part < q ? part : part - 1) * P.share * 512 + row * 16);
         for (int c = t0; c < t1; c += 16) {
@@ -833,8 +835,8 @@ __global__ void __launch_bounds__(kFewThreads) k_mx_few(const __grid_constant__ 
         if (lane == 0) latch_error(P.err, kErrTimeout);
       } else if (good && unit < P.tiles) {
         __syncwarp();
-        const int t0 = min(P.T, part * P.share);
-        finish(unit, t0, min(P.T, t0 + P.share), smem_raw + sums);
+        const int t0 = min(T, part * P.share);
+        finish(unit, t0, min(T, t0 + P.share), smem_raw + sums);
       }
     }
     __syncwarp();
@@ -858,13 +860,14 @@ cudaError_t launch_few(FewParams &P, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   const cudaError_t attr = allow_smem(k_mx_few, 224 * 1024, ready);
   if (attr != cudaSuccess) return attr;
-  P.t8 = (P.T + 7) / 8 * 8;
-  P.t16 = (P.T + 15) / 16 * 16;
+  const int tokens = std::min(P.T, kFewTokens), groups = (P.T + kFewTokens - 1) / kFewTokens;
+  P.t8 = (tokens + 7) / 8 * 8;
+  P.t16 = (tokens + 15) / 16 * 16;
   P.tiles = (P.N + 127) / 128;
   P.split = 1;
   // more CTAs to a tile while they fit two to an SM and each keeps two steps
-  while (P.split < 4 && P.tiles * P.split * 2 <= 2 * num_sms && P.nk >= 4 * P.split) P.split *= 2;
-  P.share = ((P.T + P.split - 1) / P.split + 3) / 4 * 4;
+  while (P.split < 4 && P.tiles * groups * P.split * 2 <= 2 * num_sms && P.nk >= 4 * P.split) P.split *= 2;
+  P.share = ((tokens + P.split - 1) / P.split + 3) / 4 * 4;
   const int stage = 16384 + 1024 + P.t8 * 128 + 1024;
   const int parts = P.split > 1 ? (P.split - 1) * P.share * 512 : 0;
   P.apart = parts <= 16 * 1024;
@@ -880,7 +883,7 @@ cudaError_t launch_few(FewParams &P, int num_sms, cudaStream_t s) {
   const size_t smem = std::max<size_t>(1024 + (P.apart ? stage_mem + parts : std::max(stage_mem, parts)),
                                        P.tmem_cols * 456 - 2048);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(P.split > 1 ? P.tiles * P.split : std::min(P.tiles, 2 * num_sms));
+  cfg.gridDim = dim3(P.split > 1 ? P.tiles * P.split : std::min(P.tiles, std::max(1, 2 * num_sms / groups)), groups);
   cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -920,13 +923,25 @@ cudaError_t quantize(const void *x, int64_t ldx, int64_t R, int K, int32_t dtype
                     static_cast<uint8_t *>(scales));
 }
 
+// More than 128 tokens go to k_mx_few in groups of 128 where k_mx's 256 x 256 tiles leave SMs
+// idle that parts of a long K can fill (256 tokens, 4096 x 11008: 17.5 us against 27.6; 512
+// tokens, 1024 x 14336: 15.8 and 34.1; but 512 tokens, 2048 x 2048, 8 steps: 12.3 and 9.9), or
+// where they take a second round and 128 x 128 tiles only one (384 tokens, 11008 x 4096: 14.5
+// and 23.4; with more tiles than two to an SM, 512 tokens: 25.5 and 23.5).
+bool few_serves(int T, int N, int nk, int sms) {
+  if (T <= kFewTokens) return true;
+  const int64_t units = (int64_t)((T + 127) / 128) * ((N + 127) / 128);
+  const int64_t tiles = (int64_t)((T + 255) / 256) * ((N + 255) / 256);
+  return (units <= sms && nk >= 16) || (units <= 2 * sms && tiles > sms / 2);
+}
+
 sfnn_status product(const void *xc, const void *xs, int T, const void *wc, const void *wsc, int N, int K, void *out,
                     int64_t ldo, int32_t out_dtype, int32_t *err, cudaStream_t s) {
   const int sms = device_sms();
   if (sms < 2) return SFNN_ERR_CUDA;
   const int nk = (K + 255) / 256;
   const int64_t rows_x = mx_rtiles(T) * nk, rows_w = mx_rtiles(N) * nk;
-  if (T <= 128) {
+  if (few_serves(T, N, nk, sms)) {
     FewParams P{};
     P.T = T;
     P.N = N;
@@ -935,7 +950,7 @@ sfnn_status product(const void *xc, const void *xs, int T, const void *wc, const
     P.ldo = ldo;
     P.out_dtype = out_dtype;
     P.err = err;
-    if (!make_tensor_map(&P.x, xc, 1, T, K / 2, K / 2, (T + 7) / 8 * 8, 128, true) ||
+    if (!make_tensor_map(&P.x, xc, 1, T, K / 2, K / 2, std::min((T + 7) / 8 * 8, kFewTokens), 128, true) ||
         !make_tensor_map(&P.w, wc, 1, N, K / 2, K / 2, 128, 128, true) ||
         !make_tensor_map(&P.sx, xs, 4, rows_x, 256, 256, 1, 256, false) ||
         !make_tensor_map(&P.sw, wsc, 4, rows_w, 256, 256, 1, 256, false))

@@ -116,6 +116,13 @@ def test_short_products_that_fill_every_sm(T, N, K):
     assert sf.dense_error() == 0
 
 
+@pytest.mark.parametrize("T,N,K", [(129, 136, 4096), (200, 513, 4128), (300, 1000, 4640), (384, 130, 8192), (511, 264, 5120),
+                                   (1000, 8, 4096), (2000, 1, 4096), (300, 11008, 288), (384, 11007, 96)])
+def test_product_in_groups_of_tokens(T, N, K):
+    """More than 128 tokens by 128: long K split over clusters, and tiles of one round."""
+    test_product(T, N, K, torch.bfloat16)
+
+
 def test_product_of_views_nan_rows_and_empty():
     x, w = data(40, 128, torch.bfloat16, 1), data(96, 128, torch.bfloat16, 2)
     wq = sf.quantize_mxfp4(w)
