@@ -453,7 +453,8 @@ __device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, ui
       const float x = __uint_as_float(raw[2 * i]), y = __uint_as_float(raw[2 * i + 1]);
       h[i] = pack16(r.x * u.x, r.y * u.y, bf16);
       du[i] = pack16(x * r.x, y * r.y, bf16);
-      dg[i] = pack16(r.x > 0.f ? x * u.x : 0.f, r.y > 0.f ? y * u.y : 0.f, bf16);  // rows past M: r = 0
+      // r is 0 where the gate is off (and in rows past M), NaN in a block that is not finite
+      dg[i] = pack16(r.x > 0.f ? x * u.x : r.x, r.y > 0.f ? y * u.y : r.y, bf16);
     }
   }
   panels_out(panel, h, static_cast<unsigned char *>(Q.out) + at, du, static_cast<unsigned char *>(P.du) + at, ld, rows,

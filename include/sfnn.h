@@ -456,7 +456,8 @@ typedef enum {
 /* What the forward pass keeps for the backward pass: nothing; relu(G) and U as blocks of 64
  * 16-bit codes with an fp32 scale each, max / 65535 for relu(G) (a positive value keeps a code
  * of at least 1) and max|U| / 32767, signed (the caller keeps X); or X, relu(G) and U as 8-bit
- * blocks (sfnn_act8_quantize).  A block with a NaN or an infinity gives NaN gradients. */
+ * blocks (sfnn_act8_quantize).  A block of relu(G) with a NaN or an infinity gives NaN dG, dU and
+ * H, one of U NaN H and, where the gate is on, dG: NaN in every gradient that they enter. */
 typedef enum { SFNN_SAVE_NONE = 0, SFNN_SAVE_FULL = 1, SFNN_SAVE_ACT8 = 2 } sfnn_save;
 typedef struct {
     int32_t T, d, n;         /* tokens, width, neurons */
