@@ -315,28 +315,32 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, u
       rt = max(rt, __float_as_uint(r[i]) & 0x7fffffffu);
       ut = max(ut, __float_as_uint(u[i]) & 0x7fffffffu);
     }
-    const Act8Scale sr = full ? block_scale(rt, 65535.f, 0x0b800000u) : act8_scale(rt, 255.f);
-    const Act8Scale su = full ? block_scale(ut, 32767.f, 0x0b800000u) : act8_scale(ut, 127.f);
-    if (lane < rows) {
-      P.rs[(row0 + lane) * P.lds + (n0 >> 6)] = sr.scale;
-      P.us[(row0 + lane) * P.lds + (n0 >> 6)] = su.scale;
-    }
+    auto scales = [&](float sr, float su) {
+      if (lane < rows) {
+        P.rs[(row0 + lane) * P.lds + (n0 >> 6)] = sr;
+        P.us[(row0 + lane) * P.lds + (n0 >> 6)] = su;
+      }
+    };
     if (full) {
+      const Code16Scale sr = code16_scale(rt, kHalfR), su = code16_scale(ut, kHalfU);
+      scales(sr.scale, su.scale);
       unsigned char *rp = static_cast<unsigned char *>(P.r) + (row0 * P.ldr + n0) * 2;
       unsigned char *up = static_cast<unsigned char *>(P.u) + (row0 * P.ldr + n0) * 2;
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
         uint32_t q[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q[i] = code16_pair_relu(r[c + 2 * i], r[c + 2 * i + 1], sr.inv);
+        for (int i = 0; i < 16; ++i) q[i] = code16_pair_relu(r[c + 2 * i], r[c + 2 * i + 1], sr.to);
         words_to(w, q);
         panel_out(panel, w, rp + c * 2, P.ldr * 2, rows, 4);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q[i] = code16_pair(u[c + 2 * i], u[c + 2 * i + 1], su.inv);
+        for (int i = 0; i < 16; ++i) q[i] = code16_pair(u[c + 2 * i], u[c + 2 * i + 1], su.to);
         words_to(w, q);
         panel_out(panel + kPanel, w, up + c * 2, P.ldr * 2, rows, 4);
       }
     } else {
+      const Act8Scale sr = act8_scale(rt, 255.f), su = act8_scale(ut, 127.f);
+      scales(sr.scale, su.scale);
       auto codes = [&](const float *v, float inv, bool relu) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -415,21 +419,31 @@ __device__ __forceinline__ void saved_request(const DenseParams &P, const Unit &
 template <bool CODES8>
 struct SavedWords {
   uint32_t r[CODES8 ? 8 : 16], u[CODES8 ? 8 : 16];
-  float rs, r0, us;  // a code as a float: its bits under the exponent of 2^23, less 2^23 (and half the range if signed)
+  float rs, r0, us;
   __device__ __forceinline__ void set_scales(float sr, float su) {
-    rs = sr == 0.f ? __uint_as_float(1u) : sr;  // a lifted code of a block whose scale is zero keeps its neuron on
-    r0 = -8388608.f * rs;
-    us = su;
+    if (CODES8) {
+      rs = sr == 0.f ? __uint_as_float(1u) : sr;  // a lifted code of a block whose scale is zero keeps its neuron on
+      r0 = -8388608.f * rs;
+      us = su;
+    } else {
+      rs = code16_from(sr);
+      us = code16_from(su);
+    }
   }
   // columns 2 i and 2 i + 1
   __device__ __forceinline__ void get(int i, float2 &rv, float2 &uv) const {
-    const uint32_t a = r[CODES8 ? i >> 1 : i], b = u[CODES8 ? i >> 1 : i] ^ (CODES8 ? 0x80808080u : 0x80008000u);
-    const uint32_t lo = CODES8 ? 0x7440u + 2u * (i & 1) : 0x7410u, hi = CODES8 ? lo + 1 : 0x7432u;
-    constexpr float kZero = CODES8 ? 8388608.f + 128.f : 8388608.f + 32768.f;
-    rv.x = fmaf(__uint_as_float(__byte_perm(a, 0x4b000000u, lo)), rs, r0);
-    rv.y = fmaf(__uint_as_float(__byte_perm(a, 0x4b000000u, hi)), rs, r0);
-    uv.x = (__uint_as_float(__byte_perm(b, 0x4b000000u, lo)) - kZero) * us;
-    uv.y = (__uint_as_float(__byte_perm(b, 0x4b000000u, hi)) - kZero) * us;
+    if (CODES8) {
+      // a code as a float: its bits under the exponent of 2^23, less 2^23 (and half the range if signed)
+      const uint32_t a = r[i >> 1], b = u[i >> 1] ^ 0x80808080u, lo = 0x7440u + 2u * (i & 1), hi = lo + 1;
+      constexpr float kZero = 8388608.f + 128.f;
+      rv.x = fmaf(__uint_as_float(__byte_perm(a, 0x4b000000u, lo)), rs, r0);
+      rv.y = fmaf(__uint_as_float(__byte_perm(a, 0x4b000000u, hi)), rs, r0);
+      uv.x = (__uint_as_float(__byte_perm(b, 0x4b000000u, lo)) - kZero) * us;
+      uv.y = (__uint_as_float(__byte_perm(b, 0x4b000000u, hi)) - kZero) * us;
+    } else {
+      rv = code16_values_relu(r[i], rs);
+      uv = code16_values(u[i], us);
+    }
   }
 };
 

@@ -45,16 +45,15 @@ struct Act8Scale {
   float scale, inv;
 };
 // `top`: the largest fp32 bit pattern of the block's magnitudes (NaN > inf > finite); below
-// `least` (2^-112 for 8-bit codes, 2^-104 for 16-bit ones) the reciprocal could overflow.
-__device__ __forceinline__ Act8Scale block_scale(uint32_t top, float qmax, uint32_t least) {
+// 2^-112 the reciprocal could overflow.
+__device__ __forceinline__ Act8Scale act8_scale(uint32_t top, float qmax) {
   Act8Scale s;
   s.scale = __uint_as_float(top) * (1.f / qmax);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inv) : "f"(s.scale));  // within an ulp: a code is off only next to a tie
-  if (top < least) s.scale = s.inv = 0.f;
+  if (top < 0x07800000u) s.scale = s.inv = 0.f;
   if (top >= 0x7f800000u) s.scale = __uint_as_float(0x7fffffffu);
   return s;
 }
-__device__ __forceinline__ Act8Scale act8_scale(uint32_t top, float qmax) { return block_scale(top, qmax, 0x07800000u); }
 
 // Codes of four values as bytes: v * inv + 1.5 * 2^23 in one fused multiply-add leaves the
 // nearest integer (ties to even) in the low byte.  |v * inv| <= qmax (1 + 2^-21), so no code
@@ -73,18 +72,72 @@ __device__ __forceinline__ uint32_t act8_lift(uint32_t codes, uint32_t positive)
 }
 
 // ---------------------------------------------------------------- the saved hidden layer in 16 bits
-// What the forward pass keeps at full precision: the same blocks of 64 with 16-bit codes,
-// relu(G) max / 65535 with codes 0..65535 (again at least 1 where positive), U max|v| / 32767
-// signed.  They hold a value to 2^-17 of its block's largest, where the values' own types
-// would round each to 2^-9 (bf16) or 2^-12 of itself: of all a gradient's error, what is left
-// is the one rounding of dG, dU or H to the tensor cores' type, and its own.
-__device__ __forceinline__ uint32_t code16_pair(float a, float b, float inv) {
-  constexpr float kMagic = 12582912.f;
-  return __byte_perm(__float_as_uint(fmaf(a, inv, kMagic)), __float_as_uint(fmaf(b, inv, kMagic)), 0x5410);
+// What the forward pass keeps at full precision: blocks of 64 that share a power of two P, the
+// one at or below the block's largest magnitude (at least 2^-101), and 16 bits a value, a float
+// with more mantissa where most values lie: U a sign and 12 bits of mantissa in the three octaves
+// from P / 4 up, 11 in the nine below them, and equal steps from 2^-11 P on down; relu(G), never
+// negative, one bit more.  So U is off by at most 2^-13 of itself, 2^-12 below P / 4, and 2^-23 P
+// below 2^-11 P, relu(G) by half of that: a neuron keeps its precision beside one thousands of
+// times as large, and loses less than fp16 would round it by (2^-11) down to 2^-12 P.  Of a
+// gradient's error, what is left is the rounding of dG, dU or H to the tensor cores' type, and its
+// own.  A positive relu(G) keeps a code of at least 1: code > 0 is exactly the ReLU's mask.
+// (Fixed point holds values of like size better, to 2^-17 of the largest, but one 2^-12 of it to
+// four bits.  Gradients of an fp16 step of 257 tokens are 0.00030 off 64 bits with either, most of
+// it the roundings to fp16; with 11 bits of mantissa throughout 0.00031.)
+//
+// The codes come from an fp32 number's bits, scaled so that P has the exponent field 12 and
+// fp32's own subnormal numbers are the small values' equal steps: its bits from the 11th
+// mantissa bit up count the lower octaves' codes, those from the 12th up the upper octaves', less
+// what puts both at one code where they meet; the larger of the two is the code.
+// The scaling takes two multiplications, as one power of two would leave fp32's range.
+constexpr float kCodeDown = 1.1754943508222875e-38f;  // 2^-126
+constexpr float kCodeUp = 8.507059173023462e37f;      // 2^126
+constexpr uint32_t kCodeLow = 26;                     // the smallest block exponent (biased): 2^-101
+constexpr uint32_t kMeet = 10u << 11;                 // the code where the octaves meet (twice that for relu(G))
+struct Code16Scale {
+  float scale, to;  // P; what a value is multiplied by, before kCodeDown
+};
+// `half`: half a step of the upper octaves in a mantissa's bits (a largest value that rounds up to a
+// power of two takes that one as P).
+__device__ __forceinline__ Code16Scale code16_scale(uint32_t top, uint32_t half) {
+  const uint32_t e = max((top + half) >> 23, kCodeLow);
+  Code16Scale s;
+  s.scale = __uint_as_float(e >= 255u ? 0x7fffffffu : e << 23);
+  s.to = __uint_as_float((265u - e) << 23);  // 2^(138 - e); of a block that is not finite the codes mean nothing
+  return s;
 }
-__device__ __forceinline__ uint32_t code16_pair_relu(float a, float b, float inv) {
-  const uint32_t positive = (a > 0.f ? 1u : 0u) | (b > 0.f ? 0x10000u : 0u);
-  return __vmaxu2(code16_pair(a, b, inv), positive);
+constexpr uint32_t kHalfU = 0x400u, kHalfR = 0x200u;
+__device__ __forceinline__ float code16_from(float scale) { return scale * 0x1p-11f; }  // 2^(e - 138)
+__device__ __forceinline__ uint32_t code16_pair(float a, float b, float to) {  // signed
+  auto code = [&](float v) {
+    const uint32_t x = __float_as_uint(fabsf(v) * to * kCodeDown);
+    return (uint32_t)max((int)(x + 0x800u) >> 12, ((int)(x + kHalfU) >> 11) - (int)kMeet);
+  };
+  const uint32_t sign = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632) & 0x80008000u;
+  return __byte_perm(code(a), code(b), 0x5410) | sign;
+}
+__device__ __forceinline__ uint32_t code16_pair_relu(float a, float b, float to) {
+  auto code = [&](float v) {
+    const uint32_t x = __float_as_uint(v * to * kCodeDown);
+    const int c = max((int)(x + 0x400u) >> 11, ((int)(x + kHalfR) >> 10) - (int)(2u * kMeet));
+    return (uint32_t)max(c, v > 0.f ? 1 : 0);
+  };
+  return __byte_perm(code(a), code(b), 0x5410);
+}
+// The values of a word of two codes (`from`: code16_from of the block's scale).
+__device__ __forceinline__ float2 code16_values(uint32_t w, float from) {
+  auto value = [&](uint32_t half) {  // the code in the upper half of a word
+    const uint32_t c = (half >> 5) & 0x03fff800u;
+    return __uint_as_float(min(2u * c, c + (kMeet << 11)) | (half & 0x80000000u)) * kCodeUp * from;
+  };
+  return make_float2(value(w << 16), value(w));
+}
+__device__ __forceinline__ float2 code16_values_relu(uint32_t w, float from) {
+  auto value = [&](uint32_t half) {
+    const uint32_t c = (half >> 6) & 0x03fffc00u;
+    return __uint_as_float(min(2u * c, c + (kMeet << 11))) * kCodeUp * from;
+  };
+  return make_float2(value(w << 16), value(w));
 }
 
 // ---------------------------------------------------------------- the product

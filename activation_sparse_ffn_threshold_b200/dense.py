@@ -383,7 +383,7 @@ def mxfp4_linear(x, w: Mxfp4, out_dtype=None, stream=None):
 
 # ------------------------------------------------------------------ gated FFN
 class GatedSaved:
-    """What gated_ffn_forward keeps for gated_ffn_backward: relu(G) and U as 16-bit blocks and
+    """What gated_ffn_forward keeps for gated_ffn_backward: relu(G) and U as 16-bit codes and
     X itself ("full"), or everything as 8-bit blocks ("act8"); see sfnn_gated_saved."""
 
     __slots__ = ("kind", "x", "_buf", "_c", "_dims", "shape", "dtype", "has_b")
@@ -439,7 +439,7 @@ def gated_ffn_forward(x, w_gate, w_up, w_down, b=None, save=None, stream=None):
 
     x [..., d]; w_gate, w_up [n, d]; w_down [d, n]; b [n] or None; fp16 or bf16, d and n
     multiples of 8, rows 16-byte aligned (any even row stride).  ``save``: None (saved is
-    None), "full" (relu(G) and U as 16-bit blocks, a reference to x) or "act8" (all three as
+    None), "full" (relu(G) and U as 16-bit codes, a reference to x) or "act8" (all three as
     8-bit blocks)."""
     if save not in SAVE:
         raise ValueError("save must be None, 'full' or 'act8'")

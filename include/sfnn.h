@@ -453,11 +453,14 @@ typedef enum {
     SFNN_DOWN_WIDTH_MAJOR = 0, /* w_down [d x n], PyTorch's down.weight */
     SFNN_DOWN_NEURON_MAJOR = 1 /* w_down [n x d], a row per neuron (forward only) */
 } sfnn_down_layout;
-/* What the forward pass keeps for the backward pass: nothing; relu(G) and U as blocks of 64
- * 16-bit codes with an fp32 scale each, max / 65535 for relu(G) (a positive value keeps a code
- * of at least 1) and max|U| / 32767, signed (the caller keeps X); or X, relu(G) and U as 8-bit
- * blocks (sfnn_act8_quantize).  A block of relu(G) with a NaN or an infinity gives NaN dG, dU and
- * H, one of U NaN H and, where the gate is on, dG: NaN in every gradient that they enter. */
+/* What the forward pass keeps for the backward pass: nothing; relu(G) and U as 16-bit codes in
+ * blocks of 64, each with an fp32 scale P, the power of two at or below the block's largest
+ * magnitude (the caller keeps X); or X, relu(G) and U as 8-bit blocks (sfnn_act8_quantize).
+ * With 16 bits U is off by at most 2^-12 of itself (2^-13 from P / 4 up), or by 2^-23 P below
+ * 2^-11 P, and relu(G) by half of that; with 8 all values of a block are multiples of its scale,
+ * and those far below its largest lose their bits.  Both keep a code above zero for a positive
+ * relu(G).  A block of relu(G) with a NaN or an infinity gives NaN dG, dU and H, one of U NaN H
+ * and, where the gate is on, dG: NaN in every gradient that they enter. */
 typedef enum { SFNN_SAVE_NONE = 0, SFNN_SAVE_FULL = 1, SFNN_SAVE_ACT8 = 2 } sfnn_save;
 typedef struct {
     int32_t T, d, n;         /* tokens, width, neurons */

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import activation_sparse_ffn_threshold_b200 as sf
-from test_gpu_dense import KINDS, layer
+from test_gpu_dense import KINDS, backward64, forward64, layer, near
 
 pytestmark = pytest.mark.gpu
 
@@ -50,4 +50,42 @@ def test_gradients_of_blocks_that_are_not_finite(where, T, save, dt):
     if where != "x":
         for g, w in ((db, want[4]), (dwg, want[1]), (dwu, want[2]), (dwd.t(), want[3].t())):
             assert torch.equal(g[~block], w[~block])
+    assert sf.dense_error() == 0
+
+
+@pytest.mark.parametrize("dt", KINDS)
+@pytest.mark.parametrize("which", ["w_up", "w_gate"])
+@pytest.mark.parametrize("T,d,n", [(1, 72, 264), (40, 264, 520), (300, 136, 1000)])
+def test_full_gradients_of_neurons_of_unlike_size(T, d, n, which, dt):
+    """Neurons that share a block with others up to 2^12 times as large keep their gradients'
+    precision: a saved relu(G) is off by at most 2^-13 of itself and a saved U by 2^-12, or, far
+    below the block's largest, either by 2^-23 of that."""
+    x, wg, wu, wd, b, dy = layer(T, d, n, dt, seed=T + 1)
+    dy = (dy.float() / 64).to(dt)  # (fp16's range)
+    size = 0.25 * torch.tensor([1.0, 8.0, 64.0, 512.0, 4096.0], device="cuda")[torch.arange(n, device="cuda") * 7 % 5]
+    if which == "w_up":
+        wu = (wu.float() * size[:, None]).to(dt)
+    else:  # (powers of two: the gate's sums stay exact)
+        wg, b = (wg.float() * size[:, None]).to(dt), (b.float() * size).to(dt)
+    y, saved = sf.gated_ffn_forward(x, wg, wu, wd, b, save="full")
+    got = sf.gated_ffn_backward(dy, saved, wg, wu, wd)
+    G, U, H = forward64(x, wg, wu, wd, b)
+    on = (G > 0).double()
+    R = G * on
+    want, terms = backward64(x, wg, wu, wd, dy, R, U, on)
+
+    def top(v):
+        v = torch.nn.functional.pad(v.abs(), (0, -n % 64)).view(T, -1, 64)
+        return v.amax(2, keepdim=True).expand_as(v).reshape(T, -1)[:, :n]
+    eR, eU = R * 2.0 ** -13 + top(R) * 2.0 ** -23, U.abs() * 2.0 ** -12 + top(U) * 2.0 ** -23
+    # U is an fp32 sum besides: d 2^-23 of its terms
+    eU = eU + d * 2.0 ** -23 * (x.double().abs() @ wu.double().abs().t())
+    adH = dy.double().abs() @ wd.double().abs()
+    eG, eV = adH * eU * on, adH * eR
+    wg64, wu64, x64 = wg.double().abs(), wu.double().abs(), x.double().abs()
+    extra = (eG @ wg64 + eV @ wu64, eG.t() @ x64, eV.t() @ x64, dy.double().abs().t() @ (eR * U.abs() + eU * R),
+             eG.sum(0))
+    for i, (g, K) in enumerate(zip(got, (2 * n + d, T + d, T + d, T + d, T + d))):
+        if g is not None:
+            near(g, want[i], terms[i] + extra[i] / (torch.finfo(dt).eps / 2), dt, 1, K)
     assert sf.dense_error() == 0
