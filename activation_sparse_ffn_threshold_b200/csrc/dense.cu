@@ -375,24 +375,26 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, u
   }
 }
 
-// Sums of a panel's 32 columns of 16-bit values over its 32 rows: a lane adds two columns of
-// every other row; lanes 0..15 get columns 2 lane and 2 lane + 1.
-template <bool bf16>
-__device__ __forceinline__ float2 column_sums(uint32_t panel) {
-  const int lane = threadIdx.x & 31, pair = lane & 15;
-  float2 s = make_float2(0.f, 0.f);
+// Sums over the warp's 32 rows of 32 columns of fp32 values, of which a lane holds its row's:
+// lane c gets column c's.  The values pass through the two panels (columns 0..15, 16..31), whose
+// rows the lower and the upper lanes read in another order, so that they meet in no bank.
+__device__ __forceinline__ float column_sums(uint32_t panel, const uint32_t v[32]) {
+  const int lane = threadIdx.x & 31, c = lane & 15, up = lane >> 4;
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int row = 2 * i + (lane >> 4);
-    uint32_t w;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(panel_at(panel, row, pair >> 2) + (uint32_t)((pair & 3) * 4)));
-    const float2 f = unpack16(w, bf16);
-    s.x += f.x;
-    s.y += f.y;
+  for (int j = 0; j < 8; ++j)
+    sts16(panel_at(panel + (j >> 2) * kPanel, lane, j & 3), make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+  __syncwarp();
+  float sum = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];"
+                 : "=f"(f)
+                 : "r"(panel_at(panel + up * kPanel, i ^ up, c >> 2) + (uint32_t)((c & 3) * 4)));
+    sum += f;
   }
-  s.x += __shfl_down_sync(0xffffffffu, s.x, 16);
-  s.y += __shfl_down_sync(0xffffffffu, s.y, 16);
-  return s;
+  return sum;
 }
 
 // Request the saved relu(G) and U of a warp's rows into the panels `in` and `in` + 1: 64 bytes
@@ -454,33 +456,39 @@ __device__ __forceinline__ void dgated32(const DenseParams &P, const Unit &Q, ui
   const int lane = threadIdx.x & 31, rows = (int)min((int64_t)32, Q.M - row0), pieces = (Q.N - n0) / 8;
   if (rows <= 0 || pieces <= 0) return;  // (the whole warp)
   const int64_t at = (row0 * Q.ldo + n0) * 2, ld = Q.ldo * 2;
-  uint32_t h[16], du[16], dg[16];
+  uint32_t h[16], du[16], dg[32];
   {
-    uint32_t raw[32];
     __syncwarp();
-    tm_ld32(taddr, raw);
+    tm_ld32(taddr, dg);
     tm_wait_ld();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float2 r, u;
       v.get(i, r, u);
-      const float x = __uint_as_float(raw[2 * i]), y = __uint_as_float(raw[2 * i + 1]);
+      const float x = __uint_as_float(dg[2 * i]), y = __uint_as_float(dg[2 * i + 1]);
       h[i] = pack16(r.x * u.x, r.y * u.y, bf16);
       du[i] = pack16(x * r.x, y * r.y, bf16);
       // r is 0 where the gate is off (and in rows past M), NaN in a block that is not finite
-      dg[i] = pack16(r.x > 0.f ? x * u.x : r.x, r.y > 0.f ? y * u.y : r.y, bf16);
+      dg[2 * i] = __float_as_uint(r.x > 0.f ? x * u.x : r.x);
+      dg[2 * i + 1] = __float_as_uint(r.y > 0.f ? y * u.y : r.y);
     }
   }
   panels_out(panel, h, static_cast<unsigned char *>(Q.out) + at, du, static_cast<unsigned char *>(P.du) + at, ld, rows,
              pieces);
-  uint4 w[4];
-  words_to(w, dg);
-  panel_out(panel, w, static_cast<unsigned char *>(P.dg) + at, ld, rows, pieces);
-  if (P.colpart) {  // of dG as it was rounded, which the panel still holds
-    const float2 sum = column_sums<bf16>(panel);
-    if (lane < 16 && n0 + 2 * lane < Q.N)
-      *reinterpret_cast<float2 *>(P.colpart + (row0 >> 5) * Q.N + n0 + 2 * lane) = sum;
+  if (P.colpart) {  // of dG before it is rounded
+    const float sum = column_sums(panel, dg);
+    if (n0 + lane < Q.N) P.colpart[(row0 >> 5) * Q.N + n0 + lane] = sum;
   }
+  uint4 w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      q[j] = pack16(__uint_as_float(dg[8 * i + 2 * j]), __uint_as_float(dg[8 * i + 2 * j + 1]), bf16);
+    w[i] = make_uint4(q[0], q[1], q[2], q[3]);
+  }
+  panel_out(panel, w, static_cast<unsigned char *>(P.dg) + at, ld, rows, pieces);
 }
 
 // `width` columns of dH from n0 on; the first saved piece has been requested.

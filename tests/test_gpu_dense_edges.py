@@ -89,3 +89,30 @@ def test_full_gradients_of_neurons_of_unlike_size(T, d, n, which, dt):
         if g is not None:
             near(g, want[i], terms[i] + extra[i] / (torch.finfo(dt).eps / 2), dt, 1, K)
     assert sf.dense_error() == 0
+
+
+@pytest.mark.parametrize("dt", KINDS)
+@pytest.mark.parametrize("save", ["full", "act8"])
+def test_bias_gradient_sums_what_was_not_rounded(save, dt):
+    """Equal tokens round dG the same way, so a db that added up rounded values would carry that
+    rounding whole; it adds the 32-bit ones and is rounded once."""
+    T, d, n = 685, 64, 2048
+    x, wg, wu, wd, b, dy = layer(1, d, n, dt, seed=5)
+    x, dy = x.expand(T, d).contiguous(), dy.expand(T, d).contiguous()
+    y, saved = sf.gated_ffn_forward(x, wg, wu, wd, b, save=save)
+    db = sf.gated_ffn_backward(dy, saved, wg, wu, wd, need=(False, False, False, False, True))[4]
+    G, U, H = forward64(x[:1], wg, wu, wd, b)
+    on = (G > 0).double()
+    if save == "full":  # U is an fp32 sum of d products, held to 2^-12 of itself or 2^-23 of its block's largest
+        eU = d * 2.0 ** -23 * (x[:1].double().abs() @ wu.double().abs().t()) + 2.0 ** -12 * U.abs() + 2.0 ** -23 * U.abs().max()
+    else:
+        U = saved.u.view(torch.int8)[:1, :n].double() * saved.u_scales[:1].double().repeat_interleave(64, 1)[:, :n]
+        eU = 2.0 ** -24 * U.abs()
+    dH, adH = dy[:1].double() @ wd.double(), dy[:1].double().abs() @ wd.double().abs()
+    want = T * dH * U * on
+    # db's own rounding; U's error; dH is an fp32 sum of d products, db one of T
+    tol = (torch.finfo(dt).eps / 2 + T * 2.0 ** -23) * want.abs() + T * on * (dH.abs() * eU + d * 2.0 ** -23 * adH * U.abs())
+    assert ((db.double() - want[0]).abs() <= 1.001 * tol[0]).all()
+    # the same sum where the other gradients' launch adds it up
+    assert torch.equal(db, sf.gated_ffn_backward(dy, saved, wg, wu, wd)[4])
+    assert sf.dense_error() == 0
