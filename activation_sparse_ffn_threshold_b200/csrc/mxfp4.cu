@@ -471,7 +471,9 @@ __global__ void __launch_bounds__(kRowThreads)
   // bytes of token t: two planes of 16 bytes a block (a warp's 16-byte reads then have no bank
   // conflicts), then its scales
   uint4 *xq = reinterpret_cast<uint4 *>(smem);
-  float *xs = reinterpret_cast<float *>(smem + (size_t)TT * K);
+  // as two factors, at most 1 and at least 1: with the weights' scale between them no product
+  // leaves fp32's range that comes back to it
+  float2 *xs = reinterpret_cast<float2 *>(smem + (size_t)TT * K);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r0 = (int)((int64_t)blockIdx.x * N / gridDim.x), r1 = (int)((int64_t)(blockIdx.x + 1) * N / gridDim.x);
   const int64_t kt = mx_ktiles(K);
@@ -535,7 +537,10 @@ __global__ void __launch_bounds__(kRowThreads)
     const uint32_t lo = __vsub4(mx_magnitudes(sel) ^ s0, s0), hi = __vsub4(mx_magnitudes(sel >> 16) ^ s1, s1);
     const int b = c >> 5, part = (c >> 3) & 3;  // 8 values: half a plane's 16 bytes
     reinterpret_cast<uint2 *>(xq + ((size_t)t * 2 + (part >> 1)) * nb + b)[part & 1] = make_uint2(lo, hi);
-    if (part == 0) xs[t * nb + b] = 0.25f * mx_scale_value(e);  // the products are of doubled values
+    if (part == 0) {
+      const float v = 0.25f * mx_scale_value(e);  // the products are of doubled values
+      xs[t * nb + b] = make_float2(v > 1.f ? 1.f : v, v > 1.f ? v : 1.f);
+    }
   }
   __syncthreads();
 
@@ -579,7 +584,8 @@ __global__ void __launch_bounds__(kRowThreads)
             dot = __dp4a((int)xv[j], (int)val[j], dot);
             over = __dp4a((int)xv[j], (int)sgn[j], over);
           }
-          acc[t] = fmaf((float)(dot - over) * xs[t * nb + b], ws, acc[t]);
+          const float2 sx = xs[t * nb + b];
+          acc[t] = fmaf((float)(dot - over) * sx.x * ws, sx.y, acc[t]);
         }
       }
     }
@@ -602,9 +608,9 @@ template <int TT>
 cudaError_t launch_rows(const void *x, int64_t ldx, int T, int vec, int bf16, const void *wc, const void *wsc, int N, int K,
                         void *y, int64_t ldy, int y_dtype, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t attr = allow_smem(k_mx_rows<TT>, (size_t)(TT == 4 ? 65536 / 3 * 4 : 65536) * 9 / 8 + 256, ready);
+  const cudaError_t attr = allow_smem(k_mx_rows<TT>, (size_t)(TT == 4 ? 65536 / 3 * 4 : 65536) * 5 / 4 + 256, ready);
   if (attr != cudaSuccess) return attr;
-  return launch_pdl(k_mx_rows<TT>, dim3(std::min(sms, (N + 15) / 16)), dim3(kRowThreads), (size_t)TT * K * 9 / 8, s,
+  return launch_pdl(k_mx_rows<TT>, dim3(std::min(sms, (N + 15) / 16)), dim3(kRowThreads), (size_t)TT * K * 5 / 4, s,
                     static_cast<const uint16_t *>(x), ldx, T, vec, bf16, static_cast<const uint4 *>(wc),
                     static_cast<const uint8_t *>(wsc), N, K, y, ldy, y_dtype);
 }

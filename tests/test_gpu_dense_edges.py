@@ -116,3 +116,18 @@ def test_bias_gradient_sums_what_was_not_rounded(save, dt):
     # the same sum where the other gradients' launch adds it up
     assert torch.equal(db, sf.gated_ffn_backward(dy, saved, wg, wu, wd)[4])
     assert sf.dense_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 6])
+def test_mxfp4_scales_at_the_ends_of_the_range(T):
+    """A block's sum of products times one scale may pass 2^128 where both scales bring it back."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    for kx, kw in ((2.0 ** 124, 2.0 ** -20), (2.0 ** -120, 2.0 ** 100), (2.0 ** -20, 2.0 ** 124)):
+        x, w = (r(T, 288) * kx).to(torch.bfloat16), (r(100, 288) * kw).to(torch.bfloat16)
+        q = sf.quantize_mxfp4(w)
+        X, Wv = (sf.dequantize_mxfp4(v).double() for v in (sf.quantize_mxfp4(x), q))  # exact in bf16
+        want, terms = X @ Wv.t(), X.abs() @ Wv.abs().t()
+        got = sf.mxfp4_linear(x, q, out_dtype=torch.float32).double()
+        assert ((got - want).abs() <= 2.0 ** -24 * want.abs() + 288 * 2.0 ** -23 * terms).all()
+    assert sf.dense_error() == 0
