@@ -284,12 +284,12 @@ class SparseFFN:
         """Y [T, d] fp32 for T tokens (any number) through all neurons, without the predictor."""
         T = X.shape[0]
         self._check_x(X, rows=T)
-        Y = Y if Y is not None else torch.empty((T, self.d), dtype=torch.float32, device=X.device)
-        if Y.dtype != torch.float32 or Y.device != X.device or not Y.is_contiguous() or Y.numel() != T * self.d:
-            raise ValueError(f"Y must be a contiguous fp32 tensor of {T}x{self.d} elements on X's device")
         stream = stream if stream is not None else torch.cuda.current_stream(X.device)
         nbytes = self._lib.sfnn_gated_workspace(T, self.d, self.n, 0)
-        with torch.cuda.stream(stream):  # the workspace belongs to the stream that uses it
+        with torch.cuda.stream(stream):  # what is allocated here belongs to the stream that uses it
+            Y = Y if Y is not None else torch.empty((T, self.d), dtype=torch.float32, device=X.device)
+            if Y.dtype != torch.float32 or Y.device != X.device or not Y.is_contiguous() or Y.numel() != T * self.d:
+                raise ValueError(f"Y must be a contiguous fp32 tensor of {T}x{self.d} elements on X's device")
             ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=X.device)
         with torch.cuda.device(X.device):
             _check(self._lib.sfnn_forward_prompt(self._h, _ptr(X), T, _ptr(Y), _ptr(ws), ws.numel(),

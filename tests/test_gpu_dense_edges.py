@@ -131,3 +131,30 @@ def test_mxfp4_scales_at_the_ends_of_the_range(T):
         got = sf.mxfp4_linear(x, q, out_dtype=torch.float32).double()
         assert ((got - want).abs() <= 2.0 ** -24 * want.abs() + 288 * 2.0 ** -23 * terms).all()
     assert sf.dense_error() == 0
+
+
+def _handle(act, d, n, seed=3, **kw):
+    import workload as W
+    cfg = W.small_config(W.CONFIGS["70b_reglu" if act == "reglu" else "opt6.7b_relu"], d=d, n=n, r=64)
+    return sf.SparseFFN.from_layer(W.make_layer(cfg, seed=seed), device="cuda:0", **kw)
+
+
+def test_prompt_output_belongs_to_the_stream_that_writes_it():
+    """Memory that the current stream freed may still be in use there: a call on another stream
+    takes its output from that stream's own."""
+    h = _handle("reglu", 128, 72)
+    X = torch.randn(30001, 128, generator=torch.Generator().manual_seed(1)).half().cuda()
+    want = h.forward_prompt(X)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = torch.empty(30001, 128, device="cuda")
+    at = old.data_ptr()
+    old.fill_(7.0)
+    del old
+    Y = h.forward_prompt(X, stream=side)
+    side.synchronize()
+    assert Y.data_ptr() != at
+    assert torch.equal(Y, want)
+    h.close()
