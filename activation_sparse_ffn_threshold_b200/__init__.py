@@ -285,13 +285,15 @@ class SparseFFN:
         T = X.shape[0]
         self._check_x(X, rows=T)
         stream = stream if stream is not None else torch.cuda.current_stream(X.device)
-        nbytes = self._lib.sfnn_gated_workspace(T, self.d, self.n, 0)
-        with torch.cuda.stream(stream):  # what is allocated here belongs to the stream that uses it
+        if stream.device != X.device:
+            raise ValueError(f"the stream is on {stream.device}, X on {X.device}")
+        # the workspace's size is the current device's, and memory belongs to the stream that uses it
+        with torch.cuda.device(X.device), torch.cuda.stream(stream):
             Y = Y if Y is not None else torch.empty((T, self.d), dtype=torch.float32, device=X.device)
             if Y.dtype != torch.float32 or Y.device != X.device or not Y.is_contiguous() or Y.numel() != T * self.d:
                 raise ValueError(f"Y must be a contiguous fp32 tensor of {T}x{self.d} elements on X's device")
+            nbytes = self._lib.sfnn_gated_workspace(T, self.d, self.n, 0)
             ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=X.device)
-        with torch.cuda.device(X.device):
             _check(self._lib.sfnn_forward_prompt(self._h, _ptr(X), T, _ptr(Y), _ptr(ws), ws.numel(),
                                                  _stream(stream)), "sfnn_forward_prompt")
         return Y

@@ -158,3 +158,32 @@ def test_prompt_output_belongs_to_the_stream_that_writes_it():
     assert Y.data_ptr() != at
     assert torch.equal(Y, want)
     h.close()
+
+
+def test_prompt_workspace_is_sized_on_the_layers_device(monkeypatch):
+    h = _handle("reglu", 128, 72)
+    inside, sized = [], []
+
+    class Device(torch.cuda.device):
+        def __enter__(self):
+            inside.append(self.idx)
+            return super().__enter__()
+
+        def __exit__(self, *a):
+            inside.pop()
+            return super().__exit__(*a)
+
+    class Library:
+        def __getattr__(self, name):
+            if name == "sfnn_gated_workspace":
+                sized.append(list(inside))
+            return getattr(lib, name)
+    lib, h._lib = h._lib, Library()
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    X = torch.randn(3, 128, generator=torch.Generator().manual_seed(1)).half().cuda()
+    h.forward_prompt(X, stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert sized and all(0 in s for s in sized)
+    monkeypatch.undo()
+    h._lib = lib
+    h.close()
