@@ -284,6 +284,8 @@ class SparseFFN:
         """Y [T, d] fp32 for T tokens (any number) through all neurons, without the predictor."""
         T = X.shape[0]
         self._check_x(X, rows=T)
+        if T > 0x7fffffff:
+            raise ValueError(f"X: {T} rows do not fit 32 bits")
         stream = stream if stream is not None else torch.cuda.current_stream(X.device)
         if stream.device != X.device:
             raise ValueError(f"the stream is on {stream.device}, X on {X.device}")

@@ -135,6 +135,9 @@ def _code(dtype) -> int:
     return code
 
 
+_INT_MAX = 0x7fffffff  # of the C entry points' sizes; ctypes would cut a larger one without a word
+
+
 def _rows(t, name, cols=None):
     """(pointer, rows, cols, row stride) of a tensor [..., cols] whose rows lie evenly apart."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -145,6 +148,8 @@ def _rows(t, name, cols=None):
         r = shape[0] if len(shape) == 2 else (t.numel() // c if c else 0)
         if cols is not None and c != cols:
             raise ValueError(f"{name} must have {cols} columns, got {c}")
+        if r > _INT_MAX or c > _INT_MAX:
+            raise ValueError(f"{name}: {r} rows of {c} columns do not fit 32 bits")
         return t.data_ptr(), r, c, c
     if len(shape) != 2:
         if not shape:
@@ -157,6 +162,8 @@ def _rows(t, name, cols=None):
     if cols is not None and c != cols:
         raise ValueError(f"{name} must have {cols} columns, got {c}")
     sr, sc = t.stride()
+    if r > _INT_MAX or c > _INT_MAX:
+        raise ValueError(f"{name}: {r} rows of {c} columns do not fit 32 bits")
     if c > 1 and sc != 1 and r:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     return t.data_ptr(), r, c, (sr if r > 1 else c)
