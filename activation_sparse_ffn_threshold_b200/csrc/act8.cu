@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 bool aligned16(const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
-dim3 grid_of(int T, int cols) { return dim3((T + kWarps - 1) / kWarps, (cols + kChunk - 1) / kChunk); }
+dim3 grid_of(int64_t T, int64_t cols) {  // (either may be near 2^31)
+  return dim3((unsigned)((T + kWarps - 1) / kWarps), (unsigned)((cols + kChunk - 1) / kChunk));
+}
 
 }  // namespace
 
@@ -259,7 +261,7 @@ static sfnn_status act8_check(const void *x, int64_t ldx, int32_t T, int32_t col
   if ((reinterpret_cast<uintptr_t>(codes) & 15u) || (reinterpret_cast<uintptr_t>(scales) & 3u) ||
       (reinterpret_cast<uintptr_t>(x) & 1u))
     return SFNN_ERR_INVALID_ARG;
-  if ((cols + sfnn::kChunk - 1) / sfnn::kChunk > 65535) return SFNN_ERR_UNSUPPORTED;
+  if (((int64_t)cols + sfnn::kChunk - 1) / sfnn::kChunk > 65535) return SFNN_ERR_UNSUPPORTED;
   return SFNN_OK;
 }
 

@@ -4,7 +4,10 @@ import warnings
 import pytest
 import torch
 
+import activation_sparse_ffn_threshold_b200 as sf
 from activation_sparse_ffn_threshold_b200 import dense
+
+UNSUPPORTED = sf.STATUS_CODES["SFNN_ERR_UNSUPPORTED"]
 
 
 def test_binding_refuses_sizes_that_32_bits_do_not_hold():
@@ -19,3 +22,11 @@ def test_binding_refuses_sizes_that_32_bits_do_not_hold():
                 dense._rows(t, "x")
         edge = torch.empty(2 ** 31 - 1, 8, dtype=torch.float16, device="cuda")
         assert dense._rows(edge, "x")[1:] == (2 ** 31 - 1, 8, 8)
+
+
+def test_act8_refuses_widths_near_the_end_of_32_bits():
+    lib = sf.load_library()
+    for cols in (65535 * 2048 + 1, 2 ** 31 - 2048, 2 ** 31 - 64, 2 ** 31 - 1):  # more than a launch's grid covers
+        args = (4096, cols, 1, cols, sf.F16, 0)
+        assert lib.sfnn_act8_quantize(*args, 4096, 2 ** 31, 4096, 2 ** 25, None) == UNSUPPORTED, cols
+        assert lib.sfnn_act8_restore(4096, 2 ** 31, 4096, 2 ** 25, 1, cols, 0, sf.F16, 4096, cols, None) == UNSUPPORTED, cols
