@@ -393,26 +393,47 @@ class GatedSaved:
     """What gated_ffn_forward keeps for gated_ffn_backward: relu(G) and U as 16-bit codes and
     X itself ("full"), or everything as 8-bit blocks ("act8"); see sfnn_gated_saved."""
 
-    __slots__ = ("kind", "x", "_buf", "_c", "_dims", "shape", "dtype", "has_b")
+    __slots__ = ("kind", "x", "_buf", "_c", "_dims", "_plan", "shape", "dtype", "has_b")
 
     def __init__(self, kind, x, T, d, n, has_b):
         self.kind, self.shape, self.dtype, self.has_b = kind, x.shape, x.dtype, has_b
         full = kind == "full"
         e = 2 if full else 1
-        nb, db = (n + 63) >> 6, (d + 63) >> 6
-        codes, scales = T * nb * 64 * e, T * nb * 4
-        size = (codes + scales + 15) & ~15  # each plane (codes, then scales) on 16 bytes
-        self._buf = buf = x.new_empty(2 * size + (0 if full else T * db * 68), dtype=torch.uint8)
+        nb, db = (n + 63) >> 6, 0 if full else (d + 63) >> 6
+        codes = T * nb * 64 * e
+        size = (codes + T * nb * 4 + 15) & ~15  # each plane (codes, then scales) on 16 bytes
+        nbytes = 2 * size + T * db * 68
+        self._dims, self._plan = (T, d, n, e, size), (nb, db, codes, nbytes)
+        self._bind(x.new_empty(nbytes, dtype=torch.uint8), x if full else None)
+
+    def _bind(self, buf, x):
+        """Take ``buf`` as the memory of the codes and scales, and x."""
+        self._buf, self.x = buf, x
+        T, _, _, _, size = self._dims
+        nb, db, codes, _ = self._plan
         p = buf.data_ptr()
-        if full:
-            self.x = x
-            self._c = _GatedSaved(1, 0, p, p + size, nb * 64, p + codes, p + size + codes, nb)
-        else:
-            self.x = None
+        if db:
             q = p + 2 * size
             self._c = _GatedSaved(2, 0, p, p + size, nb * 64, p + codes, p + size + codes, nb, q, db * 64,
                                   q + T * db * 64, db)
-        self._dims = (T, d, n, e, size)
+        else:
+            self._c = _GatedSaved(1, 0, p, p + size, nb * 64, p + codes, p + size + codes, nb)
+
+    def _release(self):
+        """Its tensors, which it holds no longer."""
+        tensors = [self._buf] if self.x is None else [self._buf, self.x]
+        self._buf = self.x = self._c = None
+        return tensors
+
+    def _with(self, buf, x=None):
+        """A copy of a released one that holds these (which may come from a hook)."""
+        if buf.dtype != torch.uint8 or buf.numel() != self._plan[3] or not buf.is_contiguous() or buf.data_ptr() % 16:
+            raise ValueError("the saved activations did not come back as they were")
+        s = GatedSaved.__new__(GatedSaved)
+        s.kind, s.shape, s.dtype, s.has_b = self.kind, self.shape, self.dtype, self.has_b
+        s._dims, s._plan = self._dims, self._plan
+        s._bind(buf, x)
+        return s
 
     def _planes(self, i):
         T, d, n, e, size = self._dims
@@ -514,28 +535,20 @@ class _GatedFFN(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, b, checkpoint):
         y, saved = gated_ffn_forward(x, w_gate, w_up, w_down, b, save=checkpoint)
+        # every tensor through autograd, which frees them with the backward pass, hands them to hooks
+        # that move them elsewhere, and notices a change in place
+        ctx.save_for_backward(w_gate, w_up, w_down, *saved._release())
         ctx.saved = saved
-        keep = [w_gate, w_up, w_down]
-        if saved.x is not None:  # through autograd, which notices a change in place
-            keep.append(saved.x)
-            saved.x = None
-        ctx.save_for_backward(*keep)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        w_gate, w_up, w_down, *x = ctx.saved_tensors
-        saved = ctx.saved
+        w_gate, w_up, w_down, *kept = ctx.saved_tensors
         if dy.stride() != torch.empty(dy.shape, device="meta").stride() or dy.data_ptr() % 16:
             dy = dy.contiguous() if not dy.is_contiguous() else dy.clone()
-        if x:
-            full = GatedSaved.__new__(GatedSaved)
-            for k in GatedSaved.__slots__:
-                setattr(full, k, getattr(saved, k))
-            full.x = x[0]
-            saved = full
-        return gated_ffn_backward(dy, saved, w_gate, w_up, w_down, need=ctx.needs_input_grad[:5]) + (None,)
+        return gated_ffn_backward(dy, ctx.saved._with(*kept), w_gate, w_up, w_down,
+                                  need=ctx.needs_input_grad[:5]) + (None,)
 
 
 def gated_ffn(x, w_gate, w_up, w_down, b=None, checkpoint: str = "full"):

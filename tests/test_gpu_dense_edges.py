@@ -187,3 +187,54 @@ def test_prompt_workspace_is_sized_on_the_layers_device(monkeypatch):
     monkeypatch.undo()
     h._lib = lib
     h.close()
+
+
+@pytest.mark.parametrize("checkpoint", ["full", "act8"])
+def test_saved_activations_end_with_the_backward_pass(checkpoint):
+    x, wg, wu, wd, b, dy = layer(512, 256, 2048, torch.bfloat16, seed=6)
+    leaves = [t.clone().requires_grad_() for t in (x, wg, wu, wd, b)]
+    want = sf.gated_ffn_backward(dy, sf.gated_ffn_forward(x, wg, wu, wd, b, save=checkpoint)[1], wg, wu, wd)
+    torch.cuda.synchronize()
+    bare = torch.cuda.memory_allocated()
+    y = sf.gated_ffn(*leaves, checkpoint=checkpoint)
+    held = torch.cuda.memory_allocated() - bare - y.numel() * y.element_size()
+    assert held >= 2 * 512 * 2048 * (2 if checkpoint == "full" else 1)
+    for again in (True, False):
+        grads = torch.autograd.grad(y, leaves, dy, retain_graph=again)
+        assert all(torch.equal(a, c) for a, c in zip(grads, want))
+        del grads
+        left = torch.cuda.memory_allocated() - bare - y.numel() * y.element_size()
+        assert left == held if again else left <= 0, "y is still here, what its backward pass read is not"
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y, leaves, dy)
+
+
+@pytest.mark.parametrize("checkpoint", ["full", "act8"])
+def test_saved_activations_pass_through_hooks(checkpoint):
+    """As every tensor that autograd saves: offloaded, and back at other addresses."""
+    x, wg, wu, wd, b, dy = layer(100, 64, 200, torch.float16, seed=7)
+    leaves = [t.clone().requires_grad_() for t in (x, wg, wu, wd, b)]
+    want = sf.gated_ffn_backward(dy, sf.gated_ffn_forward(x, wg, wu, wd, b, save=checkpoint)[1], wg, wu, wd)
+    packed = []
+
+    def pack(t):
+        packed.append(t.numel() * t.element_size())
+        return t.cpu()
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t.cuda()):
+        y = sf.gated_ffn(*leaves, checkpoint=checkpoint)
+    assert max(packed) >= 2 * 100 * 200 * (2 if checkpoint == "full" else 1)
+    junk = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")  # over what the forward pass freed
+    grads = torch.autograd.grad(y, leaves, dy)
+    assert all(torch.equal(a, c) for a, c in zip(grads, want))
+    del junk
+
+
+def test_saved_activations_that_come_back_otherwise_are_refused():
+    x, wg, wu, wd, b, dy = layer(10, 64, 128, torch.float16, seed=7)
+    leaf = wg.clone().requires_grad_()
+    for unpack in (lambda t: t[:-16] if t.dtype == torch.uint8 else t, lambda t: t.int() if t.dtype == torch.uint8 else t,
+                   lambda t: t.cpu() if t.dtype == torch.uint8 else t):
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: t, unpack):
+            y = sf.gated_ffn(x, leaf, wu, wd, b)
+        with pytest.raises(ValueError):
+            torch.autograd.grad(y, leaf, dy)
