@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import BF16, F16, F32, _check, load_library
@@ -189,6 +190,14 @@ def _same_device(index, *ts):
 
 def _vp(t):
     return None if t is None else t.data_ptr()
+
+
+def _follows(*ts) -> bool:
+    """Whether autograd follows one of these: a result without it would lose their gradient or tangent."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts):
+        return True
+    return getattr(_forward_ad, "_current_level", 0) >= 0 and any(
+        t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in ts)
 
 
 def _like(t):
@@ -552,10 +561,10 @@ class _GatedFFN(torch.autograd.Function):
 
 
 def gated_ffn(x, w_gate, w_up, w_down, b=None, checkpoint: str = "full"):
-    """gated_ffn_forward as a differentiable function; ``checkpoint`` ("full" or "act8") is
-    how the activations are held until the backward pass."""
+    """gated_ffn_forward as a differentiable function (once, in reverse mode); ``checkpoint``
+    ("full" or "act8") is how the activations are held until the backward pass."""
     if checkpoint not in ("full", "act8"):
         raise ValueError("checkpoint must be 'full' or 'act8'")
-    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in (x, w_gate, w_up, w_down, b)):
+    if not _follows(x, w_gate, w_up, w_down, b):
         return gated_ffn_forward(x, w_gate, w_up, w_down, b)[0]
     return _GatedFFN.apply(x, w_gate, w_up, w_down, b, checkpoint)

@@ -238,3 +238,17 @@ def test_saved_activations_that_come_back_otherwise_are_refused():
             y = sf.gated_ffn(x, leaf, wu, wd, b)
         with pytest.raises(ValueError):
             torch.autograd.grad(y, leaf, dy)
+
+
+def test_forward_mode_is_refused():
+    import torch.autograd.forward_ad as fw
+    x, wg, wu, wd, b, dy = layer(8, 64, 128, torch.float16, seed=8)
+    want = sf.gated_ffn(x, wg, wu, wd, b)
+    with fw.dual_level():
+        for i in (0, 1, 4):
+            args = [x, wg, wu, wd, b]
+            args[i] = fw.make_dual(args[i], torch.ones_like(args[i]))
+            with pytest.raises((RuntimeError, NotImplementedError)):
+                sf.gated_ffn(*args)
+        assert torch.equal(sf.gated_ffn(x, wg, wu, wd, b), want)  # no tangent: nothing to refuse
+    assert torch.equal(sf.gated_ffn(x, wg, wu, wd, b), want)
