@@ -6,6 +6,10 @@ Tensors are fp16 or bf16 on one CUDA device; results belong to the current strea
 ``stream``, which the call then runs on).  A bounded device-side wait that runs out is
 latched per device and returned by ``dense_error``; the word it is latched in is allocated
 by a device's first call, which must not be inside a graph capture.
+
+Autograd follows ``gated_ffn`` alone.  ``gated_ffn_forward`` and ``gated_ffn_backward`` are its two
+passes as plain calls; what is quantised (``Act8``, ``Mxfp4``), and what is made from it, carries
+no gradient.
 """
 from __future__ import annotations
 
@@ -194,9 +198,11 @@ def _vp(t):
 
 def _follows(*ts) -> bool:
     """Whether autograd follows one of these: a result without it would lose their gradient or tangent."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts):
-        return True
-    return getattr(_forward_ad, "_current_level", 0) >= 0 and any(
+    if torch.is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                return True
+    return _forward_ad._current_level >= 0 and any(
         t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in ts)
 
 
@@ -375,9 +381,25 @@ def mxfp4_matmul(x: Mxfp4, w: Mxfp4, out_dtype=None, stream=None):
     return y
 
 
+class _NoGradient(torch.autograd.Function):
+    """A call whose result remembers that it followed from x, and says so instead of ending x's gradient."""
+
+    @staticmethod
+    def forward(ctx, x, call, name, *args):
+        ctx.name = name
+        return call(x, *args)  # (autograd is off in here)
+
+    @staticmethod
+    def backward(ctx, dy):
+        raise RuntimeError(f"{ctx.name} has no gradient: call it on x.detach() or under torch.no_grad()")
+
+
 def mxfp4_linear(x, w: Mxfp4, out_dtype=None, stream=None):
-    """A linear layer with MXFP4 weights: x [..., K] in fp16 or bf16 is quantised by the call."""
+    """A linear layer with MXFP4 weights: x [..., K] in fp16 or bf16 is quantised by the call.
+    It has no gradient: a backward pass that reaches it raises."""
     p, T, K, ld = _rows(x, "x")
+    if (x.requires_grad or _forward_ad._current_level >= 0) and _follows(x):
+        return _NoGradient.apply(x, mxfp4_linear, "mxfp4_linear", w, out_dtype, stream)
     dt = x.dtype
     xcode = _code(dt)
     if out_dtype is not None:

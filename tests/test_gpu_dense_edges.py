@@ -252,3 +252,21 @@ def test_forward_mode_is_refused():
                 sf.gated_ffn(*args)
         assert torch.equal(sf.gated_ffn(x, wg, wu, wd, b), want)  # no tangent: nothing to refuse
     assert torch.equal(sf.gated_ffn(x, wg, wu, wd, b), want)
+
+
+@pytest.mark.parametrize("T", [2, 40])
+def test_mxfp4_linear_says_that_it_has_no_gradient(T):
+    import torch.autograd.forward_ad as fw
+    x, wg, *_ = layer(T, 64, 128, torch.float16, seed=9)
+    q = sf.quantize_mxfp4(wg)
+    want = sf.mxfp4_linear(x, q)
+    leaf = x.clone().requires_grad_()
+    y = sf.mxfp4_linear(leaf * 1, q)
+    assert torch.equal(y, want)
+    with pytest.raises(RuntimeError, match="gradient"):
+        y.sum().backward()
+    with torch.no_grad():
+        y = sf.mxfp4_linear(leaf, q)
+    assert not y.requires_grad and torch.equal(y, want)
+    with fw.dual_level(), pytest.raises((RuntimeError, NotImplementedError)):
+        sf.mxfp4_linear(fw.make_dual(x, torch.ones_like(x)), q)
