@@ -172,8 +172,9 @@ cudaError_t join(const DenseProblem &P, int bf16, int sms, cudaStream_t s) {
                     bf16, P.out32, P.out, P.ldo);
 }
 
+// (`kernels` counts the launches.)
 sfnn_status product(const Operand &a, const Operand &b, int M, int N, int64_t K, void *out, int64_t ldo, int out32, int bf16,
-                    float *parts, int32_t *err, cudaStream_t s, const void *relu_bias = nullptr) {
+                    float *parts, int32_t *err, cudaStream_t s, int &kernels, const void *relu_bias = nullptr) {
   const int sms = device_sms();
   DenseParams P{};
   P.count = 1;
@@ -186,17 +187,11 @@ sfnn_status product(const Operand &a, const Operand &b, int M, int N, int64_t K,
   P.bf16 = bf16;
   P.err = err;
   if (launch_dense(P, kEpiStore, sms, s) != cudaSuccess || join(P.p[0], bf16, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
+  kernels += split > 1 ? 2 : 1;
   return SFNN_OK;
 }
 
-}  // namespace
-}  // namespace sfnn
-
-using namespace sfnn;
-
-extern "C" {
-
-int64_t sfnn_gated_workspace(int32_t T, int32_t d, int32_t n, int32_t backward) {
+int64_t workspace(int32_t T, int32_t d, int32_t n, int32_t backward) {
   if (T < 0 || d < 1 || n < 1) return -1;
   const int sms = device_sms();
   if (!backward) return hidden_bytes(T, n) + parts_bytes(T, d, chunks(n), sms);
@@ -204,8 +199,8 @@ int64_t sfnn_gated_workspace(int32_t T, int32_t d, int32_t n, int32_t backward) 
          parts_bytes(T, d, 2 * chunks(n), sms);
 }
 
-sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, int32_t y_dtype, sfnn_gated_saved *sv,
-                               void *ws, int64_t ws_bytes, int32_t *err, sfnn_stream_t stream) {
+sfnn_status forward(const sfnn_gated_desc *q, void *y, int64_t ldy, int32_t y_dtype, sfnn_gated_saved *sv, void *ws,
+                    int64_t ws_bytes, int32_t *err, sfnn_stream_t stream, int &kernels) {
   sfnn_status st = check(q);
   if (st != SFNN_OK) return st;
   const int kind = sv ? sv->kind : SFNN_SAVE_NONE;
@@ -213,7 +208,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
   if (y_dtype != q->dtype && y_dtype != SFNN_F32) return SFNN_ERR_INVALID_ARG;
   if (q->T == 0) return SFNN_OK;
   if (!mat_ok(y, y_dtype == SFNN_F32 ? ldy * 2 : ldy, q->d) || ldy < q->d || !err || !ws || !a16(ws) ||
-      ws_bytes < sfnn_gated_workspace(q->T, q->d, q->n, 0))
+      ws_bytes < workspace(q->T, q->d, q->n, 0))
     return SFNN_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int bf16 = q->dtype == SFNN_BF16;
@@ -222,6 +217,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
       launch_act8_quantize(q->x, q->ldx, q->T, q->d, bf16, false, static_cast<uint8_t *>(sv->x), sv->ld_x,
                            sv->x_scales, sv->lds_x, s) != cudaSuccess)
     return SFNN_ERR_CUDA;
+  kernels += kind == SFNN_SAVE_ACT8;
   const int sms = device_sms();
   const bool slim_up = kind == SFNN_SAVE_NONE && slim_serves(q->T, q->n, q->d, true, sms);
   const bool slim_down =
@@ -229,7 +225,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
   float *parts = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + hidden_bytes(q->T, q->n));
   const Operand h{ws, ldh, false}, wd{q->w_down, q->ld_down, q->down_layout == SFNN_DOWN_NEURON_MAJOR};
   auto down = [&](int early) -> sfnn_status {
-    if (!slim_down) return product(h, wd, q->T, q->d, q->n, y, ldy, y_dtype == SFNN_F32, bf16, parts, err, s);
+    if (!slim_down) return product(h, wd, q->T, q->d, q->n, y, ldy, y_dtype == SFNN_F32, bf16, parts, err, s, kernels);
     SlimArgs a{};
     a.x = ws;
     a.ldx = ldh;
@@ -244,6 +240,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
     a.out32 = y_dtype == SFNN_F32;
     a.early = early;
     a.err = err;
+    ++kernels;
     return launch_slim(a, sms, s);
   };
   if (slim_up) {
@@ -263,6 +260,7 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
     a.bf16 = bf16;
     a.err = err;
     if ((st = launch_slim(a, sms, s)) != SFNN_OK) return st;
+    ++kernels;
     return down(1);
   }
   DenseParams P{};
@@ -294,7 +292,23 @@ sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, i
   }
   P.err = err;
   if (launch_dense(P, kEpiGated, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
+  ++kernels;
   return down(0);
+}
+
+}  // namespace
+}  // namespace sfnn
+
+using namespace sfnn;
+
+extern "C" {
+
+int64_t sfnn_gated_workspace(int32_t T, int32_t d, int32_t n, int32_t backward) { return workspace(T, d, n, backward); }
+
+sfnn_status sfnn_gated_forward(const sfnn_gated_desc *q, void *y, int64_t ldy, int32_t y_dtype, sfnn_gated_saved *sv,
+                               void *ws, int64_t ws_bytes, int32_t *err, sfnn_stream_t stream) {
+  int kernels = 0;
+  return forward(q, y, ldy, y_dtype, sv, ws, ws_bytes, err, stream, kernels);
 }
 
 sfnn_status sfnn_gated_backward(const sfnn_gated_desc *q, const void *dy, int64_t lddy, const sfnn_gated_saved *sv,
@@ -416,8 +430,9 @@ sfnn_status sfnn_forward_prompt(sfnn_handle h, const void *X, int32_t T, float *
     q.w_down = rows + 2 * (int64_t)L.d;
     q.ld_gate = q.ld_up = q.ld_down = ld;
     q.b = h->bias;
-    const sfnn_status st = sfnn_gated_forward(&q, Y, L.d, SFNN_F32, nullptr, ws, ws_bytes, h->err, stream);
-    if (st == SFNN_OK) h->launches += 2;
+    int kernels = 0;
+    const sfnn_status st = forward(&q, Y, L.d, SFNN_F32, nullptr, ws, ws_bytes, h->err, stream, kernels);
+    h->launches += kernels;
     return st;
   }
   if (!mat_ok(X, L.d, L.d) || !Y || !a16(Y) || !ws || !a16(ws) || ws_bytes < sfnn_gated_workspace(T, L.d, L.n, 0))
@@ -426,9 +441,10 @@ sfnn_status sfnn_forward_prompt(sfnn_handle h, const void *X, int32_t T, float *
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   float *parts = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + hidden_bytes(T, L.n));
   const Operand x{X, L.d, false}, wu{rows, ld, false}, hh{ws, up(L.n, 8), false}, wd{rows + L.d, ld, true};
-  sfnn_status st = product(x, wu, T, L.n, L.d, ws, up(L.n, 8), 0, 0, nullptr, h->err, s, h->bias);
-  if (st == SFNN_OK) st = product(hh, wd, T, L.d, L.n, Y, L.d, 1, 0, parts, h->err, s);
-  if (st == SFNN_OK) h->launches += 2;
+  int kernels = 0;
+  sfnn_status st = product(x, wu, T, L.n, L.d, ws, up(L.n, 8), 0, 0, nullptr, h->err, s, kernels, h->bias);
+  if (st == SFNN_OK) st = product(hh, wd, T, L.d, L.n, Y, L.d, 1, 0, parts, h->err, s, kernels);
+  h->launches += kernels;
   return st;
 }
 

@@ -270,3 +270,15 @@ def test_mxfp4_linear_says_that_it_has_no_gradient(T):
     assert not y.requires_grad and torch.equal(y, want)
     with fw.dual_level(), pytest.raises((RuntimeError, NotImplementedError)):
         sf.mxfp4_linear(fw.make_dual(x, torch.ones_like(x)), q)
+
+
+@pytest.mark.parametrize("act", ["reglu", "relu"])
+@pytest.mark.parametrize("d,n,T,kernels", [(512, 2051, 33, 3), (512, 2051, 300, 3), (128, 72, 33, 2), (128, 72, 1, 2)])
+def test_prompt_counts_its_launches(d, n, T, kernels, act):
+    """A down product whose K is split (few tiles, many neurons) joins its parts in a kernel of its own."""
+    h = _handle(act, d, n)
+    X = torch.randn(T, d, generator=torch.Generator().manual_seed(1)).half().cuda()
+    before = h.info()["launches"]
+    h.forward_prompt(X)
+    assert h.info()["launches"] - before == kernels
+    h.close()
