@@ -214,7 +214,7 @@ struct SlimArgs {
   int64_t K;
   void *out;
   int64_t ldo;
-  int bf16, out32, relu, early;
+  int bf16, out32, early;
   int32_t *err;
 };
 int64_t slim_cost(int T, int N, int64_t K, bool gated, int num_sms);

@@ -39,7 +39,7 @@ struct alignas(64) SlimParams {
   int m64;              // 64-lane MMAs (a row's accumulators: lane r % 16 of quarter r / 16)
   int early;            // weights may be read before the kernel before has finished
   int tmem_cols, up_col;
-  int bf16, out32, relu;
+  int bf16, out32;
   const void *bias;
   void *out;
   int64_t ldo;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
   const bool busy = worker && quad * (P.m64 ? 16 : 32) < P.nb;
   auto load_bias = [&](int t) {
     const int col = t * P.nb + row;
-    return (GATED || P.relu) && P.bias && row < P.nb && col < P.N ? load16(P.bias, col, P.bf16) : 0.f;
+    return GATED && P.bias && row < P.nb && col < P.N ? load16(P.bias, col, P.bf16) : 0.f;
   };
   // the epilogue of this thread's weight row, with the other parts of a split tile at `sums`
   auto epilogue = [&](int t, float bias, const float *sums) {
@@ -220,11 +220,11 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[i] = __uint_as_float(g[i]);
-        if (GATED || P.relu) {
+        if (GATED) {
           v[i] += bias;
           v[i] = v[i] < 0.f ? 0.f : v[i];
+          v[i] *= __uint_as_float(u[i]);
         }
-        if (GATED) v[i] *= __uint_as_float(u[i]);
       }
       store_tokens(P, col, c, v);
     }
@@ -410,7 +410,6 @@ sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
   P.early = q.early;
   P.bf16 = q.bf16;
   P.out32 = q.out32;
-  P.relu = q.relu;
   P.bias = q.bias;
   P.out = q.out;
   P.ldo = q.ldo;
