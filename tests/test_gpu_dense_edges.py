@@ -282,3 +282,25 @@ def test_prompt_counts_its_launches(d, n, T, kernels, act):
     h.forward_prompt(X)
     assert h.info()["launches"] - before == kernels
     h.close()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4])
+def test_mxfp4_blocks_that_are_not_finite_with_few_tokens(rows):
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, 160, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(96, 160, generator=g, device="cuda").to(torch.bfloat16)
+    q = sf.quantize_mxfp4(w)
+    want = sf.mxfp4_linear(x, q)
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        for t in range(rows):  # one token's block: its whole output, no other token's
+            x2 = x.clone()
+            x2[t, 70] = bad
+            got = sf.mxfp4_linear(x2, q)
+            rest = torch.arange(rows, device="cuda") != t
+            assert got[t].isnan().all() and torch.equal(got[rest], want[rest])
+        w2 = w.clone()  # one weight row's block: its column
+        w2[5, 130] = bad
+        got = sf.mxfp4_linear(x, sf.quantize_mxfp4(w2))
+        keep = torch.arange(96, device="cuda") != 5
+        assert got[:, 5].isnan().all() and torch.equal(got[:, keep], want[:, keep])
+    assert sf.dense_error() == 0
