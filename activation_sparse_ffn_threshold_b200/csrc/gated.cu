@@ -64,7 +64,8 @@ int64_t row_blocks(int64_t T) { return (T + 31) / 32; }
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 int64_t hidden_bytes(int64_t T, int64_t n) { return up(T * up(n, 8) * 2, 256); }
 
-bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool on(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool a16(const void *p) { return on(p, 16); }
 bool mat_ok(const void *p, int64_t ld, int64_t cols) {
   return p && a16(p) && ld >= cols && ld % 8 == 0 && ld <= (1ll << 36);
 }
@@ -80,7 +81,7 @@ sfnn_status check(const sfnn_gated_desc *q) {
   if (!mat_ok(q->w_gate, q->ld_gate, q->d) || !mat_ok(q->w_up, q->ld_up, q->d) ||
       !mat_ok(q->w_down, q->ld_down, q->down_layout == SFNN_DOWN_WIDTH_MAJOR ? q->n : q->d))
     return SFNN_ERR_INVALID_ARG;
-  if (q->T > 0 && !mat_ok(q->x, q->ldx, q->d)) return SFNN_ERR_INVALID_ARG;
+  if ((q->T > 0 && !mat_ok(q->x, q->ldx, q->d)) || !on(q->b, 2)) return SFNN_ERR_INVALID_ARG;
   return SFNN_OK;
 }
 
@@ -92,8 +93,9 @@ sfnn_status check_saved(const sfnn_gated_desc *q, const sfnn_gated_saved *sv) {
   if (sv->ld < nb * kAct8Block || sv->ld % 16 || sv->lds < nb) return SFNN_ERR_INVALID_ARG;
   if (eight && (sv->ld_x < db * kAct8Block || sv->ld_x % 16 || sv->lds_x < db)) return SFNN_ERR_INVALID_ARG;
   if (q->T == 0) return SFNN_OK;
-  if (!sv->r || !sv->u || !sv->r_scales || !sv->u_scales || !a16(sv->r) || !a16(sv->u)) return SFNN_ERR_INVALID_ARG;
-  if (eight && (!sv->x || !sv->x_scales || !a16(sv->x))) return SFNN_ERR_INVALID_ARG;
+  if (!sv->r || !sv->u || !a16(sv->r) || !a16(sv->u)) return SFNN_ERR_INVALID_ARG;
+  if (!sv->r_scales || !sv->u_scales || !on(sv->r_scales, 4) || !on(sv->u_scales, 4)) return SFNN_ERR_INVALID_ARG;
+  if (eight && (!sv->x || !sv->x_scales || !a16(sv->x) || !on(sv->x_scales, 4))) return SFNN_ERR_INVALID_ARG;
   return SFNN_OK;
 }
 
@@ -207,7 +209,7 @@ sfnn_status forward(const sfnn_gated_desc *q, void *y, int64_t ldy, int32_t y_dt
   if (kind != SFNN_SAVE_NONE && (st = check_saved(q, sv)) != SFNN_OK) return st;
   if (y_dtype != q->dtype && y_dtype != SFNN_F32) return SFNN_ERR_INVALID_ARG;
   if (q->T == 0) return SFNN_OK;
-  if (!mat_ok(y, y_dtype == SFNN_F32 ? ldy * 2 : ldy, q->d) || ldy < q->d || !err || !ws || !a16(ws) ||
+  if (!mat_ok(y, y_dtype == SFNN_F32 ? ldy * 2 : ldy, q->d) || ldy < q->d || !err || !on(err, 4) || !ws || !a16(ws) ||
       ws_bytes < workspace(q->T, q->d, q->n, 0))
     return SFNN_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -326,7 +328,8 @@ sfnn_status sfnn_gated_backward(const sfnn_gated_desc *q, const void *dy, int64_
   if ((st = check_saved(q, sv)) != SFNN_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int T = q->T, d = q->d, n = q->n, bf16 = q->dtype == SFNN_BF16;
-  if ((dx && !a16(dx)) || (dw_gate && !a16(dw_gate)) || (dw_up && !a16(dw_up)) || (dw_down && !a16(dw_down)))
+  if ((dx && !a16(dx)) || (dw_gate && !a16(dw_gate)) || (dw_up && !a16(dw_up)) || (dw_down && !a16(dw_down)) ||
+      !on(db, 2))
     return SFNN_ERR_INVALID_ARG;
   if (T == 0) {  // sums over no tokens
     if ((dw_gate && cudaMemsetAsync(dw_gate, 0, (size_t)n * d * 2, s) != cudaSuccess) ||
@@ -336,7 +339,7 @@ sfnn_status sfnn_gated_backward(const sfnn_gated_desc *q, const void *dy, int64_
       return SFNN_ERR_CUDA;
     return SFNN_OK;
   }
-  if (!mat_ok(dy, lddy, d) || !err || !ws || !a16(ws) || ws_bytes < sfnn_gated_workspace(T, d, n, 1))
+  if (!mat_ok(dy, lddy, d) || !err || !on(err, 4) || !ws || !a16(ws) || ws_bytes < sfnn_gated_workspace(T, d, n, 1))
     return SFNN_ERR_INVALID_ARG;
   const int64_t hb = hidden_bytes(T, n), ldh = up(n, 8);
   unsigned char *w = static_cast<unsigned char *>(ws);

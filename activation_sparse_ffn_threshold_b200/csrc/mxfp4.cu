@@ -1025,7 +1025,7 @@ sfnn_status sfnn_mxfp4_product(const void *x_codes, const void *x_scales, int32_
   if (st == SFNN_OK) st = N < 1 ? SFNN_ERR_INVALID_ARG : mx_check(N, K, w_codes, w_scales);
   if (st == SFNN_OK) st = value_check(y, ldy, T, N, y_dtype, true);
   if (st != SFNN_OK || T == 0) return st;
-  if (!err) return SFNN_ERR_INVALID_ARG;
+  if (!err || !aligned(err, 4)) return SFNN_ERR_INVALID_ARG;
   return product(x_codes, x_scales, T, w_codes, w_scales, N, K, y, ldy, y_dtype, err,
                  reinterpret_cast<cudaStream_t>(stream));
 }
@@ -1044,7 +1044,7 @@ sfnn_status sfnn_mxfp4_linear(const void *x, int64_t ldx, int32_t T, int32_t dty
   if (st == SFNN_OK) st = value_check(x, ldx, T, K, dtype, false);
   if (st == SFNN_OK) st = value_check(y, ldy, T, N, y_dtype, true);
   if (st != SFNN_OK || T == 0) return st;
-  if (!err) return SFNN_ERR_INVALID_ARG;
+  if (!err || !aligned(err, 4)) return SFNN_ERR_INVALID_ARG;
   const int64_t need = sfnn_mxfp4_linear_workspace(T, K);
   if (need > 0 && (!ws || !aligned(ws, 16) || ws_bytes < need)) return SFNN_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -1,4 +1,5 @@
-"""Sizes near and beyond the end of 32 bits, refused without a GPU."""
+"""Sizes near and beyond the end of 32 bits and addresses off their alignment, refused without a GPU."""
+import ctypes
 import warnings
 
 import pytest
@@ -6,8 +7,7 @@ import torch
 
 import activation_sparse_ffn_threshold_b200 as sf
 from activation_sparse_ffn_threshold_b200 import dense
-
-UNSUPPORTED = sf.STATUS_CODES["SFNN_ERR_UNSUPPORTED"]
+from test_dense_cpu import INVALID, UNSUPPORTED, desc, forward, saved_of
 
 
 def test_binding_refuses_sizes_that_32_bits_do_not_hold():
@@ -30,3 +30,23 @@ def test_act8_refuses_widths_near_the_end_of_32_bits():
         args = (4096, cols, 1, cols, sf.F16, 0)
         assert lib.sfnn_act8_quantize(*args, 4096, 2 ** 31, 4096, 2 ** 25, None) == UNSUPPORTED, cols
         assert lib.sfnn_act8_restore(4096, 2 ** 31, 4096, 2 ** 25, 1, cols, 0, sf.F16, 4096, cols, None) == UNSUPPORTED, cols
+
+
+def test_addresses_off_their_types_alignment_are_refused():
+    """A kernel that loads or stores there would fault."""
+    lib = sf.load_library()
+    assert forward(desc(b=4097)) == INVALID and forward(desc(), err=4098) == INVALID
+    for kind, name in ((1, "r_scales"), (1, "u_scales"), (2, "r_scales"), (2, "u_scales"), (2, "x_scales")):
+        s = saved_of(kind=kind)
+        setattr(s, name, 4098)
+        assert forward(desc(), saved=s) == INVALID, name
+
+    def back(s=None, db=4096, err=4096):
+        q, s = desc(), s or saved_of()
+        return lib.sfnn_gated_backward(ctypes.byref(q), 4096, 64, ctypes.byref(s), 4096, 4096, 4096, 4096, db, 4096, 1 << 40,
+                                       err, None)
+    s = saved_of()
+    s.u_scales = 4098
+    assert back(s) == INVALID and back(db=4097) == INVALID and back(err=4098) == INVALID
+    assert lib.sfnn_mxfp4_product(4096, 4096, 4, 4096, 4096, 8, 64, 4096, 8, sf.F32, 4098, None) == INVALID
+    assert lib.sfnn_mxfp4_linear(4096, 64, 16, sf.F16, 4096, 4096, 8, 64, 4096, 8, sf.F16, 4096, 1 << 30, 4098, None) == INVALID
