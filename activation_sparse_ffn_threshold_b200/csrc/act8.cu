@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     uint32_t q[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      q[j] = act8_codes(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], s.inv);
+      q[j] = act8_codes<RELU>(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], s.inv);
       if (RELU)  // a relu'd value is positive where its bits are not zero
         q[j] = act8_lift(q[j], __byte_perm(__vminu2(a[2 * j], 0x00010001u), __vminu2(a[2 * j + 1], 0x00010001u), 0x6420));
     }

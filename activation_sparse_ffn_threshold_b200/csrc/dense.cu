@@ -348,7 +348,7 @@ __device__ __forceinline__ void epi_gated(const DenseParams &P, const Unit &Q, u
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float *a = v + 16 * i + 4 * j;
-            q[j] = act8_codes(a[0], a[1], a[2], a[3], inv);
+            q[j] = relu ? act8_codes<true>(a[0], a[1], a[2], a[3], inv) : act8_codes<false>(a[0], a[1], a[2], a[3], inv);
             if (relu) {
               uint32_t pos = 0;
 #pragma unroll

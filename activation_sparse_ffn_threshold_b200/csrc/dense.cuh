@@ -33,9 +33,8 @@ __device__ __forceinline__ float load16(const void *p, int64_t i, bool bf16) {
 
 // ---------------------------------------------------------------- act8
 // 64 values of a row share an fp32 scale: max|v| / 127 with codes -127..127, or for
-// relu(v) max / 255 with codes 0..255.  A code is rint(v / scale), as one multiply-add per value
-// by the scale's reciprocal: off from the nearest code only where two are equally near to
-// within fp32 roundings.  A
+// relu(v) max / 255 with codes 0..255.  A code is the integer nearest to v / scale, the even one
+// where two are equally near (or within 2^-16 of it).  A
 // positive relu'd value keeps a code of at least 1: code > 0 is exactly the ReLU's mask,
 // which the backward pass needs.  A block with a NaN or an infinity gets a NaN scale (and so
 // restores as NaN); a block whose largest magnitude is below 2^-112 gets scale 0.
@@ -45,23 +44,31 @@ struct Act8Scale {
   float scale, inv;
 };
 // `top`: the largest fp32 bit pattern of the block's magnitudes (NaN > inf > finite); below
-// 2^-112 the reciprocal could overflow.
+// 2^-112 the reciprocal could overflow.  inv = qmax / top to half an ulp: an approximate
+// reciprocal and a Newton step, whose residual is exact.
 __device__ __forceinline__ Act8Scale act8_scale(uint32_t top, float qmax) {
   Act8Scale s;
+  float r;
   s.scale = __uint_as_float(top) * (1.f / qmax);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inv) : "f"(s.scale));  // within an ulp: a code is off only next to a tie
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s.scale));
+  s.inv = fmaf(fmaf(-__uint_as_float(top), r, qmax), r * (1.f / qmax), r);
   if (top < 0x07800000u) s.scale = s.inv = 0.f;
   if (top >= 0x7f800000u) s.scale = __uint_as_float(0x7fffffffu);
   return s;
 }
 
-// Codes of four values as bytes: v * inv + 1.5 * 2^23 in one fused multiply-add leaves the
-// nearest integer (ties to even) in the low byte.  |v * inv| <= qmax (1 + 2^-21), so no code
-// leaves its range; in a NaN block the codes mean nothing.
+// Codes of four values as bytes.  16-bit values and their block's largest often meet where
+// v / scale lies exactly between two codes, and v * inv, off by up to 2^-24 of itself, would fall to
+// either side (2.3e-4 of normal fp16 values' codes).  v * inv + 384 (256 where no value is
+// negative) is one fused multiply-add whose sum has a step of 2^-15, so that such a quotient is
+// exact again; adding 1.5 * 2^23 less that then leaves the nearest integer, ties to even, in the
+// low byte.  |v * inv| <= qmax (1 + 2^-23), so no code leaves its range; in a NaN block the codes
+// mean nothing.
+template <bool RELU>
 __device__ __forceinline__ uint32_t act8_codes(float a, float b, float c, float d, float inv) {
-  constexpr float kMagic = 12582912.f;
-  const uint32_t x = __float_as_uint(fmaf(a, inv, kMagic)), y = __float_as_uint(fmaf(b, inv, kMagic));
-  const uint32_t z = __float_as_uint(fmaf(c, inv, kMagic)), w = __float_as_uint(fmaf(d, inv, kMagic));
+  constexpr float kGrid = RELU ? 256.f : 384.f, kMagic = 12582912.f - kGrid;
+  const uint32_t x = __float_as_uint(fmaf(a, inv, kGrid) + kMagic), y = __float_as_uint(fmaf(b, inv, kGrid) + kMagic);
+  const uint32_t z = __float_as_uint(fmaf(c, inv, kGrid) + kMagic), w = __float_as_uint(fmaf(d, inv, kGrid) + kMagic);
   return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
 }
 // ... and of four relu'd values: a positive one whose code is 0 gets code 1 (`positive`: bit 0

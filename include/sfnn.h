@@ -522,7 +522,8 @@ SFNN_API sfnn_status sfnn_forward_prompt(sfnn_handle h, const void *X, int32_t T
  * 8-bit activation blocks.  Each 64 values of a row (the last block may be short) share an
  * fp32 scale: with relu = 0, max|v| / 127 and signed codes; with relu = 1, relu(v) is held,
  * scale max / 255 and codes 0..255, and a positive value keeps a code of at least 1, so
- * that code > 0 is the ReLU's mask.  code = rint(v / scale).  A block with a NaN or an
+ * that code > 0 is the ReLU's mask.  A code is the integer nearest to v / scale, the even one
+ * of two that are equally near (or within 2^-16 of it).  A block with a NaN or an
  * infinity restores as NaN; one whose largest magnitude is below 2^-112 is held as zeros.
  * x [T x cols] fp16 or bf16 values, any row stride; code rows ldq bytes apart (a multiple
  * of 16, at least cols rounded up to 64; columns past cols get code 0), 16-byte aligned;

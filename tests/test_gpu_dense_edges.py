@@ -304,3 +304,34 @@ def test_mxfp4_blocks_that_are_not_finite_with_few_tokens(rows):
         keep = torch.arange(96, device="cuda") != 5
         assert got[:, 5].isnan().all() and torch.equal(got[:, keep], want[:, keep])
     assert sf.dense_error() == 0
+
+
+@pytest.mark.parametrize("dt", KINDS)
+@pytest.mark.parametrize("relu", [False, True])
+def test_act8_codes_are_the_nearest_ties_to_even(relu, dt):
+    """In whole numbers: 16-bit values and their block's largest often meet where a quotient lies
+    exactly between two codes.  (Quotients that are not there but within 2^-15 of it may go as if.)"""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (torch.randn(4000, 512, generator=g, device="cuda") * torch.exp(torch.randn(4000, 1, generator=g, device="cuda"))).to(dt)
+    x[:64] = (torch.randint(-255, 256, (64, 512), generator=g, device="cuda") / 2).to(dt)  # halves: many ties
+    x[:64, ::64] = 255.0 if relu else 127.0
+    q = sf.quantize_act8(x, relu=relu)
+    codes = (q.codes if relu else q.codes.view(torch.int8)).long().view(-1, 64)
+    top = 255 if relu else 127
+    v = (x.float() * 2.0 ** 20).round().long().view(-1, 64)  # exact, but for bits below 2^-20 of values that small
+    x20 = v.double() * 2.0 ** -20
+    exact = (x20 == x.double().view(-1, 64)).all(1)  # blocks without such
+    if relu:
+        v = v.clamp_min(0)
+    m = v.abs().amax(1, keepdim=True)
+    exact &= m[:, 0] > 0
+    two = 2 * top * v.abs()  # twice the quotient, times m
+    k = two // (2 * m).clamp_min(1)
+    rest = two - 2 * m * k   # 0 .. 2 m: the half is m
+    want = torch.where(rest > m, k + 1, torch.where(rest < m, k, k + (k & 1)))
+    if relu:
+        want = torch.where((v > 0) & (want < 1), 1, want)
+    near_half = (rest != m) & ((rest - m).abs().double() < 2 * m.double() * 2.0 ** -15)
+    ok = (codes == want * v.sign()) | (near_half & ((codes.abs() - want).abs() <= 1))
+    assert exact.sum() > 1000 and (rest[exact] == m[exact].expand_as(rest[exact])).sum() > 1000  # the ties are there
+    assert ok[exact].all(), f"{int((~ok[exact]).sum())} codes of {int(exact.sum()) * 64}"
