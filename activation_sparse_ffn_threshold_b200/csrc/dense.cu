@@ -15,9 +15,10 @@
 // (TMA, 128-byte swizzle), warp 1 of the pair's first CTA issues the MMAs, warps 2-9 run
 // the epilogue of the tile before out of the other half of tensor memory (2 x 256 columns).
 //
-// Measured (4096 x 11008 bf16, 4096 tokens): forward and backward 2.35 ms, 1.41 PFLOP/s, what
-// the power cap leaves a dense product for long; the tensor pipe is busy 60 to 77 % of a
-// kernel's cycles alone.  What it waits for there: the last round of tiles, and L2.
+// Measured (4096 x 11008 bf16, 4096 tokens): forward and backward 2.56 to 2.64 ms on several cards,
+// 1.26 to 1.30 PFLOP/s (a library product holds 1.39 for long under the power cap); the tensor
+// pipe is busy 57 to 77 % of a kernel's cycles alone.  What it waits for there: the last round
+// of tiles, and L2.
 //
 // Every wait is bounded (about a second); one that runs out latches SFNN_ERR_TIMEOUT and the
 // kernel leaves in order: its loads have landed by then, tensor memory is freed.

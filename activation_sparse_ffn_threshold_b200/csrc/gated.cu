@@ -127,9 +127,10 @@ int64_t parts_bytes(int64_t M, int64_t N, int nk, int sms) {
 }
 
 // Columns of a tile: 128 where that many tiles still fit one round of CTA pairs (a tile's
-// latency counts: step of 257 tokens, 512 x 2048, 46.7 us against 51.8 with 256).  Beyond, 256,
-// even where halves would fill the last round better: they read each operand byte for half
-// the products (4096 tokens, 4096 x 11008, with halves in the down product: 2585 us against 2365).
+// latency counts: step of 257 tokens, 512 x 2048, 46.7 us against 51.8 with 256, timed in turn; 52
+// to 57 with 128 on other cards and hosts).  Beyond, 256, even where halves would fill the last
+// round better: they read each operand byte for half the products (4096 tokens, 4096 x 11008,
+// with halves in the down product: 1.09 times as long).
 int tile_columns(int M, int N, int split, int sms) {
   return (int64_t)((M + 255) / 256) * ((N + 127) / 128) * split <= sms / 2 ? 128 : 256;
 }

@@ -14,9 +14,9 @@
 // Product: Y = (Xq 2^ex) . (Wq 2^ew)^T with tcgen05's block-scaled MMA (kind::mxf4, K = 64 an
 // instruction, four times the 16-bit rate), fp32 accumulators.  At that rate a 256 x 256 x 256
 // step of a CTA pair takes 512 cycles; the six copies of its scales into tensor memory take
-// their turn in the same pipe and add about 300 (4096 x 28672 x 8192: about 470 us, 4.1 PFLOP/s;
-// 337 with the copies left out).  Issuing them a step ahead (499 us) or writing the scales
-// from registers by four warps of their own (760 us) measured slower.
+// their turn in the same pipe and add about 300 (4096 x 28672 x 8192: 470 us, 337 with the copies
+// left out; issuing them a step ahead 499, writing the scales from registers by four warps of
+// their own 760, all timed in turn.  511 to 529 us, 3.7 PFLOP/s, for seconds on several cards).
 #include <algorithm>
 
 #include "common.cuh"
@@ -65,7 +65,8 @@ constexpr int kVecs = 8;
 constexpr int kChunk = 32 * kVecs * 8;  // columns per warp
 
 // A warp takes 2048 columns of one (padded) row: 8 values a lane at a time, all its loads
-// requested first; four lanes hold a block.  Bound by bytes (2 read, 0.53 written a value).
+// requested first; four lanes hold a block.  Bound by instructions: 11008 x 4096 takes 35 us with 0.77
+// of the issue slots in use, its bytes (2 read, 0.53 written a value) 17.5 at the copy rate.
 __global__ void __launch_bounds__(kWarps * 32)
     k_mx_quantize(const uint16_t *__restrict__ x, int64_t ldx, int64_t R, int K, int bf16, int vec,
                   uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
@@ -452,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_mx(co
 // multiply.  A negative weight's byte is its one's complement; the sum of x over the negative
 // weights, which that takes too much, is added back by a second dp4a on the sign bytes.
 //
-// Measured: 1 token, 11008 x 4096: 10.4 us, 0.63 of the issue slots (the bytes alone: 3.7).
+// Measured: 1 token, 11008 x 4096: 10.1 to 10.5 us, 0.63 of the issue slots (the bytes alone: 3.7).
 //
 // A CTA owns a contiguous share of the rows, a warp takes one row at a time: a lane holds 32
 // values (16 bytes) of every 1024, a row's loads go out while the row before is multiplied.

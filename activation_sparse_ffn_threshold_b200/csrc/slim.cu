@@ -13,8 +13,9 @@
 // A stage holds at least two 64-deep chunks of every row: 256 contiguous bytes of it (TMA,
 // 128-byte swizzle).
 //
-// Measured: 37 tokens, 8192 x 28672 bf16, both kernels 226 us (6.2 TB/s of weights); 1 token,
-// 4096 x 11008 fp16, 54.6 us: 6.4 and 7.1 TB/s while they stream, 12 us of ends and beginnings.
+// Measured: 37 tokens, 8192 x 28672 bf16, both kernels 243 to 267 us on several cards (5.3 to 5.8
+// TB/s of weights); 1 token, 4096 x 11008 fp16, 53.9 us: 6.4 and 7.1 TB/s while they stream, 12 us
+// of ends and beginnings.
 #include <algorithm>
 
 #include "common.cuh"
@@ -398,8 +399,9 @@ sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
   while (P.tmem_cols < P.up_col + up_to(P.t16, 32)) P.tmem_cols *= 2;
   const int chunk = (P.t8 + np * P.nb8) * 128;
   const int over = std::max(0, (P.m64 ? 8192 : 16384) - P.nb8 * 128);  // an MMA reads all its lanes' rows
-  // All of shared memory in flight (1 token, 4096 x 11008: 54.6 us; with 131 and 83 KB, so that
-  // the gate/up and the down kernel share an SM, 59.0; 37 tokens, 8192 x 28672: 226 and 254).
+  // All of shared memory in flight (timed in turn: 1 token, 4096 x 11008, 54.6 us; with 131 and 83
+  // KB, so that the gate/up and the down kernel share an SM, 59.0; 37 tokens, 8192 x 28672, 0.89 of
+  // the time).
   const int budget = 190 * 1024;
   const int parts = (P.split - 1) * np * P.T * 512;  // bytes of the other ranks' accumulators
   P.apart = parts <= 16 * 1024;

@@ -435,9 +435,10 @@ SFNN_API sfnn_status sfnn_get_error(sfnn_handle h);
  *     dX = dG . W_gate + dU . W_up,  dW_gate = dG^T . X,  dW_up = dU^T . X,
  *     dW_down = dY^T . H,  db = sum over tokens of dG.
  *
- * fp16 or bf16 values (fp32: SFNN_ERR_UNSUPPORTED), fp32 sums on the tensor cores; H, dG
- * and dU are rounded to the values' type between the products that make and read them (fp16:
- * to infinity beyond its range); db adds up dG before it is rounded.
+ * fp16 or bf16 values (fp32: SFNN_ERR_UNSUPPORTED), fp32 sums on the tensor cores; H, dG, dU
+ * and an X restored from 8-bit blocks are rounded to the values' type between the products
+ * that make and read them (fp16: to infinity beyond its range); db adds up dG before it is
+ * rounded.
  * These calls need no handle: weights are read where the caller keeps them, and the caller
  * gives the workspace (sfnn_gated_workspace bytes, 16-byte aligned), which is free again
  * when the call's kernels have run and must not be shared by calls that run at the same
