@@ -335,3 +335,43 @@ def test_act8_codes_are_the_nearest_ties_to_even(relu, dt):
     ok = (codes == want * v.sign()) | (near_half & ((codes.abs() - want).abs() <= 1))
     assert exact.sum() > 1000 and (rest[exact] == m[exact].expand_as(rest[exact])).sum() > 1000  # the ties are there
     assert ok[exact].all(), f"{int((~ok[exact]).sum())} codes of {int(exact.sum()) * 64}"
+
+
+@pytest.mark.parametrize("T,n,spread", [(3, 72, 0.0), (130, 200, 1.0), (257, 520, 3.0), (40, 64, 8.0)])
+def test_full_codes_hold_what_they_promise(T, n, spread):
+    """relu(G) and U as they are kept, of any size: one product each, exact in 32 bits, under
+    factors from 2^-60 to 2^60 a token and neurons spread over many octaves."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x = torch.zeros(T, 8, device="cuda", dtype=torch.bfloat16)
+    x[:, 0] = (r(T) * 2.0 ** torch.randint(-60, 61, (T,), generator=g, device="cuda")).bfloat16()
+    wg, wu = (torch.zeros(n, 8, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    for w in (wg, wu):
+        w[:, 0] = (r(n) * torch.exp(spread * r(n))).clamp(-2.0 ** 60, 2.0 ** 60).bfloat16()
+    x[0], wg[5], wu[7] = 0, 0, -0.0
+    if T > 100:  # largest values that round up to a power of two
+        x[1, 0], wg[64:128, 0], wu[64:128, 0] = 255 / 256, 1 + 127 / 128, -1 - 127 / 128
+    _, s = sf.gated_ffn_forward(x, wg, wu, torch.zeros(8, n, device="cuda", dtype=torch.bfloat16), save="full")
+    G, U = (x[:, :1].double() @ w[:, :1].double().t() for w in (wg, wu))
+    for codes, scales, v, bits, signed in ((s.r, s.r_scales, G.clamp_min(0), 13, False), (s.u, s.u_scales, U, 12, True)):
+        c = codes[:, :n].long() & 0xffff
+        m = c & 0x7fff if signed else c
+        meet = 10 << (bits - 1)
+        word = torch.minimum(2 * m, m + meet) << (23 - bits)
+        P = scales.double().repeat_interleave(64, 1)[:, :n]
+        held = word.int().view(torch.float32).double() * 2.0 ** 115 * P
+        if signed:
+            held = torch.where(c >= 0x8000, -held, held)
+        else:
+            assert torch.equal(c > 0, v > 0)
+        # the scale: the power of two at or below the largest (or the next, which that rounds to), 2^-101 at least
+        top = torch.nn.functional.pad(v.abs(), (0, -n % 64)).view(T, -1, 64).amax(2)
+        S = scales.double()
+        assert torch.equal(torch.frexp(S).mantissa, torch.full_like(S, 0.5)) and (S >= 2.0 ** -101).all()
+        assert ((S <= top * (1 + 2.0 ** -bits)) & (top < 2 * S) | (S == 2.0 ** -101) & (top < 2 * S)).all()
+        step = torch.where(v.abs() >= P / 4, 2.0 ** -(bits + 1), 2.0 ** -bits).double()
+        tol = torch.maximum(v.abs() * step, P * 2.0 ** -(bits + 11))
+        if not signed:
+            tol = torch.where(c == 1, torch.maximum(tol, P * 2.0 ** -(bits + 10)), tol)  # lifted: a whole step
+        assert ((held - v).abs() <= tol * (1 + 2.0 ** -10)).all()
+    assert sf.dense_error() == 0
