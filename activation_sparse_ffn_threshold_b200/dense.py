@@ -55,7 +55,8 @@ def _err_ptr(index: int) -> int:
     if p is None:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the first dense call on a device allocates its error word: make one before capturing")
-        w = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", index))
+        with torch.inference_mode(False):  # an inference tensor could not be cleared outside that mode
+            w = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", index))
         torch.cuda.synchronize(index)  # zeroed before a call on another stream uses it
         _err_words[index] = w
         p = _err_ptrs[index] = w.data_ptr()

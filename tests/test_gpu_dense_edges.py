@@ -375,3 +375,15 @@ def test_full_codes_hold_what_they_promise(T, n, spread):
             tol = torch.where(c == 1, torch.maximum(tol, P * 2.0 ** -(bits + 10)), tol)  # lifted: a whole step
         assert ((held - v).abs() <= tol * (1 + 2.0 ** -10)).all()
     assert sf.dense_error() == 0
+
+
+def test_error_word_made_in_inference_mode_can_be_cleared(monkeypatch):
+    from activation_sparse_ffn_threshold_b200 import dense
+    monkeypatch.setattr(dense, "_err_words", {})
+    monkeypatch.setattr(dense, "_err_ptrs", {})
+    x, wg, wu, wd, b, dy = layer(4, 64, 128, torch.float16, seed=1)
+    with torch.inference_mode():  # the first call, which allocates the word
+        sf.gated_ffn_forward(x, wg, wu, wd, b)
+        torch.cuda.synchronize()
+        dense._err_words[torch.cuda.current_device()].fill_(5)  # as a wait that ran out would
+    assert sf.dense_error() == 5 and sf.dense_error() == 0
