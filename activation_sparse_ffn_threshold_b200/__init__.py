@@ -18,6 +18,11 @@ The dense operators (no handle, fp16 or bf16, differentiable) are in ``dense``:
     y, saved = gated_ffn_forward(...); grads = gated_ffn_backward(dy, saved, ...)
     q = quantize_act8(x); x = dequantize_act8(q)                   # 8-bit activation blocks
     w = quantize_mxfp4(weight); y = mxfp4_linear(x, w)             # 4-bit weights and activations
+
+What surrounds them in a block and a training step is in ``block``:
+
+    r, h = residual_norm(x, z, pre="rms", w=w)      # r = x + z, h = norm(r); post norm, gate, scales
+    norm = clip_grad_norm(grads, 1.0)               # global norm and clipping over many tensors
 """
 from __future__ import annotations
 
@@ -32,7 +37,8 @@ __all__ = ["SparseFFN", "SfnnError", "forward_stack", "predict_noalloc", "hotnes
            "RELU", "REGLU", "F32", "F16", "I8", "I4", "BATCH_AUTO", "BATCH_CUDA_CORE", "BATCH_TENSOR_CORE",
            "BATCH_FUSED", "BF16", "gated_ffn", "gated_ffn_forward", "gated_ffn_backward", "GatedSaved",
            "quantize_act8", "dequantize_act8", "Act8", "dense_error", "quantize_mxfp4", "dequantize_mxfp4", "mxfp4_matmul",
-           "mxfp4_linear", "Mxfp4"]
+           "mxfp4_linear", "Mxfp4", "residual_norm", "residual_norm_forward", "residual_norm_backward", "NormSaved",
+           "clip_grad_norm"]
 
 RELU, REGLU = 0, 1
 F32, F16, I8, I4, BF16 = 0, 1, 2, 3, 4
@@ -83,7 +89,7 @@ def load_library():
         raise ImportError(f"{_LIB_PATH} is missing: build it with "
                           f"`python -m activation_sparse_ffn_threshold_b200.build` (nvcc, sm_100a)")
     lib = ctypes.CDLL(_LIB_PATH)
-    P, I, L, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int
+    P, I, L, S, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int, ctypes.c_float
     sig = {
         "sfnn_create": ([ctypes.POINTER(LayerDesc), P, ctypes.POINTER(P)], S),
         "sfnn_destroy": ([P], S),
@@ -119,6 +125,11 @@ def load_library():
         "sfnn_mxfp4_product": ([P, P, I, P, P, I, I, P, L, I, P, P], S),
         "sfnn_mxfp4_linear_workspace": ([I, I], L),
         "sfnn_mxfp4_linear": ([P, L, I, I, P, P, I, I, P, L, I, P, L, P, P], S),
+        "sfnn_norm_workspace": ([I, I], L),
+        "sfnn_norm_forward": ([P, P, L, P, L, P, P], S),
+        "sfnn_norm_backward": ([P, P, P, L, P, L, P, P, P, P, P, P, P, P, L, P], S),
+        "sfnn_clip_workspace": ([I], L),
+        "sfnn_clip_grad_norm": ([P, I, F, F, F, P, P, L, P], S),
         "sfnn_act8_restore": ([P, L, P, L, I, I, I, I, P, L, P], S),
     }
     for name, (args, res) in sig.items():
@@ -439,3 +450,5 @@ def forward_stack(layers, X0, XL=None, idx=None, counts=None, return_sets: bool 
 
 from .dense import (Act8, GatedSaved, Mxfp4, dense_error, dequantize_act8, dequantize_mxfp4, gated_ffn,  # noqa: E402
                     gated_ffn_backward, gated_ffn_forward, mxfp4_linear, mxfp4_matmul, quantize_act8, quantize_mxfp4)
+from .block import (NormSaved, clip_grad_norm, residual_norm, residual_norm_backward,  # noqa: E402
+                    residual_norm_forward)

@@ -86,7 +86,8 @@ typedef enum {
 } sfnn_status;
 
 typedef enum { SFNN_RELU = 0, SFNN_REGLU = 1 } sfnn_act;
-/* SFNN_BF16: the dense operators only (sfnn_gated_*, sfnn_act8_*, sfnn_mxfp4_*). */
+/* SFNN_BF16: the operators without a handle (sfnn_gated_*, sfnn_act8_*, sfnn_mxfp4_*, sfnn_linear_*,
+ * sfnn_norm_*, sfnn_clip_*). */
 typedef enum { SFNN_F32 = 0, SFNN_F16 = 1, SFNN_I8 = 2, SFNN_I4 = 3, SFNN_BF16 = 4 } sfnn_dtype;
 
 /*
@@ -562,6 +563,71 @@ SFNN_API int64_t sfnn_mxfp4_linear_workspace(int32_t T, int32_t K);
 SFNN_API sfnn_status sfnn_mxfp4_linear(const void *x, int64_t ldx, int32_t T, int32_t dtype, const void *w_codes,
                                        const void *w_scales, int32_t N, int32_t K, void *y, int64_t ldy, int32_t y_dtype,
                                        void *ws, int64_t ws_bytes, int32_t *err, sfnn_stream_t stream);
+
+/*
+ * The norms before and after a block, with its gate and residual scale:
+ *
+ *     R = residual_scale * X + branch_scale * gate * post(Z),   H = pre(R)
+ *
+ * X [T x d] the residual stream, Z [T x d] the block's output (NULL: R is X, not written), pre and
+ * post each none, v rsqrt(mean v^2 + eps) * w + b, or (v - mean v) rsqrt(var v + eps) * w + b; w and b
+ * may be NULL (ones, zeros), gate NULL (ones), a row for all tokens (ldg = 0) or one for each.  H, w,
+ * b and gate are fp16 or bf16 (dtype), X and Z of that type or fp32, R and dR, dX of X's type, dZ of
+ * Z's.  Sums and norms are fp32; H is formed from R before its rounding.
+ * d up to 32768, any row stride of at least d, T up to 2^28; T = 0 is valid.  Rows that all start on 16
+ * bytes with d a multiple of 8 are read by vectors.  R may be X (the same rows), else nothing that is
+ * written may overlap anything else.
+ */
+typedef enum { SFNN_NORM_NONE = 0, SFNN_NORM_RMS = 1, SFNN_NORM_LAYER = 2 } sfnn_norm;
+typedef struct {
+    int32_t T, d;
+    int32_t dtype;            /* SFNN_F16 or SFNN_BF16 */
+    int32_t x_dtype, z_dtype; /* dtype or SFNN_F32 */
+    int32_t pre, post;        /* sfnn_norm */
+    float eps, residual_scale, branch_scale; /* residual_scale must be 1 without z */
+    const void *x;
+    int64_t ldx;
+    const void *z;
+    int64_t ldz;
+    const void *gate;
+    int64_t ldg;
+    const void *w, *b, *post_w, *post_b; /* [d] */
+} sfnn_norm_desc;
+
+/* stats (may be NULL) [T x 4], 16-byte aligned: what the backward pass needs besides the inputs. */
+SFNN_API sfnn_status sfnn_norm_forward(const sfnn_norm_desc *q, void *r, int64_t ldr, void *h, int64_t ldh, float *stats,
+                                       sfnn_stream_t stream);
+/* The gradients from dR [T x d] and dH [T x d] (either may be NULL: zeros), contiguous; a NULL one is
+ * not computed.  dgate: [d] for one row of gates, else [T x d].  Sums over the tokens are fp32, in an
+ * order that the sizes and the device alone decide.  ws: sfnn_norm_workspace bytes, 16-byte aligned,
+ * shared with no call that runs at the same time. */
+SFNN_API int64_t sfnn_norm_workspace(int32_t T, int32_t d);
+SFNN_API sfnn_status sfnn_norm_backward(const sfnn_norm_desc *q, const float *stats, const void *dr, int64_t lddr,
+                                        const void *dh, int64_t lddh, void *dx, void *dz, void *dgate, void *dw, void *db,
+                                        void *dpost_w, void *dpost_b, void *ws, int64_t ws_bytes, sfnn_stream_t stream);
+
+/*
+ * The norm of all gradients together, and their clipping:
+ *
+ *     n = scale * sqrt(sum over all tensors of g^2),   out = g * scale * min(1, max_norm / (n + eps))
+ *
+ * grads: HOST array of `count` tensors of fp16, bf16 or fp32 values without gaps, any alignment of
+ * their type; out has the type of in and is in itself, or overlaps nothing else that the call reads
+ * or writes (else SFNN_ERR_INVALID_ARG).  norm [1]: n.  A NaN, or an infinite n where max_norm is
+ * infinite, makes every out NaN; an infinite n otherwise makes it 0 (NaN where g is infinite).
+ * Squares are summed in 64 bits (8 at a time in 32 where those hold them), in an order that the sizes
+ * and the device alone decide.  ws: sfnn_clip_workspace bytes, 8-byte aligned, shared with no call
+ * that runs at the same time.
+ */
+typedef struct {
+    const void *in;
+    void *out;
+    int64_t numel;
+    int64_t dtype; /* sfnn_dtype */
+} sfnn_grad;
+SFNN_API int64_t sfnn_clip_workspace(int32_t count);
+SFNN_API sfnn_status sfnn_clip_grad_norm(const sfnn_grad *grads, int32_t count, float max_norm, float scale, float eps,
+                                         float *norm, void *ws, int64_t ws_bytes, sfnn_stream_t stream);
 
 /* Static description of a status code; never NULL. */
 SFNN_API const char *sfnn_status_str(sfnn_status s);
