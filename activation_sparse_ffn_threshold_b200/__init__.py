@@ -19,8 +19,9 @@ The dense operators (no handle, fp16 or bf16, differentiable) are in ``dense``:
     q = quantize_act8(x); x = dequantize_act8(q)                   # 8-bit activation blocks
     w = quantize_mxfp4(weight); y = mxfp4_linear(x, w)             # 4-bit weights and activations
 
-What surrounds them in a block and a training step is in ``block``:
+What else a block and its training step need is in ``block``:
 
+    y = linear(x, w, b, act="relu", residual=r)     # act(x w^T + b) + residual, differentiable
     r, h = residual_norm(x, z, pre="rms", w=w)      # r = x + z, h = norm(r); post norm, gate, scales
     norm = clip_grad_norm(grads, 1.0)               # global norm and clipping over many tensors
 """
@@ -38,7 +39,7 @@ __all__ = ["SparseFFN", "SfnnError", "forward_stack", "predict_noalloc", "hotnes
            "BATCH_FUSED", "BF16", "gated_ffn", "gated_ffn_forward", "gated_ffn_backward", "GatedSaved",
            "quantize_act8", "dequantize_act8", "Act8", "dense_error", "quantize_mxfp4", "dequantize_mxfp4", "mxfp4_matmul",
            "mxfp4_linear", "Mxfp4", "residual_norm", "residual_norm_forward", "residual_norm_backward", "NormSaved",
-           "clip_grad_norm"]
+           "clip_grad_norm", "linear", "linear_forward", "linear_backward", "LinearSaved"]
 
 RELU, REGLU = 0, 1
 F32, F16, I8, I4, BF16 = 0, 1, 2, 3, 4
@@ -125,6 +126,10 @@ def load_library():
         "sfnn_mxfp4_product": ([P, P, I, P, P, I, I, P, L, I, P, P], S),
         "sfnn_mxfp4_linear_workspace": ([I, I], L),
         "sfnn_mxfp4_linear": ([P, L, I, I, P, P, I, I, P, L, I, P, L, P, P], S),
+        "sfnn_linear_workspace": ([I, I, I, I], L),
+        "sfnn_linear_slope_bytes": ([I, I, I], L),
+        "sfnn_linear_forward": ([P, P, L, P, L, P, P, L, P, P], S),
+        "sfnn_linear_backward": ([P, P, P, L, P, P, P, P, L, P, P], S),
         "sfnn_norm_workspace": ([I, I], L),
         "sfnn_norm_forward": ([P, P, L, P, L, P, P], S),
         "sfnn_norm_backward": ([P, P, P, L, P, L, P, P, P, P, P, P, P, P, L, P], S),
@@ -450,5 +455,5 @@ def forward_stack(layers, X0, XL=None, idx=None, counts=None, return_sets: bool 
 
 from .dense import (Act8, GatedSaved, Mxfp4, dense_error, dequantize_act8, dequantize_mxfp4, gated_ffn,  # noqa: E402
                     gated_ffn_backward, gated_ffn_forward, mxfp4_linear, mxfp4_matmul, quantize_act8, quantize_mxfp4)
-from .block import (NormSaved, clip_grad_norm, residual_norm, residual_norm_backward,  # noqa: E402
-                    residual_norm_forward)
+from .block import (LinearSaved, NormSaved, clip_grad_norm, linear, linear_backward, linear_forward,  # noqa: E402
+                    residual_norm, residual_norm_backward, residual_norm_forward)

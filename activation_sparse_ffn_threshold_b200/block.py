@@ -1,10 +1,10 @@
-"""What surrounds the feed-forward products in a block and in its training step: the norms before
-and after a block with its gate and residual scale, and the clipping of gradients.
+"""What else a block and its training step need: the linear layer with bias, activation and residual,
+the norms before and after a block with its gate and residual scale, and the clipping of gradients.
 
 As ``dense``, this module only checks and marshals arguments into ``libsfnn.so``
 (include/sfnn.h); tensors lie on one CUDA device, and results belong to the current stream (or to
-``stream``, which the call then runs on).  Autograd follows ``residual_norm``; the functions with
-``_forward`` and ``_backward`` are its passes as plain calls.
+``stream``, which the call then runs on).  Autograd follows ``linear`` and ``residual_norm``; the
+functions with ``_forward`` and ``_backward`` are their passes as plain calls.
 """
 from __future__ import annotations
 
@@ -14,11 +14,150 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import BF16, F16, F32, _check, load_library
-from .dense import _CODES, _follows, _on, _raw_stream, _rows, _vp
+from .dense import _CODES, _code, _err_ptr, _follows, _mat, _on, _raw_stream, _rows, _same_device, _vp
 
-__all__ = ["residual_norm", "residual_norm_forward", "residual_norm_backward", "NormSaved", "clip_grad_norm"]
+__all__ = ["linear", "linear_forward", "linear_backward", "LinearSaved", "residual_norm", "residual_norm_forward", "residual_norm_backward", "NormSaved", "clip_grad_norm"]
 
+ACTS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "silu": 3}
 NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
+
+
+# ------------------------------------------------------------------ linear
+class _LinearDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("b", ctypes.c_void_p)]
+
+
+class LinearSaved:
+    """What linear_forward keeps for linear_backward: a reference to x, and act' (None without an
+    activation): a bit per value for a ReLU, 16 bits for the others."""
+
+    __slots__ = ("x", "slopes", "act", "N", "y_dtype", "has_b")
+
+    def __init__(self, x, slopes, act, N, y_dtype, has_b):
+        self.x, self.slopes, self.act, self.N, self.y_dtype, self.has_b = x, slopes, act, N, y_dtype, has_b
+
+    @property
+    def nbytes(self) -> int:
+        """Bytes held, x included."""
+        return self.x.numel() * self.x.element_size() + (0 if self.slopes is None else self.slopes.numel())
+
+
+def _linear_desc(x, w, b, act, y_dtype):
+    """(descriptor, N) of a layer's inputs."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    dt = x.dtype
+    code = _code(dt)
+    px, T, K, ldx = _mat(x, "x", dt)
+    pw, N, _, ldw = _mat(w, "w", dt, None, K)
+    if not K or K % 8 or not N:
+        raise ValueError(f"w must be [N, K] with K a positive multiple of 8, got {tuple(w.shape)}")
+    if y_dtype != dt and y_dtype != torch.float32:
+        raise TypeError(f"the output is {dt} or fp32, not {y_dtype}")
+    pb = _channels(b, "b", N, dt)
+    _same_device(x.get_device(), w, b)
+    return _LinearDesc(T, K, N, code, F32 if y_dtype == torch.float32 else code, act, px, ldx, pw, ldw, pb), N
+
+
+def linear_forward(x, w, b=None, act=None, residual=None, out_dtype=None, save=False, out=None, stream=None):
+    """(y, saved): y = act(x w^T + b) + residual.
+
+    x [..., K], w [N, K], b [N] or None in fp16 or bf16, K a multiple of 8 and rows 16-byte aligned;
+    ``act``: None, "relu", "gelu" (z Phi(z)) or "silu".  y [..., N] has the residual's type, x's or
+    fp32, or without one ``out_dtype`` (default: x's).  ``out`` takes y and may be the residual itself;
+    ``saved`` (with ``save``) goes to linear_backward."""
+    if act not in ACTS:
+        raise ValueError("act must be None, 'relu', 'gelu' or 'silu'")
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    kind = ACTS[act]
+    dt = out_dtype or (x.dtype if residual is None else residual.dtype)
+    q, N = _linear_desc(x, w, b, kind, dt)
+    index = x.get_device()
+    shape = x.shape[:-1] + (N,)
+    pr, ldr, py, ldy = None, 0, None, N
+    for t, name in ((residual, "residual"), (out, "out")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != dt or t.shape != shape or t.get_device() != index:
+            raise ValueError(f"{name} must be a {dt} tensor of shape {tuple(shape)} on x's device")
+        p, r, _, ld = _rows(t, name, N)
+        if r and ld < N:
+            raise ValueError(f"{name}: rows must not overlap")
+        if t is out:
+            py, ldy = p, ld
+        if t is residual:
+            pr, ldr = p, ld
+    lib = load_library()
+    with _on(index, stream):
+        if out is None:
+            out = x.new_empty(shape, dtype=dt)
+            py = out.data_ptr()
+        slopes = None
+        if save and kind:
+            slopes = x.new_empty(lib.sfnn_linear_slope_bytes(q.T, N, kind), dtype=torch.uint8)
+        if q.T:
+            nbytes = lib.sfnn_linear_workspace(q.T, q.K, N, 0)
+            ws = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+            _check(lib.sfnn_linear_forward(ctypes.byref(q), pr, ldr, py, ldy, _vp(slopes), _vp(ws), nbytes,
+                                           _err_ptr(index), _raw_stream(index)), "sfnn_linear_forward")
+    return out, LinearSaved(x, slopes, kind, N, dt, b is not None) if save else None
+
+
+def linear_backward(dy, saved: LinearSaved, w, need=(True, True, True), stream=None):
+    """(dx, dw, db) from dy [..., N] (of y's type) and a forward pass's ``saved``; those that ``need``
+    leaves out, and db without a bias, are None.  The residual's gradient is dy itself."""
+    x = saved.x
+    q, N = _linear_desc(x, w, None, saved.act, saved.y_dtype)
+    index = x.get_device()
+    if N != saved.N:
+        raise ValueError("w must have the forward pass's shape")
+    if not isinstance(dy, torch.Tensor) or dy.dtype != saved.y_dtype or dy.shape != x.shape[:-1] + (N,) \
+            or dy.get_device() != index:
+        raise ValueError(f"dy must be a {saved.y_dtype} tensor of the output's shape on x's device")
+    pdy, r, _, lddy = _rows(dy, "dy", N)
+    if r and lddy < N:
+        raise ValueError("dy: rows must not overlap")
+    lib = load_library()
+    with _on(index, stream):
+        new = x.new_empty
+        dx = new(x.shape) if need[0] else None
+        dw = new(w.shape) if need[1] else None
+        db = new(N) if need[2] and saved.has_b else None
+        nbytes = lib.sfnn_linear_workspace(q.T, q.K, N, 1)
+        ws = new(max(16, nbytes), dtype=torch.uint8)
+        _check(lib.sfnn_linear_backward(ctypes.byref(q), _vp(saved.slopes), pdy, lddy, _vp(dx), _vp(dw), _vp(db),
+                                        ws.data_ptr(), nbytes, _err_ptr(index), _raw_stream(index)),
+               "sfnn_linear_backward")
+    return dx, dw, db
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, residual, act, out_dtype):
+        y, saved = linear_forward(x, w, b, act, residual, out_dtype, save=True)
+        ctx.save_for_backward(x, w, saved.slopes)
+        ctx.rest = saved.act, saved.N, saved.y_dtype, saved.has_b
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, slopes = ctx.saved_tensors
+        dx = dw = db = None
+        need = ctx.needs_input_grad
+        if any(need[:3]):
+            dx, dw, db = linear_backward(_even_rows(dy), LinearSaved(x, slopes, *ctx.rest), w, need=need[:3])
+        return dx, dw, db, dy if need[3] else None, None, None
+
+
+def linear(x, w, b=None, act=None, residual=None, out_dtype=None):
+    """y of linear_forward, differentiable (once, in reverse mode)."""
+    if not _follows(x, w, b, residual):
+        return linear_forward(x, w, b, act, residual, out_dtype)[0]
+    return _Linear.apply(x, w, b, residual, act, out_dtype)
 
 
 # ------------------------------------------------------------------ norms

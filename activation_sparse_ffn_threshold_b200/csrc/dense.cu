@@ -518,6 +518,184 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, 
   __syncwarp();
 }
 
+// ---------------------------------------------------------------- the linear layer's epilogue
+// 32 columns of the residual for a warp's rows, requested as panels are read (a row's 64 bytes by 4
+// lanes; 16-bit values fill the first half).
+struct ResPiece {
+  uint4 w[8];
+};
+__device__ __forceinline__ void res_request(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows, ResPiece &p) {
+  if (!E.res || !E.vec_res) return;
+  const int lane = threadIdx.x & 31, esize = Q.out32 ? 4 : 2, per = 16 / esize;
+  const unsigned char *base = static_cast<const unsigned char *>(E.res) + row0 * E.ldres * esize;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i >= 4 && !Q.out32) break;
+    const int row = (i & 3) * 8 + (lane >> 2), c = col + ((i >> 2) * 4 + (lane & 3)) * per;
+    p.w[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows && c < Q.N) p.w[i] = *reinterpret_cast<const uint4 *>(base + (row * E.ldres + c) * esize);
+  }
+}
+// Added to this lane's row of 32 columns.
+template <bool bf16>
+__device__ __forceinline__ void res_add(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows, const ResPiece &p,
+                                        uint32_t panel, float v[32]) {
+  if (!E.res) return;
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  if (!E.vec_res) {  // value by value, staged as 32 bits
+    for (int r = 0; r < 32; ++r) {
+      float f = 0.f;
+      if (r < rows && col + lane < Q.N) {
+        const int64_t i = (row0 + r) * E.ldres + col + lane;
+        f = Q.out32 ? static_cast<const float *>(E.res)[i] : load16(E.res, i, bf16);
+      }
+      const uint32_t at = panel_at(panel + (lane >> 4) * kPanel, r, (lane & 15) >> 2) + (lane & 3) * 4;
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(f) : "memory");
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= 4 && !Q.out32) break;
+      sts16(panel_at(panel + (i >> 2) * kPanel, (i & 3) * 8 + (lane >> 2), lane & 3), p.w[i]);
+    }
+  }
+  __syncwarp();
+  if (Q.out32 || !E.vec_res) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint4 w = lds16(panel_at(panel + (j >> 2) * kPanel, lane, j & 3));
+      v[4 * j] += __uint_as_float(w.x), v[4 * j + 1] += __uint_as_float(w.y);
+      v[4 * j + 2] += __uint_as_float(w.z), v[4 * j + 3] += __uint_as_float(w.w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 w = lds16(panel_at(panel, lane, j));
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16(u[i], bf16);
+        v[8 * j + 2 * i] += f.x, v[8 * j + 2 * i + 1] += f.y;
+      }
+    }
+  }
+}
+// 32 columns of this lane's row, value by value: rows that do not consist of 16-byte pieces.
+template <bool bf16>
+__device__ __forceinline__ void ragged_out(const Unit &Q, int64_t row0, int col, int rows, uint32_t panel, const float v[32]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    sts16(panel_at(panel + (j >> 2) * kPanel, lane, j & 3),
+          make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                     __float_as_uint(v[4 * j + 3])));
+  __syncwarp();
+  if (col + lane >= Q.N) return;
+  for (int r = 0; r < rows; ++r) {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];"
+                 : "=f"(f)
+                 : "r"(panel_at(panel + (lane >> 4) * kPanel, r, (lane & 15) >> 2) + (uint32_t)((lane & 3) * 4)));
+    const int64_t i = (row0 + r) * Q.ldo + col + lane;
+    if (Q.out32)
+      static_cast<float *>(Q.out)[i] = f;
+    else
+      static_cast<uint16_t *>(Q.out)[i] = (uint16_t)pack16(f, 0.f, bf16);
+  }
+}
+__device__ __forceinline__ void words32_out(uint32_t panel, const float v[32], unsigned char *base, int64_t ld, int rows,
+                                            int cols) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = make_uint4(__float_as_uint(v[16 * h + 4 * j]), __float_as_uint(v[16 * h + 4 * j + 1]),
+                        __float_as_uint(v[16 * h + 4 * j + 2]), __float_as_uint(v[16 * h + 4 * j + 3]));
+    panel_out(panel + h * kPanel, w, base + 64 * h, ld, rows, (cols - 16 * h + 3) / 4);
+  }
+}
+
+template <bool bf16, int width>
+__device__ __forceinline__ void epi_linear(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
+                                           uint32_t panel, ResPiece &piece) {
+  const LinearEnd &E = P.end;
+  const int lane = threadIdx.x & 31;
+  const int rows = (int)min((int64_t)32, Q.M - row0);
+  if (rows <= 0 || n0 >= Q.N) return;  // (the whole warp)
+  uint32_t bits[width / 32] = {};
+#pragma unroll 1
+  for (int c = 0; c < width; c += 32) {
+    const int col = n0 + c, cols = Q.N - col;
+    if (cols <= 0) break;  // (the whole warp)
+    uint32_t raw[32];
+    float v[32];
+    __syncwarp();
+    tm_ld32(taddr + c, raw);
+    tm_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+    if (Q.split > 1) {  // sums of a part of K, rows of N rounded up to 4
+      const int64_t ld = (Q.N + 3) / 4 * 16;
+      words32_out(panel, v, reinterpret_cast<unsigned char *>(Q.parts) + ((int64_t)Q.part * Q.M + row0) * ld + (int64_t)col * 4,
+                  ld, rows, cols);
+      continue;
+    }
+    if (E.bias) {
+      const float own = lane < cols ? load16(E.bias, col + lane, bf16) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, own, i);
+    }
+    if (E.act == SFNN_LINEAR_RELU) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        word |= v[i] <= 0.f ? 0u : 1u << i;
+        v[i] = v[i] < 0.f ? 0.f : v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < width / 32; ++i)
+        if (c == 32 * i) bits[i] = word;
+    } else if (E.act != SFNN_LINEAR_NONE) {
+      uint32_t q[16];
+      const bool keep = E.slopes != nullptr;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint32_t lo = 0, hi = 0;
+        v[2 * i] = act_value(v[2 * i], E.act, keep, lo);
+        v[2 * i + 1] = act_value(v[2 * i + 1], E.act, keep, hi);
+        q[i] = lo | hi << 16;
+      }
+      if (keep) {
+        uint4 w[4];
+        words_to(w, q);
+        const int64_t ld = slope_row_bytes(Q.N, E.act);
+        panel_out(panel, w, static_cast<unsigned char *>(E.slopes) + row0 * ld + (int64_t)col * 2, ld, rows, 4);
+      }
+    }
+    res_add<bf16>(E, Q, row0, col, rows, piece, panel, v);
+    if (c + 32 < width) res_request(E, Q, row0, col + 32, rows, piece);
+    if (!E.vec_out) {
+      ragged_out<bf16>(Q, row0, col, rows, panel, v);
+    } else if (Q.out32) {
+      words32_out(panel, v, static_cast<unsigned char *>(Q.out) + (row0 * Q.ldo + col) * 4, Q.ldo * 4, rows, cols);
+    } else {
+      uint4 w[4];
+      pack32(w, v, bf16);
+      panel_out(panel, w, static_cast<unsigned char *>(Q.out) + (row0 * Q.ldo + col) * 2, Q.ldo * 2, rows, (cols + 7) / 8);
+    }
+  }
+  if (E.slopes && E.act == SFNN_LINEAR_RELU && Q.split == 1 && lane < rows) {
+    uint32_t *p = static_cast<uint32_t *>(E.slopes) + (row0 + lane) * (slope_row_bytes(Q.N, E.act) / 4) + n0 / 32;
+    if (width == 128)
+      *reinterpret_cast<uint4 *>(p) = make_uint4(bits[0], bits[1], bits[width / 32 - 2], bits[width / 32 - 1]);
+    else
+      *reinterpret_cast<uint2 *>(p) = make_uint2(bits[0], bits[1]);
+  }
+}
+
 // ---------------------------------------------------------------- the kernel
 template <int EPI, bool BF16, int TN>  // TN: columns of a tile
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -678,6 +856,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (kDGated) saved_request<EPI == kEpiDGated8>(P, w, row0, n0, panel + 2 * kPanel, scales);
+      ResPiece piece;
+      if (EPI == kEpiLinear && w.split == 1)
+        res_request(P.end, w, row0, n0, (int)max((int64_t)0, min((int64_t)32, w.M - row0)), piece);
       if (!__all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((n >> 1) & 1)))) {
         if (lane == 0) latch_error(P.err, kErrTimeout);
         break;
@@ -695,6 +876,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         if (kDGated)
           epi_dgated<EPI == kEpiDGated8, BF16, kWide>(P, w, acc + half * kWide, row0, n0, scales, panel);
+        else if (EPI == kEpiLinear)
+          epi_linear<BF16, kWide>(P, w, acc + half * kWide, row0, n0, panel, piece);
         else
           epi_store<BF16, kWide>(P, w, acc + half * kWide, row0, n0, panel);
         done();
@@ -748,6 +931,7 @@ cudaError_t launch_dense(DenseParams &P, int epi, int num_sms, cudaStream_t s) {
   P.extra = P.count > 1 ? (lead + len / 2 + 1) / len : 0;
   if (epi == kEpiGated) return run<kEpiGated>(P, num_sms, s);
   if (epi == kEpiDGated) return P.save == SFNN_SAVE_ACT8 ? run<kEpiDGated8>(P, num_sms, s) : run<kEpiDGated>(P, num_sms, s);
+  if (epi == kEpiLinear) return run<kEpiLinear>(P, num_sms, s);
   return run<kEpiStore>(P, num_sms, s);
 }
 

@@ -153,8 +153,47 @@ enum DenseEpi : int {
   kEpiStore = 0,  // C as 16-bit or fp32 values
   kEpiGated = 1,  // B0 = gate rows, B1 = up rows (128 each per tile): H = relu(G + b) * U
   kEpiDGated = 2,  // C = dH: dU = dH * R, dG = dH * U * [R > 0], H = R * U
-  kEpiDGated8 = 3  // the same with R and U held as 8-bit blocks
+  kEpiDGated8 = 3,  // the same with R and U held as 8-bit blocks
+  kEpiLinear = 4  // act(C + bias) + residual
 };
+
+// The end of a linear layer: Y = act(Z + bias) + residual, and what the backward pass needs of act'.
+struct LinearEnd {
+  const void *bias;  // [N] or null
+  const void *res;   // [M x N] of the output's type, or null
+  int64_t ldres;
+  int act;           // sfnn_linear_act
+  void *slopes;      // or null: act'(Z) as it is kept (below)
+  int vec_out, vec_res;  // rows of whole 16-byte pieces
+};
+
+// What is kept of act': of a ReLU a bit per value (a value above zero, or a NaN), 32 columns a word,
+// rows of whole 128 columns; of the others 16-bit fixed point, code = 2^15 act' + 2^14, which holds
+// act' (-0.13 to 1.13) to 2^-16, where the type would round it as often as the result itself; 0xffff
+// is a NaN.  Rows of whole 32 columns.
+__host__ __device__ inline int64_t slope_row_bytes(int64_t N, int act) {
+  return act == SFNN_LINEAR_NONE ? 0 : act == SFNN_LINEAR_RELU ? (N + 127) / 128 * 16 : (N + 31) / 32 * 64;
+}
+// act(z) and, where `keep`, the code of act'(z) of the smooth ones; the limits at the infinities, NaN
+// for a NaN.  gelu: z Phi(z), Phi the normal distribution's integral; silu: z / (1 + e^-z).
+__device__ __forceinline__ float act_value(float z, int act, bool keep, uint32_t &code) {
+  if (act == SFNN_LINEAR_NONE) return z;
+  if (act == SFNN_LINEAR_RELU) return z < 0.f ? 0.f : z;
+  const float b = z < -80.f ? -80.f : z > 80.f ? 80.f : z;  // both are 0 or z beyond, and the products below finite
+  float p, s;
+  if (act == SFNN_LINEAR_GELU) {
+    p = normcdff(b);
+    s = fmaf(b * 0.3989422804f, __expf(-0.5f * b * b), p);
+  } else {
+    p = 1.f / (1.f + __expf(-b));
+    s = p * fmaf(b, 1.f - p, 1.f);
+  }
+  if (keep) code = s == s ? __float2uint_rn(fmaf(s, 32768.f, 16384.f)) : 0xffffu;
+  return (z < b ? b : z) * p;
+}
+__device__ __forceinline__ float slope_value(uint32_t code) {
+  return code == 0xffffu ? __uint_as_float(0x7fffffffu) : (float)((int)code - 16384) * 0x1p-15f;
+}
 
 struct alignas(64) DenseProblem {
   CUtensorMap a0, b0, a1, b1;
@@ -190,6 +229,8 @@ struct DenseParams {
                       // kEpiStore: such sums to add up over `col_blocks` blocks into
   uint16_t *colsum;   // this, of `cols` columns (null: none)
   int col_blocks, cols;
+  // kEpiLinear (and bias above): what joins the product on its way out
+  LinearEnd end;
   int32_t *err;
 };
 
@@ -206,7 +247,31 @@ cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &ready) {
   return e;
 }
 
+// ---------------------------------------------------------------- host (product.cu)
 int device_sms();  // SMs of the current device (0: no device)
+
+inline int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+inline int chunks(int64_t K) { return (int)((K + 63) / 64); }
+inline bool on(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+inline bool a16(const void *p) { return on(p, 16); }
+bool mat_ok(const void *p, int64_t ld, int64_t cols);  // an operand: aligned rows of 16-bit values
+
+struct Operand {
+  const void *p;
+  int64_t ld;
+  bool mn;  // M or N contiguous, not K
+};
+bool set_pair(DenseProblem &P, int which, const Operand &a, const Operand &b, int M, int N, int64_t K);
+bool set_problem(DenseProblem &P, const Operand &a, const Operand &b, int M, int N, int64_t K, void *out, int64_t ldo,
+                 int split = 1, int tn = 256);
+int parts_of(int64_t M, int64_t N, int nk, int sms);
+int64_t parts_bytes(int64_t M, int64_t N, int nk, int sms);
+int tile_columns(int M, int N, int split, int sms);
+bool slim_serves(int T, int N, int64_t K, bool gated, int sms);
+// What a split product leaves, added up (nothing to do where K was not split).
+cudaError_t join(const DenseProblem &P, int bf16, int sms, cudaStream_t s);
+// out[c] = sum over the blocks of part[block][c]
+cudaError_t launch_colsum(const float *part, int blocks, int n, int bf16, void *out, cudaStream_t s);
 
 // Fills first, rest and extra from the problems.
 cudaError_t launch_dense(DenseParams &P, int epi, int num_sms, cudaStream_t s);
@@ -214,6 +279,7 @@ cudaError_t launch_dense(DenseParams &P, int epi, int num_sms, cudaStream_t s);
 // The products of few tokens (slim.cu): out = x . w0^T, or with w1 the gated hidden layer
 // relu(x . w0^T + bias) * (x . w1^T).  K-major weights; `early`: w0 may be read while the
 // kernel launched before still runs (it waited for everything before it).
+// ... `end`: a linear layer's (never gated).
 struct SlimArgs {
   const void *x, *w0, *w1, *bias;
   int64_t ldx, ldw0, ldw1;
@@ -222,6 +288,7 @@ struct SlimArgs {
   void *out;
   int64_t ldo;
   int bf16, out32, early;
+  const LinearEnd *end;
   int32_t *err;
 };
 int64_t slim_cost(int T, int N, int64_t K, bool gated, int num_sms);

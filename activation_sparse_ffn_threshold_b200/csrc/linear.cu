@@ -1,0 +1,349 @@
+// linear.cu -- the linear layer with its epilogue: Y = act(X W^T + b) + residual, and its gradients
+//
+//     dZ = dY act'(Z),   dX = dZ W,   dW = dZ^T X,   db = sum over tokens of dZ,   dresidual = dY
+//
+// Forward: one product (dense.cu, or slim.cu for few tokens) whose epilogue does the rest; a K split
+// over CTA pairs is joined by k_linear_join, which then does it.  Backward: k_linear_slopes makes dZ
+// in the tensor cores' type and its columns' sums over 32 rows, from its values before that rounding;
+// then dX and dW in one launch, which adds the sums up on its way.  Without an activation dY is dZ.
+#include <algorithm>
+
+#include "common.cuh"
+#include "dense.cuh"
+#include "launch.cuh"
+
+namespace sfnn {
+namespace {
+
+// Rows of a split product's parts are `ld` floats (N rounded up to 4) apart.
+__host__ __device__ constexpr int64_t part_ld(int64_t N) { return (N + 3) / 4 * 4; }
+
+// A warp takes 128 columns of a row, a lane 4 of them.
+__global__ void __launch_bounds__(256) k_linear_join(const float *__restrict__ part, int parts, int M, int N, int bf16,
+                                                     int out32, void *out, int64_t ldo,
+                                                     const __grid_constant__ LinearEnd E) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, blocks = (N + 127) / 128;
+  const int64_t ld = part_ld(N), work = (int64_t)M * blocks, slope_ld = slope_row_bytes(N, E.act);
+  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < work; i += (int64_t)gridDim.x * 8) {
+    const int64_t row = i / blocks;
+    const int col = (int)(i - row * blocks) * 128 + lane * 4;
+    const int cols = min(4, N - col);  // (may be negative)
+    float v[4] = {};
+    if (cols > 0) {
+#pragma unroll 4
+      for (int p = 0; p < parts; ++p) {
+        const float4 f = __ldg(reinterpret_cast<const float4 *>(part + ((int64_t)p * M + row) * ld + col));
+        v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+      }
+    }
+    uint32_t bits = 0, code[4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j < cols && E.bias) v[j] += load16(E.bias, col + j, bf16);
+      bits |= v[j] <= 0.f || j >= cols ? 0u : 1u << (4 * (lane & 7) + j);
+      v[j] = act_value(v[j], E.act, E.slopes != nullptr, code[j]);
+      if (j < cols && E.res) {
+        const int64_t at = row * E.ldres + col + j;
+        v[j] += out32 ? static_cast<const float *>(E.res)[at] : load16(E.res, at, bf16);
+      }
+      if (j < cols) {
+        const int64_t at = row * ldo + col + j;
+        if (out32)
+          static_cast<float *>(out)[at] = v[j];
+        else
+          static_cast<uint16_t *>(out)[at] = (uint16_t)pack16(v[j], 0.f, bf16);
+      }
+    }
+    if (!E.slopes) continue;
+    unsigned char *s = static_cast<unsigned char *>(E.slopes) + row * slope_ld;
+    if (E.act == SFNN_LINEAR_RELU) {
+#pragma unroll
+      for (int o = 1; o < 8; o *= 2) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+      if ((lane & 7) == 0) reinterpret_cast<uint32_t *>(s)[col / 32] = bits;
+    } else if (col < (N + 31) / 32 * 32) {
+      *reinterpret_cast<uint2 *>(s + (int64_t)col * 2) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+    }
+  }
+}
+
+// dZ from dY, and its columns' sums over 32 rows before it is rounded.  A CTA has 32 rows of 256
+// columns, a warp 4 rows of it; a lane's 8 columns are neighbours where vectors can be read (V = 8),
+// else 32 apart.
+struct SlopeParams {
+  const void *dy;
+  int64_t lddy;
+  int dy32, act, M, N;
+  const void *slopes;
+  void *dz;  // or null: dY is dZ
+  int64_t lddz;
+  float *colpart;  // or null
+};
+template <bool bf16, int V>
+__global__ void __launch_bounds__(256) k_linear_slopes(const __grid_constant__ SlopeParams P) {
+  __shared__ float sums[8][264];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c0 = blockIdx.x * 256;
+  const int64_t slope_ld = slope_row_bytes(P.N, P.act);
+  auto column = [&](int j) { return V == 8 ? c0 + lane * 8 + j : c0 + lane + 32 * j; };
+  for (int64_t block = blockIdx.y; block * 32 < P.M; block += gridDim.y) {
+    float sum[8] = {};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t row = block * 32 + warp * 4 + r;
+      if (row >= P.M || column(0) >= P.N) break;
+      float v[8];
+      if (V == 8) {
+        const int64_t at = row * P.lddy + column(0);
+        if (P.dy32) {
+          const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(P.dy) + at);
+          const float4 a = __ldg(q), b = __ldg(q + 1);
+          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+          const uint4 a = ld_stream(static_cast<const uint16_t *>(P.dy) + at);
+          const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack16(u[i], bf16);
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t at = row * P.lddy + column(j);
+          v[j] = column(j) >= P.N ? 0.f : P.dy32 ? static_cast<const float *>(P.dy)[at] : load16(P.dy, at, bf16);
+        }
+      }
+      const unsigned char *s = static_cast<const unsigned char *>(P.slopes) + row * slope_ld;
+      if (P.act == SFNN_LINEAR_RELU) {
+        const uint32_t *words = reinterpret_cast<const uint32_t *>(s);
+        const uint32_t own = V == 8 ? __ldg(words + column(0) / 32) >> (column(0) & 31) : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool on = V == 8 ? (own >> j) & 1u : column(j) < P.N && (__ldg(words + column(j) / 32) >> lane) & 1u;
+          v[j] = on ? v[j] : 0.f;
+        }
+      } else if (P.act != SFNN_LINEAR_NONE) {
+        if (V == 8) {
+          const uint4 a = ld_stream(s + (int64_t)column(0) * 2);
+          const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[2 * i] *= slope_value(u[i] & 0xffffu), v[2 * i + 1] *= slope_value(u[i] >> 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (column(j) < P.N) v[j] *= slope_value(reinterpret_cast<const uint16_t *>(s)[column(j)]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      if (!P.dz) continue;
+      uint16_t *out = static_cast<uint16_t *>(P.dz) + row * P.lddz;
+      if (V == 8)
+        *reinterpret_cast<uint4 *>(out + column(0)) =
+            make_uint4(pack16(v[0], v[1], bf16), pack16(v[2], v[3], bf16), pack16(v[4], v[5], bf16), pack16(v[6], v[7], bf16));
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (column(j) < P.N) out[column(j)] = (uint16_t)pack16(v[j], 0.f, bf16);
+    }
+    if (!P.colpart) continue;
+    __syncthreads();  // the block before has been added up
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[warp][column(j) - c0] = sum[j];
+    __syncthreads();
+    const int c = c0 + threadIdx.x;
+    if (c >= P.N) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += sums[w][threadIdx.x];
+    P.colpart[block * P.N + c] = v;
+  }
+}
+
+// ---------------------------------------------------------------- host
+constexpr int kMaxWidth = 1 << 20;
+int64_t row_blocks(int64_t T) { return (T + 31) / 32; }
+
+sfnn_status check(const sfnn_linear_desc *q) {
+  if (!q || q->T < 0 || q->K < 1 || q->N < 1) return SFNN_ERR_INVALID_ARG;
+  if (q->dtype != SFNN_F16 && q->dtype != SFNN_BF16) return q->dtype == SFNN_F32 ? SFNN_ERR_UNSUPPORTED : SFNN_ERR_INVALID_ARG;
+  if (q->y_dtype != q->dtype && q->y_dtype != SFNN_F32) return SFNN_ERR_INVALID_ARG;
+  if (q->act < SFNN_LINEAR_NONE || q->act > SFNN_LINEAR_SILU) return SFNN_ERR_INVALID_ARG;
+  if (q->K % 8 || q->K > kMaxWidth || q->N > kMaxWidth || q->T > (1 << 24)) return SFNN_ERR_UNSUPPORTED;
+  if (!mat_ok(q->w, q->ldw, q->K) || (q->T > 0 && !mat_ok(q->x, q->ldx, q->K)) || !on(q->b, 2)) return SFNN_ERR_INVALID_ARG;
+  return SFNN_OK;
+}
+// Rows of values of the output's type: any alignment of it, any row stride of at least N.
+bool values_ok(const void *p, int64_t ld, const sfnn_linear_desc *q) {
+  return p && on(p, q->y_dtype == SFNN_F32 ? 4 : 2) && ld >= q->N && ld <= (1ll << 36);
+}
+bool pieces(const void *p, int64_t ld, const sfnn_linear_desc *q) {
+  const int per = q->y_dtype == SFNN_F32 ? 4 : 8;
+  return a16(p) && ld % per == 0 && q->N % per == 0;
+}
+bool slopes_ok(const void *p) { return p && a16(p); }
+
+int64_t dz_bytes(int64_t T, int64_t N) { return up(T * up(N, 8) * 2, 256); }
+int64_t workspace(int64_t T, int64_t K, int64_t N, bool backward, int sms) {
+  if (!backward) return parts_bytes(T, N, chunks(K), sms);
+  return dz_bytes(T, N) + up(row_blocks(T) * N * 4, 256) + parts_bytes(T, K, chunks(N), sms) +
+         parts_bytes(N, K, chunks(T), sms);
+}
+
+}  // namespace
+}  // namespace sfnn
+
+using namespace sfnn;
+
+extern "C" {
+
+int64_t sfnn_linear_workspace(int32_t T, int32_t K, int32_t N, int32_t backward) {
+  if (T < 0 || K < 1 || N < 1) return -1;
+  return workspace(T, K, N, backward != 0, std::max(1, device_sms()));
+}
+int64_t sfnn_linear_slope_bytes(int32_t T, int32_t N, int32_t act) {
+  if (T < 0 || N < 1 || act < SFNN_LINEAR_NONE || act > SFNN_LINEAR_SILU) return -1;
+  return T * slope_row_bytes(N, act);
+}
+
+sfnn_status sfnn_linear_forward(const sfnn_linear_desc *q, const void *residual, int64_t ldr, void *y, int64_t ldy,
+                                void *slopes, void *ws, int64_t ws_bytes, int32_t *err, sfnn_stream_t stream) {
+  const sfnn_status st = check(q);
+  if (st != SFNN_OK) return st;
+  if (slopes && (!a16(slopes) || q->act == SFNN_LINEAR_NONE)) return SFNN_ERR_INVALID_ARG;
+  if (q->T == 0) return SFNN_OK;
+  if (!values_ok(y, ldy, q) || (residual && !values_ok(residual, ldr, q)) || !err || !on(err, 4)) return SFNN_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms < 2) return SFNN_ERR_CUDA;
+  const int64_t need = workspace(q->T, q->K, q->N, false, sms);
+  if (need && (!ws || !a16(ws) || ws_bytes < need)) return SFNN_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int T = q->T, N = q->N, bf16 = q->dtype == SFNN_BF16, out32 = q->y_dtype == SFNN_F32;
+  LinearEnd end{};
+  end.bias = q->b;
+  end.res = residual;
+  end.ldres = ldr;
+  end.act = q->act;
+  end.slopes = slopes;
+  end.vec_out = pieces(y, ldy, q);
+  end.vec_res = residual && pieces(residual, ldr, q);
+  if (!slopes && slim_serves(T, N, q->K, false, sms)) {
+    SlimArgs a{};
+    a.x = q->x;
+    a.ldx = q->ldx;
+    a.w0 = q->w;
+    a.ldw0 = q->ldw;
+    a.T = T;
+    a.N = N;
+    a.K = q->K;
+    a.out = y;
+    a.ldo = ldy;
+    a.bf16 = bf16;
+    a.out32 = out32;
+    a.end = &end;
+    a.err = err;
+    return launch_slim(a, sms, s);
+  }
+  DenseParams P{};
+  P.count = 1;
+  const int split = parts_of(T, N, chunks(q->K), sms);
+  if (!set_problem(P.p[0], Operand{q->x, q->ldx, false}, Operand{q->w, q->ldw, false}, T, N, q->K, y, ldy, split,
+                   tile_columns(T, N, split, sms)))
+    return SFNN_ERR_CUDA;
+  P.p[0].out32 = out32;
+  P.p[0].part = static_cast<float *>(ws);
+  P.bf16 = bf16;
+  P.end = end;
+  P.err = err;
+  if (launch_dense(P, kEpiLinear, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
+  if (split > 1) {
+    const int64_t warps = (int64_t)T * ((N + 127) / 128);
+    if (launch_pdl(k_linear_join, dim3((unsigned)std::min<int64_t>((warps + 7) / 8, 8 * sms)), dim3(256), 0, s, P.p[0].part,
+                   split, T, N, bf16, out32, y, ldy, end) != cudaSuccess)
+      return SFNN_ERR_CUDA;
+  }
+  return SFNN_OK;
+}
+
+sfnn_status sfnn_linear_backward(const sfnn_linear_desc *q, const void *slopes, const void *dy, int64_t lddy, void *dx,
+                                 void *dw, void *db, void *ws, int64_t ws_bytes, int32_t *err, sfnn_stream_t stream) {
+  const sfnn_status st = check(q);
+  if (st != SFNN_OK) return st;
+  if (!a16(dx) || !a16(dw) || !on(db, 2)) return SFNN_ERR_INVALID_ARG;
+  const int T = q->T, K = q->K, N = q->N, bf16 = q->dtype == SFNN_BF16;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {  // sums over no tokens
+    if ((dw && cudaMemsetAsync(dw, 0, (size_t)N * K * 2, s) != cudaSuccess) ||
+        (db && cudaMemsetAsync(db, 0, (size_t)N * 2, s) != cudaSuccess))
+      return SFNN_ERR_CUDA;
+    return SFNN_OK;
+  }
+  if (!values_ok(dy, lddy, q) || (q->act != SFNN_LINEAR_NONE && !slopes_ok(slopes)) || !err || !on(err, 4))
+    return SFNN_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms < 2) return SFNN_ERR_CUDA;
+  if (!ws || !a16(ws) || ws_bytes < workspace(T, K, N, true, sms)) return SFNN_ERR_INVALID_ARG;
+  unsigned char *w = static_cast<unsigned char *>(ws);
+  float *colpart = reinterpret_cast<float *>(w + dz_bytes(T, N));
+  float *parts_x = colpart + up(row_blocks(T) * N * 4, 256) / 4;
+  float *parts_w = parts_x + parts_bytes(T, K, chunks(N), sms) / 4;
+
+  // dY itself where it is what the tensor cores read
+  const bool as_is = q->act == SFNN_LINEAR_NONE && q->y_dtype == q->dtype && mat_ok(dy, lddy, N);
+  Operand dz{dy, lddy, false};
+  if (!as_is) dz = Operand{w, up(N, 8), false};
+  if (db || (!as_is && (dx || dw))) {
+    SlopeParams P{};
+    P.dy = dy;
+    P.lddy = lddy;
+    P.dy32 = q->y_dtype == SFNN_F32;
+    P.act = q->act;
+    P.M = T;
+    P.N = N;
+    P.slopes = slopes;
+    P.dz = as_is || (!dx && !dw) ? nullptr : w;
+    P.lddz = up(N, 8);
+    P.colpart = db ? colpart : nullptr;
+    const bool vec = N % 8 == 0 && a16(dy) && lddy % 8 == 0;
+    const dim3 grid((unsigned)((N + 255) / 256), (unsigned)std::min<int64_t>(row_blocks(T), 65535));
+    auto run = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, P); };
+    if ((vec ? (bf16 ? run(k_linear_slopes<true, 8>) : run(k_linear_slopes<false, 8>))
+             : (bf16 ? run(k_linear_slopes<true, 1>) : run(k_linear_slopes<false, 1>))) != cudaSuccess)
+      return SFNN_ERR_CUDA;
+  }
+  // dX and dW in one launch, the one with the longer tiles first
+  DenseParams P{};
+  auto add_x = [&] {
+    DenseProblem &D = P.p[P.count++];
+    const int split = parts_of(T, K, chunks(N), sms);
+    D.part = parts_x;
+    return set_problem(D, dz, Operand{q->w, q->ldw, true}, T, K, N, dx, K, split);
+  };
+  auto add_w = [&] {
+    DenseProblem &D = P.p[P.count++];
+    const int split = parts_of(N, K, chunks(T), sms);
+    D.part = parts_w;
+    return set_problem(D, Operand{dz.p, dz.ld, true}, Operand{q->x, q->ldx, true}, N, K, T, dw, K, split);
+  };
+  const bool x_first = chunks(N) / parts_of(T, K, chunks(N), sms) >= chunks(T) / parts_of(N, K, chunks(T), sms);
+  if ((dx && x_first && !add_x()) || (dw && !add_w()) || (dx && !x_first && !add_x())) return SFNN_ERR_CUDA;
+  const int blocks = (int)row_blocks(T);
+  if (!P.count) return !db || launch_colsum(colpart, blocks, N, bf16, db, s) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
+  P.bf16 = bf16;
+  P.err = err;
+  P.colpart = colpart;
+  P.colsum = static_cast<uint16_t *>(db);
+  P.col_blocks = blocks;
+  P.cols = N;
+  if (launch_dense(P, kEpiStore, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
+  for (int i = 0; i < P.count; ++i)
+    if (join(P.p[i], bf16, sms, s) != cudaSuccess) return SFNN_ERR_CUDA;
+  return SFNN_OK;
+}
+
+}  // extern "C"

@@ -427,8 +427,6 @@ __global__ void __launch_bounds__(256) k_norm_sums(const __grid_constant__ NormS
 }
 
 // ---------------------------------------------------------------- host
-bool on(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 constexpr int kMaxWidth = 32768;
 
 bool rows_ok(const void *p, int64_t ld, int d, bool wide) { return p && on(p, wide ? 4 : 2) && ld >= d && ld <= (1ll << 36); }

@@ -44,8 +44,10 @@ struct alignas(64) SlimParams {
   const void *bias;
   void *out;
   int64_t ldo;
+  LinearEnd end;  // MODE kSlimLinear
   int32_t *err;
 };
+enum SlimMode : int { kSlimPlain = 0, kSlimGated = 1, kSlimLinear = 2 };
 
 // This thread's weight row: its accumulators of tokens [t0, t0 + 8) -> out[t][col].  (The
 // epilogues go by eight tokens in a loop: unrolled further, a single token's few instructions
@@ -64,8 +66,9 @@ __device__ __forceinline__ void store_tokens(const SlimParams &P, int col, int t
   }
 }
 
-template <bool GATED>
+template <int MODE>
 __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimParams P) {
+  constexpr bool GATED = MODE == kSlimGated;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty, parts_in;
   __shared__ uint32_t tmem_slot;
@@ -192,7 +195,8 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
   const bool busy = worker && quad * (P.m64 ? 16 : 32) < P.nb;
   auto load_bias = [&](int t) {
     const int col = t * P.nb + row;
-    return GATED && P.bias && row < P.nb && col < P.N ? load16(P.bias, col, P.bf16) : 0.f;
+    const void *b = MODE == kSlimLinear ? P.end.bias : P.bias;
+    return MODE != kSlimPlain && b && row < P.nb && col < P.N ? load16(b, col, P.bf16) : 0.f;
   };
   // the epilogue of this thread's weight row, with the other parts of a split tile at `sums`
   auto epilogue = [&](int t, float bias, const float *sums) {
@@ -201,7 +205,15 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
 #pragma unroll 1
     for (int c = 0; c < P.T; c += 8) {
       uint32_t g[8], u[8];
-      float v[8];
+      float v[8], res[8];
+      if (MODE == kSlimLinear)  // on its way while the accumulators are read
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t at = (int64_t)(c + i) * P.end.ldres + col;
+          res[i] = !P.end.res || !live || c + i >= P.T ? 0.f
+                   : P.out32                           ? static_cast<const float *>(P.end.res)[at]
+                                                       : load16(P.end.res, at, P.bf16);
+        }
       __syncwarp();
       tm_ld8(lanes + c, g);
       if (GATED) tm_ld8(lanes + (uint32_t)P.up_col + c, u);
@@ -226,6 +238,8 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
           v[i] = v[i] < 0.f ? 0.f : v[i];
           v[i] *= __uint_as_float(u[i]);
         }
+        uint32_t code;
+        if (MODE == kSlimLinear) v[i] = act_value(v[i] + bias, P.end.act, false, code) + res[i];
       }
       store_tokens(P, col, c, v);
     }
@@ -298,10 +312,10 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
 
 int up_to(int v, int to) { return (v + to - 1) / to * to; }
 
-template <bool GATED>
+template <int MODE>
 cudaError_t launch(SlimParams &P, int grid, size_t smem, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t attr = allow_smem(k_slim<GATED>, 224 * 1024, ready);
+  const cudaError_t attr = allow_smem(k_slim<MODE>, 224 * 1024, ready);
   if (attr != cudaSuccess) return attr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -317,7 +331,7 @@ cudaError_t launch(SlimParams &P, int grid, size_t smem, cudaStream_t s) {
   attrs[1].val.clusterDim.z = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = P.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_slim<GATED>, P);
+  return cudaLaunchKernelEx(&cfg, k_slim<MODE>, P);
 }
 
 // Clusters of `split` CTAs, one CTA to an SM, that the device runs at a time (a cluster lies
@@ -330,7 +344,7 @@ int active_clusters(int split) {
   int n = slot.load(std::memory_order_relaxed);
   if (n) return n;
   static std::atomic<uint64_t> ready{0};
-  if (allow_smem(k_slim<false>, 224 * 1024, ready) != cudaSuccess) return 0;
+  if (allow_smem(k_slim<kSlimPlain>, 224 * 1024, ready) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(split * 64);
   cfg.blockDim = dim3(kThreads);
@@ -341,7 +355,7 @@ int active_clusters(int split) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, k_slim<false>, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, k_slim<kSlimPlain>, &cfg) != cudaSuccess) return 0;
   slot.store(n, std::memory_order_relaxed);
   return n;
 }
@@ -421,7 +435,10 @@ sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
       (gated && !make_tensor_map(&P.w1, q.w1, 2, q.N, q.K, q.ldw1, P.nb, 64, true)))
     return SFNN_ERR_CUDA;
   const int grid = P.split > 1 ? P.tiles * P.split : std::min(P.tiles, sms);
-  const cudaError_t e = gated ? launch<true>(P, grid, smem, s) : launch<false>(P, grid, smem, s);
+  if (q.end) P.end = *q.end;
+  const cudaError_t e = gated   ? launch<kSlimGated>(P, grid, smem, s)
+                        : q.end ? launch<kSlimLinear>(P, grid, smem, s)
+                                : launch<kSlimPlain>(P, grid, smem, s);
   return e == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
 }
 

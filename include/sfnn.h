@@ -565,6 +565,48 @@ SFNN_API sfnn_status sfnn_mxfp4_linear(const void *x, int64_t ldx, int32_t T, in
                                        void *ws, int64_t ws_bytes, int32_t *err, sfnn_stream_t stream);
 
 /*
+ * The linear layer with its epilogue:
+ *
+ *     Z = X . W^T + b,   Y = act(Z) + residual
+ *
+ * and its backward pass
+ *
+ *     dZ = dY act'(Z),  dX = dZ . W,  dW = dZ^T . X,  db = sum over tokens of dZ   (dresidual = dY).
+ *
+ * act: none, ReLU, GELU (z Phi(z), Phi the normal distribution's integral) or SiLU (z / (1 + e^-z)).
+ * X [T x K], W [N x K] and b [N] (or NULL) are fp16 or bf16 (fp32: SFNN_ERR_UNSUPPORTED), Y, the
+ * residual and dY [T x N] of that type or fp32 (y_dtype), sums fp32 on the tensor cores.  X and W as
+ * the gated FFN's matrices: K a multiple of 8, 16-byte aligned rows; N any number, and Y, the residual
+ * and dY at any alignment of their type and any row stride of at least N.  Y may be the residual (the
+ * same rows), else nothing that is written may overlap anything else.  T = 0 is valid.
+ * slopes (may be NULL; sfnn_linear_slope_bytes, 16-byte aligned): what the backward pass needs of
+ * act'(Z): a bit per value for a ReLU (Z above zero, or a NaN), 16 bits of fixed point that hold it to
+ * 2^-16 for the others.  A backward pass without an activation needs none.  dZ is rounded to the
+ * values' type between the products; db adds it up before that.
+ * ws: sfnn_linear_workspace bytes, 16-byte aligned, as the gated FFN's; err likewise.
+ */
+typedef enum { SFNN_LINEAR_NONE = 0, SFNN_LINEAR_RELU = 1, SFNN_LINEAR_GELU = 2, SFNN_LINEAR_SILU = 3 } sfnn_linear_act;
+typedef struct {
+    int32_t T, K, N;
+    int32_t dtype;   /* SFNN_F16 or SFNN_BF16 */
+    int32_t y_dtype; /* dtype or SFNN_F32 */
+    int32_t act;     /* sfnn_linear_act */
+    const void *x;
+    int64_t ldx;
+    const void *w;
+    int64_t ldw;
+    const void *b;   /* not read by a backward pass */
+} sfnn_linear_desc;
+SFNN_API int64_t sfnn_linear_workspace(int32_t T, int32_t K, int32_t N, int32_t backward);
+SFNN_API int64_t sfnn_linear_slope_bytes(int32_t T, int32_t N, int32_t act);
+SFNN_API sfnn_status sfnn_linear_forward(const sfnn_linear_desc *q, const void *residual, int64_t ldr, void *y, int64_t ldy,
+                                         void *slopes, void *ws, int64_t ws_bytes, int32_t *err, sfnn_stream_t stream);
+/* The gradients, contiguous, in q->dtype; a NULL one is not computed. */
+SFNN_API sfnn_status sfnn_linear_backward(const sfnn_linear_desc *q, const void *slopes, const void *dy, int64_t lddy,
+                                          void *dx, void *dw, void *db, void *ws, int64_t ws_bytes, int32_t *err,
+                                          sfnn_stream_t stream);
+
+/*
  * The norms before and after a block, with its gate and residual scale:
  *
  *     R = residual_scale * X + branch_scale * gate * post(Z),   H = pre(R)

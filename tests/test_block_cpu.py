@@ -105,3 +105,58 @@ def test_binding_refuses_host_tensors_and_bad_options():
             sf.clip_grad_norm([x], **kw)
     with pytest.raises(ValueError):
         sf.clip_grad_norm([x], 1.0, out=[])
+
+
+def linear(T=4, K=64, N=40, dtype=sf.F16, y_dtype=None, act=1, **kw):
+    q = block._LinearDesc(T, K, N, dtype, dtype if y_dtype is None else y_dtype, act, 4096, K, 4096, K, 4096)
+    for k, v in kw.items():
+        setattr(q, k, v)
+    return q
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), INVALID), (dict(K=0), INVALID), (dict(N=0), INVALID), (dict(dtype=sf.F32), UNSUPPORTED),
+    (dict(dtype=7), INVALID), (dict(y_dtype=sf.BF16), INVALID), (dict(act=4), INVALID), (dict(act=-1), INVALID),
+    (dict(K=60), UNSUPPORTED), (dict(K=(1 << 20) + 8), UNSUPPORTED), (dict(N=(1 << 20) + 1), UNSUPPORTED),
+    (dict(T=(1 << 24) + 1), UNSUPPORTED), (dict(x=None), INVALID), (dict(x=4104), INVALID), (dict(ldx=60), INVALID),
+    (dict(ldx=68), INVALID), (dict(w=None), INVALID), (dict(w=8), INVALID), (dict(ldw=66), INVALID), (dict(b=4097), INVALID)])
+def test_linear_refuses_bad_descriptors(kw, want):
+    lib = sf.load_library()
+    q = linear(**kw)
+    assert lib.sfnn_linear_forward(ctypes.byref(q), None, 0, 4096, 40, None, 4096, 1 << 40, 4096, None) == want
+    assert lib.sfnn_linear_backward(ctypes.byref(q), 4096, 4096, 40, 4096, 4096, 4096, 4096, 1 << 40, 4096, None) == want
+
+
+def test_linear_refuses_bad_buffers():
+    lib = sf.load_library()
+
+    def forward(q, res=None, ldr=40, y=4096, ldy=40, slopes=None, err=4096):
+        return lib.sfnn_linear_forward(None if q is None else ctypes.byref(q), res, ldr, y, ldy, slopes, 4096, 1 << 40, err,
+                                       None)
+    assert forward(None) == INVALID
+    for kw in (dict(y=None), dict(y=4097), dict(ldy=39), dict(res=4097), dict(res=4096, ldr=39), dict(slopes=4100),
+               dict(err=None), dict(err=4098)):
+        assert forward(linear(), **kw) == INVALID, kw
+    assert forward(linear(y_dtype=sf.F32), y=4098) == INVALID and forward(linear(act=0), slopes=4096) == INVALID
+    assert forward(linear(T=0), y=None) == 0
+
+    def backward(q, slopes=4096, dy=4096, lddy=40, dx=4096, dw=4096, db=4096, err=4096):
+        return lib.sfnn_linear_backward(None if q is None else ctypes.byref(q), slopes, dy, lddy, dx, dw, db, 4096, 1 << 40,
+                                        err, None)
+    assert backward(None) == INVALID
+    for kw in (dict(slopes=None), dict(slopes=4100), dict(dy=None), dict(dy=4097), dict(lddy=32), dict(dx=4104),
+               dict(dw=4098), dict(db=4097), dict(err=None)):
+        assert backward(linear(), **kw) == INVALID, kw
+    assert lib.sfnn_linear_workspace(-1, 64, 64, 0) < 0 and lib.sfnn_linear_workspace(0, 64, 64, 1) >= 0
+    assert lib.sfnn_linear_slope_bytes(3, 129, 1) == 3 * 32 and lib.sfnn_linear_slope_bytes(3, 33, 2) == 3 * 128
+    assert lib.sfnn_linear_slope_bytes(3, 129, 0) == 0 and lib.sfnn_linear_slope_bytes(3, 129, 4) < 0
+
+
+def test_linear_binding_refuses():
+    x, w = torch.zeros(4, 64, dtype=torch.float16), torch.zeros(40, 64, dtype=torch.float16)
+    with pytest.raises(TypeError):
+        sf.linear_forward(x, w)
+    with pytest.raises(ValueError):
+        sf.linear_forward(x, w, act="tanh")
+    with pytest.raises(TypeError):
+        sf.linear(x, w)
