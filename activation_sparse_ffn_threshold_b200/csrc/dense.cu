@@ -521,25 +521,27 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, 
 // ---------------------------------------------------------------- the linear layer's epilogue
 // 32 columns of the residual for a warp's rows, requested as panels are read (a row's 64 bytes by 4
 // lanes; 16-bit values fill the first half).
+template <bool WIDE>
 struct ResPiece {
-  uint4 w[8];
+  uint4 w[WIDE ? 8 : 4];
 };
-__device__ __forceinline__ void res_request(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows, ResPiece &p) {
+template <bool WIDE>
+__device__ __forceinline__ void res_request(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows,
+                                            ResPiece<WIDE> &p) {
   if (!E.res || !E.vec_res) return;
-  const int lane = threadIdx.x & 31, esize = Q.out32 ? 4 : 2, per = 16 / esize;
+  const int lane = threadIdx.x & 31, esize = WIDE ? 4 : 2, per = 16 / esize;
   const unsigned char *base = static_cast<const unsigned char *>(E.res) + row0 * E.ldres * esize;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i >= 4 && !Q.out32) break;
+  for (int i = 0; i < (WIDE ? 8 : 4); ++i) {
     const int row = (i & 3) * 8 + (lane >> 2), c = col + ((i >> 2) * 4 + (lane & 3)) * per;
     p.w[i] = make_uint4(0, 0, 0, 0);
     if (row < rows && c < Q.N) p.w[i] = *reinterpret_cast<const uint4 *>(base + (row * E.ldres + c) * esize);
   }
 }
 // Added to this lane's row of 32 columns.
-template <bool bf16>
-__device__ __forceinline__ void res_add(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows, const ResPiece &p,
-                                        uint32_t panel, float v[32]) {
+template <bool bf16, bool WIDE>
+__device__ __forceinline__ void res_add(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows,
+                                        const ResPiece<WIDE> &p, uint32_t panel, float *v) {
   if (!E.res) return;
   const int lane = threadIdx.x & 31;
   __syncwarp();
@@ -548,20 +550,19 @@ __device__ __forceinline__ void res_add(const LinearEnd &E, const Unit &Q, int64
       float f = 0.f;
       if (r < rows && col + lane < Q.N) {
         const int64_t i = (row0 + r) * E.ldres + col + lane;
-        f = Q.out32 ? static_cast<const float *>(E.res)[i] : load16(E.res, i, bf16);
+        f = WIDE ? static_cast<const float *>(E.res)[i] : load16(E.res, i, bf16);
       }
       const uint32_t at = panel_at(panel + (lane >> 4) * kPanel, r, (lane & 15) >> 2) + (lane & 3) * 4;
       asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(f) : "memory");
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i >= 4 && !Q.out32) break;
+    for (int i = 0; i < (WIDE ? 8 : 4); ++i) {
       sts16(panel_at(panel + (i >> 2) * kPanel, (i & 3) * 8 + (lane >> 2), lane & 3), p.w[i]);
     }
   }
   __syncwarp();
-  if (Q.out32 || !E.vec_res) {
+  if (WIDE || !E.vec_res) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint4 w = lds16(panel_at(panel + (j >> 2) * kPanel, lane, j & 3));
@@ -582,8 +583,8 @@ __device__ __forceinline__ void res_add(const LinearEnd &E, const Unit &Q, int64
   }
 }
 // 32 columns of this lane's row, value by value: rows that do not consist of 16-byte pieces.
-template <bool bf16>
-__device__ __forceinline__ void ragged_out(const Unit &Q, int64_t row0, int col, int rows, uint32_t panel, const float v[32]) {
+template <bool bf16, bool WIDE>
+__device__ __forceinline__ void ragged_out(const Unit &Q, int64_t row0, int col, int rows, uint32_t panel, const float *v) {
   const int lane = threadIdx.x & 31;
   __syncwarp();
 #pragma unroll
@@ -599,13 +600,13 @@ __device__ __forceinline__ void ragged_out(const Unit &Q, int64_t row0, int col,
                  : "=f"(f)
                  : "r"(panel_at(panel + (lane >> 4) * kPanel, r, (lane & 15) >> 2) + (uint32_t)((lane & 3) * 4)));
     const int64_t i = (row0 + r) * Q.ldo + col + lane;
-    if (Q.out32)
+    if (WIDE)
       static_cast<float *>(Q.out)[i] = f;
     else
       static_cast<uint16_t *>(Q.out)[i] = (uint16_t)pack16(f, 0.f, bf16);
   }
 }
-__device__ __forceinline__ void words32_out(uint32_t panel, const float v[32], unsigned char *base, int64_t ld, int rows,
+__device__ __forceinline__ void words32_out(uint32_t panel, const float *v, unsigned char *base, int64_t ld, int rows,
                                             int cols) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -618,89 +619,118 @@ __device__ __forceinline__ void words32_out(uint32_t panel, const float v[32], u
   }
 }
 
+// One 32-column piece of the tile, whose sums are in v; `bits` of a ReLU's slopes for the caller to keep.
+template <bool bf16, int width, bool WIDE>
+__device__ __forceinline__ void linear32(const DenseParams &P, const Unit &Q, int64_t row0, int n0, int c, int rows,
+                                         uint32_t panel, ResPiece<WIDE> &piece, float *v, uint32_t &word) {
+  const LinearEnd &E = P.end;
+  const int lane = threadIdx.x & 31, col = n0 + c, cols = Q.N - col;
+  if (Q.split > 1) {  // sums of a part of K, rows of N rounded up to 4
+    const int64_t ld = (Q.N + 3) / 4 * 16;
+    words32_out(panel, v, reinterpret_cast<unsigned char *>(Q.parts) + ((int64_t)Q.part * Q.M + row0) * ld + (int64_t)col * 4,
+                ld, rows, cols);
+    return;
+  }
+  if (E.bias) {
+    const float own = lane < cols ? load16(E.bias, col + lane, bf16) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, own, i);
+  }
+  if (E.act == SFNN_LINEAR_RELU) {
+    word = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      word |= v[i] <= 0.f ? 0u : 1u << i;
+      v[i] = v[i] < 0.f ? 0.f : v[i];
+    }
+  } else if (E.act != SFNN_LINEAR_NONE) {
+    uint32_t q[16];
+    const bool keep = E.slopes != nullptr;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint32_t lo = 0, hi = 0;
+      v[2 * i] = act_value(v[2 * i], E.act, keep, lo);
+      v[2 * i + 1] = act_value(v[2 * i + 1], E.act, keep, hi);
+      q[i] = lo | hi << 16;
+    }
+    if (keep) {
+      uint4 w[4];
+      words_to(w, q);
+      const int64_t ld = slope_row_bytes(Q.N, E.act);
+      panel_out(panel, w, static_cast<unsigned char *>(E.slopes) + row0 * ld + (int64_t)col * 2, ld, rows, 4);
+    }
+  }
+  res_add<bf16, WIDE>(E, Q, row0, col, rows, piece, panel, v);
+  if (c + 32 < width) res_request<WIDE>(E, Q, row0, col + 32, rows, piece);
+  if (!E.vec_out) {
+    ragged_out<bf16, WIDE>(Q, row0, col, rows, panel, v);
+  } else if (WIDE) {
+    words32_out(panel, v, static_cast<unsigned char *>(Q.out) + (row0 * Q.ldo + col) * 4, Q.ldo * 4, rows, cols);
+  } else {
+    uint4 w[4];
+    pack32(w, v, bf16);
+    panel_out(panel, w, static_cast<unsigned char *>(Q.out) + (row0 * Q.ldo + col) * 2, Q.ldo * 2, rows, (cols + 7) / 8);
+  }
+}
+
 template <bool bf16, int width>
-__device__ __forceinline__ void epi_linear(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
-                                           uint32_t panel, ResPiece &piece) {
+__device__ __forceinline__ void keep_bits(const DenseParams &P, const Unit &Q, int64_t row0, int n0, int rows,
+                                          const uint32_t *bits) {
   const LinearEnd &E = P.end;
   const int lane = threadIdx.x & 31;
+  if (!E.slopes || E.act != SFNN_LINEAR_RELU || Q.split > 1 || lane >= rows) return;
+  uint32_t *p = static_cast<uint32_t *>(E.slopes) + (row0 + lane) * (slope_row_bytes(Q.N, E.act) / 4) + n0 / 32;
+  if (width == 128)
+    *reinterpret_cast<uint4 *>(p) = make_uint4(bits[0], bits[1], bits[width / 32 - 2], bits[width / 32 - 1]);
+  else
+    *reinterpret_cast<uint2 *>(p) = make_uint2(bits[0], bits[1]);
+}
+
+template <bool bf16, int width>
+__device__ __forceinline__ void epi_linear(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
+                                           uint32_t panel, ResPiece<false> &piece) {
   const int rows = (int)min((int64_t)32, Q.M - row0);
   if (rows <= 0 || n0 >= Q.N) return;  // (the whole warp)
   uint32_t bits[width / 32] = {};
 #pragma unroll 1
-  for (int c = 0; c < width; c += 32) {
-    const int col = n0 + c, cols = Q.N - col;
-    if (cols <= 0) break;  // (the whole warp)
-    uint32_t raw[32];
+  for (int c = 0; c < width && n0 + c < Q.N; c += 32) {
+    uint32_t raw[32], word = 0;
     float v[32];
     __syncwarp();
     tm_ld32(taddr + c, raw);
     tm_wait_ld();
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
-    if (Q.split > 1) {  // sums of a part of K, rows of N rounded up to 4
-      const int64_t ld = (Q.N + 3) / 4 * 16;
-      words32_out(panel, v, reinterpret_cast<unsigned char *>(Q.parts) + ((int64_t)Q.part * Q.M + row0) * ld + (int64_t)col * 4,
-                  ld, rows, cols);
-      continue;
-    }
-    if (E.bias) {
-      const float own = lane < cols ? load16(E.bias, col + lane, bf16) : 0.f;
+    linear32<bf16, width, false>(P, Q, row0, n0, c, rows, panel, piece, v, word);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, own, i);
-    }
-    if (E.act == SFNN_LINEAR_RELU) {
-      uint32_t word = 0;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        word |= v[i] <= 0.f ? 0u : 1u << i;
-        v[i] = v[i] < 0.f ? 0.f : v[i];
-      }
-#pragma unroll
-      for (int i = 0; i < width / 32; ++i)
-        if (c == 32 * i) bits[i] = word;
-    } else if (E.act != SFNN_LINEAR_NONE) {
-      uint32_t q[16];
-      const bool keep = E.slopes != nullptr;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        uint32_t lo = 0, hi = 0;
-        v[2 * i] = act_value(v[2 * i], E.act, keep, lo);
-        v[2 * i + 1] = act_value(v[2 * i + 1], E.act, keep, hi);
-        q[i] = lo | hi << 16;
-      }
-      if (keep) {
-        uint4 w[4];
-        words_to(w, q);
-        const int64_t ld = slope_row_bytes(Q.N, E.act);
-        panel_out(panel, w, static_cast<unsigned char *>(E.slopes) + row0 * ld + (int64_t)col * 2, ld, rows, 4);
-      }
-    }
-    res_add<bf16>(E, Q, row0, col, rows, piece, panel, v);
-    if (c + 32 < width) res_request(E, Q, row0, col + 32, rows, piece);
-    if (!E.vec_out) {
-      ragged_out<bf16>(Q, row0, col, rows, panel, v);
-    } else if (Q.out32) {
-      words32_out(panel, v, static_cast<unsigned char *>(Q.out) + (row0 * Q.ldo + col) * 4, Q.ldo * 4, rows, cols);
-    } else {
-      uint4 w[4];
-      pack32(w, v, bf16);
-      panel_out(panel, w, static_cast<unsigned char *>(Q.out) + (row0 * Q.ldo + col) * 2, Q.ldo * 2, rows, (cols + 7) / 8);
-    }
+    for (int i = 0; i < width / 32; ++i)
+      if (c == 32 * i) bits[i] = word;
   }
-  if (E.slopes && E.act == SFNN_LINEAR_RELU && Q.split == 1 && lane < rows) {
-    uint32_t *p = static_cast<uint32_t *>(E.slopes) + (row0 + lane) * (slope_row_bytes(Q.N, E.act) / 4) + n0 / 32;
-    if (width == 128)
-      *reinterpret_cast<uint4 *>(p) = make_uint4(bits[0], bits[1], bits[width / 32 - 2], bits[width / 32 - 1]);
-    else
-      *reinterpret_cast<uint2 *>(p) = make_uint2(bits[0], bits[1]);
-  }
+  keep_bits<bf16, width>(P, Q, row0, n0, rows, bits);
+}
+
+// An fp32 result shows what the tensor cores' accumulators lose: they cut each sum off instead of
+// rounding it, about 2^-25 of it a 16-deep step towards zero (K = 28672: 1.1e-5 of the result with a
+// quarter of K in one sum).  So K is summed up in segments of kSegment chunks, each from zero, which
+// the epilogue's threads add up in registers while the next segment is multiplied.
+constexpr int kSegment = 8;
+template <bool bf16, int width>
+__device__ __forceinline__ void epi_linear32(const DenseParams &P, const Unit &Q, int64_t row0, int n0, uint32_t panel,
+                                             ResPiece<true> &piece, float (&sum)[width]) {
+  const int rows = (int)min((int64_t)32, Q.M - row0);
+  if (rows <= 0 || n0 >= Q.N) return;  // (the whole warp)
+  uint32_t bits[width / 32] = {};
+#pragma unroll
+  for (int c = 0; c < width; c += 32)
+    if (n0 + c < Q.N) linear32<bf16, width, true>(P, Q, row0, n0, c, rows, panel, piece, sum + c, bits[c / 32]);
+  keep_bits<bf16, width>(P, Q, row0, n0, rows, bits);
 }
 
 // ---------------------------------------------------------------- the kernel
 template <int EPI, bool BF16, int TN>  // TN: columns of a tile
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_dense(const __grid_constant__ DenseParams P) {
-  constexpr bool kDGated = EPI == kEpiDGated || EPI == kEpiDGated8;
+  constexpr bool kDGated = EPI == kEpiDGated || EPI == kEpiDGated8, kSegments = EPI == kEpiLinear32;
   constexpr int kStages = kStagesOf<EPI>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
@@ -786,7 +816,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      int it = 0;
+      int it = 0, turn = 0;
       bool ok = true;
       int id = walk.unit(0);
       Unit w{}, next = unit_at(P, max(id, 0));
@@ -797,32 +827,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // a 16-deep step of an operand: 2 KB of an MN-major tile, 32 bytes of a K-major one
         const uint32_t step_a = a_mn ? 2048u : 32u, step_b = b_mn ? 2048u : 32u;
         const uint32_t lbo_a = a_mn ? 8192u : 16u, lbo_b = b_mn ? 8192u : 16u;
-        const int buf = n & 1;
-        if (!bar_wait(&acc_empty[buf], (uint32_t)((n >> 1) & 1) ^ 1u)) {
-          ok = false;
-          break;
-        }
-        tm_fence_after();
-        const uint32_t d = tmem + (uint32_t)buf * 256u;
-        for (int kc = w.k_lo; kc < w.k_hi; ++kc, ++it) {
-          if (kc == w.k_lo + 1 || w.k_hi == w.k_lo + 1) {  // the next unit, while this one's MMAs run
-            id = walk.unit(n + 1);
-            next = unit_at(P, max(id, 0));
-          }
-          const int s = it % kStages;
-          if (!bar_wait(&full[s], (uint32_t)((it / kStages) & 1))) {
+        for (int k_lo = w.k_lo, k_hi; ok && k_lo < w.k_hi; k_lo = k_hi, ++turn) {
+          k_hi = kSegments ? min(k_lo + kSegment, w.k_hi) : w.k_hi;
+          const int buf = turn & 1;
+          if (!bar_wait(&acc_empty[buf], (uint32_t)((turn >> 1) & 1) ^ 1u)) {
             ok = false;
             break;
           }
           tm_fence_after();
-          const uint32_t sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + 16384u;
+          const uint32_t d = tmem + (uint32_t)buf * 256u;
+          for (int kc = k_lo; kc < k_hi; ++kc, ++it) {
+            if (kc == w.k_lo + 1 || w.k_hi == w.k_lo + 1) {  // the next unit, while this one's MMAs run
+              id = walk.unit(n + 1);
+              next = unit_at(P, max(id, 0));
+            }
+            const int s = it % kStages;
+            if (!bar_wait(&full[s], (uint32_t)((it / kStages) & 1))) {
+              ok = false;
+              break;
+            }
+            tm_fence_after();
+            const uint32_t sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + 16384u;
 #pragma unroll
-          for (uint32_t k = 0; k < 4; ++k)
-            mma_16<2>(d, mat_desc(sa + k * step_a, lbo_a, 1024), mat_desc(sb + k * step_b, lbo_b, 1024), idesc,
-                      (kc > w.k_lo || k > 0) ? 1u : 0u);
-          mma_commit_pair(&empty[s]);
+            for (uint32_t k = 0; k < 4; ++k)
+              mma_16<2>(d, mat_desc(sa + k * step_a, lbo_a, 1024), mat_desc(sb + k * step_b, lbo_b, 1024), idesc,
+                        (kc > k_lo || k > 0) ? 1u : 0u);
+            mma_commit_pair(&empty[s]);
+          }
+          if (ok) mma_commit_pair(&acc_full[buf]);
         }
-        if (ok) mma_commit_pair(&acc_full[buf]);
       }
       if (!ok) latch_error(P.err, kErrTimeout);
     }
@@ -839,6 +872,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+    int turn = 0;
     for (int n = 0, id; (id = walk.unit(n)) >= 0; ++n) {
       const Unit w = unit_at(P, id);
       const int buf = n & 1;
@@ -856,9 +890,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (kDGated) saved_request<EPI == kEpiDGated8>(P, w, row0, n0, panel + 2 * kPanel, scales);
-      ResPiece piece;
-      if (EPI == kEpiLinear && w.split == 1)
-        res_request(P.end, w, row0, n0, (int)max((int64_t)0, min((int64_t)32, w.M - row0)), piece);
+      ResPiece<kSegments> piece;
+      if ((EPI == kEpiLinear || kSegments) && w.split == 1)
+        res_request<kSegments>(P.end, w, row0, n0, (int)max((int64_t)0, min((int64_t)32, w.M - row0)), piece);
+      if constexpr (kSegments) {
+        float sum[kWide];
+#pragma unroll
+        for (int i = 0; i < kWide; ++i) sum[i] = 0.f;
+        bool there = true;
+        for (int k = w.k_lo; k < w.k_hi; k += kSegment, ++turn) {
+          const int buf = turn & 1;
+          there = __all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((turn >> 1) & 1)));
+          if (!there) break;
+          __syncwarp();
+          tm_fence_after();
+#pragma unroll
+          for (int c = 0; c < kWide; c += 32) {
+            uint32_t raw[32];
+            tm_ld32(tmem + lanes + (uint32_t)(buf * 256 + half * kWide + c), raw);
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(raw[i]);
+          }
+          tm_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive_cluster_relaxed(cluster_addr(&acc_empty[buf], 0));
+        }
+        if (!there) {
+          if (lane == 0) latch_error(P.err, kErrTimeout);
+          break;
+        }
+        epi_linear32<BF16, kWide>(P, w, row0, n0, panel, piece, sum);
+        continue;
+      }
       if (!__all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((n >> 1) & 1)))) {
         if (lane == 0) latch_error(P.err, kErrTimeout);
         break;
@@ -876,7 +940,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         if (kDGated)
           epi_dgated<EPI == kEpiDGated8, BF16, kWide>(P, w, acc + half * kWide, row0, n0, scales, panel);
-        else if (EPI == kEpiLinear)
+        else if constexpr (EPI == kEpiLinear)
           epi_linear<BF16, kWide>(P, w, acc + half * kWide, row0, n0, panel, piece);
         else
           epi_store<BF16, kWide>(P, w, acc + half * kWide, row0, n0, panel);
@@ -931,7 +995,7 @@ cudaError_t launch_dense(DenseParams &P, int epi, int num_sms, cudaStream_t s) {
   P.extra = P.count > 1 ? (lead + len / 2 + 1) / len : 0;
   if (epi == kEpiGated) return run<kEpiGated>(P, num_sms, s);
   if (epi == kEpiDGated) return P.save == SFNN_SAVE_ACT8 ? run<kEpiDGated8>(P, num_sms, s) : run<kEpiDGated>(P, num_sms, s);
-  if (epi == kEpiLinear) return run<kEpiLinear>(P, num_sms, s);
+  if (epi == kEpiLinear) return P.p[0].out32 ? run<kEpiLinear32>(P, num_sms, s) : run<kEpiLinear>(P, num_sms, s);
   return run<kEpiStore>(P, num_sms, s);
 }
 

@@ -154,7 +154,8 @@ enum DenseEpi : int {
   kEpiGated = 1,  // B0 = gate rows, B1 = up rows (128 each per tile): H = relu(G + b) * U
   kEpiDGated = 2,  // C = dH: dU = dH * R, dG = dH * U * [R > 0], H = R * U
   kEpiDGated8 = 3,  // the same with R and U held as 8-bit blocks
-  kEpiLinear = 4  // act(C + bias) + residual
+  kEpiLinear = 4,  // act(C + bias) + residual, 16-bit
+  kEpiLinear32 = 5  // the same as fp32, K summed up in segments
 };
 
 // The end of a linear layer: Y = act(Z + bias) + residual, and what the backward pass needs of act'.

@@ -44,7 +44,8 @@ struct alignas(64) SlimParams {
   const void *bias;
   void *out;
   int64_t ldo;
-  LinearEnd end;  // MODE kSlimLinear
+  LinearEnd end;        // MODE kSlimLinear, and ...
+  int accs, acc_cols;   // its accumulators, chunks of K dealt to them in turn, and their columns
   int32_t *err;
 };
 enum SlimMode : int { kSlimPlain = 0, kSlimGated = 1, kSlimLinear = 2 };
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
           break;
         }
         tm_fence_after();
+        int acc = 0, round = 0;  // the chunk's accumulator; whether it holds sums already
         for (int i = 0; i < steps; ++i, ++it) {
           const int s = it % stages, kn = min(P.kps, k_hi - (k_lo + i * P.kps));
           if (!bar_wait(&full[s], (uint32_t)((it / stages) & 1))) {
@@ -175,11 +177,13 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
             const uint32_t x = stage0 + (uint32_t)s * stage_bytes + (uint32_t)c * chunk_bytes, w = x + x_bytes;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t acc = (i > 0 || c > 0 || k > 0) ? 1u : 0u;
+              const bool more = (MODE == kSlimLinear ? round > 0 : i > 0 || c > 0) || k > 0;
               const uint64_t dx = mat_desc(x + k * 32, 16, 1024);
-              mma_16<1>(tmem, mat_desc(w + k * 32, 16, 1024), dx, idesc, acc);
-              if (GATED) mma_16<1>(tmem + (uint32_t)P.up_col, mat_desc(w + w_bytes + k * 32, 16, 1024), dx, idesc, acc);
+              const uint32_t d = tmem + (MODE == kSlimLinear ? (uint32_t)(acc * P.acc_cols) : 0u);
+              mma_16<1>(d, mat_desc(w + k * 32, 16, 1024), dx, idesc, more);
+              if (GATED) mma_16<1>(tmem + (uint32_t)P.up_col, mat_desc(w + w_bytes + k * 32, 16, 1024), dx, idesc, more);
             }
+            if (MODE == kSlimLinear && ++acc == P.accs) acc = 0, round = 1;
           }
           mma_commit(&empty[s]);
         }
@@ -198,6 +202,20 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
     const void *b = MODE == kSlimLinear ? P.end.bias : P.bias;
     return MODE != kSlimPlain && b && row < P.nb && col < P.N ? load16(b, col, P.bf16) : 0.f;
   };
+  // 8 tokens' sums of this thread's weight row
+  auto sums8 = [&](uint32_t at, uint32_t g[8]) {
+    __syncwarp();
+    tm_ld8(at, g);
+    if (MODE == kSlimLinear)
+#pragma unroll 1
+      for (int a = 1; a < P.accs; ++a) {
+        uint32_t h[8];
+        tm_ld8(at + (uint32_t)(a * P.acc_cols), h);
+        tm_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = __float_as_uint(__uint_as_float(g[i]) + __uint_as_float(h[i]));
+      }
+  };
   // the epilogue of this thread's weight row, with the other parts of a split tile at `sums`
   auto epilogue = [&](int t, float bias, const float *sums) {
     const int col = t * P.nb + row;
@@ -214,8 +232,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
                    : P.out32                           ? static_cast<const float *>(P.end.res)[at]
                                                        : load16(P.end.res, at, P.bf16);
         }
-      __syncwarp();
-      tm_ld8(lanes + c, g);
+      sums8(lanes + c, g);
       if (GATED) tm_ld8(lanes + (uint32_t)P.up_col + c, u);
       tm_wait_ld();
       if (!live) continue;
@@ -278,8 +295,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
 #pragma unroll 1
           for (int c = 0; c < P.T; c += 8) {
             uint32_t g[8];
-            __syncwarp();
-            tm_ld8(lanes + (uint32_t)(p * P.up_col + c), g);
+            sums8(lanes + (uint32_t)(p * P.up_col + c), g);
             tm_wait_ld();
             const uint32_t dst = dst0 + (uint32_t)(p * P.T + c) * 512u;
 #pragma unroll
@@ -409,8 +425,13 @@ sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
   P.m64 = P.split == 1 && P.nb <= 64;
   P.tiles = (q.N + P.nb - 1) / P.nb;
   P.up_col = gated ? up_to(P.t16, 32) : 0;  // tensor memory is read 32 columns at a time
+  P.accs = 1;
+  P.acc_cols = up_to(P.t16, 32);
+  // an fp32 result: no more than 64 sums of the tensor cores (which cut off, see dense.cu) in one
+  // accumulator, as far as tensor memory goes
+  if (q.end && q.out32) P.accs = std::max(1, std::min({P.nk / P.split, (P.nk / P.split + 15) / 16, 512 / P.acc_cols}));
   P.tmem_cols = 32;
-  while (P.tmem_cols < P.up_col + up_to(P.t16, 32)) P.tmem_cols *= 2;
+  while (P.tmem_cols < (gated ? 2 : P.accs) * P.acc_cols) P.tmem_cols *= 2;
   const int chunk = (P.t8 + np * P.nb8) * 128;
   const int over = std::max(0, (P.m64 ? 8192 : 16384) - P.nb8 * 128);  // an MMA reads all its lanes' rows
   // All of shared memory in flight (timed in turn: 1 token, 4096 x 11008, 54.6 us; with 131 and 83
