@@ -519,24 +519,25 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, 
 }
 
 // ---------------------------------------------------------------- the linear layer's epilogue
-// 32 columns of the residual for a warp's rows, requested as panels are read (a row's 64 bytes by 4
-// lanes; 16-bit values fill the first half).
+// The residual: 32 columns of a warp's rows come in as panels go out (a row's 64 bytes by 4 lanes).
+// 16-bit values wait in registers, requested a piece ahead; an fp32 result has its sums there.
 template <bool WIDE>
 struct ResPiece {
-  uint4 w[WIDE ? 8 : 4];
+  uint4 w[WIDE ? 1 : 4];
 };
+template <int ESIZE>
+__device__ __forceinline__ uint4 res_word(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows, int i) {
+  const int lane = threadIdx.x & 31, row = (i & 3) * 8 + (lane >> 2), c = col + ((i >> 2) * 4 + (lane & 3)) * (16 / ESIZE);
+  const unsigned char *base = static_cast<const unsigned char *>(E.res) + row0 * E.ldres * ESIZE;
+  if (row < rows && c < Q.N) return *reinterpret_cast<const uint4 *>(base + (row * E.ldres + c) * ESIZE);
+  return make_uint4(0, 0, 0, 0);
+}
 template <bool WIDE>
 __device__ __forceinline__ void res_request(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows,
                                             ResPiece<WIDE> &p) {
-  if (!E.res || !E.vec_res) return;
-  const int lane = threadIdx.x & 31, esize = WIDE ? 4 : 2, per = 16 / esize;
-  const unsigned char *base = static_cast<const unsigned char *>(E.res) + row0 * E.ldres * esize;
+  if (WIDE || !E.res || !E.vec_res) return;
 #pragma unroll
-  for (int i = 0; i < (WIDE ? 8 : 4); ++i) {
-    const int row = (i & 3) * 8 + (lane >> 2), c = col + ((i >> 2) * 4 + (lane & 3)) * per;
-    p.w[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows && c < Q.N) p.w[i] = *reinterpret_cast<const uint4 *>(base + (row * E.ldres + c) * esize);
-  }
+  for (int i = 0; i < (WIDE ? 0 : 4); ++i) p.w[i] = res_word<2>(E, Q, row0, col, rows, i);
 }
 // Added to this lane's row of 32 columns.
 template <bool bf16, bool WIDE>
@@ -555,11 +556,18 @@ __device__ __forceinline__ void res_add(const LinearEnd &E, const Unit &Q, int64
       const uint32_t at = panel_at(panel + (lane >> 4) * kPanel, r, (lane & 15) >> 2) + (lane & 3) * 4;
       asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(f) : "memory");
     }
+  } else if (WIDE) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = res_word<4>(E, Q, row0, col, rows, 4 * h + i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sts16(panel_at(panel + h * kPanel, i * 8 + (lane >> 2), lane & 3), w[i]);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < (WIDE ? 8 : 4); ++i) {
-      sts16(panel_at(panel + (i >> 2) * kPanel, (i & 3) * 8 + (lane >> 2), lane & 3), p.w[i]);
-    }
+    for (int i = 0; i < (WIDE ? 0 : 4); ++i) sts16(panel_at(panel, i * 8 + (lane >> 2), lane & 3), p.w[i]);
   }
   __syncwarp();
   if (WIDE || !E.vec_res) {
@@ -641,7 +649,7 @@ __device__ __forceinline__ void linear32(const DenseParams &P, const Unit &Q, in
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       word |= v[i] <= 0.f ? 0u : 1u << i;
-      v[i] = v[i] < 0.f ? 0.f : v[i];
+      v[i] = max_nan(v[i], 0.f);
     }
   } else if (E.act != SFNN_LINEAR_NONE) {
     uint32_t q[16];
@@ -651,7 +659,7 @@ __device__ __forceinline__ void linear32(const DenseParams &P, const Unit &Q, in
       uint32_t lo = 0, hi = 0;
       v[2 * i] = act_value(v[2 * i], E.act, keep, lo);
       v[2 * i + 1] = act_value(v[2 * i + 1], E.act, keep, hi);
-      q[i] = lo | hi << 16;
+      q[i] = __byte_perm(lo, hi, 0x5410);
     }
     if (keep) {
       uint4 w[4];
@@ -713,7 +721,7 @@ __device__ __forceinline__ void epi_linear(const DenseParams &P, const Unit &Q, 
 // rounding it, about 2^-25 of it a 16-deep step towards zero (K = 28672: 1.1e-5 of the result with a
 // quarter of K in one sum).  So K is summed up in segments of kSegment chunks, each from zero, which
 // the epilogue's threads add up in registers while the next segment is multiplied.
-constexpr int kSegment = 8;
+constexpr int kSegment = 16;
 template <bool bf16, int width>
 __device__ __forceinline__ void epi_linear32(const DenseParams &P, const Unit &Q, int64_t row0, int n0, uint32_t panel,
                                              ResPiece<true> &piece, float (&sum)[width]) {
@@ -905,12 +913,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           tm_fence_after();
 #pragma unroll
-          for (int c = 0; c < kWide; c += 32) {
-            uint32_t raw[32];
-            tm_ld32(tmem + lanes + (uint32_t)(buf * 256 + half * kWide + c), raw);
+          for (int c = 0; c < kWide; c += 16) {  // (more at a time do not fit the registers)
+            uint32_t raw[16];
+            tm_ld16(tmem + lanes + (uint32_t)(buf * 256 + half * kWide + c), raw);
             tm_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(raw[i]);
+            for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(raw[i]);
           }
           tm_fence_before();
           __syncwarp();

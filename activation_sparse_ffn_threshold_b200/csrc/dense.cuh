@@ -175,22 +175,57 @@ struct LinearEnd {
 __host__ __device__ inline int64_t slope_row_bytes(int64_t N, int act) {
   return act == SFNN_LINEAR_NONE ? 0 : act == SFNN_LINEAR_RELU ? (N + 127) / 128 * 16 : (N + 31) / 32 * 64;
 }
-// act(z) and, where `keep`, the code of act'(z) of the smooth ones; the limits at the infinities, NaN
-// for a NaN.  gelu: z Phi(z), Phi the normal distribution's integral; silu: z / (1 + e^-z).
+// act(z) and, where `keep`, the code of act'(z) of the smooth ones in a word's lower half; the limits
+// at the infinities, NaN for a NaN.
+//
+// gelu: z Phi(z), Phi the normal distribution's integral.  Phi(-a) e^(a^2 / 2) is smooth from 1/2 at
+// a = 0 to 0; it is taken as a polynomial of degree 8 in t = 1 / (1 + 0.295 a), fitted to its smallest
+// relative error over a in [0, 14] (3.7e-8; with the roundings 1e-6 down to z = -5, 5e-6 of 1e-38 at
+// -13), and times the e^(-z^2 / 2) that Phi' takes too: two special functions and 12 multiply-adds
+// (1999 tokens, 4096 x 16384: 399 us with CUDA's normcdff, 230 without an activation).
+// silu: z / (1 + e^-z).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float v;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float v;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ float exp2_approx(float v) {
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v));
+  return v;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(v));
+  return v;
+}
 __device__ __forceinline__ float act_value(float z, int act, bool keep, uint32_t &code) {
   if (act == SFNN_LINEAR_NONE) return z;
-  if (act == SFNN_LINEAR_RELU) return z < 0.f ? 0.f : z;
-  const float b = z < -80.f ? -80.f : z > 80.f ? 80.f : z;  // both are 0 or z beyond, and the products below finite
+  if (act == SFNN_LINEAR_RELU) return max_nan(z, 0.f);
+  const float low = max_nan(z, -80.f), b = min_nan(low, 80.f);  // both are 0 or z beyond, and the products below finite
   float p, s;
   if (act == SFNN_LINEAR_GELU) {
-    p = normcdff(b);
-    s = fmaf(b * 0.3989422804f, __expf(-0.5f * b * b), p);
+    const float e = exp2_approx(b * b * -0.7213475204f), t = rcp_approx(fmaf(0.295f, fabsf(b), 1.f));
+    float q = fmaf(0.0394212678f, t, -0.183406666f);
+    q = fmaf(q, t, 0.271017522f);
+    q = fmaf(q, t, -0.117072001f);
+    q = fmaf(q, t, 0.166289508f);
+    q = fmaf(q, t, 0.0847446173f);
+    q = fmaf(q, t, 0.12169943f);
+    q = fmaf(q, t, 0.117289335f);
+    q = fmaf(q, t, 1.7007178e-05f) * e;
+    p = b > 0.f ? 1.f - q : q;
+    s = fmaf(b * 0.3989422804f, e, p);
   } else {
-    p = 1.f / (1.f + __expf(-b));
+    p = rcp_approx(1.f + exp2_approx(b * -1.4426950409f));
     s = p * fmaf(b, 1.f - p, 1.f);
   }
-  if (keep) code = s == s ? __float2uint_rn(fmaf(s, 32768.f, 16384.f)) : 0xffffu;
-  return (z < b ? b : z) * p;
+  // the sum's last bit is worth 1; a NaN's lower half is 0xffff
+  if (keep) code = __float_as_uint(fmaf(s, 32768.f, 8388608.f + 16384.f));
+  return low * p;
 }
 __device__ __forceinline__ float slope_value(uint32_t code) {
   return code == 0xffffu ? __uint_as_float(0x7fffffffu) : (float)((int)code - 16384) * 0x1p-15f;

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const float *__restrict__ p
       for (int o = 1; o < 8; o *= 2) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
       if ((lane & 7) == 0) reinterpret_cast<uint32_t *>(s)[col / 32] = bits;
     } else if (col < (N + 31) / 32 * 32) {
-      *reinterpret_cast<uint2 *>(s + (int64_t)col * 2) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+      *reinterpret_cast<uint2 *>(s + (int64_t)col * 2) = make_uint2(__byte_perm(code[0], code[1], 0x5410), __byte_perm(code[2], code[3], 0x5410));
     }
   }
 }
