@@ -131,8 +131,8 @@ def load_library():
         "sfnn_linear_forward": ([P, P, L, P, L, P, P, L, P, P], S),
         "sfnn_linear_backward": ([P, P, P, L, P, P, P, P, L, P, P], S),
         "sfnn_norm_workspace": ([I, I], L),
-        "sfnn_norm_forward": ([P, P, L, P, L, P, P], S),
-        "sfnn_norm_backward": ([P, P, P, L, P, L, P, P, P, P, P, P, P, P, L, P], S),
+        "sfnn_norm_forward": ([P, P, L, P, L, P, P, P], S),
+        "sfnn_norm_backward": ([P, P, P, L, P, L, P, P, P, P, P, P, P, P, L, P, P], S),
         "sfnn_clip_workspace": ([I], L),
         "sfnn_clip_grad_norm": ([P, I, F, F, F, P, P, L, P], S),
         "sfnn_act8_restore": ([P, L, P, L, I, I, I, I, P, L, P], S),

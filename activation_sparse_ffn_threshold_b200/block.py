@@ -289,8 +289,8 @@ def residual_norm_forward(x, z=None, pre="rms", w=None, b=None, post="none", pos
             pr, ldr = r.data_ptr(), q.d
         h = x.new_empty(x.shape, dtype=dt) if q.pre else None
         stats = x.new_empty((q.T, 4), dtype=torch.float32) if save else None
-        _check(load_library().sfnn_norm_forward(ctypes.byref(q), pr, ldr, _vp(h), q.d, _vp(stats), _raw_stream(index)),
-               "sfnn_norm_forward")
+        _check(load_library().sfnn_norm_forward(ctypes.byref(q), pr, ldr, _vp(h), q.d, _vp(stats), _err_ptr(index),
+                                                _raw_stream(index)), "sfnn_norm_forward")
     return r, h, NormSaved(tensors, stats, options, dt) if save else None
 
 
@@ -326,7 +326,7 @@ def residual_norm_backward(dr, dh, saved: NormSaved, need=(True,) * 7, stream=No
         ws = new(max(nbytes, 16), dtype=torch.uint8)
         _check(lib.sfnn_norm_backward(ctypes.byref(q), _vp(saved.stats), pdr, lddr, pdh, lddh, _vp(dx), _vp(dz),
                                       _vp(dgate), _vp(dw), _vp(db), _vp(dpw), _vp(dpb), ws.data_ptr(), nbytes,
-                                      _raw_stream(index)), "sfnn_norm_backward")
+                                      _err_ptr(index), _raw_stream(index)), "sfnn_norm_backward")
     return dx, dz, dgate, dw, db, dpw, dpb
 
 

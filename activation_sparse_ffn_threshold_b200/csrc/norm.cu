@@ -13,6 +13,7 @@
 // R is formed again from X and Z (which the backward pass reads anyway) and not read back: R
 // rounded to its type would add its rounding to dw.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "dense.cuh"
@@ -84,43 +85,59 @@ __device__ __forceinline__ void store_values(void *p, int64_t at, int type32, bo
 
 // ---------------------------------------------------------------- sums over a row
 constexpr int kMaxCluster = 8;  // CTAs that share a row (the portable size)
-constexpr int kMaxWarps = 32;
+constexpr int kMaxWarps = 16;  // of a CTA
 
 // A row belongs to `warps` warps of the CTA, all rows of a CTA in step, or (CLUSTER) to all warps of
-// `ctas` CTAs, which then write their warps' sums into each other's shared memory.  The sums of two
+// `ctas` CTAs, which then write their warps' sums into each other's shared memory.  The sums of N
 // values; the buffers alternate, so one barrier a sum is enough: who writes a buffer again has passed
 // the barrier of the sum between, which every reader of it reached after reading.
 template <bool CLUSTER>
 struct RowSum {
-  static constexpr int kSlots = CLUSTER ? kMaxCluster * 16 : kMaxWarps;
+  static constexpr int kSlots = CLUSTER ? kMaxCluster * kMaxWarps : kMaxWarps;
   float2 *slots;  // [2][kSlots]
   int warps, ctas, rank, turn;
-  __device__ __forceinline__ float2 operator()(float2 v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-    if (!CLUSTER && warps == 1) return v;
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    static_assert(N == 1 || N == 2, "a slot holds two");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    spread<N, 16>(v);
+    if (!CLUSTER && warps == 1) return;
     float2 *s = slots + turn * kSlots;
     turn ^= 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float2 own = make_float2(v[0], v[N - 1]);
     if (CLUSTER) {
       if (lane < ctas)
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr(s + rank * warps + warp, lane)),
-                     "f"(v.x), "f"(v.y)
+                     "f"(own.x), "f"(own.y)
                      : "memory");
       __syncwarp();
       cluster_sync_all();
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] = 0.f;
+      for (int i = lane; i < warps * ctas; i += 32) {
+        v[0] += s[i].x;
+        if (N == 2) v[N - 1] += s[i].y;
+      }
+      spread<N, 16>(v);
     } else {
-      if (lane == 0) s[warp] = v;
+      if (lane == 0) s[warp] = own;
       __syncthreads();
-      s += warp / warps * warps;
+      // every lane takes a warp's sum (16 of them, twice over), and they are added up again
+      const int i = lane & 15;
+      const float2 part = i < warps ? s[warp / warps * warps + i] : make_float2(0.f, 0.f);
+      v[0] = part.x;
+      if (N == 2) v[N - 1] = part.y;
+      spread<N, 8>(v);
     }
-    v = make_float2(0.f, 0.f);
-    const int n = CLUSTER ? warps * ctas : warps;
-    for (int i = 0; i < n; ++i) v.x += s[i].x, v.y += s[i].y;
-    return v;
+  }
+
+ private:
+  template <int N, int FROM>
+  __device__ __forceinline__ void spread(float (&v)[N]) {
+#pragma unroll
+    for (int o = FROM; o > 0; o >>= 1)
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
   }
 };
 
@@ -146,7 +163,7 @@ struct Place {
 // ---------------------------------------------------------------- forward
 // NV vectors of V values a thread, a row to `threads` threads of a CTA (CLUSTER: of all the cluster's).
 template <bool bf16, int V, int NV, bool CLUSTER>
-__global__ void __launch_bounds__(512) k_norm_forward(const __grid_constant__ NormParams P, int threads) {
+__global__ void __launch_bounds__(256, 2) k_norm_forward(const __grid_constant__ NormParams P, int threads) {
   __shared__ float2 slots[2 * RowSum<CLUSTER>::kSlots];
   pdl_wait();
   pdl_launch_dependents();
@@ -173,14 +190,18 @@ __global__ void __launch_bounds__(512) k_norm_forward(const __grid_constant__ No
     if (kind == SFNN_NORM_LAYER) {
 #pragma unroll
       for (int i = 0; i < NV * V; ++i) m += v[i];
-      m = sum(make_float2(m, 0.f)).x * P.inv_d;
+      float t[1] = {m};
+      sum(t);
+      m = t[0] * P.inv_d;
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if ((lane + k * threads) * V < P.d)
 #pragma unroll
         for (int i = 0; i < V; ++i) q = fmaf(v[k * V + i] - m, v[k * V + i] - m, q);
-    return make_float2(m, rsqrtf(sum(make_float2(q, 0.f)).x * P.inv_d + P.eps));
+    float t[1] = {q};
+    sum(t);
+    return make_float2(m, rsqrtf(t[0] * P.inv_d + P.eps));
   };
   float2 of_z = make_float2(0.f, 1.f), of_r = make_float2(0.f, 1.f);
   if (P.z) {
@@ -224,19 +245,25 @@ __global__ void __launch_bounds__(512) k_norm_forward(const __grid_constant__ No
 }
 
 // ---------------------------------------------------------------- backward
+// What is summed over the rows.  Behind the post norm two sums serve five gradients, since a gate row,
+// w_post and b_post are the same for every row (with p = D, or D gate where each token has its gate):
+//
+//     S1 = sum p Z^,  S0 = sum p:   dw_post = c gate S1,  db_post = c gate S0,  dgate = c (w_post S1 + b_post S0)
+enum { kSumW, kSumB, kSum1, kSum0, kSums };
 struct NormBackParams {
   NormParams f;
   const void *dr, *dh;
   int64_t lddr, lddh;
   void *dx, *dz, *dgate;  // contiguous; dgate: of a gate of every token
   float *part;            // [groups][sums][d], or null
-  int sums;               // vectors that are summed over the rows
-  int at_w, at_b, at_gate, at_wp, at_bp;  // their places in part, -1: not asked for
+  int32_t *err;
+  int sums;       // that are asked for
+  int at[kSums];  // their places in part, or -1
 };
 
 // 8 values of a row a thread, a row to `threads` threads of a CTA (CLUSTER: of all the cluster's CTAs),
-// rows dealt to these groups in turn; a group keeps its columns' sums in registers.  FULL: every sum,
-// else dw and dw_post alone.
+// rows dealt to these groups in turn; a group keeps its columns' sums in registers.  FULL: all four,
+// else dw and S1 alone.
 template <bool bf16, int V, bool FULL, bool CLUSTER>
 __global__ void __launch_bounds__(512, FULL ? 1 : 2) k_norm_backward(const __grid_constant__ NormBackParams P, int threads) {
   constexpr int NV = 8 / V;
@@ -249,11 +276,11 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) k_norm_backward(const __gri
   const int64_t unit = at.unit, units = at.units;
   RowSum<CLUSTER> sum = at.sums(slots, threads);
   if (CLUSTER) cluster_sync_all();
-  float sw[8], sb[FULL ? 8 : 1], sg[FULL ? 8 : 1], swp[8], sbp[FULL ? 8 : 1];
+  float sw[8], sb[FULL ? 8 : 1], sum1[8], sum0[FULL ? 8 : 1];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    sw[i] = swp[i] = 0.f;
-    if (FULL) sb[i] = sg[i] = sbp[i] = 0.f;
+    sw[i] = sum1[i] = 0.f;
+    if (FULL) sb[i] = sum0[i] = 0.f;
   }
   // every group makes the same number of turns
   for (int64_t first = unit * groups; first < F.T; first += units * groups) {
@@ -315,8 +342,9 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) k_norm_backward(const __gri
           if (FULL) sb[j] += dh[j];
         }
       }
-      const float2 s = sum(make_float2(s1, s2));
-      const float m1 = F.pre == SFNN_NORM_LAYER ? s.x * F.inv_d : 0.f, m2 = s.y * F.inv_d;
+      float s[2] = {s1, s2};
+      sum(s);
+      const float m1 = F.pre == SFNN_NORM_LAYER ? s[0] * F.inv_d : 0.f, m2 = s[1] * F.inv_d;
 #pragma unroll
       for (int j = 0; j < 8; ++j) dr[j] = fmaf(st.y, u[j] - fmaf(x[j], m2, m1), dr[j]);
     }
@@ -351,10 +379,10 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) k_norm_backward(const __gri
         const int j = k * V + i;
         const float q = F.c * dr[j];
         dg[i] = q * fmaf(z[j], w[i], b[i]);
-        const float p = q * g[i];
-        if (FULL) sg[j] += dg[i], sbp[j] += p;
-        swp[j] = fmaf(p, z[j], swp[j]);
-        dr[j] = p * w[i];
+        const float p = F.ldg ? dr[j] * g[i] : dr[j];
+        if (FULL) sum0[j] += p;
+        sum1[j] = fmaf(p, z[j], sum1[j]);
+        dr[j] = q * g[i] * w[i];
         n1 += dr[j];
         n2 = fmaf(dr[j], z[j], n2);
       }
@@ -362,9 +390,10 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) k_norm_backward(const __gri
     }
     if (!P.dz) continue;
     if (F.post != SFNN_NORM_NONE) {
-      const float2 s = sum(make_float2(n1, n2));
-      n1 = F.post == SFNN_NORM_LAYER ? s.x * F.inv_d : 0.f;
-      n2 = s.y * F.inv_d;
+      float s[2] = {n1, n2};
+      sum(s);
+      n1 = F.post == SFNN_NORM_LAYER ? s[0] * F.inv_d : 0.f;
+      n2 = s[1] * F.inv_d;
     } else {
       n1 = n2 = 0.f;
     }
@@ -388,42 +417,532 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) k_norm_backward(const __gri
       if (c < F.d) store_values<true, V>(part, (int64_t)at * F.d + c, 1, bf16, v + k * V);
     }
   };
-  put(P.at_w, sw);
-  put(P.at_wp, swp);
+  put(P.at[kSumW], sw);
+  put(P.at[kSum1], sum1);
   if (FULL) {
-    put(P.at_b, sb);
-    put(P.at_gate, sg);
-    put(P.at_bp, sbp);
+    put(P.at[kSumB], sb);
+    put(P.at[kSum0], sum0);
   }
 }
 
-// out[s][c] = sum over the groups of part[group][s][c], in their order: 32 columns a CTA, a share of
-// the groups a warp.
+// ---------------------------------------------------------------- rows through shared memory
+// The kernels above hold a row's values in registers, and while a row's sums go round nothing is
+// on its way from memory.  These keep the next rows coming: persistent CTAs, each with a ring of
+// stages that bulk copies fill while the row before is worked on; the values stay in shared memory
+// until each is needed, the channels' weights beside them.  16 values a thread (two vectors of 8),
+// a row to `threads` threads, `rows` rows a step.
+constexpr int kMaxStages = 4;
+constexpr int kRingValues = 16;
+enum { kOfX, kOfZ, kOfDr, kOfDh, kOfGate, kOfRows };
+
+struct RingParams {
+  const void *p[kOfRows];  // arrays whose rows pass through the ring (null: none)
+  int64_t ld[kOfRows];     // bytes
+  int bytes[kOfRows];      // of a row
+  int at[kOfRows];         // in a stage
+  int stage, stages;       // bytes of a stage
+  int rows, threads;
+  int held;  // the channels' weights lie in shared memory (else they are formed where they are used)
+};
+// The channels' weights as the kernels use them, in 32 bits: c gate w_post (without the gate where every
+// token has its own), w, and for FULL c gate b_post and b.
+enum { kPostW, kPreW, kPostB, kPreB, kWeights };
+
+// Pairs of fp32 values: one instruction for both.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+template <bool bf16, bool WIDE, bool FULL>  // WIDE: X or Z is fp32; FULL: means and biases
+struct Ring {
+  static constexpr int kHeld = FULL ? 4 : 2;
+  const RingParams &R;
+  const NormParams &F;
+  int32_t *err;
+  const unsigned char *smem;  // stages, then the weights
+  uint64_t *full;
+  int T, d;
+  int steps;                 // of this CTA
+  int slot, phase;           // of the step at hand
+  const unsigned char *cur;  // its stage
+  __device__ __forceinline__ Ring(const RingParams &R_, const NormParams &F_, unsigned char *smem_, uint64_t *full_,
+                                  int32_t *err_)
+      : R(R_), F(F_), err(err_), smem(smem_), full(full_), T(F_.T), d(F_.d), slot(-1), phase(1), cur(nullptr) {
+    const int units = (T + R.rows - 1) / R.rows;
+    steps = (units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // (the grid is no larger than units)
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < R.stages; ++s) bar_init(&full[s], 1);
+      bar_init_fence();
+      fence_async_shared();
+    }
+    __syncthreads();
+    if (threadIdx.x < 32)
+      for (int s = 0; s < R.stages; ++s) request(s, s);
+    if (R.held) {  // (the first arrival's barrier publishes them)
+      float *to = reinterpret_cast<float *>(smem_ + R.stages * R.stage);
+      for (int k = 0; k < kHeld; ++k)
+        for (int c = threadIdx.x * 8; c < d; c += blockDim.x * 8) {
+          float2 v[4];
+          form(k, c, v);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float4 *>(to + k * d + c + 4 * i) = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+        }
+    }
+  }
+  __device__ __forceinline__ int64_t row0(int step) const { return (blockIdx.x + (int64_t)step * gridDim.x) * R.rows; }
+  __device__ __forceinline__ void request(int step, int s) const {  // warp 0
+    if (step >= steps) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t first = row0(step);
+    const int live = (int)min((int64_t)R.rows, T - first);
+    uint32_t row_bytes = 0;
+    for (int k = 0; k < kOfRows; ++k) row_bytes += R.p[k] ? R.bytes[k] : 0;
+    if (lane == 0) bar_expect_tx(&full[s], row_bytes * (uint32_t)live);
+    __syncwarp();
+    for (int k = 0; k < kOfRows; ++k) {
+      if (!R.p[k]) continue;
+      for (int r = lane; r < live; r += 32)
+        bulk_load(smem_u32(smem) + (uint32_t)(s * R.stage + R.at[k] + r * R.bytes[k]),
+                  static_cast<const unsigned char *>(R.p[k]) + (first + r) * R.ld[k], (uint32_t)R.bytes[k], &full[s]);
+    }
+    __syncwarp();
+  }
+  // The whole CTA: the step's rows are there, and those of the step before are done with (their
+  // stage is filled again).
+  __device__ __forceinline__ bool arrive(int step) {
+    const int before = slot;
+    if (++slot == R.stages) slot = 0;
+    if (slot == 0) phase ^= 1;
+    cur = smem + slot * R.stage;
+    if (R.stages == 1 && step > 0) {
+      __syncthreads();
+      if (threadIdx.x < 32) request(step, 0);
+    }
+    if (!__syncthreads_and(bar_wait(&full[slot], (uint32_t)phase))) {
+      if (threadIdx.x == 0) latch_error(err, kErrTimeout);
+      abandon(step);
+      return false;
+    }
+    if (R.stages > 1 && step > 0 && threadIdx.x < 32) request(step - 1 + R.stages, before);
+    return true;
+  }
+  // After a wait that ran out: this CTA's copies land before it ends (again with a limit).
+  __device__ __forceinline__ void abandon(int step) {
+    if (threadIdx.x == 0)
+      for (int i = 0; i < max(1, R.stages - 1) && step + i < steps; ++i) {
+        if (!bar_wait(&full[slot], (uint32_t)phase)) break;
+        if (++slot == R.stages) slot = 0, phase ^= 1;
+      }
+    __syncthreads();
+  }
+  // 8 values of the row at hand, of an array, from column c on
+  __device__ __forceinline__ void row(int r, int k, int c, bool wide, float2 v[4]) const {
+    const unsigned char *p = cur + R.at[k] + r * R.bytes[k];
+    if (WIDE && wide) {
+      const float4 *q = reinterpret_cast<const float4 *>(p + c * 4);
+      const float4 a = q[0], b = q[1];
+      v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+    } else {
+      widen8(*reinterpret_cast<const uint4 *>(p + c * 2), v);
+    }
+  }
+  // 8 weights, as the enumeration above says
+  __device__ __forceinline__ void weight(int k, int c, float2 v[4]) const {
+    if (R.held) {
+      const float4 *q = reinterpret_cast<const float4 *>(smem + R.stages * R.stage + (k * d + c) * 4);
+      const float4 a = q[0], b = q[1];
+      v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+    } else {
+      form(k, c, v);
+    }
+  }
+  __device__ __forceinline__ void form(int k, int c, float2 v[4]) const {
+    const void *p = k == kPostW ? F.wp : k == kPreW ? F.w : k == kPostB ? F.bp : F.b;
+    if (p)
+      widen8(ld_keep(static_cast<const uint16_t *>(p) + c), v);
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = both(k == kPostW || k == kPreW ? 1.f : 0.f);
+    if (k == kPreW || k == kPreB) return;
+    float2 g[4];
+    if (F.gate && !F.ldg)
+      widen8(ld_keep(static_cast<const uint16_t *>(F.gate) + c), g);
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = both(1.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(mul2(g[i], both(F.c)), v[i]);
+  }
+  static __device__ __forceinline__ void widen8(const uint4 &w, float2 v[4]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = bf16 ? make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u)) : unpack16(u[i], false);
+  }
+  static __device__ __forceinline__ void store(void *p, int64_t at, bool wide, const float2 v[4]) {
+    if (WIDE && wide) {
+      float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
+      q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+    } else {
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = make_uint4(
+          pack16(v[0].x, v[0].y, bf16), pack16(v[1].x, v[1].y, bf16), pack16(v[2].x, v[2].y, bf16), pack16(v[3].x, v[3].y, bf16));
+    }
+  }
+  // Z^ and R of 8 columns (Z^ untouched without Z).
+  __device__ __forceinline__ void residual(int r, int c, float mz, float sz, float2 zhat[4], float2 v[4]) const {
+    row(r, kOfX, c, F.x32, v);
+    if (!F.z) return;
+    float2 w[4];
+    row(r, kOfZ, c, F.z32, zhat);
+    weight(kPostW, c, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (FULL) zhat[i] = add2(zhat[i], both(-mz));
+      zhat[i] = mul2(zhat[i], both(sz));
+      v[i] = mul2(v[i], both(F.a));
+    }
+    if (!FULL && !R.p[kOfGate]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fma2(zhat[i], w[i], v[i]);
+      return;
+    }
+    float2 b[4], g[4];
+    if (FULL) weight(kPostB, c, b);
+    if (R.p[kOfGate]) row(r, kOfGate, c, false, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      b[i] = fma2(zhat[i], w[i], FULL ? b[i] : both(0.f));
+      v[i] = R.p[kOfGate] ? fma2(b[i], g[i], v[i]) : add2(b[i], v[i]);
+    }
+  }
+};
+
+template <bool bf16, bool WIDE, bool FULL>
+__global__ void __launch_bounds__(512, 2) k_norm_forward_ring(const __grid_constant__ NormParams P,
+                                                              const __grid_constant__ RingParams R, int32_t *err) {
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  __shared__ float2 slots[2 * kMaxWarps];
+  pdl_wait();
+  pdl_launch_dependents();
+  Ring<bf16, WIDE, FULL> ring(R, P, ring_smem, full, err);
+  const int threads = R.threads, lane = threadIdx.x % threads, mine = threadIdx.x / threads;
+  RowSum<false> sum{slots, threads / 32, 1, 0, 0};
+  auto mean_of = [&](float2 v) {
+    float t[1] = {v.x + v.y};
+    sum(t);
+    return t[0] * P.inv_d;
+  };
+  for (int step = 0; step < ring.steps; ++step) {
+    if (!ring.arrive(step)) return;
+    const int64_t row = ring.row0(step) + mine;
+    const bool live = row < P.T;
+    float mz = 0.f, sz = 1.f, mr = 0.f, sr = 1.f;
+    if (P.post != SFNN_NORM_NONE) {
+#pragma unroll
+      for (int pass = FULL ? 0 : 1; pass < 2; ++pass) {  // mean, then deviation
+        if (FULL && pass == 0 && P.post != SFNN_NORM_LAYER) continue;
+        float2 q = both(0.f);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = (lane + k * threads) * 8;
+          if (!live || c >= P.d) continue;
+          float2 z[4];
+          ring.row(mine, kOfZ, c, P.z32, z);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (FULL && pass) z[i] = add2(z[i], both(-mz));
+            q = FULL && !pass ? add2(q, z[i]) : fma2(z[i], z[i], q);
+          }
+        }
+        const float m = mean_of(q);
+        if (pass)
+          sz = rsqrtf(m + P.eps);
+        else
+          mz = m;
+      }
+    }
+    float2 r[8], q = both(0.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = (lane + k * threads) * 8;
+      float2 *rk = r + 4 * k, z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rk[i] = both(0.f);
+      if (!live || c >= P.d) continue;
+      ring.residual(mine, c, mz, sz, z, rk);
+      if (P.z) ring.store(P.r, row * P.ldr + c, P.x32, rk);
+      if (!FULL)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q = fma2(rk[i], rk[i], q);
+    }
+    if (P.pre != SFNN_NORM_NONE) {
+      if (FULL) {
+        if (P.pre == SFNN_NORM_LAYER) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q = add2(q, r[i]);
+          mr = mean_of(q);
+        }
+        q = both(0.f);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if ((lane + k * threads) * 8 < P.d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              r[4 * k + i] = add2(r[4 * k + i], both(-mr));
+              q = fma2(r[4 * k + i], r[4 * k + i], q);
+            }
+      }
+      sr = rsqrtf(mean_of(q) + P.eps);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int c = (lane + k * threads) * 8;
+        if (!live || c >= P.d) continue;
+        float2 w[4], b[4];
+        ring.weight(kPreW, c, w);
+        if (FULL) ring.weight(kPreB, c, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 hat = mul2(r[4 * k + i], both(sr));
+          w[i] = FULL ? fma2(hat, w[i], b[i]) : mul2(hat, w[i]);
+        }
+        ring.store(P.h, row * P.ldh + c, false, w);
+      }
+    }
+    if (P.stats && live && lane == 0) *reinterpret_cast<float4 *>(P.stats + row * 4) = make_float4(mr, sr, mz, sz);
+  }
+}
+
+template <bool bf16, bool WIDE, bool FULL>  // FULL: the sums of dH and D as well
+__global__ void __launch_bounds__(512, 1) k_norm_backward_ring(const __grid_constant__ NormBackParams P,
+                                                               const __grid_constant__ RingParams R) {
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  __shared__ float2 slots[2 * kMaxWarps];
+  pdl_wait();
+  pdl_launch_dependents();
+  const NormParams &F = P.f;
+  Ring<bf16, WIDE, FULL> ring(R, F, ring_smem, full, P.err);
+  const int threads = R.threads, lane = threadIdx.x % threads, mine = threadIdx.x / threads;
+  RowSum<false> sum{slots, threads / 32, 1, 0, 0};
+  float2 sw[8], sum1[8], sb[FULL ? 8 : 1], sum0[FULL ? 8 : 1];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    sw[i] = sum1[i] = both(0.f);
+    if (FULL) sb[i] = sum0[i] = both(0.f);
+  }
+  for (int step = 0; step < ring.steps; ++step) {
+    const int64_t row = ring.row0(step) + mine;
+    const bool live = row < F.T;
+    float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) st = __ldg(reinterpret_cast<const float4 *>(F.stats) + row);
+    if (!ring.arrive(step)) return;
+    float2 D[8], hat[8], zhat[8];
+    float2 s1 = both(0.f), s2 = both(0.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = (lane + k * threads) * 8;
+      float2 *Dk = D + 4 * k, *hk = hat + 4 * k, *zk = zhat + 4 * k;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) Dk[i] = hk[i] = zk[i] = both(0.f);
+      if (!live || c >= F.d) continue;
+      ring.residual(mine, c, st.z, st.w, zk, hk);
+      if (!P.dh) continue;
+      float2 dh[4], w[4];
+      ring.row(mine, kOfDh, c, false, dh);
+      ring.weight(kPreW, c, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (FULL) hk[i] = add2(hk[i], both(-st.x));
+        hk[i] = mul2(hk[i], both(st.y));
+        Dk[i] = mul2(dh[i], w[i]);
+        if (FULL) s1 = add2(s1, Dk[i]), sb[4 * k + i] = add2(sb[4 * k + i], dh[i]);
+        s2 = fma2(Dk[i], hk[i], s2);
+        sw[4 * k + i] = fma2(dh[i], hk[i], sw[4 * k + i]);
+      }
+    }
+    if (P.dh) {  // D: s (u - mean u - R^ mean(u R^)), dR is added below
+      float m1 = 0.f, m2;
+      if (FULL) {
+        float t[2] = {s1.x + s1.y, s2.x + s2.y};
+        sum(t);
+        m1 = F.pre == SFNN_NORM_LAYER ? t[0] * F.inv_d : 0.f;
+        m2 = t[1] * F.inv_d;
+      } else {
+        float t[1] = {s2.x + s2.y};
+        sum(t);
+        m2 = t[0] * F.inv_d;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (FULL) D[j] = add2(D[j], both(-m1));
+        D[j] = mul2(both(st.y), fma2(hat[j], both(-m2), D[j]));
+      }
+    }
+    float2 n1 = both(0.f), n2 = both(0.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = (lane + k * threads) * 8;
+      float2 *Dk = D + 4 * k, *zk = zhat + 4 * k;
+      if (!live || c >= F.d) continue;
+      float2 v[4];
+      if (P.dr) {
+        ring.row(mine, kOfDr, c, F.x32, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Dk[i] = add2(Dk[i], v[i]);
+      }
+      if (P.dx) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = mul2(both(F.a), Dk[i]);
+        ring.store(P.dx, row * F.d + c, F.x32, v);
+      }
+      if (!F.z) continue;
+      float2 w[4];
+      ring.weight(kPostW, c, w);
+      if (R.p[kOfGate]) {
+        float2 g[4];
+        ring.row(mine, kOfGate, c, false, g);
+        if (P.dgate) {
+          if (FULL) ring.weight(kPostB, c, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = mul2(Dk[i], fma2(zk[i], w[i], FULL ? v[i] : both(0.f)));
+          ring.store(P.dgate, row * F.d + c, false, v);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Dk[i] = mul2(Dk[i], g[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (FULL) sum0[4 * k + i] = add2(sum0[4 * k + i], Dk[i]);
+        sum1[4 * k + i] = fma2(Dk[i], zk[i], sum1[4 * k + i]);
+        Dk[i] = mul2(Dk[i], w[i]);
+        if (FULL) n1 = add2(n1, Dk[i]);
+        n2 = fma2(Dk[i], zk[i], n2);
+      }
+    }
+    if (!P.dz) continue;
+    float m1 = 0.f, m2 = 0.f;
+    if (F.post != SFNN_NORM_NONE) {
+      float t[FULL ? 2 : 1];
+      t[0] = n2.x + n2.y;
+      if (FULL) t[FULL ? 1 : 0] = n1.x + n1.y;
+      sum(t);
+      m2 = t[0] * F.inv_d;
+      if (FULL && F.post == SFNN_NORM_LAYER) m1 = t[FULL ? 1 : 0] * F.inv_d;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = (lane + k * threads) * 8;
+      if (!live || c >= F.d) continue;
+      float2 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = fma2(zhat[4 * k + i], both(-m2), D[4 * k + i]);
+        if (FULL) v[i] = add2(v[i], both(-m1));
+        v[i] = mul2(both(st.w), v[i]);
+      }
+      ring.store(P.dz, row * F.d + c, F.z32, v);
+    }
+  }
+  if (!P.part) return;
+  float *part = P.part + ((int64_t)blockIdx.x * R.rows + mine) * P.sums * F.d;
+  auto put = [&](int at, const float2 *v) {
+    if (at < 0) return;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = (lane + k * threads) * 8;
+      if (c >= F.d) continue;
+      float4 *q = reinterpret_cast<float4 *>(part + (int64_t)at * F.d + c);
+      q[0] = make_float4(v[4 * k].x, v[4 * k].y, v[4 * k + 1].x, v[4 * k + 1].y);
+      q[1] = make_float4(v[4 * k + 2].x, v[4 * k + 2].y, v[4 * k + 3].x, v[4 * k + 3].y);
+    }
+  };
+  put(P.at[kSumW], sw);
+  put(P.at[kSum1], sum1);
+  if (FULL) {
+    put(P.at[kSumB], sb);
+    put(P.at[kSum0], sum0);
+  }
+}
+
+// The gradients of the channels' weights from the groups' sums: 32 columns a CTA, a share of the
+// groups a warp, added up in their order.
 struct NormSums {
   const float *part;
   int groups, sums, d;
-  void *out[5];
+  int at[kSums];
+  float c;
+  const void *gate, *wp, *bp;  // one gate row, or null
+  void *dw, *db, *dgate, *dwp, *dbp;
 };
+constexpr int kSumWarps = 16;
 template <bool bf16>
-__global__ void __launch_bounds__(256) k_norm_sums(const __grid_constant__ NormSums P) {
-  __shared__ float s[8][33];
+__global__ void __launch_bounds__(kSumWarps * 32) k_norm_sums(const __grid_constant__ NormSums P) {
+  __shared__ float s[kSums][kSumWarps][33];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t cols = (int64_t)P.sums * P.d, c = (int64_t)blockIdx.x * 32 + lane;
-  float v = 0.f;
-  if (c < cols)
-#pragma unroll 4
-    for (int g = warp; g < P.groups; g += 8) v += __ldg(P.part + g * cols + c);
-  s[warp][lane] = v;
-  __syncthreads();
-  if (warp == 0 && c < cols) {
-    v = 0.f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  const int64_t group = (int64_t)P.sums * P.d;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += s[i][lane];
-    const int which = (int)(c / P.d);
-    static_cast<uint16_t *>(P.out[which])[c - (int64_t)which * P.d] = (uint16_t)pack16(v, 0.f, bf16);
+  for (int k = 0; k < kSums; ++k) {
+    if (P.at[k] < 0) continue;
+    const float *p = P.part + (int64_t)P.at[k] * P.d + c;
+    float v = 0.f;
+    if (c < P.d)
+#pragma unroll 8
+      for (int g = warp; g < P.groups; g += kSumWarps) v += __ldg(p + g * group);
+    s[k][warp][lane] = v;
   }
+  __syncthreads();
+  if (warp || c >= P.d) return;
+  float v[kSums];
+#pragma unroll
+  for (int k = 0; k < kSums; ++k) {
+    v[k] = 0.f;
+    if (P.at[k] >= 0)
+#pragma unroll
+      for (int i = 0; i < kSumWarps; ++i) v[k] += s[k][i][lane];
+  }
+  auto put = [&](void *p, float f) {
+    if (p) static_cast<uint16_t *>(p)[c] = (uint16_t)pack16(f, 0.f, bf16);
+  };
+  const float g = P.c * (P.gate ? load16(P.gate, c, bf16) : 1.f);
+  put(P.dw, v[kSumW]);
+  put(P.db, v[kSumB]);
+  put(P.dwp, g * v[kSum1]);
+  put(P.dbp, g * v[kSum0]);
+  if (P.dgate)
+    put(P.dgate, P.c * fmaf(P.wp ? load16(P.wp, c, bf16) : 1.f, v[kSum1], P.bp ? load16(P.bp, c, bf16) * v[kSum0] : 0.f));
 }
 
 // ---------------------------------------------------------------- host
@@ -490,17 +1009,19 @@ cudaError_t launch_rows(Kernel kernel, int grid, int block, int ctas, int thread
 
 template <bool bf16>
 cudaError_t run_forward(const NormParams &P, bool vec, cudaStream_t s) {
-  const int per = P.d <= 256 ? 8 : 16;  // values a thread
+  // A thread holds 8, 16 or 32 values: as many as leave a row a warp, at most 32.
+  const int per = P.d <= 256 ? 8 : P.d <= 512 ? 16 : 32;
   int ctas = 1;
-  while (P.d > per * 512 * ctas) ctas *= 2;
+  while (P.d > per * 256 * ctas) ctas *= 2;
   int block = (int)up((P.d + per * ctas - 1) / (per * ctas), 32);
   const int threads = block * ctas, rows = ctas > 1 ? 1 : std::max(1, 128 / block);
   block *= rows;
   const int64_t units = (P.T + (int64_t)rows - 1) / rows;  // (T is at most 2^28, a row's CTAs at most 4)
   auto run = [&](auto kernel) { return launch_rows(kernel, (int)(units * ctas), block, ctas, threads, P, s); };
-  if (ctas > 1) return vec ? run(k_norm_forward<bf16, 8, 2, true>) : run(k_norm_forward<bf16, 1, 16, true>);
+  if (ctas > 1) return vec ? run(k_norm_forward<bf16, 8, 4, true>) : run(k_norm_forward<bf16, 1, 32, true>);
   if (per == 8) return vec ? run(k_norm_forward<bf16, 8, 1, false>) : run(k_norm_forward<bf16, 1, 8, false>);
-  return vec ? run(k_norm_forward<bf16, 8, 2, false>) : run(k_norm_forward<bf16, 1, 16, false>);
+  if (per == 16) return vec ? run(k_norm_forward<bf16, 8, 2, false>) : run(k_norm_forward<bf16, 1, 16, false>);
+  return vec ? run(k_norm_forward<bf16, 8, 4, false>) : run(k_norm_forward<bf16, 1, 32, false>);
 }
 
 // The backward kernel's shape: a row's threads, and the groups that rows are dealt to.
@@ -520,8 +1041,13 @@ BackShape back_shape(int64_t T, int d, bool full, int sms) {
   b.grid = (int)std::min(units, most) * b.ctas;
   return b;
 }
-int64_t back_workspace(int64_t T, int d, int sums, int sms) {  // (the larger grid)
-  return up(back_shape(std::max<int64_t>(T, 1), d, false, sms).groups() * sums * d * 4, 256);
+int64_t ring_groups(int64_t T, int d, int sms) {  // at most, with two CTAs an SM
+  const int rows = std::max(1, 256 / (int)up((d + kRingValues - 1) / kRingValues, 32));
+  return std::min((T + rows - 1) / rows, (int64_t)2 * sms) * rows;
+}
+int64_t back_workspace(int64_t T, int d, int sums, int sms) {  // (the larger of the two kernels')
+  T = std::max<int64_t>(T, 1);
+  return up(std::max(back_shape(T, d, false, sms).groups(), ring_groups(T, d, sms)) * sums * d * 4, 256);
 }
 
 template <bool bf16, int V, bool FULL>
@@ -529,9 +1055,82 @@ cudaError_t run_backward(const NormBackParams &P, const BackShape &b, cudaStream
   return b.ctas == 1 ? launch_rows(k_norm_backward<bf16, V, FULL, false>, b.grid, b.block, 1, b.threads, P, s)
                      : launch_rows(k_norm_backward<bf16, V, FULL, true>, b.grid, b.block, b.ctas, b.threads, P, s);
 }
+// The rows' way through shared memory: (ctas per SM, shared memory of a CTA) in R and the return values.
+struct RingShape {
+  int block, grid, smem;
+  int64_t groups;
+};
+RingShape ring_shape(RingParams &R, const NormParams &F, bool full, const void *dr, int64_t lddr, const void *dh, int64_t lddh,
+                     int sms) {
+  const int d = F.d;
+  R.threads = (int)up((d + kRingValues - 1) / kRingValues, 32);
+  R.rows = std::max(1, 256 / R.threads);
+  auto row = [&](int k, const void *p, int64_t ld, bool wide) {
+    R.p[k] = p;
+    R.ld[k] = ld * (wide ? 4 : 2);
+    R.bytes[k] = d * (wide ? 4 : 2);
+    R.at[k] = R.stage;
+    if (p) R.stage += R.bytes[k] * R.rows;
+  };
+  row(kOfX, F.x, F.ldx, F.x32);
+  row(kOfZ, F.z, F.ldz, F.z32);
+  row(kOfDr, dr, lddr, F.x32);
+  row(kOfDh, dh, lddh, false);
+  row(kOfGate, F.ldg ? F.gate : nullptr, F.ldg, false);
+  RingShape s;
+  s.block = R.threads * R.rows;
+  // Two CTAs an SM where each has room for two stages at least; the weights in shared memory where two
+  // stages are left beside them.
+  const int held = (full ? 4 : 2) * d * 4, half = 112 * 1024;
+  const int per_sm = s.block <= 320 && 2 * R.stage <= half ? 2 : 1;
+  const int budget = per_sm == 2 ? half : 2 * half;
+  R.held = 2 * R.stage + held <= budget;
+  R.stages = std::max(1, std::min(kMaxStages, (budget - (R.held ? held : 0)) / R.stage));
+  s.smem = R.stages * R.stage + (R.held ? held : 0);
+  const int64_t units = (F.T + (int64_t)R.rows - 1) / R.rows;
+  s.grid = (int)std::min<int64_t>(units, (int64_t)sms * per_sm);
+  s.groups = (int64_t)s.grid * R.rows;
+  return s;
+}
+constexpr int kRingWidth = 512 * kRingValues;
+constexpr size_t kRingSmem = 225 * 1024;
+constexpr int kRingRows = 4;  // rows an SM from which the ring is worth its start
+template <class Kernel, class... Args>
+cudaError_t launch_ring(Kernel kernel, const RingShape &s, std::atomic<uint64_t> &ready, cudaStream_t stream, const Args &...args) {
+  const cudaError_t e = allow_smem(kernel, kRingSmem, ready);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3((unsigned)s.grid), dim3((unsigned)s.block), (size_t)s.smem, stream, args...);
+}
+template <bool bf16, bool WIDE, bool FULL>
+cudaError_t run_ring(const RingShape &s, const NormParams &P, const RingParams &R, int32_t *err, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};
+  return launch_ring(k_norm_forward_ring<bf16, WIDE, FULL>, s, ready, stream, P, R, err);
+}
+template <bool bf16, bool WIDE, bool FULL>
+cudaError_t run_ring(const RingShape &s, const NormBackParams &P, const RingParams &R, int32_t *, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};
+  return launch_ring(k_norm_backward_ring<bf16, WIDE, FULL>, s, ready, stream, P, R);
+}
+template <class Params>
+cudaError_t run_ring(bool bf16, bool wide, bool full, const RingShape &s, const Params &P, const RingParams &R, int32_t *err,
+                     cudaStream_t stream) {
+  switch (bf16 * 4 + wide * 2 + full) {
+    case 0: return run_ring<false, false, false>(s, P, R, err, stream);
+    case 1: return run_ring<false, false, true>(s, P, R, err, stream);
+    case 2: return run_ring<false, true, false>(s, P, R, err, stream);
+    case 3: return run_ring<false, true, true>(s, P, R, err, stream);
+    case 4: return run_ring<true, false, false>(s, P, R, err, stream);
+    case 5: return run_ring<true, false, true>(s, P, R, err, stream);
+    case 6: return run_ring<true, true, false>(s, P, R, err, stream);
+    default: return run_ring<true, true, true>(s, P, R, err, stream);
+  }
+}
+
 template <bool bf16>
 cudaError_t run_backward(const NormBackParams &P, bool vec, bool full, const BackShape &b, cudaStream_t s) {
-  if (vec) return full ? run_backward<bf16, 8, true>(P, b, s) : run_backward<bf16, 8, false>(P, b, s);
+  if (vec)  // (narrower rows go through the ring)
+    return full ? launch_rows(k_norm_backward<bf16, 8, true, true>, b.grid, b.block, b.ctas, b.threads, P, s)
+                : launch_rows(k_norm_backward<bf16, 8, false, true>, b.grid, b.block, b.ctas, b.threads, P, s);
   return full ? run_backward<bf16, 1, true>(P, b, s) : run_backward<bf16, 1, false>(P, b, s);
 }
 
@@ -544,16 +1143,17 @@ extern "C" {
 
 int64_t sfnn_norm_workspace(int32_t T, int32_t d) {
   if (T < 0 || d < 1 || d > kMaxWidth) return -1;
-  return back_workspace(T, d, 5, std::max(1, device_sms()));
+  return back_workspace(T, d, kSums, std::max(1, device_sms()));
 }
 
 sfnn_status sfnn_norm_forward(const sfnn_norm_desc *q, void *r, int64_t ldr, void *h, int64_t ldh, float *stats,
-                              sfnn_stream_t stream) {
+                              int32_t *err, sfnn_stream_t stream) {
   const sfnn_status st = check(q);
   if (st != SFNN_OK) return st;
   if (q->T == 0) return SFNN_OK;
   NormParams P = params(q);
-  if ((q->z && !rows_ok(r, ldr, q->d, P.x32)) || (q->pre != SFNN_NORM_NONE && !rows_ok(h, ldh, q->d, false)) || !on(stats, 16))
+  if ((q->z && !rows_ok(r, ldr, q->d, P.x32)) || (q->pre != SFNN_NORM_NONE && !rows_ok(h, ldh, q->d, false)) || !on(stats, 16) || !err ||
+      !on(err, 4))
     return SFNN_ERR_INVALID_ARG;
   P.r = q->z ? r : nullptr;
   P.h = q->pre != SFNN_NORM_NONE ? h : nullptr;
@@ -562,13 +1162,24 @@ sfnn_status sfnn_norm_forward(const sfnn_norm_desc *q, void *r, int64_t ldr, voi
   P.stats = stats;
   const bool vec = vectors(P) && vectors(P.r, ldr) && vectors(P.h, ldh);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = q->dtype == SFNN_BF16 ? run_forward<true>(P, vec, s) : run_forward<false>(P, vec, s);
+  const bool bf16 = q->dtype == SFNN_BF16;
+  const int sms = device_sms();
+  if (sms < 1) return SFNN_ERR_CUDA;
+  cudaError_t e;
+  if (vec && P.d <= kRingWidth && P.T >= kRingRows * sms) {
+    RingParams R{};
+    const bool full = P.pre == SFNN_NORM_LAYER || P.post == SFNN_NORM_LAYER || P.b || P.bp;
+    const RingShape shape = ring_shape(R, P, full, nullptr, 0, nullptr, 0, sms);
+    e = run_ring(bf16, P.x32 || P.z32, full, shape, P, R, err, s);
+  } else {
+    e = bf16 ? run_forward<true>(P, vec, s) : run_forward<false>(P, vec, s);
+  }
   return e == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
 }
 
 sfnn_status sfnn_norm_backward(const sfnn_norm_desc *q, const float *stats, const void *dr, int64_t lddr, const void *dh,
                                int64_t lddh, void *dx, void *dz, void *dgate, void *dw, void *db, void *dpost_w,
-                               void *dpost_b, void *ws, int64_t ws_bytes, sfnn_stream_t stream) {
+                               void *dpost_b, void *ws, int64_t ws_bytes, int32_t *err, sfnn_stream_t stream) {
   const sfnn_status st = check(q);
   if (st != SFNN_OK) return st;
   const bool bf16 = q->dtype == SFNN_BF16;
@@ -580,31 +1191,23 @@ sfnn_status sfnn_norm_backward(const sfnn_norm_desc *q, const float *stats, cons
   if (!on(dx, q->x_dtype == SFNN_F32 ? 4 : 2) || !on(dz, q->z_dtype == SFNN_F32 ? 4 : 2)) return SFNN_ERR_INVALID_ARG;
   const bool one_gate = q->gate && q->ldg == 0;
   NormSums S{};
-  NormBackParams P{};
-  auto asked = [&](void *out) {
-    if (!out) return -1;
-    S.out[S.sums] = out;
-    return S.sums++;
-  };
-  P.at_w = asked(dw);
-  P.at_wp = asked(dpost_w);
-  const int plain = S.sums;
-  P.at_b = asked(db);
-  P.at_gate = asked(one_gate ? dgate : nullptr);
-  P.at_bp = asked(dpost_b);
-  const bool full = S.sums > plain;
+  S.dw = dw, S.db = db, S.dwp = dpost_w, S.dbp = dpost_b, S.dgate = one_gate ? dgate : nullptr;
+  const bool asked[kSums] = {dw != nullptr, db != nullptr, dpost_w || S.dgate, dpost_b || (S.dgate && q->post_b)};
+  for (int i = 0; i < kSums; ++i) S.at[i] = asked[i] ? S.sums++ : -1;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (q->T == 0) {  // sums over no tokens
-    for (int i = 0; i < S.sums; ++i)
-      if (cudaMemsetAsync(S.out[i], 0, (size_t)q->d * 2, s) != cudaSuccess) return SFNN_ERR_CUDA;
+    for (void *p : {S.dw, S.db, S.dwp, S.dbp, S.dgate})
+      if (p && cudaMemsetAsync(p, 0, (size_t)q->d * 2, s) != cudaSuccess) return SFNN_ERR_CUDA;
     return SFNN_OK;
   }
   const bool x32 = q->x_dtype == SFNN_F32;
-  if ((dr && !rows_ok(dr, lddr, q->d, x32)) || (dh && !rows_ok(dh, lddh, q->d, false)) || !stats || !on(stats, 16))
+  if ((dr && !rows_ok(dr, lddr, q->d, x32)) || (dh && !rows_ok(dh, lddh, q->d, false)) || !stats || !on(stats, 16) ||
+      !err || !on(err, 4))
     return SFNN_ERR_INVALID_ARG;
   const int sms = device_sms();
   if (sms < 1) return SFNN_ERR_CUDA;
   if (S.sums && (!ws || !on(ws, 16) || ws_bytes < back_workspace(q->T, q->d, S.sums, sms))) return SFNN_ERR_INVALID_ARG;
+  NormBackParams P{};
   P.f = params(q);
   P.f.stats = const_cast<float *>(stats);
   P.dr = dr, P.lddr = lddr;
@@ -612,19 +1215,36 @@ sfnn_status sfnn_norm_backward(const sfnn_norm_desc *q, const float *stats, cons
   P.dx = dx, P.dz = dz;
   P.dgate = one_gate ? nullptr : dgate;
   P.part = S.sums ? static_cast<float *>(ws) : nullptr;
+  P.err = err;
   P.sums = S.sums;
+  std::copy(S.at, S.at + kSums, P.at);
   const bool vec = vectors(P.f) && vectors(dr, lddr) && vectors(dh, lddh) && vectors(dx, 0) && vectors(dz, 0) &&
                    vectors(P.dgate, 0);
-  const BackShape b = back_shape(q->T, q->d, full, sms);
-  const cudaError_t e = bf16 ? run_backward<true>(P, vec, full, b, s) : run_backward<false>(P, vec, full, b, s);
+  int64_t groups;
+  cudaError_t e;
+  if (vec && q->d <= kRingWidth) {
+    RingParams R{};
+    const bool full = P.f.pre == SFNN_NORM_LAYER || P.f.post == SFNN_NORM_LAYER || P.f.bp || asked[kSumB] || asked[kSum0];
+    const RingShape shape = ring_shape(R, P.f, full, dr, lddr, dh, lddh, sms);
+    groups = shape.groups;
+    e = run_ring(bf16, P.f.x32 || P.f.z32, full, shape, P, R, err, s);
+  } else {
+    const bool full = asked[kSumB] || asked[kSum0];
+    const BackShape b = back_shape(q->T, q->d, full, sms);
+    groups = b.groups();
+    e = bf16 ? run_backward<true>(P, vec, full, b, s) : run_backward<false>(P, vec, full, b, s);
+  }
   if (e != cudaSuccess) return SFNN_ERR_CUDA;
   if (S.sums) {
     S.part = P.part;
-    S.groups = (int)b.groups();
+    S.groups = (int)groups;
     S.d = q->d;
-    const dim3 grid((unsigned)(((int64_t)S.sums * q->d + 31) / 32));
-    if ((bf16 ? launch_pdl(k_norm_sums<true>, grid, dim3(256), 0, s, S)
-              : launch_pdl(k_norm_sums<false>, grid, dim3(256), 0, s, S)) != cudaSuccess)
+    S.c = P.f.c;
+    S.gate = one_gate ? q->gate : nullptr;
+    S.wp = q->post_w, S.bp = q->post_b;
+    const dim3 grid((unsigned)((q->d + 31) / 32)), block(kSumWarps * 32);
+    if ((bf16 ? launch_pdl(k_norm_sums<true>, grid, block, 0, s, S) : launch_pdl(k_norm_sums<false>, grid, block, 0, s, S)) !=
+        cudaSuccess)
       return SFNN_ERR_CUDA;
   }
   return SFNN_OK;

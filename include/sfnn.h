@@ -617,7 +617,7 @@ SFNN_API sfnn_status sfnn_linear_backward(const sfnn_linear_desc *q, const void 
  * b and gate are fp16 or bf16 (dtype), X and Z of that type or fp32, R and dR, dX of X's type, dZ of
  * Z's.  Sums and norms are fp32; H is formed from R before its rounding.
  * d up to 32768, any row stride of at least d, T up to 2^28; T = 0 is valid.  Rows that all start on 16
- * bytes with d a multiple of 8 are read by vectors.  R may be X (the same rows), else nothing that is
+ * bytes with d a multiple of 8 are read by vectors.  err as for sfnn_gated_forward.  R may be X (the same rows), else nothing that is
  * written may overlap anything else.
  */
 typedef enum { SFNN_NORM_NONE = 0, SFNN_NORM_RMS = 1, SFNN_NORM_LAYER = 2 } sfnn_norm;
@@ -638,7 +638,7 @@ typedef struct {
 
 /* stats (may be NULL) [T x 4], 16-byte aligned: what the backward pass needs besides the inputs. */
 SFNN_API sfnn_status sfnn_norm_forward(const sfnn_norm_desc *q, void *r, int64_t ldr, void *h, int64_t ldh, float *stats,
-                                       sfnn_stream_t stream);
+                                       int32_t *err, sfnn_stream_t stream);
 /* The gradients from dR [T x d] and dH [T x d] (either may be NULL: zeros), contiguous; a NULL one is
  * not computed.  dgate: [d] for one row of gates, else [T x d].  Sums over the tokens are fp32, in an
  * order that the sizes and the device alone decide.  ws: sfnn_norm_workspace bytes, 16-byte aligned,
@@ -646,7 +646,8 @@ SFNN_API sfnn_status sfnn_norm_forward(const sfnn_norm_desc *q, void *r, int64_t
 SFNN_API int64_t sfnn_norm_workspace(int32_t T, int32_t d);
 SFNN_API sfnn_status sfnn_norm_backward(const sfnn_norm_desc *q, const float *stats, const void *dr, int64_t lddr,
                                         const void *dh, int64_t lddh, void *dx, void *dz, void *dgate, void *dw, void *db,
-                                        void *dpost_w, void *dpost_b, void *ws, int64_t ws_bytes, sfnn_stream_t stream);
+                                        void *dpost_w, void *dpost_b, void *ws, int64_t ws_bytes, int32_t *err,
+                                        sfnn_stream_t stream);
 
 /*
  * The norm of all gradients together, and their clipping:

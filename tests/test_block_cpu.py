@@ -33,27 +33,28 @@ NORM_REFUSALS = [
 def test_norms_refuse_bad_descriptors(kw, want):
     lib = sf.load_library()
     q = norm(**kw)
-    assert lib.sfnn_norm_forward(ctypes.byref(q), 4096, 64, 4096, 64, None, None) == want
+    assert lib.sfnn_norm_forward(ctypes.byref(q), 4096, 64, 4096, 64, None, 4096, None) == want
     assert lib.sfnn_norm_backward(ctypes.byref(q), 4096, 4096, 64, None, 64, 4096, None, None, None, None, None, None,
-                                  4096, 1 << 40, None) == want
+                                  4096, 1 << 40, 4096, None) == want
 
 
 def test_norms_refuse_bad_buffers():
     lib = sf.load_library()
 
-    def forward(q, r=4096, ldr=64, h=4096, ldh=64, stats=None):
-        return lib.sfnn_norm_forward(ctypes.byref(q), r, ldr, h, ldh, stats, None)
-    assert lib.sfnn_norm_forward(None, 4096, 64, 4096, 64, None, None) == INVALID
-    for kw in (dict(r=None), dict(ldr=63), dict(r=4097), dict(h=None), dict(ldh=60), dict(stats=4100)):
+    def forward(q, r=4096, ldr=64, h=4096, ldh=64, stats=None, err=4096):
+        return lib.sfnn_norm_forward(ctypes.byref(q), r, ldr, h, ldh, stats, err, None)
+    assert lib.sfnn_norm_forward(None, 4096, 64, 4096, 64, None, 4096, None) == INVALID
+    for kw in (dict(r=None), dict(ldr=63), dict(r=4097), dict(h=None), dict(ldh=60), dict(stats=4100), dict(err=None),
+               dict(err=4098)):
         assert forward(norm(), **kw) == INVALID, kw
     assert forward(norm(T=0), r=None, h=None) == 0
 
     def backward(q, stats=4096, dr=4096, lddr=64, dh=4096, lddh=64, dx=4096, dz=4096, dgate=None, dw=4096, db=None, dpw=None,
-                 dpb=None, ws=4096, nbytes=1 << 40):
+                 dpb=None, ws=4096, nbytes=1 << 40, err=4096):
         return lib.sfnn_norm_backward(None if q is None else ctypes.byref(q), stats, dr, lddr, dh, lddh, dx, dz, dgate, dw,
-                                      db, dpw, dpb, ws, nbytes, None)
+                                      db, dpw, dpb, ws, nbytes, err, None)
     assert backward(None) == INVALID
-    for kw in (dict(stats=None), dict(stats=4104), dict(lddr=63), dict(dr=4097), dict(dh=4097), dict(lddh=8), dict(dx=4097),
+    for kw in (dict(stats=None), dict(stats=4104), dict(err=None), dict(lddr=63), dict(dr=4097), dict(dh=4097), dict(lddh=8), dict(dx=4097),
                dict(dz=4097), dict(dgate=4096), dict(dw=4097), dict(dpw=4096), dict(dpb=4096), dict(ws=None),
                dict(ws=4104), dict(nbytes=8)):
         status = backward(norm(), **kw)
