@@ -9,6 +9,7 @@ functions with ``_forward`` and ``_backward`` are their passes as plain calls.
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -56,8 +57,9 @@ def _linear_desc(x, w, b, act, y_dtype):
         raise ValueError(f"w must be [N, K] with K a positive multiple of 8, got {tuple(w.shape)}")
     if y_dtype != dt and y_dtype != torch.float32:
         raise TypeError(f"the output is {dt} or fp32, not {y_dtype}")
-    pb = _channels(b, "b", N, dt)
-    _same_device(x.get_device(), w, b)
+    index = x.get_device()
+    pb = _channels(b, "b", N, dt, index)
+    _same_device(index, w)
     return _LinearDesc(T, K, N, code, F32 if y_dtype == torch.float32 else code, act, px, ldx, pw, ldw, pb), N
 
 
@@ -100,7 +102,7 @@ def linear_forward(x, w, b=None, act=None, residual=None, out_dtype=None, save=F
             slopes = x.new_empty(lib.sfnn_linear_slope_bytes(q.T, N, kind), dtype=torch.uint8)
         if q.T:
             nbytes = lib.sfnn_linear_workspace(q.T, q.K, N, 0)
-            ws = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+            ws = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=x.device) if nbytes else None
             _check(lib.sfnn_linear_forward(ctypes.byref(q), pr, ldr, py, ldy, _vp(slopes), _vp(ws), nbytes,
                                            _err_ptr(index), _raw_stream(index)), "sfnn_linear_forward")
     return out, LinearSaved(x, slopes, kind, N, dt, b is not None) if save else None
@@ -122,12 +124,11 @@ def linear_backward(dy, saved: LinearSaved, w, need=(True, True, True), stream=N
         raise ValueError("dy: rows must not overlap")
     lib = load_library()
     with _on(index, stream):
-        new = x.new_empty
-        dx = new(x.shape) if need[0] else None
-        dw = new(w.shape) if need[1] else None
-        db = new(N) if need[2] and saved.has_b else None
+        dx = _like(x) if need[0] else None
+        dw = _like(w) if need[1] else None
+        db = x.new_empty(N) if need[2] and saved.has_b else None
         nbytes = lib.sfnn_linear_workspace(q.T, q.K, N, 1)
-        ws = new(max(16, nbytes), dtype=torch.uint8)
+        ws = torch.empty_strided((max(16, nbytes),), (1,), dtype=torch.uint8, device=x.device)
         _check(lib.sfnn_linear_backward(ctypes.byref(q), _vp(saved.slopes), pdy, lddy, _vp(dx), _vp(dw), _vp(db),
                                         ws.data_ptr(), nbytes, _err_ptr(index), _raw_stream(index)),
                "sfnn_linear_backward")
@@ -180,6 +181,11 @@ class NormSaved:
         self.tensors, self.stats, self.options, self.dtype = tensors, stats, options, dtype
 
 
+def _like(t, dtype=None):
+    """An uninitialised contiguous tensor of t's shape, in its type or another."""
+    return torch.empty_like(t, dtype=dtype) if t.is_contiguous() else t.new_empty(t.shape, dtype=dtype)
+
+
 def _value_rows(t, name, d, dtype, like=None):
     """(pointer, rows, row stride, type code) of values [..., d] of ``dtype`` (None: no matter) or fp32."""
     p, r, c, ld = _rows(t, name, d)
@@ -190,18 +196,19 @@ def _value_rows(t, name, d, dtype, like=None):
         code = _CODES.get(dt)
         if code is None or (dtype is not None and dt != dtype):
             raise TypeError(f"{name} must be a tensor of fp32 or {dtype or 'fp16 or bf16'}, got {dt}")
-    if r and ld < c:
+    if ld < c and r:
         raise ValueError(f"{name}: rows must not overlap")
     if like is not None and t.shape != like.shape:
         raise ValueError(f"{name} must have the shape {tuple(like.shape)}, got {tuple(t.shape)}")
     return p, r, ld, code
 
 
-def _channels(t, name, d, dtype):
+def _channels(t, name, d, dtype, index):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.shape != (d,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {d} elements")
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != (d,) or not t.is_contiguous() \
+            or t.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {d} elements on the others' device")
     return t.data_ptr()
 
 
@@ -225,7 +232,7 @@ def _norm_desc(tensors, options, dtype):
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError(f"the norms give fp16 or bf16, not {dtype}")
-    d = x.shape[-1]
+    d, index = x.shape[-1], x.get_device()
     px, T, ldx, xc = _value_rows(x, "x", d, dtype)
     pz, ldz, zc = None, 0, xc
     if z is not None:
@@ -235,7 +242,7 @@ def _norm_desc(tensors, options, dtype):
     pg, ldg = None, 0
     if gate is not None:
         if isinstance(gate, torch.Tensor) and gate.dim() == 1:
-            pg = _channels(gate, "gate", d, dtype)
+            pg = _channels(gate, "gate", d, dtype, index)
         else:
             if not isinstance(gate, torch.Tensor) or gate.dtype != dtype:
                 raise TypeError(f"gate must be a CUDA tensor of {dtype}")
@@ -244,13 +251,10 @@ def _norm_desc(tensors, options, dtype):
         raise ValueError("weights are given for a norm that is not there")
     if not 1 <= d <= 32768:
         raise ValueError(f"the norms take rows of 1 to 32768 values, got {d}")
-    index = x.get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError("all tensors must be on one device")
+    _same_device(index, z, gate)
     return _NormDesc(T, d, code, xc, zc, pre, post, eps, residual_scale, branch_scale, px, ldx, pz, ldz, pg, ldg,
-                     _channels(w, "w", d, dtype), _channels(b, "b", d, dtype), _channels(post_w, "post_w", d, dtype),
-                     _channels(post_b, "post_b", d, dtype)), dtype
+                     _channels(w, "w", d, dtype, index), _channels(b, "b", d, dtype, index),
+                     _channels(post_w, "post_w", d, dtype, index), _channels(post_b, "post_b", d, dtype, index)), dtype
 
 
 def _norm_options(pre, post, residual_scale, branch_scale, eps):
@@ -285,9 +289,9 @@ def residual_norm_forward(x, z=None, pre="rms", w=None, b=None, post="none", pos
     with _on(index, stream):
         r = x if z is None else out
         if r is None:
-            r = x.new_empty(x.shape)
+            r = _like(x)
             pr, ldr = r.data_ptr(), q.d
-        h = x.new_empty(x.shape, dtype=dt) if q.pre else None
+        h = _like(x, dt) if q.pre else None
         stats = x.new_empty((q.T, 4), dtype=torch.float32) if save else None
         _check(load_library().sfnn_norm_forward(ctypes.byref(q), pr, ldr, _vp(h), q.d, _vp(stats), _err_ptr(index),
                                                 _raw_stream(index)), "sfnn_norm_forward")
@@ -316,14 +320,10 @@ def residual_norm_backward(dr, dh, saved: NormSaved, need=(True,) * 7, stream=No
             raise ValueError("all tensors must be on one device")
     lib = load_library()
     with _on(index, stream):
-        new = x.new_empty
-        dx = new(x.shape) if need[0] else None
-        dz = new(z.shape, dtype=z.dtype) if need[1] and z is not None else None
-        dgate = new(gate.shape, dtype=dt) if need[2] and gate is not None else None
-        dw, db, dpw, dpb = (new(d, dtype=dt) if n and t is not None else None
-                            for n, t in zip(need[3:], (w, b, post_w, post_b)))
+        dx, dz, dgate, dw, db, dpw, dpb = [_like(t) if n and t is not None else None
+                                           for n, t in zip(need, saved.tensors)]
         nbytes = lib.sfnn_norm_workspace(T, d)
-        ws = new(max(nbytes, 16), dtype=torch.uint8)
+        ws = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=x.device)
         _check(lib.sfnn_norm_backward(ctypes.byref(q), _vp(saved.stats), pdr, lddr, pdh, lddh, _vp(dx), _vp(dz),
                                       _vp(dgate), _vp(dw), _vp(db), _vp(dpw), _vp(dpb), ws.data_ptr(), nbytes,
                                       _err_ptr(index), _raw_stream(index)), "sfnn_norm_backward")
@@ -383,6 +383,38 @@ def _dense(t) -> bool:
     return True
 
 
+def _grad_table(grads, outs, n):
+    """The entries of sfnn_grad, four words a tensor; None if something is not a CUDA tensor."""
+    T = torch.Tensor
+    if not all(map(T.is_cuda.__get__, grads)) or len(set(map(T.get_device, grads))) != 1:
+        return None
+    dtypes = list(map(T.dtype.__get__, grads))
+    codes = list(map(_GRAD_CODES.get, dtypes))
+    if None in codes:
+        bad = dtypes[codes.index(None)]
+        raise TypeError(f"gradients are fp16, bf16 or fp32, got {bad}")
+    in_order = list(map(T.is_contiguous, grads))
+    sizes = list(map(T.numel, grads))
+    if not all(in_order) and not all(c or _dense(g) for c, g in zip(in_order, grads)):
+        raise ValueError("a gradient's values must lie without gaps")
+    table = array("q", bytes(32 * n))
+    ptrs = array("q", map(T.data_ptr, grads))
+    table[0::4] = table[1::4] = ptrs
+    table[2::4] = array("q", sizes)
+    table[3::4] = array("q", codes)
+    if outs is not grads:
+        if list(map(T.get_device, outs)) != [grads[0].get_device()] * n:
+            return None
+        same = list(map(T.dtype.__get__, outs)) == dtypes and list(map(T.numel, outs)) == sizes
+        if same and not (all(in_order) and all(map(T.is_contiguous, outs))):
+            same = all(o.shape == g.shape and (o.stride() == g.stride() or c and o.is_contiguous())
+                       for g, o, c in zip(grads, outs, in_order))
+        if not same:
+            raise ValueError("each output must have its gradient's type, size and order of values")
+        table[1::4] = array("q", map(T.data_ptr, outs))
+    return table
+
+
 def clip_grad_norm(grads, max_norm, scale=1.0, out=None, eps=1e-6, stream=None):
     """The norm of all ``grads`` together times ``scale``, as an fp32 tensor of no dimension; the
     gradients become g * scale * min(1, max_norm / (norm + eps)) in place, or in the tensors ``out``.
@@ -393,37 +425,27 @@ def clip_grad_norm(grads, max_norm, scale=1.0, out=None, eps=1e-6, stream=None):
     NaN): nothing waits for the device here."""
     grads = list(grads)
     outs = grads if out is None else list(out)
-    if not grads:
+    n = len(grads)
+    if not n:
         raise ValueError("there are no gradients")
-    if len(outs) != len(grads):
-        raise ValueError(f"{len(grads)} gradients, but {len(outs)} outputs")
+    if len(outs) != n:
+        raise ValueError(f"{n} gradients, but {len(outs)} outputs")
     if not (max_norm >= 0 and eps >= 0 and 0 <= scale < float("inf")):
         raise ValueError("max_norm, scale and eps must not be negative, nor scale infinite")
+    # whole lists at a time: a hundred tensors' checks one by one would take longer than the kernels
+    try:
+        table = _grad_table(grads, outs, n)
+    except (AttributeError, TypeError):
+        table = None
+    if table is None:  # which one it is
+        raise TypeError("grads and out must be dense CUDA tensors of fp16, bf16 or fp32 on one device")
     first = grads[0]
-    if not isinstance(first, torch.Tensor) or not first.is_cuda:
-        raise TypeError("grads must be CUDA tensors")
     index = first.get_device()
-    table = []
-    for g, o in zip(grads, outs):
-        if not isinstance(g, torch.Tensor) or not isinstance(o, torch.Tensor) or g.layout != torch.strided:
-            raise TypeError("grads must be CUDA tensors")
-        code = _GRAD_CODES.get(g.dtype)
-        if code is None:
-            raise TypeError(f"gradients are fp16, bf16 or fp32, got {g.dtype}")
-        if g.get_device() != index or o.get_device() != index:
-            raise ValueError("all tensors must be on one device")
-        if not g.is_contiguous() and not _dense(g):
-            raise ValueError("a gradient's values must lie without gaps")
-        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or
-                           (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous()))):
-            raise ValueError("each output must have its gradient's type, shape and strides")
-        table += (g.data_ptr(), o.data_ptr(), g.numel(), code)
     lib = load_library()
-    n = len(grads)
     with _on(index, stream):
         norm = first.new_empty((), dtype=torch.float32)
         nbytes = lib.sfnn_clip_workspace(n)
         ws = first.new_empty(nbytes, dtype=torch.uint8)
-        _check(lib.sfnn_clip_grad_norm((ctypes.c_int64 * len(table))(*table), n, max_norm, scale, eps, norm.data_ptr(),
-                                       ws.data_ptr(), nbytes, _raw_stream(index)), "sfnn_clip_grad_norm")
+        _check(lib.sfnn_clip_grad_norm(table.buffer_info()[0], n, max_norm, scale, eps, norm.data_ptr(), ws.data_ptr(), nbytes,
+                                       _raw_stream(index)), "sfnn_clip_grad_norm")
     return norm

@@ -427,11 +427,12 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) k_norm_backward(const __gri
 
 // ---------------------------------------------------------------- rows through shared memory
 // The kernels above hold a row's values in registers, and while a row's sums go round nothing is
-// on its way from memory.  These keep the next rows coming: persistent CTAs, each with a ring of
-// stages that bulk copies fill while the row before is worked on; the values stay in shared memory
-// until each is needed, the channels' weights beside them.  16 values a thread (two vectors of 8),
-// a row to `threads` threads, `rows` rows a step.
+// on its way from memory.  These keep the next rows coming: a CTA an SM, its threads in groups that
+// each take a row at a time, with stages of their own that bulk copies fill while the rows before are
+// worked on; a group waits for nothing but its own rows and sums.  The values stay in shared memory
+// until each is needed, beside them the channels' weights.  A thread has 16 values (two vectors of 8).
 constexpr int kMaxStages = 4;
+constexpr int kMaxGroups = 16;  // 15 named barriers; 16 groups are warps, which need none
 constexpr int kRingValues = 16;
 enum { kOfX, kOfZ, kOfDr, kOfDh, kOfGate, kOfRows };
 
@@ -440,40 +441,47 @@ struct RingParams {
   int64_t ld[kOfRows];     // bytes
   int bytes[kOfRows];      // of a row
   int at[kOfRows];         // in a stage
-  int stage, stages;       // bytes of a stage
-  int rows, threads;
-  int held;  // the channels' weights lie in shared memory (else they are formed where they are used)
+  int stage, stages;       // bytes of a stage (a row of every array)
+  int groups, threads;     // of a CTA, of a group
+  int held[4];             // where the channels' weights lie behind the stages (-1: all the same, see weight())
 };
 // The channels' weights as the kernels use them, in 32 bits: c gate w_post (without the gate where every
 // token has its own), w, and for FULL c gate b_post and b.
 enum { kPostW, kPreW, kPostB, kPreB, kWeights };
 
-// Pairs of fp32 values: one instruction for both.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+// Pairs of fp32 values in a 64-bit register, one instruction for both.  (Kept as such from the load to
+// the store: taken apart in between, every instruction is joined by moves.)
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ float2 apart(Pair p) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+__device__ __forceinline__ float within(Pair p) {
+  const float2 v = apart(p);
+  return v.x + v.y;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 a, a, b;\n"
-      " mov.b64 {%0, %1}, a;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 a, a, b;\n"
-      " mov.b64 {%0, %1}, a;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -481,204 +489,256 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                : "memory");
 }
 
-template <bool bf16, bool WIDE, bool FULL>  // WIDE: X or Z is fp32; FULL: means and biases
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void lds_pairs(uint32_t a, Pair &x, Pair &y) {
+  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+struct RingSmem {  // beside the stages and the weights
+  uint64_t full[kMaxGroups * kMaxStages];
+  float slots[2][2][64];  // [turn][value][a group's warps, rounded up to 4]
+};
+
+// WIDE: X or Z is fp32.  FULL: means and biases.  EXACT: what is usual -- both vectors of every thread are
+// there (a width of whole 512s), X, Z, the pre norm and, backward, all gradients, no gate for each
+// token -- whose tests cost as much as the arithmetic (backward, 4096 wide: 727 instructions a warp and
+// row with them).
+template <bool bf16, bool WIDE, bool FULL, bool EXACT>
 struct Ring {
-  static constexpr int kHeld = FULL ? 4 : 2;
   const RingParams &R;
   const NormParams &F;
+  RingSmem &S;
   int32_t *err;
-  const unsigned char *smem;  // stages, then the weights
-  uint64_t *full;
-  int T, d;
-  int steps;                 // of this CTA
-  int slot, phase;           // of the step at hand
-  const unsigned char *cur;  // its stage
-  __device__ __forceinline__ Ring(const RingParams &R_, const NormParams &F_, unsigned char *smem_, uint64_t *full_,
-                                  int32_t *err_)
-      : R(R_), F(F_), err(err_), smem(smem_), full(full_), T(F_.T), d(F_.d), slot(-1), phase(1), cur(nullptr) {
-    const int units = (T + R.rows - 1) / R.rows;
-    steps = (units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // (the grid is no larger than units)
+  int mine, lane;        // the group, the thread's place in it
+  int row, step;         // the row at hand; from one to the next
+  int slot, phase, turn;
+  bool dead;             // a wait has run out
+  uint32_t cur, stage0;  // the stage at hand, the group's first
+  uint32_t weights, slots;
+
+  __device__ __forceinline__ Ring(const RingParams &R_, const NormParams &F_, unsigned char *smem, RingSmem &S_, int32_t *err_)
+      : R(R_), F(F_), S(S_), err(err_), slot(0), phase(0), turn(0), dead(false) {
+    mine = threadIdx.x / R.threads;
+    lane = threadIdx.x - mine * R.threads;
+    slots = smem_u32(S.slots) + (uint32_t)(mine * ((R.threads / 32 + 3) & ~3) * 4);
+    row = blockIdx.x * R.groups + mine;
+    step = gridDim.x * R.groups;
+    cur = stage0 = smem_u32(smem) + (uint32_t)(mine * R.stages * R.stage);
+    weights = smem_u32(smem) + (uint32_t)(R.groups * R.stages * R.stage);
+    for (int i = threadIdx.x; i < 4 * 64; i += blockDim.x) S.slots[i >> 7][(i >> 6) & 1][i & 63] = 0.f;
     if (threadIdx.x == 0) {
-      for (int s = 0; s < R.stages; ++s) bar_init(&full[s], 1);
+      for (int i = 0; i < R.groups * R.stages; ++i) bar_init(&S.full[i], 1);
       bar_init_fence();
       fence_async_shared();
     }
     __syncthreads();
-    if (threadIdx.x < 32)
-      for (int s = 0; s < R.stages; ++s) request(s, s);
-    if (R.held) {  // (the first arrival's barrier publishes them)
-      float *to = reinterpret_cast<float *>(smem_ + R.stages * R.stage);
-      for (int k = 0; k < kHeld; ++k)
-        for (int c = threadIdx.x * 8; c < d; c += blockDim.x * 8) {
-          float2 v[4];
-          form(k, c, v);
+    if (lane < 32)
+      for (int i = 0; i < R.stages; ++i) request(row + i * step, i);
+#pragma unroll 1
+    for (int k = 0; k < kWeights; ++k) {
+      const int at = k == 0 ? R.held[0] : k == 1 ? R.held[1] : k == 2 ? R.held[2] : R.held[3];
+      if (at < 0) continue;
+      ulonglong2 *to = reinterpret_cast<ulonglong2 *>(smem + (size_t)R.groups * R.stages * R.stage + at);
+      const void *p = k == kPostW ? F.wp : k == kPreW ? F.w : k == kPostB ? F.bp : F.b;
+      for (int c = threadIdx.x * 8; c < F.d; c += blockDim.x * 8) {
+        Pair v[4], g[4];
+        if (p)
+          widen8(ld_keep(static_cast<const uint16_t *>(p) + c), v);
+        else
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float4 *>(to + k * d + c + 4 * i) = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+          for (int j = 0; j < 4; ++j) v[j] = both(1.f);
+        if (k == kPostW || k == kPostB) {
+          if (F.gate && !F.ldg)
+            widen8(ld_keep(static_cast<const uint16_t *>(F.gate) + c), g);
+          else
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] = both(1.f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = mul2(mul2(g[j], both(F.c)), v[j]);
         }
-    }
-  }
-  __device__ __forceinline__ int64_t row0(int step) const { return (blockIdx.x + (int64_t)step * gridDim.x) * R.rows; }
-  __device__ __forceinline__ void request(int step, int s) const {  // warp 0
-    if (step >= steps) return;
-    const int lane = threadIdx.x & 31;
-    const int64_t first = row0(step);
-    const int live = (int)min((int64_t)R.rows, T - first);
-    uint32_t row_bytes = 0;
-    for (int k = 0; k < kOfRows; ++k) row_bytes += R.p[k] ? R.bytes[k] : 0;
-    if (lane == 0) bar_expect_tx(&full[s], row_bytes * (uint32_t)live);
-    __syncwarp();
-    for (int k = 0; k < kOfRows; ++k) {
-      if (!R.p[k]) continue;
-      for (int r = lane; r < live; r += 32)
-        bulk_load(smem_u32(smem) + (uint32_t)(s * R.stage + R.at[k] + r * R.bytes[k]),
-                  static_cast<const unsigned char *>(R.p[k]) + (first + r) * R.ld[k], (uint32_t)R.bytes[k], &full[s]);
-    }
-    __syncwarp();
-  }
-  // The whole CTA: the step's rows are there, and those of the step before are done with (their
-  // stage is filled again).
-  __device__ __forceinline__ bool arrive(int step) {
-    const int before = slot;
-    if (++slot == R.stages) slot = 0;
-    if (slot == 0) phase ^= 1;
-    cur = smem + slot * R.stage;
-    if (R.stages == 1 && step > 0) {
-      __syncthreads();
-      if (threadIdx.x < 32) request(step, 0);
-    }
-    if (!__syncthreads_and(bar_wait(&full[slot], (uint32_t)phase))) {
-      if (threadIdx.x == 0) latch_error(err, kErrTimeout);
-      abandon(step);
-      return false;
-    }
-    if (R.stages > 1 && step > 0 && threadIdx.x < 32) request(step - 1 + R.stages, before);
-    return true;
-  }
-  // After a wait that ran out: this CTA's copies land before it ends (again with a limit).
-  __device__ __forceinline__ void abandon(int step) {
-    if (threadIdx.x == 0)
-      for (int i = 0; i < max(1, R.stages - 1) && step + i < steps; ++i) {
-        if (!bar_wait(&full[slot], (uint32_t)phase)) break;
-        if (++slot == R.stages) slot = 0, phase ^= 1;
+        to[c / 4] = make_ulonglong2(v[0], v[1]);
+        to[c / 4 + 1] = make_ulonglong2(v[2], v[3]);
       }
+    }
     __syncthreads();
   }
+  __device__ __forceinline__ void request(int r, int s) const {  // the group's first warp, an array a lane
+    if (r >= F.T) return;
+    uint64_t *bar = &S.full[mine * R.stages + s];
+    if (lane == 0) bar_expect_tx(bar, (uint32_t)R.stage);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kOfRows; ++k)
+      if (lane == k && R.p[k])
+        bulk_load(stage0 + (uint32_t)(s * R.stage + R.at[k]), static_cast<const unsigned char *>(R.p[k]) + r * R.ld[k],
+                  (uint32_t)R.bytes[k], bar);
+    __syncwarp();
+  }
+  // The row at hand is there.  A wait that runs out is latched, and the kernel goes on with what it
+  // has: only its last waits, for the copies that must have landed before it ends, then take their time.
+  __device__ __forceinline__ void wait() {
+    uint64_t *bar = &S.full[mine * R.stages + slot];
+    const bool ok = dead && row + R.stages * step < F.T ? bar_try(bar, (uint32_t)phase) : bar_wait(bar, (uint32_t)phase);
+    if (!ok) {
+      if (!dead) latch_error(err, kErrTimeout);
+      dead = true;
+    }
+  }
+  __device__ __forceinline__ void barrier() const {  // the group's threads
+    if (R.threads == 32)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(mine + 1), "r"(R.threads) : "memory");
+  }
+  // The group is done with the row's stage (a barrier lies behind its last use): on to the next.
+  __device__ __forceinline__ void release() const {
+    if (lane < 32) request(row + R.stages * step, slot);
+  }
+  __device__ __forceinline__ void next() {
+    row += step;
+    cur += (uint32_t)R.stage;
+    if (++slot == R.stages) slot = 0, phase ^= 1, cur = stage0;
+  }
+  // Sums over the row; buffers alternate, so one barrier a sum is enough.
+  template <int N>
+  __device__ __forceinline__ void sum(float (&v)[N]) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    if (R.threads == 32) return;
+    const uint32_t at = slots + (uint32_t)turn * 512u;
+    turn ^= 1;
+    if ((lane & 31) == 0)
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + n * 256u + (uint32_t)(lane >> 5) * 4u), "f"(v[n]) : "memory");
+    barrier();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float4 t = lds_f4(at + n * 256u);
+      v[n] = (t.x + t.y) + (t.z + t.w);
+      for (int i = 4; i * 32 < R.threads; i += 4) {
+        t = lds_f4(at + n * 256u + i * 4);
+        v[n] += (t.x + t.y) + (t.z + t.w);
+      }
+    }
+  }
+
   // 8 values of the row at hand, of an array, from column c on
-  __device__ __forceinline__ void row(int r, int k, int c, bool wide, float2 v[4]) const {
-    const unsigned char *p = cur + R.at[k] + r * R.bytes[k];
+  __device__ __forceinline__ void value8(int k, int c, bool wide, Pair v[4]) const {
     if (WIDE && wide) {
-      const float4 *q = reinterpret_cast<const float4 *>(p + c * 4);
-      const float4 a = q[0], b = q[1];
-      v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+      const uint32_t p = cur + (uint32_t)(R.at[k] + c * 4);
+      lds_pairs(p, v[0], v[1]);
+      lds_pairs(p + 16, v[2], v[3]);
     } else {
-      widen8(*reinterpret_cast<const uint4 *>(p + c * 2), v);
+      widen8(lds_u4(cur + (uint32_t)(R.at[k] + c * 2)), v);
     }
   }
   // 8 weights, as the enumeration above says
-  __device__ __forceinline__ void weight(int k, int c, float2 v[4]) const {
-    if (R.held) {
-      const float4 *q = reinterpret_cast<const float4 *>(smem + R.stages * R.stage + (k * d + c) * 4);
-      const float4 a = q[0], b = q[1];
-      v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
-    } else {
-      form(k, c, v);
-    }
-  }
-  __device__ __forceinline__ void form(int k, int c, float2 v[4]) const {
-    const void *p = k == kPostW ? F.wp : k == kPreW ? F.w : k == kPostB ? F.bp : F.b;
-    if (p)
-      widen8(ld_keep(static_cast<const uint16_t *>(p) + c), v);
-    else
+  __device__ __forceinline__ void weight(int k, int c, Pair v[4]) const {
+    if (!(EXACT && (k == kPostW || k == kPreW)) && R.held[k] < 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = both(k == kPostW || k == kPreW ? 1.f : 0.f);
-    if (k == kPreW || k == kPreB) return;
-    float2 g[4];
-    if (F.gate && !F.ldg)
-      widen8(ld_keep(static_cast<const uint16_t *>(F.gate) + c), g);
-    else
-#pragma unroll
-      for (int i = 0; i < 4; ++i) g[i] = both(1.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = mul2(mul2(g[i], both(F.c)), v[i]);
-  }
-  static __device__ __forceinline__ void widen8(const uint4 &w, float2 v[4]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = bf16 ? make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u)) : unpack16(u[i], false);
-  }
-  static __device__ __forceinline__ void store(void *p, int64_t at, bool wide, const float2 v[4]) {
-    if (WIDE && wide) {
-      float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
-      q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-      q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-    } else {
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = make_uint4(
-          pack16(v[0].x, v[0].y, bf16), pack16(v[1].x, v[1].y, bf16), pack16(v[2].x, v[2].y, bf16), pack16(v[3].x, v[3].y, bf16));
-    }
-  }
-  // Z^ and R of 8 columns (Z^ untouched without Z).
-  __device__ __forceinline__ void residual(int r, int c, float mz, float sz, float2 zhat[4], float2 v[4]) const {
-    row(r, kOfX, c, F.x32, v);
-    if (!F.z) return;
-    float2 w[4];
-    row(r, kOfZ, c, F.z32, zhat);
-    weight(kPostW, c, w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (FULL) zhat[i] = add2(zhat[i], both(-mz));
-      zhat[i] = mul2(zhat[i], both(sz));
-      v[i] = mul2(v[i], both(F.a));
-    }
-    if (!FULL && !R.p[kOfGate]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = fma2(zhat[i], w[i], v[i]);
+      for (int i = 0; i < 4; ++i) v[i] = both(k == kPostW ? F.c : k == kPreW ? 1.f : 0.f);
       return;
     }
-    float2 b[4], g[4];
-    if (FULL) weight(kPostB, c, b);
-    if (R.p[kOfGate]) row(r, kOfGate, c, false, g);
+    const uint32_t p = weights + (uint32_t)(R.held[k] + c * 4);
+    lds_pairs(p, v[0], v[1]);
+    lds_pairs(p + 16, v[2], v[3]);
+  }
+  static __device__ __forceinline__ void widen8(const uint4 &w, Pair v[4]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      b[i] = fma2(zhat[i], w[i], FULL ? b[i] : both(0.f));
-      v[i] = R.p[kOfGate] ? fma2(b[i], g[i], v[i]) : add2(b[i], v[i]);
+      const float2 f = bf16 ? make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u)) : unpack16(u[i], false);
+      v[i] = pair(f.x, f.y);
     }
+  }
+  static __device__ __forceinline__ void store(void *p, int64_t at, bool wide, const Pair v[4]) {
+    if (WIDE && wide) {
+      ulonglong2 *q = reinterpret_cast<ulonglong2 *>(static_cast<float *>(p) + at);
+      q[0] = make_ulonglong2(v[0], v[1]);
+      q[1] = make_ulonglong2(v[2], v[3]);
+    } else {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = apart(v[i]);
+        u[i] = pack16(f.x, f.y, bf16);
+      }
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  }
+  __device__ __forceinline__ bool gated() const { return !EXACT && R.p[kOfGate]; }  // a gate for each token
+  // (Z - mean) and post(Z) gate c of 8 columns.
+  __device__ __forceinline__ void branch(int c, float mz, float sz, Pair z[4], Pair v[4]) const {
+    value8(kOfZ, c, F.z32, z);
+    weight(kPostW, c, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (FULL) z[i] = add2(z[i], both(-mz));
+      v[i] = mul2(z[i], v[i]);
+    }
+    if (!FULL && !gated()) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(sz));
+      return;
+    }
+    Pair b[4];
+    if (FULL)
+      weight(kPostB, c, b);
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = both(0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fma2(v[i], both(sz), b[i]);
+    if (!gated()) return;
+    value8(kOfGate, c, false, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], b[i]);
   }
 };
 
-template <bool bf16, bool WIDE, bool FULL>
-__global__ void __launch_bounds__(512, 2) k_norm_forward_ring(const __grid_constant__ NormParams P,
-                                                              const __grid_constant__ RingParams R, int32_t *err) {
+constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
+
+template <bool bf16, bool WIDE, bool FULL, bool EXACT>
+__global__ void __launch_bounds__(kForwardThreads, 1) k_norm_forward_ring(const __grid_constant__ NormParams P,
+                                                                          const __grid_constant__ RingParams R, int32_t *err) {
   extern __shared__ __align__(128) unsigned char ring_smem[];
-  __shared__ __align__(8) uint64_t full[kMaxStages];
-  __shared__ float2 slots[2 * kMaxWarps];
+  __shared__ RingSmem more;
   pdl_wait();
   pdl_launch_dependents();
-  Ring<bf16, WIDE, FULL> ring(R, P, ring_smem, full, err);
-  const int threads = R.threads, lane = threadIdx.x % threads, mine = threadIdx.x / threads;
-  RowSum<false> sum{slots, threads / 32, 1, 0, 0};
-  auto mean_of = [&](float2 v) {
-    float t[1] = {v.x + v.y};
-    sum(t);
+  Ring<bf16, WIDE, FULL, EXACT> ring(R, P, ring_smem, more, err);
+  const int c0 = ring.lane * 8, c1 = c0 + R.threads * 8;
+  const bool in[2] = {EXACT || c0 < P.d, EXACT || c1 < P.d}, has_z = EXACT || P.z, has_pre = EXACT || P.pre != SFNN_NORM_NONE;
+  auto mean_of = [&](Pair v) {
+    float t[1] = {within(v)};
+    ring.sum(t);
     return t[0] * P.inv_d;
   };
-  for (int step = 0; step < ring.steps; ++step) {
-    if (!ring.arrive(step)) return;
-    const int64_t row = ring.row0(step) + mine;
-    const bool live = row < P.T;
+  for (; ring.row < P.T; ring.next()) {
+    ring.wait();
     float mz = 0.f, sz = 1.f, mr = 0.f, sr = 1.f;
     if (P.post != SFNN_NORM_NONE) {
 #pragma unroll
       for (int pass = FULL ? 0 : 1; pass < 2; ++pass) {  // mean, then deviation
         if (FULL && pass == 0 && P.post != SFNN_NORM_LAYER) continue;
-        float2 q = both(0.f);
+        Pair q = both(0.f);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int c = (lane + k * threads) * 8;
-          if (!live || c >= P.d) continue;
-          float2 z[4];
-          ring.row(mine, kOfZ, c, P.z32, z);
+          if (!in[k]) continue;
+          Pair z[4];
+          ring.value8(kOfZ, k ? c1 : c0, P.z32, z);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (FULL && pass) z[i] = add2(z[i], both(-mz));
@@ -692,21 +752,28 @@ __global__ void __launch_bounds__(512, 2) k_norm_forward_ring(const __grid_const
           mz = m;
       }
     }
-    float2 r[8], q = both(0.f);
+    Pair r[8], q = both(0.f);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int c = (lane + k * threads) * 8;
-      float2 *rk = r + 4 * k, z[4];
+      const int c = k ? c1 : c0;
+      Pair *rk = r + 4 * k, z[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) rk[i] = both(0.f);
-      if (!live || c >= P.d) continue;
-      ring.residual(mine, c, mz, sz, z, rk);
-      if (P.z) ring.store(P.r, row * P.ldr + c, P.x32, rk);
+      if (!in[k]) continue;
+      ring.value8(kOfX, c, P.x32, rk);
+      if (has_z) {
+        Pair v[4];
+        ring.branch(c, mz, sz, z, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rk[i] = fma2(rk[i], both(P.a), v[i]);
+      }
+      if (has_z) ring.store(P.r, (int64_t)ring.row * P.ldr + c, P.x32, rk);
       if (!FULL)
 #pragma unroll
         for (int i = 0; i < 4; ++i) q = fma2(rk[i], rk[i], q);
     }
-    if (P.pre != SFNN_NORM_NONE) {
+    if (!has_pre || R.threads == 32) ring.barrier();
+    if (has_pre) {
       if (FULL) {
         if (P.pre == SFNN_NORM_LAYER) {
 #pragma unroll
@@ -716,7 +783,7 @@ __global__ void __launch_bounds__(512, 2) k_norm_forward_ring(const __grid_const
         q = both(0.f);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          if ((lane + k * threads) * 8 < P.d)
+          if (in[k])
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               r[4 * k + i] = add2(r[4 * k + i], both(-mr));
@@ -724,167 +791,193 @@ __global__ void __launch_bounds__(512, 2) k_norm_forward_ring(const __grid_const
             }
       }
       sr = rsqrtf(mean_of(q) + P.eps);
+    }
+    ring.release();
+    if (has_pre) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int c = (lane + k * threads) * 8;
-        if (!live || c >= P.d) continue;
-        float2 w[4], b[4];
+        const int c = k ? c1 : c0;
+        if (!in[k]) continue;
+        Pair w[4], b[4];
         ring.weight(kPreW, c, w);
         if (FULL) ring.weight(kPreB, c, b);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 hat = mul2(r[4 * k + i], both(sr));
+          const Pair hat = mul2(r[4 * k + i], both(sr));
           w[i] = FULL ? fma2(hat, w[i], b[i]) : mul2(hat, w[i]);
         }
-        ring.store(P.h, row * P.ldh + c, false, w);
+        ring.store(P.h, (int64_t)ring.row * P.ldh + c, false, w);
       }
     }
-    if (P.stats && live && lane == 0) *reinterpret_cast<float4 *>(P.stats + row * 4) = make_float4(mr, sr, mz, sz);
+    if (P.stats && ring.lane == 0) *reinterpret_cast<float4 *>(P.stats + (int64_t)ring.row * 4) = make_float4(mr, sr, mz, sz);
   }
 }
 
-template <bool bf16, bool WIDE, bool FULL>  // FULL: the sums of dH and D as well
-__global__ void __launch_bounds__(512, 1) k_norm_backward_ring(const __grid_constant__ NormBackParams P,
-                                                               const __grid_constant__ RingParams R) {
+template <bool bf16, bool WIDE, bool FULL, bool EXACT>  // FULL: the sums of dH and D as well
+__global__ void __launch_bounds__(kBackwardThreads, 1) k_norm_backward_ring(const __grid_constant__ NormBackParams P,
+                                                                            const __grid_constant__ RingParams R) {
   extern __shared__ __align__(128) unsigned char ring_smem[];
-  __shared__ __align__(8) uint64_t full[kMaxStages];
-  __shared__ float2 slots[2 * kMaxWarps];
+  __shared__ RingSmem more;
   pdl_wait();
   pdl_launch_dependents();
   const NormParams &F = P.f;
-  Ring<bf16, WIDE, FULL> ring(R, F, ring_smem, full, P.err);
-  const int threads = R.threads, lane = threadIdx.x % threads, mine = threadIdx.x / threads;
-  RowSum<false> sum{slots, threads / 32, 1, 0, 0};
-  float2 sw[8], sum1[8], sb[FULL ? 8 : 1], sum0[FULL ? 8 : 1];
+  Ring<bf16, WIDE, FULL, EXACT> ring(R, F, ring_smem, more, P.err);
+  const int c0 = ring.lane * 8, c1 = c0 + R.threads * 8;
+  const bool in[2] = {EXACT || c0 < F.d, EXACT || c1 < F.d};
+  const bool has_z = EXACT || F.z, has_dh = EXACT || P.dh, has_dr = EXACT || P.dr, has_dx = EXACT || P.dx;
+  Pair sw[8], sum1[8], sb[FULL ? 8 : 1], sum0[FULL ? 8 : 1];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     sw[i] = sum1[i] = both(0.f);
     if (FULL) sb[i] = sum0[i] = both(0.f);
   }
-  for (int step = 0; step < ring.steps; ++step) {
-    const int64_t row = ring.row0(step) + mine;
-    const bool live = row < F.T;
-    float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) st = __ldg(reinterpret_cast<const float4 *>(F.stats) + row);
-    if (!ring.arrive(step)) return;
-    float2 D[8], hat[8], zhat[8];
-    float2 s1 = both(0.f), s2 = both(0.f);
+  const bool has_dz = EXACT || P.dz, two_sums = has_dz && F.post != SFNN_NORM_NONE;
+  // (of columns past d these stay zero)
+  Pair D[8], hat[8], z[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) D[i] = hat[i] = z[i] = both(0.f);
+  for (; ring.row < F.T; ring.next()) {
+    const float4 st = __ldg(reinterpret_cast<const float4 *>(F.stats) + ring.row);  // of R, of Z: mean, 1 / deviation
+    ring.wait();
+    Pair s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int c = (lane + k * threads) * 8;
-      float2 *Dk = D + 4 * k, *hk = hat + 4 * k, *zk = zhat + 4 * k;
+      const int c = k ? c1 : c0;
+      Pair *Dk = D + 4 * k, *hk = hat + 4 * k, *zk = z + 4 * k;
+      if (!in[k]) continue;
+      if (has_dh) {
+        ring.value8(kOfX, c, F.x32, hk);
+        if (has_z) {  // R^ = a s X + s (c gate post(Z) - mean)
+          Pair v[4];
+          ring.branch(c, st.z, st.w * (FULL || ring.gated() ? 1.f : st.y), zk, v);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) Dk[i] = hk[i] = zk[i] = both(0.f);
-      if (!live || c >= F.d) continue;
-      ring.residual(mine, c, st.z, st.w, zk, hk);
-      if (!P.dh) continue;
-      float2 dh[4], w[4];
-      ring.row(mine, kOfDh, c, false, dh);
-      ring.weight(kPreW, c, w);
+          for (int i = 0; i < 4; ++i) {
+            if (FULL) v[i] = add2(v[i], both(-st.x));
+            if (FULL || ring.gated()) v[i] = mul2(v[i], both(st.y));
+            hk[i] = fma2(hk[i], both(F.a * st.y), v[i]);
+          }
+        } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (FULL) hk[i] = add2(hk[i], both(-st.x));
-        hk[i] = mul2(hk[i], both(st.y));
-        Dk[i] = mul2(dh[i], w[i]);
-        if (FULL) s1 = add2(s1, Dk[i]), sb[4 * k + i] = add2(sb[4 * k + i], dh[i]);
-        s2 = fma2(Dk[i], hk[i], s2);
-        sw[4 * k + i] = fma2(dh[i], hk[i], sw[4 * k + i]);
+          for (int i = 0; i < 4; ++i) hk[i] = mul2(FULL ? add2(hk[i], both(-st.x)) : hk[i], both(st.y));
+        }
+        Pair dh[4];
+        ring.value8(kOfDh, c, false, dh);
+        ring.weight(kPreW, c, Dk);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          Dk[i] = mul2(dh[i], Dk[i]);
+          if (FULL) s1 = add2(s1, Dk[i]), sb[4 * k + i] = add2(sb[4 * k + i], dh[i]);
+          s2 = fma2(Dk[i], hk[i], s2);
+          sw[4 * k + i] = fma2(dh[i], hk[i], sw[4 * k + i]);
+        }
+      } else if (has_z) {
+        ring.value8(kOfZ, c, F.z32, zk);
+        if (FULL)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) zk[i] = add2(zk[i], both(-st.z));
       }
     }
-    if (P.dh) {  // D: s (u - mean u - R^ mean(u R^)), dR is added below
-      float m1 = 0.f, m2;
+    float k1 = 0.f, k2 = 0.f;  // D = dR + s u - s mean u - s mean(u R^) R^
+    if (has_dh) {
       if (FULL) {
-        float t[2] = {s1.x + s1.y, s2.x + s2.y};
-        sum(t);
-        m1 = F.pre == SFNN_NORM_LAYER ? t[0] * F.inv_d : 0.f;
-        m2 = t[1] * F.inv_d;
+        float t[2] = {within(s1), within(s2)};
+        ring.sum(t);
+        k1 = F.pre == SFNN_NORM_LAYER ? -st.y * t[0] * F.inv_d : 0.f;
+        k2 = -st.y * t[1] * F.inv_d;
       } else {
-        float t[1] = {s2.x + s2.y};
-        sum(t);
-        m2 = t[0] * F.inv_d;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (FULL) D[j] = add2(D[j], both(-m1));
-        D[j] = mul2(both(st.y), fma2(hat[j], both(-m2), D[j]));
+        float t[1] = {within(s2)};
+        ring.sum(t);
+        k2 = -st.y * t[0] * F.inv_d;
       }
     }
-    float2 n1 = both(0.f), n2 = both(0.f);
+    Pair n1 = both(0.f), n2 = both(0.f);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int c = (lane + k * threads) * 8;
-      float2 *Dk = D + 4 * k, *zk = zhat + 4 * k;
-      if (!live || c >= F.d) continue;
-      float2 v[4];
-      if (P.dr) {
-        ring.row(mine, kOfDr, c, F.x32, v);
+      const int c = k ? c1 : c0;
+      Pair *Dk = D + 4 * k, *hk = hat + 4 * k, *zk = z + 4 * k;
+      if (!in[k]) continue;
+      Pair v[4];
+      if (has_dr)
+        ring.value8(kOfDr, c, F.x32, v);
+      else
 #pragma unroll
-        for (int i = 0; i < 4; ++i) Dk[i] = add2(Dk[i], v[i]);
+        for (int i = 0; i < 4; ++i) v[i] = both(0.f);
+      if (has_dh) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (FULL) v[i] = add2(v[i], both(k1));
+          Dk[i] = fma2(Dk[i], both(st.y), fma2(hk[i], both(k2), v[i]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Dk[i] = v[i];
       }
-      if (P.dx) {
+      if (has_dx) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = mul2(both(F.a), Dk[i]);
-        ring.store(P.dx, row * F.d + c, F.x32, v);
+        ring.store(P.dx, (int64_t)ring.row * F.d + c, F.x32, v);
       }
-      if (!F.z) continue;
-      float2 w[4];
+      if (!has_z) continue;
+      Pair w[4];
       ring.weight(kPostW, c, w);
-      if (R.p[kOfGate]) {
-        float2 g[4];
-        ring.row(mine, kOfGate, c, false, g);
+      if (ring.gated()) {
+        Pair g[4];
+        ring.value8(kOfGate, c, false, g);
         if (P.dgate) {
           if (FULL) ring.weight(kPostB, c, v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = mul2(Dk[i], fma2(zk[i], w[i], FULL ? v[i] : both(0.f)));
-          ring.store(P.dgate, row * F.d + c, false, v);
+          for (int i = 0; i < 4; ++i)
+            v[i] = mul2(Dk[i], fma2(mul2(zk[i], both(st.w)), w[i], FULL ? v[i] : both(0.f)));
+          ring.store(P.dgate, (int64_t)ring.row * F.d + c, false, v);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) Dk[i] = mul2(Dk[i], g[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) {  // D becomes s_z v
         if (FULL) sum0[4 * k + i] = add2(sum0[4 * k + i], Dk[i]);
+        Dk[i] = mul2(Dk[i], both(st.w));
         sum1[4 * k + i] = fma2(Dk[i], zk[i], sum1[4 * k + i]);
         Dk[i] = mul2(Dk[i], w[i]);
         if (FULL) n1 = add2(n1, Dk[i]);
         n2 = fma2(Dk[i], zk[i], n2);
       }
     }
-    if (!P.dz) continue;
-    float m1 = 0.f, m2 = 0.f;
-    if (F.post != SFNN_NORM_NONE) {
+    if (!two_sums || R.threads == 32) ring.barrier();
+    float m1 = 0.f, m2 = 0.f;  // dZ = s_z (v - mean v - Z^ mean(v Z^))
+    if (two_sums) {
       float t[FULL ? 2 : 1];
-      t[0] = n2.x + n2.y;
-      if (FULL) t[FULL ? 1 : 0] = n1.x + n1.y;
-      sum(t);
-      m2 = t[0] * F.inv_d;
-      if (FULL && F.post == SFNN_NORM_LAYER) m1 = t[FULL ? 1 : 0] * F.inv_d;
+      t[0] = within(n2);
+      if (FULL) t[FULL ? 1 : 0] = within(n1);
+      ring.sum(t);
+      m2 = -st.w * st.w * t[0] * F.inv_d;
+      if (FULL && F.post == SFNN_NORM_LAYER) m1 = -t[FULL ? 1 : 0] * F.inv_d;
     }
+    ring.release();
+    if (!has_dz) continue;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int c = (lane + k * threads) * 8;
-      if (!live || c >= F.d) continue;
-      float2 v[4];
+      const int c = k ? c1 : c0;
+      if (!in[k]) continue;
+      Pair v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = fma2(zhat[4 * k + i], both(-m2), D[4 * k + i]);
-        if (FULL) v[i] = add2(v[i], both(-m1));
-        v[i] = mul2(both(st.w), v[i]);
+        v[i] = fma2(z[4 * k + i], both(m2), D[4 * k + i]);
+        if (FULL) v[i] = add2(v[i], both(m1));
       }
-      ring.store(P.dz, row * F.d + c, F.z32, v);
+      ring.store(P.dz, (int64_t)ring.row * F.d + c, F.z32, v);
     }
   }
   if (!P.part) return;
-  float *part = P.part + ((int64_t)blockIdx.x * R.rows + mine) * P.sums * F.d;
-  auto put = [&](int at, const float2 *v) {
+  float *part = P.part + ((int64_t)blockIdx.x * R.groups + ring.mine) * P.sums * F.d;
+  auto put = [&](int at, const Pair *v) {
     if (at < 0) return;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int c = (lane + k * threads) * 8;
-      if (c >= F.d) continue;
-      float4 *q = reinterpret_cast<float4 *>(part + (int64_t)at * F.d + c);
-      q[0] = make_float4(v[4 * k].x, v[4 * k].y, v[4 * k + 1].x, v[4 * k + 1].y);
-      q[1] = make_float4(v[4 * k + 2].x, v[4 * k + 2].y, v[4 * k + 3].x, v[4 * k + 3].y);
+      if (!in[k]) continue;
+      ulonglong2 *q = reinterpret_cast<ulonglong2 *>(part + (int64_t)at * F.d + (k ? c1 : c0));
+      q[0] = make_ulonglong2(v[4 * k], v[4 * k + 1]);
+      q[1] = make_ulonglong2(v[4 * k + 2], v[4 * k + 3]);
     }
   };
   put(P.at[kSumW], sw);
@@ -1041,9 +1134,10 @@ BackShape back_shape(int64_t T, int d, bool full, int sms) {
   b.grid = (int)std::min(units, most) * b.ctas;
   return b;
 }
-int64_t ring_groups(int64_t T, int d, int sms) {  // at most, with two CTAs an SM
-  const int rows = std::max(1, 256 / (int)up((d + kRingValues - 1) / kRingValues, 32));
-  return std::min((T + rows - 1) / rows, (int64_t)2 * sms) * rows;
+int ring_threads(int d) { return (int)up((d + kRingValues - 1) / kRingValues, 32); }
+int64_t ring_groups(int64_t T, int d, int sms) {  // at most
+  const int groups = std::max(1, std::min(kMaxGroups, kBackwardThreads / ring_threads(d)));
+  return std::min((T + groups - 1) / groups, (int64_t)sms) * groups;
 }
 int64_t back_workspace(int64_t T, int d, int sums, int sms) {  // (the larger of the two kernels')
   T = std::max<int64_t>(T, 1);
@@ -1055,45 +1149,49 @@ cudaError_t run_backward(const NormBackParams &P, const BackShape &b, cudaStream
   return b.ctas == 1 ? launch_rows(k_norm_backward<bf16, V, FULL, false>, b.grid, b.block, 1, b.threads, P, s)
                      : launch_rows(k_norm_backward<bf16, V, FULL, true>, b.grid, b.block, b.ctas, b.threads, P, s);
 }
-// The rows' way through shared memory: (ctas per SM, shared memory of a CTA) in R and the return values.
+// The rows' way through shared memory.
+constexpr int kRingSmem = 225 * 1024;
 struct RingShape {
   int block, grid, smem;
   int64_t groups;
+  bool fits;  // (else the rows are too long for shared memory)
 };
-RingShape ring_shape(RingParams &R, const NormParams &F, bool full, const void *dr, int64_t lddr, const void *dh, int64_t lddh,
-                     int sms) {
+RingShape ring_shape(RingParams &R, const NormParams &F, bool exact, bool backward, const void *dr, int64_t lddr, const void *dh, int64_t lddh,
+                     int most_threads, int sms) {
   const int d = F.d;
-  R.threads = (int)up((d + kRingValues - 1) / kRingValues, 32);
-  R.rows = std::max(1, 256 / R.threads);
+  R.threads = ring_threads(d);
   auto row = [&](int k, const void *p, int64_t ld, bool wide) {
     R.p[k] = p;
     R.ld[k] = ld * (wide ? 4 : 2);
     R.bytes[k] = d * (wide ? 4 : 2);
     R.at[k] = R.stage;
-    if (p) R.stage += R.bytes[k] * R.rows;
+    if (p) R.stage += R.bytes[k];
   };
   row(kOfX, F.x, F.ldx, F.x32);
   row(kOfZ, F.z, F.ldz, F.z32);
   row(kOfDr, dr, lddr, F.x32);
   row(kOfDh, dh, lddh, false);
   row(kOfGate, F.ldg ? F.gate : nullptr, F.ldg, false);
+  int held = 0;
+  const bool gate = F.gate && !F.ldg;
+  const bool needed[kWeights] = {exact || (F.z && (gate || F.wp)), exact || F.w, F.bp != nullptr, F.b && !backward};
+  for (int k = 0; k < kWeights; ++k) {
+    R.held[k] = needed[k] ? held : -1;
+    held += needed[k] ? d * 4 : 0;
+  }
+  // As many groups as threads allow, fewer where that leaves them two stages each.
+  const int budget = kRingSmem - held;
+  R.groups = std::max(1, std::min(R.threads == 32 ? kMaxGroups : kMaxGroups - 1, most_threads / R.threads));
+  while (R.groups > 1 && R.groups * 2 * R.stage > budget) --R.groups;
+  R.stages = std::min(kMaxStages, budget / (R.groups * R.stage));
   RingShape s;
-  s.block = R.threads * R.rows;
-  // Two CTAs an SM where each has room for two stages at least; the weights in shared memory where two
-  // stages are left beside them.
-  const int held = (full ? 4 : 2) * d * 4, half = 112 * 1024;
-  const int per_sm = s.block <= 320 && 2 * R.stage <= half ? 2 : 1;
-  const int budget = per_sm == 2 ? half : 2 * half;
-  R.held = 2 * R.stage + held <= budget;
-  R.stages = std::max(1, std::min(kMaxStages, (budget - (R.held ? held : 0)) / R.stage));
-  s.smem = R.stages * R.stage + (R.held ? held : 0);
-  const int64_t units = (F.T + (int64_t)R.rows - 1) / R.rows;
-  s.grid = (int)std::min<int64_t>(units, (int64_t)sms * per_sm);
-  s.groups = (int64_t)s.grid * R.rows;
+  s.block = R.threads * R.groups;
+  s.smem = R.groups * R.stages * R.stage + held;
+  s.grid = (int)std::min<int64_t>(((int64_t)F.T + R.groups - 1) / R.groups, sms);
+  s.groups = (int64_t)s.grid * R.groups;
+  s.fits = R.threads <= most_threads && R.stages > 0;
   return s;
 }
-constexpr int kRingWidth = 512 * kRingValues;
-constexpr size_t kRingSmem = 225 * 1024;
 constexpr int kRingRows = 4;  // rows an SM from which the ring is worth its start
 template <class Kernel, class... Args>
 cudaError_t launch_ring(Kernel kernel, const RingShape &s, std::atomic<uint64_t> &ready, cudaStream_t stream, const Args &...args) {
@@ -1101,34 +1199,34 @@ cudaError_t launch_ring(Kernel kernel, const RingShape &s, std::atomic<uint64_t>
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3((unsigned)s.grid), dim3((unsigned)s.block), (size_t)s.smem, stream, args...);
 }
-template <bool bf16, bool WIDE, bool FULL>
+template <bool bf16, bool WIDE, bool FULL, bool EXACT>
 cudaError_t run_ring(const RingShape &s, const NormParams &P, const RingParams &R, int32_t *err, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
-  return launch_ring(k_norm_forward_ring<bf16, WIDE, FULL>, s, ready, stream, P, R, err);
+  return launch_ring(k_norm_forward_ring<bf16, WIDE, FULL, EXACT>, s, ready, stream, P, R, err);
 }
-template <bool bf16, bool WIDE, bool FULL>
+template <bool bf16, bool WIDE, bool FULL, bool EXACT>
 cudaError_t run_ring(const RingShape &s, const NormBackParams &P, const RingParams &R, int32_t *, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
-  return launch_ring(k_norm_backward_ring<bf16, WIDE, FULL>, s, ready, stream, P, R);
+  return launch_ring(k_norm_backward_ring<bf16, WIDE, FULL, EXACT>, s, ready, stream, P, R);
+}
+template <bool bf16, bool WIDE, class Params>
+cudaError_t run_ring(bool full, bool exact, const RingShape &s, const Params &P, const RingParams &R, int32_t *err,
+                     cudaStream_t stream) {
+  if (full) return exact ? run_ring<bf16, WIDE, true, true>(s, P, R, err, stream) : run_ring<bf16, WIDE, true, false>(s, P, R, err, stream);
+  return exact ? run_ring<bf16, WIDE, false, true>(s, P, R, err, stream) : run_ring<bf16, WIDE, false, false>(s, P, R, err, stream);
 }
 template <class Params>
-cudaError_t run_ring(bool bf16, bool wide, bool full, const RingShape &s, const Params &P, const RingParams &R, int32_t *err,
-                     cudaStream_t stream) {
-  switch (bf16 * 4 + wide * 2 + full) {
-    case 0: return run_ring<false, false, false>(s, P, R, err, stream);
-    case 1: return run_ring<false, false, true>(s, P, R, err, stream);
-    case 2: return run_ring<false, true, false>(s, P, R, err, stream);
-    case 3: return run_ring<false, true, true>(s, P, R, err, stream);
-    case 4: return run_ring<true, false, false>(s, P, R, err, stream);
-    case 5: return run_ring<true, false, true>(s, P, R, err, stream);
-    case 6: return run_ring<true, true, false>(s, P, R, err, stream);
-    default: return run_ring<true, true, true>(s, P, R, err, stream);
-  }
+cudaError_t run_ring(bool bf16, bool wide, bool full, bool exact, const RingShape &s, const Params &P, const RingParams &R,
+                     int32_t *err, cudaStream_t stream) {
+  if (bf16)
+    return wide ? run_ring<true, true>(full, exact, s, P, R, err, stream) : run_ring<true, false>(full, exact, s, P, R, err, stream);
+  return wide ? run_ring<false, true>(full, exact, s, P, R, err, stream) : run_ring<false, false>(full, exact, s, P, R, err, stream);
 }
+bool exact_rows(const NormParams &P) { return P.d % (32 * kRingValues) == 0 && P.z && P.pre != SFNN_NORM_NONE && !P.ldg; }
 
 template <bool bf16>
 cudaError_t run_backward(const NormBackParams &P, bool vec, bool full, const BackShape &b, cudaStream_t s) {
-  if (vec)  // (narrower rows go through the ring)
+  if (vec)  // rows too long for the ring (at least 4096 values), and so for one CTA
     return full ? launch_rows(k_norm_backward<bf16, 8, true, true>, b.grid, b.block, b.ctas, b.threads, P, s)
                 : launch_rows(k_norm_backward<bf16, 8, false, true>, b.grid, b.block, b.ctas, b.threads, P, s);
   return full ? run_backward<bf16, 1, true>(P, b, s) : run_backward<bf16, 1, false>(P, b, s);
@@ -1166,14 +1264,14 @@ sfnn_status sfnn_norm_forward(const sfnn_norm_desc *q, void *r, int64_t ldr, voi
   const int sms = device_sms();
   if (sms < 1) return SFNN_ERR_CUDA;
   cudaError_t e;
-  if (vec && P.d <= kRingWidth && P.T >= kRingRows * sms) {
-    RingParams R{};
-    const bool full = P.pre == SFNN_NORM_LAYER || P.post == SFNN_NORM_LAYER || P.b || P.bp;
-    const RingShape shape = ring_shape(R, P, full, nullptr, 0, nullptr, 0, sms);
-    e = run_ring(bf16, P.x32 || P.z32, full, shape, P, R, err, s);
-  } else {
+  RingParams R{};
+  const bool full = P.pre == SFNN_NORM_LAYER || P.post == SFNN_NORM_LAYER || P.b || P.bp;
+  const bool exact = exact_rows(P);
+  const RingShape shape = ring_shape(R, P, exact, false, nullptr, 0, nullptr, 0, kForwardThreads, sms);
+  if (vec && shape.fits && P.T >= kRingRows * sms)
+    e = run_ring(bf16, P.x32 || P.z32, full, exact, shape, P, R, err, s);
+  else
     e = bf16 ? run_forward<true>(P, vec, s) : run_forward<false>(P, vec, s);
-  }
   return e == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
 }
 
@@ -1222,14 +1320,15 @@ sfnn_status sfnn_norm_backward(const sfnn_norm_desc *q, const float *stats, cons
                    vectors(P.dgate, 0);
   int64_t groups;
   cudaError_t e;
-  if (vec && q->d <= kRingWidth) {
-    RingParams R{};
-    const bool full = P.f.pre == SFNN_NORM_LAYER || P.f.post == SFNN_NORM_LAYER || P.f.bp || asked[kSumB] || asked[kSum0];
-    const RingShape shape = ring_shape(R, P.f, full, dr, lddr, dh, lddh, sms);
+  RingParams R{};
+  bool full = P.f.pre == SFNN_NORM_LAYER || P.f.post == SFNN_NORM_LAYER || P.f.bp || asked[kSumB] || asked[kSum0];
+  const bool exact = exact_rows(P.f) && dr && dh && dx && dz;
+  const RingShape shape = ring_shape(R, P.f, exact, true, dr, lddr, dh, lddh, kBackwardThreads, sms);
+  if (vec && shape.fits) {
     groups = shape.groups;
-    e = run_ring(bf16, P.f.x32 || P.f.z32, full, shape, P, R, err, s);
+    e = run_ring(bf16, P.f.x32 || P.f.z32, full, exact, shape, P, R, err, s);
   } else {
-    const bool full = asked[kSumB] || asked[kSum0];
+    full = asked[kSumB] || asked[kSum0];
     const BackShape b = back_shape(q->T, q->d, full, sms);
     groups = b.groups();
     e = bf16 ? run_backward<true>(P, vec, full, b, s) : run_backward<false>(P, vec, full, b, s);
