@@ -386,7 +386,8 @@ def _dense(t) -> bool:
 def _grad_table(grads, outs, n):
     """The entries of sfnn_grad, four words a tensor; None if something is not a CUDA tensor."""
     T = torch.Tensor
-    if not all(map(T.is_cuda.__get__, grads)) or len(set(map(T.get_device, grads))) != 1:
+    where = set(map(T.get_device, grads))
+    if len(where) != 1 or not grads[0].is_cuda:
         return None
     dtypes = list(map(T.dtype.__get__, grads))
     codes = list(map(_GRAD_CODES.get, dtypes))
@@ -403,7 +404,7 @@ def _grad_table(grads, outs, n):
     table[2::4] = array("q", sizes)
     table[3::4] = array("q", codes)
     if outs is not grads:
-        if list(map(T.get_device, outs)) != [grads[0].get_device()] * n:
+        if set(map(T.get_device, outs)) != where:
             return None
         same = list(map(T.dtype.__get__, outs)) == dtypes and list(map(T.numel, outs)) == sizes
         if same and not (all(in_order) and all(map(T.is_contiguous, outs))):
