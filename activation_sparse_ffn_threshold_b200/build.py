@@ -1,4 +1,5 @@
-"""Build libsfnn.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libsfnn.so (the C-ABI library) in-tree with nvcc for sm_100a, and _block.so (native
+marshalling of block.py's tensors into it) with the host compiler against torch's headers.
 
 Each ``csrc/*.cu`` file is compiled to an object under ``_build/`` (rebuilt
 when it or a header is newer), then linked into a shared library next to this
@@ -18,6 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsfnn.so")
+BIND = os.path.join(PKG, "_block.so")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -66,7 +69,35 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    build_binding(verbose=verbose, force=force)
     return LIB
+
+
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    """_block.so: csrc/bind/block.cpp against torch's headers and libsfnn.so."""
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(CSRC, "bind", "block.cpp")
+    if not force and not _stale(BIND, [src, os.path.join(INCLUDE, "sfnn.h"), torch.__file__]):
+        return BIND
+    t = os.path.dirname(torch.__file__)
+    includes = [f"{t}/include", f"{t}/include/torch/csrc/api/include", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+                sysconfig.get_paths()["include"]]
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w", "-I", INCLUDE,
+           *(a for i in includes for a in ("-isystem", i)),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp, f"-L{t}/lib", f"-L{PKG}",
+           "-l:libsfnn.so", "-ltorch_python", "-ltorch", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building {BIND} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
 
 
 if __name__ == "__main__":

@@ -7,13 +7,26 @@ import pytest
 import torch
 
 import activation_sparse_ffn_threshold_b200 as sf
-from activation_sparse_ffn_threshold_b200 import block
+
+
+class NormDesc(ctypes.Structure):  # sfnn_norm_desc
+    _fields_ = [(k, ctypes.c_int32) for k in ("T", "d", "dtype", "x_dtype", "z_dtype", "pre", "post")] + \
+        [(k, ctypes.c_float) for k in ("eps", "residual_scale", "branch_scale")] + \
+        [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+         ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64)] + [(k, ctypes.c_void_p) for k in ("w", "b", "post_w", "post_b")]
+
+
+class LinearDesc(ctypes.Structure):  # sfnn_linear_desc
+    _fields_ = [(k, ctypes.c_int32) for k in ("T", "K", "N", "dtype", "y_dtype", "act")] + \
+        [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+         ("b", ctypes.c_void_p)]
+
 
 INVALID, UNSUPPORTED = sf.STATUS_CODES["SFNN_ERR_INVALID_ARG"], sf.STATUS_CODES["SFNN_ERR_UNSUPPORTED"]
 
 
 def norm(T=2, d=64, dtype=sf.F16, **kw):
-    q = block._NormDesc(T, d, dtype, dtype, dtype, 1, 0, 1e-5, 1.0, 1.0, 4096, d, 4096, d, None, 0, 4096, None, None, None)
+    q = NormDesc(T, d, dtype, dtype, dtype, 1, 0, 1e-5, 1.0, 1.0, 4096, d, 4096, d, None, 0, 4096, None, None, None)
     for k, v in kw.items():
         setattr(q, k, v)
     return q
@@ -109,7 +122,7 @@ def test_binding_refuses_host_tensors_and_bad_options():
 
 
 def linear(T=4, K=64, N=40, dtype=sf.F16, y_dtype=None, act=1, **kw):
-    q = block._LinearDesc(T, K, N, dtype, dtype if y_dtype is None else y_dtype, act, 4096, K, 4096, K, 4096)
+    q = LinearDesc(T, K, N, dtype, dtype if y_dtype is None else y_dtype, act, 4096, K, 4096, K, 4096)
     for k, v in kw.items():
         setattr(q, k, v)
     return q
