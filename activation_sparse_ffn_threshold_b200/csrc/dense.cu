@@ -546,15 +546,23 @@ __device__ __forceinline__ void res_add(const LinearEnd &E, const Unit &Q, int64
   if (!E.res) return;
   const int lane = threadIdx.x & 31;
   __syncwarp();
-  if (!E.vec_res) {  // value by value, staged as 32 bits
-    for (int r = 0; r < 32; ++r) {
-      float f = 0.f;
-      if (r < rows && col + lane < Q.N) {
-        const int64_t i = (row0 + r) * E.ldres + col + lane;
-        f = WIDE ? static_cast<const float *>(E.res)[i] : load16(E.res, i, bf16);
+  if (!E.vec_res) {  // value by value, staged as 32 bits, 16 rows requested together
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+      float f[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        f[r] = 0.f;
+        if (r0 + r < rows && col + lane < Q.N) {
+          const int64_t i = (row0 + r0 + r) * E.ldres + col + lane;
+          f[r] = WIDE ? static_cast<const float *>(E.res)[i] : load16(E.res, i, bf16);
+        }
       }
-      const uint32_t at = panel_at(panel + (lane >> 4) * kPanel, r, (lane & 15) >> 2) + (lane & 3) * 4;
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(f) : "memory");
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const uint32_t at = panel_at(panel + (lane >> 4) * kPanel, r0 + r, (lane & 15) >> 2) + (lane & 3) * 4;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(f[r]) : "memory");
+      }
     }
   } else if (WIDE) {
 #pragma unroll
@@ -602,6 +610,7 @@ __device__ __forceinline__ void ragged_out(const Unit &Q, int64_t row0, int col,
                      __float_as_uint(v[4 * j + 3])));
   __syncwarp();
   if (col + lane >= Q.N) return;
+#pragma unroll 8
   for (int r = 0; r < rows; ++r) {
     float f;
     asm volatile("ld.shared.f32 %0, [%1];"

@@ -90,66 +90,85 @@ __global__ void __launch_bounds__(256) k_linear_slopes(const __grid_constant__ S
   const int64_t slope_ld = slope_row_bytes(P.N, P.act);
   auto column = [&](int j) { return V == 8 ? c0 + lane * 8 + j : c0 + lane + 32 * j; };
   for (int64_t block = blockIdx.y; block * 32 < P.M; block += gridDim.y) {
-    float sum[8] = {};
+    float sum[8] = {}, v[4][8];
+    uint32_t code[4][V == 8 ? 4 : 8];  // act' of the row: words of two codes or of 32 bits (V = 8), else one a value
+    // all of them requested before the first is used
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int64_t row = block * 32 + warp * 4 + r;
-      if (row >= P.M || column(0) >= P.N) break;
-      float v[8];
+      const bool live = row < P.M;
+      const unsigned char *s = static_cast<const unsigned char *>(P.slopes) + row * slope_ld;
       if (V == 8) {
+        const bool there = live && column(0) < P.N;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[r][j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[r][V == 8 ? i : 0] = 0;
+        if (!there) continue;
         const int64_t at = row * P.lddy + column(0);
         if (P.dy32) {
           const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(P.dy) + at);
           const float4 a = __ldg(q), b = __ldg(q + 1);
-          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+          v[r][0] = a.x, v[r][1] = a.y, v[r][2] = a.z, v[r][3] = a.w;
+          v[r][4] = b.x, v[r][5] = b.y, v[r][6] = b.z, v[r][7] = b.w;
         } else {
           const uint4 a = ld_stream(static_cast<const uint16_t *>(P.dy) + at);
           const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 f = unpack16(u[i], bf16);
-            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            v[r][2 * i] = f.x, v[r][2 * i + 1] = f.y;
           }
+        }
+        if (P.act == SFNN_LINEAR_RELU) {
+          code[r][0] = __ldg(reinterpret_cast<const uint32_t *>(s) + column(0) / 32) >> (column(0) & 31);
+        } else if (P.act != SFNN_LINEAR_NONE) {
+          const uint4 a = ld_stream(s + (int64_t)column(0) * 2);
+          code[r][0] = a.x, code[r][1] = a.y, code[r][V == 8 ? 2 : 0] = a.z, code[r][V == 8 ? 3 : 0] = a.w;
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+          const bool there = live && column(j) < P.N;
           const int64_t at = row * P.lddy + column(j);
-          v[j] = column(j) >= P.N ? 0.f : P.dy32 ? static_cast<const float *>(P.dy)[at] : load16(P.dy, at, bf16);
+          v[r][j] = !there ? 0.f : P.dy32 ? static_cast<const float *>(P.dy)[at] : load16(P.dy, at, bf16);
+          code[r][V == 8 ? 0 : j] = !there || P.act == SFNN_LINEAR_NONE ? 0u
+                                    : P.act == SFNN_LINEAR_RELU
+                                        ? (__ldg(reinterpret_cast<const uint32_t *>(s) + column(j) / 32) >> lane) & 1u
+                                        : reinterpret_cast<const uint16_t *>(s)[column(j)];
         }
       }
-      const unsigned char *s = static_cast<const unsigned char *>(P.slopes) + row * slope_ld;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t row = block * 32 + warp * 4 + r;
       if (P.act == SFNN_LINEAR_RELU) {
-        const uint32_t *words = reinterpret_cast<const uint32_t *>(s);
-        const uint32_t own = V == 8 ? __ldg(words + column(0) / 32) >> (column(0) & 31) : 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const bool on = V == 8 ? (own >> j) & 1u : column(j) < P.N && (__ldg(words + column(j) / 32) >> lane) & 1u;
-          v[j] = on ? v[j] : 0.f;
+          const uint32_t on = V == 8 ? code[r][0] >> j : code[r][V == 8 ? 0 : j];
+          v[r][j] = on & 1u ? v[r][j] : 0.f;
         }
       } else if (P.act != SFNN_LINEAR_NONE) {
-        if (V == 8) {
-          const uint4 a = ld_stream(s + (int64_t)column(0) * 2);
-          const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[2 * i] *= slope_value(u[i] & 0xffffu), v[2 * i + 1] *= slope_value(u[i] >> 16);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (column(j) < P.N) v[j] *= slope_value(reinterpret_cast<const uint16_t *>(s)[column(j)]);
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t c = V == 8 ? (code[r][j / 2] >> (16 * (j & 1))) & 0xffffu : code[r][V == 8 ? 0 : j];
+          v[r][j] *= slope_value(c);
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += v[j];
-      if (!P.dz) continue;
+      for (int j = 0; j < 8; ++j) sum[j] += v[r][j];
+      if (!P.dz || row >= P.M) continue;
       uint16_t *out = static_cast<uint16_t *>(P.dz) + row * P.lddz;
-      if (V == 8)
-        *reinterpret_cast<uint4 *>(out + column(0)) =
-            make_uint4(pack16(v[0], v[1], bf16), pack16(v[2], v[3], bf16), pack16(v[4], v[5], bf16), pack16(v[6], v[7], bf16));
-      else
+      if (V == 8) {
+        if (column(0) < P.N)
+          *reinterpret_cast<uint4 *>(out + column(0)) =
+              make_uint4(pack16(v[r][0], v[r][1], bf16), pack16(v[r][2], v[r][3], bf16), pack16(v[r][4], v[r][5], bf16),
+                         pack16(v[r][6], v[r][7], bf16));
+      } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (column(j) < P.N) out[column(j)] = (uint16_t)pack16(v[j], 0.f, bf16);
+          if (column(j) < P.N) out[column(j)] = (uint16_t)pack16(v[r][j], 0.f, bf16);
+      }
     }
     if (!P.colpart) continue;
     __syncthreads();  // the block before has been added up
@@ -158,10 +177,10 @@ __global__ void __launch_bounds__(256) k_linear_slopes(const __grid_constant__ S
     __syncthreads();
     const int c = c0 + threadIdx.x;
     if (c >= P.N) continue;
-    float v = 0.f;
+    float total = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += sums[w][threadIdx.x];
-    P.colpart[block * P.N + c] = v;
+    for (int w = 0; w < 8; ++w) total += sums[w][threadIdx.x];
+    P.colpart[block * P.N + c] = total;
   }
 }
 

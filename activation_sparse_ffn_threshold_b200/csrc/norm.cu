@@ -403,7 +403,7 @@ struct NormSums {
   const void *gate, *wp, *bp;  // one gate row, or null
   void *dw, *db, *dgate, *dwp, *dbp;
 };
-constexpr int kSumWarps = 16;
+constexpr int kSumWarps = 16, kSumAhead = 10;  // a CTA's sums of every SM in one request
 template <bool bf16>
 __global__ void __launch_bounds__(kSumWarps * 32) k_norm_sums(const __grid_constant__ NormSums P) {
   __shared__ float s[kSums][kSumWarps][33];
@@ -411,19 +411,24 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_norm_sums(const __grid_const
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   const int64_t group = (int64_t)P.sums * P.d;
+  float v[kSums] = {};
+  if (c < P.d)
+    for (int g = warp; g < P.groups; g += kSumWarps * kSumAhead) {
 #pragma unroll
-  for (int k = 0; k < kSums; ++k) {
-    if (P.at[k] < 0) continue;
-    const float *p = P.part + (int64_t)P.at[k] * P.d + c;
-    float v = 0.f;
-    if (c < P.d)
-#pragma unroll 8
-      for (int g = warp; g < P.groups; g += kSumWarps) v += __ldg(p + g * group);
-    s[k][warp][lane] = v;
-  }
+      for (int k = 0; k < kSums; ++k) {
+        if (P.at[k] < 0) continue;
+        const float *p = P.part + (int64_t)P.at[k] * P.d + c;
+        float f[kSumAhead];
+#pragma unroll
+        for (int i = 0; i < kSumAhead; ++i) f[i] = g + i * kSumWarps < P.groups ? __ldg(p + (g + i * kSumWarps) * group) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kSumAhead; ++i) v[k] += f[i];
+      }
+    }
+#pragma unroll
+  for (int k = 0; k < kSums; ++k) s[k][warp][lane] = v[k];
   __syncthreads();
   if (warp || c >= P.d) return;
-  float v[kSums];
 #pragma unroll
   for (int k = 0; k < kSums; ++k) {
     v[k] = 0.f;
@@ -539,12 +544,9 @@ BackShape back_shape(int64_t T, int d, bool full, int sms) {
   b.grid = (int)std::min<int64_t>(T, std::max(1, sms * (full ? 1 : 2) / b.ctas)) * b.ctas;
   return b;
 }
-int64_t ring_groups(int64_t T, int d, int sms) {  // at most: a CTA's share of the rows, or all its groups
-  return std::min(T + sms, (int64_t)sms * ring_groups_most(d));
-}
 int64_t back_workspace(int64_t T, int d, int sums, int sms) {  // (the larger of the two kernels')
   T = std::max<int64_t>(T, 1);
-  return up(std::max(back_shape(T, d, false, sms).groups(), ring_groups(T, d, sms)) * sums * d * 4, 256);
+  return up(std::max(back_shape(T, d, false, sms).groups(), std::min<int64_t>(T, sms)) * sums * d * 4, 256);
 }
 
 template <bool bf16>
@@ -642,13 +644,13 @@ sfnn_status sfnn_norm_backward(const sfnn_norm_desc *q, const float *stats, cons
   cudaError_t e = norm_backward_ring(P, all, bf16, vec, sms, s, plan);
   if (!plan.fits) {
     const BackShape b = back_shape(q->T, q->d, all, sms);
-    plan.groups = b.groups();
+    plan.groups = (int)b.groups();
     e = bf16 ? run_backward<true>(P, vec, all, b, s) : run_backward<false>(P, vec, all, b, s);
   }
   if (e != cudaSuccess) return SFNN_ERR_CUDA;
   if (S.sums) {
     S.part = P.part;
-    S.groups = (int)plan.groups;
+    S.groups = plan.groups;
     S.d = q->d;
     S.c = P.f.c;
     S.gate = one_gate ? q->gate : nullptr;

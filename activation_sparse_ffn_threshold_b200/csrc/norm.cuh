@@ -33,15 +33,12 @@ struct NormBackParams {
   int at[kSums];  // their places in part, or -1
 };
 
-// Rows through shared memory (norm_ring.cu).  A plan says how many groups of threads take rows; `fits` is
-// false where a row is too long for it.
+// Rows through shared memory (norm_ring.cu).  `fits` is false, and nothing was launched, where a row is
+// too long for it; groups: of sums in part, no more than SMs or rows.
 struct RingPlan {
   bool fits;
-  int64_t groups;
+  int groups;
 };
-constexpr int kRingThreads = 512;  // of a backward CTA
-int ring_threads(int d);           // of a group
-int ring_groups_most(int d);       // groups of a backward CTA, at most
 cudaError_t norm_forward_ring(const NormParams &P, int32_t *err, bool bf16, bool vec, int sms, cudaStream_t s,
                               RingPlan &plan);
 cudaError_t norm_backward_ring(const NormBackParams &P, bool sums_all, bool bf16, bool vec, int sms, cudaStream_t s,

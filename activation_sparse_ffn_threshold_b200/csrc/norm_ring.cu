@@ -143,9 +143,35 @@ struct Ring {
       float *to = reinterpret_cast<float *>(smem + (size_t)R.groups * R.stages * R.stage + at);
       const void *p = k == kPostW ? F.wp : k == kPreW ? F.w : k == kPostB ? F.bp : F.b;
       const bool post = k == kPostW || k == kPostB;
-      for (int c = threadIdx.x; c < F.d; c += blockDim.x) {
-        const float v = p ? load16(p, c, bf16) : 1.f;
-        to[c] = post ? (F.gate && !F.ldg ? load16(F.gate, c, bf16) : 1.f) * F.c * v : v;
+      const void *gate = post && !F.ldg ? F.gate : nullptr;
+      if (!ODD) {
+        for (int c = threadIdx.x * 8; c < F.d; c += blockDim.x * 8) {
+          Pair v[4], g[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = g[i] = both(1.f);
+          if (p) widen8(ld_keep(static_cast<const uint16_t *>(p) + c), v);
+          if (gate) widen8(ld_keep(static_cast<const uint16_t *>(gate) + c), g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (post) v[i] = mul2(mul2(g[i], both(F.c)), v[i]);
+          *reinterpret_cast<ulonglong2 *>(to + c) = make_ulonglong2(v[0], v[1]);
+          *reinterpret_cast<ulonglong2 *>(to + c + 4) = make_ulonglong2(v[2], v[3]);
+        }
+      } else {
+        for (int c0 = threadIdx.x; c0 < F.d; c0 += 8 * blockDim.x) {
+          float v[8], g[8];  // requested together
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = c0 + i * (int)blockDim.x;
+            v[i] = p && c < F.d ? load16(p, c, bf16) : 1.f;
+            g[i] = gate && c < F.d ? load16(gate, c, bf16) : 1.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = c0 + i * (int)blockDim.x;
+            if (c < F.d) to[c] = post ? g[i] * F.c * v[i] : v[i];
+          }
+        }
       }
     }
     __syncthreads();
@@ -357,7 +383,7 @@ struct Ring {
   }
 };
 
-constexpr int kForwardThreads = 1024, kBackwardThreads = kRingThreads;
+constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
 
 template <bool bf16, bool WIDE, bool FULL, bool EXACT, bool ODD>
 __global__ void __launch_bounds__(kForwardThreads, 1) k_norm_forward_ring(const __grid_constant__ NormParams P,
@@ -611,13 +637,17 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_norm_backward_ring(cons
     }
   }
   if (!P.part) return;
-  float *part = P.part + ((int64_t)blockIdx.x * R.groups + ring.mine) * P.sums * F.d;
+  // The groups' sums, by way of shared memory (no copy is on its way any more), as one of the CTA's.
+  const int width = P.sums * F.d;
+  float *part = P.part + (int64_t)blockIdx.x * width;
+  float *own = reinterpret_cast<float *>(ring_smem) + (size_t)ring.mine * width;
+  __syncthreads();
   auto put = [&](int at, const Pair *v) {
     if (at < 0) return;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!ring.in(k)) continue;
-      float *to = part + (int64_t)at * F.d;
+      float *to = own + (size_t)at * F.d;
       if (ODD) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -637,17 +667,24 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_norm_backward_ring(cons
     put(P.at[kSumB], sb);
     put(P.at[kSum0], sum0);
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < width; i += blockDim.x) {
+    const float *from = reinterpret_cast<const float *>(ring_smem) + i;
+    float v = 0.f;
+    for (int g = 0; g < R.groups; ++g) v += from[(size_t)g * width];
+    part[i] = v;
+  }
 }
 
 // The rows' way through shared memory.
 constexpr int kRingSmem = 225 * 1024;
 struct RingShape {
   int block, grid, smem;
-  int64_t groups;
   bool fits;
 };
+int ring_threads(int d) { return (int)up((d + kRingValues - 1) / kRingValues, 32); }
 RingShape ring_shape(RingParams &R, const NormParams &F, bool odd, bool exact, bool backward, const void *dr, int64_t lddr,
-                     const void *dh, int64_t lddh, int most_threads, int sms) {
+                     const void *dh, int64_t lddh, int sums, int most_threads, int sms) {
   const int d = F.d;
   R.threads = ring_threads(d);
   auto row = [&](int k, const void *p, int64_t ld, bool wide) {
@@ -674,14 +711,13 @@ RingShape ring_shape(RingParams &R, const NormParams &F, bool odd, bool exact, b
   const int budget = kRingSmem - held;
   R.groups = std::max(1, std::min(R.threads == 32 ? kMaxGroups : kMaxGroups - 1, most_threads / R.threads));
   R.groups = std::min(R.groups, std::max(1, (F.T + sms - 1) / sms));
-  while (R.groups > 1 && R.groups * 2 * R.stage > budget) --R.groups;
+  while (R.groups > 1 && (R.groups * 2 * R.stage > budget || R.groups * sums * d * 4 > kRingSmem)) --R.groups;
   R.stages = std::max(0, std::min(kMaxStages, budget / (R.groups * R.stage)));
   RingShape s;
   s.block = R.threads * R.groups;
-  s.smem = R.groups * R.stages * R.stage + held;
+  s.smem = std::max(R.groups * R.stages * R.stage + held, R.groups * sums * d * 4);
   s.grid = (int)std::min<int64_t>(((int64_t)F.T + R.groups - 1) / R.groups, sms);
-  s.groups = (int64_t)s.grid * R.groups;
-  s.fits = R.threads <= most_threads && R.stages > 0;
+  s.fits = R.threads <= most_threads && R.stages > 0 && s.smem <= kRingSmem;
   return s;
 }
 
@@ -721,14 +757,11 @@ cudaError_t run_ring(bool wide, bool full, bool exact, bool odd, const RingShape
 
 }  // namespace
 
-int ring_threads(int d) { return (int)up((d + kRingValues - 1) / kRingValues, 32); }
-int ring_groups_most(int d) { return std::max(1, std::min(kMaxGroups, kBackwardThreads / ring_threads(d))); }
-
 cudaError_t norm_forward_ring(const NormParams &P, int32_t *err, bool bf16, bool vec, int sms, cudaStream_t s, RingPlan &plan) {
   const bool full = P.pre == SFNN_NORM_LAYER || P.post == SFNN_NORM_LAYER || P.b || P.bp, exact = exact_rows(P, vec);
   RingParams R{};
-  const RingShape shape = ring_shape(R, P, !vec, exact, false, nullptr, 0, nullptr, 0, kForwardThreads, sms);
-  plan = {shape.fits, shape.groups};
+  const RingShape shape = ring_shape(R, P, !vec, exact, false, nullptr, 0, nullptr, 0, 0, kForwardThreads, sms);
+  plan = {shape.fits, shape.grid};
   if (!shape.fits) return cudaSuccess;
   return bf16 ? run_ring<true>(P.x32 || P.z32, full, exact, !vec, shape, P, R, err, s)
               : run_ring<false>(P.x32 || P.z32, full, exact, !vec, shape, P, R, err, s);
@@ -738,8 +771,8 @@ cudaError_t norm_backward_ring(const NormBackParams &P, bool sums_all, bool bf16
   const bool full = F.pre == SFNN_NORM_LAYER || F.post == SFNN_NORM_LAYER || F.bp || sums_all;
   const bool exact = exact_rows(F, vec) && P.dr && P.dh && P.dx && P.dz;
   RingParams R{};
-  const RingShape shape = ring_shape(R, F, !vec, exact, true, P.dr, P.lddr, P.dh, P.lddh, kBackwardThreads, sms);
-  plan = {shape.fits, shape.groups};
+  const RingShape shape = ring_shape(R, F, !vec, exact, true, P.dr, P.lddr, P.dh, P.lddh, P.sums, kBackwardThreads, sms);
+  plan = {shape.fits, shape.grid};
   if (!shape.fits) return cudaSuccess;
   return bf16 ? run_ring<true>(F.x32 || F.z32, full, exact, !vec, shape, P, R, P.err, s)
               : run_ring<false>(F.x32 || F.z32, full, exact, !vec, shape, P, R, P.err, s);
