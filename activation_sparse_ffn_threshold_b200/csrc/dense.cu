@@ -519,12 +519,18 @@ __device__ __forceinline__ void epi_dgated(const DenseParams &P, const Unit &Q, 
 }
 
 // ---------------------------------------------------------------- the linear layer's epilogue
-// The residual: 32 columns of a warp's rows come in as panels go out (a row's 64 bytes by 4 lanes).
-// 16-bit values wait in registers, requested a piece ahead; an fp32 result has its sums there.
+// The residual: 32 columns of a warp's rows come in as panels go out (a row's 64 bytes by 4 lanes), or,
+// where rows do not consist of 16-byte pieces, a column a lane.  16-bit values wait in registers,
+// requested a piece ahead; an fp32 result has its sums there.
 template <bool WIDE>
 struct ResPiece {
   uint4 w[WIDE ? 1 : 4];
 };
+__device__ __forceinline__ uint32_t res_half(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows, int r) {
+  const int lane = threadIdx.x & 31;
+  if (r >= rows || col + lane >= Q.N) return 0u;
+  return static_cast<const uint16_t *>(E.res)[(row0 + r) * E.ldres + col + lane];
+}
 template <int ESIZE>
 __device__ __forceinline__ uint4 res_word(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows, int i) {
   const int lane = threadIdx.x & 31, row = (i & 3) * 8 + (lane >> 2), c = col + ((i >> 2) * 4 + (lane & 3)) * (16 / ESIZE);
@@ -535,9 +541,19 @@ __device__ __forceinline__ uint4 res_word(const LinearEnd &E, const Unit &Q, int
 template <bool WIDE>
 __device__ __forceinline__ void res_request(const LinearEnd &E, const Unit &Q, int64_t row0, int col, int rows,
                                             ResPiece<WIDE> &p) {
-  if (WIDE || !E.res || !E.vec_res) return;
+  if (WIDE || !E.res) return;
+  if (E.vec_res) {
 #pragma unroll
-  for (int i = 0; i < (WIDE ? 0 : 4); ++i) p.w[i] = res_word<2>(E, Q, row0, col, rows, i);
+    for (int i = 0; i < (WIDE ? 0 : 4); ++i) p.w[i] = res_word<2>(E, Q, row0, col, rows, i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < (WIDE ? 0 : 4); ++i) {
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = res_half(E, Q, row0, col, rows, 8 * i + j);
+      p.w[i] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+  }
 }
 // Added to this lane's row of 32 columns.
 template <bool bf16, bool WIDE>
@@ -546,7 +562,18 @@ __device__ __forceinline__ void res_add(const LinearEnd &E, const Unit &Q, int64
   if (!E.res) return;
   const int lane = threadIdx.x & 31;
   __syncwarp();
-  if (!E.vec_res) {  // value by value, staged as 32 bits, 16 rows requested together
+  if (!WIDE && !E.vec_res) {  // a column, staged as 32 bits
+#pragma unroll
+    for (int i = 0; i < (WIDE ? 0 : 4); ++i) {
+      const uint32_t u[4] = {p.w[i].x, p.w[i].y, p.w[i].z, p.w[i].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 f = unpack16(u[j / 2], bf16);
+        const uint32_t at = panel_at(panel + (lane >> 4) * kPanel, 8 * i + j, (lane & 15) >> 2) + (lane & 3) * 4;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(j % 2 ? f.y : f.x) : "memory");
+      }
+    }
+  } else if (!E.vec_res) {  // the same, 16 rows requested together
 #pragma unroll 1
     for (int r0 = 0; r0 < 32; r0 += 16) {
       float f[16];
@@ -555,7 +582,7 @@ __device__ __forceinline__ void res_add(const LinearEnd &E, const Unit &Q, int64
         f[r] = 0.f;
         if (r0 + r < rows && col + lane < Q.N) {
           const int64_t i = (row0 + r0 + r) * E.ldres + col + lane;
-          f[r] = WIDE ? static_cast<const float *>(E.res)[i] : load16(E.res, i, bf16);
+          f[r] = static_cast<const float *>(E.res)[i];
         }
       }
 #pragma unroll

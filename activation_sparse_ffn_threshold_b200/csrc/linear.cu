@@ -69,50 +69,47 @@ __global__ void __launch_bounds__(256) k_linear_join(const float *__restrict__ p
 }
 
 // dZ from dY, and its columns' sums over 32 rows before it is rounded.  A CTA has 32 rows of 256
-// columns, a warp 4 rows of it; a lane's 8 columns are neighbours where vectors can be read (V = 8),
-// else 32 apart.
+// columns, a warp 4 rows of it, a lane 8 neighbouring columns; all that it reads is requested before the
+// first of it is used.  VEC: dY's rows start on 16 bytes (those of act' and dZ always do).  (Value by value
+// throughout, unrolled, 333 x 2047 took 9 us, most of it first fetches of its instructions.)
 struct SlopeParams {
   const void *dy;
   int64_t lddy;
   int dy32, act, M, N;
   const void *slopes;
-  void *dz;  // or null: dY is dZ
+  void *dz;  // or null: dY is dZ.  Rows of N rounded up to 8
   int64_t lddz;
   float *colpart;  // or null
 };
-template <bool bf16, int V>
+template <bool bf16, bool VEC>
 __global__ void __launch_bounds__(256) k_linear_slopes(const __grid_constant__ SlopeParams P) {
-  __shared__ float sums[8][264];
+  __shared__ float sums[8][256];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c0 = blockIdx.x * 256;
+  const int c0 = blockIdx.x * 256, col = c0 + lane * 8;
   const int64_t slope_ld = slope_row_bytes(P.N, P.act);
-  auto column = [&](int j) { return V == 8 ? c0 + lane * 8 + j : c0 + lane + 32 * j; };
   for (int64_t block = blockIdx.y; block * 32 < P.M; block += gridDim.y) {
     float sum[8] = {}, v[4][8];
-    uint32_t code[4][V == 8 ? 4 : 8];  // act' of the row: words of two codes or of 32 bits (V = 8), else one a value
-    // all of them requested before the first is used
+    uint4 code[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int64_t row = block * 32 + warp * 4 + r;
-      const bool live = row < P.M;
-      const unsigned char *s = static_cast<const unsigned char *>(P.slopes) + row * slope_ld;
-      if (V == 8) {
-        const bool there = live && column(0) < P.N;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[r][j] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) code[r][V == 8 ? i : 0] = 0;
-        if (!there) continue;
-        const int64_t at = row * P.lddy + column(0);
+      const bool live = row < P.M && col < P.N;
+      const int64_t at = row * P.lddy + col;
+      if (VEC) {
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (live && P.dy32) {
+          a = ld_stream(static_cast<const float *>(P.dy) + at);
+          b = ld_stream(static_cast<const float *>(P.dy) + at + 4);
+        } else if (live) {
+          a = ld_stream(static_cast<const uint16_t *>(P.dy) + at);
+        }
         if (P.dy32) {
-          const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(P.dy) + at);
-          const float4 a = __ldg(q), b = __ldg(q + 1);
-          v[r][0] = a.x, v[r][1] = a.y, v[r][2] = a.z, v[r][3] = a.w;
-          v[r][4] = b.x, v[r][5] = b.y, v[r][6] = b.z, v[r][7] = b.w;
+          v[r][0] = __uint_as_float(a.x), v[r][1] = __uint_as_float(a.y), v[r][2] = __uint_as_float(a.z);
+          v[r][3] = __uint_as_float(a.w), v[r][4] = __uint_as_float(b.x), v[r][5] = __uint_as_float(b.y);
+          v[r][6] = __uint_as_float(b.z), v[r][7] = __uint_as_float(b.w);
         } else {
-          const uint4 a = ld_stream(static_cast<const uint16_t *>(P.dy) + at);
           const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -120,60 +117,49 @@ __global__ void __launch_bounds__(256) k_linear_slopes(const __grid_constant__ S
             v[r][2 * i] = f.x, v[r][2 * i + 1] = f.y;
           }
         }
-        if (P.act == SFNN_LINEAR_RELU) {
-          code[r][0] = __ldg(reinterpret_cast<const uint32_t *>(s) + column(0) / 32) >> (column(0) & 31);
-        } else if (P.act != SFNN_LINEAR_NONE) {
-          const uint4 a = ld_stream(s + (int64_t)column(0) * 2);
-          code[r][0] = a.x, code[r][1] = a.y, code[r][V == 8 ? 2 : 0] = a.z, code[r][V == 8 ? 3 : 0] = a.w;
-        }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const bool there = live && column(j) < P.N;
-          const int64_t at = row * P.lddy + column(j);
-          v[r][j] = !there ? 0.f : P.dy32 ? static_cast<const float *>(P.dy)[at] : load16(P.dy, at, bf16);
-          code[r][V == 8 ? 0 : j] = !there || P.act == SFNN_LINEAR_NONE ? 0u
-                                    : P.act == SFNN_LINEAR_RELU
-                                        ? (__ldg(reinterpret_cast<const uint32_t *>(s) + column(j) / 32) >> lane) & 1u
-                                        : reinterpret_cast<const uint16_t *>(s)[column(j)];
+          const bool there = live && col + j < P.N;
+          v[r][j] = !there ? 0.f : P.dy32 ? static_cast<const float *>(P.dy)[at + j] : load16(P.dy, at + j, bf16);
         }
       }
+      code[r] = make_uint4(0, 0, 0, 0);
+      const unsigned char *s = static_cast<const unsigned char *>(P.slopes) + row * slope_ld;
+      if (live && P.act == SFNN_LINEAR_RELU)
+        code[r].x = (uint32_t)__ldg(s + (col >> 3));
+      else if (live && P.act != SFNN_LINEAR_NONE)
+        code[r] = ld_stream(s + (int64_t)col * 2);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int64_t row = block * 32 + warp * 4 + r;
       if (P.act == SFNN_LINEAR_RELU) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t on = V == 8 ? code[r][0] >> j : code[r][V == 8 ? 0 : j];
-          v[r][j] = on & 1u ? v[r][j] : 0.f;
-        }
+        for (int j = 0; j < 8; ++j) v[r][j] = code[r].x >> j & 1u ? v[r][j] : 0.f;
       } else if (P.act != SFNN_LINEAR_NONE) {
+        const uint32_t u[4] = {code[r].x, code[r].y, code[r].z, code[r].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t c = V == 8 ? (code[r][j / 2] >> (16 * (j & 1))) & 0xffffu : code[r][V == 8 ? 0 : j];
-          v[r][j] *= slope_value(c);
+        for (int j = 0; j < 4; ++j) {
+          v[r][2 * j] *= slope_value(u[j] & 0xffffu);
+          v[r][2 * j + 1] *= slope_value(u[j] >> 16);
         }
+        if (!VEC)  // (codes past the row are anything)
+#pragma unroll
+          for (int j = 1; j < 8; ++j) v[r][j] = col + j < P.N ? v[r][j] : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += v[r][j];
-      if (!P.dz || row >= P.M) continue;
-      uint16_t *out = static_cast<uint16_t *>(P.dz) + row * P.lddz;
-      if (V == 8) {
-        if (column(0) < P.N)
-          *reinterpret_cast<uint4 *>(out + column(0)) =
-              make_uint4(pack16(v[r][0], v[r][1], bf16), pack16(v[r][2], v[r][3], bf16), pack16(v[r][4], v[r][5], bf16),
-                         pack16(v[r][6], v[r][7], bf16));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (column(j) < P.N) out[column(j)] = (uint16_t)pack16(v[r][j], 0.f, bf16);
-      }
+      if (P.dz && row < P.M && col < P.N)
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.dz) + row * P.lddz + col) =
+            make_uint4(pack16(v[r][0], v[r][1], bf16), pack16(v[r][2], v[r][3], bf16), pack16(v[r][4], v[r][5], bf16),
+                       pack16(v[r][6], v[r][7], bf16));
     }
     if (!P.colpart) continue;
     __syncthreads();  // the block before has been added up
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sums[warp][column(j) - c0] = sum[j];
+    float4 *mine = reinterpret_cast<float4 *>(&sums[warp][lane * 8]);
+    mine[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    mine[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
     __syncthreads();
     const int c = c0 + threadIdx.x;
     if (c >= P.N) continue;
@@ -331,8 +317,8 @@ sfnn_status sfnn_linear_backward(const sfnn_linear_desc *q, const void *slopes, 
     const bool vec = N % 8 == 0 && a16(dy) && lddy % 8 == 0;
     const dim3 grid((unsigned)((N + 255) / 256), (unsigned)std::min<int64_t>(row_blocks(T), 65535));
     auto run = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, P); };
-    if ((vec ? (bf16 ? run(k_linear_slopes<true, 8>) : run(k_linear_slopes<false, 8>))
-             : (bf16 ? run(k_linear_slopes<true, 1>) : run(k_linear_slopes<false, 1>))) != cudaSuccess)
+    if ((vec ? (bf16 ? run(k_linear_slopes<true, true>) : run(k_linear_slopes<false, true>))
+             : (bf16 ? run(k_linear_slopes<true, false>) : run(k_linear_slopes<false, false>))) != cudaSuccess)
       return SFNN_ERR_CUDA;
   }
   // dX and dW in one launch, the one with the longer tiles first
