@@ -7,7 +7,10 @@
 // in the tensor cores' type and its columns' sums over 32 rows, from its values before that rounding;
 // then dX and dW in one launch, which adds the sums up on its way.  Without an activation dY is dZ.
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
+#include "async.cuh"
 #include "common.cuh"
 #include "dense.cuh"
 #include "launch.cuh"
@@ -68,93 +71,116 @@ __global__ void __launch_bounds__(256) k_linear_join(const float *__restrict__ p
   }
 }
 
-// dZ from dY, and its columns' sums over 32 rows before it is rounded.  A CTA has 32 rows of 256
-// columns, a warp 4 rows of it, a lane 8 neighbouring columns; all that it reads is requested before the
-// first of it is used.  VEC: dY's rows start on 16 bytes (those of act' and dZ always do).  (Value by value
-// throughout, unrolled, 333 x 2047 took 9 us, most of it first fetches of its instructions.)
+// dZ from dY, and its columns' sums over blocks of rows before it is rounded.  A CTA has a block of 8
+// `per` rows and 256 columns, a warp `per` rows of it, a lane 8 neighbouring columns.  VEC: dY's rows start
+// on 16 bytes (those of act' and dZ always do); a lane's pieces of the next kAhead rows are then on their
+// way into shared memory, where nobody else reads them.  Else four rows are read at a time.
+// Bound by bytes.  (Rows in flight in registers instead: 4096 x 16384 bf16 with a ReLU's slopes 98 us.
+// Value by value, unrolled, 333 x 2047 took 9 us, most of it first fetches of its instructions.)
 struct SlopeParams {
   const void *dy;
   int64_t lddy;
-  int dy32, act, M, N;
+  int act, M, N, per;
   const void *slopes;
   void *dz;  // or null: dY is dZ.  Rows of N rounded up to 8
   int64_t lddz;
   float *colpart;  // or null
 };
-template <bool bf16, bool VEC>
+constexpr int kAhead = 6;
+constexpr int slope_piece(bool dy32) { return dy32 ? 48 : 32; }  // bytes of a lane's row: dY, act'
+constexpr size_t slope_smem(bool dy32, bool vec) { return vec ? (size_t)kAhead * 256 * slope_piece(dy32) : 0; }
+
+template <bool bf16, bool DY32, bool VEC>
 __global__ void __launch_bounds__(256) k_linear_slopes(const __grid_constant__ SlopeParams P) {
+  extern __shared__ __align__(16) unsigned char ahead[];
   __shared__ float sums[8][256];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = blockIdx.x * 256, col = c0 + lane * 8;
-  const int64_t slope_ld = slope_row_bytes(P.N, P.act);
-  for (int64_t block = blockIdx.y; block * 32 < P.M; block += gridDim.y) {
-    float sum[8] = {}, v[4][8];
-    uint4 code[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t row = block * 32 + warp * 4 + r;
-      const bool live = row < P.M && col < P.N;
-      const int64_t at = row * P.lddy + col;
+  const int64_t slope_ld = slope_row_bytes(P.N, P.act), rows = 8 * P.per;
+  constexpr int E = DY32 ? 4 : 2;
+  constexpr uint32_t kPlane = kAhead * 256 * 16;  // a 16-byte column of the pieces
+  const uint32_t own = smem_u32(ahead) + threadIdx.x * 16u;
+  const bool relu = P.act == SFNN_LINEAR_RELU, smooth = !relu && P.act != SFNN_LINEAR_NONE;
+  for (int64_t block = blockIdx.y; block * rows < P.M; block += gridDim.y) {
+    float sum[8] = {};
+    const int64_t row0 = block * rows + (int64_t)warp * P.per;
+    const int live = col < P.N ? (int)max((int64_t)0, min((int64_t)P.per, P.M - row0)) : 0;
+    const unsigned char *dy = static_cast<const unsigned char *>(P.dy) + (row0 * P.lddy + col) * E;
+    const unsigned char *slopes = static_cast<const unsigned char *>(P.slopes) + row0 * slope_ld + (relu ? col >> 5 << 2 : col * 2);
+    uint16_t *dz = static_cast<uint16_t *>(P.dz) + row0 * P.lddz + col;
+    auto request = [&](int r) {
+      if (VEC && r < live) {
+        const uint32_t to = own + (uint32_t)(r % kAhead) * (256u * 16u);
+        const unsigned char *d = dy + r * P.lddy * E, *s = slopes + r * slope_ld;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(d) : "memory");
+        if (DY32) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + kPlane), "l"(d + 16) : "memory");
+        if (relu) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + (DY32 ? 2 : 1) * kPlane), "l"(s) : "memory");
+        if (smooth) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (DY32 ? 2 : 1) * kPlane), "l"(s) : "memory");
+      }
+      cp_async_commit();
+    };
+    if (VEC)
+#pragma unroll 1
+      for (int r = 0; r < kAhead - 1; ++r) request(r);
+#pragma unroll(VEC ? 1 : 4)
+    for (int r = 0; r < live; ++r) {
+      float v[8];
+      uint4 code = make_uint4(0, 0, 0, 0);
       if (VEC) {
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (live && P.dy32) {
-          a = ld_stream(static_cast<const float *>(P.dy) + at);
-          b = ld_stream(static_cast<const float *>(P.dy) + at + 4);
-        } else if (live) {
-          a = ld_stream(static_cast<const uint16_t *>(P.dy) + at);
-        }
-        if (P.dy32) {
-          v[r][0] = __uint_as_float(a.x), v[r][1] = __uint_as_float(a.y), v[r][2] = __uint_as_float(a.z);
-          v[r][3] = __uint_as_float(a.w), v[r][4] = __uint_as_float(b.x), v[r][5] = __uint_as_float(b.y);
-          v[r][6] = __uint_as_float(b.z), v[r][7] = __uint_as_float(b.w);
-        } else {
-          const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+        request(r + kAhead - 1);
+        cp_async_wait<kAhead - 1>();
+        const uint32_t at = own + (uint32_t)(r % kAhead) * (256u * 16u);
+        uint4 a, b = code;
+        auto lds = [](uint32_t p) {
+          uint4 w;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(p) : "memory");
+          return w;
+        };
+        a = lds(at);
+        if (DY32) b = lds(at + kPlane);
+        if (relu || smooth) code = lds(at + (DY32 ? 2 : 1) * kPlane);
+        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+          if (DY32) {
+            v[i] = __uint_as_float(u[i]), v[4 + i] = __uint_as_float(u[4 + i]);
+          } else {
             const float2 f = unpack16(u[i], bf16);
-            v[r][2 * i] = f.x, v[r][2 * i + 1] = f.y;
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
           }
         }
       } else {
+        const unsigned char *d = dy + r * P.lddy * E, *s = slopes + r * slope_ld;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool there = live && col + j < P.N;
-          v[r][j] = !there ? 0.f : P.dy32 ? static_cast<const float *>(P.dy)[at + j] : load16(P.dy, at + j, bf16);
-        }
+        for (int j = 0; j < 8; ++j)
+          v[j] = col + j >= P.N ? 0.f : DY32 ? reinterpret_cast<const float *>(d)[j] : load16(d, j, bf16);
+        if (relu) code.x = __ldg(reinterpret_cast<const uint32_t *>(s));
+        if (smooth) code = ld_stream(s);
       }
-      code[r] = make_uint4(0, 0, 0, 0);
-      const unsigned char *s = static_cast<const unsigned char *>(P.slopes) + row * slope_ld;
-      if (live && P.act == SFNN_LINEAR_RELU)
-        code[r].x = (uint32_t)__ldg(s + (col >> 3));
-      else if (live && P.act != SFNN_LINEAR_NONE)
-        code[r] = ld_stream(s + (int64_t)col * 2);
-    }
+      if (relu) {
+        const uint32_t on = code.x >> (col & 31);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t row = block * 32 + warp * 4 + r;
-      if (P.act == SFNN_LINEAR_RELU) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[r][j] = code[r].x >> j & 1u ? v[r][j] : 0.f;
-      } else if (P.act != SFNN_LINEAR_NONE) {
-        const uint32_t u[4] = {code[r].x, code[r].y, code[r].z, code[r].w};
+        for (int j = 0; j < 8; ++j) v[j] = on >> j & 1u ? v[j] : 0.f;
+      } else if (smooth) {
+        const uint32_t u[4] = {code.x, code.y, code.z, code.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          v[r][2 * j] *= slope_value(u[j] & 0xffffu);
-          v[r][2 * j + 1] *= slope_value(u[j] >> 16);
+          v[2 * j] *= slope_value(u[j] & 0xffffu);
+          v[2 * j + 1] *= slope_value(u[j] >> 16);
         }
         if (!VEC)  // (codes past the row are anything)
 #pragma unroll
-          for (int j = 1; j < 8; ++j) v[r][j] = col + j < P.N ? v[r][j] : 0.f;
+          for (int j = 1; j < 8; ++j) v[j] = col + j < P.N ? v[j] : 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += v[r][j];
-      if (P.dz && row < P.M && col < P.N)
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.dz) + row * P.lddz + col) =
-            make_uint4(pack16(v[r][0], v[r][1], bf16), pack16(v[r][2], v[r][3], bf16), pack16(v[r][4], v[r][5], bf16),
-                       pack16(v[r][6], v[r][7], bf16));
+      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      if (P.dz)
+        *reinterpret_cast<uint4 *>(dz + r * P.lddz) =
+            make_uint4(pack16(v[0], v[1], bf16), pack16(v[2], v[3], bf16), pack16(v[4], v[5], bf16), pack16(v[6], v[7], bf16));
     }
+    if (VEC) cp_async_wait<0>();
     if (!P.colpart) continue;
     __syncthreads();  // the block before has been added up
     float4 *mine = reinterpret_cast<float4 *>(&sums[warp][lane * 8]);
@@ -169,10 +195,19 @@ __global__ void __launch_bounds__(256) k_linear_slopes(const __grid_constant__ S
     P.colpart[block * P.N + c] = total;
   }
 }
+template <bool bf16, bool DY32, bool VEC>
+cudaError_t launch_slopes(const SlopeParams &P, dim3 grid, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  constexpr size_t smem = slope_smem(DY32, VEC);
+  const cudaError_t e = smem ? allow_smem(k_linear_slopes<bf16, DY32, VEC>, smem, ready) : cudaSuccess;
+  return e != cudaSuccess ? e : launch_pdl(k_linear_slopes<bf16, DY32, VEC>, grid, dim3(256), smem, s, P);
+}
 
 // ---------------------------------------------------------------- host
 constexpr int kMaxWidth = 1 << 20;
-int64_t row_blocks(int64_t T) { return (T + 31) / 32; }
+int64_t row_blocks(int64_t T) { return (T + 31) / 32; }  // at most
+// Rows of a warp in k_linear_slopes: 4, or 16 where blocks of 128 rows still fill the SMs.
+int slope_rows(int64_t T, int64_t N, int sms) { return (T + 127) / 128 * ((N + 255) / 256) >= 4 * sms ? 16 : 4; }
 
 sfnn_status check(const sfnn_linear_desc *q) {
   if (!q || q->T < 0 || q->K < 1 || q->N < 1) return SFNN_ERR_INVALID_ARG;
@@ -302,11 +337,11 @@ sfnn_status sfnn_linear_backward(const sfnn_linear_desc *q, const void *slopes, 
   const bool as_is = q->act == SFNN_LINEAR_NONE && q->y_dtype == q->dtype && mat_ok(dy, lddy, N);
   Operand dz{dy, lddy, false};
   if (!as_is) dz = Operand{w, up(N, 8), false};
+  int blocks = 0;
   if (db || (!as_is && (dx || dw))) {
     SlopeParams P{};
     P.dy = dy;
     P.lddy = lddy;
-    P.dy32 = q->y_dtype == SFNN_F32;
     P.act = q->act;
     P.M = T;
     P.N = N;
@@ -315,10 +350,16 @@ sfnn_status sfnn_linear_backward(const sfnn_linear_desc *q, const void *slopes, 
     P.lddz = up(N, 8);
     P.colpart = db ? colpart : nullptr;
     const bool vec = N % 8 == 0 && a16(dy) && lddy % 8 == 0;
-    const dim3 grid((unsigned)((N + 255) / 256), (unsigned)std::min<int64_t>(row_blocks(T), 65535));
-    auto run = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, P); };
-    if ((vec ? (bf16 ? run(k_linear_slopes<true, true>) : run(k_linear_slopes<false, true>))
-             : (bf16 ? run(k_linear_slopes<true, false>) : run(k_linear_slopes<false, false>))) != cudaSuccess)
+    P.per = slope_rows(T, N, sms);
+    blocks = (T + 8 * P.per - 1) / (8 * P.per);
+    const dim3 grid((unsigned)((N + 255) / 256), (unsigned)std::min(blocks, 65535));
+    const bool wide = q->y_dtype == SFNN_F32;
+    auto of_type = [&](auto b16) {
+      constexpr bool B = decltype(b16)::value;
+      if (vec) return wide ? launch_slopes<B, true, true>(P, grid, s) : launch_slopes<B, false, true>(P, grid, s);
+      return wide ? launch_slopes<B, true, false>(P, grid, s) : launch_slopes<B, false, false>(P, grid, s);
+    };
+    if ((bf16 ? of_type(std::true_type{}) : of_type(std::false_type{})) != cudaSuccess)
       return SFNN_ERR_CUDA;
   }
   // dX and dW in one launch, the one with the longer tiles first
@@ -337,7 +378,6 @@ sfnn_status sfnn_linear_backward(const sfnn_linear_desc *q, const void *slopes, 
   };
   const bool x_first = chunks(N) / parts_of(T, K, chunks(N), sms) >= chunks(T) / parts_of(N, K, chunks(T), sms);
   if ((dx && x_first && !add_x()) || (dw && !add_w()) || (dx && !x_first && !add_x())) return SFNN_ERR_CUDA;
-  const int blocks = (int)row_blocks(T);
   if (!P.count) return !db || launch_colsum(colpart, blocks, N, bf16, db, s) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
   P.bf16 = bf16;
   P.err = err;
