@@ -315,7 +315,6 @@ cudaError_t launch_dense(DenseParams &P, int epi, int num_sms, cudaStream_t s);
 // The products of few tokens (slim.cu): out = x . w0^T, or with w1 the gated hidden layer
 // relu(x . w0^T + bias) * (x . w1^T).  K-major weights; `early`: w0 may be read while the
 // kernel launched before still runs (it waited for everything before it).
-// ... `end`: a linear layer's (never gated).
 struct SlimArgs {
   const void *x, *w0, *w1, *bias;
   int64_t ldx, ldw0, ldw1;
@@ -324,11 +323,30 @@ struct SlimArgs {
   void *out;
   int64_t ldo;
   int bf16, out32, early;
-  const LinearEnd *end;
   int32_t *err;
 };
 int64_t slim_cost(int T, int N, int64_t K, bool gated, int num_sms);
 sfnn_status launch_slim(const SlimArgs &q, int num_sms, cudaStream_t s);
+
+// The linear layer for few tokens (few.cu): weight rows of a tile, CTAs to a cluster, and the time it
+// should take in ns (INT64_MAX: more tokens than it takes).  `words`: a ReLU's slopes are kept.
+struct FewPlan {
+  int nb, split;
+  int64_t cost;
+};
+FewPlan few_plan(int T, int N, int64_t K, bool words, int sms);
+struct FewArgs {
+  const void *x, *w;
+  int64_t ldx, ldw;
+  int T, N;
+  int64_t K;
+  void *out;
+  int64_t ldo;
+  int bf16, out32;
+  const LinearEnd *end;
+  int32_t *err;
+};
+sfnn_status launch_few(const FewArgs &q, const FewPlan &plan, int sms, cudaStream_t s);
 
 // Rows of 16-bit values to act8 blocks and back (act8.cu).  Code rows are ldq bytes apart
 // (a multiple of 16, at least T's columns rounded up to 64), scale rows lds floats.

@@ -2,7 +2,7 @@
 //
 //     dZ = dY act'(Z),   dX = dZ W,   dW = dZ^T X,   db = sum over tokens of dZ,   dresidual = dY
 //
-// Forward: one product (dense.cu, or slim.cu for few tokens) whose epilogue does the rest; a K split
+// Forward: one product (dense.cu, or few.cu for few tokens) whose epilogue does the rest; a K split
 // over CTA pairs is joined by k_linear_join, which then does it.  Backward: k_linear_slopes makes dZ
 // in the tensor cores' type and its columns' sums over 32 rows, from its values before that rounding;
 // then dX and dW in one launch, which adds the sums up on its way.  Without an activation dY is dZ.
@@ -228,6 +228,14 @@ bool pieces(const void *p, int64_t ld, const sfnn_linear_desc *q) {
 }
 bool slopes_ok(const void *p) { return p && a16(p); }
 
+// The square tiles' time in ns for up to 256 tokens, fitted as few_plan's is (off by 8 % on average).
+int64_t dense_cost(int T, int N, int64_t K, int sms) {
+  const int split = parts_of(T, N, chunks(K), sms), rows = tile_columns(T, N, split, sms);
+  const int64_t units = (int64_t)((N + rows - 1) / rows) * split, pairs = sms / 2, rounds = (units + pairs - 1) / pairs;
+  return 3240 + rounds * (chunks(K) / split * (170000 + 989 * rows + 642 * T) / 1000 + 28 * (rows / 2 + 30)) +
+         (split > 1 ? 1930 : 0);
+}
+
 int64_t dz_bytes(int64_t T, int64_t N) { return up(T * up(N, 8) * 2, 256); }
 int64_t workspace(int64_t T, int64_t K, int64_t N, bool backward, int sms) {
   if (!backward) return parts_bytes(T, N, chunks(K), sms);
@@ -272,12 +280,14 @@ sfnn_status sfnn_linear_forward(const sfnn_linear_desc *q, const void *residual,
   end.slopes = slopes;
   end.vec_out = pieces(y, ldy, q);
   end.vec_res = residual && pieces(residual, ldr, q);
-  if (!slopes && slim_serves(T, N, q->K, false, sms)) {
-    SlimArgs a{};
+  // (at most 256 tokens)
+  const FewPlan few = few_plan(T, N, q->K, slopes && q->act == SFNN_LINEAR_RELU, sms);
+  if (T <= 256 && few.cost < dense_cost(T, N, q->K, sms)) {
+    FewArgs a{};
     a.x = q->x;
     a.ldx = q->ldx;
-    a.w0 = q->w;
-    a.ldw0 = q->ldw;
+    a.w = q->w;
+    a.ldw = q->ldw;
     a.T = T;
     a.N = N;
     a.K = q->K;
@@ -287,7 +297,7 @@ sfnn_status sfnn_linear_forward(const sfnn_linear_desc *q, const void *residual,
     a.out32 = out32;
     a.end = &end;
     a.err = err;
-    return launch_slim(a, sms, s);
+    return launch_few(a, few, sms, s);
   }
   DenseParams P{};
   P.count = 1;

@@ -44,11 +44,8 @@ struct alignas(64) SlimParams {
   const void *bias;
   void *out;
   int64_t ldo;
-  LinearEnd end;        // MODE kSlimLinear, and ...
-  int accs, acc_cols;   // its accumulators, chunks of K dealt to them in turn, and their columns
   int32_t *err;
 };
-enum SlimMode : int { kSlimPlain = 0, kSlimGated = 1, kSlimLinear = 2 };
 
 // This thread's weight row: its accumulators of tokens [t0, t0 + 8) -> out[t][col].  (The
 // epilogues go by eight tokens in a loop: unrolled further, a single token's few instructions
@@ -67,9 +64,8 @@ __device__ __forceinline__ void store_tokens(const SlimParams &P, int col, int t
   }
 }
 
-template <int MODE>
+template <bool GATED>
 __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimParams P) {
-  constexpr bool GATED = MODE == kSlimGated;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty, parts_in;
   __shared__ uint32_t tmem_slot;
@@ -165,7 +161,6 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
           break;
         }
         tm_fence_after();
-        int acc = 0, round = 0;  // the chunk's accumulator; whether it holds sums already
         for (int i = 0; i < steps; ++i, ++it) {
           const int s = it % stages, kn = min(P.kps, k_hi - (k_lo + i * P.kps));
           if (!bar_wait(&full[s], (uint32_t)((it / stages) & 1))) {
@@ -177,13 +172,11 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
             const uint32_t x = stage0 + (uint32_t)s * stage_bytes + (uint32_t)c * chunk_bytes, w = x + x_bytes;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const bool more = (MODE == kSlimLinear ? round > 0 : i > 0 || c > 0) || k > 0;
+              const uint32_t acc = (i > 0 || c > 0 || k > 0) ? 1u : 0u;
               const uint64_t dx = mat_desc(x + k * 32, 16, 1024);
-              const uint32_t d = tmem + (MODE == kSlimLinear ? (uint32_t)(acc * P.acc_cols) : 0u);
-              mma_16<1>(d, mat_desc(w + k * 32, 16, 1024), dx, idesc, more);
-              if (GATED) mma_16<1>(tmem + (uint32_t)P.up_col, mat_desc(w + w_bytes + k * 32, 16, 1024), dx, idesc, more);
+              mma_16<1>(tmem, mat_desc(w + k * 32, 16, 1024), dx, idesc, acc);
+              if (GATED) mma_16<1>(tmem + (uint32_t)P.up_col, mat_desc(w + w_bytes + k * 32, 16, 1024), dx, idesc, acc);
             }
-            if (MODE == kSlimLinear && ++acc == P.accs) acc = 0, round = 1;
           }
           mma_commit(&empty[s]);
         }
@@ -199,22 +192,7 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
   const bool busy = worker && quad * (P.m64 ? 16 : 32) < P.nb;
   auto load_bias = [&](int t) {
     const int col = t * P.nb + row;
-    const void *b = MODE == kSlimLinear ? P.end.bias : P.bias;
-    return MODE != kSlimPlain && b && row < P.nb && col < P.N ? load16(b, col, P.bf16) : 0.f;
-  };
-  // 8 tokens' sums of this thread's weight row
-  auto sums8 = [&](uint32_t at, uint32_t g[8]) {
-    __syncwarp();
-    tm_ld8(at, g);
-    if (MODE == kSlimLinear)
-#pragma unroll 1
-      for (int a = 1; a < P.accs; ++a) {
-        uint32_t h[8];
-        tm_ld8(at + (uint32_t)(a * P.acc_cols), h);
-        tm_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = __float_as_uint(__uint_as_float(g[i]) + __uint_as_float(h[i]));
-      }
+    return GATED && P.bias && row < P.nb && col < P.N ? load16(P.bias, col, P.bf16) : 0.f;
   };
   // the epilogue of this thread's weight row, with the other parts of a split tile at `sums`
   auto epilogue = [&](int t, float bias, const float *sums) {
@@ -223,16 +201,9 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
 #pragma unroll 1
     for (int c = 0; c < P.T; c += 8) {
       uint32_t g[8], u[8];
-      float v[8], res[8];
-      if (MODE == kSlimLinear)  // on its way while the accumulators are read
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int64_t at = (int64_t)(c + i) * P.end.ldres + col;
-          res[i] = !P.end.res || !live || c + i >= P.T ? 0.f
-                   : P.out32                           ? static_cast<const float *>(P.end.res)[at]
-                                                       : load16(P.end.res, at, P.bf16);
-        }
-      sums8(lanes + c, g);
+      float v[8];
+      __syncwarp();
+      tm_ld8(lanes + c, g);
       if (GATED) tm_ld8(lanes + (uint32_t)P.up_col + c, u);
       tm_wait_ld();
       if (!live) continue;
@@ -255,8 +226,6 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
           v[i] = v[i] < 0.f ? 0.f : v[i];
           v[i] *= __uint_as_float(u[i]);
         }
-        uint32_t code;
-        if (MODE == kSlimLinear) v[i] = act_value(v[i] + bias, P.end.act, false, code) + res[i];
       }
       store_tokens(P, col, c, v);
     }
@@ -295,7 +264,8 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
 #pragma unroll 1
           for (int c = 0; c < P.T; c += 8) {
             uint32_t g[8];
-            sums8(lanes + (uint32_t)(p * P.up_col + c), g);
+            __syncwarp();
+            tm_ld8(lanes + (uint32_t)(p * P.up_col + c), g);
             tm_wait_ld();
             const uint32_t dst = dst0 + (uint32_t)(p * P.T + c) * 512u;
 #pragma unroll
@@ -328,10 +298,10 @@ __global__ void __launch_bounds__(kThreads) k_slim(const __grid_constant__ SlimP
 
 int up_to(int v, int to) { return (v + to - 1) / to * to; }
 
-template <int MODE>
+template <bool GATED>
 cudaError_t launch(SlimParams &P, int grid, size_t smem, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t attr = allow_smem(k_slim<MODE>, 224 * 1024, ready);
+  const cudaError_t attr = allow_smem(k_slim<GATED>, 224 * 1024, ready);
   if (attr != cudaSuccess) return attr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -347,7 +317,7 @@ cudaError_t launch(SlimParams &P, int grid, size_t smem, cudaStream_t s) {
   attrs[1].val.clusterDim.z = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = P.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_slim<MODE>, P);
+  return cudaLaunchKernelEx(&cfg, k_slim<GATED>, P);
 }
 
 // Clusters of `split` CTAs, one CTA to an SM, that the device runs at a time (a cluster lies
@@ -360,7 +330,7 @@ int active_clusters(int split) {
   int n = slot.load(std::memory_order_relaxed);
   if (n) return n;
   static std::atomic<uint64_t> ready{0};
-  if (allow_smem(k_slim<kSlimPlain>, 224 * 1024, ready) != cudaSuccess) return 0;
+  if (allow_smem(k_slim<false>, 224 * 1024, ready) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(split * 64);
   cfg.blockDim = dim3(kThreads);
@@ -371,7 +341,7 @@ int active_clusters(int split) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, k_slim<kSlimPlain>, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, k_slim<false>, &cfg) != cudaSuccess) return 0;
   slot.store(n, std::memory_order_relaxed);
   return n;
 }
@@ -425,13 +395,8 @@ sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
   P.m64 = P.split == 1 && P.nb <= 64;
   P.tiles = (q.N + P.nb - 1) / P.nb;
   P.up_col = gated ? up_to(P.t16, 32) : 0;  // tensor memory is read 32 columns at a time
-  P.accs = 1;
-  P.acc_cols = up_to(P.t16, 32);
-  // an fp32 result: no more than 64 sums of the tensor cores (which cut off, see dense.cu) in one
-  // accumulator, as far as tensor memory goes
-  if (q.end && q.out32) P.accs = std::max(1, std::min({P.nk / P.split, (P.nk / P.split + 15) / 16, 512 / P.acc_cols}));
   P.tmem_cols = 32;
-  while (P.tmem_cols < (gated ? 2 : P.accs) * P.acc_cols) P.tmem_cols *= 2;
+  while (P.tmem_cols < P.up_col + up_to(P.t16, 32)) P.tmem_cols *= 2;
   const int chunk = (P.t8 + np * P.nb8) * 128;
   const int over = std::max(0, (P.m64 ? 8192 : 16384) - P.nb8 * 128);  // an MMA reads all its lanes' rows
   // All of shared memory in flight (timed in turn: 1 token, 4096 x 11008, 54.6 us; with 131 and 83
@@ -456,10 +421,7 @@ sfnn_status launch_slim(const SlimArgs &q, int sms, cudaStream_t s) {
       (gated && !make_tensor_map(&P.w1, q.w1, 2, q.N, q.K, q.ldw1, P.nb, 64, true)))
     return SFNN_ERR_CUDA;
   const int grid = P.split > 1 ? P.tiles * P.split : std::min(P.tiles, sms);
-  if (q.end) P.end = *q.end;
-  const cudaError_t e = gated   ? launch<kSlimGated>(P, grid, smem, s)
-                        : q.end ? launch<kSlimLinear>(P, grid, smem, s)
-                                : launch<kSlimPlain>(P, grid, smem, s);
+  const cudaError_t e = gated ? launch<true>(P, grid, smem, s) : launch<false>(P, grid, smem, s);
   return e == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
 }
 
