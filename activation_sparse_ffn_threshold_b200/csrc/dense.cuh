@@ -328,11 +328,11 @@ struct SlimArgs {
 int64_t slim_cost(int T, int N, int64_t K, bool gated, int num_sms);
 sfnn_status launch_slim(const SlimArgs &q, int num_sms, cudaStream_t s);
 
-// The linear layer for few tokens (few.cu): weight rows of a tile, CTAs to a cluster, and the time it
-// should take in ns (INT64_MAX: more tokens than it takes).  `words`: a ReLU's slopes are kept.
+// The linear layer for few tokens (few.cu): weight rows and tokens of a tile, CTAs to a cluster, and the time it
+// should take in ns (1e30: it does not take the product).  `words`: a ReLU's slopes are kept.
 struct FewPlan {
-  int nb, split;
-  int64_t cost;
+  int nb, tn, split;
+  double cost;
 };
 FewPlan few_plan(int T, int N, int64_t K, bool words, int sms);
 struct FewArgs {

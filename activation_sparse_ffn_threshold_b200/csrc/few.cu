@@ -1,13 +1,19 @@
-// few.cu -- the linear layer for few tokens (up to 256; the rule is few_plan's cost against the square
+// few.cu -- the linear layer for few tokens (up to 1024; the rule is few_plan's cost against the square
 // tiles of dense.cu, in linear.cu).
 //
 // What bounds it is the weights' bytes, and after them the tokens', which every CTA reads beside its
 // weights.  So the weights lie on the MMA's M side, up to 256 rows a CTA (two M = 128 products that share
-// the tokens' chunk in shared memory), the tokens on its N side, and K is split over the CTAs of a cluster
-// so that few wide tiles still fill the SMs.  The ranks then exchange their sums through distributed
-// shared memory, each taking a share of the tokens, adds them in rank order and stores it -- the work at
-// the end is split too.  A tile need not fill the 128 lanes: the rest of the A tile is whatever shared
-// memory holds, and only reaches accumulator lanes nobody reads.
+// the tokens' chunk in shared memory), the tokens on its N side, whose width goes by 16, and K is split over
+// the CTAs of a cluster so that few wide tiles still fill the SMs.  The ranks then exchange their sums
+// through distributed shared memory, each taking a share of the tokens, adds them in rank order and stores
+// it -- the work at the end is split too.  A tile need not fill the 128 lanes: the rest of the A tile is
+// whatever shared memory holds, and only reaches accumulator lanes nobody reads.  More tokens than 256 are
+// tiles of their own, which read the same weights beside one another, through the L2.
+//
+// Measured (fp16, bias; the weights from memory): 4096 x 16384 1 token 26 us and 64 tokens 30 (the weights'
+// bytes alone 20.5), 28672 x 7168 50 tokens onto fp32 82 (63), 4096 x 4096 1 token 12, 128 tokens 14 and
+// 512 tokens 28 (a library's product 14, 10 and 15: its tiles share loads across SMs, these read the L2 at 11.7
+// bytes a ns and exchange sums at the 15 bytes a clock of an SM's way to its cluster), 1024 x 1024 256 tokens 7.
 //
 // Sums that leave as fp32 are dealt to several accumulators (see kSegment in dense.cu).
 #include <algorithm>
@@ -24,16 +30,20 @@ constexpr int kThreads = 320;  // warp 0 loads, warp 1 issues the MMAs, warps 2-
 constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;
 constexpr int kRows = 256;     // weight rows of a tile, at most
+constexpr int kTokens = 256;   // and tokens
+constexpr int kMostTokens = 1024;
 constexpr int kBudget = 200 * 1024;
 constexpr int kApart = 40 * 1024;      // up to this, the exchange has memory of its own
 constexpr int kExchange = 224 * 1024;  // and this is the most it may have
+constexpr int kMostSmem = 226 * 1024;
 
 struct alignas(64) FewParams {
   CUtensorMap x, w;
   int T, N, nk;        // nk: 64-deep chunks of K
-  int nb, nb8, tiles;  // weight rows of a tile; rounded up to 8
+  int nb, nb8;         // weight rows of a tile; rounded up to 8
   int halves;          // of 128 rows
-  int t8, t16;         // T rounded up to 8 (rows loaded), to 16 (MMA N)
+  int t8, t16;         // tokens of a tile, eights (rows loaded); rounded up to 16 (MMA N)
+  int tt, tiles;       // tiles of tokens, which lie side by side for each tile of weight rows; tiles in all
   int kps, stages;     // chunks a stage
   int split, share;    // CTAs of a cluster that share a tile's K; tokens that each of them ends
   int apart;           // the exchange's memory lies behind the stages (else in them)
@@ -93,8 +103,8 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
           bar_expect_tx(&full[s], (x_bytes + (uint32_t)P.nb * 128u) * (uint32_t)kn);
           const uint32_t at = stage0 + (uint32_t)s * stage_bytes;
           for (int c = 0; c < kn; ++c)
-            tma_load_2d(at + (uint32_t)c * chunk_bytes + x_bytes, &P.w, (k0 + c) * 64, t * P.nb, &full[s]);
-          for (int c = 0; c < kn; ++c) tma_load_2d(at + (uint32_t)c * chunk_bytes, &P.x, (k0 + c) * 64, 0, &full[s]);
+            tma_load_2d(at + (uint32_t)c * chunk_bytes + x_bytes, &P.w, (k0 + c) * 64, t / P.tt * P.nb, &full[s]);
+          for (int c = 0; c < kn; ++c) tma_load_2d(at + (uint32_t)c * chunk_bytes, &P.x, (k0 + c) * 64, t % P.tt * P.t8, &full[s]);
         }
       for (int s = 0; s < P.stages && ok; ++s) {  // every load has been consumed before the CTA ends
         const int j = it - P.stages + s;
@@ -144,28 +154,32 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
   const int quad = warp & 3, set = (warp - 2) >> 2;
   const int half = P.halves > 1 ? set : 0;            // this warp's rows ...
   const int row = half * 128 + quad * 32 + lane;
-  const int turn = P.halves > 1 ? 8 : 16, first = P.halves > 1 ? 0 : set * 8;  // ... and its eights of tokens
+  const int turn = P.halves > 1 ? 16 : 32, first = P.halves > 1 ? 0 : set * 16;  // ... and its sixteens of tokens
   const bool busy = worker && half * 128 + quad * 32 < P.nb;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * P.accs * P.acc_cols);
-  // eight tokens' sums of this thread's weight row
-  auto sums8 = [&](int t, uint32_t g[8]) {
+  const int row_slots = P.halves * 128;
+  // sums of this thread's weight row: tokens [t, t + 8) of its tile and, if `more`, the next eight
+  auto sums = [&](int t, bool more, uint32_t g[16]) {
     __syncwarp();
     tm_ld8(lanes + (uint32_t)t, g);
+    if (more) tm_ld8(lanes + (uint32_t)t + 8, g + 8);
 #pragma unroll 1
     for (int a = 1; a < P.accs; ++a) {
-      uint32_t h[8];
+      uint32_t h[16];
       tm_ld8(lanes + (uint32_t)(a * P.acc_cols + t), h);
+      if (more) tm_ld8(lanes + (uint32_t)(a * P.acc_cols + t) + 8, h + 8);
       tm_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = __float_as_uint(__uint_as_float(g[i]) + __uint_as_float(h[i]));
+      for (int i = 0; i < 16; ++i)
+        if (i < 8 || more) g[i] = __float_as_uint(__uint_as_float(g[i]) + __uint_as_float(h[i]));
     }
     tm_wait_ld();
   };
-  const int row_slots = P.halves * 128;
-  // The tokens [lo, hi) of tile t; `parts`: the other ranks' sums of them.  (With each choice made value
-  // by value this was 67 instructions a value, and 40 us of 48 at 256 tokens, 200 x 20000.)
+  // The tokens [lo, hi) of tile t; `parts`: the other ranks' sums of them, [4 tokens][row][4].
+  // (With each choice made value by value this was 67 instructions a value, and 40 us of 48 at 256 tokens,
+  // 200 x 20000; eight tokens at a time 600 clocks for 140 instructions, most of it waiting.)
   auto finish = [&](int t, int lo, int hi, const float *parts) {
-    const int col = t * P.nb + row;
+    const int col = t / P.tt * P.nb + row, t0 = t % P.tt * P.t8;
     const bool live = row < P.nb && col < P.N;
     const LinearEnd &E = P.end;
     const float bias = E.bias && live ? load16(E.bias, col, BF16) : 0.f;
@@ -173,84 +187,91 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
     const bool res = E.res && live;
 #pragma unroll 1
     for (int c = lo + first; c < hi; c += turn) {
-      const int n = min(8, hi - c);
-      float v[8], r[8];
+      const int n = min(16, hi - c);
+      float v[16], r[16];
       if (res) {  // on its way while the accumulators are read
-        const int64_t at = (int64_t)c * E.ldres + col;
+        const int64_t at = (int64_t)(t0 + c) * E.ldres + col;
         if (P.out32) {
           const float *q = static_cast<const float *>(E.res) + at;
 #pragma unroll
-          for (int i = 0; i < 8; ++i, q += E.ldres) r[i] = i < n ? *q : 0.f;
+          for (int i = 0; i < 16; ++i, q += E.ldres) r[i] = i < n ? *q : 0.f;
         } else {
           const uint16_t *q = static_cast<const uint16_t *>(E.res) + at;
 #pragma unroll
-          for (int i = 0; i < 8; ++i, q += E.ldres) r[i] = i < n ? load16(q, 0, BF16) : 0.f;
+          for (int i = 0; i < 16; ++i, q += E.ldres) r[i] = i < n ? load16(q, 0, BF16) : 0.f;
         }
       }
-      uint32_t g[8];
-      sums8(c, g);
+      uint32_t g[16];
+      sums(c, n > 8, g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(g[i]);
+      for (int i = 0; i < 16; ++i) v[i] = i < 8 || n > 8 ? __uint_as_float(g[i]) : 0.f;
       if (parts) {
-        float own[8];
+        float own[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) own[i] = v[i], v[i] = 0.f;
-        const float *from = parts + (size_t)(c - lo) * row_slots + row;
+        for (int i = 0; i < 16; ++i) own[i] = v[i], v[i] = 0.f;
+        const float4 *from = reinterpret_cast<const float4 *>(parts) + (size_t)((c - lo) >> 2) * row_slots + row;
 #pragma unroll 1
         for (int p = 0; p < split; ++p) {
           if (p == rank) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += own[i];
+            for (int i = 0; i < 16; ++i) v[i] += own[i];
             continue;
           }
-          const float *q = from;
 #pragma unroll
-          for (int i = 0; i < 8; ++i, q += row_slots) v[i] += *q;  // (tokens past the last: whatever is there)
-          from += (size_t)P.share * row_slots;
+          for (int i = 0; i < 4; ++i)
+            if (i < 2 || n > 8) {  // (tokens past the last of an eight: whatever is there)
+              const float4 f = from[i * row_slots];
+              v[4 * i] += f.x, v[4 * i + 1] += f.y, v[4 * i + 2] += f.z, v[4 * i + 3] += f.w;
+            }
+          from += (size_t)(P.share >> 2) * row_slots;
         }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += bias;
+      for (int i = 0; i < 16; ++i) v[i] += bias;
       if (act == SFNN_LINEAR_RELU) {
         if (E.slopes) {  // nb is a multiple of 32 then: a warp's columns are a word
-          unsigned char *s = static_cast<unsigned char *>(E.slopes) + c * slope_row_bytes(P.N, act) + (col >> 5) * 4;
+          unsigned char *s = static_cast<unsigned char *>(E.slopes) + (t0 + c) * slope_row_bytes(P.N, act) + (col >> 5) * 4;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 16; ++i) {
             const uint32_t word = __ballot_sync(0xffffffffu, live && !(v[i] <= 0.f));
             if (lane == 0 && live && i < n) *reinterpret_cast<uint32_t *>(s + i * slope_row_bytes(P.N, act)) = word;
           }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = max_nan(v[i], 0.f);
+        for (int i = 0; i < 16; ++i) v[i] = max_nan(v[i], 0.f);
       } else if (act != SFNN_LINEAR_NONE) {
-        uint32_t code[8];
+        uint32_t code[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], act, E.slopes != nullptr, code[i]);
+        for (int i = 0; i < 16; ++i) v[i] = act_value(v[i], act, E.slopes != nullptr, code[i]);
         if (E.slopes && live) {
-          unsigned char *s = static_cast<unsigned char *>(E.slopes) + c * slope_row_bytes(P.N, act) + (int64_t)col * 2;
+          unsigned char *s = static_cast<unsigned char *>(E.slopes) + (t0 + c) * slope_row_bytes(P.N, act) + (int64_t)col * 2;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 16; ++i)
             if (i < n) *reinterpret_cast<uint16_t *>(s + i * slope_row_bytes(P.N, act)) = (uint16_t)code[i];
         }
       }
       if (res)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
+        for (int i = 0; i < 16; ++i) v[i] += r[i];
       if (!live) continue;
-      const int64_t at = (int64_t)c * P.ldo + col;
+      const int64_t at = (int64_t)(t0 + c) * P.ldo + col;
       if (P.out32) {
         float *o = static_cast<float *>(P.out) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i, o += P.ldo)
+        for (int i = 0; i < 16; ++i, o += P.ldo)
           if (i < n) *o = v[i];
       } else {
         uint16_t *o = static_cast<uint16_t *>(P.out) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i, o += P.ldo)
-          if (i < n) *o = (uint16_t)pack16(v[i], 0.f, BF16);
+        for (int i = 0; i < 16; i += 2, o += 2 * P.ldo) {
+          const uint32_t two = pack16(v[i], v[i + 1], BF16);
+          if (i < n) *o = (uint16_t)two;
+          if (i + 1 < n) o[P.ldo] = (uint16_t)(two >> 16);
+        }
       }
     }
   };
+  auto tokens = [&](int t) { return min(P.t8, P.T - t % P.tt * P.t8); };
   bool ok = true;
   if (worker) {
     pdl_wait();  // nothing is written, nor the residual read, before the kernel before has finished
@@ -264,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
       __syncwarp();
       tm_fence_after();
       if (split > 1) break;  // one tile per cluster, joined below
-      if (busy) finish(t, 0, P.T, nullptr);
+      if (busy) finish(t, 0, tokens(t), nullptr);
       tm_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_cluster_relaxed(cluster_addr(&acc_empty, 0));
@@ -276,19 +297,23 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
     const uint32_t place = stage0 - raw + (P.apart ? (uint32_t)P.stages * stage_bytes : 0u);
     if (!P.apart) cluster_sync_all();  // no load or MMA touches the stages any more, in any CTA
     if (worker && busy && ok) {
+      const int count = tokens(unit);
 #pragma unroll 1
       for (int j = 1; j < split; ++j) {
-        const int q = (rank + j) % split, lo = q * P.share, hi = min(P.T, lo + P.share);
+        const int q = (rank + j) % split, lo = q * P.share, hi = min(count, lo + P.share);
         const uint32_t dst = cluster_addr(smem_raw, (uint32_t)q) + place +
-                             (uint32_t)(((rank < q ? rank : rank - 1) * P.share * row_slots + row) * 4);
+                             (uint32_t)((rank < q ? rank : rank - 1) * (P.share >> 2) * row_slots + row) * 16u;
 #pragma unroll 1
         for (int c = lo + first; c < hi; c += turn) {
-          uint32_t g[8];
-          sums8(c, g);
+          const bool more = hi - c > 8;
+          uint32_t g[16];
+          sums(c, more, g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c + i < hi)
-              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + (uint32_t)((c + i - lo) * row_slots * 4)), "r"(g[i])
+          for (int i = 0; i < 4; ++i)
+            if (i < 2 || more)
+              asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               dst + (uint32_t)((((c - lo) >> 2) + i) * row_slots) * 16u),
+                           "r"(g[4 * i]), "r"(g[4 * i + 1]), "r"(g[4 * i + 2]), "r"(g[4 * i + 3])
                            : "memory");
         }
       }
@@ -296,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
     __syncwarp();
     cluster_sync_all();  // (also: no CTA ends while another still writes to it)
     if (worker && busy && ok && unit < P.tiles) {
-      const int lo = rank * P.share, hi = min(P.T, lo + P.share);
+      const int lo = rank * P.share, hi = min(tokens(unit), lo + P.share);
       finish(unit, lo, hi, reinterpret_cast<const float *>(smem_raw + place));
     }
   }
@@ -310,6 +335,13 @@ int up_to(int v, int to) { return (v + to - 1) / to * to; }
 // Tokens that a rank ends: whole eights, as tensor memory is read.
 int share_of(int T, int split) { return up_to((T + split - 1) / split, 8); }
 
+// One limit for every launch: set again, a lower one would take back the higher.
+template <bool BF16>
+cudaError_t allow() {
+  static std::atomic<uint64_t> ready{0};
+  return allow_smem(k_few<BF16>, kMostSmem, ready);
+}
+
 // Clusters of `split` CTAs, one CTA to an SM, that the device runs at a time (a cluster lies within one
 // GPC).  0: the query failed.
 int active_clusters(int split, int sms) {
@@ -320,8 +352,7 @@ int active_clusters(int split, int sms) {
   std::atomic<int> &slot = known[dev][split];
   int n = slot.load(std::memory_order_relaxed);
   if (n) return n;
-  static std::atomic<uint64_t> ready{0};
-  if (allow_smem(k_few<false>, 224 * 1024, ready) != cudaSuccess) return 0;
+  if (allow<false>() != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(split * 64);
   cfg.blockDim = dim3(kThreads);
@@ -339,31 +370,46 @@ int active_clusters(int split, int sms) {
 
 }  // namespace
 
-// The shape with the least time (ns) of 1, 2, 4 and 8 CTAs to a cluster.  The time is a fit to 110 random
-// products of 1 to 256 tokens, 64 to 28672 wide either way, each with every split: a chunk of K costs its
-// weight rows, its tokens and its MMAs, whose times add up more than they overlap while the chunks in
-// flight bound the rate; then the exchange, and the end by tokens.  It is off by 6 % on average, and the
-// choice, dense.cu's tiles among its options (linear.cu), takes 1.2 % longer than the best.
+// The shape with the least time (ns) of 1, 2, 4 and 8 CTAs to a cluster and a few widths of the tiles of
+// tokens.  The time is a fit to 255 products of 1 to 1024 tokens, 64 to 28672 wide either way, each in every
+// shape (off by 5 % on average; the shape it takes is 0.8 % slower than the best of them, the square tiles
+// among them, at most 15 %).  A chunk of K costs the longest of one CTA's pace, the weights' bytes from memory
+// and all bytes through the L2 (5.5 and 11.7 bytes a ns of all CTAs); then come the end by tokens and the
+// exchange.  No one shape does for all: 4096 x 4096, 8 tokens, takes 21, 14 and 12 us with 1, 2 and 4 CTAs,
+// 4096 x 16384 27 us with 1 and none wider than 2 fits; 256 tokens of 2048 x 8192 take 19 us as two tiles,
+// 257 of 4096 x 12288 43 as three.  Against the square tiles: 257 tokens of 2048 x 2048 12 us to 15, of 4096
+// x 12288 43 to 54, 400 of 4096 x 16384 60 to 58.  More than 1024 tokens are not looked at: there the square
+// tiles, which read each byte for more products, lose by little at most (1000 of 1024 x 1024: 10 us to 14).
 FewPlan few_plan(int T, int N, int64_t K, bool words, int sms) {
   FewPlan best{};
-  best.cost = INT64_MAX;
-  if (T > 256) return best;
-  const int nk = (int)((K + 63) / 64), t16 = up_to(T, 16);
+  best.cost = 1e30;
+  if (T > kMostTokens) return best;
+  const int nk = (int)((K + 63) / 64), least = (T + kTokens - 1) / kTokens;
   for (int split = 1; split <= kMaxSplit; split *= 2) {
     if (split > 1 && nk < 2 * split) break;
     const int clusters = active_clusters(split, sms);
     if (clusters < 1) continue;
-    const int64_t rounds = ((int64_t)N + clusters * kRows - 1) / (clusters * kRows);
-    if (rounds > 1 && split > 1) continue;
-    FewPlan p;
-    p.split = split;
-    p.nb = std::max(16, up_to((int)((N + clusters * rounds - 1) / (clusters * rounds)), words ? 32 : 8));
-    if (p.nb > kRows) continue;
-    const int64_t chunks = (nk + split - 1) / split, share = share_of(T, split), wide = p.nb > 128 ? 2 : 1;
-    if ((split - 1) * share * wide * 512 > kExchange) continue;
-    p.cost = 3250 + rounds * chunks * (202000 + 2185 * p.nb + 315 * T + 538 * wide * t16) / 1000 + rounds * share * 20 * wide +
-             (split > 1 ? 625 + 182 * split + 12 * T * wide : 0);
-    if (p.cost < best.cost) best = p;
+    for (int want = least; want <= 2 * least + 2; ++want) {
+      FewPlan p;
+      p.split = split;
+      p.tn = up_to((T + want - 1) / want, 8);
+      const int tt = (T + p.tn - 1) / p.tn;
+      if (tt < want) break;
+      const int64_t rounds = ((int64_t)tt * ((N + kRows - 1) / kRows) + clusters - 1) / clusters;
+      if (rounds > 1 && split > 1) continue;
+      const int64_t wide_tiles = std::max<int64_t>(1, clusters * rounds / tt);
+      p.nb = std::max(16, up_to((int)((N + wide_tiles - 1) / wide_tiles), words ? 32 : 8));
+      if (p.nb > kRows) continue;
+      const int share = share_of(p.tn, split), halves = p.nb > 128 ? 2 : 1;
+      if ((split - 1) * share * halves * 512 > kExchange) continue;
+      const double tiles = (double)((N + p.nb - 1) / p.nb) * tt, ctas = std::min<double>(tiles * split, sms);
+      const double weights = std::max(1., ctas / tt / split) * split * p.nb;  // rows of a chunk that differ
+      const double chunk = std::max({232 + 0.869 * p.nb + 0.718 * halves * up_to(p.tn, 16), weights * 128 / 5480,
+                                     ctas * (p.nb + p.tn) * 128 / 11700});
+      p.cost = 3640 + rounds * (((nk + split - 1) / split) * chunk + 15.2 * share * halves) +
+               (split > 1 ? 432 + 284 * split + 13.6 * p.tn * halves : 0);
+      if (p.cost < best.cost) best = p;
+    }
   }
   return best;
 }
@@ -375,12 +421,13 @@ sfnn_status launch_few(const FewArgs &q, const FewPlan &plan, int sms, cudaStrea
   P.nk = (int)((q.K + 63) / 64);
   P.nb = plan.nb;
   P.nb8 = up_to(P.nb, 8);
-  P.tiles = (q.N + P.nb - 1) / P.nb;
   P.halves = P.nb > 128 ? 2 : 1;
-  P.t8 = up_to(q.T, 8);
-  P.t16 = up_to(q.T, 16);
+  P.t8 = plan.tn;
+  P.t16 = up_to(P.t8, 16);
+  P.tt = (q.T + P.t8 - 1) / P.t8;
+  P.tiles = (q.N + P.nb - 1) / P.nb * P.tt;
   P.split = plan.split;
-  P.share = share_of(q.T, P.split);
+  P.share = share_of(P.t8, P.split);
   P.acc_cols = up_to(P.t16, 32);
   P.accs = 1;
   // an fp32 result: no more than 64 sums of the tensor cores in one accumulator, as far as tensor memory goes
@@ -393,11 +440,16 @@ sfnn_status launch_few(const FewArgs &q, const FewPlan &plan, int sms, cudaStrea
   const int parts = (P.split - 1) * P.share * P.halves * 512;
   P.apart = parts <= kApart;
   // four chunks of every row at a time, 512 contiguous bytes of it, or as many as leave three stages
-  // (28672 x 7168, one token: 120 us a chunk at a time, 82 with two, 69 with four)
+  // (28672 x 7168, one token: 120 us a chunk at a time, 82 with two, 69 with four; two where the work has
+  // no second stage of four: no faster, 1024 x 1024 5.7 -> 6.1)
   const int room = kBudget - over - (P.apart ? parts : 0);
   P.kps = 4;
   while (P.kps > 1 && (P.kps > 2 ? 3 : 2) * P.kps * chunk > room) --P.kps;
-  P.stages = std::max(2, std::min(kMaxStages, room / (P.kps * chunk)));
+  // No more stages than the work fills: what is left is the next launch's, whose CTAs then get ready beside
+  // these (in a row of launches, 1 token: 2048 x 2048 7.4 -> 6.9 us, 512 x 2048 5.9 -> 5.3).
+  const int rounds = P.split > 1 ? 1 : (P.tiles + sms - 1) / sms;
+  const int loads = rounds * ((P.nk + P.split * P.kps - 1) / (P.split * P.kps));
+  P.stages = std::max(1, std::min({kMaxStages, room / (P.kps * chunk), loads}));
   const int stage_mem = P.stages * P.kps * chunk;
   const size_t smem = 1024 + std::max(stage_mem + std::max(over, P.apart ? parts : 0), parts);
   P.bf16 = q.bf16;
@@ -409,9 +461,7 @@ sfnn_status launch_few(const FewArgs &q, const FewPlan &plan, int sms, cudaStrea
   if (!make_tensor_map(&P.x, q.x, 2, q.T, q.K, q.ldx, P.t8, 64, true) ||
       !make_tensor_map(&P.w, q.w, 2, q.N, q.K, q.ldw, P.nb, 64, true))
     return SFNN_ERR_CUDA;
-  static std::atomic<uint64_t> ready[2];
-  auto kernel = P.bf16 ? k_few<true> : k_few<false>;
-  if (smem > 226 * 1024 || allow_smem(kernel, 226 * 1024, ready[P.bf16]) != cudaSuccess) return SFNN_ERR_CUDA;
+  if (smem > kMostSmem || (P.bf16 ? allow<true>() : allow<false>()) != cudaSuccess) return SFNN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(P.split > 1 ? P.tiles * P.split : std::min(P.tiles, sms)));
   cfg.blockDim = dim3(kThreads);
@@ -425,7 +475,7 @@ sfnn_status launch_few(const FewArgs &q, const FewPlan &plan, int sms, cudaStrea
   attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = P.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, P.bf16 ? k_few<true> : k_few<false>, P) == cudaSuccess ? SFNN_OK : SFNN_ERR_CUDA;
 }
 
 }  // namespace sfnn

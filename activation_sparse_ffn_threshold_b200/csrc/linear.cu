@@ -228,12 +228,13 @@ bool pieces(const void *p, int64_t ld, const sfnn_linear_desc *q) {
 }
 bool slopes_ok(const void *p) { return p && a16(p); }
 
-// The square tiles' time in ns for up to 256 tokens, fitted as few_plan's is (off by 8 % on average).
-int64_t dense_cost(int T, int N, int64_t K, int sms) {
+// The square tiles' time in ns, fitted to the products that few_plan's is fitted to (off by 6 % on average).
+double dense_cost(int T, int N, int64_t K, int sms) {
   const int split = parts_of(T, N, chunks(K), sms), rows = tile_columns(T, N, split, sms);
-  const int64_t units = (int64_t)((N + rows - 1) / rows) * split, pairs = sms / 2, rounds = (units + pairs - 1) / pairs;
-  return 3240 + rounds * (chunks(K) / split * (170000 + 989 * rows + 642 * T) / 1000 + 28 * (rows / 2 + 30)) +
-         (split > 1 ? 1930 : 0);
+  const int64_t units = (int64_t)((N + rows - 1) / rows) * ((T + 255) / 256) * split, pairs = sms / 2;
+  const int64_t rounds = (units + pairs - 1) / pairs;
+  return 2820 + rounds * (chunks(K) / split * (245 + 0.528 * rows) + 32.3 * (rows / 2 + 30)) +
+         (split > 1 ? 2130 + 1.28e-3 * split * T * N : 0);
 }
 
 int64_t dz_bytes(int64_t T, int64_t N) { return up(T * up(N, 8) * 2, 256); }
@@ -280,9 +281,8 @@ sfnn_status sfnn_linear_forward(const sfnn_linear_desc *q, const void *residual,
   end.slopes = slopes;
   end.vec_out = pieces(y, ldy, q);
   end.vec_res = residual && pieces(residual, ldr, q);
-  // (at most 256 tokens)
   const FewPlan few = few_plan(T, N, q->K, slopes && q->act == SFNN_LINEAR_RELU, sms);
-  if (T <= 256 && few.cost < dense_cost(T, N, q->K, sms)) {
+  if (few.cost < dense_cost(T, N, q->K, sms)) {
     FewArgs a{};
     a.x = q->x;
     a.ldx = q->ldx;

@@ -257,3 +257,42 @@ def test_graphs_and_streams(T):
         for out in outs:
             assert all(torch.equal(u, v) for u, v in zip(out, step()))
     assert sf.dense_error() == 0
+
+
+# Few tokens: 1, 2, 4 and 8 CTAs to a tile's K, one and two halves of 128 weight rows, one tile of tokens and
+# several, one round of tiles and more, the exchange in memory of its own and in the stages', ragged ends.
+FEW = [(3, 8, 3977), (13, 48, 1434), (85, 568, 1), (831, 24, 7510), (3, 96, 19009), (327, 8, 18255), (275, 304, 27645),
+       (80, 16, 10328), (310, 8, 25612), (196, 1776, 5647), (8, 624, 1961), (321, 1576, 3157), (852, 1384, 1664),
+       (35, 624, 1246), (83, 2208, 10924), (269, 2016, 6115), (104, 1840, 2083), (193, 1208, 1603), (971, 816, 40),
+       (212, 520, 3), (35, 2856, 5591), (269, 3512, 3363), (167, 1704, 2414), (65, 3968, 937), (1, 4600, 101),
+       (144, 3656, 679), (569, 3880, 6), (1, 6328, 2095), (264, 9144, 1697), (187, 7128, 957), (1024, 1024, 1000)]
+
+
+@pytest.mark.parametrize("T,K,N", FEW)
+def test_few_tokens(T, K, N):
+    for j in range(4):
+        i = T + K + N + j
+        check(T, K, N, KINDS[j % 2], ACTS[i % 4], res=["f32", None, "same"][i % 3], bias=i % 5 != 0, seed=i)
+
+
+def test_few_tokens_leave_the_rows_beside_them():
+    """Rows past the last token and columns past the last are as they were, residual in place."""
+    for T, K, N in [(9, 640, 131), (300, 1024, 515), (33, 4096, 1030)]:
+        x, w, b, _, _ = make(T, K, N, torch.float16, "relu", seed=T)
+        for dt in (torch.float16, torch.float32):
+            frame = torch.full((T + 3, N + 5), 3.0, device="cuda", dtype=dt)
+            y = frame[1:T + 1, 2:N + 2]
+            want, extra, *_ = forward64(x, w, b, "relu", y)
+            sf.linear_forward(x, w, b, "relu", y, out=y)
+            near(y, want, extra)
+            edge = frame.clone()
+            edge[1:T + 1, 2:N + 2] = 3.0
+            assert torch.equal(edge, torch.full_like(edge, 3.0))
+
+
+def test_few_tokens_of_products_in_turn():
+    """A product's launch does not depend on those before it in the process, short K and long."""
+    for T, K, N in [(5, 64, 77), (250, 8192, 3500), (6, 160, 3404), (250, 28672, 3800), (2, 1688, 597), (250, 12448, 4487)]:
+        x, w, b, _, _ = make(T, K, N, torch.bfloat16, "none", seed=K)
+        want, extra, *_ = forward64(x, w, b, "none", None)
+        near(sf.linear_forward(x, w, b)[0], want, extra)
