@@ -18,6 +18,7 @@
 // Sums that leave as fp32 are dealt to several accumulators (see kSegment in dense.cu).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "dense.cuh"
@@ -178,7 +179,8 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
   // The tokens [lo, hi) of tile t; `parts`: the other ranks' sums of them, [4 tokens][row][4].
   // (With each choice made value by value this was 67 instructions a value, and 40 us of 48 at 256 tokens,
   // 200 x 20000; eight tokens at a time 600 clocks for 140 instructions, most of it waiting.)
-  auto finish = [&](int t, int lo, int hi, const float *parts) {
+  auto finish_by = [&](auto by, int t, int lo, int hi, const float *parts) {
+    constexpr int G = decltype(by)::value;
     const int col = t / P.tt * P.nb + row, t0 = t % P.tt * P.t8;
     const bool live = row < P.nb && col < P.N;
     const LinearEnd &E = P.end;
@@ -187,38 +189,38 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
     const bool res = E.res && live;
 #pragma unroll 1
     for (int c = lo + first; c < hi; c += turn) {
-      const int n = min(16, hi - c);
-      float v[16], r[16];
+      const int n = min(G, hi - c);
+      float v[G], r[G];
       if (res) {  // on its way while the accumulators are read
         const int64_t at = (int64_t)(t0 + c) * E.ldres + col;
         if (P.out32) {
           const float *q = static_cast<const float *>(E.res) + at;
 #pragma unroll
-          for (int i = 0; i < 16; ++i, q += E.ldres) r[i] = i < n ? *q : 0.f;
+          for (int i = 0; i < G; ++i, q += E.ldres) r[i] = i < n ? *q : 0.f;
         } else {
           const uint16_t *q = static_cast<const uint16_t *>(E.res) + at;
 #pragma unroll
-          for (int i = 0; i < 16; ++i, q += E.ldres) r[i] = i < n ? load16(q, 0, BF16) : 0.f;
+          for (int i = 0; i < G; ++i, q += E.ldres) r[i] = i < n ? load16(q, 0, BF16) : 0.f;
         }
       }
       uint32_t g[16];
       sums(c, n > 8, g);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = i < 8 || n > 8 ? __uint_as_float(g[i]) : 0.f;
+      for (int i = 0; i < G; ++i) v[i] = i < 8 || n > 8 ? __uint_as_float(g[i]) : 0.f;
       if (parts) {
-        float own[16];
+        float own[G];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) own[i] = v[i], v[i] = 0.f;
+        for (int i = 0; i < G; ++i) own[i] = v[i], v[i] = 0.f;
         const float4 *from = reinterpret_cast<const float4 *>(parts) + (size_t)((c - lo) >> 2) * row_slots + row;
 #pragma unroll 1
         for (int p = 0; p < split; ++p) {
           if (p == rank) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] += own[i];
+            for (int i = 0; i < G; ++i) v[i] += own[i];
             continue;
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < G / 4; ++i)
             if (i < 2 || n > 8) {  // (tokens past the last of an eight: whatever is there)
               const float4 f = from[i * row_slots];
               v[4 * i] += f.x, v[4 * i + 1] += f.y, v[4 * i + 2] += f.z, v[4 * i + 3] += f.w;
@@ -227,49 +229,54 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
         }
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] += bias;
+      for (int i = 0; i < G; ++i) v[i] += bias;
       if (act == SFNN_LINEAR_RELU) {
         if (E.slopes) {  // nb is a multiple of 32 then: a warp's columns are a word
           unsigned char *s = static_cast<unsigned char *>(E.slopes) + (t0 + c) * slope_row_bytes(P.N, act) + (col >> 5) * 4;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < G; ++i) {
             const uint32_t word = __ballot_sync(0xffffffffu, live && !(v[i] <= 0.f));
             if (lane == 0 && live && i < n) *reinterpret_cast<uint32_t *>(s + i * slope_row_bytes(P.N, act)) = word;
           }
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = max_nan(v[i], 0.f);
+        for (int i = 0; i < G; ++i) v[i] = max_nan(v[i], 0.f);
       } else if (act != SFNN_LINEAR_NONE) {
-        uint32_t code[16];
+        uint32_t code[G];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = act_value(v[i], act, E.slopes != nullptr, code[i]);
+        for (int i = 0; i < G; ++i) v[i] = act_value(v[i], act, E.slopes != nullptr, code[i]);
         if (E.slopes && live) {
           unsigned char *s = static_cast<unsigned char *>(E.slopes) + (t0 + c) * slope_row_bytes(P.N, act) + (int64_t)col * 2;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
+          for (int i = 0; i < G; ++i)
             if (i < n) *reinterpret_cast<uint16_t *>(s + i * slope_row_bytes(P.N, act)) = (uint16_t)code[i];
         }
       }
       if (res)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] += r[i];
+        for (int i = 0; i < G; ++i) v[i] += r[i];
       if (!live) continue;
       const int64_t at = (int64_t)(t0 + c) * P.ldo + col;
       if (P.out32) {
         float *o = static_cast<float *>(P.out) + at;
 #pragma unroll
-        for (int i = 0; i < 16; ++i, o += P.ldo)
+        for (int i = 0; i < G; ++i, o += P.ldo)
           if (i < n) *o = v[i];
       } else {
         uint16_t *o = static_cast<uint16_t *>(P.out) + at;
 #pragma unroll
-        for (int i = 0; i < 16; i += 2, o += 2 * P.ldo) {
+        for (int i = 0; i < G; i += 2, o += 2 * P.ldo) {
           const uint32_t two = pack16(v[i], v[i + 1], BF16);
           if (i < n) *o = (uint16_t)two;
           if (i + 1 < n) o[P.ldo] = (uint16_t)(two >> 16);
         }
       }
     }
+  };
+  auto finish = [&](int t, int lo, int hi, const float *parts) {
+    // (eight at a time for one token: gelu 27.8 us with sixteens, 27.0 so, of 4096 x 16384)
+    if (P.t8 > 8) finish_by(std::integral_constant<int, 16>{}, t, lo, hi, parts);
+    else finish_by(std::integral_constant<int, 8>{}, t, lo, hi, parts);
   };
   auto tokens = [&](int t) { return min(P.t8, P.T - t % P.tt * P.t8); };
   bool ok = true;
