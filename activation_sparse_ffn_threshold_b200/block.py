@@ -85,8 +85,9 @@ def linear_forward(x, w, b=None, act=None, residual=None, out_dtype=None, save=F
 
     x [..., K], w [N, K], b [N] or None in fp16 or bf16, K a multiple of 8 and rows 16-byte aligned;
     ``act``: None, "relu", "gelu" (z Phi(z)) or "silu".  y [..., N] has the residual's type, x's or
-    fp32, or without one ``out_dtype`` (default: x's).  ``out`` takes y and may be the residual itself;
-    ``saved`` (with ``save``) goes to linear_backward."""
+    fp32, or without one ``out_dtype`` (default: x's).  ``out`` takes y, and may be the residual
+    itself but share no memory with another input; ``saved`` (with ``save``) goes to
+    linear_backward."""
     kind = ACTS.get(act, -1)
     if kind < 0:
         raise ValueError("act must be None, 'relu', 'gelu' or 'silu'")
@@ -156,7 +157,7 @@ def residual_norm_forward(x, z=None, pre="rms", w=None, b=None, post="none", pos
     fp16 or bf16 (h's type: ``dtype``, by default the weights' or the inputs') or fp32; ``pre`` and
     ``post`` are "none", "rms" or "layer", with weights and biases [d] or None; gate is [d], of x's
     shape, or None.  r has x's type, h is None without ``pre``.  ``out`` takes r, and may be x itself
-    unless ``save``; ``saved`` goes to residual_norm_backward."""
+    unless ``save`` but share no memory with another input; ``saved`` goes to residual_norm_backward."""
     options = _norm_options(pre, post, residual_scale, branch_scale, eps)
     r, h, stats, dtype = _call(stream, x, "norm_forward", "sfnn_norm_forward", x, z, gate, w, b, post_w, post_b, *options,
                                dtype, save, out, _err(x))
@@ -215,7 +216,7 @@ def clip_grad_norm(grads, max_norm, scale=1.0, out=None, eps=1e-6, stream=None):
     """The norm of all ``grads`` together times ``scale``, as an fp32 tensor of no dimension; the
     gradients become g * scale * min(1, max_norm / (norm + eps)) in place, or in the tensors ``out``.
 
-    grads: CUDA tensors of fp16, bf16 or fp32 in any mix, dense in memory, none twice; ``scale``
+    grads: CUDA tensors of fp16, bf16 or fp32 in any mix, dense in memory, no memory written twice; ``scale``
     takes a loss scale back out; max_norm = inf leaves them but for ``scale``.  A norm that is not
     finite is returned as it is (an infinite one makes the gradients 0 or NaN, a NaN all of them
     NaN): nothing waits for the device here."""

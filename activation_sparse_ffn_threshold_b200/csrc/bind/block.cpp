@@ -112,6 +112,22 @@ void *channels(const at::Tensor *t, const char *name, int64_t d, at::ScalarType 
            (long long)d);
   return t->data_ptr();
 }
+// Whether two sets of rows of `ea` and `eb` bytes a value share memory.  Rows equally far apart may lie
+// between one another (columns of one buffer); others whose ranges meet count as sharing it.
+bool share(const Rows &a, int64_t ea, const Rows &b, int64_t eb) {
+  if (!a.rows || !a.cols || !b.rows || !b.cols) return false;
+  const int64_t la = a.ld * ea, lb = b.ld * eb, ca = a.cols * ea, cb = b.cols * eb;
+  const int64_t pa = reinterpret_cast<int64_t>(a.p), pb = reinterpret_cast<int64_t>(b.p);
+  if (pa + (a.rows - 1) * la + ca <= pb || pb + (b.rows - 1) * lb + cb <= pa) return false;
+  const int64_t ld = a.rows > 1 ? la : lb;
+  if (a.rows > 1 && b.rows > 1 && la != lb) return true;
+  const int64_t off = ((pb - pa) % ld + ld) % ld;  // b's columns, from a's on
+  return off < ca || off + cb > ld;
+}
+void apart(const Rows &out, int64_t eo, const at::Tensor *t, const char *name) {
+  if (!t) return;
+  if (share(out, eo, rows_of(*t, name), t->element_size())) refuse(PyExc_ValueError, "out must not overlap %s", name);
+}
 void same_shape(const at::Tensor &t, const char *name, at::IntArrayRef shape) {
   if (t.sizes() != shape)
     refuse(PyExc_ValueError, "%s must have the shape %s, got %s", name, shape_text(shape).c_str(), shape_text(t.sizes()).c_str());
@@ -167,7 +183,11 @@ long whole(PyObject *o) {
   if (v == -1 && PyErr_Occurred()) throw python_error();
   return v;
 }
-bool truth(PyObject *o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject *o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v == 1;
+}
 at::ScalarType dtype_of(PyObject *o) {
   if (!THPDtype_Check(o)) refuse(PyExc_TypeError, "a dtype was expected, not %s", Py_TYPE(o)->tp_name);
   return reinterpret_cast<THPDtype *>(o)->scalar_type;
@@ -234,6 +254,11 @@ PyObject *linear_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   at::Tensor y, slopes, ws;
   if (out) {
     ry = output(*out, "out", shape, dt, device);
+    const int64_t size = out->element_size();
+    apart(ry, size, &x, "x");
+    apart(ry, size, &w, "w");
+    apart(ry, size, b, "b");
+    if (!res || r.p != ry.p || r.ld != ry.ld) apart(ry, size, res, "the residual");  // (it may be the residual)
     y = *out;
   } else {
     y = empty(shape, dt, device);
@@ -368,6 +393,14 @@ PyObject *norm_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     r = values(*out, "out", dtype, *t.x, &code);
     if (code != q.x_dtype) refuse(PyExc_ValueError, "out must be a tensor of x's type on its device");
     if (save && r.p == q.x) refuse(PyExc_ValueError, "x is needed by the backward pass: out must not be x");
+    const int64_t size = out->element_size();
+    if (r.p != q.x || r.ld != q.ldx) apart(r, size, t.x, "x but for x itself");
+    apart(r, size, t.z, "z");
+    apart(r, size, t.gate, "gate");
+    apart(r, size, t.w, "w");
+    apart(r, size, t.b, "b");
+    apart(r, size, t.post_w, "post_w");
+    apart(r, size, t.post_b, "post_b");
   }
   const c10::cuda::CUDAGuard guard(device);
   at::Tensor made, h, stats;

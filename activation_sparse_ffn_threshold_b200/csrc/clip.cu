@@ -7,7 +7,8 @@
 // alone) and multiplies its share of the values.  The tensors' table travels in the kernels'
 // parameters, so nothing is copied to the device and a captured call holds its own table.
 //
-// Bound by bytes: each value is read twice and written once.
+// Bound by bytes: each value is read twice and written once.  Measured: 1.08 GB in 20 bf16
+// tensors, into others, 515 us (the bytes 496), 270 MB 126; the squares alone 169 for 1.08 GB (6.4 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <new>

@@ -151,6 +151,8 @@ struct Place {
 
 // ---------------------------------------------------------------- forward
 // NV vectors of V values a thread, a row to `threads` threads of a CTA (CLUSTER: of all the cluster's).
+// Bound by latency at the few rows it serves: loads, then a chain of sums.  1 x 4096 fp32, RMS: 4 us in a
+// row of launches, 5.6 with the call.
 template <bool bf16, int V, int NV, bool CLUSTER>
 __global__ void __launch_bounds__(256, 2) k_norm_forward(const __grid_constant__ NormParams P, int threads) {
   __shared__ float2 slots[2 * RowSum<CLUSTER>::kSlots];

@@ -617,8 +617,8 @@ SFNN_API sfnn_status sfnn_linear_backward(const sfnn_linear_desc *q, const void 
  * b and gate are fp16 or bf16 (dtype), X and Z of that type or fp32, R and dR, dX of X's type, dZ of
  * Z's.  Sums and norms are fp32; H is formed from R before its rounding.
  * d up to 32768, any row stride of at least d, T up to 2^28; T = 0 is valid.  Rows that all start on 16
- * bytes with d a multiple of 8 are read by vectors.  err as for sfnn_gated_forward.  R may be X (the same rows), else nothing that is
- * written may overlap anything else.
+ * bytes with d a multiple of 8 are read by vectors.  err as for sfnn_gated_forward.  R may be X (the
+ * same rows), else nothing that is written may overlap anything else.
  */
 typedef enum { SFNN_NORM_NONE = 0, SFNN_NORM_RMS = 1, SFNN_NORM_LAYER = 2 } sfnn_norm;
 typedef struct {

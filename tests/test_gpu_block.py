@@ -475,3 +475,19 @@ def test_clip_in_a_graph_and_on_another_stream():
     n2 = sf.clip_grad_norm(g, 1.0, out=other, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(n, n2) and all(torch.equal(u, v) for u, v in zip(out, other))
+
+
+def test_out_that_shares_memory():
+    d = 64
+    buf = torch.randn(9, 3 * d, device="cuda").half()
+    x, z, w = buf[:8, :d], buf[:8, d:2 * d], torch.ones(d, device="cuda").half()
+    want = sf.residual_norm_forward(x, z, "rms", w)
+    beside = sf.residual_norm_forward(x, z, "rms", w, out=buf[:8, 2 * d:])  # between the rows of x and z
+    assert torch.equal(want[0], beside[0]) and torch.equal(want[1], beside[1])
+    for out in (z, buf[1:, :d], buf[:8, 8:d + 8], buf[:8, d - 8:2 * d - 8]):
+        with pytest.raises(ValueError, match="overlap"):
+            sf.residual_norm_forward(x, z, "rms", w, out=out)
+    with pytest.raises(ValueError, match="overlap"):
+        sf.residual_norm_forward(x[:1], z[:1], "rms", w, out=w[None])
+    inside = sf.residual_norm_forward(x, z, "rms", w, out=x)
+    assert torch.equal(want[0], inside[0]) and torch.equal(want[1], inside[1])

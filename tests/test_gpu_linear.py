@@ -296,3 +296,22 @@ def test_few_tokens_of_products_in_turn():
         x, w, b, _, _ = make(T, K, N, torch.bfloat16, "none", seed=K)
         want, extra, *_ = forward64(x, w, b, "none", None)
         near(sf.linear_forward(x, w, b)[0], want, extra)
+
+
+def test_out_that_shares_memory():
+    x = torch.randn(6, 64, device="cuda").half()
+    w = torch.randn(64, 64, device="cuda").half()
+    b = torch.randn(64, device="cuda").half()
+    buf = torch.zeros(7, 192, device="cuda", dtype=torch.float16)
+    left, right, late = buf[:6, :64], buf[:6, 64:128], buf[:6, 72:136]
+    left.copy_(x)
+    want = sf.linear_forward(x, w, b)[0]
+    assert torch.equal(sf.linear_forward(left, w, b, out=right)[0], want)  # side by side
+    for kw in (dict(x=x, out=x), dict(x=left, out=left), dict(x=left, out=buf[:6, 8:72]), dict(x=x, w=w, out=w[:6]),
+               dict(x=x[:1], b=b, out=b[None]), dict(x=x, residual=right, out=late), dict(x=x, residual=right, out=buf[1:, 64:128]),
+               dict(x=left, out=buf.view(-1)[:6 * 64].view(6, 64))):
+        kw = dict(w=w, b=None) | kw
+        with pytest.raises(ValueError, match="overlap"):
+            sf.linear_forward(**kw)
+    right.copy_(x)
+    assert torch.equal(sf.linear_forward(x, w, b, residual=right, out=right)[0], sf.linear_forward(x, w, b, residual=x)[0])
