@@ -277,6 +277,39 @@ __device__ __forceinline__ void epi_store(const DenseParams &P, const Unit &Q, u
   }
 }
 
+__device__ __forceinline__ void words32_out(uint32_t panel, const float *v, unsigned char *base, int64_t ld, int rows,
+                                            int cols) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = make_uint4(__float_as_uint(v[16 * h + 4 * j]), __float_as_uint(v[16 * h + 4 * j + 1]),
+                        __float_as_uint(v[16 * h + 4 * j + 2]), __float_as_uint(v[16 * h + 4 * j + 3]));
+    panel_out(panel + h * kPanel, w, base + 64 * h, ld, rows, (cols - 16 * h + 3) / 4);
+  }
+}
+
+// The same of a tall tile, whose sums are in registers (neither parts of K nor a hidden layer's ReLU).
+template <bool bf16, int width>
+__device__ __forceinline__ void epi_store_sums(const Unit &Q, int64_t row0, int n0, uint32_t panel, float (&sum)[width]) {
+  const int rows = (int)min((int64_t)32, Q.M - row0);
+  const int64_t ld = Q.ldo * (Q.out32 ? 4 : 2);
+  unsigned char *base = static_cast<unsigned char *>(Q.out) + row0 * ld;
+#pragma unroll
+  for (int c = 0; c < width; c += 32) {
+    const int cols = Q.N - (n0 + c);
+    if (rows <= 0 || cols <= 0) break;  // (the whole warp)
+    if (Q.out32) {
+      words32_out(panel, sum + c, base + (int64_t)(n0 + c) * 4, ld, rows, cols);
+    } else {
+      uint4 w[4];
+      pack32(w, sum + c, bf16);
+      panel_out(panel + ((c >> 5) & 1) * kPanel, w, base + (int64_t)(n0 + c) * 2, ld, rows, (cols + 7) / 8);
+    }
+  }
+}
+
 // The pair's tile holds 128 neurons: gate columns 0..127, up columns 128..255.  This
 // warp takes 64 of them from n0 on (one act8 block); its first panel holds their biases.
 template <bool bf16, class Done>
@@ -650,23 +683,20 @@ __device__ __forceinline__ void ragged_out(const Unit &Q, int64_t row0, int col,
       static_cast<uint16_t *>(Q.out)[i] = (uint16_t)pack16(f, 0.f, bf16);
   }
 }
-__device__ __forceinline__ void words32_out(uint32_t panel, const float *v, unsigned char *base, int64_t ld, int rows,
-                                            int cols) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint4 w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = make_uint4(__float_as_uint(v[16 * h + 4 * j]), __float_as_uint(v[16 * h + 4 * j + 1]),
-                        __float_as_uint(v[16 * h + 4 * j + 2]), __float_as_uint(v[16 * h + 4 * j + 3]));
-    panel_out(panel + h * kPanel, w, base + 64 * h, ld, rows, (cols - 16 * h + 3) / 4);
-  }
+// Two columns' biases to each of a piece's first 16 lanes (zeros past the last), requested a piece ahead and
+// handed round.  (A column's own to each lane is twice the shuffles: 1.5 us of a tile's 5; all of them read
+// by every lane 2.7.)
+__device__ __forceinline__ uint32_t bias_request(const LinearEnd &E, int col, int N) {
+  if (!E.bias) return 0u;
+  const uint16_t *p = static_cast<const uint16_t *>(E.bias);
+  const int c = col + 2 * ((int)threadIdx.x & 15);
+  return (c < N ? __ldg(p + c) : 0u) | (c + 1 < N ? (uint32_t)__ldg(p + c + 1) << 16 : 0u);
 }
 
 // One 32-column piece of the tile, whose sums are in v; `bits` of a ReLU's slopes for the caller to keep.
 template <bool bf16, int width, bool WIDE>
 __device__ __forceinline__ void linear32(const DenseParams &P, const Unit &Q, int64_t row0, int n0, int c, int rows,
-                                         uint32_t panel, ResPiece<WIDE> &piece, float *v, uint32_t &word) {
+                                         uint32_t panel, ResPiece<WIDE> &piece, uint32_t &bias, float *v, uint32_t &word) {
   const LinearEnd &E = P.end;
   const int lane = threadIdx.x & 31, col = n0 + c, cols = Q.N - col;
   if (Q.split > 1) {  // sums of a part of K, rows of N rounded up to 4
@@ -676,9 +706,12 @@ __device__ __forceinline__ void linear32(const DenseParams &P, const Unit &Q, in
     return;
   }
   if (E.bias) {
-    const float own = lane < cols ? load16(E.bias, col + lane, bf16) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, own, i);
+    for (int i = 0; i < 16; ++i) {
+      const float2 f = unpack16(__shfl_sync(0xffffffffu, bias, i), bf16);
+      v[2 * i] += f.x, v[2 * i + 1] += f.y;
+    }
+    if (c + 32 < width) bias = bias_request(E, col + 32, Q.N);
   }
   if (E.act == SFNN_LINEAR_RELU) {
     word = 0;
@@ -689,15 +722,14 @@ __device__ __forceinline__ void linear32(const DenseParams &P, const Unit &Q, in
     }
   } else if (E.act != SFNN_LINEAR_NONE) {
     uint32_t q[16];
-    const bool keep = E.slopes != nullptr;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      uint32_t lo = 0, hi = 0;
-      v[2 * i] = act_value(v[2 * i], E.act, keep, lo);
-      v[2 * i + 1] = act_value(v[2 * i + 1], E.act, keep, hi);
-      q[i] = __byte_perm(lo, hi, 0x5410);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t code[16];
+      act_values<16>(v + 16 * h, E.act, E.slopes != nullptr, code);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[8 * h + i] = __byte_perm(code[2 * i], code[2 * i + 1], 0x5410);
     }
-    if (keep) {
+    if (E.slopes) {
       uint4 w[4];
       words_to(w, q);
       const int64_t ld = slope_row_bytes(Q.N, E.act);
@@ -732,7 +764,7 @@ __device__ __forceinline__ void keep_bits(const DenseParams &P, const Unit &Q, i
 
 template <bool bf16, int width>
 __device__ __forceinline__ void epi_linear(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
-                                           uint32_t panel, ResPiece<false> &piece) {
+                                           uint32_t panel, ResPiece<false> &piece, uint32_t &bias) {
   const int rows = (int)min((int64_t)32, Q.M - row0);
   if (rows <= 0 || n0 >= Q.N) return;  // (the whole warp)
   uint32_t bits[width / 32] = {};
@@ -745,7 +777,7 @@ __device__ __forceinline__ void epi_linear(const DenseParams &P, const Unit &Q, 
     tm_wait_ld();
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
-    linear32<bf16, width, false>(P, Q, row0, n0, c, rows, panel, piece, v, word);
+    linear32<bf16, width, false>(P, Q, row0, n0, c, rows, panel, piece, bias, v, word);
 #pragma unroll
     for (int i = 0; i < width / 32; ++i)
       if (c == 32 * i) bits[i] = word;
@@ -758,24 +790,30 @@ __device__ __forceinline__ void epi_linear(const DenseParams &P, const Unit &Q, 
 // quarter of K in one sum).  So K is summed up in segments of kSegment chunks, each from zero, which
 // the epilogue's threads add up in registers while the next segment is multiplied.
 constexpr int kSegment = 16;
-template <bool bf16, int width>
-__device__ __forceinline__ void epi_linear32(const DenseParams &P, const Unit &Q, int64_t row0, int n0, uint32_t panel,
-                                             ResPiece<true> &piece, float (&sum)[width]) {
+template <bool bf16, int width, bool WIDE>
+__device__ __forceinline__ void epi_linear_sums(const DenseParams &P, const Unit &Q, int64_t row0, int n0, uint32_t panel,
+                                                ResPiece<WIDE> &piece, uint32_t &bias, float (&sum)[width]) {
   const int rows = (int)min((int64_t)32, Q.M - row0);
   if (rows <= 0 || n0 >= Q.N) return;  // (the whole warp)
   uint32_t bits[width / 32] = {};
 #pragma unroll
   for (int c = 0; c < width; c += 32)
-    if (n0 + c < Q.N) linear32<bf16, width, true>(P, Q, row0, n0, c, rows, panel, piece, sum + c, bits[c / 32]);
+    if (n0 + c < Q.N) linear32<bf16, width, WIDE>(P, Q, row0, n0, c, rows, panel, piece, bias, sum + c, bits[c / 32]);
   keep_bits<bf16, width>(P, Q, row0, n0, rows, bits);
 }
 
 // ---------------------------------------------------------------- the kernel
-template <int EPI, bool BF16, int TN>  // TN: columns of a tile
+// TN: columns of a tile.  TALL: two 256-row halves to a tile of 512, whose chunks share the B operand's: a
+// quarter less comes through the L2, which bounds the main loop of the others (4096 x 4096 -> 16384: 4.3 GB,
+// 11.1 TB/s).  Both halves' sums fill tensor memory, so the epilogue takes a half into registers, gives its
+// columns back, and works while the other half, or the next tile's first chunks, are multiplied: the first
+// half is a ring of chunks ahead of the second at a tile's start and end.
+template <int EPI, bool BF16, int TN, bool TALL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_dense(const __grid_constant__ DenseParams P) {
   constexpr bool kDGated = EPI == kEpiDGated || EPI == kEpiDGated8, kSegments = EPI == kEpiLinear32;
-  constexpr int kStages = kStagesOf<EPI>;
+  constexpr int kStages = TALL ? 4 : kStagesOf<EPI>, kRows = TALL ? 512 : kTile;
+  constexpr uint32_t kStageBytes = TALL ? 49152 : sfnn::kStageBytes;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
@@ -814,7 +852,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int n = 0; ok && id >= 0; ++n) {
         w = next;
         const CUtensorMap *a0 = &w.p->a0, *b0 = &w.p->b0, *a1 = &w.p->a1, *b1 = &w.p->b1;
-        const int m0 = w.pos.m * kTile + (int)rank * 128;
+        const int m0 = w.pos.m * kRows + (int)rank * 128;
         // gated: the first CTA loads 128 gate rows, the second the same 128 up rows
         const int n0 = EPI == kEpiGated ? w.pos.n * 128 : w.pos.n * TN + (int)rank * (TN / 2);
         for (int kc = w.k_lo; kc < w.k_hi; ++kc, ++it) {
@@ -827,9 +865,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (rank == 0) bar_expect_tx(&full[s], 2 * 16384u + (uint32_t)TN * 128u);
+          if (rank == 0) bar_expect_tx(&full[s], (TALL ? 4 : 2) * 16384u + (uint32_t)TN * 128u);
           const uint32_t bar = cluster_addr(&full[s], 0);
-          const uint32_t sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + 16384u;
+          const uint32_t sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + kStageBytes - 16384u;
           const bool second = kc >= w.nk0;
           const int k0 = (second ? kc - w.nk0 : kc) * 64;
           const CUtensorMap *ma = second ? a1 : a0;
@@ -837,8 +875,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (EPI == kEpiStore && w.a_mn) {
             tma_load_2d_pair(sa, ma, m0, k0, bar);
             tma_load_2d_pair(sa + 8192u, ma, m0 + 64, k0, bar);
+            if (TALL) {
+              tma_load_2d_pair(sa + 16384u, ma, m0 + 256, k0, bar);
+              tma_load_2d_pair(sa + 24576u, ma, m0 + 320, k0, bar);
+            }
           } else {
             tma_load_2d_pair(sa, ma, k0, m0, bar);
+            if (TALL) tma_load_2d_pair(sa + 16384u, ma, k0, m0 + 256, bar);
           }
           if (kDGated || (EPI == kEpiStore && w.b_mn)) {
             tma_load_2d_pair(sb, mb, n0, k0, bar);
@@ -871,6 +914,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // a 16-deep step of an operand: 2 KB of an MN-major tile, 32 bytes of a K-major one
         const uint32_t step_a = a_mn ? 2048u : 32u, step_b = b_mn ? 2048u : 32u;
         const uint32_t lbo_a = a_mn ? 8192u : 16u, lbo_b = b_mn ? 8192u : 16u;
+        if constexpr (TALL) {
+          // a chunk's MMAs into one half's sums
+          auto multiply = [&](int i, int h) {
+            const uint32_t sa = stage0 + (uint32_t)((it + i) % kStages) * kStageBytes, sb = sa + kStageBytes - 16384u;
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)
+              mma_16<2>(tmem + (uint32_t)h * 256u, mat_desc(sa + (uint32_t)h * 16384u + k * step_a, lbo_a, 1024),
+                        mat_desc(sb + k * step_b, lbo_b, 1024), idesc, (i > 0 || k > 0) ? 1u : 0u);
+          };
+          const int nk = w.k_hi - w.k_lo, head = min(kStages, nk), tail = min(kStages, nk - head), base = it;
+          auto there = [&](int i) {
+            const int j = base + i;
+            const bool got = bar_wait(&full[j % kStages], (uint32_t)((j / kStages) & 1));
+            tm_fence_after();
+            return got;
+          };
+          const uint32_t parity = (uint32_t)(n & 1) ^ 1u;
+          ok = bar_wait(&acc_empty[0], parity);
+          tm_fence_after();
+          for (int i = 0; ok && i < head; ++i) {
+            ok = there(i);
+            if (ok) multiply(i, 0);
+          }
+          id = walk.unit(n + 1);  // the next unit, while this one's MMAs run
+          next = unit_at(P, max(id, 0));
+          ok = ok && bar_wait(&acc_empty[1], parity);
+          tm_fence_after();
+          for (int i = 0; ok && i < nk - tail; ++i) {
+            if (i >= head) {
+              ok = there(i);
+              if (!ok) break;
+              multiply(i, 0);
+            }
+            multiply(i, 1);
+            mma_commit_pair(&empty[(base + i) % kStages]);
+          }
+          for (int i = nk - tail; ok && i < nk; ++i) {
+            ok = there(i);
+            if (ok) multiply(i, 0);
+          }
+          if (ok) {
+            mma_commit_pair(&acc_full[0]);
+            for (int i = nk - tail; i < nk; ++i) {
+              multiply(i, 1);
+              mma_commit_pair(&empty[(base + i) % kStages]);
+            }
+            mma_commit_pair(&acc_full[1]);
+          }
+          it += nk;
+          continue;
+        }
         for (int k_lo = w.k_lo, k_hi; ok && k_lo < w.k_hi; k_lo = k_hi, ++turn) {
           k_hi = kSegments ? min(k_lo + kSegment, w.k_hi) : w.k_hi;
           const int buf = turn & 1;
@@ -920,7 +1014,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int n = 0, id; (id = walk.unit(n)) >= 0; ++n) {
       const Unit w = unit_at(P, id);
       const int buf = n & 1;
-      const int64_t row0 = (int64_t)w.pos.m * kTile + rank * 128 + quad * 32;
+      int64_t row0 = (int64_t)w.pos.m * kRows + rank * 128 + quad * 32;
       constexpr int kWide = TN / 2;  // columns of this warp
       const int n0 = EPI == kEpiGated ? w.pos.n * 128 + half * 64 : w.pos.n * TN + half * kWide;
       // what the epilogue reads besides the accumulators, requested before they are there
@@ -935,8 +1029,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (kDGated) saved_request<EPI == kEpiDGated8>(P, w, row0, n0, panel + 2 * kPanel, scales);
       ResPiece<kSegments> piece;
-      if ((EPI == kEpiLinear || kSegments) && w.split == 1)
+      uint32_t bias = 0;
+      if ((EPI == kEpiLinear || kSegments) && w.split == 1) {
         res_request<kSegments>(P.end, w, row0, n0, (int)max((int64_t)0, min((int64_t)32, w.M - row0)), piece);
+        bias = bias_request(P.end, n0, w.N);
+      }
+      if constexpr (TALL) {
+        bool there = true;
+        for (int h = 0; h < 2; ++h, row0 += 256) {
+          if (EPI == kEpiLinear && h) {
+            res_request<kSegments>(P.end, w, row0, n0, (int)max((int64_t)0, min((int64_t)32, w.M - row0)), piece);
+            bias = bias_request(P.end, n0, w.N);
+          }
+          there = __all_sync(0xffffffffu, bar_wait(&acc_full[h], (uint32_t)(n & 1)));
+          if (!there) break;
+          __syncwarp();
+          tm_fence_after();
+          float sum[kWide];
+#pragma unroll
+          for (int c = 0; c < kWide; c += 32) {
+            uint32_t raw[32];
+            tm_ld32(tmem + lanes + (uint32_t)(h * 256 + half * kWide + c), raw);
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c + i] = __uint_as_float(raw[i]);
+          }
+          tm_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive_cluster_relaxed(cluster_addr(&acc_empty[h], 0));
+          if constexpr (EPI == kEpiLinear)
+            epi_linear_sums<BF16, kWide, false>(P, w, row0, n0, panel, piece, bias, sum);
+          else
+            epi_store_sums<BF16, kWide>(w, row0, n0, panel, sum);
+        }
+        if (!there) {
+          if (lane == 0) latch_error(P.err, kErrTimeout);
+          break;
+        }
+        continue;
+      }
       if constexpr (kSegments) {
         float sum[kWide];
 #pragma unroll
@@ -964,7 +1095,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) latch_error(P.err, kErrTimeout);
           break;
         }
-        epi_linear32<BF16, kWide>(P, w, row0, n0, panel, piece, sum);
+        epi_linear_sums<BF16, kWide, true>(P, w, row0, n0, panel, piece, bias, sum);
         continue;
       }
       if (!__all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((n >> 1) & 1)))) {
@@ -985,7 +1116,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (kDGated)
           epi_dgated<EPI == kEpiDGated8, BF16, kWide>(P, w, acc + half * kWide, row0, n0, scales, panel);
         else if constexpr (EPI == kEpiLinear)
-          epi_linear<BF16, kWide>(P, w, acc + half * kWide, row0, n0, panel, piece);
+          epi_linear<BF16, kWide>(P, w, acc + half * kWide, row0, n0, panel, piece, bias);
         else
           epi_store<BF16, kWide>(P, w, acc + half * kWide, row0, n0, panel);
         done();
@@ -1004,13 +1135,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int EPI>
 constexpr size_t kSmem = (size_t)kStagesOf<EPI> * kStageBytes + 8 * kWarpPanels<EPI> + 1024;
 
-template <int EPI, bool BF16, int TN>
+template <int EPI, bool BF16, int TN, bool TALL = false>
 cudaError_t run_as(const DenseParams &P, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose kernel attribute is set
-  const cudaError_t attr = allow_smem(k_dense<EPI, BF16, TN>, kSmem<EPI>, ready);
+  const cudaError_t attr = allow_smem(k_dense<EPI, BF16, TN, TALL>, kSmem<EPI>, ready);
   if (attr != cudaSuccess) return attr;
   const int grid = 2 * std::min(num_sms / 2, P.first + P.rest);
-  return launch_pdl(k_dense<EPI, BF16, TN>, dim3(grid), dim3(kThreads), kSmem<EPI>, s, P);
+  return launch_pdl(k_dense<EPI, BF16, TN, TALL>, dim3(grid), dim3(kThreads), kSmem<EPI>, s, P);
 }
 template <int EPI>
 cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
@@ -1018,12 +1149,43 @@ cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
     constexpr int kNarrow = EPI != kEpiGated ? 128 : 256;
     return P.bf16 ? run_as<EPI, true, kNarrow>(P, num_sms, s) : run_as<EPI, false, kNarrow>(P, num_sms, s);
   }
+  if constexpr (EPI == kEpiLinear || EPI == kEpiStore)
+    if (P.tall) return P.bf16 ? run_as<EPI, true, 256, true>(P, num_sms, s) : run_as<EPI, false, 256, true>(P, num_sms, s);
   return P.bf16 ? run_as<EPI, true, 256>(P, num_sms, s) : run_as<EPI, false, 256>(P, num_sms, s);
 }
 
 }  // namespace
 
+namespace {
+// About when the last pair is done, in ns: `chunk` for a chunk of a tile of `rows` rows, units of one length
+// after the other's.
+int64_t done_at(const DenseParams &P, int rows, int chunk, int pairs) {
+  int64_t units = 0, work = 0, longest = 0, shortest = INT64_MAX;
+  for (int i = 0; i < P.count; ++i) {
+    const int64_t n = (int64_t)((P.p[i].M + rows - 1) / rows) * P.p[i].tiles_n, len = (int64_t)P.p[i].nk * chunk;
+    units += n;
+    work += n * len;
+    longest = std::max(longest, len);
+    shortest = std::min(shortest, len);
+  }
+  if (units <= 2 * pairs) return units <= pairs ? longest : std::max(longest, 2 * shortest);
+  return std::max(longest, work / pairs + shortest / 2);
+}
+// Tiles of 512 rows: where they are done first.  (Gradients of T x K x N, bf16, us with 256 rows and with 512:
+// 4096 x 4096 x 16384 785 and 714, 3000 x 8192 x 8192 584 and 524, 8192 x 1024 x 4096 120 and 112, but 1500 x
+// 2048 x 8192 83 and 97, whose 24 long units leave most pairs idle at the end.)
+bool tall_tiles(const DenseParams &P, int epi, int num_sms) {
+  if (epi != kEpiStore) return false;
+  for (int i = 0; i < P.count; ++i)
+    if (P.p[i].relu || P.p[i].tn != 256 || P.p[i].split > 1) return false;
+  return done_at(P, 512, 770, num_sms / 2) < done_at(P, 256, 430, num_sms / 2);
+}
+}  // namespace
+
 cudaError_t launch_dense(DenseParams &P, int epi, int num_sms, cudaStream_t s) {
+  P.tall = tall_tiles(P, epi, num_sms);
+  if (P.tall)
+    for (int i = 0; i < P.count; ++i) P.p[i].tiles_m = (P.p[i].M + 511) / 512;
   auto units = [&](int i) { return P.p[i].tiles_m * P.p[i].tiles_n * P.p[i].split; };
   // a unit's length in K chunks: a tile's epilogue (about 2.5 us) takes as long as nine
   constexpr int kEpilogue = 9;

@@ -243,8 +243,7 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
         for (int i = 0; i < G; ++i) v[i] = max_nan(v[i], 0.f);
       } else if (act != SFNN_LINEAR_NONE) {
         uint32_t code[G];
-#pragma unroll
-        for (int i = 0; i < G; ++i) v[i] = act_value(v[i], act, E.slopes != nullptr, code[i]);
+        act_values<G>(v, act, E.slopes != nullptr, code);
         if (E.slopes && live) {
           unsigned char *s = static_cast<unsigned char *>(E.slopes) + (t0 + c) * slope_row_bytes(P.N, act) + (int64_t)col * 2;
 #pragma unroll

@@ -46,7 +46,10 @@ __global__ void __launch_bounds__(256) k_linear_join(const float *__restrict__ p
     for (int j = 0; j < 4; ++j) {
       if (j < cols && E.bias) v[j] += load16(E.bias, col + j, bf16);
       bits |= v[j] <= 0.f || j >= cols ? 0u : 1u << (4 * (lane & 7) + j);
-      v[j] = act_value(v[j], E.act, E.slopes != nullptr, code[j]);
+    }
+    act_values<4>(v, E.act, E.slopes != nullptr, code);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
       if (j < cols && E.res) {
         const int64_t at = row * E.ldres + col + j;
         v[j] += out32 ? static_cast<const float *>(E.res)[at] : load16(E.res, at, bf16);

@@ -315,3 +315,11 @@ def test_out_that_shares_memory():
             sf.linear_forward(**kw)
     right.copy_(x)
     assert torch.equal(sf.linear_forward(x, w, b, residual=right, out=right)[0], sf.linear_forward(x, w, b, residual=x)[0])
+
+
+# Gradients' products of enough rows for tiles of 512: rows, columns and K that fill none of them.
+@pytest.mark.parametrize("T,K,N", [(2500, 1000, 2600), (2305, 1160, 2311), (4100, 600, 4503), (2049, 1288, 5000)])
+@pytest.mark.parametrize("dt", KINDS)
+def test_gradients_of_many_rows(T, K, N, dt):
+    check(T, K, N, dt, "relu", res=None, seed=T)
+    check(T, K, N, dt, "silu", res="f32", bias=False, seed=N)
