@@ -790,15 +790,15 @@ __device__ __forceinline__ void epi_linear(const DenseParams &P, const Unit &Q, 
 // quarter of K in one sum).  So K is summed up in segments of kSegment chunks, each from zero, which
 // the epilogue's threads add up in registers while the next segment is multiplied.
 constexpr int kSegment = 16;
-template <bool bf16, int width, bool WIDE>
-__device__ __forceinline__ void epi_linear_sums(const DenseParams &P, const Unit &Q, int64_t row0, int n0, uint32_t panel,
-                                                ResPiece<WIDE> &piece, uint32_t &bias, float (&sum)[width]) {
+template <bool bf16, int width>
+__device__ __forceinline__ void epi_linear32(const DenseParams &P, const Unit &Q, int64_t row0, int n0, uint32_t panel,
+                                             ResPiece<true> &piece, uint32_t &bias, float (&sum)[width]) {
   const int rows = (int)min((int64_t)32, Q.M - row0);
   if (rows <= 0 || n0 >= Q.N) return;  // (the whole warp)
   uint32_t bits[width / 32] = {};
 #pragma unroll
   for (int c = 0; c < width; c += 32)
-    if (n0 + c < Q.N) linear32<bf16, width, WIDE>(P, Q, row0, n0, c, rows, panel, piece, bias, sum + c, bits[c / 32]);
+    if (n0 + c < Q.N) linear32<bf16, width, true>(P, Q, row0, n0, c, rows, panel, piece, bias, sum + c, bits[c / 32]);
   keep_bits<bf16, width>(P, Q, row0, n0, rows, bits);
 }
 
@@ -807,7 +807,9 @@ __device__ __forceinline__ void epi_linear_sums(const DenseParams &P, const Unit
 // quarter less comes through the L2, which bounds the main loop of the others (4096 x 4096 -> 16384: 4.3 GB,
 // 11.1 TB/s).  Both halves' sums fill tensor memory, so the epilogue takes a half into registers, gives its
 // columns back, and works while the other half, or the next tile's first chunks, are multiplied: the first
-// half is a ring of chunks ahead of the second at a tile's start and end.
+// half is a ring of chunks ahead of the second at a tile's start and end.  Plain stores only: the linear
+// layer's epilogue takes 5 us a half (GELU 10), more than that hides (4096 x 4096 -> 16384 GELU, with 384
+// threads and 216 registers for its warps: 551 us against 410).
 template <int EPI, bool BF16, int TN, bool TALL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_dense(const __grid_constant__ DenseParams P) {
@@ -1037,10 +1039,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if constexpr (TALL) {
         bool there = true;
         for (int h = 0; h < 2; ++h, row0 += 256) {
-          if (EPI == kEpiLinear && h) {
-            res_request<kSegments>(P.end, w, row0, n0, (int)max((int64_t)0, min((int64_t)32, w.M - row0)), piece);
-            bias = bias_request(P.end, n0, w.N);
-          }
           there = __all_sync(0xffffffffu, bar_wait(&acc_full[h], (uint32_t)(n & 1)));
           if (!there) break;
           __syncwarp();
@@ -1057,10 +1055,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tm_fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive_cluster_relaxed(cluster_addr(&acc_empty[h], 0));
-          if constexpr (EPI == kEpiLinear)
-            epi_linear_sums<BF16, kWide, false>(P, w, row0, n0, panel, piece, bias, sum);
-          else
-            epi_store_sums<BF16, kWide>(w, row0, n0, panel, sum);
+          epi_store_sums<BF16, kWide>(w, row0, n0, panel, sum);
         }
         if (!there) {
           if (lane == 0) latch_error(P.err, kErrTimeout);
@@ -1095,7 +1090,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) latch_error(P.err, kErrTimeout);
           break;
         }
-        epi_linear_sums<BF16, kWide, true>(P, w, row0, n0, panel, piece, bias, sum);
+        epi_linear32<BF16, kWide>(P, w, row0, n0, panel, piece, bias, sum);
         continue;
       }
       if (!__all_sync(0xffffffffu, bar_wait(&acc_full[buf], (uint32_t)((n >> 1) & 1)))) {
@@ -1149,7 +1144,7 @@ cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
     constexpr int kNarrow = EPI != kEpiGated ? 128 : 256;
     return P.bf16 ? run_as<EPI, true, kNarrow>(P, num_sms, s) : run_as<EPI, false, kNarrow>(P, num_sms, s);
   }
-  if constexpr (EPI == kEpiLinear || EPI == kEpiStore)
+  if constexpr (EPI == kEpiStore)
     if (P.tall) return P.bf16 ? run_as<EPI, true, 256, true>(P, num_sms, s) : run_as<EPI, false, 256, true>(P, num_sms, s);
   return P.bf16 ? run_as<EPI, true, 256>(P, num_sms, s) : run_as<EPI, false, 256>(P, num_sms, s);
 }
