@@ -762,12 +762,85 @@ __device__ __forceinline__ void keep_bits(const DenseParams &P, const Unit &Q, i
     *reinterpret_cast<uint2 *>(p) = make_uint2(bits[0], bits[1]);
 }
 
+// The whole tile where neither a residual, a ragged output nor a part of K stands in the way: without those
+// branches between them a value takes 9 instructions instead of 12 with a bias, 22 instead of 33 with GELU
+// (8192 tokens, 512 -> 8192: bias 78 -> 70 us, ReLU 89 -> 72, GELU 148 -> 101; 1999 tokens, 4096 -> 16384,
+// GELU, for seconds under the power cap 237 -> 232).
+template <int ACT>
+using Act = std::integral_constant<int, ACT>;
+template <bool bf16, int width, int ACT, bool KEEP>
+__device__ __forceinline__ void linear_plain(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
+                                             int rows, uint32_t panel, uint32_t bias, uint32_t *bits) {
+  const LinearEnd &E = P.end;
+#pragma unroll 1
+  for (int c = 0; c < width && n0 + c < Q.N; c += 32) {
+    const int col = n0 + c;
+    uint32_t raw[32], word = 0, code[32];
+    float v[32];
+    __syncwarp();
+    tm_ld32(taddr + c, raw);
+    tm_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 f = unpack16(__shfl_sync(0xffffffffu, bias, i), bf16);
+      v[2 * i] = __uint_as_float(raw[2 * i]) + f.x;
+      v[2 * i + 1] = __uint_as_float(raw[2 * i + 1]) + f.y;
+    }
+    if (c + 32 < width) bias = bias_request(E, col + 32, Q.N);
+    if (ACT == SFNN_LINEAR_RELU) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (KEEP) word |= v[i] <= 0.f ? 0u : 1u << i;
+        v[i] = max_nan(v[i], 0.f);
+      }
+    } else if (ACT != SFNN_LINEAR_NONE) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+        smooth_values<ACT == SFNN_LINEAR_GELU, KEEP>(v[i], v[i + 1], code[i], code[i + 1]);
+    }
+    uint4 w[4];
+    if (KEEP && ACT > SFNN_LINEAR_RELU) {
+      uint32_t q[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) q[i] = __byte_perm(code[2 * i], code[2 * i + 1], 0x5410);
+      words_to(w, q);
+      const int64_t ld = slope_row_bytes(Q.N, ACT);
+      panel_out(panel + kPanel, w, static_cast<unsigned char *>(E.slopes) + row0 * ld + (int64_t)col * 2, ld, rows, 4);
+    }
+    pack32(w, v, bf16);
+    panel_out(panel, w, static_cast<unsigned char *>(Q.out) + (row0 * Q.ldo + col) * 2, Q.ldo * 2, rows, (Q.N - col + 7) / 8);
+    if (KEEP && ACT == SFNN_LINEAR_RELU)
+#pragma unroll
+      for (int i = 0; i < width / 32; ++i)
+        if (c == 32 * i) bits[i] = word;
+  }
+}
+
 template <bool bf16, int width>
 __device__ __forceinline__ void epi_linear(const DenseParams &P, const Unit &Q, uint32_t taddr, int64_t row0, int n0,
                                            uint32_t panel, ResPiece<false> &piece, uint32_t &bias) {
   const int rows = (int)min((int64_t)32, Q.M - row0);
   if (rows <= 0 || n0 >= Q.N) return;  // (the whole warp)
   uint32_t bits[width / 32] = {};
+  const LinearEnd &E = P.end;
+  if (Q.split == 1 && !E.res && E.vec_out) {
+    const bool keep = E.slopes != nullptr;
+    auto plain = [&](auto act, auto kept) {
+      linear_plain<bf16, width, decltype(act)::value, decltype(kept)::value>(P, Q, taddr, row0, n0, rows, panel, bias, bits);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (E.act == SFNN_LINEAR_NONE)
+      plain(Act<SFNN_LINEAR_NONE>{}, No{});
+    else if (E.act == SFNN_LINEAR_RELU)
+      keep ? plain(Act<SFNN_LINEAR_RELU>{}, Yes{}) : plain(Act<SFNN_LINEAR_RELU>{}, No{});
+    else if (E.act == SFNN_LINEAR_GELU)
+      keep ? plain(Act<SFNN_LINEAR_GELU>{}, Yes{}) : plain(Act<SFNN_LINEAR_GELU>{}, No{});
+    else
+      keep ? plain(Act<SFNN_LINEAR_SILU>{}, Yes{}) : plain(Act<SFNN_LINEAR_SILU>{}, No{});
+    keep_bits<bf16, width>(P, Q, row0, n0, rows, bits);
+    return;
+  }
 #pragma unroll 1
   for (int c = 0; c < width && n0 + c < Q.N; c += 32) {
     uint32_t raw[32], word = 0;

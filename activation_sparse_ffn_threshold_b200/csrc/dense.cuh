@@ -175,13 +175,48 @@ struct LinearEnd {
 __host__ __device__ inline int64_t slope_row_bytes(int64_t N, int act) {
   return act == SFNN_LINEAR_NONE ? 0 : act == SFNN_LINEAR_RELU ? (N + 127) / 128 * 16 : (N + 31) / 32 * 64;
 }
+// Pairs of fp32 values in a 64-bit register, one instruction for both.  (Kept as such from the load to
+// the store: taken apart in between, every instruction is joined by moves.)
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ float2 apart(Pair p) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+__device__ __forceinline__ float within(Pair p) {
+  const float2 v = apart(p);
+  return v.x + v.y;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // act(z) and, where `keep`, the code of act'(z) of the smooth ones in a word's lower half; the limits
 // at the infinities, NaN for a NaN.
 //
 // gelu: z Phi(z), Phi the normal distribution's integral.  Phi(-a) e^(a^2 / 2) is smooth from 1/2 at
 // a = 0 to 0; it is taken as a polynomial of degree 8 in t = 1 / (1 + 0.295 a), fitted to its smallest
 // relative error over a in [0, 14] (3.7e-8; with the roundings 1e-6 down to z = -5, 5e-6 of 1e-38 at
-// -13), and times the e^(-z^2 / 2) that Phi' takes too: two special functions and 12 multiply-adds
+// -13), and times the e^(-z^2 / 2) that Phi' takes too: two special functions and a dozen
+// multiply-adds, most of them two values to an instruction
 // (1999 tokens, 4096 x 16384: 399 us with CUDA's normcdff, 230 without an activation).
 // silu: z / (1 + e^-z).
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -203,28 +238,46 @@ __device__ __forceinline__ float rcp_approx(float v) {
   return v;
 }
 template <bool GELU, bool KEEP>
-__device__ __forceinline__ float smooth_value(float z, uint32_t &code) {
-  const float low = max_nan(z, -80.f), b = min_nan(low, 80.f);  // both are 0 or z beyond, and the products below finite
-  float p, s;
+__device__ __forceinline__ void smooth_values(float &z0, float &z1, uint32_t &code0, uint32_t &code1) {
+  const float low0 = max_nan(z0, -80.f), low1 = max_nan(z1, -80.f);  // both results are 0 beyond
+  // (with a slope both are finite: 0 or 1 beyond)
+  const float b0 = KEEP ? min_nan(low0, 80.f) : low0, b1 = KEEP ? min_nan(low1, 80.f) : low1;
+  const Pair b = pair(b0, b1);
+  float p0, p1, s0, s1;
   if (GELU) {
-    const float e = exp2_approx(b * b * -0.7213475204f), t = rcp_approx(fmaf(0.295f, fabsf(b), 1.f));
-    float q = fmaf(0.0394212678f, t, -0.183406666f);
-    q = fmaf(q, t, 0.271017522f);
-    q = fmaf(q, t, -0.117072001f);
-    q = fmaf(q, t, 0.166289508f);
-    q = fmaf(q, t, 0.0847446173f);
-    q = fmaf(q, t, 0.12169943f);
-    q = fmaf(q, t, 0.117289335f);
-    q = fmaf(q, t, 1.7007178e-05f) * e;
-    p = b > 0.f ? 1.f - q : q;
-    s = fmaf(b * 0.3989422804f, e, p);
+    const float2 x = apart(mul2(mul2(b, b), pair(-0.7213475204f, -0.7213475204f)));
+    const Pair e = pair(exp2_approx(x.x), exp2_approx(x.y));
+    const Pair t = pair(rcp_approx(fmaf(0.295f, fabsf(b0), 1.f)), rcp_approx(fmaf(0.295f, fabsf(b1), 1.f)));
+    Pair q = fma2(pair(0.0394212678f, 0.0394212678f), t, pair(-0.183406666f, -0.183406666f));
+    q = fma2(q, t, pair(0.271017522f, 0.271017522f));
+    q = fma2(q, t, pair(-0.117072001f, -0.117072001f));
+    q = fma2(q, t, pair(0.166289508f, 0.166289508f));
+    q = fma2(q, t, pair(0.0847446173f, 0.0847446173f));
+    q = fma2(q, t, pair(0.12169943f, 0.12169943f));
+    q = fma2(q, t, pair(0.117289335f, 0.117289335f));
+    q = mul2(fma2(q, t, pair(1.7007178e-05f, 1.7007178e-05f)), e);
+    const float2 r = apart(q);
+    p0 = b0 > 0.f ? 1.f - r.x : r.x;
+    p1 = b1 > 0.f ? 1.f - r.y : r.y;
+    if (KEEP) {
+      const float2 s = apart(fma2(mul2(b, pair(0.3989422804f, 0.3989422804f)), e, pair(p0, p1)));
+      s0 = s.x, s1 = s.y;
+    }
   } else {
-    p = rcp_approx(1.f + exp2_approx(b * -1.4426950409f));
-    s = p * fmaf(b, 1.f - p, 1.f);
+    const float2 x = apart(mul2(b, pair(-1.4426950409f, -1.4426950409f)));
+    p0 = rcp_approx(1.f + exp2_approx(x.x));
+    p1 = rcp_approx(1.f + exp2_approx(x.y));
+    if (KEEP) {
+      s0 = p0 * fmaf(b0, 1.f - p0, 1.f);
+      s1 = p1 * fmaf(b1, 1.f - p1, 1.f);
+    }
   }
-  // the sum's last bit is worth 1; a NaN's lower half is 0xffff
-  if (KEEP) code = __float_as_uint(fmaf(s, 32768.f, 8388608.f + 16384.f));
-  return low * p;
+  if (KEEP) {  // the sum's last bit is worth 1; a NaN's lower half is 0xffff
+    code0 = __float_as_uint(fmaf(s0, 32768.f, 8388608.f + 16384.f));
+    code1 = __float_as_uint(fmaf(s1, 32768.f, 8388608.f + 16384.f));
+  }
+  z0 = low0 * p0;
+  z1 = low1 * p1;
 }
 // The same for N values.  The choice stands outside: made value by value it kept their chains of
 // multiply-adds from running beside one another (8192 tokens, 512 -> 8192, GELU: 208 us, 148 so).
@@ -232,7 +285,8 @@ template <int N>
 __device__ __forceinline__ void act_values(float *v, int act, bool keep, uint32_t *code) {
   auto all = [&](auto gelu, auto kept) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = smooth_value<decltype(gelu)::value, decltype(kept)::value>(v[i], code[i]);
+    for (int i = 0; i < N; i += 2)
+      smooth_values<decltype(gelu)::value, decltype(kept)::value>(v[i], v[i + 1], code[i], code[i + 1]);
   };
   using Yes = std::true_type;
   using No = std::false_type;
