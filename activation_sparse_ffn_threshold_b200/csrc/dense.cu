@@ -14,11 +14,12 @@
 // tensor pipe only as long as L2 -> shared memory traffic stays under it.  Warp 0 loads
 // (TMA, 128-byte swizzle), warp 1 of the pair's first CTA issues the MMAs, warps 2-9 run
 // the epilogue of the tile before out of the other half of tensor memory (2 x 256 columns).
+// Plain stores also have tiles of 512 x 256 (TALL, at the kernel).
 //
-// Measured (4096 x 11008 bf16, 4096 tokens): forward and backward 2.56 to 2.64 ms on several cards,
-// 1.26 to 1.30 PFLOP/s (a library product holds 1.39 for long under the power cap); the tensor
-// pipe is busy 57 to 77 % of a kernel's cycles alone.  What it waits for there: the last round
-// of tiles, and L2.
+// Measured (4096 x 11008 bf16, 4096 tokens): forward and backward 2.2 ms in a graph, 2.36 before the
+// tall tiles (1.5 PFLOP/s; a library product holds 1.39 for long under the power cap).  The tensor
+// pipe is busy 57 to 77 % of a kernel's cycles alone with square tiles.  What it waits for there: the
+// last round of tiles, and L2.
 //
 // Every wait is bounded (about a second); one that runs out latches SFNN_ERR_TIMEOUT and the
 // kernel leaves in order: its loads have landed by then, tensor memory is freed.
