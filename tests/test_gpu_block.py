@@ -491,3 +491,26 @@ def test_out_that_shares_memory():
         sf.residual_norm_forward(x[:1], z[:1], "rms", w, out=w[None])
     inside = sf.residual_norm_forward(x, z, "rms", w, out=x)
     assert torch.equal(want[0], inside[0]) and torch.equal(want[1], inside[1])
+
+
+# Neither a post norm nor a gate: the backward kernel without Z's own sums, its widths and what may be missing.
+@pytest.mark.parametrize("dt", KINDS)
+@pytest.mark.parametrize("pre", ["rms", "layer"])
+@pytest.mark.parametrize("T,d", [(1, 512), (3, 8), (700, 512), (301, 1001), (150, 4096), (9, 4104), (40, 8192), (5, 8200), (3000, 96)])
+def test_plain_branches(T, d, pre, dt):
+    for i in range(3):
+        check(T, d, dt, A=[1.0, 0.75, 1.0][i], C=[1.0, -0.5, 2.0][i], seed=T + i, pre=pre, bias=i != 1, x32=i == 1, z32=i == 2)
+    a, rows, saved = check(T, d, dt, seed=d, pre=pre, bias=True, pad=i)
+    dr, dh = rows(a["x"].dtype), rows(dt)
+    full = sf.residual_norm_backward(dr, dh, saved)
+    for j, k in enumerate(GRADS):  # one at a time
+        one = sf.residual_norm_backward(dr, dh, saved, need=[i == j for i in range(7)])
+        assert all((t is None) == (i != j or full[i] is None) for i, t in enumerate(one))
+        if full[j] is not None:
+            assert torch.equal(one[j], full[j]) if full[j].dim() == 2 else True
+            near(one[j], *plain(a, pre, "none", 1.0, 1.0, dr, dh)[k], K=T if full[j].dim() == 1 else 0)
+    for r_, h_ in ((dr, None), (None, dh)):  # one of the two is missing
+        want = plain(a, pre, "none", 1.0, 1.0, torch.zeros_like(dr) if r_ is None else r_, h_)
+        for k, v in zip(GRADS, sf.residual_norm_backward(r_, h_, saved)):
+            if v is not None:
+                near(v, *want.get(k, (torch.zeros_like(v, dtype=torch.float64),) * 2), K=T if v.dim() == 1 else 0)

@@ -323,3 +323,44 @@ def test_out_that_shares_memory():
 def test_gradients_of_many_rows(T, K, N, dt):
     check(T, K, N, dt, "relu", res=None, seed=T)
     check(T, K, N, dt, "silu", res="f32", bias=False, seed=N)
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 64, 1 << 20), (300, 64, 200003), (2, 1 << 20, 24), (1030, 8, 3), (1024, 64, 70001)])
+def test_ends_of_the_range(T, K, N):
+    check(T, K, N, KINDS[T % 2], "relu", res=[None, "f32"][T % 2], seed=T, save=T * N < 1 << 25)
+
+
+def test_first_calls_inside_a_capture():
+    """Only the error word lies on the device: kernels' limits and clusters are looked up while capturing."""
+    import subprocess
+    import sys
+    code = """
+import torch
+import activation_sparse_ffn_threshold_b200 as sf
+x = torch.randn(1, 64, device="cuda").half()
+sf.residual_norm_forward(x, x.clone(), "rms")
+r = lambda *s: torch.randn(*s, device="cuda").half() * 0.1
+sets = [(r(T, K), r(N, K), r(N)) for T, K, N in ((1, 4096, 1000), (40, 1024, 1024), (250, 8192, 3500), (2500, 1000, 2600))]
+def step():
+    out = []
+    for x, w, b in sets:
+        y, s = sf.linear_forward(x, w, b, "gelu", save=True)
+        out += [y, *sf.linear_backward(y, s, w)]
+    return out + [sf.clip_grad_norm([t.clone() for t in out], 1.0)]
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    held = step()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(held, step()))
+assert sf.dense_error() == 0
+"""
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_truth_that_has_none():
+    x, w = torch.ones(1, 8, device="cuda").half(), torch.ones(2, 8, device="cuda").half()
+    with pytest.raises(RuntimeError):
+        sf.linear_forward(x, w, save=torch.ones(2))
