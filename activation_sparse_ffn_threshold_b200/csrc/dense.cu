@@ -12,8 +12,8 @@
 // (M = 256, N = 256) reads both CTAs' shared memory, so an operand byte loaded feeds twice
 // the products of a single CTA's tile -- what bounds a 16-bit product on this part is the
 // tensor pipe only as long as L2 -> shared memory traffic stays under it.  Warp 0 loads
-// (TMA, 128-byte swizzle), warp 1 of the pair's first CTA issues the MMAs, warps 2-9 run
-// the epilogue of the tile before out of the other half of tensor memory (2 x 256 columns).
+// (TMA, 128-byte swizzle), warp 1 of the pair's first CTA issues the MMAs, the others (8, or
+// 16 for fp32 results) run the epilogue of the tile before out of the other half of tensor memory (2 x 256 columns).
 // Plain stores also have tiles of 512 x 256 (TALL, at the kernel).
 //
 // Measured (4096 x 11008 bf16, 4096 tokens): forward and backward 2.2 ms in a graph, 2.36 before the
@@ -32,10 +32,16 @@
 namespace sfnn {
 namespace {
 
-constexpr int kThreads = 320;
-// K chunks in flight; the backward epilogue's saved values take one's place (below)
+// Epilogue warps: 16 for fp32 results, which read and write most and add up segments besides (8192 tokens, 64 ->
+// 8192 onto an fp32 residual 226 us with 8, 191 with 16; 4096, 4096 -> 16384 477 and 457).  8 for the others,
+// whose epilogue hides behind a ring of 6 chunks (16-bit residual 107 and 114 us, none 46 and 50).
 template <int EPI>
-constexpr int kStagesOf = EPI == kEpiDGated || EPI == kEpiDGated8 ? 5 : 6;
+constexpr int kEpiWarps = EPI == kEpiLinear32 ? 16 : 8;
+template <int EPI>
+constexpr int kThreads = 64 + 32 * kEpiWarps<EPI>;
+// K chunks in flight; the backward epilogue's saved values take one's place (below), as do 16 warps' panels
+template <int EPI>
+constexpr int kStagesOf = EPI == kEpiDGated || EPI == kEpiDGated8 || kEpiWarps<EPI> == 16 ? 5 : 6;
 constexpr int kMaxStages = 6;
 constexpr uint32_t kStageBytes = 32768;  // per CTA: 128 x 64 of A, 128 x 64 of B
 constexpr int kTile = 256;
@@ -757,10 +763,12 @@ __device__ __forceinline__ void keep_bits(const DenseParams &P, const Unit &Q, i
   const int lane = threadIdx.x & 31;
   if (!E.slopes || E.act != SFNN_LINEAR_RELU || Q.split > 1 || lane >= rows) return;
   uint32_t *p = static_cast<uint32_t *>(E.slopes) + (row0 + lane) * (slope_row_bytes(Q.N, E.act) / 4) + n0 / 32;
-  if (width == 128)
+  if constexpr (width == 128)
     *reinterpret_cast<uint4 *>(p) = make_uint4(bits[0], bits[1], bits[width / 32 - 2], bits[width / 32 - 1]);
+  else if constexpr (width == 64)
+    *reinterpret_cast<uint2 *>(p) = make_uint2(bits[0], bits[width / 32 - 1]);
   else
-    *reinterpret_cast<uint2 *>(p) = make_uint2(bits[0], bits[1]);
+    *p = bits[0];
 }
 
 // The whole tile where neither a residual, a ragged output nor a part of K stands in the way: without those
@@ -885,7 +893,7 @@ __device__ __forceinline__ void epi_linear32(const DenseParams &P, const Unit &Q
 // layer's epilogue takes 5 us a half (GELU 10), more than that hides (4096 x 4096 -> 16384 GELU, with 384
 // threads and 216 registers for its warps: 551 us against 410).
 template <int EPI, bool BF16, int TN, bool TALL>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<EPI>, 1)
     k_dense(const __grid_constant__ DenseParams P) {
   constexpr bool kDGated = EPI == kEpiDGated || EPI == kEpiDGated8, kSegments = EPI == kEpiLinear32;
   constexpr int kStages = TALL ? 4 : kStagesOf<EPI>, kRows = TALL ? 512 : kTile;
@@ -906,7 +914,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&acc_full[i], 1);
-      bar_init(&acc_empty[i], 16);  // 8 epilogue warps of each CTA
+      bar_init(&acc_empty[i], 2 * kEpiWarps<EPI>);  // both CTAs' epilogue warps
     }
     bar_init_fence();
   }
@@ -1091,7 +1099,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Unit w = unit_at(P, id);
       const int buf = n & 1;
       int64_t row0 = (int64_t)w.pos.m * kRows + rank * 128 + quad * 32;
-      constexpr int kWide = TN / 2;  // columns of this warp
+      constexpr int kWide = TN / (kEpiWarps<EPI> / 4);  // columns of this warp
       const int n0 = EPI == kEpiGated ? w.pos.n * 128 + half * 64 : w.pos.n * TN + half * kWide;
       // what the epilogue reads besides the accumulators, requested before they are there
       float2 scales;
@@ -1202,7 +1210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int EPI>
-constexpr size_t kSmem = (size_t)kStagesOf<EPI> * kStageBytes + 8 * kWarpPanels<EPI> + 1024;
+constexpr size_t kSmem = (size_t)kStagesOf<EPI> * kStageBytes + kEpiWarps<EPI> * kWarpPanels<EPI> + 1024;
 
 template <int EPI, bool BF16, int TN, bool TALL = false>
 cudaError_t run_as(const DenseParams &P, int num_sms, cudaStream_t s) {
@@ -1210,7 +1218,7 @@ cudaError_t run_as(const DenseParams &P, int num_sms, cudaStream_t s) {
   const cudaError_t attr = allow_smem(k_dense<EPI, BF16, TN, TALL>, kSmem<EPI>, ready);
   if (attr != cudaSuccess) return attr;
   const int grid = 2 * std::min(num_sms / 2, P.first + P.rest);
-  return launch_pdl(k_dense<EPI, BF16, TN, TALL>, dim3(grid), dim3(kThreads), kSmem<EPI>, s, P);
+  return launch_pdl(k_dense<EPI, BF16, TN, TALL>, dim3(grid), dim3(kThreads<EPI>), kSmem<EPI>, s, P);
 }
 template <int EPI>
 cudaError_t run(const DenseParams &P, int num_sms, cudaStream_t s) {
