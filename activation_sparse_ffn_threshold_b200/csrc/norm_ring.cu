@@ -675,6 +675,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_norm_backward_ring(cons
 
 // The rows' way through shared memory.
 constexpr int kRingSmem = 225 * 1024;
+// Where the backward kernel has more values than registers (Z's own sums with means or biases) it takes no
+// more than this for stages beyond the second: what is left of the SM's 256 KB serves the loads of what it
+// spilled (8192 x 4096 bf16, LayerNorm and RMS: three stages 133 us, two 121; 16384 x 2048 124 and 115).
+constexpr int kLeftSmem = 194 * 1024;
 struct RingShape {
   int block, grid, smem;
   bool fits;
@@ -682,7 +686,7 @@ struct RingShape {
 bool plain_branch(const NormParams &F) { return F.post == SFNN_NORM_NONE && !F.gate; }
 int ring_threads(int d) { return (int)up((d + kRingValues - 1) / kRingValues, 32); }
 RingShape ring_shape(RingParams &R, const NormParams &F, bool odd, bool exact, bool backward, const void *dr, int64_t lddr,
-                     const void *dh, int64_t lddh, int sums, int most_threads, int sms) {
+                     const void *dh, int64_t lddh, int sums, int most_threads, int most, int sms) {
   const int d = F.d;
   R.threads = ring_threads(d);
   auto row = [&](int k, const void *p, int64_t ld, bool wide) {
@@ -711,6 +715,7 @@ RingShape ring_shape(RingParams &R, const NormParams &F, bool odd, bool exact, b
   R.groups = std::min(R.groups, std::max(1, (F.T + sms - 1) / sms));
   while (R.groups > 1 && (R.groups * 2 * R.stage > budget || R.groups * sums * d * 4 > kRingSmem)) --R.groups;
   R.stages = std::max(0, std::min(kMaxStages, budget / (R.groups * R.stage)));
+  R.stages = std::min(R.stages, std::max(2, (most - held) / (R.groups * R.stage)));
   RingShape s;
   s.block = R.threads * R.groups;
   s.smem = std::max(R.groups * R.stages * R.stage + held, R.groups * sums * d * 4);
@@ -759,7 +764,7 @@ cudaError_t run_ring(bool wide, bool full, bool exact, bool odd, const RingShape
 cudaError_t norm_forward_ring(const NormParams &P, int32_t *err, bool bf16, bool vec, int sms, cudaStream_t s, RingPlan &plan) {
   const bool full = P.pre == SFNN_NORM_LAYER || P.post == SFNN_NORM_LAYER || P.b || P.bp, exact = exact_rows(P, vec);
   RingParams R{};
-  const RingShape shape = ring_shape(R, P, !vec, exact, false, nullptr, 0, nullptr, 0, 0, kForwardThreads, sms);
+  const RingShape shape = ring_shape(R, P, !vec, exact, false, nullptr, 0, nullptr, 0, 0, kForwardThreads, kRingSmem, sms);
   plan = {shape.fits, shape.grid};
   if (!shape.fits) return cudaSuccess;
   return bf16 ? run_ring<true>(P.x32 || P.z32, full, exact, !vec, shape, P, R, err, s)
@@ -770,7 +775,8 @@ cudaError_t norm_backward_ring(const NormBackParams &P, bool sums_all, bool bf16
   const bool full = F.pre == SFNN_NORM_LAYER || F.post == SFNN_NORM_LAYER || F.bp || sums_all;
   const bool exact = exact_rows(F, vec) && P.dr && P.dh && P.dx && P.dz;
   RingParams R{};
-  const RingShape shape = ring_shape(R, F, !vec, exact, true, P.dr, P.lddr, P.dh, P.lddh, P.sums, kBackwardThreads, sms);
+  const RingShape shape = ring_shape(R, F, !vec, exact, true, P.dr, P.lddr, P.dh, P.lddh, P.sums, kBackwardThreads,
+                                     full && !plain_branch(F) ? kLeftSmem : kRingSmem, sms);
   plan = {shape.fits, shape.grid};
   if (!shape.fits) return cudaSuccess;
   return bf16 ? run_ring<true>(F.x32 || F.z32, full, exact, !vec, shape, P, R, P.err, s)
