@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
   __syncthreads();
   tm_fence_after();
   const uint32_t tmem = tmem_slot;
+  if (split > 1 && P.apart) cluster_arrive();  // this CTA has started: the others may write to it (waited for below)
 
   if (warp == 0) {
     if (lane == 0) {
@@ -301,7 +302,12 @@ __global__ void __launch_bounds__(kThreads) k_few(const __grid_constant__ FewPar
   if (split > 1) {
     // the same place in every CTA's shared memory
     const uint32_t place = stage0 - raw + (P.apart ? (uint32_t)P.stages * stage_bytes : 0u);
-    if (!P.apart) cluster_sync_all();  // no load or MMA touches the stages any more, in any CTA
+    // Every CTA has started before a sum is written to it, and where that goes into the stages, no load or MMA
+    // touches those any more.  (The first is known long before it is asked for.)
+    if (P.apart)
+      cluster_wait();
+    else
+      cluster_sync_all();
     if (worker && busy && ok) {
       const int count = tokens(unit);
 #pragma unroll 1
