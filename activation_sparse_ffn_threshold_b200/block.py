@@ -5,7 +5,8 @@ Calls are checked and marshalled into ``libsfnn.so`` (include/sfnn.h) by ``_bloc
 (csrc/bind/block.cpp) -- native, as their work on the GPU is often shorter than the same in Python.
 Tensors lie on one CUDA device, and results belong to the current stream (or to ``stream``, which
 the call then runs on).  Autograd follows ``linear`` and ``residual_norm``; the functions with
-``_forward`` and ``_backward`` are their passes as plain calls.
+``_forward`` and ``_backward`` are their passes as plain calls.  What a call writes in place counts as
+changed for autograd, as after PyTorch's own operations.
 """
 from __future__ import annotations
 

@@ -136,6 +136,11 @@ void same_device(const at::Tensor &t, c10::Device device) {
   if (t.device() != device) refuse(PyExc_ValueError, "all tensors must be on one device");
 }
 
+// What was written in place: autograd then refuses a backward pass that saved what was there before.
+void written(const at::Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 at::Tensor empty(at::IntArrayRef size, at::ScalarType dtype, c10::Device device) {
   return at::Tensor(at::detail::empty_cuda(size, dtype, device, c10::nullopt));
 }
@@ -274,7 +279,10 @@ PyObject *linear_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const sfnn_status st = unlocked([&] { return sfnn_linear_forward(&q, r.p, r.ld, ry.p, ry.ld, ps, pw, bytes, err, stream); });
     if (st != SFNN_OK) return status(st);
   }
-  if (out) Py_INCREF(a[7]);
+  if (out) {
+    written(*out);
+    Py_INCREF(a[7]);
+  }
   return tuple({out ? a[7] : wrap(y), wrap(slopes)});
   NATIVE_END
 }
@@ -416,6 +424,7 @@ PyObject *norm_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   sfnn_stream_t stream = stream_of(device);
   const sfnn_status st = unlocked([&] { return sfnn_norm_forward(&q, r.p, r.ld, ph, q.d, ps, err, stream); });
   if (st != SFNN_OK) return status(st);
+  if (out) written(*out);
   PyObject *given = out ? a[14] : t.z ? nullptr : a[0];  // r is out, or x itself
   Py_XINCREF(given);
   return tuple({given ? given : wrap(made), wrap(h), wrap(stats), dtype_object(dtype)});
@@ -511,6 +520,7 @@ PyObject *clip_grad_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                stream);
   });
   if (st != SFNN_OK) return status(st);
+  for (Py_ssize_t i = 0; i < count; ++i) written(*tensor(PyList_GET_ITEM(apart ? a[1] : a[0], i)));
   return wrap(norm);
   NATIVE_END
 }
