@@ -402,12 +402,12 @@ int64_t slim_cost(int T, int N, int64_t K, bool gated, int num_sms);
 sfnn_status launch_slim(const SlimArgs &q, int num_sms, cudaStream_t s);
 
 // The linear layer for few tokens (few.cu): weight rows and tokens of a tile, CTAs to a cluster, and the time it
-// should take in ns (1e30: it does not take the product).  `words`: a ReLU's slopes are kept.
+// should take in ns (1e30: it does not take the product).  `words`: a ReLU's slopes are kept; `out32`: an fp32 result.
 struct FewPlan {
   int nb, tn, split;
   double cost;
 };
-FewPlan few_plan(int T, int N, int64_t K, bool words, int sms);
+FewPlan few_plan(int T, int N, int64_t K, bool words, bool out32, int sms);
 struct FewArgs {
   const void *x, *w;
   int64_t ldx, ldw;

@@ -15,7 +15,11 @@
 // 512 tokens 28 (a library's product 14, 10 and 15: its tiles share loads across SMs, these read the L2 at 11.7
 // bytes a ns and exchange sums at the 15 bytes a clock of an SM's way to its cluster), 1024 x 1024 256 tokens 7.
 //
-// Sums that leave as fp32 are dealt to several accumulators (see kSegment in dense.cu).
+// Sums that leave as fp32 are dealt to several accumulators (see kSegment in dense.cu), kMostDealt chunks to
+// one at most: 128 steps of 16 products, each of which costs up to 2^-24 of the sum (measured, K = 28672: rms
+// 2.2e-6 of the result at 50 tokens, whose accumulators take 28 chunks, 1.3e-6 with 16; without the limit 4.3e-6
+// at 128 tokens, 8.5e-6 at 200 and 3.4e-5 at 1024).  Shapes that would need more are left to the square tiles,
+// which add up 16 chunks at a time.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -37,6 +41,8 @@ constexpr int kBudget = 200 * 1024;
 constexpr int kApart = 40 * 1024;      // up to this, the exchange has memory of its own
 constexpr int kExchange = 224 * 1024;  // and this is the most it may have
 constexpr int kMostSmem = 226 * 1024;
+constexpr int kDealt = 16;      // chunks of K that an accumulator of an fp32 result should hold ...
+constexpr int kMostDealt = 32;  // ... and may
 
 struct alignas(64) FewParams {
   CUtensorMap x, w;
@@ -347,6 +353,12 @@ int up_to(int v, int to) { return (v + to - 1) / to * to; }
 // Tokens that a rank ends: whole eights, as tensor memory is read.
 int share_of(int T, int split) { return up_to((T + split - 1) / split, 8); }
 
+// Accumulators of an fp32 result, as far as tensor memory goes; `chunks`: the fewest of a rank, which every
+// accumulator must get one of.
+int accumulators(int chunks, int tokens, int halves) {
+  return std::max(1, std::min({chunks, (chunks + kDealt - 1) / kDealt, 512 / (up_to(tokens, 32) * halves)}));
+}
+
 // One limit for every launch: set again, a lower one would take back the higher.
 template <bool BF16>
 cudaError_t allow() {
@@ -392,7 +404,7 @@ int active_clusters(int split, int sms) {
 // 257 of 4096 x 12288 43 as three.  Against the square tiles: 257 tokens of 2048 x 2048 12 us to 15, of 4096
 // x 12288 43 to 54, 400 of 4096 x 16384 60 to 58.  More than 1024 tokens are not looked at: there the square
 // tiles, which read each byte for more products, lose by little at most (1000 of 1024 x 1024: 10 us to 14).
-FewPlan few_plan(int T, int N, int64_t K, bool words, int sms) {
+FewPlan few_plan(int T, int N, int64_t K, bool words, bool out32, int sms) {
   FewPlan best{};
   best.cost = 1e30;
   if (T > kMostTokens) return best;
@@ -414,11 +426,13 @@ FewPlan few_plan(int T, int N, int64_t K, bool words, int sms) {
       if (p.nb > kRows) continue;
       const int share = share_of(p.tn, split), halves = p.nb > 128 ? 2 : 1;
       if ((split - 1) * share * halves * 512 > kExchange) continue;
+      const int rank_chunks = (nk + split - 1) / split;
+      if (out32 && rank_chunks > kMostDealt * accumulators(nk / split, p.tn, halves)) continue;
       const double tiles = (double)((N + p.nb - 1) / p.nb) * tt, ctas = std::min<double>(tiles * split, sms);
       const double weights = std::max(1., ctas / tt / split) * split * p.nb;  // rows of a chunk that differ
       const double chunk = std::max({232 + 0.869 * p.nb + 0.718 * halves * up_to(p.tn, 16), weights * 128 / 5480,
                                      ctas * (p.nb + p.tn) * 128 / 11700});
-      p.cost = 3640 + rounds * (((nk + split - 1) / split) * chunk + 15.2 * share * halves) +
+      p.cost = 3640 + rounds * (rank_chunks * chunk + 15.2 * share * halves) +
                (split > 1 ? 432 + 284 * split + 13.6 * p.tn * halves : 0);
       if (p.cost < best.cost) best = p;
     }
@@ -441,10 +455,7 @@ sfnn_status launch_few(const FewArgs &q, const FewPlan &plan, int sms, cudaStrea
   P.split = plan.split;
   P.share = share_of(P.t8, P.split);
   P.acc_cols = up_to(P.t16, 32);
-  P.accs = 1;
-  // an fp32 result: no more than 64 sums of the tensor cores in one accumulator, as far as tensor memory goes
-  const int nk = P.nk / P.split;
-  if (q.out32) P.accs = std::max(1, std::min({nk, (nk + 15) / 16, 512 / (P.acc_cols * P.halves)}));
+  P.accs = q.out32 ? accumulators(P.nk / P.split, P.t8, P.halves) : 1;
   P.tmem_cols = 32;
   while (P.tmem_cols < P.halves * P.accs * P.acc_cols) P.tmem_cols *= 2;
   const int chunk = (P.t8 + P.nb8) * 128;

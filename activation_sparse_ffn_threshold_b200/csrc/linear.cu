@@ -284,7 +284,7 @@ sfnn_status sfnn_linear_forward(const sfnn_linear_desc *q, const void *residual,
   end.slopes = slopes;
   end.vec_out = pieces(y, ldy, q);
   end.vec_res = residual && pieces(residual, ldr, q);
-  const FewPlan few = few_plan(T, N, q->K, slopes && q->act == SFNN_LINEAR_RELU, sms);
+  const FewPlan few = few_plan(T, N, q->K, slopes && q->act == SFNN_LINEAR_RELU, out32, sms);
   if (few.cost < dense_cost(T, N, q->K, sms)) {
     FewArgs a{};
     a.x = q->x;

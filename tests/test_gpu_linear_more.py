@@ -35,3 +35,24 @@ def test_split_products_on_two_streams_at_once():
         for got, want in zip(out, alone):
             assert all(torch.equal(y, want) for y in got)
     assert sf.dense_error() == 0
+
+
+# An accumulator of an fp32 result takes at most 128 steps of 16 products, each of which cuts up to 2^-23, on average
+# 2^-24, off the sum so far; sums of random signs grow with the root of their length, 2/3 of the last on average, so
+# that 128 2^-24 2/3 = 5.1e-6 of the result would be lost at the most.  The accumulators hold a few bits more than a
+# result does: half of that for the mean over values, 128 2^-25 = 3.8e-6, is allowed.
+LONG = [(28672, 7168, (1, 50, 100, 128, 200, 300, 400, 800, 1024, 1100)), (16384, 4096, (2, 160, 300, 400, 513)),
+        (8192, 8192, (64, 160, 300, 800, 1024)), (65536, 1000, (3, 128, 700))]
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("K,N,tokens", LONG)
+def test_long_sums_that_leave_as_fp32(K, N, tokens, dt):
+    w = normal(N, K, seed=K, size=K ** -0.5, dt=dt)
+    W = w.double()
+    for T in tokens:
+        x = normal(T, K, seed=T, dt=dt)
+        want = x.double() @ W.t()
+        error = sf.linear_forward(x, w, out_dtype=torch.float32)[0].double() - want
+        assert error.square().mean().sqrt() <= 128 * 2.0 ** -25 * want.square().mean().sqrt(), T
+    assert sf.dense_error() == 0
