@@ -239,7 +239,8 @@ __device__ __forceinline__ float rcp_approx(float v) {
 }
 template <bool GELU, bool KEEP>
 __device__ __forceinline__ void smooth_values(float &z0, float &z1, uint32_t &code0, uint32_t &code1) {
-  const float low0 = max_nan(z0, -80.f), low1 = max_nan(z1, -80.f);  // both results are 0 beyond
+  // (both results are 0 from there on: e^88 is beyond 2^126, its reciprocal flushed; silu is off by 88 2^-126 at most)
+  const float low0 = max_nan(z0, -88.f), low1 = max_nan(z1, -88.f);
   // (with a slope both are finite: 0 or 1 beyond)
   const float b0 = KEEP ? min_nan(low0, 80.f) : low0, b1 = KEEP ? min_nan(low1, 80.f) : low1;
   const Pair b = pair(b0, b1);

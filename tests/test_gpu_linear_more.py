@@ -56,3 +56,26 @@ def test_long_sums_that_leave_as_fp32(K, N, tokens, dt):
         error = sf.linear_forward(x, w, out_dtype=torch.float32)[0].double() - want
         assert error.square().mean().sqrt() <= 128 * 2.0 ** -25 * want.square().mean().sqrt(), T
     assert sf.dense_error() == 0
+
+
+# silu: the exponent z log2 e is off by 1.5 roundings, which e^-z takes |z| 1.5 2^-24 of itself from; the special functions'
+# 2^-22 and 2^-23 and three products' roundings: (|z| + 8) 2^-23.  Below -87.3 its 1 / (1 + e^-z) leaves the
+# normal range: up to 88 2^-126 is lost.  gelu: likewise z^2 / 2 times 2.5 roundings, the polynomial's 3.7e-8 and
+# its nine steps of at most twice the sum's size: (1.25 z^2 + 32) 2^-24; below -13 its e^(-z^2 / 2) leaves the range.
+@pytest.mark.parametrize("T", [1, 64, 1200])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_activations_far_out(act, T):
+    far = torch.cat([torch.linspace(-16, 16, 513), torch.linspace(-104, -16, 353), torch.tensor([16.0, 40, 87, 88, 89, 104, 1000, 3e4])])
+    z = far.half()
+    w = torch.zeros(z.numel(), 8, dtype=torch.float16)
+    w[:, 0] = z
+    x = torch.zeros(T, 8, dtype=torch.float16)
+    x[:, 0] = 1
+    y = sf.linear_forward(x.cuda(), w.cuda(), act=act, out_dtype=torch.float32)[0].double()
+    z = z.double().cuda()
+    # (through erfc: 1 + erf has nothing left beyond -8.3)
+    want = z * 0.5 * torch.special.erfc(z * -0.5 ** 0.5) if act == "gelu" else z / (1 + torch.exp(-z))
+    rel = (1.25 * z.clamp(-14, 14).square() + 32) * 2.0 ** -24 if act == "gelu" else (z.abs().clamp_max(104) + 8) * 2.0 ** -23
+    tol = rel * want.abs() + (1 if act == "gelu" else 88) * 2.0 ** -126
+    off = (y - want).abs() / tol
+    assert (off <= 1).all(), (off.max().item(), z[off.max(0)[0].argmax()].item())
