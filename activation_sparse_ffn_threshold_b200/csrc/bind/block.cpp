@@ -136,6 +136,16 @@ void same_device(const at::Tensor &t, c10::Device device) {
   if (t.device() != device) refuse(PyExc_ValueError, "all tensors must be on one device");
 }
 
+// What a forward pass kept, as it may come back from saved-tensor hooks.
+const at::Tensor &kept(PyObject *o, const char *name, at::ScalarType dtype, at::IntArrayRef shape, c10::Device device) {
+  const at::Tensor *t = tensor(o);
+  if (!t || t->layout() != at::kStrided || t->device() != device || t->scalar_type() != dtype || t->sizes() != shape ||
+      !t->is_contiguous())
+    refuse(PyExc_ValueError, "%s must be as the forward pass saved them: a contiguous %s tensor of shape %s on x's device", name,
+           name_of(dtype), shape_text(shape).c_str());
+  return *t;
+}
+
 // What was written in place: autograd then refuses a backward pass that saved what was there before.
 void written(const at::Tensor &t) {
   if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
@@ -291,7 +301,6 @@ PyObject *linear_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   NATIVE_BEGIN(10);
   const at::Tensor &dy = cuda_tensor(a[0], "dy"), &x = cuda_tensor(a[1], "x"), &w = cuda_tensor(a[7], "w");
-  const at::Tensor *slopes = tensor(a[2]);
   const at::ScalarType y_dtype = dtype_of(a[5]);
   const sfnn_linear_desc q = linear_desc(x, w, nullptr, (int)whole(a[3]), y_dtype);
   if (q.N != whole(a[4])) refuse(PyExc_ValueError, "w must have the forward pass's shape");
@@ -300,6 +309,9 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
   shape.back() = q.N;
   const Rows r = output(dy, "dy", shape, y_dtype, device);
+  const void *ps = nullptr;
+  if (q.act != SFNN_LINEAR_NONE)
+    ps = kept(a[2], "slopes", at::kByte, {sfnn_linear_slope_bytes(q.T, q.N, q.act)}, device).data_ptr();
   const c10::cuda::CUDAGuard guard(device);
   const at::ScalarType dt = x.scalar_type();
   at::Tensor dx, dw, db;
@@ -309,7 +321,6 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const int64_t bytes = std::max<int64_t>(16, sfnn_linear_workspace(q.T, q.K, q.N, 1));
   const at::Tensor ws = empty({bytes}, at::kByte, device);
   auto p = [](const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
-  const void *ps = slopes ? slopes->data_ptr() : nullptr;
   int32_t *err = error_word(a[9]);
   sfnn_stream_t stream = stream_of(device);
   const sfnn_status st = unlocked(
@@ -438,9 +449,9 @@ PyObject *norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const NormInputs t = norm_inputs(a);
   at::ScalarType dtype = dtype_of(a[12]);
   const sfnn_norm_desc q = norm_desc(t, a + 7, dtype);
-  const at::Tensor &stats = cuda_tensor(a[13], "stats");
-  const at::Tensor *dr = tensor(a[14]), *dh = tensor(a[15]);
   const c10::Device device = t.x->device();
+  const at::Tensor &stats = kept(a[13], "stats", at::kFloat, {q.T, 4}, device);
+  const at::Tensor *dr = tensor(a[14]), *dh = tensor(a[15]);
   Rows r{nullptr, 0, 0, 0}, h{nullptr, 0, 0, 0};
   int code;
   if (dr) {
