@@ -326,15 +326,19 @@ int grid_of(const sfnn_grad *g, int count, int sms) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(chunks_of(g, count), (int64_t)sms * kCtasPerSm));
 }
 
-// Whether something that is written overlaps something else that is written or read.
+// Whether something that is written, the norm and the workspace among it, overlaps something else that is
+// written or read.
 struct Span {
   uintptr_t lo, hi;
   bool written;
 };
-sfnn_status overlaps(const sfnn_grad *g, int count) {
-  Span *s = new (std::nothrow) Span[2 * (size_t)count + 1];
+sfnn_status overlaps(const sfnn_grad *g, int count, const float *norm, const void *ws, int64_t ws_bytes) {
+  Span *s = new (std::nothrow) Span[2 * (size_t)count + 2];
   if (!s) return SFNN_ERR_OOM;
   size_t n = 0;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(norm), work = reinterpret_cast<uintptr_t>(ws);
+  s[n++] = {at, at + 4, true};
+  s[n++] = {work, work + (uintptr_t)ws_bytes, true};
   for (int i = 0; i < count; ++i) {
     if (!g[i].numel) continue;
     const uintptr_t bytes = (uintptr_t)g[i].numel * elem_bytes((int)g[i].dtype);
@@ -383,7 +387,7 @@ sfnn_status sfnn_clip_grad_norm(const sfnn_grad *grads, int32_t count, float max
       ws_bytes < sfnn_clip_workspace(count))
     return SFNN_ERR_INVALID_ARG;
   if (chunks_of(grads, count) > 0x7fffffffll) return SFNN_ERR_UNSUPPORTED;
-  const sfnn_status st = overlaps(grads, count);
+  const sfnn_status st = overlaps(grads, count, norm, ws, sfnn_clip_workspace(count));
   if (st != SFNN_OK) return st;
   const int sms = device_sms();
   if (sms < 1) return SFNN_ERR_CUDA;
