@@ -62,7 +62,7 @@ __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
 
 struct RingSmem {  // beside the stages and the weights
   uint64_t full[kMaxGroups * kMaxStages];
-  float slots[2][2][64];  // [turn][value][a group's warps, rounded up to 4]
+  alignas(16) float slots[2][2][64];  // [turn][value][a group's warps, rounded up to 4], read four at a time
 };
 
 // WIDE: X or Z is fp32.  FULL: means and biases.  EXACT: what is usual -- both vectors of every thread are
