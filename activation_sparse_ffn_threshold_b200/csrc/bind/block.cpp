@@ -36,16 +36,21 @@ struct Refused {
   throw Refused{type, text};
 }
 
+// A tensor whose memory holds its values (the imaginary part of a conjugate is negated when it is read).
+const at::Tensor &plain(PyObject *o) {
+  const at::Tensor &t = THPVariable_Unpack(o);
+  if (t.layout() != at::kStrided) refuse(PyExc_TypeError, "a strided tensor was expected");
+  if (t.is_neg()) refuse(PyExc_TypeError, "a tensor is negated lazily: resolve_neg() gives one that is not");
+  return t;
+}
 const at::Tensor *tensor(PyObject *o) {  // null for None
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "a tensor was expected, not %s", Py_TYPE(o)->tp_name);
-  return &THPVariable_Unpack(o);
+  return &plain(o);
 }
 const at::Tensor &cuda_tensor(PyObject *o, const char *name) {
   if (!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda()) refuse(PyExc_TypeError, "%s must be a CUDA tensor", name);
-  const at::Tensor &t = THPVariable_Unpack(o);
-  if (t.layout() != at::kStrided) refuse(PyExc_TypeError, "%s must be a strided tensor", name);
-  return t;
+  return plain(o);
 }
 std::string shape_text(at::IntArrayRef s) {
   std::string t = "(";
@@ -139,7 +144,7 @@ void same_device(const at::Tensor &t, c10::Device device) {
 // What a forward pass kept, as it may come back from saved-tensor hooks.
 const at::Tensor &kept(PyObject *o, const char *name, at::ScalarType dtype, at::IntArrayRef shape, c10::Device device) {
   const at::Tensor *t = tensor(o);
-  if (!t || t->layout() != at::kStrided || t->device() != device || t->scalar_type() != dtype || t->sizes() != shape ||
+  if (!t || t->device() != device || t->scalar_type() != dtype || t->sizes() != shape ||
       !t->is_contiguous())
     refuse(PyExc_ValueError, "%s must be as the forward pass saved them: a contiguous %s tensor of shape %s on x's device", name,
            name_of(dtype), shape_text(shape).c_str());

@@ -79,3 +79,23 @@ def test_plain_calls_of_batches_are_refused():
         with pytest.raises((RuntimeError, NotImplementedError, TypeError, ValueError)):
             torch.func.vmap(f)(two(t))
     assert sf.dense_error() == 0
+
+
+def test_tensors_whose_memory_is_not_their_values():
+    """Negated when read (the imaginary part of a conjugate), or not in rows at all: refused, also where an optional
+    argument is one."""
+    parts = torch.view_as_complex(torch.randn(6, 40, 2, device="cuda"))
+    neg = parts.conj().imag
+    assert neg.is_neg() and not neg.resolve_neg().is_neg()
+    x, w, b, _ = linear_args()
+    sparse = torch.eye(40, device="cuda").to_sparse()
+    rows, sparse_rows = neg.resolve_neg().contiguous(), torch.randn(6, 40, device="cuda").to_sparse()
+    for bad in (neg, sparse_rows):
+        for call in (lambda: sf.linear_forward(x, w, b, residual=bad), lambda: sf.linear_forward(x, w, b, out=bad, out_dtype=torch.float32),
+                     lambda: sf.residual_norm_forward(bad, rows, dtype=torch.float16), lambda: sf.clip_grad_norm([bad], 1.0),
+                     lambda: sf.residual_norm_forward(rows, bad, dtype=torch.float16), lambda: sf.clip_grad_norm([rows], 1.0, out=[bad])):
+            with pytest.raises(TypeError):
+                call()
+    with pytest.raises(TypeError):
+        sf.linear_forward(x, w, sparse[0].half())
+    assert sf.linear_forward(x, w, b, residual=rows)[0].shape == (6, 40) and sf.dense_error() == 0
