@@ -290,6 +290,7 @@ def quantize_act8(x, relu: bool = False, stream=None) -> Act8:
 def dequantize_act8(q: Act8, dtype=None, out=None, stream=None):
     """The values that q stands for, [..., cols] in ``dtype`` (default: the quantised tensor's)."""
     dtype = dtype or (out.dtype if out is not None else q.dtype)
+    given = out is not None
     code = _code(dtype)
     buf, T = q._p.buf, q._p.T
     pc, ldq, ps, lds = q._p.pointers()
@@ -307,6 +308,8 @@ def dequantize_act8(q: Act8, dtype=None, out=None, stream=None):
                 raise ValueError("out: rows must not overlap")
         _check(load_library().sfnn_act8_restore(pc, ldq, ps, lds, T, cols, 1 if q.relu else 0, code, out.data_ptr(), ld,
                                                 _raw_stream(index)), "sfnn_act8_restore")
+    if given and not out.is_inference():  # autograd then refuses a backward pass that saved what was there before
+        torch.autograd.graph.increment_version(out)
     return out
 
 

@@ -37,7 +37,11 @@ def clipped_into(t):
     sf.clip_grad_norm([normal(5), normal(6, 40)], 1.0, out=[torch.empty(5, device="cuda").half(), t])
 
 
-WRITERS = [onto_residual, into_rows, next_stream, norm_into, clipped, clipped_into]
+def dequantized(t):
+    sf.dequantize_act8(sf.quantize_act8(normal(6, 40, seed=7)), out=t)
+
+
+WRITERS = [onto_residual, into_rows, next_stream, norm_into, clipped, clipped_into, dequantized]
 
 
 @pytest.mark.parametrize("write", WRITERS)
