@@ -3,8 +3,8 @@
 //     n = scale * sqrt(sum over all tensors of g^2),   out = g * scale * min(1, max_norm / (n + eps))
 //
 // Two kernels: k_grad_squares adds up squares, a partial sum per CTA; every CTA of k_grad_scale
-// adds the partial sums up again in the same order (no atomics: the result depends on the sizes
-// alone) and multiplies its share of the values.  The tensors' table travels in the kernels'
+// adds the partial sums up again in the same order (no atomics: the result depends on the tensors'
+// sizes, types and alignments alone) and multiplies its share of the values.  The tensors' table travels in the kernels'
 // parameters, so nothing is copied to the device and a captured call holds its own table.
 //
 // Bound by bytes: each value is read twice and written once.  Measured: 1.08 GB in 20 bf16

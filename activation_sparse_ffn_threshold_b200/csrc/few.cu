@@ -397,7 +397,8 @@ int active_clusters(int split, int sms) {
 // The shape with the least time (ns) of 1, 2, 4 and 8 CTAs to a cluster and a few widths of the tiles of
 // tokens.  The time is a fit to 255 products of 1 to 1024 tokens, 64 to 28672 wide either way, each in every
 // shape (off by 5 % on average; the shape it takes is 0.8 % slower than the best of them, the square tiles
-// among them, at most 15 %).  A chunk of K costs the longest of one CTA's pace, the weights' bytes from memory
+// among them, at most 15 %).  The products of the fit have a bias and no activation; neither this cost nor that of
+// the square tiles knows the epilogue.  A chunk of K costs the longest of one CTA's pace, the weights' bytes from memory
 // and all bytes through the L2 (5.5 and 11.7 bytes a ns of all CTAs); then come the end by tokens and the
 // exchange.  No one shape does for all: 4096 x 4096, 8 tokens, takes 21, 14 and 12 us with 1, 2 and 4 CTAs,
 // 4096 x 16384 27 us with 1 and none wider than 2 fits; 256 tokens of 2048 x 8192 take 19 us as two tiles,

@@ -19,7 +19,10 @@ namespace {
 //
 // Bound by bytes.  Measured, bf16, both norms and one gate row (us; bytes over the time in TB/s):
 //     8192 x 4096   forward 52 (5.2)   backward 82 and 5 for the sums (4.9)
-//     4000 x 8192   forward 51 (5.1)
+//     4000 x 8192   forward 51 (5.1)   backward 88 (4.5)
+// Backward from 4097 values on there is one group (8192 x 5120: 133 us, 3.8 TB/s), and of an fp32 stream near 8192
+// one stage, so that nothing is on its way while a row is worked on (4000 x 8192: 148 us, 4.0 TB/s).
+// Forward the longest rows are 8856 values of an fp32 stream with everything that may be there, 16384 at most.
 // Rows held in registers instead took 99 for 4000 x 8192 and 244 for 8192 x 4096 backward.
 constexpr int kMaxStages = 4;
 constexpr int kMaxGroups = 16;  // 15 named barriers; 16 groups are warps, which need none

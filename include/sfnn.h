@@ -641,7 +641,8 @@ SFNN_API sfnn_status sfnn_norm_forward(const sfnn_norm_desc *q, void *r, int64_t
                                        int32_t *err, sfnn_stream_t stream);
 /* The gradients from dR [T x d] and dH [T x d] (either may be NULL: zeros), contiguous; a NULL one is
  * not computed.  dgate: [d] for one row of gates, else [T x d].  Sums over the tokens are fp32, in an
- * order that the sizes and the device alone decide.  ws: sfnn_norm_workspace bytes, 16-byte aligned,
+ * order that sizes, types, alignments, strides, which arguments and gradients there are, and the device
+ * decide: the same call gives the same bits.  ws: sfnn_norm_workspace bytes, 16-byte aligned,
  * shared with no call that runs at the same time. */
 SFNN_API int64_t sfnn_norm_workspace(int32_t T, int32_t d);
 SFNN_API sfnn_status sfnn_norm_backward(const sfnn_norm_desc *q, const float *stats, const void *dr, int64_t lddr,
@@ -658,8 +659,8 @@ SFNN_API sfnn_status sfnn_norm_backward(const sfnn_norm_desc *q, const float *st
  * their type; out has the type of in and is in itself, or overlaps nothing else that the call reads
  * or writes (else SFNN_ERR_INVALID_ARG).  norm [1]: n.  A NaN, or an infinite n where max_norm is
  * infinite, makes every out NaN; an infinite n otherwise makes it 0 (NaN where g is infinite).
- * Squares are summed in 64 bits (8 at a time in 32 where those hold them), in an order that the sizes
- * and the device alone decide.  ws: sfnn_clip_workspace bytes, 8-byte aligned, shared with no call
+ * Squares are summed in 64 bits (8 at a time in 32 where those hold them), in an order that the
+ * tensors' sizes, types and alignments and the device decide.  ws: sfnn_clip_workspace bytes, 8-byte aligned, shared with no call
  * that runs at the same time.
  */
 typedef struct {
